@@ -69,8 +69,11 @@ enum smla_status {
     SMLA_ERR_TIMEOUT = 12,      /* device: a bounded wait inside a kernel ran out */
     SMLA_ERR_SINK = 13,         /* d_sink given without sink, or sink without d_sink */
     SMLA_ERR_ARG = 14,          /* any other invalid argument (e.g. a non-finite scale) */
-    SMLA_ERR_DEVICE = 15        /* a pointer that must be device memory is not device (or managed)
+    SMLA_ERR_DEVICE = 15,       /* a pointer that must be device memory is not device (or managed)
                                    memory of the current device */
+    SMLA_ERR_PAGES = 16,        /* device: the pool has fewer free pages than the call needs */
+    SMLA_ERR_REFCOUNT = 17,     /* device: a page with no owner was shared or given back */
+    SMLA_ERR_CACHE = 18         /* page_size / scale_block / num_pages of a cache unsupported */
 };
 
 /* Problem dimensions. */
@@ -244,6 +247,159 @@ int smla_dsink_static(const uint16_t* dO, const uint16_t* o, const float* lse,
                       const float* sink, float* d_sink, int32_t T, int32_t H, void* stream);
 
 /*
+ * ------------------------------------------------- paged 8-bit cache (serving)
+ * A pool of pages that holds the kv rows of many sequences in 8 bits. A page
+ * has page_size rows of 512 e4m3 values; each scale_block consecutive rows of
+ * it share one fp32 scale, and the row's value is code * scale. Sequences find
+ * their pages through a block table: position p of the sequence in row b of
+ * `table` [B, max_pages] int32 is row p % page_size of page
+ * table[b, p / page_size]; -1 marks an entry without a page. refcount[i] is
+ * the number of table entries that hold page i; 0 marks a free page.
+ *
+ * All of it is device memory owned by the caller. The calls below run wholly
+ * on the device: none reads a length or a table back to the host, so each can
+ * be captured into a CUDA graph. Two calls that use one workspace, or of
+ * which one changes pages, tables or counts that the other uses, must be
+ * ordered on the device (one stream, or events): nothing here locks.
+ * A call takes at most 2^24 sequences (B, n).
+ */
+typedef struct smla_cache {
+    uint8_t* pages;       /* [num_pages, page_size, 512] e4m3 bit patterns */
+    float* scales;        /* [num_pages, page_size / scale_block] fp32, finite and >= 0 */
+    int32_t* refcount;    /* [num_pages]; may be NULL for smla_fwd_paged, smla_cache_write and
+                             smla_cache_copy_pages */
+    int32_t num_pages;    /* >= 1; num_pages * page_size < 2^31 */
+    int32_t page_size;    /* 16, 32, 64, 128 or 256 */
+    int32_t scale_block;  /* 16, 32 or 64, at most page_size */
+    int32_t D;            /* must be 512 */
+} smla_cache;
+
+typedef struct smla_paged_dims {
+    int32_t T;          /* query tokens */
+    int32_t H;          /* query heads: a multiple of 16, 16..128 */
+    int32_t D;          /* must be 512 */
+    int32_t topk;       /* ranks per token; 0: every visible position (topk == NULL) */
+    int32_t B;          /* rows of table (sequences) */
+    int32_t max_pages;  /* columns of table; max_pages * page_size < 2^31 */
+    float scale;        /* score scale: 0 = 1/sqrt(D) */
+} smla_paged_dims;
+
+/*
+ * Attention of T query tokens over the cache (the serving form of smla_fwd:
+ * one token or a few per sequence). Token t belongs to the sequence in table
+ * row seq[t] (row t if seq is NULL; then T <= B) and sees its positions
+ * [0, lens[t]). With topk, it attends to the ranks r whose position topk[t,r]
+ * is visible (-1: masked; the same position twice counts twice), else to
+ * every visible position:
+ *   s_r = scale * <q[t,h,:], x_r>,  x_r the cache row as code * block scale
+ *   lse[t,h] = log(exp(sink[h]) + sum_r exp(s_r)),  o[t,h,:] = sum_r exp(s_r - lse) x_r
+ * A token with no valid rank (lens[t] = 0: a padded slot of the batch) gets
+ * o = 0 and lse = sink[h] (or -inf without a sink). Cache rows that no valid
+ * rank names are not used, whatever bytes they hold.
+ *   q [T,H,512] bf16, lens [T], seq [T] or NULL, topk [T,topk] or NULL int32,
+ *   sink [H] fp32 or NULL -> o [T,H,512] bf16 (RNE), lse [T,H] fp32.
+ * On the device: lens[t] outside [0, max_pages * page_size] is clamped, and a
+ * seq, a topk entry >= lens[t] or < -1, or a page number that is out of range
+ * masks what it names; each sets SMLA_ERR_INDEX in the status word.
+ * workspace: smla_paged_workspace_size() bytes.
+ */
+int smla_fwd_paged(const uint16_t* q, const smla_cache* cache, const int32_t* table,
+                   const int32_t* seq, const int32_t* lens, const int32_t* topk,
+                   const float* sink, uint16_t* o, float* lse, const smla_paged_dims* dims,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+int smla_paged_workspace_size(const smla_paged_dims* dims, size_t* bytes);
+
+/*
+ * Writes new rows into the cache. Rows [cu[b], cu[b+1]) of `rows` go to the
+ * positions start[b], start[b] + 1, ... of the sequence in table row b (whose
+ * entries must hold pages: see smla_cache_alloc).
+ * A scale block's scale becomes the least power of two 2^e, e >= -100, with
+ * max |x| <= 448 * 2^e over the block's new finite values; a block that holds
+ * earlier rows of the sequence (positions before start[b]) keeps the larger of
+ * that and its present scale, and if the scale grows the earlier rows' codes
+ * are rounded to the new one (by a power of two: exact but for e4m3
+ * subnormals). Codes are x / scale rounded to nearest even; +-inf becomes +-448 and NaN
+ * the e4m3 NaN. Rows of the block behind the last new one keep their bytes.
+ *   rows [n_rows,512] bf16, cu [B+1] (cu[0] = 0, not decreasing, cu[B] <= n_rows),
+ *   start [B], table [B,max_pages] int32.
+ * The rows of one call must go to different places: two sequences of the call
+ * must not write one page (a shared last page is copied by smla_cache_fork).
+ * On the device, a row whose position or page is out of range is dropped
+ * and SMLA_ERR_INDEX set.
+ * workspace: at least 256 bytes (status word).
+ */
+int smla_cache_write(const smla_cache* cache, const int32_t* table, const int32_t* start,
+                     const int32_t* cu, const uint16_t* rows, int32_t B, int32_t max_pages,
+                     int32_t n_rows, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gives every sequence the pages that its length needs: each entry table[b,j]
+ * = -1 with j < ceil(lens[b] / page_size) gets a free page, whose refcount
+ * becomes 1. Entries are served in the order of (b, j), pages in the order of
+ * their numbers. All or nothing: with too few free pages nothing changes and
+ * SMLA_ERR_PAGES is set. Lengths are clamped to [0, max_pages * page_size]
+ * (SMLA_ERR_INDEX). In place on table and cache->refcount.
+ * workspace: smla_cache_workspace_size(cache, B) bytes, as for fork and compact.
+ */
+int smla_cache_alloc(const smla_cache* cache, int32_t* table, const int32_t* lens, int32_t B,
+                     int32_t max_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Forks sequences: child i (row i of child_table [n, max_pages], written
+ * whole) continues the sequence in row parents[i] of `table`, of length
+ * lens[parents[i]]. It shares the parent's full pages (their refcounts rise by
+ * one) and gets a copy, in a free page, of a partly filled last one, so that
+ * parent and children can each be written on. Several children may have one
+ * parent. Free pages go to the children in order, by page number. All or
+ * nothing: with too few free pages the refcounts stay, child_table is filled
+ * with -1 and SMLA_ERR_PAGES is set. A parent outside [0, B), a length
+ * beyond the table or a page number out of range (SMLA_ERR_INDEX), or a page
+ * whose refcount is 0 (SMLA_ERR_REFCOUNT), leaves -1 where it would have gone.
+ */
+int smla_cache_fork(const smla_cache* cache, const int32_t* table, const int32_t* lens,
+                    const int32_t* parents, int32_t* child_table, int32_t B, int32_t n,
+                    int32_t max_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gives back the pages of sequences: for each of the n rows listed in `rows`
+ * (all B rows if rows is NULL) every page entry becomes -1 and the page's
+ * refcount falls by one. A row listed twice is given back once. A row or page
+ * out of range sets SMLA_ERR_INDEX; a refcount that is 0 already stays 0 and
+ * sets SMLA_ERR_REFCOUNT. workspace: at least 256 bytes.
+ */
+int smla_cache_free(const smla_cache* cache, int32_t* table, const int32_t* rows, int32_t B,
+                    int32_t n, int32_t max_pages, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * Compacts the pool: with n live pages (refcount > 0), the live pages numbered
+ * n and up move, in order, to the free pages numbered below n, in order.
+ * Writes the table and the refcounts of the compacted pool to new_table
+ * [B, max_pages] and new_refcount [num_pages]; `table` and cache->refcount are
+ * left as they are, and still describe the same rows until a page is
+ * written, because pages move only into free ones. A table entry that names
+ * a page out of range (SMLA_ERR_INDEX) or a free one (SMLA_ERR_REFCOUNT) becomes -1.
+ */
+int smla_cache_compact(const smla_cache* cache, const int32_t* table, int32_t* new_table,
+                       int32_t* new_refcount, int32_t B, int32_t max_pages, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Copies whole pages with their scales: page src[i] to page dst[i], i < n.
+ * Every dst must differ from the others and from every src: otherwise nothing
+ * is copied and SMLA_ERR_OVERLAP is set on the device. A pair with a number
+ * out of range is skipped (SMLA_ERR_INDEX). Refcounts and tables are the
+ * caller's. workspace: smla_cache_workspace_size(cache, n) bytes.
+ */
+int smla_cache_copy_pages(const smla_cache* cache, const int32_t* src, const int32_t* dst,
+                          int32_t n, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of smla_cache_alloc (n = B), smla_cache_fork (n children),
+ * smla_cache_compact (any n) and smla_cache_copy_pages (n pairs). */
+int smla_cache_workspace_size(const smla_cache* cache, int32_t n, size_t* bytes);
+
+/*
  * Self-test of the kernels' bounded waits (the pages have no counterpart; it
  * exists so that the failure path can be exercised without faulting a GPU).
  * Launches one CTA that waits on an mbarrier nothing arrives on, through the
@@ -259,8 +415,9 @@ int smla_selftest_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t
 
 /*
  * Synchronizes `stream`, then reads the device status word that the last
- * call given this workspace wrote (SMLA_OK, SMLA_ERR_INDEX or
- * SMLA_ERR_TIMEOUT) into *status. Returns SMLA_ERR_CUDA if the stream or
+ * call given this workspace wrote (SMLA_OK, or one of SMLA_ERR_INDEX,
+ * SMLA_ERR_PAGES, SMLA_ERR_REFCOUNT, SMLA_ERR_OVERLAP and SMLA_ERR_TIMEOUT)
+ * into *status. Returns SMLA_ERR_CUDA if the stream or
  * the copy failed.
  */
 int smla_get_device_status(const void* workspace, void* stream, int* status);

@@ -32,13 +32,19 @@ SMLA_ERR_TIMEOUT = 12
 SMLA_ERR_SINK = 13
 SMLA_ERR_ARG = 14
 SMLA_ERR_DEVICE = 15
+SMLA_ERR_PAGES = 16
+SMLA_ERR_REFCOUNT = 17
+SMLA_ERR_CACHE = 18
 
 SMLA_OP_FWD, SMLA_OP_BWD, SMLA_OP_CSR, SMLA_OP_BWD_HOST = 0, 1, 2, 3
 
 EXPORTED = ("smla_workspace_size", "smla_fwd", "smla_bwd", "smla_bwd_host", "smla_csr_build",
             "smla_get_device_status", "smla_status_string", "smla_version",
             "smla_profiling", "smla_profile_read", "smla_dsink_static",
-            "smla_selftest_wait_timeout", "smla_bwd_partial", "smla_reduce_partials")
+            "smla_selftest_wait_timeout", "smla_bwd_partial", "smla_reduce_partials",
+            "smla_fwd_paged", "smla_paged_workspace_size", "smla_cache_write", "smla_cache_alloc",
+            "smla_cache_fork", "smla_cache_free", "smla_cache_compact", "smla_cache_copy_pages",
+            "smla_cache_workspace_size")
 
 
 class SmlaDims(ctypes.Structure):
@@ -47,6 +53,23 @@ class SmlaDims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("topk", ctypes.c_int32), ("num_kv", ctypes.c_int32),
                 ("r_chunk", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class SmlaCache(ctypes.Structure):
+    """Mirror of ``smla_cache``."""
+
+    _fields_ = [("pages", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("refcount", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("scale_block", ctypes.c_int32),
+                ("D", ctypes.c_int32)]
+
+
+class SmlaPagedDims(ctypes.Structure):
+    """Mirror of ``smla_paged_dims``."""
+
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("topk", ctypes.c_int32), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class SmlaPhaseStat(ctypes.Structure):
@@ -93,11 +116,19 @@ def load(path: str = LIB_PATH):
                                           ctypes.POINTER(ctypes.c_int)]
         lib.smla_status_string.argtypes = [ctypes.c_int]
         lib.smla_status_string.restype = ctypes.c_char_p
-        for name in ("smla_workspace_size", "smla_fwd", "smla_bwd", "smla_bwd_host", "smla_csr_build",
-                     "smla_get_device_status", "smla_version", "smla_profiling",
-                     "smla_profile_read", "smla_dsink_static", "smla_selftest_wait_timeout",
-                     "smla_bwd_partial", "smla_reduce_partials"):
-            getattr(lib, name).restype = ctypes.c_int
+        cache_p, pdims_p = ctypes.POINTER(SmlaCache), ctypes.POINTER(SmlaPagedDims)
+        lib.smla_fwd_paged.argtypes = [vp, cache_p] + [vp] * 7 + [pdims_p, vp, sz, vp]
+        lib.smla_paged_workspace_size.argtypes = [pdims_p, ctypes.POINTER(sz)]
+        lib.smla_cache_write.argtypes = [cache_p] + [vp] * 4 + [i32] * 3 + [vp, sz, vp]
+        lib.smla_cache_alloc.argtypes = [cache_p] + [vp] * 2 + [i32] * 2 + [vp, sz, vp]
+        lib.smla_cache_fork.argtypes = [cache_p] + [vp] * 4 + [i32] * 3 + [vp, sz, vp]
+        lib.smla_cache_free.argtypes = [cache_p] + [vp] * 2 + [i32] * 3 + [vp, sz, vp]
+        lib.smla_cache_compact.argtypes = [cache_p] + [vp] * 3 + [i32] * 2 + [vp, sz, vp]
+        lib.smla_cache_copy_pages.argtypes = [cache_p] + [vp] * 2 + [i32] + [vp, sz, vp]
+        lib.smla_cache_workspace_size.argtypes = [cache_p, i32, ctypes.POINTER(sz)]
+        for name in EXPORTED:
+            if name != "smla_status_string":
+                getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
 

@@ -120,17 +120,14 @@ float eff_scale(const smla_dims& d) {
     return d.scale > 0.f ? d.scale : 1.0f / std::sqrt(float(d.D));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Span { const void* p; size_t n; };
-
 bool overlaps(const Span& a, const Span& b) {
     if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
     return a0 < b0 + b.n && b0 < a0 + a.n;
 }
 
-// Each output must be disjoint from every other span (inputs, outputs, workspace).
+}  // namespace
+
 int check_overlap(const Span* outs, int nout, const Span* ins, int nin) {
     for (int i = 0; i < nout; ++i) {
         for (int j = 0; j < nin; ++j)
@@ -156,10 +153,6 @@ int check_arch() {
     if (dev >= 0 && dev < 64) cached[dev] = ok ? 1 : 2;
     return ok ? SMLA_OK : SMLA_ERR_ARCH;
 }
-
-int cuda_rc(cudaError_t e) { return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA; }
-
-}  // namespace
 
 // Every non-NULL pointer must be device memory of the current device (or
 // managed memory): a host pointer handed to a kernel faults the GPU, so it is
@@ -485,6 +478,9 @@ const char* smla_status_string(int code) {
         case SMLA_ERR_SINK: return "d_sink must be given exactly when sink is given";
         case SMLA_ERR_ARG: return "invalid argument (scale must be finite and >= 0)";
         case SMLA_ERR_DEVICE: return "a pointer that must be device memory is not device memory of the current device";
+        case SMLA_ERR_PAGES: return "the pool has fewer free pages than the call needs (nothing was changed)";
+        case SMLA_ERR_REFCOUNT: return "a page that no table entry owns was shared or given back";
+        case SMLA_ERR_CACHE: return "unsupported cache (page_size 16, 32, 64, 128 or 256; scale_block 16, 32 or 64, at most page_size; num_pages * page_size < 2^31)";
         default: return "unknown status code";
     }
 }
@@ -761,6 +757,9 @@ int smla_get_device_status(const void* workspace, void* stream, int* status) {
     }
     *status = SMLA_OK;
     if (bits & (1u << SMLA_ERR_INDEX)) *status = SMLA_ERR_INDEX;
+    else if (bits & (1u << SMLA_ERR_PAGES)) *status = SMLA_ERR_PAGES;
+    else if (bits & (1u << SMLA_ERR_REFCOUNT)) *status = SMLA_ERR_REFCOUNT;
+    else if (bits & (1u << SMLA_ERR_OVERLAP)) *status = SMLA_ERR_OVERLAP;
     else if (bits & (1u << SMLA_ERR_TIMEOUT)) *status = SMLA_ERR_TIMEOUT;
     else if (bits) *status = SMLA_ERR_CUDA;
     return SMLA_OK;

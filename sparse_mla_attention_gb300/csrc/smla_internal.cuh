@@ -49,10 +49,23 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// ------------------------------------------------------- host-side validation
 // Returns SMLA_OK if every non-NULL pointer of `ptrs` is device memory of the
 // current device (or managed memory), else SMLA_ERR_DEVICE (SMLA_ERR_CUDA if
 // the device cannot be queried).
 int check_device_ptrs(const void* const* ptrs, int n);
+
+// SMLA_OK if the current device is compute capability 10.3 (cached per device).
+int check_arch();
+
+struct Span { const void* p; size_t n; };
+
+// Each output must be disjoint from every other span (inputs, outputs, workspace).
+int check_overlap(const Span* outs, int nout, const Span* ins, int nin);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int cuda_rc(cudaError_t e) { return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA; }
 
 // ------------------------------------------------------------ workspace plans
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -169,5 +182,50 @@ cudaError_t launch_attn_sdi(const ChunkArgs& a, cudaStream_t s);
 // SMLA_ERR_TIMEOUT in `status` through the kernels' own unwind path.
 cudaError_t launch_wait_selftest(unsigned* status, uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_attn_dq(const ChunkArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------- paged 8-bit cache
+// Kernel view of an smla_cache. Rows are numbered page * page_size + slot, so
+// row r is pages + 512 r and its scale is scales[r >> block_shift].
+struct CacheView {
+    uint8_t* pages; float* scales; int32_t* refcount;
+    int num_pages, page_shift, block_shift;
+};
+
+cudaError_t launch_cache_write(const CacheView& c, const int32_t* table, const int32_t* start,
+                               const int32_t* cu, const uint16_t* rows, int B, int max_pages,
+                               int n_rows, unsigned* status, cudaStream_t s);
+
+// Scratch of the page operations, carved from the workspace behind the status word.
+struct PageScratch {
+    int32_t* count;      // [1] pairs to copy
+    int32_t* need;       // [n] pages that row i needs, then their exclusive sum
+    int32_t* src;        // [max(n, num_pages)] pages to copy from
+    int32_t* dst;        // [max(n, num_pages)] pages to copy to / free pages in order
+    int32_t* map;        // [num_pages] new number of a moved page / marks
+};
+cudaError_t launch_cache_alloc(const CacheView& c, int32_t* table, const int32_t* lens, int B,
+                               int max_pages, const PageScratch& w, unsigned* status, cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const int32_t* lens,
+                              const int32_t* parents, int32_t* child_table, int B, int n,
+                              int max_pages, const PageScratch& w, unsigned* status, cudaStream_t s);
+cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t* rows, int B, int n,
+                              int max_pages, unsigned* status, cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheView& c, const int32_t* table, int32_t* new_table,
+                                 int32_t* new_refcount, int B, int max_pages, const PageScratch& w,
+                                 unsigned* status, cudaStream_t s);
+cudaError_t launch_cache_copy(const CacheView& c, const int32_t* src, const int32_t* dst, int n,
+                              const PageScratch& w, unsigned* status, cudaStream_t s);
+
+// Arguments of the attention over the cache.
+struct PagedArgs {
+    const uint16_t* q; CacheView cache; const int32_t* table; const int32_t* seq;
+    const int32_t* lens; const int32_t* topk; const float* sink; uint16_t* o; float* lse;
+    int T, H, K, B, max_pages;
+    float scale;
+    unsigned* status;
+    char* scratch;       // workspace behind the status word
+};
+size_t paged_scratch_bytes(int T, int H);
+cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s);
 
 }  // namespace smla

@@ -1,154 +1,899 @@
-// k_fwd_paged.cu -- attention over the paged 8-bit cache.
+// k_fwd_paged.cu -- attention over the paged 8-bit cache on the tensor cores.
 //
 // For token t (sequence seq[t]) and head h, over the valid ranks r (positions
 // below lens[t], all of them or the picks topk[t, :]):
 //   s_r = scale * <q[t,h,:], x_r>, lse = log(exp(sink_h) + sum exp(s_r)),
 //   o = sum_r exp(s_r - lse) * x_r,   x_r = e4m3 code * block scale.
 //
-// One CTA per token and group of 16 heads, one warp per head (lane l holds
-// columns 16l .. 16l+15 of q and of o), rows of 32 ranks staged in shared
-// memory as bytes; one pass with a running maximum and sum, all in fp32.
+// The codes go from the cache to the tensor cores as they are (kind::f8f6f4);
+// what meets them is split so that nothing but the codes is 8 bits wide:
+//  * q: a row's power-of-two scale 2^e, then hi = e4m3(q / 2^e) and lo =
+//    e4m3(16 (q / 2^e - hi)): e4m3 has 4 significant bits and bf16 8, so hi +
+//    lo / 16 is q itself (to 2^-23 of the row's largest value for small ones).
+//  * the weights w = exp(s - m) * block scale: e4m3(w) and, of what is left,
+//    e5m2(w - e4m3(w)), whose range reaches further down: off by at most 2^-7 w
+//    (bf16: 2^-8), and 2^-18 of the largest weight for weights near zero. Both parts
+//    accumulate into one fp32 accumulator; the denominator sums unrounded weights.
+// Block scales: s_r is multiplied by its row's scale in fp32, and w carries it.
+//
+// S = Q K^T: M = 128 (up to 64 heads; lanes 16i .. 16i+15 of each lane quarter's first half
+// hold hi, its second half lo), N = 64 ranks, K = 512, A = Q from TMEM.
+// O^T = V^T W^T: M = 128 columns of D (four blocks), N = heads, K = 64 ranks hi
+// then 64 ranks lo; A = the very tile that S read, as its MN-major transpose.
+// TMEM: S two buffers of 64 columns, Q 128 columns, O^T 4 x 64 columns.
+//
+// fwd_paged_kernel: persistent, one CTA per SM. The tiles (64 ranks) of all
+// tokens, in order, are dealt out evenly: CTA c of a head group takes the
+// tiles [c X / G, (c+1) X / G), finds its first token by a scan over lens, and
+// works through its items (a token's part of the range). An item that holds a
+// whole token writes o and lse; a part of a token goes to the workspace as fp32
+// (unnormalised O, maximum, sum), and combine_paged_kernel joins the parts in order.
+// Warps: 0-3 softmax (a thread has one head and half of the tile's ranks: the
+// two lanes of a head swap their halves of S, which adds hi and lo), 4-7 q
+// conversion and output, 8 MMA, 9-10 loads (TMA boxes where a tile's rows lie in
+// whole pages, four-row gathers otherwise). A masked rank loads a valid row of its
+// tile instead of its own (weight 0, and no byte of a row that nothing
+// names is ever read); a tile without a valid rank is skipped.
+// Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the
+// CTA's loops, waits (bounded) for its own copies and MMAs and frees TMEM.
 #include <cuda_fp8.h>
 
 #include "smla_internal.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
 
 namespace smla {
+using namespace sm100;
 
 namespace {
 
-constexpr int kPgHeads = 16;
-constexpr int kPgTile = 32;
+constexpr uint64_t kPgWaitNs = 2000000000ull;
+constexpr float kPgLog2e = 1.4426950408889634f;
+constexpr float kPgLn2 = 0.6931471805599453f;
+constexpr int kPgTile = 64;                      // ranks per tile
+constexpr int kPgSlots = 6;
+constexpr int kPgSlotBytes = kPgTile * kD;       // 32 KB: four blocks of 64 rows x 128 bytes
+constexpr int kPgBlockBytes = kPgTile * 128;
+constexpr int kPgHeads = 64;                     // heads of a group at most
+constexpr int kPgPBytes = kPgHeads * 128;        // weights of a tile: 64 bytes hi, 64 bytes lo a head
+constexpr int kPgMmaWarp = 8, kPgLoadWarp = 9, kPgLoadWarps = 2;
+constexpr int kPgThreads = (kPgLoadWarp + kPgLoadWarps) * 32;
+constexpr int kPgMaxCtas = 160;
+// TMEM columns
+constexpr uint32_t kPgColS = 0, kPgColQ = 128, kPgColO = 256;
+// Weights are scaled so that the running reference's is 2^kPgBias; the
+// reference follows the maximum when it is passed by more than 2^kPgSlack
+// (e4m3 ends at 448 > 2^(kPgBias + kPgSlack)).
+constexpr float kPgBias = 5.f, kPgSlack = 3.f;
 
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v & 0xffffu), __NV_E4M3);
-    return __half22float2(__half2(h));
+struct PgShared {
+    uint64_t full[kPgSlots], empty[kPgSlots], q_load[2];
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
+    uint64_t q_full, q_empty, o_full, o_empty, vote_bar, drain;
+    uint32_t tbase;
+    volatile int abort_flag;
+    int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
+    long long sum[kPgThreads / 32];
+    int any[kPgSlots];                           // 0: no valid rank in the tile, 1: some, 2: all
+    uint32_t vote[2][4];
+    int item_any[4];
+    float sref[4];
+    __align__(16) float scale[kPgSlots][kPgTile];     // block scale of each rank, -1: masked
+    __align__(16) float fac[2][kPgHeads];             // rescaling factors
+    float qfac[4][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
+    float m[4][kPgHeads], l[4][kPgHeads];        // per item: reference and sum of a head
+    float fin[4][kPgHeads];                      // per output warp: 1 / denominator
+};
+
+constexpr int kPgSmem = int(sizeof(PgShared)) + 1024 + kPgSlots * kPgSlotBytes + 2 * kPgPBytes;
+static_assert(kPgSmem <= 232448, "shared memory of one CTA is at most 227 KB");
+
+struct PgParams {
+    const int32_t* table; const int32_t* seq; const int32_t* lens; const int32_t* topk;
+    const float* scales; const float* sink;
+    uint16_t* o; float* lse;
+    int T, H, K, B, max_pages, num_pages, page_shift, block_shift;
+    int groups, group_heads;                     // head groups, heads of a full one
+    float scale;
+    unsigned* status;
+    int4* meta;                                  // [CTAs] end of a split token: {t, first CTA, its part, 0}
+    long long* total;                            // tiles of all tokens
+    float2* part_ml;                             // [CTAs][2][group_heads] maximum (log2) and sum
+    float* part_o;                               // [CTAs][2][group_heads][512]
+};
+
+__device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                        unsigned* status) {
+    if (*abort_flag) return false;
+    if (mbar_wait(bar, parity, kPgWaitNs)) return true;
+    *abort_flag = 1;
+    flag_status(status, SMLA_ERR_TIMEOUT);
+    return false;
 }
 
-__device__ __forceinline__ void unpack16(const uint4& v, float* x) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ bool pg_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             unsigned* status) {
+    const bool ok = pg_wait(bar, parity, abort_flag, status);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+__device__ __forceinline__ int pg_len(const PgParams& p, int t) {
+    const int64_t limit = int64_t(p.max_pages) << p.page_shift;
+    const int len = __ldg(p.lens + t);
+    return len < 0 ? 0 : len > limit ? int(limit) : len;
+}
+
+// Tiles of token t; at least one, so that every token is somebody's item.
+__device__ __forceinline__ int pg_tiles(const PgParams& p, int t) {
+    const int n = p.topk ? p.K : pg_len(p, t);
+    return n < 1 ? 1 : (n + kPgTile - 1) / kPgTile;
+}
+
+// The ring's uses are an item's q (two) and then its tiles, numbered over all
+// items; use g is in slot g % kPgSlots. A parity wait tells a phase only from the
+// one before, so whoever waits for a barrier sees each of its phases in turn:
+// `empty` counts every use (each slot is refilled by one loading warp), `full` the
+// tiles alone (MMA and softmax keep a parity bit a slot), and q has barriers of its
+// own, q_load[item & 1] (the q of item + 2 goes no earlier than six uses on, into
+// slots that item's q has left).
+static_assert(kPgSlots % 2 == 0 && kPgSlots >= 6, "a slot belongs to one of the two loading warps");
+__device__ __forceinline__ int pg_slot(int g) { return g % kPgSlots; }
+__device__ __forceinline__ uint32_t pg_parity(uint32_t bits, int slot) { return (bits >> slot) & 1u; }
+
+__device__ __forceinline__ long long pg_first(long long total, int c, int ctas) { return total * c / ctas; }
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3)));
+}
+
+// The CTA's share of the tiles: sums the tiles of all tokens (thread i those of
+// a run of tokens), then the thread whose run holds the CTA's first tile finds its token.
+__device__ void pg_locate(const PgParams& p, PgShared& sh, int c, int ctas) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = (p.T + kPgThreads - 1) / kPgThreads;
+    const int64_t t_lo = int64_t(threadIdx.x) * run;
+    const int t0 = int(t_lo < p.T ? t_lo : p.T), t1 = int(t_lo + run < p.T ? t_lo + run : p.T);
+    long long mine = 0;
+    for (int t = t0; t < t1; ++t) mine += pg_tiles(p, t);
+    long long x = mine;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = e4m3x2_to_float2(w[i]), b = e4m3x2_to_float2(w[i] >> 16);
-        x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
     }
+    if (lane == 31) sh.sum[warp] = x;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kPgThreads / 32; ++w) {
+        if (w < warp) before += sh.sum[w];
+        total += sh.sum[w];
+    }
+    const long long a = pg_first(total, c, ctas), b = pg_first(total, c + 1, ctas);
+    long long at = before + x - mine;
+    if (threadIdx.x == 0) {
+        sh.count = int(b - a);
+        if (blockIdx.x == 0) *p.total = total;
+    }
+    if (a < b && at <= a && a < at + mine) {
+        int t = t0;
+        for (;; ++t) {
+            const int n = pg_tiles(p, t);
+            if (a < at + n) break;
+            at += n;
+        }
+        sh.t0 = t;
+        sh.k0 = int(a - at);
+        // this CTA ends a token that began in an earlier one: it names the parts to join
+        int4 end = make_int4(-1, 0, 0, 0);
+        if (a > at && b - at >= pg_tiles(p, t)) {
+            const int first = int(((at + 1) * ctas - 1) / total);
+            end = make_int4(t, first, pg_first(total, first, ctas) == at ? 0 : 1, 0);
+        }
+        p.meta[blockIdx.x] = end;
+    } else if (a >= b && threadIdx.x == 0) {
+        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+}
+
+// The CTA's items: parts [k0, k0 + n) of the tiles of token t.
+struct PgWalk {
+    int t, k0, left;
+    __device__ __forceinline__ PgWalk(const PgShared& sh) : t(sh.t0), k0(sh.k0), left(sh.count) {}
+    __device__ __forceinline__ int tiles(const PgParams& p) const {
+        const int n = pg_tiles(p, t) - k0;
+        return n < left ? n : left;
+    }
+    __device__ __forceinline__ void next(int n) { left -= n; ++t; k0 = 0; }
+};
+
+}  // namespace
+
+__global__ void __launch_bounds__(kPgThreads, 1)
+fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_box,
+                 const __grid_constant__ CUtensorMap map_row, const PgParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    PgShared& sh = *reinterpret_cast<PgShared*>(smem_raw);
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw + sizeof(PgShared)) + 1023) & ~uintptr_t(1023));
+    uint8_t* pbuf = ring + kPgSlots * kPgSlotBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
+    const int ctas = int(gridDim.x) / p.groups;
+    const int head0 = group * p.group_heads;
+    const int heads = p.H - head0 < p.group_heads ? p.H - head0 : p.group_heads;
+    volatile int* ab = &sh.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPgSlots; ++s) {
+            mbar_init(&sh.full[s], 32);          // the lanes of the loading warp
+            mbar_init(&sh.empty[s], 5);          // tile: MMA and four softmax warps; q: the output warps
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sh.q_load[b], 8);         // four lanes a use
+            mbar_init(&sh.s_full[b], 2);         // MMA completion and the issuing thread
+            mbar_init(&sh.s_empty[b], 4);
+            mbar_init(&sh.p_full[b], 4);
+            mbar_init(&sh.p_empty[b], 1);
+        }
+        mbar_init(&sh.q_full, 4);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.o_full, 2);                // MMA completion and the issuing thread
+        mbar_init(&sh.o_empty, 4);
+        mbar_init(&sh.vote_bar, 4);
+        mbar_init(&sh.drain, 1);
+        sh.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kPgMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
+    pg_locate(p, sh, cta, ctas);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sh.tbase;
+
+    if (warp >= kPgLoadWarp) {
+        // --------------------------------------------------------------- loads
+        // Two warps take the ring uses in turn: an item's q (two uses of four 64-column boxes)
+        // and its tiles. Lanes 2i and 2i + 1 look up the ranks 4i .. 4i+3 of a tile
+        // and, where they are gathered, load two of their four column blocks each.
+        const int quad = lane >> 1, half = lane & 1;
+        const int box_rows = (1 << p.page_shift) < kPgTile ? (1 << p.page_shift) : kPgTile;
+        int g = 0, item = 0;
+        uint32_t loads = 0;                      // parity of each slot's last tile load
+        int q_last = -1;
+        bool ok = true, bad = false;
+        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+            const int n = w.tiles(p), t = w.t;
+            int len = __ldg(p.lens + t);
+            const int64_t limit = int64_t(p.max_pages) << p.page_shift;
+            if (len < 0 || len > limit) { bad = true; len = len < 0 ? 0 : int(limit); }
+            const int b = p.seq ? __ldg(p.seq + t) : t;
+            if (b < 0 || b >= p.B) { bad = true; len = 0; }
+            for (int i = 0; i < n + 2 && ok; ++i, ++g) {
+                if (g % kPgLoadWarps != warp - kPgLoadWarp) continue;
+                const int slot = pg_slot(g);
+                const uint32_t free_ph = (uint32_t(g / kPgSlots) & 1u) ^ 1u;
+                uint8_t* dst = ring + slot * kPgSlotBytes;
+                if (i < 2) {
+                    ok = pg_wait_warp(&sh.empty[slot], free_ph, ab, p.status);
+                    if (!ok) break;
+                    q_last = item;
+                    if (lane < 4) {
+                        mbar_arrive_expect_tx(&sh.q_load[item & 1], uint32_t(p.group_heads) * 128u);
+                        tma_load_2d(dst + lane * kPgBlockBytes, &map_q, (4 * i + lane) * 64, t * p.H + head0,
+                                    &sh.q_load[item & 1]);
+                    }
+                    continue;
+                }
+                const int r0 = kPgTile * (w.k0 + i - 2) + 4 * quad;
+                int row[4];
+                float sc[4];
+                if (p.topk) {
+                    int pos[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        pos[e] = r0 + e < p.K ? __ldg(p.topk + int64_t(t) * p.K + r0 + e) : -1;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        bad |= pos[e] < -1 || pos[e] >= len;
+                        const bool v = pos[e] >= 0 && pos[e] < len;
+                        row[e] = v ? __ldg(p.table + int64_t(b) * p.max_pages + (pos[e] >> p.page_shift)) : -1;
+                        bad |= v && (row[e] < 0 || row[e] >= p.num_pages);
+                        row[e] = row[e] < 0 || row[e] >= p.num_pages
+                                     ? -1
+                                     : (row[e] << p.page_shift) + (pos[e] & ((1 << p.page_shift) - 1));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[e] = row[e] >= 0 ? __ldg(p.scales + (row[e] >> p.block_shift)) : -1.f;
+                } else {
+                    // four consecutive positions: one page, one scale block
+                    int first = -1;
+                    float s = -1.f;
+                    if (r0 < len) {
+                        const int page = __ldg(p.table + int64_t(b) * p.max_pages + (r0 >> p.page_shift));
+                        if (page < 0 || page >= p.num_pages) {
+                            bad = true;
+                        } else {
+                            first = (page << p.page_shift) + (r0 & ((1 << p.page_shift) - 1));
+                            s = __ldg(p.scales + (first >> p.block_shift));
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool v = first >= 0 && r0 + e < len;
+                        row[e] = v ? first + e : -1;
+                        sc[e] = v ? s : -1.f;
+                    }
+                }
+                const bool mine = row[0] >= 0 || row[1] >= 0 || row[2] >= 0 || row[3] >= 0;
+                const bool whole = row[0] >= 0 && row[1] >= 0 && row[2] >= 0 && row[3] >= 0;
+                const unsigned some = __ballot_sync(0xffffffffu, mine);
+                const bool all = __all_sync(0xffffffffu, whole) != 0;
+                // a valid row of the tile, loaded in place of masked ones
+                int stand = row[0] >= 0 ? row[0] : row[1] >= 0 ? row[1] : row[2] >= 0 ? row[2] : row[3];
+                stand = __shfl_sync(0xffffffffu, stand, some ? __ffs(some) - 1 : 0);
+                ok = pg_wait_warp(&sh.empty[slot], free_ph, ab, p.status);
+                if (!ok) break;
+                loads ^= 1u << slot;             // full's phase of this load has the parity before
+                if (half == 0)
+                    *reinterpret_cast<float4*>(&sh.scale[slot][4 * quad]) = make_float4(sc[0], sc[1], sc[2], sc[3]);
+                if (lane == 0) sh.any[slot] = some == 0 ? 0 : all ? 2 : 1;
+                if (some == 0) {
+                    mbar_arrive(&sh.full[slot]);
+                } else if (all && !p.topk) {
+                    const int seg = lane >> 2, cb = lane & 3;
+                    const int y = __shfl_sync(0xffffffffu, row[0], (seg * box_rows / 4 * 2) & 31);
+                    if (seg * box_rows < kPgTile) {
+                        mbar_arrive_expect_tx(&sh.full[slot], uint32_t(box_rows) * 128u);
+                        tma_load_2d(dst + cb * kPgBlockBytes + seg * box_rows * 128, &map_box, cb * 128, y,
+                                    &sh.full[slot]);
+                    } else {
+                        mbar_arrive(&sh.full[slot]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) row[e] = row[e] >= 0 ? row[e] : stand;
+                    mbar_arrive_expect_tx(&sh.full[slot], 1024u);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int cb = 2 * half + k;
+                        tma_gather4(dst + cb * kPgBlockBytes + quad * 512, &map_row, cb * 128, row[0], row[1], row[2],
+                                    row[3], &sh.full[slot]);
+                    }
+                }
+            }
+            w.next(n);
+        }
+        if (bad) flag_status(p.status, SMLA_ERR_INDEX);
+        if (sh.abort_flag) {     // the loads already issued land before the CTA exits
+            for (int slot = warp - kPgLoadWarp; slot < kPgSlots; slot += kPgLoadWarps)
+                mbar_wait(&sh.full[slot], pg_parity(loads, slot) ^ 1u, kPgWaitNs / 8);
+            for (int q = q_last > 0 ? q_last - 1 : 0; q <= q_last; ++q)
+                mbar_wait(&sh.q_load[q & 1], uint32_t(q >> 1) & 1u, kPgWaitNs / 8);
+        }
+        __syncwarp();
+    } else if (warp == kPgMmaWarp) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            const uint32_t id_s = idesc_f8(128, kPgTile, false, false);
+            const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
+            int g = 0, nb = 0, item = 0;
+            uint32_t seen = 0;
+            bool ok = true, pending = false, pend_first = false;
+            int pend_slot = 0, pend_nb = 0, pend_item = 0;
+            int open = -1;                       // the item whose output is not announced yet
+            // the O product of the pending tile
+            auto flush = [&]() {
+                const int b = pend_nb & 1;
+                ok = pg_wait(&sh.p_full[b], uint32_t(pend_nb >> 1) & 1u, ab, p.status);
+                if (ok && pend_first && pend_item > 0)
+                    ok = pg_wait(&sh.o_empty, uint32_t(pend_item - 1) & 1u, ab, p.status);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t va = smem_u32(ring + pend_slot * kPgSlotBytes), wa = smem_u32(pbuf + b * kPgPBytes);
+#pragma unroll
+                for (int db = 0; db < 4; ++db)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
+                        mma_f8_ss(tbase + kPgColO + 64 * db,
+                                  sdesc_sw128(va + db * kPgBlockBytes + (k & 1) * 4096, 16, 1024),
+                                  sdesc_sw128(wa + k * 32, 16, 1024), k < 2 ? id_hi : id_lo,
+                                  !(pend_first && k == 0));
+                mma_commit(&sh.empty[pend_slot]);
+                mma_commit(&sh.p_empty[b]);
+                pending = false;
+            };
+            auto announce = [&](int which, int any) {
+                sh.item_any[which & 3] = any;
+                mbar_arrive(&sh.o_full);
+                mma_commit(&sh.o_full);
+                open = -1;
+            };
+            // the pending tile's O product, and the output of an item before this one. Also
+            // before a tile without a valid rank: the pending tile's slot must come free while
+            // the loads go on through a run of such tiles
+            auto settle = [&](int now) {
+                if (pending) flush();
+                if (ok && open >= 0 && open != now) announce(open, 1);
+            };
+            for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+                const int n = w.tiles(p);
+                g += 2;
+                int used = 0;
+                for (int i = 0; i < n && ok; ++i, ++g) {
+                    const int slot = pg_slot(g);
+                    ok = pg_wait(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
+                    if (!ok) break;
+                    seen ^= 1u << slot;
+                    if (sh.any[slot] == 0) {
+                        mbar_arrive(&sh.empty[slot]);
+                        settle(item);
+                        continue;
+                    }
+                    if (used == 0) ok = pg_wait(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                    if (ok) ok = pg_wait(&sh.s_empty[nb & 1], (uint32_t(nb >> 1) & 1u) ^ 1u, ab, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t ka = smem_u32(ring + slot * kPgSlotBytes);
+#pragma unroll
+                    for (int k = 0; k < kD / 32; ++k)
+                        mma_f8_ts(tbase + kPgColS + kPgTile * (nb & 1), tbase + kPgColQ + 8 * k,
+                                  sdesc_sw128(ka + (k >> 2) * kPgBlockBytes + (k & 3) * 32, 16, 1024), id_s, k != 0);
+                    mbar_arrive(&sh.s_full[nb & 1]);
+                    mma_commit(&sh.s_full[nb & 1]);
+                    settle(item);
+                    pending = true;
+                    open = item;
+                    pend_slot = slot; pend_nb = nb; pend_item = item; pend_first = used == 0;
+                    ++used; ++nb;
+                }
+                if (!ok) break;
+                if (used == 0) {                 // no valid rank in the whole item
+                    ok = pg_wait(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                    if (ok) settle(item);
+                    if (ok && item > 0) ok = pg_wait(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
+                    if (!ok) break;
+                    announce(item, 0);
+                }
+                mma_commit(&sh.q_empty);
+                w.next(n);
+            }
+            if (ok) settle(item);
+            mma_commit(&sh.drain);
+            mbar_wait(&sh.drain, 0, kPgWaitNs);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // -------------------------------------------------------------- softmax
+        const int part = lane >> 4, head = 16 * warp + (lane & 15);
+        const bool active = 16 * warp < heads;
+        const uint32_t trow = tbase + (uint32_t(warp * 32) << 16);
+        const float lo_factor = part ? 0.0625f : 1.f;
+        int g = 0, nb = 0, item = 0, votes = 0;
+        uint32_t seen = 0;
+        bool ok = true;
+        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+            const int n = w.tiles(p);
+            g += 2;
+            bool fresh = true;
+            float m_ref = -INFINITY, l = 0.f, sref = 0.f, f = 0.f;
+            for (int i = 0; i < n && ok; ++i, ++g) {
+                const int slot = pg_slot(g);
+                ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
+                if (!ok) break;
+                seen ^= 1u << slot;
+                const int any = sh.any[slot];
+                if (any == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                    continue;
+                }
+                const int b = nb & 1;
+                ok = pg_wait_warp(&sh.s_full[b], uint32_t(nb >> 1) & 1u, ab, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                if (fresh) f = sh.qfac[item & 3][head] * lo_factor;
+                const float4* scp = reinterpret_cast<const float4*>(&sh.scale[slot][32 * part]);
+                float s[32];
+                float mx = -INFINITY, smax = 0.f;
+                {
+                    uint32_t v0[32], v1[32];
+                    tmem_ld32(trow + kPgColS + kPgTile * b, v0);
+                    tmem_ld32(trow + kPgColS + kPgTile * b + 32, v1);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.s_empty[b]);
+                    // the head's other lane has the other part of q: swap halves and add
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float own = __uint_as_float(part ? v1[e] : v0[e]) * f;
+                        const float give = __uint_as_float(part ? v0[e] : v1[e]) * f;
+                        s[e] = own + __shfl_xor_sync(0xffffffffu, give, 16);
+                    }
+                }
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const float4 c4 = scp[e4];
+                    const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float& x = s[4 * e4 + e];
+                        x = c[e] >= 0.f ? x * c[e] : -INFINITY;
+                        mx = fmaxf(mx, x);
+                        smax = fmaxf(smax, c[e]);
+                    }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 16));
+                if (fresh) {
+                    m_ref = mx;
+                    sref = smax;
+                    fresh = false;
+                } else {
+                    // the reference follows the maximum in steps; the warps agree on it, because
+                    // a warp's TMEM lanes are columns of D, not heads
+                    const int vb = votes & 1;
+                    const bool grow = active && mx > m_ref + kPgSlack;
+                    const bool need = grow || smax > sref;
+                    const float mn = grow ? mx : m_ref, sn = fmaxf(sref, smax);
+                    const float fm = m_ref == -INFINITY ? 1.f : ex2_approx(m_ref - mn);
+                    if (part == 0) sh.fac[vb][head] = fm * (sref > 0.f ? sref / sn : 1.f);
+                    const bool wneed = __any_sync(0xffffffffu, need) != 0;
+                    __syncwarp();
+                    if (lane == 0) {
+                        sh.vote[vb][warp] = wneed;
+                        mbar_arrive(&sh.vote_bar);
+                    }
+                    ok = pg_wait_warp(&sh.vote_bar, uint32_t(votes) & 1u, ab, p.status);
+                    if (!ok) break;
+                    ++votes;
+                    if (sh.vote[vb][0] | sh.vote[vb][1] | sh.vote[vb][2] | sh.vote[vb][3]) {
+                        l *= fm;
+                        m_ref = mn;
+                        sref = sn;
+                        // the O products of the item's earlier tiles are complete
+                        ok = pg_wait_warp(&sh.p_empty[b ^ 1], uint32_t((nb - 1) >> 1) & 1u, ab, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 4 * heads; c += 16) {
+                            const int db = c / heads, h = c - db * heads;
+                            const uint32_t at = trow + kPgColO + 64 * db + h;
+                            uint32_t v[16];
+                            tmem_ld16(at, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                v[e] = __float_as_uint(__uint_as_float(v[e]) * sh.fac[vb][h + e]);
+                            tmem_st16(at, v);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                ok = pg_wait_warp(&sh.p_empty[b], (uint32_t(nb >> 1) & 1u) ^ 1u, ab, p.status);
+                if (!ok) break;
+                if (active) {
+                    const float off = kPgBias - (m_ref == -INFINITY ? 0.f : m_ref);
+                    const float inv = sref > 0.f ? 1.f / sref : 0.f;
+                    uint8_t* prow = pbuf + b * kPgPBytes + head * 128;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {            // 16 ranks: 16 bytes hi and 16 bytes lo
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4) {
+                            const float4 c4 = scp[4 * q + e4];
+                            const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+                            float x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float pr = ex2_approx(s[16 * q + 4 * e4 + e] + off);
+                                l += pr;
+                                x[e] = pr * (c[e] * inv);
+                            }
+                            const uint32_t a = e4m3x2(x[0], x[1]), d = e4m3x2(x[2], x[3]);
+                            const float2 av = e4m3x2_value(a), dv = e4m3x2_value(d);
+                            hi[e4] = a | d << 16;
+                            lo[e4] = e5m2x2(x[0] - av.x, x[1] - av.y) | e5m2x2(x[2] - dv.x, x[3] - dv.y) << 16;
+                        }
+                        const int ch = 2 * part + q;
+                        *reinterpret_cast<uint4*>(prow + ((ch ^ (head & 7)) << 4)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (head & 7)) << 4)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    const float both = l + __shfl_xor_sync(0xffffffffu, l, 16);
+                    if (part == 0) {
+                        sh.m[item & 3][head] = m_ref;
+                        sh.l[item & 3][head] = both;
+                    }
+                }
+                if (threadIdx.x == 0) sh.sref[item & 3] = sref;
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.p_full[b]);
+                    mbar_arrive(&sh.empty[slot]);
+                }
+                ++nb;
+            }
+            w.next(n);
+        }
+    } else {
+        // ------------------------------------- q into TMEM, output out of TMEM
+        const int quarter = warp & 3, part = lane >> 4, head = 16 * quarter + (lane & 15);
+        const bool active = 16 * quarter < heads;
+        const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
+        int g = 0, item = 0;
+        bool ok = true;
+        int t_prev = 0;
+        bool whole_prev = false, first_prev = false;
+
+        auto output = [&](int n_item, int t, bool whole, bool first) {
+            ok = pg_wait_warp(&sh.o_full, uint32_t(n_item) & 1u, ab, p.status);
+            if (!ok) return;
+            tc_fence_after();
+            const int st = n_item & 3;
+            const bool any = sh.item_any[st] != 0;
+            float* fin = sh.fin[quarter];
+            const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
+            for (int h = lane; h < heads; h += 32) {
+                // sums are in units of 2^(reference - bias)
+                const float mu = any ? sh.m[st][h] : -INFINITY;
+                const float m2 = mu == -INFINITY ? 0.f : mu - kPgBias, l = any ? sh.l[st][h] : 0.f;
+                const float so = any ? sh.sref[st] : 0.f;
+                if (whole) {
+                    const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
+                    // a NaN sum stays one; a sum of zero leaves the sink alone
+                    const float top = l == 0.f ? sink : fmaxf(m2, sink);
+                    const float base = top == -INFINITY ? 0.f : top;
+                    const float sum = l * ex2_approx(m2 - base) + (p.sink ? ex2_approx(sink - base) : 0.f);
+                    fin[h] = sum == 0.f ? 0.f : ex2_approx(m2 - base) * so / sum;
+                    if (quarter == 0)
+                        p.lse[int64_t(t) * p.H + head0 + h] =
+                            sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
+                } else {
+                    fin[h] = so;
+                    if (quarter == 0)
+                        p.part_ml[int64_t(part_at) * p.group_heads + h] = make_float2(l == 0.f ? -INFINITY : m2, l);
+                }
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int db = 0; db < 4; ++db) {
+                const int d = 128 * db + 32 * quarter + lane;
+#pragma unroll 1
+                for (int h = 0; h < heads; h += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(trow + kPgColO + 64 * db + h, v);
+                    tmem_wait_ld();
+                    if (whole) {
+                        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) +
+                                             (int64_t(t) * p.H + head0 + h) * kD + d;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            dst[e * kD] = __float2bfloat16_rn(any ? __uint_as_float(v[e]) * fin[h + e] : 0.f);
+                    } else {
+                        float* dst = p.part_o + (int64_t(part_at) * p.group_heads + h) * kD + d;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            dst[e * kD] = any ? __uint_as_float(v[e]) * fin[h + e] : 0.f;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty);
+        };
+
+        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+            const int n = w.tiles(p);
+            const int s0 = pg_slot(g), s1 = pg_slot(g + 1);
+            g += n + 2;
+            ok = pg_wait_warp(&sh.q_load[item & 1], uint32_t(item >> 1) & 1u, ab, p.status);
+            if (!ok) break;
+            uint32_t word[128];
+            float qf = 0.f;
+            if (active) {
+                const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128;
+                const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128;
+                // largest finite |q| of the row: each of the head's lanes looks at one half
+                uint32_t top = 0;
+#pragma unroll 8
+                for (int c = 0; c < 32; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>((part ? q1 : q0) + (c >> 3) * kPgBlockBytes +
+                                                                     (((c & 7) ^ (head & 7)) << 4));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a = xs[e] & 0x7fff7fffu;
+                        top = __vmaxu2(top, a & __vcmpltu2(a, 0x7f807f80u));
+                    }
+                }
+                top = max(top >> 16, top & 0xffffu);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                int e2 = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+                if (e2 < -100 || top == 0) e2 = top == 0 ? 0 : -100;
+                const float inv = __int_as_float((127 - e2) << 23);
+                qf = __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>((c < 32 ? q0 : q1) + ((c >> 3) & 3) * kPgBlockBytes +
+                                                                     (((c & 7) ^ (head & 7)) << 4));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t out[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a = bf16_lo(xs[e]), d = bf16_hi(xs[e]);
+                        a = (a + (a - a)) * inv;             // infinities become NaN: so do their scores
+                        d = (d + (d - d)) * inv;
+                        const uint32_t h = e4m3x2(a, d);
+                        const float2 hv = e4m3x2_value(h);
+                        out[e] = part ? e4m3x2((a - hv.x) * 16.f, (d - hv.y) * 16.f) : h;
+                    }
+                    word[2 * c] = out[0] | out[1] << 16;
+                    word[2 * c + 1] = out[2] | out[3] << 16;
+                }
+                if (part == 0) sh.qfac[item & 3][head] = qf;
+            }
+            __syncwarp();
+            if (lane == 0) {                     // five arrivals a slot, from four warps
+                mbar_arrive_cnt(&sh.empty[s0], quarter == 0 ? 2 : 1);
+                mbar_arrive_cnt(&sh.empty[s1], quarter == 0 ? 2 : 1);
+            }
+            if (item > 0) ok = pg_wait_warp(&sh.q_empty, uint32_t(item - 1) & 1u, ab, p.status);
+            if (!ok) break;
+            if (active) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) tmem_st8(trow + kPgColQ + 8 * c, word + 8 * c);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full);
+            if (item > 0) {
+                output(item - 1, t_prev, whole_prev, first_prev);
+                if (!ok) break;
+            }
+            t_prev = w.t;
+            whole_prev = w.k0 == 0 && n == pg_tiles(p, w.t);
+            first_prev = item == 0;
+            w.next(n);
+        }
+        if (ok && item > 0) output(item - 1, t_prev, whole_prev, first_prev);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kPgMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// Joins the parts of a token that several CTAs shared, in their order. Block
+// (c, y): the token that ends in CTA c, heads 8y .. 8y + 7 of its group, a warp each.
+__global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p, int ctas) {
+    const int4 end = p.meta[blockIdx.x];
+    if (end.x < 0) return;
+    const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
+    const int head0 = group * p.group_heads;
+    const int h = 8 * int(blockIdx.y) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (h >= p.group_heads || head0 + h >= p.H) return;
+    const long long total = *p.total;
+    auto part_of = [&](int c) {          // -1: CTA c has no tile
+        if (pg_first(total, c, ctas) == pg_first(total, c + 1, ctas)) return int64_t(-1);
+        return (int64_t(c) * p.groups + group) * 2 + (c == end.y ? end.z : 0);
+    };
+    const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
+    float top = sink;
+    bool nan = false;
+    for (int c = end.y + lane; c <= cta; c += 32) {
+        const int64_t at = part_of(c);
+        if (at < 0) continue;
+        const float2 ml = p.part_ml[at * p.group_heads + h];
+        if (ml.y != 0.f) top = fmaxf(top, ml.x);
+        nan |= ml.x != ml.x || ml.y != ml.y;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = p.sink ? ex2_approx(sink - base) : 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = end.y; c <= cta; ++c) {
+        const int64_t at = part_of(c);
+        if (at < 0) continue;
+        const float2 ml = p.part_ml[at * p.group_heads + h];
+        if (ml.y == 0.f) continue;
+        const float wgt = ex2_approx(ml.x - base);
+        sum += ml.y * wgt;
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (at * p.group_heads + h) * kD) + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = __ldcg(src + 32 * k);
+            acc[k].x = fmaf(wgt, v.x, acc[k].x);
+            acc[k].y = fmaf(wgt, v.y, acc[k].y);
+            acc[k].z = fmaf(wgt, v.z, acc[k].z);
+            acc[k].w = fmaf(wgt, v.w, acc[k].w);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2* dst = reinterpret_cast<uint2*>(p.o + (int64_t(end.x) * p.H + head0 + h) * kD) + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                                 pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (lane == 0) p.lse[int64_t(end.x) * p.H + head0 + h] = sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
+}
+
+namespace {
+
+struct PgPlan { int groups, group_heads; size_t meta, total, ml, o, bytes; };
+
+PgPlan plan_paged(int H) {
+    PgPlan x{};
+    x.groups = (H + kPgHeads - 1) / kPgHeads;
+    x.group_heads = (H / 16 + x.groups - 1) / x.groups * 16;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes, 256); return o; };
+    x.total = take(8);
+    x.meta = take(size_t(kPgMaxCtas) * sizeof(int4));
+    x.ml = take(size_t(kPgMaxCtas) * 2 * x.group_heads * sizeof(float2));
+    x.o = take(size_t(kPgMaxCtas) * 2 * x.group_heads * kD * 4);
+    x.bytes = off;
+    return x;
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kPgHeads * 32) fwd_paged_kernel(const PagedArgs p) {
-    __shared__ uint4 tile[kPgTile][kD / 16];
-    __shared__ int64_t row_of[kPgTile];
-    __shared__ float scale_of[kPgTile];
-    const int t = blockIdx.x, h = blockIdx.y * kPgHeads + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const CacheView& c = p.cache;
-    const int64_t limit = int64_t(p.max_pages) << c.page_shift;
-    int len = __ldg(p.lens + t);
-    if (len < 0 || len > limit) {
-        if (threadIdx.x == 0) flag_status(p.status, SMLA_ERR_INDEX);
-        len = len < 0 ? 0 : int(limit);
-    }
-    const int b = p.seq ? __ldg(p.seq + t) : t;
-    if (b < 0 || b >= p.B) {
-        if (threadIdx.x == 0) flag_status(p.status, SMLA_ERR_INDEX);
-        len = 0;
-    }
-    const int ranks = p.topk ? (len > 0 ? p.K : 0) : len;
-    float qf[16], acc[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    const uint4* qrow = reinterpret_cast<const uint4*>(p.q) + (int64_t(t) * p.H + h) * (kD / 8) + 2 * lane;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint4 v = __ldg(qrow + k);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { qf[8 * k + 2 * e] = bf16_lo(w[e]); qf[8 * k + 2 * e + 1] = bf16_hi(w[e]); }
-    }
-    const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY;
-    float m = sink, l = p.sink ? 1.f : 0.f;
-    for (int r0 = 0; r0 < ranks; r0 += kPgTile) {
-        __syncthreads();
-        if (threadIdx.x < kPgTile) {
-            const int r = r0 + int(threadIdx.x);
-            int pos = -1;
-            if (r < ranks) {
-                pos = p.topk ? __ldg(p.topk + int64_t(t) * p.K + r) : r;
-                if (pos < -1 || pos >= len) { flag_status(p.status, SMLA_ERR_INDEX); pos = -1; }
-            }
-            int64_t row = -1;
-            float sc = 0.f;
-            if (pos >= 0) {
-                const int page = __ldg(p.table + int64_t(b) * p.max_pages + (pos >> c.page_shift));
-                if (page < 0 || page >= c.num_pages) {
-                    flag_status(p.status, SMLA_ERR_INDEX);
-                } else {
-                    row = (int64_t(page) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
-                    sc = __ldg(c.scales + (row >> c.block_shift));
-                }
-            }
-            row_of[threadIdx.x] = row;
-            scale_of[threadIdx.x] = sc;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < kPgTile * (kD / 16); i += blockDim.x) {
-            const int rr = i / (kD / 16), col = i % (kD / 16);
-            const int64_t row = row_of[rr];
-            tile[rr][col] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.pages + row * kD) + col)
-                                     : make_uint4(0, 0, 0, 0);
-        }
-        __syncthreads();
-        float my_s = -INFINITY;
-        for (int rr = 0; rr < kPgTile; ++rr) {
-            float x[16], part = 0.f;
-            unpack16(tile[rr][lane], x);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) part = fmaf(qf[k], x[k], part);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-            if (lane == rr) my_s = part * scale_of[rr] * p.scale;
-        }
-        const bool valid = row_of[lane] >= 0;
-        if (!valid) my_s = -INFINITY;
-        float tmax = my_s;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, off));
-        const float m_new = fmaxf(m, tmax);
-        if (!__any_sync(0xffffffffu, valid)) continue;
-        const float base = m_new == -INFINITY ? 0.f : m_new;
-        const float e = valid ? expf(my_s - base) : 0.f;
-        const float corr = m == -INFINITY ? 0.f : expf(m - base);
-        float sum = e;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        l = l * corr + sum;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) acc[k] *= corr;
-        for (int rr = 0; rr < kPgTile; ++rr) {
-            if (row_of[rr] < 0) continue;
-            const float w = __shfl_sync(0xffffffffu, e, rr) * scale_of[rr];
-            float x[16];
-            unpack16(tile[rr][lane], x);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) acc[k] = fmaf(w, x[k], acc[k]);
-        }
-        m = m_new;
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    uint4* orow = reinterpret_cast<uint4*>(p.o) + (int64_t(t) * p.H + h) * (kD / 8) + 2 * lane;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        orow[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
-                             pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
-                             pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
-                             pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
-    if (lane == 0) p.lse[int64_t(t) * p.H + h] = l == 0.f ? -INFINITY : m + logf(l);
-}
-
-size_t paged_scratch_bytes(int, int) { return 0; }
+size_t paged_scratch_bytes(int T, int H) { return T > 0 ? plan_paged(H).bytes : 0; }
 
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
-    fwd_paged_kernel<<<dim3(a.T, a.H / kPgHeads), kPgHeads * 32, 0, s>>>(a);
-    note_launch();
+    static bool attr_done[64] = {false};
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(fwd_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmem);
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+    }
+    const PgPlan plan = plan_paged(a.H);
+    const CacheView& c = a.cache;
+    const uint64_t rows = uint64_t(c.num_pages) << c.page_shift;
+    const uint32_t box = (1 << c.page_shift) < kPgTile ? uint32_t(1) << c.page_shift : uint32_t(kPgTile);
+    CUtensorMap mq, mb, mr;
+    if (!make_tmap_bf16_2d(&mq, a.q, uint64_t(a.T) * a.H, kD, kD, plan.group_heads, 64, true) ||
+        !make_tmap_u8_rows(&mb, c.pages, rows, box) || !make_tmap_u8_rows(&mr, c.pages, rows, 1))
+        return cudaErrorInvalidValue;
+    PgParams p{};
+    p.table = a.table; p.seq = a.seq; p.lens = a.lens; p.topk = a.topk;
+    p.scales = c.scales; p.sink = a.sink; p.o = a.o; p.lse = a.lse;
+    p.T = a.T; p.H = a.H; p.K = a.K; p.B = a.B; p.max_pages = a.max_pages;
+    p.num_pages = c.num_pages; p.page_shift = c.page_shift; p.block_shift = c.block_shift;
+    p.groups = plan.groups; p.group_heads = plan.group_heads;
+    p.scale = a.scale; p.status = a.status;
+    p.total = reinterpret_cast<long long*>(a.scratch + plan.total);
+    p.meta = reinterpret_cast<int4*>(a.scratch + plan.meta);
+    p.part_ml = reinterpret_cast<float2*>(a.scratch + plan.ml);
+    p.part_o = reinterpret_cast<float*>(a.scratch + plan.o);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int ctas = (sms < kPgMaxCtas ? sms : kPgMaxCtas) / plan.groups;
+    fwd_paged_kernel<<<ctas * plan.groups, kPgThreads, kPgSmem, s>>>(mq, mb, mr, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    combine_paged_kernel<<<dim3(ctas * plan.groups, (plan.group_heads + 7) / 8), 256, 0, s>>>(p, ctas);
+    note_launch(2);
     return cudaGetLastError();
 }
 

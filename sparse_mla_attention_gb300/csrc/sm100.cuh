@@ -94,6 +94,18 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, int
         : "memory");
 }
 
+// Four rows r0..r3 of a 2-D tensor (the map's box is one row high), columns from
+// x on, into four consecutive box rows in smem.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, int x, int r0, int r1,
+                                            int r2, int r3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Prefetch one box of a 2-D tiled tensor into L2 (no shared-memory destination).
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
@@ -204,6 +216,26 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// The same two forms for kind::f8f6f4 (8-bit operands, fp32 accumulate).
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrives once on `bar` when every tcgen05.mma issued so far by this thread completes.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile(
@@ -261,6 +293,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+// Each thread of the warp writes 16 consecutive 32-bit columns of its lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // 2^x by the PTX ex2.approx.ftz.f32 instruction (relative error about 2^-22;
 // results below the smallest normal float flush to zero).
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -273,8 +315,8 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // Shared-memory matrix descriptor, 128-byte swizzle. Tiles are stored as
 // 8-row x 128-byte swizzle atoms (1024 B, 1024-byte aligned).
 //   K-major operand:  lbo unused, sbo = byte stride between 8-row groups.
-//   MN-major operand: lbo = byte stride between 64-element MN blocks,
-//                     sbo = byte stride between 8-row K groups.
+//   MN-major operand: lbo = byte stride between 128-byte MN blocks (64 elements of
+//                     16 bits, 128 of 8 bits), sbo = byte stride between 8-row K groups.
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
     uint64_t d = 0;
     d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
@@ -292,6 +334,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
            | (1u << 10)                      // B: bf16
            | (uint32_t(a_mn_major) << 15) | (uint32_t(b_mn_major) << 16) |
            (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// Instruction descriptor: kind::f8f6f4, fp32 accumulator; A is e4m3, B e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn_major, bool b_e5m2) {
+    return (1u << 4)                         // D: f32
+           | (uint32_t(b_e5m2) << 10)        // B: e4m3 0, e5m2 1 (A: e4m3 0)
+           | (uint32_t(a_mn_major) << 15) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
 }  // namespace sm100

@@ -44,6 +44,21 @@ inline bool make_tmap_bf16_2d(CUtensorMap* m, const void* base, uint64_t rows, u
     return r == CUDA_SUCCESS;
 }
 
+// Row-major 2-D byte tensor [rows, 512], box of box_rows x 128 bytes, 128-byte
+// swizzle (box_rows = 1: also the map of a four-row gather).
+inline bool make_tmap_u8_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+    auto fn = encode_tiled_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {512, rows};
+    cuuint64_t strides[1] = {512};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // Two row-major bf16 tensors of the same shape [T, H, 512] (rows of 512
 // contiguous elements), a and b, seen as one 5-D tensor whose dimensions are,
 // innermost first: column inside a 64-column block (64), head (H, stride one

@@ -400,6 +400,37 @@ def test_long_sequences_are_split(H):
     _attend_and_check(pool, table, lens, H, seed=H)
 
 
+@pytest.mark.parametrize("H,page", [(128, 64), (64, 16)])
+def test_many_tiles_and_sequences_for_each_processor(H, page):
+    # tens of tiles and several items for each of the GPU's SMs: every buffer and barrier comes round
+    rng = np.random.default_rng(H)
+    lens = [9000, 1, 64, 5000, 700, 700, 65, 4000, 0, 0, 3] + [int(n) for n in rng.integers(1, 2500, size=33)]
+    lens = lens if H == 128 else [2 * n for n in lens]
+    pool = Pool(sum(-(-n // page) for n in lens) + 2, page, 16, seed=33)
+    table = pool.place(lens)
+    pool.fill(table, lens)
+    _attend_and_check(pool, table, lens, H, seed=34)
+
+
+@pytest.mark.parametrize("H,T", [(128, 300), (48, 700)])
+def test_many_tokens_with_picks(H, T):
+    rng = np.random.default_rng(T)
+    lens_b = [3000, 700, 5000]
+    pool = Pool(150, 64, 32, seed=35)
+    table = pool.place(lens_b)
+    pool.fill(table, lens_b)
+    seq = rng.integers(0, 3, size=T)
+    lens = np.array([rng.integers(1, lens_b[b] + 1) for b in seq])
+    K = 449
+    topk = np.array([rng.integers(0, n, size=K) for n in lens])
+    # whole tiles without a valid rank, in front, behind, and everywhere
+    for t in range(0, T, 7):
+        topk[t, :64 * (t % 8)] = -1
+    for t in range(3, T, 11):
+        topk[t, 64 * (t % 7):] = -1
+    _attend_and_check(pool, table, lens, H, seed=36, topk=topk, seq=seq, sink=H == 48)
+
+
 def test_scales_of_every_size_and_scores_far_apart():
     # rows whose blocks' scales differ by 2^20, scores that rise along the sequence
     # (the running maximum grows again and again), and one row that outweighs all others

@@ -97,7 +97,6 @@ struct PgParams {
     float scale;
     unsigned* status;
     int4* meta;                                  // [CTAs] end of a split token: {t, first CTA, its part, 0}
-    long long* total;                            // tiles of all tokens
     float2* part_ml;                             // [CTAs][2][group_heads] maximum (log2) and sum
     float* part_o;                               // [CTAs][2][group_heads][512]
 };
@@ -140,13 +139,28 @@ static_assert(kPgSlots % 2 == 0 && kPgSlots >= 6, "a slot belongs to one of the 
 __device__ __forceinline__ int pg_slot(int g) { return g % kPgSlots; }
 __device__ __forceinline__ uint32_t pg_parity(uint32_t bits, int slot) { return (bits >> slot) & 1u; }
 
-__device__ __forceinline__ long long pg_first(long long total, int c, int ctas) { return total * c / ctas; }
+// The tiles are dealt out in runs of per or (the first rem CTAs) per + 1.
+struct PgDeal {
+    long long per, rem;
+    __device__ __forceinline__ PgDeal(long long total, int ctas) : per(total / ctas), rem(total - per * ctas) {}
+    __device__ __forceinline__ long long first(int c) const { return per * c + (c < rem ? c : rem); }
+    __device__ __forceinline__ int owner(long long tile) const {
+        const long long longer = rem * (per + 1);
+        return int(tile < longer ? tile / (per + 1) : rem + (tile - longer) / per);
+    }
+};
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
+    return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 e4m3x2_half(uint32_t v) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3));
 }
 __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3)));
@@ -174,12 +188,10 @@ __device__ void pg_locate(const PgParams& p, PgShared& sh, int c, int ctas) {
         if (w < warp) before += sh.sum[w];
         total += sh.sum[w];
     }
-    const long long a = pg_first(total, c, ctas), b = pg_first(total, c + 1, ctas);
+    const PgDeal deal(total, ctas);
+    const long long a = deal.first(c), b = deal.first(c + 1);
     long long at = before + x - mine;
-    if (threadIdx.x == 0) {
-        sh.count = int(b - a);
-        if (blockIdx.x == 0) *p.total = total;
-    }
+    if (threadIdx.x == 0) sh.count = int(b - a);
     if (a < b && at <= a && a < at + mine) {
         int t = t0;
         for (;; ++t) {
@@ -192,8 +204,8 @@ __device__ void pg_locate(const PgParams& p, PgShared& sh, int c, int ctas) {
         // this CTA ends a token that began in an earlier one: it names the parts to join
         int4 end = make_int4(-1, 0, 0, 0);
         if (a > at && b - at >= pg_tiles(p, t)) {
-            const int first = int(((at + 1) * ctas - 1) / total);
-            end = make_int4(t, first, pg_first(total, first, ctas) == at ? 0 : 1, 0);
+            const int first = deal.owner(at);
+            end = make_int4(t, first, deal.first(first) == at ? 0 : 1, 0);
         }
         p.meta[blockIdx.x] = end;
     } else if (a >= b && threadIdx.x == 0) {
@@ -700,66 +712,76 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             g += n + 2;
             ok = pg_wait_warp(&sh.q_load[item & 1], uint32_t(item >> 1) & 1u, ab, p.status);
             if (!ok) break;
-            uint32_t word[128];
-            float qf = 0.f;
+            uint8_t* qhalf = ring + (part ? s1 : s0) * kPgSlotBytes + head * 128;
+            auto piece = [&](int c) {            // 16 bytes of the row's half: 8 values
+                return reinterpret_cast<uint4*>(qhalf + (c >> 3) * kPgBlockBytes + (((c & 7) ^ (head & 7)) << 4));
+            };
             if (active) {
-                const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128;
-                const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128;
-                // largest finite |q| of the row: each of the head's lanes looks at one half
+                // largest |q| of the row; each of the head's lanes has one half
                 uint32_t top = 0;
 #pragma unroll 8
                 for (int c = 0; c < 32; ++c) {
-                    const uint4 x = *reinterpret_cast<const uint4*>((part ? q1 : q0) + (c >> 3) * kPgBlockBytes +
-                                                                     (((c & 7) ^ (head & 7)) << 4));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t a = xs[e] & 0x7fff7fffu;
-                        top = __vmaxu2(top, a & __vcmpltu2(a, 0x7f807f80u));
-                    }
+                    const uint4 x = *piece(c);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                 __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
                 }
                 top = max(top >> 16, top & 0xffffu);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 int e2 = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-                if (e2 < -100 || top == 0) e2 = top == 0 ? 0 : -100;
+                e2 = top == 0 || e2 > 119 ? 0 : e2 < -100 ? -100 : e2;
                 const float inv = __int_as_float((127 - e2) << 23);
-                qf = __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
-#pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    const uint4 x = *reinterpret_cast<const uint4*>((c < 32 ? q0 : q1) + ((c >> 3) & 3) * kPgBlockBytes +
-                                                                     (((c & 7) ^ (head & 7)) << 4));
+                // infinities and NaN in q make every score of the head NaN
+                if (part == 0)
+                    sh.qfac[item & 3][head] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                                             : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
+                // in place: eight values become eight bytes hi and eight bytes lo
+#pragma unroll 4
+                for (int c = 0; c < 32; ++c) {
+                    uint4* at = piece(c);
+                    const uint4 x = *at;
                     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t out[4];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float a = bf16_lo(xs[e]), d = bf16_hi(xs[e]);
-                        a = (a + (a - a)) * inv;             // infinities become NaN: so do their scores
-                        d = (d + (d - d)) * inv;
-                        const uint32_t h = e4m3x2(a, d);
-                        const float2 hv = e4m3x2_value(h);
-                        out[e] = part ? e4m3x2((a - hv.x) * 16.f, (d - hv.y) * 16.f) : h;
+                        // half precision holds a scaled value and what e4m3 leaves of it exactly
+                        const __half2 v = __floats2half2_rn(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
+                        hi[e] = e4m3x2(v);
+                        lo[e] = e4m3x2(__hmul2(__hsub2(v, e4m3x2_half(hi[e])), __float2half2_rn(16.f)));
                     }
-                    word[2 * c] = out[0] | out[1] << 16;
-                    word[2 * c + 1] = out[2] | out[3] << 16;
+                    *at = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
+                                     lo[2] | lo[3] << 16);
                 }
-                if (part == 0) sh.qfac[item & 3][head] = qf;
             }
             __syncwarp();
-            if (lane == 0) {                     // five arrivals a slot, from four warps
-                mbar_arrive_cnt(&sh.empty[s0], quarter == 0 ? 2 : 1);
-                mbar_arrive_cnt(&sh.empty[s1], quarter == 0 ? 2 : 1);
-            }
             if (item > 0) ok = pg_wait_warp(&sh.q_empty, uint32_t(item - 1) & 1u, ab, p.status);
             if (!ok) break;
             if (active) {
                 tc_fence_after();
+                const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128 + 8 * part;
+                const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128 + 8 * part;
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {   // 32 values of the row's part
+                    const uint8_t* src = (c < 8 ? q0 : q1) + ((c >> 1) & 3) * kPgBlockBytes;
+                    uint32_t word[8];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) tmem_st8(trow + kPgColQ + 8 * c, word + 8 * c);
+                    for (int k = 0; k < 4; ++k) {
+                        const int ch = 4 * (c & 1) + k;
+                        const uint2 x = *reinterpret_cast<const uint2*>(src + ((ch ^ (head & 7)) << 4));
+                        word[2 * k] = x.x;
+                        word[2 * k + 1] = x.y;
+                    }
+                    tmem_st8(trow + kPgColQ + 8 * c, word);
+                }
                 tmem_wait_st();
                 tc_fence_before();
             }
+            fence_proxy_async_smem();            // the slots' next loads come after these writes
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full);
+            if (lane == 0) {
+                mbar_arrive(&sh.q_full);
+                mbar_arrive_cnt(&sh.empty[s0], quarter == 0 ? 2 : 1);    // five arrivals, from four warps
+                mbar_arrive_cnt(&sh.empty[s1], quarter == 0 ? 2 : 1);
+            }
             if (item > 0) {
                 output(item - 1, t_prev, whole_prev, first_prev);
                 if (!ok) break;
@@ -780,65 +802,76 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 }
 
 // Joins the parts of a token that several CTAs shared, in their order. Block
-// (c, y): the token that ends in CTA c, heads 8y .. 8y + 7 of its group, a warp each.
-__global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p, int ctas) {
+// (c, y): the token that ends in CTA c, heads 2y and 2y + 1 of its group, 128
+// threads each (four columns a thread).
+__global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
+    __shared__ float wgt[2][kPgMaxCtas];
+    __shared__ float red[8];
     const int4 end = p.meta[blockIdx.x];
     if (end.x < 0) return;
     const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
     const int head0 = group * p.group_heads;
-    const int h = 8 * int(blockIdx.y) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int side = threadIdx.x >> 7, lane = threadIdx.x & 127;
+    const int h = 2 * int(blockIdx.y) + side;            // heads come in sixteens: both or neither
     if (h >= p.group_heads || head0 + h >= p.H) return;
-    const long long total = *p.total;
-    auto part_of = [&](int c) {          // -1: CTA c has no tile
-        if (pg_first(total, c, ctas) == pg_first(total, c + 1, ctas)) return int64_t(-1);
-        return (int64_t(c) * p.groups + group) * 2 + (c == end.y ? end.z : 0);
+    const int n = cta - end.y + 1;                       // parts, at most the CTAs of a group
+    auto part_of = [&](int i) {
+        return (int64_t(end.y + i) * p.groups + group) * 2 + (i == 0 ? end.z : 0);
     };
     const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
+    float2 ml[2];
     float top = sink;
-    bool nan = false;
-    for (int c = end.y + lane; c <= cta; c += 32) {
-        const int64_t at = part_of(c);
-        if (at < 0) continue;
-        const float2 ml = p.part_ml[at * p.group_heads + h];
-        if (ml.y != 0.f) top = fmaxf(top, ml.x);
-        nan |= ml.x != ml.x || ml.y != ml.y;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = lane + 128 * k;
+        ml[k] = i < n ? p.part_ml[part_of(i) * p.group_heads + h] : make_float2(-INFINITY, 0.f);
+        if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, red[4 * side + k]);
     const float base = top == -INFINITY ? 0.f : top;
-    float sum = p.sink ? ex2_approx(sink - base) : 0.f;
-    float4 acc[4];
+    __syncthreads();
+    float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = end.y; c <= cta; ++c) {
-        const int64_t at = part_of(c);
-        if (at < 0) continue;
-        const float2 ml = p.part_ml[at * p.group_heads + h];
-        if (ml.y == 0.f) continue;
-        const float wgt = ex2_approx(ml.x - base);
-        sum += ml.y * wgt;
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + (at * p.group_heads + h) * kD) + lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldcg(src + 32 * k);
-            acc[k].x = fmaf(wgt, v.x, acc[k].x);
-            acc[k].y = fmaf(wgt, v.y, acc[k].y);
-            acc[k].z = fmaf(wgt, v.z, acc[k].z);
-            acc[k].w = fmaf(wgt, v.w, acc[k].w);
-        }
+    for (int k = 0; k < 2; ++k) {
+        const int i = lane + 128 * k;
+        const float w = ml[k].y == 0.f ? 0.f : ex2_approx(ml[k].x - base);
+        if (i < n) wgt[side][i] = w;
+        sum += w * ml[k].y;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint2* dst = reinterpret_cast<uint2*>(p.o + (int64_t(end.x) * p.H + head0 + h) * kD) + lane;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                                 pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = p.sink ? ex2_approx(sink - base) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += red[4 * side + k];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t step = int64_t(p.groups) * 2 * p.group_heads * (kD / 4);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + lane;
+    const float4* rest = src + (part_of(1) * p.group_heads + h) * (kD / 4);
+    auto add = [&](const float4& v, float w) {
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+    };
+    add(__ldcg(src + (part_of(0) * p.group_heads + h) * (kD / 4)), wgt[side][0]);
+#pragma unroll 8
+    for (int i = 1; i < n; ++i) add(__ldcg(rest + (i - 1) * step), wgt[side][i]);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    reinterpret_cast<uint2*>(p.o + (int64_t(end.x) * p.H + head0 + h) * kD)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0) p.lse[int64_t(end.x) * p.H + head0 + h] = sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
 }
 
 namespace {
 
-struct PgPlan { int groups, group_heads; size_t meta, total, ml, o, bytes; };
+struct PgPlan { int groups, group_heads; size_t meta, ml, o, bytes; };
 
 PgPlan plan_paged(int H) {
     PgPlan x{};
@@ -846,7 +879,6 @@ PgPlan plan_paged(int H) {
     x.group_heads = (H / 16 + x.groups - 1) / x.groups * 16;
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes, 256); return o; };
-    x.total = take(8);
     x.meta = take(size_t(kPgMaxCtas) * sizeof(int4));
     x.ml = take(size_t(kPgMaxCtas) * 2 * x.group_heads * sizeof(float2));
     x.o = take(size_t(kPgMaxCtas) * 2 * x.group_heads * kD * 4);
@@ -883,7 +915,6 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     p.num_pages = c.num_pages; p.page_shift = c.page_shift; p.block_shift = c.block_shift;
     p.groups = plan.groups; p.group_heads = plan.group_heads;
     p.scale = a.scale; p.status = a.status;
-    p.total = reinterpret_cast<long long*>(a.scratch + plan.total);
     p.meta = reinterpret_cast<int4*>(a.scratch + plan.meta);
     p.part_ml = reinterpret_cast<float2*>(a.scratch + plan.ml);
     p.part_o = reinterpret_cast<float*>(a.scratch + plan.o);
@@ -892,7 +923,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     fwd_paged_kernel<<<ctas * plan.groups, kPgThreads, kPgSmem, s>>>(mq, mb, mr, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    combine_paged_kernel<<<dim3(ctas * plan.groups, (plan.group_heads + 7) / 8), 256, 0, s>>>(p, ctas);
+    combine_paged_kernel<<<dim3(ctas * plan.groups, plan.group_heads / 2), 256, 0, s>>>(p);
     note_launch(2);
     return cudaGetLastError();
 }

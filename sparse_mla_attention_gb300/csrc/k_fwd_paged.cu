@@ -103,6 +103,7 @@ struct PgParams {
 
 __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                         unsigned* status) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (mbar_wait(bar, parity, kPgWaitNs)) return true;
     *abort_flag = 1;
@@ -216,9 +217,12 @@ __device__ void pg_locate(const PgParams& p, PgShared& sh, int c, int ctas) {
 // The CTA's items: parts [k0, k0 + n) of the tiles of token t.
 struct PgWalk {
     int t, k0, left;
-    __device__ __forceinline__ PgWalk(const PgShared& sh) : t(sh.t0), k0(sh.k0), left(sh.count) {}
+    // (the shuffles tell the compiler that a warp's lanes agree)
+    __device__ __forceinline__ PgWalk(const PgShared& sh)
+        : t(__shfl_sync(0xffffffffu, sh.t0, 0)), k0(__shfl_sync(0xffffffffu, sh.k0, 0)),
+          left(__shfl_sync(0xffffffffu, sh.count, 0)) {}
     __device__ __forceinline__ int tiles(const PgParams& p) const {
-        const int n = pg_tiles(p, t) - k0;
+        const int n = __shfl_sync(0xffffffffu, pg_tiles(p, t), 0) - k0;
         return n < left ? n : left;
     }
     __device__ __forceinline__ void next(int n) { left -= n; ++t; k0 = 0; }
@@ -393,91 +397,107 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         __syncwarp();
     } else if (warp == kPgMmaWarp) {
         // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            const uint32_t id_s = idesc_f8(128, kPgTile, false, false);
-            const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
-            int g = 0, nb = 0, item = 0;
-            uint32_t seen = 0;
-            bool ok = true, pending = false, pend_first = false;
-            int pend_slot = 0, pend_nb = 0, pend_item = 0;
-            int open = -1;                       // the item whose output is not announced yet
-            // the O product of the pending tile
-            auto flush = [&]() {
-                const int b = pend_nb & 1;
-                ok = pg_wait(&sh.p_full[b], uint32_t(pend_nb >> 1) & 1u, ab, p.status);
-                if (ok && pend_first && pend_item > 0)
-                    ok = pg_wait(&sh.o_empty, uint32_t(pend_item - 1) & 1u, ab, p.status);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t va = smem_u32(ring + pend_slot * kPgSlotBytes), wa = smem_u32(pbuf + b * kPgPBytes);
+        // The whole warp walks the tiles, so that descriptors stay in uniform registers; one
+        // elected lane issues.
+        const uint32_t id_s = idesc_f8(128, kPgTile, false, false);
+        const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
+        const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
+        const bool leader = elect_one();
+        int g = 0, nb = 0, item = 0;
+        uint32_t seen = 0;
+        bool ok = true, pending = false, pend_first = false;
+        int pend_slot = 0, pend_nb = 0, pend_item = 0;
+        int open = -1;                           // the item whose output is not announced yet
+        // the O product of the pending tile
+        auto flush = [&]() {
+            const int b = pend_nb & 1;
+            ok = pg_wait_warp(&sh.p_full[b], uint32_t(pend_nb >> 1) & 1u, ab, p.status);
+            if (ok && pend_first && pend_item > 0)
+                ok = pg_wait_warp(&sh.o_empty, uint32_t(pend_item - 1) & 1u, ab, p.status);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t va = ring_desc + uint32_t(pend_slot) * (kPgSlotBytes >> 4);
+            const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
+            if (leader) {
 #pragma unroll
                 for (int db = 0; db < 4; ++db)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
                         mma_f8_ss(tbase + kPgColO + 64 * db,
-                                  sdesc_sw128(va + db * kPgBlockBytes + (k & 1) * 4096, 16, 1024),
-                                  sdesc_sw128(wa + k * 32, 16, 1024), k < 2 ? id_hi : id_lo,
-                                  !(pend_first && k == 0));
+                                  va + ((db * kPgBlockBytes + (k & 1) * 4096) >> 4), wa + 2 * k,
+                                  k < 2 ? id_hi : id_lo, !(pend_first && k == 0));
                 mma_commit(&sh.empty[pend_slot]);
                 mma_commit(&sh.p_empty[b]);
-                pending = false;
-            };
-            auto announce = [&](int which, int any) {
+            }
+            __syncwarp();
+            pending = false;
+        };
+        auto announce = [&](int which, int any) {
+            if (leader) {
                 sh.item_any[which & 3] = any;
                 mbar_arrive(&sh.o_full);
                 mma_commit(&sh.o_full);
-                open = -1;
-            };
-            // the pending tile's O product, and the output of an item before this one. Also
-            // before a tile without a valid rank: the pending tile's slot must come free while
-            // the loads go on through a run of such tiles
-            auto settle = [&](int now) {
-                if (pending) flush();
-                if (ok && open >= 0 && open != now) announce(open, 1);
-            };
-            for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-                const int n = w.tiles(p);
-                g += 2;
-                int used = 0;
-                for (int i = 0; i < n && ok; ++i, ++g) {
-                    const int slot = pg_slot(g);
-                    ok = pg_wait(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
-                    if (!ok) break;
-                    seen ^= 1u << slot;
-                    if (sh.any[slot] == 0) {
-                        mbar_arrive(&sh.empty[slot]);
-                        settle(item);
-                        continue;
-                    }
-                    if (used == 0) ok = pg_wait(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
-                    if (ok) ok = pg_wait(&sh.s_empty[nb & 1], (uint32_t(nb >> 1) & 1u) ^ 1u, ab, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t ka = smem_u32(ring + slot * kPgSlotBytes);
+            }
+            __syncwarp();
+            open = -1;
+        };
+        // the pending tile's O product, and the output of an item before this one. Also
+        // before a tile without a valid rank: the pending tile's slot must come free while
+        // the loads go on through a run of such tiles
+        auto settle = [&](int now) {
+            if (pending) flush();
+            if (ok && open >= 0 && open != now) announce(open, 1);
+        };
+        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+            const int n = w.tiles(p);
+            g += 2;
+            int used = 0;
+            for (int i = 0; i < n && ok; ++i, ++g) {
+                const int slot = pg_slot(g);
+                ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
+                if (!ok) break;
+                seen ^= 1u << slot;
+                if (sh.any[slot] == 0) {
+                    __syncwarp();
+                    if (leader) mbar_arrive(&sh.empty[slot]);
+                    settle(item);
+                    continue;
+                }
+                if (used == 0) ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                if (ok) ok = pg_wait_warp(&sh.s_empty[nb & 1], (uint32_t(nb >> 1) & 1u) ^ 1u, ab, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ka = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < kD / 32; ++k)
                         mma_f8_ts(tbase + kPgColS + kPgTile * (nb & 1), tbase + kPgColQ + 8 * k,
-                                  sdesc_sw128(ka + (k >> 2) * kPgBlockBytes + (k & 3) * 32, 16, 1024), id_s, k != 0);
+                                  ka + (((k >> 2) * kPgBlockBytes + (k & 3) * 32) >> 4), id_s, k != 0);
                     mbar_arrive(&sh.s_full[nb & 1]);
                     mma_commit(&sh.s_full[nb & 1]);
-                    settle(item);
-                    pending = true;
-                    open = item;
-                    pend_slot = slot; pend_nb = nb; pend_item = item; pend_first = used == 0;
-                    ++used; ++nb;
                 }
-                if (!ok) break;
-                if (used == 0) {                 // no valid rank in the whole item
-                    ok = pg_wait(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
-                    if (ok) settle(item);
-                    if (ok && item > 0) ok = pg_wait(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
-                    if (!ok) break;
-                    announce(item, 0);
-                }
-                mma_commit(&sh.q_empty);
-                w.next(n);
+                __syncwarp();
+                settle(item);
+                pending = true;
+                open = item;
+                pend_slot = slot; pend_nb = nb; pend_item = item; pend_first = used == 0;
+                ++used; ++nb;
             }
-            if (ok) settle(item);
+            if (!ok) break;
+            if (used == 0) {                     // no valid rank in the whole item
+                ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                if (ok) settle(item);
+                if (ok && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
+                if (!ok) break;
+                announce(item, 0);
+            }
+            if (leader) mma_commit(&sh.q_empty);
+            __syncwarp();
+            w.next(n);
+        }
+        if (ok) settle(item);
+        if (leader) {
             mma_commit(&sh.drain);
             mbar_wait(&sh.drain, 0, kPgWaitNs);
         }

@@ -280,7 +280,8 @@ typedef struct smla_paged_dims {
     int32_t D;          /* must be 512 */
     int32_t topk;       /* ranks per token; 0: every visible position (topk == NULL) */
     int32_t B;          /* rows of table (sequences) */
-    int32_t max_pages;  /* columns of table; max_pages * page_size < 2^31 */
+    int32_t max_pages;  /* columns of table; max_pages * page_size < 2^31, and
+                           T * ceil(max_pages * page_size / 64) < 2^31 */
     float scale;        /* score scale: 0 = 1/sqrt(D) */
 } smla_paged_dims;
 

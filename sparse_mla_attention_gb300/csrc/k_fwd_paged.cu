@@ -28,9 +28,9 @@
 // works through its items (a token's part of the range). An item that holds a
 // whole token writes o and lse; a part of a token goes to the workspace as fp32
 // (unnormalised O, maximum, sum), and combine_paged_kernel joins the parts in order.
-// Warps: 0-3 softmax (a thread has one head and half of the tile's ranks: the
-// two lanes of a head swap their halves of S, which adds hi and lo), 4-7 q
-// conversion and output, 8 MMA, 9-10 loads (TMA boxes where a tile's rows lie in
+// Warps: 0-3 and 4-7 softmax, on alternate tiles (a thread has one head and half of
+// the tile's ranks: the two lanes of a head swap their halves of S, which adds hi and
+// lo), 8-11 q conversion and output, 12 MMA, 13-14 loads (TMA boxes where a tile's rows lie in
 // whole pages, four-row gathers otherwise). A masked rank loads a valid row of its
 // tile instead of its own (weight 0, and no byte of a row that nothing
 // names is ever read); a tile without a valid rank is skipped.
@@ -56,7 +56,7 @@ constexpr int kPgSlotBytes = kPgTile * kD;       // 32 KB: four blocks of 64 row
 constexpr int kPgBlockBytes = kPgTile * 128;
 constexpr int kPgHeads = 64;                     // heads of a group at most
 constexpr int kPgPBytes = kPgHeads * 128;        // weights of a tile: 64 bytes hi, 64 bytes lo a head
-constexpr int kPgMmaWarp = 8, kPgLoadWarp = 9, kPgLoadWarps = 2;
+constexpr int kPgOutWarp = 8, kPgMmaWarp = 12, kPgLoadWarp = 13, kPgLoadWarps = 2;
 constexpr int kPgThreads = (kPgLoadWarp + kPgLoadWarps) * 32;
 constexpr int kPgMaxCtas = 160;
 // TMEM columns
@@ -69,20 +69,23 @@ constexpr float kPgBias = 5.f, kPgSlack = 3.f;
 struct PgShared {
     uint64_t full[kPgSlots], empty[kPgSlots], q_load[2];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-    uint64_t q_full, q_empty, o_full, o_empty, vote_bar, drain;
+    uint64_t q_full, q_empty, o_full, o_empty, dec[4], vote_bar[2], drain;
     uint32_t tbase;
     volatile int abort_flag;
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
-    long long sum[kPgThreads / 32];
+    int sum[kPgThreads / 32];
     int any[kPgSlots];                           // 0: no valid rank in the tile, 1: some, 2: all
     uint32_t vote[2][4];
-    int item_any[4];
-    float sref[4];
+    int item_any[4];                             // bit b: softmax team b had a tile of the item
+    int st_item[4], st_buf[4], st_use[4];        // per lane quarter: the last tile's item, team and its count there
+    float st_sref[4];                            // and the largest block scale of the item so far
+    float sref[4][2];
     __align__(16) float scale[kPgSlots][kPgTile];     // block scale of each rank, -1: masked
     __align__(16) float fac[2][kPgHeads];             // rescaling factors
     float qfac[4][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
-    float m[4][kPgHeads], l[4][kPgHeads];        // per item: reference and sum of a head
-    float fin[4][kPgHeads];                      // per output warp: 1 / denominator
+    float st_m[kPgHeads];                        // running reference of a head
+    float m[4][2][kPgHeads], l[4][2][kPgHeads];  // per item and team: reference and sum of a head
+    __align__(16) float fin[4][kPgHeads];        // per output warp: 1 / denominator
 };
 
 constexpr int kPgSmem = int(sizeof(PgShared)) + 1024 + kPgSlots * kPgSlotBytes + 2 * kPgPBytes;
@@ -101,9 +104,10 @@ struct PgParams {
     float* part_o;                               // [CTAs][2][group_heads][512]
 };
 
-__device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                        unsigned* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+// The waiting itself stays out of line: the kernel's warps run different code, and
+// forty copies of the loop cost more in instruction fetches than the call.
+__device__ __noinline__ bool pg_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned* status) {
     if (*abort_flag) return false;
     if (mbar_wait(bar, parity, kPgWaitNs)) return true;
     *abort_flag = 1;
@@ -113,7 +117,8 @@ __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile
 
 __device__ __forceinline__ bool pg_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              unsigned* status) {
-    const bool ok = pg_wait(bar, parity, abort_flag, status);
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = pg_wait_slow(bar, parity, abort_flag, status);
     return __all_sync(0xffffffffu, ok) != 0;
 }
 
@@ -140,14 +145,14 @@ static_assert(kPgSlots % 2 == 0 && kPgSlots >= 6, "a slot belongs to one of the 
 __device__ __forceinline__ int pg_slot(int g) { return g % kPgSlots; }
 __device__ __forceinline__ uint32_t pg_parity(uint32_t bits, int slot) { return (bits >> slot) & 1u; }
 
-// The tiles are dealt out in runs of per or (the first rem CTAs) per + 1.
+// The tiles (fewer than 2^31) are dealt out in runs of per or (the first rem CTAs) per + 1.
 struct PgDeal {
-    long long per, rem;
-    __device__ __forceinline__ PgDeal(long long total, int ctas) : per(total / ctas), rem(total - per * ctas) {}
-    __device__ __forceinline__ long long first(int c) const { return per * c + (c < rem ? c : rem); }
-    __device__ __forceinline__ int owner(long long tile) const {
-        const long long longer = rem * (per + 1);
-        return int(tile < longer ? tile / (per + 1) : rem + (tile - longer) / per);
+    unsigned per, rem;
+    __device__ __forceinline__ PgDeal(unsigned total, unsigned ctas) : per(total / ctas), rem(total - per * ctas) {}
+    __device__ __forceinline__ unsigned first(unsigned c) const { return per * c + (c < rem ? c : rem); }
+    __device__ __forceinline__ unsigned owner(unsigned tile) const {
+        const unsigned longer = rem * (per + 1);
+        return tile < longer ? tile / (per + 1) : rem + (tile - longer) / per;
     }
 };
 
@@ -167,46 +172,63 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3)));
 }
 
-// The CTA's share of the tiles: sums the tiles of all tokens (thread i those of
-// a run of tokens), then the thread whose run holds the CTA's first tile finds its token.
-__device__ void pg_locate(const PgParams& p, PgShared& sh, int c, int ctas) {
+// The CTA's share of the tiles. Picks: every token has as many tiles. All
+// positions: sums the tiles of the tokens (thread i those of a run of tokens), then
+// the thread whose run holds the CTA's first tile finds its token.
+__device__ void pg_locate(const PgParams& p, PgShared& sh, unsigned c, unsigned ctas) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int run = (p.T + kPgThreads - 1) / kPgThreads;
-    const int64_t t_lo = int64_t(threadIdx.x) * run;
-    const int t0 = int(t_lo < p.T ? t_lo : p.T), t1 = int(t_lo + run < p.T ? t_lo + run : p.T);
-    long long mine = 0;
-    for (int t = t0; t < t1; ++t) mine += pg_tiles(p, t);
-    long long x = mine;
+    unsigned total, at;
+    int t0 = 0, mine = 0;
+    if (p.topk) {
+        const int n = pg_tiles(p, 0);
+        total = unsigned(p.T) * n;
+        at = 0;
+    } else {
+        const int run = (p.T + kPgThreads - 1) / kPgThreads;
+        t0 = min(int(threadIdx.x) * run, p.T);
+        const int t1 = min(t0 + run, p.T);
+#pragma unroll 4
+        for (int t = t0; t < t1; ++t) mine += pg_tiles(p, t);
+        int x = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) sh.sum[warp] = x;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < kPgThreads / 32; ++w) {
-        if (w < warp) before += sh.sum[w];
-        total += sh.sum[w];
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) sh.sum[warp] = x;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll 1
+        for (int w = 0; w < kPgThreads / 32; ++w) {
+            if (w < warp) before += sh.sum[w];
+            all += sh.sum[w];
+        }
+        total = unsigned(all);
+        at = unsigned(before + x - mine);
     }
     const PgDeal deal(total, ctas);
-    const long long a = deal.first(c), b = deal.first(c + 1);
-    long long at = before + x - mine;
+    const unsigned a = deal.first(c), b = deal.first(c + 1);
     if (threadIdx.x == 0) sh.count = int(b - a);
-    if (a < b && at <= a && a < at + mine) {
-        int t = t0;
-        for (;; ++t) {
-            const int n = pg_tiles(p, t);
-            if (a < at + n) break;
-            at += n;
+    const bool mine_to_find = p.topk ? threadIdx.x == 0 : at <= a && a < at + unsigned(mine);
+    if (a < b && mine_to_find) {
+        int t = t0, n = pg_tiles(p, t);
+        if (p.topk) {
+            t = int(a / unsigned(n));
+            at = unsigned(t) * n;
+        } else {
+#pragma unroll 1
+            while (a >= at + unsigned(n)) {
+                at += unsigned(n);
+                n = pg_tiles(p, ++t);
+            }
         }
         sh.t0 = t;
         sh.k0 = int(a - at);
         // this CTA ends a token that began in an earlier one: it names the parts to join
         int4 end = make_int4(-1, 0, 0, 0);
-        if (a > at && b - at >= pg_tiles(p, t)) {
-            const int first = deal.owner(at);
-            end = make_int4(t, first, deal.first(first) == at ? 0 : 1, 0);
+        if (a > at && b - at >= unsigned(n)) {
+            const unsigned first = deal.owner(at);
+            end = make_int4(t, int(first), deal.first(first) == at ? 0 : 1, 0);
         }
         p.meta[blockIdx.x] = end;
     } else if (a >= b && threadIdx.x == 0) {
@@ -261,13 +283,18 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.o_full, 2);                // MMA completion and the issuing thread
         mbar_init(&sh.o_empty, 4);
-        mbar_init(&sh.vote_bar, 4);
+        mbar_init(&sh.vote_bar[0], 4);
+        mbar_init(&sh.vote_bar[1], 4);
+        for (int q = 0; q < 4; ++q) {
+            mbar_init(&sh.dec[q], 1);
+            sh.st_item[q] = -1;
+        }
         mbar_init(&sh.drain, 1);
         sh.abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kPgMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
-    pg_locate(p, sh, cta, ctas);
+    pg_locate(p, sh, unsigned(cta), unsigned(ctas));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -404,145 +431,171 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
         const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
         const bool leader = elect_one();
-        int g = 0, nb = 0, item = 0;
+        int g = 0, item = 0;
+        int uses[2] = {0, 0};                    // tiles given to each softmax team
         uint32_t seen = 0;
         bool ok = true, pending = false, pend_first = false;
-        int pend_slot = 0, pend_nb = 0, pend_item = 0;
-        int open = -1;                           // the item whose output is not announced yet
-        // the O product of the pending tile
-        auto flush = [&]() {
-            const int b = pend_nb & 1;
-            ok = pg_wait_warp(&sh.p_full[b], uint32_t(pend_nb >> 1) & 1u, ab, p.status);
-            if (ok && pend_first && pend_item > 0)
-                ok = pg_wait_warp(&sh.o_empty, uint32_t(pend_item - 1) & 1u, ab, p.status);
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t va = ring_desc + uint32_t(pend_slot) * (kPgSlotBytes >> 4);
-            const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
-            if (leader) {
-#pragma unroll
-                for (int db = 0; db < 4; ++db)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
-                        mma_f8_ss(tbase + kPgColO + 64 * db,
-                                  va + ((db * kPgBlockBytes + (k & 1) * 4096) >> 4), wa + 2 * k,
-                                  k < 2 ? id_hi : id_lo, !(pend_first && k == 0));
-                mma_commit(&sh.empty[pend_slot]);
-                mma_commit(&sh.p_empty[b]);
-            }
-            __syncwarp();
-            pending = false;
-        };
-        auto announce = [&](int which, int any) {
-            if (leader) {
-                sh.item_any[which & 3] = any;
-                mbar_arrive(&sh.o_full);
-                mma_commit(&sh.o_full);
-            }
-            __syncwarp();
-            open = -1;
-        };
-        // the pending tile's O product, and the output of an item before this one. Also
-        // before a tile without a valid rank: the pending tile's slot must come free while
-        // the loads go on through a run of such tiles
-        auto settle = [&](int now) {
-            if (pending) flush();
-            if (ok && open >= 0 && open != now) announce(open, 1);
-        };
-        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-            const int n = w.tiles(p);
-            g += 2;
-            int used = 0;
-            for (int i = 0; i < n && ok; ++i, ++g) {
-                const int slot = pg_slot(g);
+        int pend_slot = 0, pend_use = 0, pend_item = 0;
+        int open = -1, teams = 0;                // the item whose output is not announced yet, and its teams
+        // Each step takes one event: a tile, the end of an item, or the end of the range. It issues
+        // the tile's S product, then the O product of the tile before it (also at a tile
+        // without a valid rank: the pending tile's slot must come free while the loads go on
+        // through a run of such tiles), then announces the output of a finished item.
+        PgWalk w(sh);
+        int n = w.left > 0 ? w.tiles(p) : 0, i = 0, used = 0;
+        g = 2;
+        while (ok) {
+            const bool over = w.left <= 0;
+            const bool item_end = !over && i == n;
+            bool valid = false;
+            int slot = 0, use = 0;
+            if (!over && !item_end) {
+                slot = pg_slot(g);
                 ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
                 if (!ok) break;
                 seen ^= 1u << slot;
-                if (sh.any[slot] == 0) {
-                    __syncwarp();
-                    if (leader) mbar_arrive(&sh.empty[slot]);
-                    settle(item);
-                    continue;
-                }
-                if (used == 0) ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
-                if (ok) ok = pg_wait_warp(&sh.s_empty[nb & 1], (uint32_t(nb >> 1) & 1u) ^ 1u, ab, p.status);
+                valid = __shfl_sync(0xffffffffu, sh.any[slot], 0) != 0;
+            }
+            if (used == 0 && (item_end || valid))
+                ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+            if (valid) {
+                const int b = slot & 1;
+                use = b ? uses[1] : uses[0];
+                if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(use) & 1u) ^ 1u, ab, p.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ka = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kD / 32; ++k)
-                        mma_f8_ts(tbase + kPgColS + kPgTile * (nb & 1), tbase + kPgColQ + 8 * k,
+                        mma_f8_ts(tbase + kPgColS + kPgTile * b, tbase + kPgColQ + 8 * k,
                                   ka + (((k >> 2) * kPgBlockBytes + (k & 3) * 32) >> 4), id_s, k != 0);
-                    mbar_arrive(&sh.s_full[nb & 1]);
-                    mma_commit(&sh.s_full[nb & 1]);
+                    mbar_arrive(&sh.s_full[b]);
+                    mma_commit(&sh.s_full[b]);
                 }
                 __syncwarp();
-                settle(item);
-                pending = true;
-                open = item;
-                pend_slot = slot; pend_nb = nb; pend_item = item; pend_first = used == 0;
-                ++used; ++nb;
+            }
+            if (ok && pending && !(item_end && used > 0)) {
+                const int b = pend_slot & 1;
+                ok = pg_wait_warp(&sh.p_full[b], uint32_t(pend_use) & 1u, ab, p.status);
+                if (ok && pend_first && pend_item > 0)
+                    ok = pg_wait_warp(&sh.o_empty, uint32_t(pend_item - 1) & 1u, ab, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t va = ring_desc + uint32_t(pend_slot) * (kPgSlotBytes >> 4);
+                const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int db = 0; db < 4; ++db)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
+                            mma_f8_ss(tbase + kPgColO + 64 * db,
+                                      va + ((db * kPgBlockBytes + (k & 1) * 4096) >> 4), wa + 2 * k,
+                                      k < 2 ? id_hi : id_lo, !(pend_first && k == 0));
+                    mma_commit(&sh.empty[pend_slot]);
+                    mma_commit(&sh.p_empty[b]);
+                }
+                __syncwarp();
+                pending = false;
             }
             if (!ok) break;
-            if (used == 0) {                     // no valid rank in the whole item
-                ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
-                if (ok) settle(item);
-                if (ok && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
+            // an item is finished when something of a later one, or the end, is at hand
+            int done = -1, any = 0;
+            if (open >= 0 && (over || open != item)) {
+                done = open;
+                any = teams;
+                open = -1;
+            } else if (item_end && used == 0) {
+                if (item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
                 if (!ok) break;
-                announce(item, 0);
+                done = item;
             }
-            if (leader) mma_commit(&sh.q_empty);
+            if (done >= 0 && leader) {
+                sh.item_any[done & 3] = any;
+                mbar_arrive(&sh.o_full);
+                mma_commit(&sh.o_full);
+            }
             __syncwarp();
-            w.next(n);
+            if (over) break;
+            if (item_end) {
+                if (used == 0 && done != item) continue;     // its own announcement comes next
+                if (leader) mma_commit(&sh.q_empty);
+                __syncwarp();
+                w.next(n);
+                n = w.left > 0 ? w.tiles(p) : 0;
+                i = 0;
+                used = 0;
+                ++item;
+                g += 2;
+                continue;
+            }
+            if (valid) {
+                teams = (open == item ? teams : 0) | 1 << (slot & 1);
+                open = item;
+                pending = true;
+                pend_slot = slot; pend_use = use; pend_item = item; pend_first = used == 0;
+                if (slot & 1) ++uses[1]; else ++uses[0];
+                ++used;
+            } else if (leader) {
+                mbar_arrive(&sh.empty[slot]);
+            }
+            __syncwarp();
+            ++i;
+            ++g;
         }
-        if (ok) settle(item);
         if (leader) {
             mma_commit(&sh.drain);
             mbar_wait(&sh.drain, 0, kPgWaitNs);
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp < kPgOutWarp) {
         // -------------------------------------------------------------- softmax
-        const int part = lane >> 4, head = 16 * warp + (lane & 15);
-        const bool active = 16 * warp < heads;
-        const uint32_t trow = tbase + (uint32_t(warp * 32) << 16);
+        // Two teams of four warps take the tiles in turn (a tile's team is its
+        // slot's parity). A head's running reference passes from team to team along dec[quarter].
+        const int team = warp >> 2, quarter = warp & 3;
+        const int part = lane >> 4, head = 16 * quarter + (lane & 15);
+        const bool active = 16 * quarter < heads;
+        const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
         const float lo_factor = part ? 0.0625f : 1.f;
-        int g = 0, nb = 0, item = 0, votes = 0;
+        int g = 0, tile = 0, use = 0, item = 0, votes = 0;
         uint32_t seen = 0;
         bool ok = true;
         for (PgWalk w(sh); w.left > 0 && ok; ++item) {
             const int n = w.tiles(p);
             g += 2;
-            bool fresh = true;
-            float m_ref = -INFINITY, l = 0.f, sref = 0.f, f = 0.f;
-            for (int i = 0; i < n && ok; ++i, ++g) {
+            float m_own = -INFINITY, l = 0.f, f = 0.f;
+            bool begun = false;
+            for (int i = 0; i < n && ok; ++i, ++g, ++tile) {
                 const int slot = pg_slot(g);
+                if ((slot & 1) != team) continue;
                 ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
                 if (!ok) break;
                 seen ^= 1u << slot;
-                const int any = sh.any[slot];
-                if (any == 0) {
+                if (sh.any[slot] == 0) {
+                    if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, p.status);
+                    if (!ok) break;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                    if (lane == 0) {
+                        mbar_arrive(&sh.dec[quarter]);
+                        mbar_arrive(&sh.empty[slot]);
+                    }
                     continue;
                 }
-                const int b = nb & 1;
-                ok = pg_wait_warp(&sh.s_full[b], uint32_t(nb >> 1) & 1u, ab, p.status);
+                ok = pg_wait_warp(&sh.s_full[team], uint32_t(use) & 1u, ab, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                if (fresh) f = sh.qfac[item & 3][head] * lo_factor;
+                if (!begun) f = sh.qfac[item & 3][head] * lo_factor;
                 const float4* scp = reinterpret_cast<const float4*>(&sh.scale[slot][32 * part]);
                 float s[32];
                 float mx = -INFINITY, smax = 0.f;
                 {
                     uint32_t v0[32], v1[32];
-                    tmem_ld32(trow + kPgColS + kPgTile * b, v0);
-                    tmem_ld32(trow + kPgColS + kPgTile * b + 32, v1);
+                    tmem_ld32(trow + kPgColS + kPgTile * team, v0);
+                    tmem_ld32(trow + kPgColS + kPgTile * team + 32, v1);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.s_empty[b]);
+                    if (lane == 0) mbar_arrive(&sh.s_empty[team]);
                     // the head's other lane has the other part of q: swap halves and add
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -565,34 +618,46 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 16));
-                if (fresh) {
-                    m_ref = mx;
-                    sref = smax;
-                    fresh = false;
-                } else {
-                    // the reference follows the maximum in steps; the warps agree on it, because
-                    // a warp's TMEM lanes are columns of D, not heads
-                    const int vb = votes & 1;
-                    const bool grow = active && mx > m_ref + kPgSlack;
-                    const bool need = grow || smax > sref;
-                    const float mn = grow ? mx : m_ref, sn = fmaxf(sref, smax);
-                    const float fm = m_ref == -INFINITY ? 1.f : ex2_approx(m_ref - mn);
-                    if (part == 0) sh.fac[vb][head] = fm * (sref > 0.f ? sref / sn : 1.f);
-                    const bool wneed = __any_sync(0xffffffffu, need) != 0;
+                // the reference after the tile before this one
+                if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, p.status);
+                if (!ok) break;
+                const bool fresh = sh.st_item[quarter] != item;
+                const int last_buf = sh.st_buf[quarter], last_use = sh.st_use[quarter];
+                const float m_old = fresh ? mx : sh.st_m[head];
+                const float s_old = fresh ? smax : sh.st_sref[quarter];
+                // the reference follows the maximum in steps
+                const bool grow = active && mx > m_old + kPgSlack;
+                const float m_ref = grow ? mx : m_old, sref = fmaxf(s_old, smax);
+                __syncwarp();
+                if (part == 0) sh.st_m[head] = m_ref;
+                if (lane == 0) {
+                    sh.st_item[quarter] = item;
+                    sh.st_sref[quarter] = sref;
+                    sh.st_buf[quarter] = team;
+                    sh.st_use[quarter] = use;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.dec[quarter]);
+                if (!fresh) {
+                    // all warps of the team agree on rescaling, because a warp's TMEM lanes are
+                    // columns of D, not heads
+                    const bool need = __any_sync(0xffffffffu, grow || smax > s_old) != 0;
+                    if (part == 0)
+                        sh.fac[team][head] =
+                            (grow && m_old != -INFINITY ? ex2_approx(m_old - m_ref) : 1.f) *
+                            (s_old > 0.f ? s_old / sref : 1.f);
                     __syncwarp();
                     if (lane == 0) {
-                        sh.vote[vb][warp] = wneed;
-                        mbar_arrive(&sh.vote_bar);
+                        sh.vote[team][quarter] = need;
+                        mbar_arrive(&sh.vote_bar[team]);
                     }
-                    ok = pg_wait_warp(&sh.vote_bar, uint32_t(votes) & 1u, ab, p.status);
+                    ok = pg_wait_warp(&sh.vote_bar[team], uint32_t(votes) & 1u, ab, p.status);
                     if (!ok) break;
                     ++votes;
-                    if (sh.vote[vb][0] | sh.vote[vb][1] | sh.vote[vb][2] | sh.vote[vb][3]) {
-                        l *= fm;
-                        m_ref = mn;
-                        sref = sn;
-                        // the O products of the item's earlier tiles are complete
-                        ok = pg_wait_warp(&sh.p_empty[b ^ 1], uint32_t((nb - 1) >> 1) & 1u, ab, p.status);
+                    if (sh.vote[team][0] | sh.vote[team][1] | sh.vote[team][2] | sh.vote[team][3]) {
+                        // the O products of the item's earlier tiles are complete (those before the
+                        // last completed ahead of this tile's S: the tensor core works in order)
+                        ok = pg_wait_warp(&sh.p_empty[last_buf], uint32_t(last_use) & 1u, ab, p.status);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -604,18 +669,21 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                v[e] = __float_as_uint(__uint_as_float(v[e]) * sh.fac[vb][h + e]);
+                                v[e] = __float_as_uint(__uint_as_float(v[e]) * sh.fac[team][h + e]);
                             tmem_st16(at, v);
                         }
                         tmem_wait_st();
                     }
                 }
-                ok = pg_wait_warp(&sh.p_empty[b], (uint32_t(nb >> 1) & 1u) ^ 1u, ab, p.status);
+                l = begun && m_own != m_ref && m_own != -INFINITY ? l * ex2_approx(m_own - m_ref) : l;
+                m_own = m_ref;
+                begun = true;
+                ok = pg_wait_warp(&sh.p_empty[team], (uint32_t(use) & 1u) ^ 1u, ab, p.status);
                 if (!ok) break;
                 if (active) {
                     const float off = kPgBias - (m_ref == -INFINITY ? 0.f : m_ref);
                     const float inv = sref > 0.f ? 1.f / sref : 0.f;
-                    uint8_t* prow = pbuf + b * kPgPBytes + head * 128;
+                    uint8_t* prow = pbuf + team * kPgPBytes + head * 128;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {            // 16 ranks: 16 bytes hi and 16 bytes lo
                         uint32_t hi[4], lo[4];
@@ -643,19 +711,19 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     const float both = l + __shfl_xor_sync(0xffffffffu, l, 16);
                     if (part == 0) {
-                        sh.m[item & 3][head] = m_ref;
-                        sh.l[item & 3][head] = both;
+                        sh.m[item & 3][team][head] = m_ref;
+                        sh.l[item & 3][team][head] = both;
                     }
                 }
-                if (threadIdx.x == 0) sh.sref[item & 3] = sref;
+                if (quarter == 0 && lane == 0) sh.sref[item & 3][team] = sref;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sh.p_full[b]);
+                    mbar_arrive(&sh.p_full[team]);
                     mbar_arrive(&sh.empty[slot]);
                 }
-                ++nb;
+                ++use;
             }
             w.next(n);
         }
@@ -667,21 +735,119 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int g = 0, item = 0;
         bool ok = true;
         int t_prev = 0;
-        bool whole_prev = false, first_prev = false;
+        bool whole_prev = false;
 
-        auto output = [&](int n_item, int t, bool whole, bool first) {
-            ok = pg_wait_warp(&sh.o_full, uint32_t(n_item) & 1u, ab, p.status);
-            if (!ok) return;
+        for (PgWalk w(sh);; ++item) {
+            const bool more = w.left > 0;
+            const int n = more ? w.tiles(p) : 0;
+            if (more) {
+                const int s0 = pg_slot(g), s1 = pg_slot(g + 1);
+                g += n + 2;
+                ok = pg_wait_warp(&sh.q_load[item & 1], uint32_t(item >> 1) & 1u, ab, p.status);
+                if (!ok) break;
+                uint8_t* qhalf = ring + (part ? s1 : s0) * kPgSlotBytes + head * 128;
+                auto piece = [&](int c) {            // 16 bytes of the row's half: 8 values
+                    return reinterpret_cast<uint4*>(qhalf + (c >> 3) * kPgBlockBytes + (((c & 7) ^ (head & 7)) << 4));
+                };
+                if (active) {
+                    // largest |q| of the row; each of the head's lanes has one half
+                    uint32_t top = 0;
+#pragma unroll 4
+                    for (int c = 0; c < 32; ++c) {
+                        const uint4 x = *piece(c);
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                    }
+                    top = max(top >> 16, top & 0xffffu);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    int e2 = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+                    e2 = top == 0 || e2 > 119 ? 0 : e2 < -100 ? -100 : e2;
+                    const float inv = __int_as_float((127 - e2) << 23);
+                    // infinities and NaN in q make every score of the head NaN
+                    if (part == 0)
+                        sh.qfac[item & 3][head] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                                                 : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
+                    // in place: eight values become eight bytes hi and eight bytes lo
+#pragma unroll 1
+                    for (int c = 0; c < 32; c += 4) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = *piece(c + k);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                // half precision holds a scaled value and what e4m3 leaves of it exactly
+                                const __half2 v = __floats2half2_rn(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
+                                hi[e] = e4m3x2(v);
+                                lo[e] = e4m3x2(__hmul2(__hsub2(v, e4m3x2_half(hi[e])), __float2half2_rn(16.f)));
+                            }
+                            x[k] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
+                                              lo[2] | lo[3] << 16);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) *piece(c + k) = x[k];
+                    }
+                }
+                __syncwarp();
+                if (item > 0) ok = pg_wait_warp(&sh.q_empty, uint32_t(item - 1) & 1u, ab, p.status);
+                if (!ok) break;
+                if (active) {
+                    tc_fence_after();
+                    const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128 + 8 * part;
+                    const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128 + 8 * part;
+#pragma unroll 2
+                    for (int c = 0; c < 8; ++c) {    // 64 values of the row's part: a box
+                        const uint8_t* src = (c < 4 ? q0 : q1) + (c & 3) * kPgBlockBytes;
+                        uint32_t word[16];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint2 x = *reinterpret_cast<const uint2*>(src + ((k ^ (head & 7)) << 4));
+                            word[2 * k] = x.x;
+                            word[2 * k + 1] = x.y;
+                        }
+                        tmem_st16(trow + kPgColQ + 16 * c, word);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                fence_proxy_async_smem();            // the slots' next loads come after these writes
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.q_full);
+                    mbar_arrive_cnt(&sh.empty[s0], quarter == 0 ? 2 : 1);    // five arrivals, from four warps
+                    mbar_arrive_cnt(&sh.empty[s1], quarter == 0 ? 2 : 1);
+                }
+            }
+            const int done = item - 1, t = t_prev;
+            const bool whole = whole_prev, first = done == 0;
+            t_prev = w.t;
+            whole_prev = more && w.k0 == 0 && n == pg_tiles(p, w.t);
+            w.next(n);
+            if (done < 0) {
+                if (!more) break;                // a CTA without a tile
+                continue;
+            }
+            // the output of the item before, once the next one's q is in place
+            ok = pg_wait_warp(&sh.o_full, uint32_t(done) & 1u, ab, p.status);
+            if (!ok) break;
             tc_fence_after();
-            const int st = n_item & 3;
-            const bool any = sh.item_any[st] != 0;
+            const int st = done & 3;
+            const int any = sh.item_any[st];     // the teams that had tiles
             float* fin = sh.fin[quarter];
             const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
             for (int h = lane; h < heads; h += 32) {
                 // sums are in units of 2^(reference - bias)
-                const float mu = any ? sh.m[st][h] : -INFINITY;
-                const float m2 = mu == -INFINITY ? 0.f : mu - kPgBias, l = any ? sh.l[st][h] : 0.f;
-                const float so = any ? sh.sref[st] : 0.f;
+                const float ma = any & 1 ? sh.m[st][0][h] : -INFINITY, mb = any & 2 ? sh.m[st][1][h] : -INFINITY;
+                const float la = any & 1 ? sh.l[st][0][h] : 0.f, lb = any & 2 ? sh.l[st][1][h] : 0.f;
+                // references only rise within an item: the larger is the accumulator's
+                const float mu = fmaxf(ma, mb);
+                const float m2 = mu == -INFINITY ? 0.f : mu - kPgBias;
+                const float l = (la == 0.f || ma == mu ? la : la * ex2_approx(ma - mu)) +
+                                (lb == 0.f || mb == mu ? lb : lb * ex2_approx(mb - mu));
+                const float so = fmaxf(any & 1 ? sh.sref[st][0] : 0.f, any & 2 ? sh.sref[st][1] : 0.f);
                 if (whole) {
                     const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
                     // a NaN sum stays one; a sum of zero leaves the sink alone
@@ -700,118 +866,44 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             __syncwarp();
 #pragma unroll 1
-            for (int db = 0; db < 4; ++db) {
-                const int d = 128 * db + 32 * quarter + lane;
+            for (int h = 0; h < heads; h += 16) {
+                float fh[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 x = *reinterpret_cast<const float4*>(fin + h + 4 * e);
+                    fh[4 * e] = x.x; fh[4 * e + 1] = x.y; fh[4 * e + 2] = x.z; fh[4 * e + 3] = x.w;
+                }
 #pragma unroll 1
-                for (int h = 0; h < heads; h += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(trow + kPgColO + 64 * db + h, v);
+                for (int db = 0; db < 4; db += 2) {
+                    uint32_t v[2][16];
+                    tmem_ld16(trow + kPgColO + 64 * db + h, v[0]);
+                    tmem_ld16(trow + kPgColO + 64 * (db + 1) + h, v[1]);
                     tmem_wait_ld();
+                    const int d = 128 * db + 32 * quarter + lane;
                     if (whole) {
                         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) +
                                              (int64_t(t) * p.H + head0 + h) * kD + d;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            dst[e * kD] = __float2bfloat16_rn(any ? __uint_as_float(v[e]) * fin[h + e] : 0.f);
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                dst[128 * k + e * kD] =
+                                    __float2bfloat16_rn(any ? __uint_as_float(v[k][e]) * fh[e] : 0.f);
                     } else {
                         float* dst = p.part_o + (int64_t(part_at) * p.group_heads + h) * kD + d;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            dst[e * kD] = any ? __uint_as_float(v[e]) * fin[h + e] : 0.f;
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                dst[128 * k + e * kD] = any ? __uint_as_float(v[k][e]) * fh[e] : 0.f;
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.o_empty);
-        };
-
-        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-            const int n = w.tiles(p);
-            const int s0 = pg_slot(g), s1 = pg_slot(g + 1);
-            g += n + 2;
-            ok = pg_wait_warp(&sh.q_load[item & 1], uint32_t(item >> 1) & 1u, ab, p.status);
-            if (!ok) break;
-            uint8_t* qhalf = ring + (part ? s1 : s0) * kPgSlotBytes + head * 128;
-            auto piece = [&](int c) {            // 16 bytes of the row's half: 8 values
-                return reinterpret_cast<uint4*>(qhalf + (c >> 3) * kPgBlockBytes + (((c & 7) ^ (head & 7)) << 4));
-            };
-            if (active) {
-                // largest |q| of the row; each of the head's lanes has one half
-                uint32_t top = 0;
-#pragma unroll 8
-                for (int c = 0; c < 32; ++c) {
-                    const uint4 x = *piece(c);
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                 __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                }
-                top = max(top >> 16, top & 0xffffu);
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                int e2 = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-                e2 = top == 0 || e2 > 119 ? 0 : e2 < -100 ? -100 : e2;
-                const float inv = __int_as_float((127 - e2) << 23);
-                // infinities and NaN in q make every score of the head NaN
-                if (part == 0)
-                    sh.qfac[item & 3][head] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
-                                                             : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
-                // in place: eight values become eight bytes hi and eight bytes lo
-#pragma unroll 4
-                for (int c = 0; c < 32; ++c) {
-                    uint4* at = piece(c);
-                    const uint4 x = *at;
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // half precision holds a scaled value and what e4m3 leaves of it exactly
-                        const __half2 v = __floats2half2_rn(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
-                        hi[e] = e4m3x2(v);
-                        lo[e] = e4m3x2(__hmul2(__hsub2(v, e4m3x2_half(hi[e])), __float2half2_rn(16.f)));
-                    }
-                    *at = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
-                                     lo[2] | lo[3] << 16);
-                }
-            }
-            __syncwarp();
-            if (item > 0) ok = pg_wait_warp(&sh.q_empty, uint32_t(item - 1) & 1u, ab, p.status);
-            if (!ok) break;
-            if (active) {
-                tc_fence_after();
-                const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128 + 8 * part;
-                const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128 + 8 * part;
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c) {   // 32 values of the row's part
-                    const uint8_t* src = (c < 8 ? q0 : q1) + ((c >> 1) & 3) * kPgBlockBytes;
-                    uint32_t word[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int ch = 4 * (c & 1) + k;
-                        const uint2 x = *reinterpret_cast<const uint2*>(src + ((ch ^ (head & 7)) << 4));
-                        word[2 * k] = x.x;
-                        word[2 * k + 1] = x.y;
-                    }
-                    tmem_st8(trow + kPgColQ + 8 * c, word);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-            }
-            fence_proxy_async_smem();            // the slots' next loads come after these writes
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.q_full);
-                mbar_arrive_cnt(&sh.empty[s0], quarter == 0 ? 2 : 1);    // five arrivals, from four warps
-                mbar_arrive_cnt(&sh.empty[s1], quarter == 0 ? 2 : 1);
-            }
-            if (item > 0) {
-                output(item - 1, t_prev, whole_prev, first_prev);
-                if (!ok) break;
-            }
-            t_prev = w.t;
-            whole_prev = w.k0 == 0 && n == pg_tiles(p, w.t);
-            first_prev = item == 0;
-            w.next(n);
+            if (!more) break;
         }
-        if (ok && item > 0) output(item - 1, t_prev, whole_prev, first_prev);
     }
     tc_fence_before();
     __syncthreads();

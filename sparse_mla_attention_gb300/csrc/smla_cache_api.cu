@@ -107,6 +107,8 @@ int smla_fwd_paged(const uint16_t* q, const smla_cache* cache, const int32_t* ta
     if (d.T < 0 || d.topk < 0 || d.H < 16 || d.H > 128 || d.H % 16 != 0 || d.B < 1) return SMLA_ERR_SHAPE;
     if ((rc = check_table(c, d.B, d.max_pages))) return rc;
     if (int64_t(d.T) * d.topk > int64_t(INT32_MAX) || (!seq && d.T > d.B)) return SMLA_ERR_SHAPE;
+    // tiles of 64 ranks are counted in 32 bits
+    if (int64_t(d.T) * ((int64_t(d.max_pages) * c.page_size + 63) / 64) > int64_t(INT32_MAX)) return SMLA_ERR_SHAPE;
     if ((d.topk > 0) != (topk != nullptr) && d.T > 0) return SMLA_ERR_ARG;
     if (!std::isfinite(d.scale) || d.scale < 0.f) return SMLA_ERR_ARG;
     if (!workspace) return SMLA_ERR_NULL;

@@ -33,7 +33,7 @@
 // lo), 8-11 q conversion and output, 12 MMA, 13-14 loads (TMA boxes where a tile's rows lie in
 // whole pages, four-row gathers otherwise). A masked rank loads a valid row of its
 // tile instead of its own (weight 0, and no byte of a row that nothing
-// names is ever read); a tile without a valid rank is skipped.
+// names is ever read); a tile without a valid rank is filled with zeros.
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the
 // CTA's loops, waits (bounded) for its own copies and MMAs and frees TMEM.
 #include <cuda_fp8.h>
@@ -74,11 +74,8 @@ struct PgShared {
     volatile int abort_flag;
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
     int sum[kPgThreads / 32];
-    int any[kPgSlots];                           // 0: no valid rank in the tile, 1: some, 2: all
     uint32_t vote[2][4];
-    int item_any[4];                             // bit b: softmax team b had a tile of the item
-    int st_item[4], st_buf[4], st_use[4];        // per lane quarter: the last tile's item, team and its count there
-    float st_sref[4];                            // and the largest block scale of the item so far
+    float st_sref[4];                            // per lane quarter: largest block scale of the item so far
     float sref[4][2];
     __align__(16) float scale[kPgSlots][kPgTile];     // block scale of each rank, -1: masked
     __align__(16) float fac[2][kPgHeads];             // rescaling factors
@@ -285,10 +282,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(&sh.o_empty, 4);
         mbar_init(&sh.vote_bar[0], 4);
         mbar_init(&sh.vote_bar[1], 4);
-        for (int q = 0; q < 4; ++q) {
-            mbar_init(&sh.dec[q], 1);
-            sh.st_item[q] = -1;
-        }
+        for (int q = 0; q < 4; ++q) mbar_init(&sh.dec[q], 1);
         mbar_init(&sh.drain, 1);
         sh.abort_flag = 0;
         fence_mbar_init();
@@ -387,8 +381,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 loads ^= 1u << slot;             // full's phase of this load has the parity before
                 if (half == 0)
                     *reinterpret_cast<float4*>(&sh.scale[slot][4 * quad]) = make_float4(sc[0], sc[1], sc[2], sc[3]);
-                if (lane == 0) sh.any[slot] = some == 0 ? 0 : all ? 2 : 1;
-                if (some == 0) {
+                if (some == 0) {                 // nothing valid: a tile of zeros, all of it masked
+#pragma unroll 4
+                    for (int k = 0; k < kPgSlotBytes / 512; ++k)
+                        reinterpret_cast<uint4*>(dst)[32 * k + lane] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
                     mbar_arrive(&sh.full[slot]);
                 } else if (all && !p.topk) {
                     const int seg = lane >> 2, cb = lane & 3;
@@ -431,117 +428,80 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
         const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
         const bool leader = elect_one();
-        int g = 0, item = 0;
-        int uses[2] = {0, 0};                    // tiles given to each softmax team
+        int g = 0, tile = 0, item = 0;
         uint32_t seen = 0;
-        bool ok = true, pending = false, pend_first = false;
-        int pend_slot = 0, pend_use = 0, pend_item = 0;
-        int open = -1, teams = 0;                // the item whose output is not announced yet, and its teams
-        // Each step takes one event: a tile, the end of an item, or the end of the range. It issues
-        // the tile's S product, then the O product of the tile before it (also at a tile
-        // without a valid rank: the pending tile's slot must come free while the loads go on
-        // through a run of such tiles), then announces the output of a finished item.
-        PgWalk w(sh);
-        int n = w.left > 0 ? w.tiles(p) : 0, i = 0, used = 0;
-        g = 2;
-        while (ok) {
-            const bool over = w.left <= 0;
-            const bool item_end = !over && i == n;
-            bool valid = false;
-            int slot = 0, use = 0;
-            if (!over && !item_end) {
-                slot = pg_slot(g);
-                ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
-                if (!ok) break;
-                seen ^= 1u << slot;
-                valid = __shfl_sync(0xffffffffu, sh.any[slot], 0) != 0;
-            }
-            if (used == 0 && (item_end || valid))
-                ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
-            if (valid) {
-                const int b = slot & 1;
-                use = b ? uses[1] : uses[0];
-                if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(use) & 1u) ^ 1u, ab, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ka = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
-                if (leader) {
+        bool ok = true, first = false, last = false;    // of the tile before: of its item
+        int prev = -1;                           // its slot; its O product follows this tile's S
+        // The O product of tile t in slot `at`
+        auto second = [&](int t, int at, int of) {
+            const int b = t & 1;
+            ok = pg_wait_warp(&sh.p_full[b], uint32_t(t >> 1) & 1u, ab, p.status);
+            if (ok && first && of > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(of - 1) & 1u, ab, p.status);
+            if (!ok) return;
+            tc_fence_after();
+            uint64_t va = ring_desc + uint32_t(at) * (kPgSlotBytes >> 4);
+            const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
+            if (leader) {
+                uint32_t acc = tbase + kPgColO;
+#pragma unroll 1
+                for (int db = 0; db < 4; ++db) {
 #pragma unroll
-                    for (int k = 0; k < kD / 32; ++k)
-                        mma_f8_ts(tbase + kPgColS + kPgTile * b, tbase + kPgColQ + 8 * k,
-                                  ka + (((k >> 2) * kPgBlockBytes + (k & 3) * 32) >> 4), id_s, k != 0);
-                    mbar_arrive(&sh.s_full[b]);
-                    mma_commit(&sh.s_full[b]);
+                    for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
+                        mma_f8_ss(acc, va + (((k & 1) * 4096) >> 4), wa + 2 * k, k < 2 ? id_hi : id_lo,
+                                  !(first && k == 0));
+                    va += kPgBlockBytes >> 4;
+                    acc += 64;
                 }
-                __syncwarp();
-            }
-            if (ok && pending && !(item_end && used > 0)) {
-                const int b = pend_slot & 1;
-                ok = pg_wait_warp(&sh.p_full[b], uint32_t(pend_use) & 1u, ab, p.status);
-                if (ok && pend_first && pend_item > 0)
-                    ok = pg_wait_warp(&sh.o_empty, uint32_t(pend_item - 1) & 1u, ab, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t va = ring_desc + uint32_t(pend_slot) * (kPgSlotBytes >> 4);
-                const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
-                if (leader) {
-#pragma unroll
-                    for (int db = 0; db < 4; ++db)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
-                            mma_f8_ss(tbase + kPgColO + 64 * db,
-                                      va + ((db * kPgBlockBytes + (k & 1) * 4096) >> 4), wa + 2 * k,
-                                      k < 2 ? id_hi : id_lo, !(pend_first && k == 0));
-                    mma_commit(&sh.empty[pend_slot]);
-                    mma_commit(&sh.p_empty[b]);
+                mma_commit(&sh.empty[at]);
+                mma_commit(&sh.p_empty[b]);
+                if (last) {
+                    mbar_arrive(&sh.o_full);
+                    mma_commit(&sh.o_full);
                 }
-                __syncwarp();
-                pending = false;
-            }
-            if (!ok) break;
-            // an item is finished when something of a later one, or the end, is at hand
-            int done = -1, any = 0;
-            if (open >= 0 && (over || open != item)) {
-                done = open;
-                any = teams;
-                open = -1;
-            } else if (item_end && used == 0) {
-                if (item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
-                if (!ok) break;
-                done = item;
-            }
-            if (done >= 0 && leader) {
-                sh.item_any[done & 3] = any;
-                mbar_arrive(&sh.o_full);
-                mma_commit(&sh.o_full);
             }
             __syncwarp();
-            if (over) break;
-            if (item_end) {
-                if (used == 0 && done != item) continue;     // its own announcement comes next
-                if (leader) mma_commit(&sh.q_empty);
-                __syncwarp();
-                w.next(n);
-                n = w.left > 0 ? w.tiles(p) : 0;
-                i = 0;
-                used = 0;
-                ++item;
-                g += 2;
-                continue;
+        };
+        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+            const int n = w.tiles(p);
+            g += 2;
+#pragma unroll 1
+            for (int i = 0; i <= n; ++i) {
+                // the O product of the range's very last tile has no S before it
+                if (i == n && w.left > n) break;
+                const int slot = pg_slot(g);
+                if (i < n) {
+                    const int b = tile & 1;
+                    ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
+                    seen ^= 1u << slot;
+                    if (ok && i == 0) ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                    if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(tile >> 1) & 1u) ^ 1u, ab, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint64_t ka = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
+                    if (leader) {
+                        uint32_t qa = tbase + kPgColQ;
+#pragma unroll 1
+                        for (int cb = 0; cb < 4; ++cb) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8_ts(tbase + kPgColS + kPgTile * b, qa + 8 * k, ka + 2 * k, id_s, (cb | k) != 0);
+                            ka += kPgBlockBytes >> 4;
+                            qa += 32;
+                        }
+                        mbar_arrive(&sh.s_full[b]);
+                        mma_commit(&sh.s_full[b]);
+                        if (i == n - 1) mma_commit(&sh.q_empty);
+                    }
+                    __syncwarp();
+                }
+                if (prev >= 0) second(tile - 1, prev, i == 0 ? item - 1 : item);
+                if (!ok) break;
+                prev = slot;
+                first = i == 0;
+                last = i == n - 1;
+                if (i < n) { ++tile; ++g; }
             }
-            if (valid) {
-                teams = (open == item ? teams : 0) | 1 << (slot & 1);
-                open = item;
-                pending = true;
-                pend_slot = slot; pend_use = use; pend_item = item; pend_first = used == 0;
-                if (slot & 1) ++uses[1]; else ++uses[0];
-                ++used;
-            } else if (leader) {
-                mbar_arrive(&sh.empty[slot]);
-            }
-            __syncwarp();
-            ++i;
-            ++g;
+            w.next(n);
         }
         if (leader) {
             mma_commit(&sh.drain);
@@ -557,34 +517,24 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const bool active = 16 * quarter < heads;
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
         const float lo_factor = part ? 0.0625f : 1.f;
-        int g = 0, tile = 0, use = 0, item = 0, votes = 0;
+        int g = 0, tile = 0, item = 0, votes = 0;
         uint32_t seen = 0;
         bool ok = true;
         for (PgWalk w(sh); w.left > 0 && ok; ++item) {
             const int n = w.tiles(p);
             g += 2;
             float m_own = -INFINITY, l = 0.f, f = 0.f;
-            bool begun = false;
             for (int i = 0; i < n && ok; ++i, ++g, ++tile) {
                 const int slot = pg_slot(g);
                 if ((slot & 1) != team) continue;
                 ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
                 if (!ok) break;
                 seen ^= 1u << slot;
-                if (sh.any[slot] == 0) {
-                    if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, p.status);
-                    if (!ok) break;
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sh.dec[quarter]);
-                        mbar_arrive(&sh.empty[slot]);
-                    }
-                    continue;
-                }
-                ok = pg_wait_warp(&sh.s_full[team], uint32_t(use) & 1u, ab, p.status);
+                const uint32_t use = uint32_t(tile >> 1) & 1u;      // parity of the team's count of tiles
+                ok = pg_wait_warp(&sh.s_full[team], use, ab, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                if (!begun) f = sh.qfac[item & 3][head] * lo_factor;
+                if (i < 2) f = sh.qfac[item & 3][head] * lo_factor;
                 const float4* scp = reinterpret_cast<const float4*>(&sh.scale[slot][32 * part]);
                 float s[32];
                 float mx = -INFINITY, smax = 0.f;
@@ -621,8 +571,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 // the reference after the tile before this one
                 if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, p.status);
                 if (!ok) break;
-                const bool fresh = sh.st_item[quarter] != item;
-                const int last_buf = sh.st_buf[quarter], last_use = sh.st_use[quarter];
+                const bool fresh = i == 0;
                 const float m_old = fresh ? mx : sh.st_m[head];
                 const float s_old = fresh ? smax : sh.st_sref[quarter];
                 // the reference follows the maximum in steps
@@ -630,12 +579,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 const float m_ref = grow ? mx : m_old, sref = fmaxf(s_old, smax);
                 __syncwarp();
                 if (part == 0) sh.st_m[head] = m_ref;
-                if (lane == 0) {
-                    sh.st_item[quarter] = item;
-                    sh.st_sref[quarter] = sref;
-                    sh.st_buf[quarter] = team;
-                    sh.st_use[quarter] = use;
-                }
+                if (lane == 0) sh.st_sref[quarter] = sref;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.dec[quarter]);
                 if (!fresh) {
@@ -657,7 +601,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (sh.vote[team][0] | sh.vote[team][1] | sh.vote[team][2] | sh.vote[team][3]) {
                         // the O products of the item's earlier tiles are complete (those before the
                         // last completed ahead of this tile's S: the tensor core works in order)
-                        ok = pg_wait_warp(&sh.p_empty[last_buf], uint32_t(last_use) & 1u, ab, p.status);
+                        ok = pg_wait_warp(&sh.p_empty[team ^ 1], uint32_t((tile - 1) >> 1) & 1u, ab, p.status);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -675,10 +619,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         tmem_wait_st();
                     }
                 }
-                l = begun && m_own != m_ref && m_own != -INFINITY ? l * ex2_approx(m_own - m_ref) : l;
+                l = m_own != m_ref && m_own != -INFINITY ? l * ex2_approx(m_own - m_ref) : l;
                 m_own = m_ref;
-                begun = true;
-                ok = pg_wait_warp(&sh.p_empty[team], (uint32_t(use) & 1u) ^ 1u, ab, p.status);
+                ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, p.status);
                 if (!ok) break;
                 if (active) {
                     const float off = kPgBias - (m_ref == -INFINITY ? 0.f : m_ref);
@@ -723,7 +666,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     mbar_arrive(&sh.p_full[team]);
                     mbar_arrive(&sh.empty[slot]);
                 }
-                ++use;
             }
             w.next(n);
         }
@@ -736,6 +678,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         bool ok = true;
         int t_prev = 0;
         bool whole_prev = false;
+        int teams_prev = 0;
 
         for (PgWalk w(sh);; ++item) {
             const bool more = w.left > 0;
@@ -825,6 +768,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const bool whole = whole_prev, first = done == 0;
             t_prev = w.t;
             whole_prev = more && w.k0 == 0 && n == pg_tiles(p, w.t);
+            const int teams = teams_prev;
+            teams_prev = n > 1 ? 3 : 1 << ((g - 1) & 1);     // (its only tile is use g - 1)
             w.next(n);
             if (done < 0) {
                 if (!more) break;                // a CTA without a tile
@@ -835,7 +780,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             if (!ok) break;
             tc_fence_after();
             const int st = done & 3;
-            const int any = sh.item_any[st];     // the teams that had tiles
+            const int any = teams;               // the softmax teams that had tiles of it
             float* fin = sh.fin[quarter];
             const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
             for (int h = lane; h < heads; h += 32) {
@@ -888,14 +833,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 dst[128 * k + e * kD] =
-                                    __float2bfloat16_rn(any ? __uint_as_float(v[k][e]) * fh[e] : 0.f);
+                                    __float2bfloat16_rn(__uint_as_float(v[k][e]) * fh[e]);
                     } else {
                         float* dst = p.part_o + (int64_t(part_at) * p.group_heads + h) * kD + d;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                dst[128 * k + e * kD] = any ? __uint_as_float(v[k][e]) * fh[e] : 0.f;
+                                dst[128 * k + e * kD] = __uint_as_float(v[k][e]) * fh[e];
                     }
                 }
             }

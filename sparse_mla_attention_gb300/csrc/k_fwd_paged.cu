@@ -30,7 +30,7 @@
 // (unnormalised O, maximum, sum), and combine_paged_kernel joins the parts in order.
 // Warps: 0-3 and 4-7 softmax, on alternate tiles (a thread has one head and half of
 // the tile's ranks: the two lanes of a head swap their halves of S, which adds hi and
-// lo), 8-11 q conversion and output, 12 MMA, 13-14 loads (TMA boxes where a tile's rows lie in
+// lo), 8-11 q conversion and output, 12 S products, 13 O products, 14-15 loads (TMA boxes where a tile's rows lie in
 // whole pages, four-row gathers otherwise). A masked rank loads a valid row of its
 // tile instead of its own (weight 0, and no byte of a row that nothing
 // names is ever read); a tile without a valid rank is filled with zeros.
@@ -56,7 +56,7 @@ constexpr int kPgSlotBytes = kPgTile * kD;       // 32 KB: four blocks of 64 row
 constexpr int kPgBlockBytes = kPgTile * 128;
 constexpr int kPgHeads = 64;                     // heads of a group at most
 constexpr int kPgPBytes = kPgHeads * 128;        // weights of a tile: 64 bytes hi, 64 bytes lo a head
-constexpr int kPgOutWarp = 8, kPgMmaWarp = 12, kPgLoadWarp = 13, kPgLoadWarps = 2;
+constexpr int kPgOutWarp = 8, kPgMmaWarp = 12, kPgLoadWarp = 14, kPgLoadWarps = 2;
 constexpr int kPgThreads = (kPgLoadWarp + kPgLoadWarps) * 32;
 constexpr int kPgMaxCtas = 160;
 // TMEM columns
@@ -69,7 +69,7 @@ constexpr float kPgBias = 5.f, kPgSlack = 3.f;
 struct PgShared {
     uint64_t full[kPgSlots], empty[kPgSlots], q_load[2];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-    uint64_t q_full, q_empty, o_full, o_empty, dec[4], vote_bar[2], drain;
+    uint64_t q_full, q_empty, o_full, o_empty, dec[4], vote_bar[2], drain[2];
     uint32_t tbase;
     volatile int abort_flag;
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
@@ -283,7 +283,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(&sh.vote_bar[0], 4);
         mbar_init(&sh.vote_bar[1], 4);
         for (int q = 0; q < 4; ++q) mbar_init(&sh.dec[q], 1);
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
         sh.abort_flag = 0;
         fence_mbar_init();
     }
@@ -419,63 +420,29 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 mbar_wait(&sh.q_load[q & 1], uint32_t(q >> 1) & 1u, kPgWaitNs / 8);
         }
         __syncwarp();
-    } else if (warp == kPgMmaWarp) {
+    } else if (warp >= kPgMmaWarp) {
         // ------------------------------------------------------------ MMA issue
-        // The whole warp walks the tiles, so that descriptors stay in uniform registers; one
-        // elected lane issues.
-        const uint32_t id_s = idesc_f8(128, kPgTile, false, false);
-        const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
+        // One warp issues the S products, one the O products: small MMAs keep the tensor core
+        // busy only if the waits for one kind pass while the other is issued. The whole warp
+        // walks the tiles, so that descriptors stay in uniform registers; one elected lane issues.
         const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
-        const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
         const bool leader = elect_one();
         int g = 0, tile = 0, item = 0;
-        uint32_t seen = 0;
-        bool ok = true, first = false, last = false;    // of the tile before: of its item
-        int prev = -1;                           // its slot; its O product follows this tile's S
-        // The O product of tile t in slot `at`
-        auto second = [&](int t, int at, int of) {
-            const int b = t & 1;
-            ok = pg_wait_warp(&sh.p_full[b], uint32_t(t >> 1) & 1u, ab, p.status);
-            if (ok && first && of > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(of - 1) & 1u, ab, p.status);
-            if (!ok) return;
-            tc_fence_after();
-            uint64_t va = ring_desc + uint32_t(at) * (kPgSlotBytes >> 4);
-            const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
-            if (leader) {
-                uint32_t acc = tbase + kPgColO;
+        bool ok = true;
+        if (warp == kPgMmaWarp) {
+            const uint32_t id_s = idesc_f8(128, kPgTile, false, false);
+            uint32_t seen = 0;
+            for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+                const int n = w.tiles(p);
+                g += 2;
 #pragma unroll 1
-                for (int db = 0; db < 4; ++db) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
-                        mma_f8_ss(acc, va + (((k & 1) * 4096) >> 4), wa + 2 * k, k < 2 ? id_hi : id_lo,
-                                  !(first && k == 0));
-                    va += kPgBlockBytes >> 4;
-                    acc += 64;
-                }
-                mma_commit(&sh.empty[at]);
-                mma_commit(&sh.p_empty[b]);
-                if (last) {
-                    mbar_arrive(&sh.o_full);
-                    mma_commit(&sh.o_full);
-                }
-            }
-            __syncwarp();
-        };
-        for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-            const int n = w.tiles(p);
-            g += 2;
-#pragma unroll 1
-            for (int i = 0; i <= n; ++i) {
-                // the O product of the range's very last tile has no S before it
-                if (i == n && w.left > n) break;
-                const int slot = pg_slot(g);
-                if (i < n) {
-                    const int b = tile & 1;
-                    ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
-                    seen ^= 1u << slot;
-                    if (ok && i == 0) ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                for (int i = 0; i < n; ++i, ++g, ++tile) {
+                    const int slot = pg_slot(g), b = tile & 1;
+                    if (i == 0) ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
                     if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(tile >> 1) & 1u) ^ 1u, ab, p.status);
+                    if (ok) ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
                     if (!ok) break;
+                    seen ^= 1u << slot;
                     tc_fence_after();
                     uint64_t ka = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
                     if (leader) {
@@ -494,18 +461,50 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     __syncwarp();
                 }
-                if (prev >= 0) second(tile - 1, prev, i == 0 ? item - 1 : item);
-                if (!ok) break;
-                prev = slot;
-                first = i == 0;
-                last = i == n - 1;
-                if (i < n) { ++tile; ++g; }
+                w.next(n);
             }
-            w.next(n);
+        } else {
+            const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
+            const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
+            for (PgWalk w(sh); w.left > 0 && ok; ++item) {
+                const int n = w.tiles(p);
+                g += 2;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, ++g, ++tile) {
+                    const int slot = pg_slot(g), b = tile & 1;
+                    if (i == 0 && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
+                    if (ok) ok = pg_wait_warp(&sh.p_full[b], uint32_t(tile >> 1) & 1u, ab, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint64_t va = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
+                    const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
+                    if (leader) {
+                        uint32_t acc = tbase + kPgColO;
+#pragma unroll 1
+                        for (int db = 0; db < 4; ++db) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)      // hi ranks 0-31, 32-63, then lo
+                                mma_f8_ss(acc, va + (((k & 1) * 4096) >> 4), wa + 2 * k, k < 2 ? id_hi : id_lo,
+                                          (i | k) != 0);
+                            va += kPgBlockBytes >> 4;
+                            acc += 64;
+                        }
+                        mma_commit(&sh.empty[slot]);
+                        mma_commit(&sh.p_empty[b]);
+                        if (i == n - 1) {
+                            mbar_arrive(&sh.o_full);
+                            mma_commit(&sh.o_full);
+                        }
+                    }
+                    __syncwarp();
+                }
+                w.next(n);
+            }
         }
         if (leader) {
-            mma_commit(&sh.drain);
-            mbar_wait(&sh.drain, 0, kPgWaitNs);
+            uint64_t* bar = &sh.drain[warp - kPgMmaWarp];
+            mma_commit(bar);
+            mbar_wait(bar, 0, kPgWaitNs);
         }
         __syncwarp();
     } else if (warp < kPgOutWarp) {
@@ -582,6 +581,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (lane == 0) sh.st_sref[quarter] = sref;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.dec[quarter]);
+                // the team's weights before these are used up
+                ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, p.status);
+                if (!ok) break;
                 if (!fresh) {
                     // all warps of the team agree on rescaling, because a warp's TMEM lanes are
                     // columns of D, not heads
@@ -599,8 +601,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (!ok) break;
                     ++votes;
                     if (sh.vote[team][0] | sh.vote[team][1] | sh.vote[team][2] | sh.vote[team][3]) {
-                        // the O products of the item's earlier tiles are complete (those before the
-                        // last completed ahead of this tile's S: the tensor core works in order)
+                        // the O products of the item's earlier tiles are complete (the one before
+                        // last is, just above, so that the parity means the last one's phase)
                         ok = pg_wait_warp(&sh.p_empty[team ^ 1], uint32_t((tile - 1) >> 1) & 1u, ab, p.status);
                         if (!ok) break;
                         tc_fence_after();
@@ -621,8 +623,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 l = m_own != m_ref && m_own != -INFINITY ? l * ex2_approx(m_own - m_ref) : l;
                 m_own = m_ref;
-                ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, p.status);
-                if (!ok) break;
                 if (active) {
                     const float off = kPgBias - (m_ref == -INFINITY ? 0.f : m_ref);
                     const float inv = sref > 0.f ? 1.f / sref : 0.f;

@@ -30,7 +30,7 @@
 // (unnormalised O, maximum, sum), and combine_paged_kernel joins the parts in order.
 // Warps: 0-3 and 4-7 softmax, on alternate tiles (a thread has one head and half of
 // the tile's ranks: the two lanes of a head swap their halves of S, which adds hi and
-// lo), 8-11 q conversion and output, 12 S products, 13 O products, 14-15 loads (TMA boxes where a tile's rows lie in
+// lo), 8-11 q conversion and output, 12 S products, 13 O products, 14-17 loads (TMA boxes where a tile's rows lie in
 // whole pages, four-row gathers otherwise). A masked rank loads a valid row of its
 // tile instead of its own (weight 0, and no byte of a row that nothing
 // names is ever read); a tile without a valid rank is filled with zeros.
@@ -47,7 +47,7 @@ using namespace sm100;
 
 namespace {
 
-constexpr uint64_t kPgWaitNs = 2000000000ull;
+constexpr uint32_t kPgWaitNs = 2000000000u;
 constexpr float kPgLog2e = 1.4426950408889634f;
 constexpr float kPgLn2 = 0.6931471805599453f;
 constexpr int kPgTile = 64;                      // ranks per tile
@@ -56,7 +56,7 @@ constexpr int kPgSlotBytes = kPgTile * kD;       // 32 KB: four blocks of 64 row
 constexpr int kPgBlockBytes = kPgTile * 128;
 constexpr int kPgHeads = 64;                     // heads of a group at most
 constexpr int kPgPBytes = kPgHeads * 128;        // weights of a tile: 64 bytes hi, 64 bytes lo a head
-constexpr int kPgOutWarp = 8, kPgMmaWarp = 12, kPgLoadWarp = 14, kPgLoadWarps = 2;
+constexpr int kPgOutWarp = 8, kPgMmaWarp = 12, kPgLoadWarp = 14, kPgLoadWarps = 4;
 constexpr int kPgThreads = (kPgLoadWarp + kPgLoadWarps) * 32;
 constexpr int kPgMaxCtas = 160;
 // TMEM columns
@@ -69,19 +69,18 @@ constexpr float kPgBias = 5.f, kPgSlack = 3.f;
 struct PgShared {
     uint64_t full[kPgSlots], empty[kPgSlots], q_load[2];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-    uint64_t q_full, q_empty, o_full, o_empty, dec[4], vote_bar[2], drain[2];
+    uint64_t q_full, q_empty, o_full, o_empty, dec[4], fixed[2], drain[2];
     uint32_t tbase;
     volatile int abort_flag;
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
     int sum[kPgThreads / 32];
-    uint32_t vote[2][4];
-    float st_sref[4];                            // per lane quarter: largest block scale of the item so far
-    float sref[4][2];
-    __align__(16) float scale[kPgSlots][kPgTile];     // block scale of each rank, -1: masked
-    __align__(16) float fac[2][kPgHeads];             // rescaling factors
+    __align__(16) uint32_t need[2][2][4];        // team, parity of its count, lane quarter: rescale O first
+    __align__(16) float smax[kPgSlots][kPgLoadWarps];     // largest block scale of 16 ranks
+    __align__(16) float2 scale[kPgSlots][kPgTile];        // of each rank: block scale and 0, or 0 and -inf (masked)
+    __align__(16) float fac[2][2][kPgHeads];     // rescaling factors (team, parity of its count)
     float qfac[4][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
-    float st_m[kPgHeads];                        // running reference of a head
-    float m[4][2][kPgHeads], l[4][2][kPgHeads];  // per item and team: reference and sum of a head
+    float st_ref[kPgHeads];                      // running reference of a head
+    float ref[4][2][kPgHeads], l[4][2][kPgHeads];         // per item and team: reference and sum of a head
     __align__(16) float fin[4][kPgHeads];        // per output warp: 1 / denominator
 };
 
@@ -101,21 +100,24 @@ struct PgParams {
     float* part_o;                               // [CTAs][2][group_heads][512]
 };
 
-// The waiting itself stays out of line: the kernel's warps run different code, and
-// forty copies of the loop cost more in instruction fetches than the call.
-__device__ __noinline__ bool pg_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned* status) {
-    if (*abort_flag) return false;
-    if (mbar_wait(bar, parity, kPgWaitNs)) return true;
-    *abort_flag = 1;
-    flag_status(status, SMLA_ERR_TIMEOUT);
-    return false;
-}
-
+// Every lane waits, for at most about two seconds; the warp goes on only if all of them
+// saw the phase. Short on purpose (the kernel has many waits, its warps run different
+// code, and instruction fetches count), and quiet: a waiting warp sleeps in
+// try_wait and looks at the timer only now and then.
 __device__ __forceinline__ bool pg_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              unsigned* status) {
     bool ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = pg_wait_slow(bar, parity, abort_flag, status);
+    if (!ok) {
+        const uint32_t t0 = globaltimer_lo_ns();
+        do {
+#pragma unroll 1
+            for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+            if (!ok && globaltimer_lo_ns() - t0 > kPgWaitNs) {
+                *abort_flag = 1;
+                flag_status(status, SMLA_ERR_TIMEOUT);
+            }
+        } while (!ok && !*abort_flag);
+    }
     return __all_sync(0xffffffffu, ok) != 0;
 }
 
@@ -134,11 +136,11 @@ __device__ __forceinline__ int pg_tiles(const PgParams& p, int t) {
 // The ring's uses are an item's q (two) and then its tiles, numbered over all
 // items; use g is in slot g % kPgSlots. A parity wait tells a phase only from the
 // one before, so whoever waits for a barrier sees each of its phases in turn:
-// `empty` counts every use (each slot is refilled by one loading warp), `full` the
+// `empty` counts every use (each loading warp has a part in each), `full` the
 // tiles alone (MMA and softmax keep a parity bit a slot), and q has barriers of its
 // own, q_load[item & 1] (the q of item + 2 goes no earlier than six uses on, into
 // slots that item's q has left).
-static_assert(kPgSlots % 2 == 0 && kPgSlots >= 6, "a slot belongs to one of the two loading warps");
+static_assert(kPgSlots % 2 == 0 && kPgSlots >= 6, "a slot belongs to one of the two softmax teams");
 __device__ __forceinline__ int pg_slot(int g) { return g % kPgSlots; }
 __device__ __forceinline__ uint32_t pg_parity(uint32_t bits, int slot) { return (bits >> slot) & 1u; }
 
@@ -153,22 +155,15 @@ struct PgDeal {
     }
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
-}
 __device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
     return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ __half2 e4m3x2_half(uint32_t v) {
     return __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3));
 }
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
-    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3)));
+__device__ __forceinline__ uint32_t e5m2x2(__half2 v) {
+    return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E5M2);
 }
-
 // The CTA's share of the tiles. Picks: every token has as many tiles. All
 // positions: sums the tiles of the tokens (thread i those of a run of tokens), then
 // the thread whose run holds the CTA's first tile finds its token.
@@ -266,11 +261,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPgSlots; ++s) {
-            mbar_init(&sh.full[s], 32);          // the lanes of the loading warp
-            mbar_init(&sh.empty[s], 5);          // tile: MMA and four softmax warps; q: the output warps
+            mbar_init(&sh.full[s], kPgLoadWarps);
+            mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sh.q_load[b], 8);         // four lanes a use
+            mbar_init(&sh.q_load[b], 2 * kPgLoadWarps);
             mbar_init(&sh.s_full[b], 2);         // MMA completion and the issuing thread
             mbar_init(&sh.s_empty[b], 4);
             mbar_init(&sh.p_full[b], 4);
@@ -280,8 +275,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.o_full, 2);                // MMA completion and the issuing thread
         mbar_init(&sh.o_empty, 4);
-        mbar_init(&sh.vote_bar[0], 4);
-        mbar_init(&sh.vote_bar[1], 4);
+        mbar_init(&sh.fixed[0], 4);
+        mbar_init(&sh.fixed[1], 4);
         for (int q = 0; q < 4; ++q) mbar_init(&sh.dec[q], 1);
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
@@ -297,124 +292,154 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
     if (warp >= kPgLoadWarp) {
         // --------------------------------------------------------------- loads
-        // Two warps take the ring uses in turn: an item's q (two uses of four 64-column boxes)
-        // and its tiles. Lanes 2i and 2i + 1 look up the ranks 4i .. 4i+3 of a tile
-        // and, where they are gathered, load two of their four column blocks each.
-        const int quad = lane >> 1, half = lane & 1;
-        const int box_rows = (1 << p.page_shift) < kPgTile ? (1 << p.page_shift) : kPgTile;
+        // Every warp has a part in each ring use: of an item's q (two uses of four 64-column
+        // boxes) one box; of a tile whose rows lie in whole runs of 16 (all positions,
+        // none masked) one column block of all 64 ranks, as TMA boxes; of other tiles 16 ranks,
+        // as four-row gathers (issued lane by lane, some 75 cycles each: hence four warps).
+        // Picks: positions are loaded two tiles ahead, pages and scales one tile ahead.
+        const int lw = warp - kPgLoadWarp;
+        const int64_t limit = int64_t(p.max_pages) << p.page_shift;
+        const int page_mask = (1 << p.page_shift) - 1;
+        const int box_rows = page_mask + 1 < kPgTile ? page_mask + 1 : kPgTile;
+        bool bad = false;
+        // Look-ups ahead of the loads: tile after tile over all items.
+        PgWalk wa(sh);
+        int na = 0, ia = 0, ba = 0, lena = 0;
+        auto open_item = [&]() {
+            ia = 0;
+            na = 0;
+            if (wa.left <= 0) return;
+            na = wa.tiles(p);
+            lena = __ldg(p.lens + wa.t);
+            if (lena < 0 || lena > limit) { bad = true; lena = lena < 0 ? 0 : int(limit); }
+            ba = p.seq ? __ldg(p.seq + wa.t) : wa.t;
+            if (ba < 0 || ba >= p.B) { bad = true; lena = 0; }
+        };
+        // Lane's position in the next tile, as it stands in topk; for all positions that of the
+        // first rank of run (lane & 3) of 16
+        struct Ahead { int pos, len, b; };
+        auto look = [&]() {
+            Ahead x{-1, 0, 0};
+            if (na > 0) {
+                const int r0 = kPgTile * (wa.k0 + ia);
+                x.len = lena;
+                x.b = ba;
+                if (p.topk) {
+                    const int r = r0 + 16 * lw + (lane & 15);
+                    x.pos = r < p.K ? __ldg(p.topk + int64_t(wa.t) * p.K + r) : -1;
+                } else {
+                    x.pos = r0 + 16 * (lane & 3);
+                }
+                if (++ia == na) {
+                    wa.next(na);
+                    open_item();
+                }
+            }
+            return x;
+        };
+        auto page_of = [&](const Ahead& x) {     // -1: masked
+            if (p.topk) bad |= x.pos < -1 || x.pos >= x.len;
+            if (x.pos < 0 || x.pos >= x.len) return -1;
+            return __ldg(p.table + int64_t(x.b) * p.max_pages + (x.pos >> p.page_shift));
+        };
+        auto row_of = [&](const Ahead& x, int page) {
+            const bool v = x.pos >= 0 && x.pos < x.len;
+            bad |= v && (page < 0 || page >= p.num_pages);
+            return v && page >= 0 && page < p.num_pages ? (page << p.page_shift) + (x.pos & page_mask) : -1;
+        };
+        open_item();
+        Ahead x0 = look(), x1 = look();          // the tile at hand and the next one
+        int row = row_of(x0, page_of(x0));
+        float sc = row >= 0 ? __ldg(p.scales + (row >> p.block_shift)) : -1.f;
+
         int g = 0, item = 0;
         uint32_t loads = 0;                      // parity of each slot's last tile load
         int q_last = -1;
-        bool ok = true, bad = false;
+        bool ok = true;
         for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-            const int n = w.tiles(p), t = w.t;
-            int len = __ldg(p.lens + t);
-            const int64_t limit = int64_t(p.max_pages) << p.page_shift;
-            if (len < 0 || len > limit) { bad = true; len = len < 0 ? 0 : int(limit); }
-            const int b = p.seq ? __ldg(p.seq + t) : t;
-            if (b < 0 || b >= p.B) { bad = true; len = 0; }
-            for (int i = 0; i < n + 2 && ok; ++i, ++g) {
-                if (g % kPgLoadWarps != warp - kPgLoadWarp) continue;
+            const int n = w.tiles(p);
+#pragma unroll 1
+            for (int i = 0; i < n + 2; ++i, ++g) {
                 const int slot = pg_slot(g);
-                const uint32_t free_ph = (uint32_t(g / kPgSlots) & 1u) ^ 1u;
                 uint8_t* dst = ring + slot * kPgSlotBytes;
+                const int page1 = i < 2 ? 0 : page_of(x1);
+                Ahead x2{};
+                if (i >= 2) x2 = look();
+                ok = pg_wait_warp(&sh.empty[slot], (uint32_t(g / kPgSlots) & 1u) ^ 1u, ab, p.status);
+                if (!ok) break;
                 if (i < 2) {
-                    ok = pg_wait_warp(&sh.empty[slot], free_ph, ab, p.status);
-                    if (!ok) break;
                     q_last = item;
-                    if (lane < 4) {
+                    if (lane == 0) {
                         mbar_arrive_expect_tx(&sh.q_load[item & 1], uint32_t(p.group_heads) * 128u);
-                        tma_load_2d(dst + lane * kPgBlockBytes, &map_q, (4 * i + lane) * 64, t * p.H + head0,
+                        tma_load_2d(dst + lw * kPgBlockBytes, &map_q, (4 * i + lw) * 64, w.t * p.H + head0,
                                     &sh.q_load[item & 1]);
                     }
                     continue;
                 }
-                const int r0 = kPgTile * (w.k0 + i - 2) + 4 * quad;
-                int row[4];
-                float sc[4];
-                if (p.topk) {
-                    int pos[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        pos[e] = r0 + e < p.K ? __ldg(p.topk + int64_t(t) * p.K + r0 + e) : -1;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        bad |= pos[e] < -1 || pos[e] >= len;
-                        const bool v = pos[e] >= 0 && pos[e] < len;
-                        row[e] = v ? __ldg(p.table + int64_t(b) * p.max_pages + (pos[e] >> p.page_shift)) : -1;
-                        bad |= v && (row[e] < 0 || row[e] >= p.num_pages);
-                        row[e] = row[e] < 0 || row[e] >= p.num_pages
-                                     ? -1
-                                     : (row[e] << p.page_shift) + (pos[e] & ((1 << p.page_shift) - 1));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[e] = row[e] >= 0 ? __ldg(p.scales + (row[e] >> p.block_shift)) : -1.f;
-                } else {
-                    // four consecutive positions: one page, one scale block
-                    int first = -1;
-                    float s = -1.f;
-                    if (r0 < len) {
-                        const int page = __ldg(p.table + int64_t(b) * p.max_pages + (r0 >> p.page_shift));
-                        if (page < 0 || page >= p.num_pages) {
-                            bad = true;
-                        } else {
-                            first = (page << p.page_shift) + (r0 & ((1 << p.page_shift) - 1));
-                            s = __ldg(p.scales + (first >> p.block_shift));
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool v = first >= 0 && r0 + e < len;
-                        row[e] = v ? first + e : -1;
-                        sc[e] = v ? s : -1.f;
-                    }
-                }
-                const bool mine = row[0] >= 0 || row[1] >= 0 || row[2] >= 0 || row[3] >= 0;
-                const bool whole = row[0] >= 0 && row[1] >= 0 && row[2] >= 0 && row[3] >= 0;
-                const unsigned some = __ballot_sync(0xffffffffu, mine);
-                const bool all = __all_sync(0xffffffffu, whole) != 0;
-                // a valid row of the tile, loaded in place of masked ones
-                int stand = row[0] >= 0 ? row[0] : row[1] >= 0 ? row[1] : row[2] >= 0 ? row[2] : row[3];
-                stand = __shfl_sync(0xffffffffu, stand, some ? __ffs(some) - 1 : 0);
-                ok = pg_wait_warp(&sh.empty[slot], free_ph, ab, p.status);
-                if (!ok) break;
                 loads ^= 1u << slot;             // full's phase of this load has the parity before
-                if (half == 0)
-                    *reinterpret_cast<float4*>(&sh.scale[slot][4 * quad]) = make_float4(sc[0], sc[1], sc[2], sc[3]);
-                if (some == 0) {                 // nothing valid: a tile of zeros, all of it masked
-#pragma unroll 4
-                    for (int k = 0; k < kPgSlotBytes / 512; ++k)
-                        reinterpret_cast<uint4*>(dst)[32 * k + lane] = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    mbar_arrive(&sh.full[slot]);
-                } else if (all && !p.topk) {
-                    const int seg = lane >> 2, cb = lane & 3;
-                    const int y = __shfl_sync(0xffffffffu, row[0], (seg * box_rows / 4 * 2) & 31);
-                    if (seg * box_rows < kPgTile) {
-                        mbar_arrive_expect_tx(&sh.full[slot], uint32_t(box_rows) * 128u);
-                        tma_load_2d(dst + cb * kPgBlockBytes + seg * box_rows * 128, &map_box, cb * 128, y,
-                                    &sh.full[slot]);
-                    } else {
-                        mbar_arrive(&sh.full[slot]);
+                const int left = x0.len - (x0.pos - 16 * (lane & 3));    // all positions: from the tile's first on
+                const bool boxes = !p.topk && __all_sync(0xffffffffu, row >= 0 && left >= kPgTile) != 0;
+                float sc16 = sc;                 // scale of the warp's rank (lane & 15)
+                if (boxes) {
+                    if (lane == 0) mbar_expect_tx(&sh.full[slot], kPgBlockBytes);
+#pragma unroll 1
+                    for (int r = 0; r < kPgTile; r += box_rows) {
+                        const int y = __shfl_sync(0xffffffffu, row, r >> 4);
+                        if (lane == 0)
+                            tma_load_2d(dst + lw * kPgBlockBytes + r * 128, &map_box, lw * 128, y, &sh.full[slot]);
                     }
+                    sc16 = __shfl_sync(0xffffffffu, sc, lw);
                 } else {
+                    int mine = row;
+                    if (!p.topk) {               // ranks 16 lw + (lane & 15), as far as the sequence goes
+                        mine = __shfl_sync(0xffffffffu, row, lw);
+                        sc16 = __shfl_sync(0xffffffffu, sc, lw);
+                        const bool v = mine >= 0 && 16 * lw + (lane & 15) < left;
+                        mine = v ? mine + (lane & 15) : -1;
+                        sc16 = v ? sc16 : -1.f;
+                    }
+                    // a masked rank loads a valid row of the warp's ranks instead; without one, zeros
+                    const unsigned some = __ballot_sync(0xffffffffu, mine >= 0);
+                    const int stand = __shfl_sync(0xffffffffu, mine, some ? __ffs(some) - 1 : 0);
+                    if (mine < 0) mine = stand;
+                    uint8_t* at = dst + 16 * lw * 128;
+                    if (some) {
+                        const int quad = (lane >> 2) & 3, cb = lane & 3;
+                        const int y0 = __shfl_sync(0xffffffffu, mine, 4 * quad);
+                        const int y1 = __shfl_sync(0xffffffffu, mine, 4 * quad + 1);
+                        const int y2 = __shfl_sync(0xffffffffu, mine, 4 * quad + 2);
+                        const int y3 = __shfl_sync(0xffffffffu, mine, 4 * quad + 3);
+                        if (lane == 0) mbar_expect_tx(&sh.full[slot], kPgBlockBytes);
+                        __syncwarp();
+                        if (lane < 16)
+                            tma_gather4(at + cb * kPgBlockBytes + quad * 512, &map_row, cb * 128, y0, y1, y2, y3,
+                                        &sh.full[slot]);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) row[e] = row[e] >= 0 ? row[e] : stand;
-                    mbar_arrive_expect_tx(&sh.full[slot], 1024u);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int cb = 2 * half + k;
-                        tma_gather4(dst + cb * kPgBlockBytes + quad * 512, &map_row, cb * 128, row[0], row[1], row[2],
-                                    row[3], &sh.full[slot]);
+                        for (int k = 0; k < 16; ++k)     // 16 rows of 128 bytes in each of four blocks
+                            *reinterpret_cast<uint4*>(at + (k >> 2) * kPgBlockBytes + (k & 3) * 512 + 16 * lane) =
+                                make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
                     }
                 }
+                if (lane < 16)
+                    sh.scale[slot][16 * lw + lane] = make_float2(fmaxf(sc16, 0.f), sc16 >= 0.f ? 0.f : -INFINITY);
+                // (scales are not negative: their bits order like unsigned integers)
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sc16, 0.f)));
+                if (lane == 0) sh.smax[slot][lw] = __uint_as_float(top);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[slot]);
+                // the next tile's rows and scales
+                row = row_of(x1, page1);
+                sc = row >= 0 ? __ldg(p.scales + (row >> p.block_shift)) : -1.f;
+                x0 = x1;
+                x1 = x2;
             }
             w.next(n);
         }
         if (bad) flag_status(p.status, SMLA_ERR_INDEX);
         if (sh.abort_flag) {     // the loads already issued land before the CTA exits
-            for (int slot = warp - kPgLoadWarp; slot < kPgSlots; slot += kPgLoadWarps)
+            for (int slot = 0; slot < kPgSlots; ++slot)
                 mbar_wait(&sh.full[slot], pg_parity(loads, slot) ^ 1u, kPgWaitNs / 8);
             for (int q = q_last > 0 ? q_last - 1 : 0; q <= q_last; ++q)
                 mbar_wait(&sh.q_load[q & 1], uint32_t(q >> 1) & 1u, kPgWaitNs / 8);
@@ -438,7 +463,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++g, ++tile) {
                     const int slot = pg_slot(g), b = tile & 1;
-                    if (i == 0) ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                    if (i == 0) {
+                        ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                        if (ok && leader) {      // q is in TMEM: its slots are free
+                            mbar_arrive(&sh.empty[pg_slot(g - 2)]);
+                            mbar_arrive(&sh.empty[pg_slot(g - 1)]);
+                        }
+                    }
                     if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(tile >> 1) & 1u) ^ 1u, ab, p.status);
                     if (ok) ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
                     if (!ok) break;
@@ -464,6 +495,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 w.next(n);
             }
         } else {
+            int fixes0 = 0, fixes1 = 0;          // times that each team rescaled O
             const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
             const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
             for (PgWalk w(sh); w.left > 0 && ok; ++item) {
@@ -475,6 +507,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (i == 0 && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
                     if (ok) ok = pg_wait_warp(&sh.p_full[b], uint32_t(tile >> 1) & 1u, ab, p.status);
                     if (!ok) break;
+                    const uint4 need = *reinterpret_cast<const uint4*>(sh.need[b][(tile >> 1) & 1]);
+                    if (need.x | need.y | need.z | need.w) {
+                        ok = pg_wait_warp(&sh.fixed[b], uint32_t(b ? fixes1 : fixes0) & 1u, ab, p.status);
+                        if (!ok) break;
+                        if (b) ++fixes1; else ++fixes0;
+                    }
                     tc_fence_after();
                     uint64_t va = ring_desc + uint32_t(slot) * (kPgSlotBytes >> 4);
                     const uint64_t wa = p_desc + uint32_t(b) * (kPgPBytes >> 4);
@@ -509,26 +547,63 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         __syncwarp();
     } else if (warp < kPgOutWarp) {
         // -------------------------------------------------------------- softmax
-        // Two teams of four warps take the tiles in turn (a tile's team is its
-        // slot's parity). A head's running reference passes from team to team along dec[quarter].
+        // Two teams of four warps take the tiles in turn (a tile's team is its slot's
+        // parity). A head's reference r is kept so that weights 2^(s - r + bias) * block scale stay
+        // below e4m3's largest value: it starts as the first tile's largest score plus
+        // log2 of its largest scale and follows when a tile passes it by more than the
+        // slack. It passes from team to team along dec[quarter]; O is rescaled for a tile by
+        // its team, before its O product but after its weights are written, so that no
+        // warp waits for the others' verdicts on the way.
         const int team = warp >> 2, quarter = warp & 3;
         const int part = lane >> 4, head = 16 * quarter + (lane & 15);
         const bool active = 16 * quarter < heads;
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
         const float lo_factor = part ? 0.0625f : 1.f;
-        int g = 0, tile = 0, item = 0, votes = 0;
-        uint32_t seen = 0;
+        uint8_t* prow = pbuf + team * kPgPBytes + head * 128;
+        int g = 0, tile = 0, item = 0, mine = -1;        // mine: the team's last tile
         bool ok = true;
+        // rescales O for the team's last tile, if one of its warps asked for it
+        auto fix = [&]() {
+            if (mine < 0) return;
+            const int c = (mine >> 1) & 1;
+            ok = pg_wait_warp(&sh.p_full[team], uint32_t(c), ab, p.status);
+            if (!ok) return;
+            const uint4 need = *reinterpret_cast<const uint4*>(sh.need[team][c]);
+            if ((need.x | need.y | need.z | need.w) == 0) return;
+            // the O products before that tile's are complete (the one before last is, since the
+            // weights could be written: so the parity means the last one's phase)
+            ok = pg_wait_warp(&sh.p_empty[team ^ 1], uint32_t((mine - 1) >> 1) & 1u, ab, p.status);
+            if (!ok) return;
+            tc_fence_after();
+            // a warp's TMEM lanes are columns of D, not heads: every warp rescales all heads
+#pragma unroll 1
+            for (int k = 0; k < 4 * heads; k += 16) {
+                const int db = k / heads, h = k - db * heads;
+                const uint32_t at = trow + kPgColO + 64 * db + h;
+                uint32_t v[16];
+                tmem_ld16(at, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] = __float_as_uint(__uint_as_float(v[e]) * sh.fac[team][c][h + e]);
+                tmem_st16(at, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.fixed[team]);
+        };
         for (PgWalk w(sh); w.left > 0 && ok; ++item) {
             const int n = w.tiles(p);
             g += 2;
-            float m_own = -INFINITY, l = 0.f, f = 0.f;
+            float own_ref = -INFINITY, l = 0.f, f = 0.f;
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++g, ++tile) {
                 const int slot = pg_slot(g);
                 if ((slot & 1) != team) continue;
-                ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
+                fix();
                 if (!ok) break;
-                seen ^= 1u << slot;
+                mine = tile;
                 const uint32_t use = uint32_t(tile >> 1) & 1u;      // parity of the team's count of tiles
                 ok = pg_wait_warp(&sh.s_full[team], use, ab, p.status);
                 if (!ok) break;
@@ -536,115 +611,74 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (i < 2) f = sh.qfac[item & 3][head] * lo_factor;
                 const float4* scp = reinterpret_cast<const float4*>(&sh.scale[slot][32 * part]);
                 float s[32];
-                float mx = -INFINITY, smax = 0.f;
-                {
-                    uint32_t v0[32], v1[32];
-                    tmem_ld32(trow + kPgColS + kPgTile * team, v0);
-                    tmem_ld32(trow + kPgColS + kPgTile * team + 32, v1);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.s_empty[team]);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
                     // the head's other lane has the other part of q: swap halves and add
+                    uint32_t v0[16], v1[16];
+                    tmem_ld16(trow + kPgColS + kPgTile * team + 16 * q, v0);
+                    tmem_ld16(trow + kPgColS + kPgTile * team + 32 + 16 * q, v1);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float own = __uint_as_float(part ? v1[e] : v0[e]) * f;
-                        const float give = __uint_as_float(part ? v0[e] : v1[e]) * f;
-                        s[e] = own + __shfl_xor_sync(0xffffffffu, give, 16);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 c2 = scp[8 * q + e / 2];       // two ranks: scale and mask
+                        const float g0 = __uint_as_float(part ? v0[e] : v1[e]) * f;
+                        const float g1 = __uint_as_float(part ? v0[e + 1] : v1[e + 1]) * f;
+                        const float x0 = fmaf(__uint_as_float(part ? v1[e] : v0[e]), f,
+                                              __shfl_xor_sync(0xffffffffu, g0, 16));
+                        const float x1 = fmaf(__uint_as_float(part ? v1[e + 1] : v0[e + 1]), f,
+                                              __shfl_xor_sync(0xffffffffu, g1, 16));
+                        s[16 * q + e] = fmaf(x0, c2.x, c2.y);
+                        s[16 * q + e + 1] = fmaf(x1, c2.z, c2.w);
+                        mx = fmaxf(mx, fmaxf(s[16 * q + e], s[16 * q + e + 1]));
                     }
                 }
-#pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    const float4 c4 = scp[e4];
-                    const float c[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float& x = s[4 * e4 + e];
-                        x = c[e] >= 0.f ? x * c[e] : -INFINITY;
-                        mx = fmaxf(mx, x);
-                        smax = fmaxf(smax, c[e]);
-                    }
-                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_empty[team]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 16));
+                const float4 sm = *reinterpret_cast<const float4*>(sh.smax[slot]);
+                const float top = mx + __log2f(fmaxf(fmaxf(fmaxf(sm.x, sm.y), fmaxf(sm.z, sm.w)), 0x1p-100f));
                 // the reference after the tile before this one
                 if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, p.status);
                 if (!ok) break;
-                const bool fresh = i == 0;
-                const float m_old = fresh ? mx : sh.st_m[head];
-                const float s_old = fresh ? smax : sh.st_sref[quarter];
-                // the reference follows the maximum in steps
-                const bool grow = active && mx > m_old + kPgSlack;
-                const float m_ref = grow ? mx : m_old, sref = fmaxf(s_old, smax);
-                __syncwarp();
-                if (part == 0) sh.st_m[head] = m_ref;
-                if (lane == 0) sh.st_sref[quarter] = sref;
+                const float old = i == 0 ? top : sh.st_ref[head];
+                const bool grow = active && top > old + kPgSlack;
+                const float ref = grow ? top : old;
+                const bool need = __any_sync(0xffffffffu, grow) != 0;
+                if (part == 0) {
+                    sh.st_ref[head] = ref;
+                    sh.fac[team][use][head] = grow && old != -INFINITY ? ex2_approx(old - ref) : 1.f;
+                }
+                if (lane == 0) sh.need[team][use][quarter] = need;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.dec[quarter]);
+                l = own_ref != ref && own_ref != -INFINITY ? l * ex2_approx(own_ref - ref) : l;
+                own_ref = ref;
                 // the team's weights before these are used up
                 ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, p.status);
                 if (!ok) break;
-                if (!fresh) {
-                    // all warps of the team agree on rescaling, because a warp's TMEM lanes are
-                    // columns of D, not heads
-                    const bool need = __any_sync(0xffffffffu, grow || smax > s_old) != 0;
-                    if (part == 0)
-                        sh.fac[team][head] =
-                            (grow && m_old != -INFINITY ? ex2_approx(m_old - m_ref) : 1.f) *
-                            (s_old > 0.f ? s_old / sref : 1.f);
-                    __syncwarp();
-                    if (lane == 0) {
-                        sh.vote[team][quarter] = need;
-                        mbar_arrive(&sh.vote_bar[team]);
-                    }
-                    ok = pg_wait_warp(&sh.vote_bar[team], uint32_t(votes) & 1u, ab, p.status);
-                    if (!ok) break;
-                    ++votes;
-                    if (sh.vote[team][0] | sh.vote[team][1] | sh.vote[team][2] | sh.vote[team][3]) {
-                        // the O products of the item's earlier tiles are complete (the one before
-                        // last is, just above, so that the parity means the last one's phase)
-                        ok = pg_wait_warp(&sh.p_empty[team ^ 1], uint32_t((tile - 1) >> 1) & 1u, ab, p.status);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < 4 * heads; c += 16) {
-                            const int db = c / heads, h = c - db * heads;
-                            const uint32_t at = trow + kPgColO + 64 * db + h;
-                            uint32_t v[16];
-                            tmem_ld16(at, v);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                v[e] = __float_as_uint(__uint_as_float(v[e]) * sh.fac[team][h + e]);
-                            tmem_st16(at, v);
-                        }
-                        tmem_wait_st();
-                    }
-                }
-                l = m_own != m_ref && m_own != -INFINITY ? l * ex2_approx(m_own - m_ref) : l;
-                m_own = m_ref;
                 if (active) {
-                    const float off = kPgBias - (m_ref == -INFINITY ? 0.f : m_ref);
-                    const float inv = sref > 0.f ? 1.f / sref : 0.f;
-                    uint8_t* prow = pbuf + team * kPgPBytes + head * 128;
+                    const float off = kPgBias - (ref == -INFINITY ? 0.f : ref);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {            // 16 ranks: 16 bytes hi and 16 bytes lo
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e4 = 0; e4 < 4; ++e4) {
-                            const float4 c4 = scp[4 * q + e4];
-                            const float c[4] = {c4.x, c4.y, c4.z, c4.w};
-                            float x[4];
+                            uint32_t hl[2], ll[2];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float pr = ex2_approx(s[16 * q + 4 * e4 + e] + off);
-                                l += pr;
-                                x[e] = pr * (c[e] * inv);
+                            for (int k = 0; k < 2; ++k) {
+                                const int e = 16 * q + 4 * e4 + 2 * k;
+                                const float4 c2 = scp[e / 2];
+                                const float p0 = ex2_approx(s[e] + off), p1 = ex2_approx(s[e + 1] + off);
+                                l += p0 + p1;
+                                // half precision holds a weight to 2^-12, and its e4m3 part exactly
+                                const __half2 x = __floats2half2_rn(p0 * c2.x, p1 * c2.z);
+                                hl[k] = e4m3x2(x);
+                                ll[k] = e5m2x2(__hsub2(x, e4m3x2_half(hl[k])));
                             }
-                            const uint32_t a = e4m3x2(x[0], x[1]), d = e4m3x2(x[2], x[3]);
-                            const float2 av = e4m3x2_value(a), dv = e4m3x2_value(d);
-                            hi[e4] = a | d << 16;
-                            lo[e4] = e5m2x2(x[0] - av.x, x[1] - av.y) | e5m2x2(x[2] - dv.x, x[3] - dv.y) << 16;
+                            hi[e4] = hl[0] | hl[1] << 16;
+                            lo[e4] = ll[0] | ll[1] << 16;
                         }
                         const int ch = 2 * part + q;
                         *reinterpret_cast<uint4*>(prow + ((ch ^ (head & 7)) << 4)) =
@@ -654,21 +688,17 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     const float both = l + __shfl_xor_sync(0xffffffffu, l, 16);
                     if (part == 0) {
-                        sh.m[item & 3][team][head] = m_ref;
+                        sh.ref[item & 3][team][head] = ref;
                         sh.l[item & 3][team][head] = both;
                     }
                 }
-                if (quarter == 0 && lane == 0) sh.sref[item & 3][team] = sref;
                 fence_proxy_async_smem();
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh.p_full[team]);
-                    mbar_arrive(&sh.empty[slot]);
-                }
+                if (lane == 0) mbar_arrive(&sh.p_full[team]);
             }
             w.next(n);
         }
+        if (ok) fix();
     } else {
         // ------------------------------------- q into TMEM, output out of TMEM
         const int quarter = warp & 3, part = lane >> 4, head = 16 * quarter + (lane & 15);
@@ -758,11 +788,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 fence_proxy_async_smem();            // the slots' next loads come after these writes
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh.q_full);
-                    mbar_arrive_cnt(&sh.empty[s0], quarter == 0 ? 2 : 1);    // five arrivals, from four warps
-                    mbar_arrive_cnt(&sh.empty[s1], quarter == 0 ? 2 : 1);
-                }
+                if (lane == 0) mbar_arrive(&sh.q_full);
             }
             const int done = item - 1, t = t_prev;
             const bool whole = whole_prev, first = done == 0;
@@ -785,26 +811,25 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
             for (int h = lane; h < heads; h += 32) {
                 // sums are in units of 2^(reference - bias)
-                const float ma = any & 1 ? sh.m[st][0][h] : -INFINITY, mb = any & 2 ? sh.m[st][1][h] : -INFINITY;
+                const float ma = any & 1 ? sh.ref[st][0][h] : -INFINITY, mb = any & 2 ? sh.ref[st][1][h] : -INFINITY;
                 const float la = any & 1 ? sh.l[st][0][h] : 0.f, lb = any & 2 ? sh.l[st][1][h] : 0.f;
                 // references only rise within an item: the larger is the accumulator's
                 const float mu = fmaxf(ma, mb);
                 const float m2 = mu == -INFINITY ? 0.f : mu - kPgBias;
                 const float l = (la == 0.f || ma == mu ? la : la * ex2_approx(ma - mu)) +
                                 (lb == 0.f || mb == mu ? lb : lb * ex2_approx(mb - mu));
-                const float so = fmaxf(any & 1 ? sh.sref[st][0] : 0.f, any & 2 ? sh.sref[st][1] : 0.f);
                 if (whole) {
                     const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
                     // a NaN sum stays one; a sum of zero leaves the sink alone
                     const float top = l == 0.f ? sink : fmaxf(m2, sink);
                     const float base = top == -INFINITY ? 0.f : top;
                     const float sum = l * ex2_approx(m2 - base) + (p.sink ? ex2_approx(sink - base) : 0.f);
-                    fin[h] = sum == 0.f ? 0.f : ex2_approx(m2 - base) * so / sum;
+                    fin[h] = sum == 0.f ? 0.f : ex2_approx(m2 - base) / sum;
                     if (quarter == 0)
                         p.lse[int64_t(t) * p.H + head0 + h] =
                             sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
                 } else {
-                    fin[h] = so;
+                    fin[h] = 1.f;
                     if (quarter == 0)
                         p.part_ml[int64_t(part_at) * p.group_heads + h] = make_float2(l == 0.f ? -INFINITY : m2, l);
                 }

@@ -52,6 +52,7 @@ constexpr float kPgLog2e = 1.4426950408889634f;
 constexpr float kPgLn2 = 0.6931471805599453f;
 constexpr int kPgTile = 64;                      // ranks per tile
 constexpr int kPgSlots = 6;
+constexpr int kPgLead = 4;
 constexpr int kPgSlotBytes = kPgTile * kD;       // 32 KB: four blocks of 64 rows x 128 bytes
 constexpr int kPgBlockBytes = kPgTile * 128;
 constexpr int kPgHeads = 64;                     // heads of a group at most
@@ -64,10 +65,10 @@ constexpr uint32_t kPgColS = 0, kPgColQ = 128, kPgColO = 256;
 // Weights are scaled so that the running reference's is 2^kPgBias; the
 // reference follows the maximum when it is passed by more than 2^kPgSlack
 // (e4m3 ends at 448 > 2^(kPgBias + kPgSlack)).
-constexpr float kPgBias = 5.f, kPgSlack = 3.f;
+constexpr float kPgBias = 4.f, kPgSlack = 4.75f;
 
 struct PgShared {
-    uint64_t full[kPgSlots], empty[kPgSlots], q_load[2];
+    uint64_t full[kPgSlots], empty[kPgSlots], q_load[4];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t q_full, q_empty, o_full, o_empty, dec[4], fixed[2], drain[2];
     uint32_t tbase;
@@ -97,7 +98,7 @@ struct PgParams {
     unsigned* status;
     int4* meta;                                  // [CTAs] end of a split token: {t, first CTA, its part, 0}
     float2* part_ml;                             // [CTAs][2][group_heads] maximum (log2) and sum
-    float* part_o;                               // [CTAs][2][group_heads][512]
+    float* part_o;                               // [CTAs][2][group_heads / 4][512][4] (head h: block h / 4, h % 4)
 };
 
 // Every lane waits, for at most about two seconds; the warp goes on only if all of them
@@ -133,13 +134,14 @@ __device__ __forceinline__ int pg_tiles(const PgParams& p, int t) {
     return n < 1 ? 1 : (n + kPgTile - 1) / kPgTile;
 }
 
-// The ring's uses are an item's q (two) and then its tiles, numbered over all
-// items; use g is in slot g % kPgSlots. A parity wait tells a phase only from the
-// one before, so whoever waits for a barrier sees each of its phases in turn:
-// `empty` counts every use (each loading warp has a part in each), `full` the
-// tiles alone (MMA and softmax keep a parity bit a slot), and q has barriers of its
-// own, q_load[item & 1] (the q of item + 2 goes no earlier than six uses on, into
-// slots that item's q has left).
+// The ring's uses are the items' q (two each) and tiles; use g is in slot g % kPgSlots. The
+// first item's q comes first, every other item's kPgLead tiles before the end of the item
+// ahead of it (PgWalk::early), so that it is loaded and split before it is needed.
+// A parity wait tells a phase only from the one before, so whoever waits for a barrier
+// sees each of its phases in turn: `empty` counts every use (each loading warp has a
+// part in each), `full` the tiles alone (the S warp keeps a parity bit a slot), and q
+// has barriers of its own, q_load[item & 3] (the uses between the q of an item and of
+// the fourth after it go round the ring).
 static_assert(kPgSlots % 2 == 0 && kPgSlots >= 6, "a slot belongs to one of the two softmax teams");
 __device__ __forceinline__ int pg_slot(int g) { return g % kPgSlots; }
 __device__ __forceinline__ uint32_t pg_parity(uint32_t bits, int slot) { return (bits >> slot) & 1u; }
@@ -239,6 +241,8 @@ struct PgWalk {
         const int n = __shfl_sync(0xffffffffu, pg_tiles(p, t), 0) - k0;
         return n < left ? n : left;
     }
+    // the tile of an item of n that the next item's q is loaded ahead of (-1: no next item)
+    __device__ __forceinline__ int early(int n) const { return left <= n ? -1 : n > kPgLead ? n - kPgLead : 0; }
     __device__ __forceinline__ void next(int n) { left -= n; ++t; k0 = 0; }
 };
 
@@ -265,12 +269,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sh.q_load[b], 2 * kPgLoadWarps);
             mbar_init(&sh.s_full[b], 2);         // MMA completion and the issuing thread
             mbar_init(&sh.s_empty[b], 4);
             mbar_init(&sh.p_full[b], 4);
             mbar_init(&sh.p_empty[b], 1);
         }
+        for (int b = 0; b < 4; ++b) mbar_init(&sh.q_load[b], 2 * kPgLoadWarps);
         mbar_init(&sh.q_full, 4);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.o_full, 2);                // MMA completion and the issuing thread
@@ -302,6 +306,25 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int page_mask = (1 << p.page_shift) - 1;
         const int box_rows = page_mask + 1 < kPgTile ? page_mask + 1 : kPgTile;
         bool bad = false;
+        int g = 0, item = 0;
+        uint32_t loads = 0;                      // parity of each slot's last tile load
+        int q_last = -1;
+        bool ok = true;
+        auto load_q = [&](int of, int t) {
+            for (int k = 0; k < 2 && ok; ++k, ++g) {
+                const int slot = pg_slot(g);
+                ok = pg_wait_warp(&sh.empty[slot], (uint32_t(g / kPgSlots) & 1u) ^ 1u, ab, p.status);
+                if (!ok) break;
+                q_last = of;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.q_load[of & 3], uint32_t(p.group_heads) * 128u);
+                    tma_load_2d(ring + slot * kPgSlotBytes + lw * kPgBlockBytes, &map_q, (4 * k + lw) * 64,
+                                t * p.H + head0, &sh.q_load[of & 3]);
+                }
+            }
+        };
+        // the first q's uses: its slots are free at the start
+        if (sh.count > 0) load_q(0, sh.t0);
         // Look-ups ahead of the loads: tile after tile over all items.
         PgWalk wa(sh);
         int na = 0, ia = 0, ba = 0, lena = 0;
@@ -352,30 +375,17 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int row = row_of(x0, page_of(x0));
         float sc = row >= 0 ? __ldg(p.scales + (row >> p.block_shift)) : -1.f;
 
-        int g = 0, item = 0;
-        uint32_t loads = 0;                      // parity of each slot's last tile load
-        int q_last = -1;
-        bool ok = true;
         for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-            const int n = w.tiles(p);
+            const int n = w.tiles(p), early = w.early(n);
 #pragma unroll 1
-            for (int i = 0; i < n + 2; ++i, ++g) {
+            for (int i = 0; i < n; ++i, ++g) {
+                if (i == early) load_q(item + 1, w.t + 1);
                 const int slot = pg_slot(g);
                 uint8_t* dst = ring + slot * kPgSlotBytes;
-                const int page1 = i < 2 ? 0 : page_of(x1);
-                Ahead x2{};
-                if (i >= 2) x2 = look();
-                ok = pg_wait_warp(&sh.empty[slot], (uint32_t(g / kPgSlots) & 1u) ^ 1u, ab, p.status);
+                const int page1 = page_of(x1);
+                const Ahead x2 = look();
+                if (ok) ok = pg_wait_warp(&sh.empty[slot], (uint32_t(g / kPgSlots) & 1u) ^ 1u, ab, p.status);
                 if (!ok) break;
-                if (i < 2) {
-                    q_last = item;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&sh.q_load[item & 1], uint32_t(p.group_heads) * 128u);
-                        tma_load_2d(dst + lw * kPgBlockBytes, &map_q, (4 * i + lw) * 64, w.t * p.H + head0,
-                                    &sh.q_load[item & 1]);
-                    }
-                    continue;
-                }
                 loads ^= 1u << slot;             // full's phase of this load has the parity before
                 const int left = x0.len - (x0.pos - 16 * (lane & 3));    // all positions: from the tile's first on
                 const bool boxes = !p.topk && __all_sync(0xffffffffu, row >= 0 && left >= kPgTile) != 0;
@@ -441,8 +451,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (sh.abort_flag) {     // the loads already issued land before the CTA exits
             for (int slot = 0; slot < kPgSlots; ++slot)
                 mbar_wait(&sh.full[slot], pg_parity(loads, slot) ^ 1u, kPgWaitNs / 8);
-            for (int q = q_last > 0 ? q_last - 1 : 0; q <= q_last; ++q)
-                mbar_wait(&sh.q_load[q & 1], uint32_t(q >> 1) & 1u, kPgWaitNs / 8);
+            for (int q = q_last > 2 ? q_last - 2 : 0; q <= q_last; ++q)
+                mbar_wait(&sh.q_load[q & 3], uint32_t(q >> 2) & 1u, kPgWaitNs / 8);
         }
         __syncwarp();
     } else if (warp >= kPgMmaWarp) {
@@ -452,22 +462,24 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         // walks the tiles, so that descriptors stay in uniform registers; one elected lane issues.
         const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
         const bool leader = elect_one();
-        int g = 0, tile = 0, item = 0;
+        int g = 2, tile = 0, item = 0;
         bool ok = true;
         if (warp == kPgMmaWarp) {
             const uint32_t id_s = idesc_f8(128, kPgTile, false, false);
             uint32_t seen = 0;
+            int q_at = 0, q_next = 0;            // the item's q uses, and the next one's
             for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-                const int n = w.tiles(p);
-                g += 2;
+                const int n = w.tiles(p), early = w.early(n);
+                q_at = q_next;
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++g, ++tile) {
+                    if (i == early) { q_next = g; g += 2; }
                     const int slot = pg_slot(g), b = tile & 1;
                     if (i == 0) {
                         ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
                         if (ok && leader) {      // q is in TMEM: its slots are free
-                            mbar_arrive(&sh.empty[pg_slot(g - 2)]);
-                            mbar_arrive(&sh.empty[pg_slot(g - 1)]);
+                            mbar_arrive(&sh.empty[pg_slot(q_at)]);
+                            mbar_arrive(&sh.empty[pg_slot(q_at + 1)]);
                         }
                     }
                     if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(tile >> 1) & 1u) ^ 1u, ab, p.status);
@@ -499,10 +511,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const uint64_t p_desc = sdesc_sw128(smem_u32(pbuf), 16, 1024);
             const uint32_t id_hi = idesc_f8(128, heads, true, false), id_lo = idesc_f8(128, heads, true, true);
             for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-                const int n = w.tiles(p);
-                g += 2;
+                const int n = w.tiles(p), early = w.early(n);
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++g, ++tile) {
+                    if (i == early) g += 2;
                     const int slot = pg_slot(g), b = tile & 1;
                     if (i == 0 && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
                     if (ok) ok = pg_wait_warp(&sh.p_full[b], uint32_t(tile >> 1) & 1u, ab, p.status);
@@ -560,7 +572,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
         const float lo_factor = part ? 0.0625f : 1.f;
         uint8_t* prow = pbuf + team * kPgPBytes + head * 128;
-        int g = 0, tile = 0, item = 0, mine = -1;        // mine: the team's last tile
+        int g = 2, tile = 0, item = 0, mine = -1;        // mine: the team's last tile
         bool ok = true;
         // rescales O for the team's last tile, if one of its warps asked for it
         auto fix = [&]() {
@@ -594,11 +606,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             if (lane == 0) mbar_arrive(&sh.fixed[team]);
         };
         for (PgWalk w(sh); w.left > 0 && ok; ++item) {
-            const int n = w.tiles(p);
-            g += 2;
+            const int n = w.tiles(p), early = w.early(n);
             float own_ref = -INFINITY, l = 0.f, f = 0.f;
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++g, ++tile) {
+                if (i == early) g += 2;
                 const int slot = pg_slot(g);
                 if ((slot & 1) != team) continue;
                 fix();
@@ -704,33 +716,37 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int quarter = warp & 3, part = lane >> 4, head = 16 * quarter + (lane & 15);
         const bool active = 16 * quarter < heads;
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
-        int g = 0, item = 0;
+        int g = 2, item = 0, q_next = 0;
         bool ok = true;
         int t_prev = 0;
         bool whole_prev = false;
-        int teams_prev = 0;
+        int teams_prev = 0, teams_next = 0;
 
         for (PgWalk w(sh);; ++item) {
             const bool more = w.left > 0;
             const int n = more ? w.tiles(p) : 0;
             if (more) {
-                const int s0 = pg_slot(g), s1 = pg_slot(g + 1);
-                g += n + 2;
-                ok = pg_wait_warp(&sh.q_load[item & 1], uint32_t(item >> 1) & 1u, ab, p.status);
+                const int s0 = pg_slot(q_next), s1 = pg_slot(q_next + 1), early = w.early(n);
+                teams_next = n > 1 ? 3 : 1 << (g & 1);   // the softmax teams that have tiles of the item
+                q_next = g + early;
+                g += early < 0 ? n : n + 2;
+                ok = pg_wait_warp(&sh.q_load[item & 3], uint32_t(item >> 2) & 1u, ab, p.status);
                 if (!ok) break;
                 uint8_t* qhalf = ring + (part ? s1 : s0) * kPgSlotBytes + head * 128;
-                auto piece = [&](int c) {            // 16 bytes of the row's half: 8 values
-                    return reinterpret_cast<uint4*>(qhalf + (c >> 3) * kPgBlockBytes + (((c & 7) ^ (head & 7)) << 4));
-                };
+                int at8[8];                      // the 16-byte pieces of a 128-byte row, swizzled
+#pragma unroll
+                for (int k = 0; k < 8; ++k) at8[k] = (k ^ (head & 7)) << 4;
                 if (active) {
                     // largest |q| of the row; each of the head's lanes has one half
                     uint32_t top = 0;
-#pragma unroll 4
-                    for (int c = 0; c < 32; ++c) {
-                        const uint4 x = *piece(c);
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                    }
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(qhalf + c * kPgBlockBytes + at8[k]);
+                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                        }
                     top = max(top >> 16, top & 0xffffu);
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     int e2 = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
@@ -742,12 +758,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                                                  : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
                     // in place: eight values become eight bytes hi and eight bytes lo
 #pragma unroll 1
-                    for (int c = 0; c < 32; c += 4) {
-                        uint4 x[4];
+                    for (int c = 0; c < 4; ++c) {
+                        uint8_t* at = qhalf + c * kPgBlockBytes;
+                        uint4 x[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = *piece(c + k);
+                        for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const uint4*>(at + at8[k]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 8; ++k) {
                             const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -757,11 +774,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 hi[e] = e4m3x2(v);
                                 lo[e] = e4m3x2(__hmul2(__hsub2(v, e4m3x2_half(hi[e])), __float2half2_rn(16.f)));
                             }
-                            x[k] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
-                                              lo[2] | lo[3] << 16);
+                            *reinterpret_cast<uint4*>(at + at8[k]) =
+                                make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
+                                           lo[2] | lo[3] << 16);
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) *piece(c + k) = x[k];
                     }
                 }
                 __syncwarp();
@@ -777,7 +793,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         uint32_t word[16];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(src + ((k ^ (head & 7)) << 4));
+                            const uint2 x = *reinterpret_cast<const uint2*>(src + at8[k]);
                             word[2 * k] = x.x;
                             word[2 * k + 1] = x.y;
                         }
@@ -794,8 +810,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const bool whole = whole_prev, first = done == 0;
             t_prev = w.t;
             whole_prev = more && w.k0 == 0 && n == pg_tiles(p, w.t);
-            const int teams = teams_prev;
-            teams_prev = n > 1 ? 3 : 1 << ((g - 1) & 1);     // (its only tile is use g - 1)
+            const int any = teams_prev;          // the softmax teams that had tiles of the item before
+            teams_prev = teams_next;
             w.next(n);
             if (done < 0) {
                 if (!more) break;                // a CTA without a tile
@@ -806,7 +822,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             if (!ok) break;
             tc_fence_after();
             const int st = done & 3;
-            const int any = teams;               // the softmax teams that had tiles of it
             float* fin = sh.fin[quarter];
             const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
             for (int h = lane; h < heads; h += 32) {
@@ -829,7 +844,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         p.lse[int64_t(t) * p.H + head0 + h] =
                             sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
                 } else {
-                    fin[h] = 1.f;
                     if (quarter == 0)
                         p.part_ml[int64_t(part_at) * p.group_heads + h] = make_float2(l == 0.f ? -INFINITY : m2, l);
                 }
@@ -851,21 +865,29 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tmem_wait_ld();
                     const int d = 128 * db + 32 * quarter + lane;
                     if (whole) {
-                        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) +
-                                             (int64_t(t) * p.H + head0 + h) * kD + d;
+                        // two lanes swap a value of a head pair, so that each stores two columns of one head
+                        const int odd = lane & 1;
+                        uint32_t* dst = reinterpret_cast<uint32_t*>(p.o) +
+                                        ((int64_t(t) * p.H + head0 + h + odd) * kD + (d & ~1)) / 2;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                dst[128 * k + e * kD] =
-                                    __float2bfloat16_rn(__uint_as_float(v[k][e]) * fh[e]);
+                            for (int e = 0; e < 16; e += 2) {
+                                const float a = __uint_as_float(v[k][e]) * fh[e];
+                                const float c = __uint_as_float(v[k][e + 1]) * fh[e + 1];
+                                const float r = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+                                dst[64 * k + e * (kD / 2)] = odd ? pack_bf16x2(r, c) : pack_bf16x2(a, r);
+                            }
                     } else {
-                        float* dst = p.part_o + (int64_t(part_at) * p.group_heads + h) * kD + d;
+                        float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                                      (int64_t(part_at) * (p.group_heads / 4) + h / 4) * kD + d;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                dst[128 * k + e * kD] = __uint_as_float(v[k][e]) * fh[e];
+                            for (int e = 0; e < 4; ++e)
+                                dst[128 * k + e * kD] = make_float4(
+                                    __uint_as_float(v[k][4 * e]), __uint_as_float(v[k][4 * e + 1]),
+                                    __uint_as_float(v[k][4 * e + 2]), __uint_as_float(v[k][4 * e + 3]));
                     }
                 }
             }
@@ -884,71 +906,86 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 }
 
 // Joins the parts of a token that several CTAs shared, in their order. Block
-// (c, y): the token that ends in CTA c, heads 2y and 2y + 1 of its group, 128
-// threads each (four columns a thread).
+// (c, y): the token that ends in CTA c, heads 4y .. 4y + 3 of its group; a
+// thread has two columns of all four.
 __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
-    __shared__ float wgt[2][kPgMaxCtas];
-    __shared__ float red[8];
+    __shared__ float4 wgt[kPgMaxCtas];
+    __shared__ float red[2][8];
     const int4 end = p.meta[blockIdx.x];
     if (end.x < 0) return;
     const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
-    const int head0 = group * p.group_heads;
-    const int side = threadIdx.x >> 7, lane = threadIdx.x & 127;
-    const int h = 2 * int(blockIdx.y) + side;            // heads come in sixteens: both or neither
-    if (h >= p.group_heads || head0 + h >= p.H) return;
+    const int h4 = blockIdx.y, head0 = group * p.group_heads + 4 * h4;
+    if (head0 >= p.H) return;                            // (heads come in sixteens)
     const int n = cta - end.y + 1;                       // parts, at most the CTAs of a group
     auto part_of = [&](int i) {
         return (int64_t(end.y + i) * p.groups + group) * 2 + (i == 0 ? end.z : 0);
     };
-    const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
-    float2 ml[2];
+    // weights: 64 threads a head
+    const int k = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const float sink = p.sink ? __ldg(p.sink + head0 + k) * kPgLog2e : -INFINITY;
+    float2 ml[3];
+    static_assert(kPgMaxCtas <= 3 * 64, "parts of a token");
     float top = sink;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int i = lane + 128 * k;
-        ml[k] = i < n ? p.part_ml[part_of(i) * p.group_heads + h] : make_float2(-INFINITY, 0.f);
-        if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
+    for (int j = 0; j < 3; ++j) {
+        const int i = lane + 64 * j;
+        ml[j] = i < n ? p.part_ml[part_of(i) * p.group_heads + 4 * h4 + k] : make_float2(-INFINITY, 0.f);
+        if (ml[j].y != 0.f) top = fmaxf(top, ml[j].x);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = top;
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, red[4 * side + k]);
+    top = fmaxf(red[0][2 * k], red[0][2 * k + 1]);
     const float base = top == -INFINITY ? 0.f : top;
-    __syncthreads();
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int i = lane + 128 * k;
-        const float w = ml[k].y == 0.f ? 0.f : ex2_approx(ml[k].x - base);
-        if (i < n) wgt[side][i] = w;
-        sum += w * ml[k].y;
+    for (int j = 0; j < 3; ++j) {
+        const int i = lane + 64 * j;
+        const float w = ml[j].y == 0.f ? 0.f : ex2_approx(ml[j].x - base);
+        if (i < n) reinterpret_cast<float*>(wgt + i)[k] = w;
+        sum += w * ml[j].y;
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = sum;
     __syncthreads();
-    sum = p.sink ? ex2_approx(sink - base) : 0.f;
+    float inv[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum += red[4 * side + k];
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t step = int64_t(p.groups) * 2 * p.group_heads * (kD / 4);
-    const float4* src = reinterpret_cast<const float4*>(p.part_o) + lane;
-    const float4* rest = src + (part_of(1) * p.group_heads + h) * (kD / 4);
-    auto add = [&](const float4& v, float w) {
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    for (int j = 0; j < 4; ++j) {
+        const float sj = p.sink ? __ldg(p.sink + head0 + j) * kPgLog2e : -INFINITY;
+        const float tj = fmaxf(red[0][2 * j], red[0][2 * j + 1]), bj = tj == -INFINITY ? 0.f : tj;
+        const float all = red[1][2 * j] + red[1][2 * j + 1] + (p.sink ? ex2_approx(sj - bj) : 0.f);
+        inv[j] = all == 0.f ? 0.f : 1.f / all;
+        if (threadIdx.x == j)
+            p.lse[int64_t(end.x) * p.H + head0 + j] = all == 0.f ? -INFINITY : bj * kPgLn2 + logf(all);
+    }
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const int64_t size = int64_t(p.group_heads / 4) * kD;        // float4s of a part
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + h4 * kD + threadIdx.x;
+    auto add = [&](const float4* at, int i) {
+        const float4 w = wgt[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 v = __ldcg(at + 256 * j);
+            acc[j].x = fmaf(w.x, v.x, acc[j].x);
+            acc[j].y = fmaf(w.y, v.y, acc[j].y);
+            acc[j].z = fmaf(w.z, v.z, acc[j].z);
+            acc[j].w = fmaf(w.w, v.w, acc[j].w);
+        }
     };
-    add(__ldcg(src + (part_of(0) * p.group_heads + h) * (kD / 4)), wgt[side][0]);
-#pragma unroll 8
-    for (int i = 1; i < n; ++i) add(__ldcg(rest + (i - 1) * step), wgt[side][i]);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    reinterpret_cast<uint2*>(p.o + (int64_t(end.x) * p.H + head0 + h) * kD)[lane] =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0) p.lse[int64_t(end.x) * p.H + head0 + h] = sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
+    add(src + part_of(0) * size, 0);
+    const float4* rest = src + part_of(1) * size;
+#pragma unroll 4
+    for (int i = 1; i < n; ++i) add(rest + (i - 1) * 2 * p.groups * size, i);
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (int64_t(end.x) * p.H + head0) * kD + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        dst[256 * j] = __float2bfloat16_rn(acc[j].x * inv[0]);
+        dst[256 * j + kD] = __float2bfloat16_rn(acc[j].y * inv[1]);
+        dst[256 * j + 2 * kD] = __float2bfloat16_rn(acc[j].z * inv[2]);
+        dst[256 * j + 3 * kD] = __float2bfloat16_rn(acc[j].w * inv[3]);
+    }
 }
 
 namespace {
@@ -1005,7 +1042,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     fwd_paged_kernel<<<ctas * plan.groups, kPgThreads, kPgSmem, s>>>(mq, mb, mr, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    combine_paged_kernel<<<dim3(ctas * plan.groups, plan.group_heads / 2), 256, 0, s>>>(p);
+    combine_paged_kernel<<<dim3(ctas * plan.groups, plan.group_heads / 4), 256, 0, s>>>(p);
     note_launch(2);
     return cudaGetLastError();
 }

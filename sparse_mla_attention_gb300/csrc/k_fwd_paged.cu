@@ -30,10 +30,9 @@
 // (unnormalised O, maximum, sum), and combine_paged_kernel joins the parts in order.
 // Warps: 0-3 and 4-7 softmax, on alternate tiles (a thread has one head and half of
 // the tile's ranks: the two lanes of a head swap their halves of S, which adds hi and
-// lo), 8-11 q conversion and output, 12 S products, 13 O products, 14-17 loads (TMA boxes where a tile's rows lie in
-// whole pages, four-row gathers otherwise). A masked rank loads a valid row of its
-// tile instead of its own (weight 0, and no byte of a row that nothing
-// names is ever read); a tile without a valid rank is filled with zeros.
+// lo), 8-11 q conversion and output, 12 S products, 13 O products, 14-17 loads (TMA boxes where a tile's rows lie in whole
+// pages, copies row by row otherwise). A masked rank's row is zeros with weight 0: no
+// byte of a row that nothing names is ever read.
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the
 // CTA's loops, waits (bounded) for its own copies and MMAs and frees TMEM.
 #include <cuda_fp8.h>
@@ -90,7 +89,7 @@ static_assert(kPgSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 
 struct PgParams {
     const int32_t* table; const int32_t* seq; const int32_t* lens; const int32_t* topk;
-    const float* scales; const float* sink;
+    const uint8_t* pages; const float* scales; const float* sink;
     uint16_t* o; float* lse;
     int T, H, K, B, max_pages, num_pages, page_shift, block_shift;
     int groups, group_heads;                     // head groups, heads of a full one
@@ -250,7 +249,7 @@ struct PgWalk {
 
 __global__ void __launch_bounds__(kPgThreads, 1)
 fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_box,
-                 const __grid_constant__ CUtensorMap map_row, const PgParams p) {
+                 const PgParams p) {
     extern __shared__ uint8_t smem_raw[];
     PgShared& sh = *reinterpret_cast<PgShared*>(smem_raw);
     uint8_t* ring = reinterpret_cast<uint8_t*>(
@@ -299,7 +298,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         // Every warp has a part in each ring use: of an item's q (two uses of four 64-column
         // boxes) one box; of a tile whose rows lie in whole runs of 16 (all positions,
         // none masked) one column block of all 64 ranks, as TMA boxes; of other tiles 16 ranks,
-        // as four-row gathers (issued lane by lane, some 75 cycles each: hence four warps).
+        // copied 16 bytes a lane (a warp issues a four-row TMA gather per 100 cycles, 16 a tile;
+        // the same bytes as copies take 16 instructions).
         // Picks: positions are loaded two tiles ahead, pages and scales one tile ahead.
         const int lw = warp - kPgLoadWarp;
         const int64_t limit = int64_t(p.max_pages) << p.page_shift;
@@ -310,10 +310,29 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         uint32_t loads = 0;                      // parity of each slot's last tile load
         int q_last = -1;
         bool ok = true;
+        // Gathered tiles whose copies are in flight, oldest first: the copies are this warp's own
+        // (cp.async), so it is the one to see them land, make them visible to the tensor
+        // core and arrive. It never sleeps on a slot before that.
+        int flying = 0, fly0 = 0, fly1 = 0;
+        auto land_all = [&]() {
+            if (flying == 0) return;
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.full[fly0]);
+                if (flying > 1) mbar_arrive(&sh.full[fly1]);
+            }
+            flying = 0;
+        };
+        auto wait_slot = [&](int slot, uint32_t parity) {
+            if (flying && !__all_sync(0xffffffffu, mbar_try_test(&sh.empty[slot], parity))) land_all();
+            return pg_wait_warp(&sh.empty[slot], parity, ab, p.status);
+        };
         auto load_q = [&](int of, int t) {
             for (int k = 0; k < 2 && ok; ++k, ++g) {
                 const int slot = pg_slot(g);
-                ok = pg_wait_warp(&sh.empty[slot], (uint32_t(g / kPgSlots) & 1u) ^ 1u, ab, p.status);
+                ok = wait_slot(slot, (uint32_t(g / kPgSlots) & 1u) ^ 1u);
                 if (!ok) break;
                 q_last = of;
                 if (lane == 0) {
@@ -384,7 +403,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 uint8_t* dst = ring + slot * kPgSlotBytes;
                 const int page1 = page_of(x1);
                 const Ahead x2 = look();
-                if (ok) ok = pg_wait_warp(&sh.empty[slot], (uint32_t(g / kPgSlots) & 1u) ^ 1u, ab, p.status);
+                if (ok) ok = wait_slot(slot, (uint32_t(g / kPgSlots) & 1u) ^ 1u);
                 if (!ok) break;
                 loads ^= 1u << slot;             // full's phase of this load has the parity before
                 const int left = x0.len - (x0.pos - 16 * (lane & 3));    // all positions: from the tile's first on
@@ -408,29 +427,18 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         mine = v ? mine + (lane & 15) : -1;
                         sc16 = v ? sc16 : -1.f;
                     }
-                    // a masked rank loads a valid row of the warp's ranks instead; without one, zeros
-                    const unsigned some = __ballot_sync(0xffffffffu, mine >= 0);
-                    const int stand = __shfl_sync(0xffffffffu, mine, some ? __ffs(some) - 1 : 0);
-                    if (mine < 0) mine = stand;
-                    uint8_t* at = dst + 16 * lw * 128;
-                    if (some) {
-                        const int quad = (lane >> 2) & 3, cb = lane & 3;
-                        const int y0 = __shfl_sync(0xffffffffu, mine, 4 * quad);
-                        const int y1 = __shfl_sync(0xffffffffu, mine, 4 * quad + 1);
-                        const int y2 = __shfl_sync(0xffffffffu, mine, 4 * quad + 2);
-                        const int y3 = __shfl_sync(0xffffffffu, mine, 4 * quad + 3);
-                        if (lane == 0) mbar_expect_tx(&sh.full[slot], kPgBlockBytes);
-                        __syncwarp();
-                        if (lane < 16)
-                            tma_gather4(at + cb * kPgBlockBytes + quad * 512, &map_row, cb * 128, y0, y1, y2, y3,
-                                        &sh.full[slot]);
-                    } else {
+                    // four rows of 128 bytes an instruction; a masked rank's row is zeros, unread
+                    uint8_t* at = dst + (16 * lw + (lane >> 3)) * 128;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)     // 16 rows of 128 bytes in each of four blocks
-                            *reinterpret_cast<uint4*>(at + (k >> 2) * kPgBlockBytes + (k & 3) * 512 + 16 * lane) =
-                                make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = __shfl_sync(0xffffffffu, mine, 4 * q + (lane >> 3));
+                        const uint8_t* src = p.pages + int64_t(r < 0 ? 0 : r) * kD + (lane & 7) * 16;
+                        uint8_t* to = at + q * 512 + (((lane & 7) ^ ((4 * q + (lane >> 3)) & 7)) << 4);
+#pragma unroll
+                        for (int cb = 0; cb < 4; ++cb)
+                            cp_async16_zfill(to + cb * kPgBlockBytes, src + cb * 128, r < 0 ? 0u : 16u);
                     }
+                    cp_async_commit();
                 }
                 if (lane < 16)
                     sh.scale[slot][16 * lw + lane] = make_float2(fmaxf(sc16, 0.f), sc16 >= 0.f ? 0.f : -INFINITY);
@@ -438,7 +446,20 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sc16, 0.f)));
                 if (lane == 0) sh.smax[slot][lw] = __uint_as_float(top);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[slot]);
+                if (boxes) {
+                    if (lane == 0) mbar_arrive(&sh.full[slot]);
+                } else {
+                    if (flying == 2) {           // the oldest lands first
+                        cp_async_wait<2>();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.full[fly0]);
+                        fly0 = fly1;
+                        flying = 1;
+                    }
+                    if (flying == 0) fly0 = slot; else fly1 = slot;
+                    ++flying;
+                }
                 // the next tile's rows and scales
                 row = row_of(x1, page1);
                 sc = row >= 0 ? __ldg(p.scales + (row >> p.block_shift)) : -1.f;
@@ -447,6 +468,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             w.next(n);
         }
+        land_all();
         if (bad) flag_status(p.status, SMLA_ERR_INDEX);
         if (sh.abort_flag) {     // the loads already issued land before the CTA exits
             for (int slot = 0; slot < kPgSlots; ++slot)
@@ -787,7 +809,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tc_fence_after();
                     const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128 + 8 * part;
                     const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128 + 8 * part;
-#pragma unroll 2
+#pragma unroll 4
                     for (int c = 0; c < 8; ++c) {    // 64 values of the row's part: a box
                         const uint8_t* src = (c < 4 ? q0 : q1) + (c & 3) * kPgBlockBytes;
                         uint32_t word[16];
@@ -849,47 +871,48 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
             }
             __syncwarp();
-#pragma unroll 1
-            for (int h = 0; h < heads; h += 16) {
-                float fh[16];
+            // 16 heads of a column block at a time, the next ones read while these are stored
+            uint32_t v[2][16];
+            const uint32_t src = trow + kPgColO;
+            tmem_ld16(src, v[0]);
+            tmem_wait_ld();
+            auto store = [&](const uint32_t (&x)[16], int k) {
+                const int h = (k >> 2) * 16, d = 128 * (k & 3) + 32 * quarter + lane;
+                if (whole) {
+                    // two lanes swap a value of a head pair, so that each stores two columns of one head
+                    const int odd = lane & 1;
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o) +
+                                    ((int64_t(t) * p.H + head0 + h + odd) * kD + (d & ~1)) / 2;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 x = *reinterpret_cast<const float4*>(fin + h + 4 * e);
-                    fh[4 * e] = x.x; fh[4 * e + 1] = x.y; fh[4 * e + 2] = x.z; fh[4 * e + 3] = x.w;
-                }
-#pragma unroll 1
-                for (int db = 0; db < 4; db += 2) {
-                    uint32_t v[2][16];
-                    tmem_ld16(trow + kPgColO + 64 * db + h, v[0]);
-                    tmem_ld16(trow + kPgColO + 64 * (db + 1) + h, v[1]);
-                    tmem_wait_ld();
-                    const int d = 128 * db + 32 * quarter + lane;
-                    if (whole) {
-                        // two lanes swap a value of a head pair, so that each stores two columns of one head
-                        const int odd = lane & 1;
-                        uint32_t* dst = reinterpret_cast<uint32_t*>(p.o) +
-                                        ((int64_t(t) * p.H + head0 + h + odd) * kD + (d & ~1)) / 2;
+                    for (int e4 = 0; e4 < 4; ++e4) {
+                        const float4 f4 = *reinterpret_cast<const float4*>(fin + h + 4 * e4);
+                        const float fe[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const float a = __uint_as_float(v[k][e]) * fh[e];
-                                const float c = __uint_as_float(v[k][e + 1]) * fh[e + 1];
-                                const float r = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-                                dst[64 * k + e * (kD / 2)] = odd ? pack_bf16x2(r, c) : pack_bf16x2(a, r);
-                            }
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o) +
-                                      (int64_t(part_at) * (p.group_heads / 4) + h / 4) * kD + d;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                dst[128 * k + e * kD] = make_float4(
-                                    __uint_as_float(v[k][4 * e]), __uint_as_float(v[k][4 * e + 1]),
-                                    __uint_as_float(v[k][4 * e + 2]), __uint_as_float(v[k][4 * e + 3]));
+                        for (int e = 0; e < 4; e += 2) {
+                            const float a = __uint_as_float(x[4 * e4 + e]) * fe[e];
+                            const float c = __uint_as_float(x[4 * e4 + e + 1]) * fe[e + 1];
+                            const float r = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+                            dst[(4 * e4 + e) * (kD / 2)] = odd ? pack_bf16x2(r, c) : pack_bf16x2(a, r);
+                        }
                     }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                                  (int64_t(part_at) * (p.group_heads / 4) + h / 4) * kD + d;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e * kD] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]),
+                                                  __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]));
                 }
+            };
+            const int chunks = heads / 4;
+#pragma unroll 1
+            for (int k = 0; k < chunks; k += 2) {
+                tmem_ld16(src + 64 * ((k + 1) & 3) + ((k + 1) >> 2) * 16, v[1]);
+                store(v[0], k);
+                tmem_wait_ld();
+                if (k + 2 < chunks) tmem_ld16(src + 64 * ((k + 2) & 3) + ((k + 2) >> 2) * 16, v[0]);
+                store(v[1], k + 1);
+                tmem_wait_ld();
             }
             tc_fence_before();
             __syncwarp();
@@ -1023,13 +1046,13 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     const CacheView& c = a.cache;
     const uint64_t rows = uint64_t(c.num_pages) << c.page_shift;
     const uint32_t box = (1 << c.page_shift) < kPgTile ? uint32_t(1) << c.page_shift : uint32_t(kPgTile);
-    CUtensorMap mq, mb, mr;
+    CUtensorMap mq, mb;
     if (!make_tmap_bf16_2d(&mq, a.q, uint64_t(a.T) * a.H, kD, kD, plan.group_heads, 64, true) ||
-        !make_tmap_u8_rows(&mb, c.pages, rows, box) || !make_tmap_u8_rows(&mr, c.pages, rows, 1))
+        !make_tmap_u8_rows(&mb, c.pages, rows, box))
         return cudaErrorInvalidValue;
     PgParams p{};
     p.table = a.table; p.seq = a.seq; p.lens = a.lens; p.topk = a.topk;
-    p.scales = c.scales; p.sink = a.sink; p.o = a.o; p.lse = a.lse;
+    p.pages = c.pages; p.scales = c.scales; p.sink = a.sink; p.o = a.o; p.lse = a.lse;
     p.T = a.T; p.H = a.H; p.K = a.K; p.B = a.B; p.max_pages = a.max_pages;
     p.num_pages = c.num_pages; p.page_shift = c.page_shift; p.block_shift = c.block_shift;
     p.groups = plan.groups; p.group_heads = plan.group_heads;
@@ -1039,7 +1062,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     p.part_o = reinterpret_cast<float*>(a.scratch + plan.o);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int ctas = (sms < kPgMaxCtas ? sms : kPgMaxCtas) / plan.groups;
-    fwd_paged_kernel<<<ctas * plan.groups, kPgThreads, kPgSmem, s>>>(mq, mb, mr, p);
+    fwd_paged_kernel<<<ctas * plan.groups, kPgThreads, kPgSmem, s>>>(mq, mb, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     combine_paged_kernel<<<dim3(ctas * plan.groups, plan.group_heads / 4), 256, 0, s>>>(p);

@@ -45,7 +45,7 @@ inline bool make_tmap_bf16_2d(CUtensorMap* m, const void* base, uint64_t rows, u
 }
 
 // Row-major 2-D byte tensor [rows, 512], box of box_rows x 128 bytes, 128-byte
-// swizzle (box_rows = 1: also the map of a four-row gather).
+// swizzle.
 inline bool make_tmap_u8_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
     auto fn = encode_tiled_fn();
     if (!fn) return false;

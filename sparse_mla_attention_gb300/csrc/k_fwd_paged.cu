@@ -71,6 +71,7 @@ struct PgShared {
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t q_full, q_empty, o_full, o_empty, dec[4], fixed[2], drain[2];
     uint32_t tbase;
+    unsigned status;                             // this CTA's status bits
     volatile int abort_flag;
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
     int sum[kPgThreads / 32];
@@ -94,7 +95,8 @@ struct PgParams {
     int T, H, K, B, max_pages, num_pages, page_shift, block_shift;
     int groups, group_heads;                     // head groups, heads of a full one
     float scale;
-    unsigned* status;
+    unsigned* status;                            // the call's status word
+    unsigned* cta_status;                        // [CTAs]
     int4* meta;                                  // [CTAs] end of a split token: {t, first CTA, its part, 0}
     float2* part_ml;                             // [CTAs][2][group_heads] maximum (log2) and sum
     float* part_o;                               // [CTAs][2][group_heads / 4][512][4] (head h: block h / 4, h % 4)
@@ -190,14 +192,16 @@ __device__ void pg_locate(const PgParams& p, PgShared& sh, unsigned c, unsigned 
         }
         if (lane == 31) sh.sum[warp] = x;
         __syncthreads();
-        int before = 0, all = 0;
-#pragma unroll 1
-        for (int w = 0; w < kPgThreads / 32; ++w) {
-            if (w < warp) before += sh.sum[w];
-            all += sh.sum[w];
+        static_assert(kPgThreads <= 1024, "a lane for each warp's sum");
+        int y = lane < kPgThreads / 32 ? sh.sum[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
         }
-        total = unsigned(all);
-        at = unsigned(before + x - mine);
+        total = unsigned(__shfl_sync(0xffffffffu, y, 31));
+        const int before = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
+        at = unsigned((warp ? before : 0) + x - mine);
     }
     const PgDeal deal(total, ctas);
     const unsigned a = deal.first(c), b = deal.first(c + 1);
@@ -284,9 +288,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
         sh.abort_flag = 0;
+        sh.status = 0;
         fence_mbar_init();
     }
     if (warp == kPgMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
+    grid_dep_wait();                             // what ran before is complete: nothing global was touched yet
+    grid_dep_launch();
     pg_locate(p, sh, unsigned(cta), unsigned(ctas));
     tc_fence_before();
     __syncthreads();
@@ -327,7 +334,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         };
         auto wait_slot = [&](int slot, uint32_t parity) {
             if (flying && !__all_sync(0xffffffffu, mbar_try_test(&sh.empty[slot], parity))) land_all();
-            return pg_wait_warp(&sh.empty[slot], parity, ab, p.status);
+            return pg_wait_warp(&sh.empty[slot], parity, ab, &sh.status);
         };
         auto load_q = [&](int of, int t) {
             for (int k = 0; k < 2 && ok; ++k, ++g) {
@@ -469,7 +476,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             w.next(n);
         }
         land_all();
-        if (bad) flag_status(p.status, SMLA_ERR_INDEX);
+        if (bad) flag_status(&sh.status, SMLA_ERR_INDEX);
         if (sh.abort_flag) {     // the loads already issued land before the CTA exits
             for (int slot = 0; slot < kPgSlots; ++slot)
                 mbar_wait(&sh.full[slot], pg_parity(loads, slot) ^ 1u, kPgWaitNs / 8);
@@ -498,14 +505,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (i == early) { q_next = g; g += 2; }
                     const int slot = pg_slot(g), b = tile & 1;
                     if (i == 0) {
-                        ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, p.status);
+                        ok = pg_wait_warp(&sh.q_full, uint32_t(item) & 1u, ab, &sh.status);
                         if (ok && leader) {      // q is in TMEM: its slots are free
                             mbar_arrive(&sh.empty[pg_slot(q_at)]);
                             mbar_arrive(&sh.empty[pg_slot(q_at + 1)]);
                         }
                     }
-                    if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(tile >> 1) & 1u) ^ 1u, ab, p.status);
-                    if (ok) ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, p.status);
+                    if (ok) ok = pg_wait_warp(&sh.s_empty[b], (uint32_t(tile >> 1) & 1u) ^ 1u, ab, &sh.status);
+                    if (ok) ok = pg_wait_warp(&sh.full[slot], pg_parity(seen, slot), ab, &sh.status);
                     if (!ok) break;
                     seen ^= 1u << slot;
                     tc_fence_after();
@@ -538,12 +545,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 for (int i = 0; i < n; ++i, ++g, ++tile) {
                     if (i == early) g += 2;
                     const int slot = pg_slot(g), b = tile & 1;
-                    if (i == 0 && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, p.status);
-                    if (ok) ok = pg_wait_warp(&sh.p_full[b], uint32_t(tile >> 1) & 1u, ab, p.status);
+                    if (i == 0 && item > 0) ok = pg_wait_warp(&sh.o_empty, uint32_t(item - 1) & 1u, ab, &sh.status);
+                    if (ok) ok = pg_wait_warp(&sh.p_full[b], uint32_t(tile >> 1) & 1u, ab, &sh.status);
                     if (!ok) break;
                     const uint4 need = *reinterpret_cast<const uint4*>(sh.need[b][(tile >> 1) & 1]);
                     if (need.x | need.y | need.z | need.w) {
-                        ok = pg_wait_warp(&sh.fixed[b], uint32_t(b ? fixes1 : fixes0) & 1u, ab, p.status);
+                        ok = pg_wait_warp(&sh.fixed[b], uint32_t(b ? fixes1 : fixes0) & 1u, ab, &sh.status);
                         if (!ok) break;
                         if (b) ++fixes1; else ++fixes0;
                     }
@@ -600,13 +607,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         auto fix = [&]() {
             if (mine < 0) return;
             const int c = (mine >> 1) & 1;
-            ok = pg_wait_warp(&sh.p_full[team], uint32_t(c), ab, p.status);
+            ok = pg_wait_warp(&sh.p_full[team], uint32_t(c), ab, &sh.status);
             if (!ok) return;
             const uint4 need = *reinterpret_cast<const uint4*>(sh.need[team][c]);
             if ((need.x | need.y | need.z | need.w) == 0) return;
             // the O products before that tile's are complete (the one before last is, since the
             // weights could be written: so the parity means the last one's phase)
-            ok = pg_wait_warp(&sh.p_empty[team ^ 1], uint32_t((mine - 1) >> 1) & 1u, ab, p.status);
+            ok = pg_wait_warp(&sh.p_empty[team ^ 1], uint32_t((mine - 1) >> 1) & 1u, ab, &sh.status);
             if (!ok) return;
             tc_fence_after();
             // a warp's TMEM lanes are columns of D, not heads: every warp rescales all heads
@@ -639,7 +646,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (!ok) break;
                 mine = tile;
                 const uint32_t use = uint32_t(tile >> 1) & 1u;      // parity of the team's count of tiles
-                ok = pg_wait_warp(&sh.s_full[team], use, ab, p.status);
+                ok = pg_wait_warp(&sh.s_full[team], use, ab, &sh.status);
                 if (!ok) break;
                 tc_fence_after();
                 if (i < 2) f = sh.qfac[item & 3][head] * lo_factor;
@@ -674,7 +681,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 const float4 sm = *reinterpret_cast<const float4*>(sh.smax[slot]);
                 const float top = mx + __log2f(fmaxf(fmaxf(fmaxf(sm.x, sm.y), fmaxf(sm.z, sm.w)), 0x1p-100f));
                 // the reference after the tile before this one
-                if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, p.status);
+                if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, &sh.status);
                 if (!ok) break;
                 const float old = i == 0 ? top : sh.st_ref[head];
                 const bool grow = active && top > old + kPgSlack;
@@ -690,7 +697,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 l = own_ref != ref && own_ref != -INFINITY ? l * ex2_approx(own_ref - ref) : l;
                 own_ref = ref;
                 // the team's weights before these are used up
-                ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, p.status);
+                ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, &sh.status);
                 if (!ok) break;
                 if (active) {
                     const float off = kPgBias - (ref == -INFINITY ? 0.f : ref);
@@ -752,7 +759,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 teams_next = n > 1 ? 3 : 1 << (g & 1);   // the softmax teams that have tiles of the item
                 q_next = g + early;
                 g += early < 0 ? n : n + 2;
-                ok = pg_wait_warp(&sh.q_load[item & 3], uint32_t(item >> 2) & 1u, ab, p.status);
+                ok = pg_wait_warp(&sh.q_load[item & 3], uint32_t(item >> 2) & 1u, ab, &sh.status);
                 if (!ok) break;
                 uint8_t* qhalf = ring + (part ? s1 : s0) * kPgSlotBytes + head * 128;
                 int at8[8];                      // the 16-byte pieces of a 128-byte row, swizzled
@@ -780,13 +787,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                                                  : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
                     // in place: eight values become eight bytes hi and eight bytes lo
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint8_t* at = qhalf + c * kPgBlockBytes;
-                        uint4 x[8];
+                    for (int c = 0; c < 32; c += 2) {
+                        uint8_t* at = qhalf + (c >> 3) * kPgBlockBytes;
+                        uint4* at0 = reinterpret_cast<uint4*>(at + (((c & 7) ^ (head & 7)) << 4));
+                        uint4* at1 = reinterpret_cast<uint4*>(at + ((((c & 7) + 1) ^ (head & 7)) << 4));
+                        uint4 x[2] = {*at0, *at1};
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const uint4*>(at + at8[k]);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < 2; ++k) {
                             const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -796,20 +803,21 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 hi[e] = e4m3x2(v);
                                 lo[e] = e4m3x2(__hmul2(__hsub2(v, e4m3x2_half(hi[e])), __float2half2_rn(16.f)));
                             }
-                            *reinterpret_cast<uint4*>(at + at8[k]) =
-                                make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
-                                           lo[2] | lo[3] << 16);
+                            x[k] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
+                                              lo[2] | lo[3] << 16);
                         }
+                        *at0 = x[0];
+                        *at1 = x[1];
                     }
                 }
                 __syncwarp();
-                if (item > 0) ok = pg_wait_warp(&sh.q_empty, uint32_t(item - 1) & 1u, ab, p.status);
+                if (item > 0) ok = pg_wait_warp(&sh.q_empty, uint32_t(item - 1) & 1u, ab, &sh.status);
                 if (!ok) break;
                 if (active) {
                     tc_fence_after();
                     const uint8_t* q0 = ring + s0 * kPgSlotBytes + head * 128 + 8 * part;
                     const uint8_t* q1 = ring + s1 * kPgSlotBytes + head * 128 + 8 * part;
-#pragma unroll 4
+#pragma unroll 2
                     for (int c = 0; c < 8; ++c) {    // 64 values of the row's part: a box
                         const uint8_t* src = (c < 4 ? q0 : q1) + (c & 3) * kPgBlockBytes;
                         uint32_t word[16];
@@ -840,7 +848,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 continue;
             }
             // the output of the item before, once the next one's q is in place
-            ok = pg_wait_warp(&sh.o_full, uint32_t(done) & 1u, ab, p.status);
+            ok = pg_wait_warp(&sh.o_full, uint32_t(done) & 1u, ab, &sh.status);
             if (!ok) break;
             tc_fence_after();
             const int st = done & 3;
@@ -922,6 +930,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) p.cta_status[blockIdx.x] = sh.status;
     if (warp == kPgMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
@@ -930,11 +939,19 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
 // Joins the parts of a token that several CTAs shared, in their order. Block
 // (c, y): the token that ends in CTA c, heads 4y .. 4y + 3 of its group; a
-// thread has two columns of all four.
+// thread has two columns of all four. Block (0, 0) also joins the CTAs' status bits.
 __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
     __shared__ float4 wgt[kPgMaxCtas];
     __shared__ float red[2][8];
-    const int4 end = p.meta[blockIdx.x];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int4 end = __ldcg(p.meta + blockIdx.x);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+        unsigned bits = 0;
+        for (int c = threadIdx.x; c < int(gridDim.x); c += 32) bits |= __ldcg(p.cta_status + c);
+        bits = __reduce_or_sync(0xffffffffu, bits);
+        if (threadIdx.x == 0) *p.status = bits;
+    }
     if (end.x < 0) return;
     const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
     const int h4 = blockIdx.y, head0 = group * p.group_heads + 4 * h4;
@@ -952,7 +969,7 @@ __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int i = lane + 64 * j;
-        ml[j] = i < n ? p.part_ml[part_of(i) * p.group_heads + 4 * h4 + k] : make_float2(-INFINITY, 0.f);
+        ml[j] = i < n ? __ldcg(p.part_ml + part_of(i) * p.group_heads + 4 * h4 + k) : make_float2(-INFINITY, 0.f);
         if (ml[j].y != 0.f) top = fmaxf(top, ml[j].x);
     }
 #pragma unroll
@@ -1013,7 +1030,7 @@ __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
 
 namespace {
 
-struct PgPlan { int groups, group_heads; size_t meta, ml, o, bytes; };
+struct PgPlan { int groups, group_heads; size_t status, meta, ml, o, bytes; };
 
 PgPlan plan_paged(int H) {
     PgPlan x{};
@@ -1021,6 +1038,7 @@ PgPlan plan_paged(int H) {
     x.group_heads = (H / 16 + x.groups - 1) / x.groups * 16;
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes, 256); return o; };
+    x.status = take(size_t(kPgMaxCtas) * 4);
     x.meta = take(size_t(kPgMaxCtas) * sizeof(int4));
     x.ml = take(size_t(kPgMaxCtas) * 2 * x.group_heads * sizeof(float2));
     x.o = take(size_t(kPgMaxCtas) * 2 * x.group_heads * kD * 4);
@@ -1057,15 +1075,31 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     p.num_pages = c.num_pages; p.page_shift = c.page_shift; p.block_shift = c.block_shift;
     p.groups = plan.groups; p.group_heads = plan.group_heads;
     p.scale = a.scale; p.status = a.status;
+    p.cta_status = reinterpret_cast<unsigned*>(a.scratch + plan.status);
     p.meta = reinterpret_cast<int4*>(a.scratch + plan.meta);
     p.part_ml = reinterpret_cast<float2*>(a.scratch + plan.ml);
     p.part_o = reinterpret_cast<float*>(a.scratch + plan.o);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int ctas = (sms < kPgMaxCtas ? sms : kPgMaxCtas) / plan.groups;
-    fwd_paged_kernel<<<ctas * plan.groups, kPgThreads, kPgSmem, s>>>(mq, mb, p);
-    const cudaError_t e = cudaGetLastError();
+    // Programmatic launches: a kernel's blocks may start when the one before no longer needs the SMs,
+    // and wait for its end (grid_dep_wait) before they read or write anything.
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas * plan.groups);
+    cfg.blockDim = dim3(kPgThreads);
+    cfg.dynamicSmemBytes = kPgSmem;
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, fwd_paged_kernel, mq, mb, p);
     if (e != cudaSuccess) return e;
-    combine_paged_kernel<<<dim3(ctas * plan.groups, plan.group_heads / 4), 256, 0, s>>>(p);
+    cfg.gridDim = dim3(ctas * plan.groups, plan.group_heads / 4);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, combine_paged_kernel, p);
+    if (e != cudaSuccess) return e;
     note_launch(2);
     return cudaGetLastError();
 }

@@ -75,12 +75,15 @@ int check_align(const void* const* ptrs, int n) {
     return SMLA_OK;
 }
 
+int check_device(const void* const* ptrs, int n) {
+    const int rc = check_arch();
+    return rc ? rc : check_device_ptrs(ptrs, n);
+}
+
 // Arch and pointer checks, then the status word of the call is cleared.
 int begin(const void* const* ptrs, int n, void* workspace, cudaStream_t s) {
-    int rc = check_arch();
-    if (rc) return rc;
-    if ((rc = check_device_ptrs(ptrs, n))) return rc;
-    return cuda_rc(cudaMemsetAsync(workspace, 0, sizeof(unsigned), s));
+    const int rc = check_device(ptrs, n);
+    return rc ? rc : cuda_rc(cudaMemsetAsync(workspace, 0, sizeof(unsigned), s));
 }
 
 }  // namespace
@@ -124,8 +127,8 @@ int smla_fwd_paged(const uint16_t* q, const smla_cache* cache, const int32_t* ta
     const Span outs[] = {{o, thd}, {lse, size_t(d.T) * d.H * 4}, {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 3, ins, 8))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 11, workspace, s))) return rc;
-    if (d.T == 0) return SMLA_OK;
+    if (d.T == 0) return begin(ptrs, 11, workspace, s);
+    if ((rc = check_device(ptrs, 11))) return rc;        // (the kernels write the status word)
     PagedArgs a{};
     a.q = q; a.cache = view(c); a.table = table; a.seq = seq; a.lens = lens; a.topk = topk; a.sink = sink;
     a.o = o; a.lse = lse;

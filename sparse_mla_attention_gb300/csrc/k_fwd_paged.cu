@@ -79,13 +79,16 @@ struct PgShared {
     __align__(16) float smax[kPgSlots][kPgLoadWarps];     // largest block scale of 16 ranks
     __align__(16) float2 scale[kPgSlots][kPgTile];        // of each rank: block scale and 0, or 0 and -inf (masked)
     __align__(16) float fac[2][2][kPgHeads];     // rescaling factors (team, parity of its count)
-    float qfac[4][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
+    // per item & 1 (an item's q is split only when the output of the item two before is done)
+    float qfac[2][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
     float st_ref[kPgHeads];                      // running reference of a head
-    float ref[4][2][kPgHeads], l[4][2][kPgHeads];         // per item and team: reference and sum of a head
+    float ref[2][2][kPgHeads], l[2][2][kPgHeads];         // and team: reference and sum of a head
     __align__(16) float fin[4][kPgHeads];        // per output warp: 1 / denominator
 };
 
-constexpr int kPgSmem = int(sizeof(PgShared)) + 1024 + kPgSlots * kPgSlotBytes + 2 * kPgPBytes;
+constexpr int kPgStageBytes = 2048;              // an output warp's staging: two halves
+constexpr int kPgSmem =
+    int(sizeof(PgShared)) + 1024 + kPgSlots * kPgSlotBytes + 2 * kPgPBytes + 4 * kPgStageBytes;
 static_assert(kPgSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 
 struct PgParams {
@@ -649,7 +652,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 ok = pg_wait_warp(&sh.s_full[team], use, ab, &sh.status);
                 if (!ok) break;
                 tc_fence_after();
-                if (i < 2) f = sh.qfac[item & 3][head] * lo_factor;
+                if (i < 2) f = sh.qfac[item & 1][head] * lo_factor;
                 const float4* scp = reinterpret_cast<const float4*>(&sh.scale[slot][32 * part]);
                 float s[32];
                 float mx = -INFINITY;
@@ -729,8 +732,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     const float both = l + __shfl_xor_sync(0xffffffffu, l, 16);
                     if (part == 0) {
-                        sh.ref[item & 3][team][head] = ref;
-                        sh.l[item & 3][team][head] = both;
+                        sh.ref[item & 1][team][head] = ref;
+                        sh.l[item & 1][team][head] = both;
                     }
                 }
                 fence_proxy_async_smem();
@@ -745,6 +748,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int quarter = warp & 3, part = lane >> 4, head = 16 * quarter + (lane & 15);
         const bool active = 16 * quarter < heads;
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
+        uint8_t* stage = pbuf + 2 * kPgPBytes + quarter * kPgStageBytes;
         int g = 2, item = 0, q_next = 0;
         bool ok = true;
         int t_prev = 0;
@@ -783,7 +787,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const float inv = __int_as_float((127 - e2) << 23);
                     // infinities and NaN in q make every score of the head NaN
                     if (part == 0)
-                        sh.qfac[item & 3][head] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
+                        sh.qfac[item & 1][head] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
                                                                  : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
                     // in place: eight values become eight bytes hi and eight bytes lo
 #pragma unroll 1
@@ -851,7 +855,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             ok = pg_wait_warp(&sh.o_full, uint32_t(done) & 1u, ab, &sh.status);
             if (!ok) break;
             tc_fence_after();
-            const int st = done & 3;
+            const int st = done & 1;
             float* fin = sh.fin[quarter];
             const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
             for (int h = lane; h < heads; h += 32) {
@@ -879,52 +883,72 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
             }
             __syncwarp();
-            // 16 heads of a column block at a time, the next ones read while these are stored
-            uint32_t v[2][16];
-            const uint32_t src = trow + kPgColO;
-            tmem_ld16(src, v[0]);
-            tmem_wait_ld();
-            auto store = [&](const uint32_t (&x)[16], int k) {
-                const int h = (k >> 2) * 16, d = 128 * (k & 3) + 32 * quarter + lane;
+            // 16 heads x 32 columns of D at a time, the next ones read from TMEM while these are
+            // stored. A whole token's are read as matrix fragments (lane i: rows i / 4 of eight
+            // columns, heads 2 (i % 4) and the next), turned by stmatrix in shared memory and stored
+            // 16 bytes a lane; a part's are stored four heads of a column at a time.
+            auto read = [&](int k, uint32_t (&x)[16]) {
+                const uint32_t src = trow + kPgColO + 64 * (k & 3) + 16 * (k >> 2);
                 if (whole) {
-                    // two lanes swap a value of a head pair, so that each stores two columns of one head
-                    const int odd = lane & 1;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o) +
-                                    ((int64_t(t) * p.H + head0 + h + odd) * kD + (d & ~1)) / 2;
+                    tmem_ld_frag16(src, x);
+                    tmem_ld_frag16(src + (16u << 16), x + 8);
+                } else {
+                    tmem_ld16(src, x);
+                }
+            };
+            auto store = [&](int k, const uint32_t (&x)[16]) {
+                const int h = (k >> 2) * 16, d = 128 * (k & 3) + 32 * quarter;
+                if (whole) {
+                    uint8_t* at = stage + 1024 * (k & 1);
 #pragma unroll
-                    for (int e4 = 0; e4 < 4; ++e4) {
-                        const float4 f4 = *reinterpret_cast<const float4*>(fin + h + 4 * e4);
-                        const float fe[4] = {f4.x, f4.y, f4.z, f4.w};
+                    for (int e = 0; e < 2; ++e) {            // heads 0-7, 8-15
+                        const float2 f = *reinterpret_cast<const float2*>(fin + h + 8 * e + 2 * (lane & 3));
+                        uint32_t m[4];
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const float a = __uint_as_float(x[4 * e4 + e]) * fe[e];
-                            const float c = __uint_as_float(x[4 * e4 + e + 1]) * fe[e + 1];
-                            const float r = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-                            dst[(4 * e4 + e) * (kD / 2)] = odd ? pack_bf16x2(r, c) : pack_bf16x2(a, r);
+                        for (int r = 0; r < 4; ++r) {        // rows 8r .. 8r + 7
+                            const int i = 8 * (r >> 1) + 4 * e + 2 * (r & 1);
+                            m[r] = pack_bf16x2(__uint_as_float(x[i]) * f.x, __uint_as_float(x[i + 1]) * f.y);
                         }
+                        // 64-byte rows, pieces of 16 bytes swizzled
+                        const int r = 8 * e + (lane & 7), c = lane >> 3;
+                        stmatrix_x4_trans(at + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), m);
+                    }
+                    __syncwarp();
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + (int64_t(t) * p.H + head0 + h) * kD + d);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * e + (lane >> 2), c = lane & 3;
+                        dst[r * (kD / 8) + c] =
+                            *reinterpret_cast<const uint4*>(at + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
                     }
                 } else {
                     float4* dst = reinterpret_cast<float4*>(p.part_o) +
-                                  (int64_t(part_at) * (p.group_heads / 4) + h / 4) * kD + d;
+                                  (int64_t(part_at) * (p.group_heads / 4) + h / 4) * kD + d + lane;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         dst[e * kD] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]),
                                                   __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]));
                 }
             };
+            uint32_t v[2][16];
+            read(0, v[0]);
+            tmem_wait_ld();
             const int chunks = heads / 4;
 #pragma unroll 1
             for (int k = 0; k < chunks; k += 2) {
-                tmem_ld16(src + 64 * ((k + 1) & 3) + ((k + 1) >> 2) * 16, v[1]);
-                store(v[0], k);
+                read(k + 1, v[1]);
+                store(k, v[0]);
                 tmem_wait_ld();
-                if (k + 2 < chunks) tmem_ld16(src + 64 * ((k + 2) & 3) + ((k + 2) >> 2) * 16, v[0]);
-                store(v[1], k + 1);
+                if (k + 2 < chunks) {
+                    read(k + 2, v[0]);
+                } else {                         // all of the accumulator is read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.o_empty);
+                }
+                store(k + 1, v[1]);
                 tmem_wait_ld();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.o_empty);
             if (!more) break;
         }
     }

@@ -316,6 +316,23 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                  : "r"(taddr));
 }
 
+// 16 lanes x 16 32-bit columns as matrix fragments: r[0], r[1] of thread i are columns
+// 2 (i % 4) and the next of lane i / 4, r[2], r[3] the same of lane i / 4 + 8; r[4 .. 7] the
+// columns eight further on.
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// Four 8x8 matrices of 16-bit values (thread i: rows 2 (i % 4) and the next of column i / 4, one
+// register a matrix), row j of matrix m to the address that thread 8m + j gives.
+__device__ __forceinline__ void stmatrix_x4_trans(void* row, const uint32_t (&m)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(row)),
+                 "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
+                 : "memory");
+}
+
 // Each thread of the warp writes 8 consecutive 32-bit columns of its lane.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
     asm volatile(

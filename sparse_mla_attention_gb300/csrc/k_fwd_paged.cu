@@ -754,6 +754,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int t_prev = 0;
         bool whole_prev = false;
         int teams_prev = 0, teams_next = 0;
+        float sinks[2];                          // of heads lane and lane + 32, in log2 units
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            sinks[k] = p.sink && lane + 32 * k < heads ? __ldg(p.sink + head0 + lane + 32 * k) * kPgLog2e : -INFINITY;
 
         for (PgWalk w(sh);; ++item) {
             const bool more = w.left > 0;
@@ -858,7 +862,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int st = done & 1;
             float* fin = sh.fin[quarter];
             const int part_at = int(blockIdx.x) * 2 + (first ? 0 : 1);
-            for (int h = lane; h < heads; h += 32) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int h = lane + 32 * j;
+                if (h >= heads) continue;
                 // sums are in units of 2^(reference - bias)
                 const float ma = any & 1 ? sh.ref[st][0][h] : -INFINITY, mb = any & 2 ? sh.ref[st][1][h] : -INFINITY;
                 const float la = any & 1 ? sh.l[st][0][h] : 0.f, lb = any & 2 ? sh.l[st][1][h] : 0.f;
@@ -868,7 +875,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 const float l = (la == 0.f || ma == mu ? la : la * ex2_approx(ma - mu)) +
                                 (lb == 0.f || mb == mu ? lb : lb * ex2_approx(mb - mu));
                 if (whole) {
-                    const float sink = p.sink ? __ldg(p.sink + head0 + h) * kPgLog2e : -INFINITY;
+                    const float sink = sinks[j];
                     // a NaN sum stays one; a sum of zero leaves the sink alone
                     const float top = l == 0.f ? sink : fmaxf(m2, sink);
                     const float base = top == -INFINITY ? 0.f : top;

@@ -18,7 +18,21 @@ import torch
 
 from . import _lib
 from ._lib import SmlaCache, SmlaPagedDims
-from .api import D_HEAD, Workspace, _need, _ptr, _stream, device_status
+from .api import D_HEAD, Workspace, _need, device_status
+
+# A decode step makes these calls once a layer, and their kernels take some ten
+# microseconds: checks and marshalling are kept to a few attribute reads a tensor.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _check(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> int:
+    """Address of a tensor that a call can take; raises what _need raises, or for its device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == cache._index
+            and t.is_contiguous()):
+        _need(t, name, dtype, ndim)
+        raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
+    return t.data_ptr()
 
 
 class PagedCache:
@@ -48,6 +62,8 @@ class PagedCache:
         self.num_pages, self.page_size = n, ps
         self.scale_block = ps // scales.shape[1]
         self.device = pages.device
+        self._index = pages.get_device()
+        self._sizes = {}
         self._c = SmlaCache(pages=pages.data_ptr(), scales=scales.data_ptr(),
                             refcount=refcount.data_ptr(), num_pages=n, page_size=ps,
                             scale_block=self.scale_block, D=d)
@@ -66,20 +82,47 @@ class PagedCache:
                    torch.zeros(num_pages, dtype=torch.int32, device=dev))
 
     def _workspace(self, workspace: Optional[Workspace], n: int) -> torch.Tensor:
-        size = ctypes.c_size_t(0)
-        _lib.check(_lib.load().smla_cache_workspace_size(self._ref, n, ctypes.byref(size)),
-                   "smla_cache_workspace_size")
-        return (workspace or Workspace(self.device)).get(size.value)
+        size = self._sizes.get(n)
+        if size is None:
+            out = ctypes.c_size_t(0)
+            _lib.check(_lib.load().smla_cache_workspace_size(self._ref, n, ctypes.byref(out)),
+                       "smla_cache_workspace_size")
+            size = self._sizes[n] = out.value
+        return _on_device(self, workspace, size)
 
 
-def _same_device(cache: PagedCache, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
+def _on_device(cache: PagedCache, workspace: Optional[Workspace], size: int) -> torch.Tensor:
+    ws = (workspace or Workspace(cache.device)).get(size)
+    if ws.get_device() != cache._index:
+        raise ValueError(f"workspace must be on {cache.device}, got {ws.device}")
+    return ws
 
 
-def _finish(code: int, where: str, ws: torch.Tensor, check_status: bool) -> None:
-    _lib.check(code, where)
+_paged_sizes = {}
+
+
+def _paged_size(dims: SmlaPagedDims) -> int:
+    key = (dims.T > 0, dims.H)            # what smla_paged_workspace_size goes by
+    size = _paged_sizes.get(key)
+    if size is None:
+        out = ctypes.c_size_t(0)
+        _lib.check(_lib.load().smla_paged_workspace_size(ctypes.byref(dims), ctypes.byref(out)),
+                   "smla_paged_workspace_size")
+        size = _paged_sizes[key] = out.value
+    return size
+
+
+def _run(cache: PagedCache, where: str, ws: torch.Tensor, check_status: bool, *args) -> None:
+    """Calls library function `where` with args, the workspace and the cache's device's stream."""
+    fn = getattr(_lib.load(), where)
+    tail = (ws.data_ptr(), ws.numel(), _raw_stream(cache._index))
+    if torch.cuda.current_device() == cache._index:
+        code = fn(*args, *tail)
+    else:
+        with torch.cuda.device(cache._index):
+            code = fn(*args, *tail)
+    if code != _lib.SMLA_OK:
+        raise _lib.SmlaError(code, where)
     if check_status:
         st = device_status(ws)
         if st != _lib.SMLA_OK:
@@ -100,48 +143,44 @@ def sparse_mla_fwd_paged(q: torch.Tensor, cache: PagedCache, table: torch.Tensor
     (a padded slot) gets zeros. ``out`` = (o, lse) writes into the caller's
     tensors.
     """
-    _need(q, "q", torch.bfloat16, 3)
-    _need(table, "table", torch.int32, 2)
-    _need(lens, "lens", torch.int32, 1)
+    p_q = _check(cache, q, "q", torch.bfloat16, 3)
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_lens = _check(cache, lens, "lens", torch.int32, 1)
     T, H, D = q.shape
+    B, max_pages = table.shape
     if lens.shape[0] != T:
         raise ValueError("lens must have shape [T]")
     K = 0
+    p_topk = p_seq = p_sink = None
     if topk is not None:
-        _need(topk, "topk", torch.int32, 2)
+        p_topk = _check(cache, topk, "topk", torch.int32, 2)
         K = topk.shape[1]
         if topk.shape[0] != T or K < 1:
             raise ValueError("topk must have shape [T, K], K >= 1")
     if seq is not None:
-        _need(seq, "seq", torch.int32, 1)
+        p_seq = _check(cache, seq, "seq", torch.int32, 1)
         if seq.shape[0] != T:
             raise ValueError("seq must have shape [T]")
-    elif T > table.shape[0]:
+    elif T > B:
         raise ValueError("without seq, table must have a row for each token")
     if sink is not None:
-        _need(sink, "sink", torch.float32, 1)
+        p_sink = _check(cache, sink, "sink", torch.float32, 1)
         if sink.shape[0] != H:
             raise ValueError("sink must have shape [H]")
     if out is None:
         o = torch.empty_like(q)
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((T, H), dtype=torch.float32)
+        p_o, p_lse = o.data_ptr(), lse.data_ptr()
     else:
         o, lse = out
-        _need(o, "o", torch.bfloat16, 3)
-        _need(lse, "lse", torch.float32, 2)
+        p_o = _check(cache, o, "o", torch.bfloat16, 3)
+        p_lse = _check(cache, lse, "lse", torch.float32, 2)
         if o.shape != q.shape or tuple(lse.shape) != (T, H):
             raise ValueError("out must be (o [T,H,D], lse [T,H])")
-    _same_device(cache, q=q, table=table, lens=lens, topk=topk, seq=seq, sink=sink, o=o, lse=lse)
-    lib = _lib.load()
-    dims = SmlaPagedDims(T, H, D, K, table.shape[0], table.shape[1], 0.0 if scale is None else float(scale))
-    ref = ctypes.byref(dims)
-    size = ctypes.c_size_t(0)
-    _lib.check(lib.smla_paged_workspace_size(ref, ctypes.byref(size)), "smla_paged_workspace_size")
-    ws = (workspace or Workspace(q.device)).get(size.value)
-    _finish(lib.smla_fwd_paged(_ptr(q), cache._ref, _ptr(table), _ptr(seq), _ptr(lens), _ptr(topk),
-                               _ptr(sink), _ptr(o), _ptr(lse), ref, _ptr(ws), ws.numel(),
-                               _stream(q.device)),
-            "smla_fwd_paged", ws, check_status)
+    dims = SmlaPagedDims(T, H, D, K, B, max_pages, 0.0 if scale is None else float(scale))
+    ws = _on_device(cache, workspace, _paged_size(dims))
+    _run(cache, "smla_fwd_paged", ws, check_status, p_q, cache._ref, p_table, p_seq, p_lens, p_topk, p_sink, p_o,
+         p_lse, ctypes.byref(dims))
     return o, lse
 
 
@@ -149,37 +188,30 @@ def cache_write(cache: PagedCache, table: torch.Tensor, start: torch.Tensor, cu_
                 rows: torch.Tensor, workspace: Optional[Workspace] = None, check_status: bool = True) -> None:
     """Write rows[cu_rows[b]:cu_rows[b+1]] (bf16 [n,512]) to the positions from start[b] on of
     the sequence in table row b, quantised block by block (smla_cache_write)."""
-    _need(table, "table", torch.int32, 2)
-    _need(start, "start", torch.int32, 1)
-    _need(cu_rows, "cu_rows", torch.int32, 1)
-    _need(rows, "rows", torch.bfloat16, 2)
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_start = _check(cache, start, "start", torch.int32, 1)
+    p_cu = _check(cache, cu_rows, "cu_rows", torch.int32, 1)
+    p_rows = _check(cache, rows, "rows", torch.bfloat16, 2)
     B = table.shape[0]
     if start.shape[0] != B or cu_rows.shape[0] != B + 1:
         raise ValueError("start must have shape [B] and cu_rows [B+1]")
     if rows.shape[1] != D_HEAD:
         raise ValueError("rows must have shape [n, 512]")
-    _same_device(cache, table=table, start=start, cu_rows=cu_rows, rows=rows)
-    ws = (workspace or Workspace(cache.device)).get(256)
-    _finish(_lib.load().smla_cache_write(cache._ref, _ptr(table), _ptr(start), _ptr(cu_rows), _ptr(rows),
-                                         B, table.shape[1], rows.shape[0], _ptr(ws), ws.numel(),
-                                         _stream(cache.device)),
-            "smla_cache_write", ws, check_status)
+    _run(cache, "smla_cache_write", _on_device(cache, workspace, 256), check_status, cache._ref, p_table, p_start,
+         p_cu, p_rows, B, table.shape[1], rows.shape[0])
 
 
 def cache_alloc(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor,
                 workspace: Optional[Workspace] = None, check_status: bool = True) -> None:
     """Give every sequence the pages that lens[b] rows need, in place on table and
     cache.refcount; lowest free pages first, all or nothing (smla_cache_alloc)."""
-    _need(table, "table", torch.int32, 2)
-    _need(lens, "lens", torch.int32, 1)
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_lens = _check(cache, lens, "lens", torch.int32, 1)
     B = table.shape[0]
     if lens.shape[0] != B:
         raise ValueError("lens must have shape [B]")
-    _same_device(cache, table=table, lens=lens)
-    ws = cache._workspace(workspace, B)
-    _finish(_lib.load().smla_cache_alloc(cache._ref, _ptr(table), _ptr(lens), B, table.shape[1], _ptr(ws),
-                                         ws.numel(), _stream(cache.device)),
-            "smla_cache_alloc", ws, check_status)
+    _run(cache, "smla_cache_alloc", cache._workspace(workspace, B), check_status, cache._ref, p_table, p_lens, B,
+         table.shape[1])
 
 
 def cache_fork(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
@@ -189,22 +221,19 @@ def cache_fork(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, paren
 
     Full pages are shared (refcount + 1), a partly filled last page is copied
     to a free one. All or nothing. ``out`` takes the child rows."""
-    _need(table, "table", torch.int32, 2)
-    _need(lens, "lens", torch.int32, 1)
-    _need(parents, "parents", torch.int32, 1)
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_lens = _check(cache, lens, "lens", torch.int32, 1)
+    p_parents = _check(cache, parents, "parents", torch.int32, 1)
     B, max_pages = table.shape
     n = parents.shape[0]
     if lens.shape[0] != B:
         raise ValueError("lens must have shape [B]")
-    child = torch.empty((n, max_pages), dtype=torch.int32, device=table.device) if out is None else out
-    _need(child, "out", torch.int32, 2)
+    child = table.new_empty((n, max_pages)) if out is None else out
+    p_child = _check(cache, child, "out", torch.int32, 2)
     if tuple(child.shape) != (n, max_pages):
         raise ValueError("out must have shape [n, max_pages]")
-    _same_device(cache, table=table, lens=lens, parents=parents, out=child)
-    ws = cache._workspace(workspace, n)
-    _finish(_lib.load().smla_cache_fork(cache._ref, _ptr(table), _ptr(lens), _ptr(parents), _ptr(child), B, n,
-                                        max_pages, _ptr(ws), ws.numel(), _stream(cache.device)),
-            "smla_cache_fork", ws, check_status)
+    _run(cache, "smla_cache_fork", cache._workspace(workspace, n), check_status, cache._ref, p_table, p_lens,
+         p_parents, p_child, B, n, max_pages)
     return child
 
 
@@ -212,16 +241,12 @@ def cache_free(cache: PagedCache, table: torch.Tensor, rows: Optional[torch.Tens
                workspace: Optional[Workspace] = None, check_status: bool = True) -> None:
     """Give back the pages of the table rows listed in ``rows`` (all rows without it): their
     entries become -1 and the pages' refcounts fall by one (smla_cache_free)."""
-    _need(table, "table", torch.int32, 2)
-    if rows is not None:
-        _need(rows, "rows", torch.int32, 1)
-    _same_device(cache, table=table, rows=rows)
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_rows = None if rows is None else _check(cache, rows, "rows", torch.int32, 1)
     B = table.shape[0]
     n = B if rows is None else rows.shape[0]
-    ws = (workspace or Workspace(cache.device)).get(256)
-    _finish(_lib.load().smla_cache_free(cache._ref, _ptr(table), _ptr(rows), B, n, table.shape[1], _ptr(ws),
-                                        ws.numel(), _stream(cache.device)),
-            "smla_cache_free", ws, check_status)
+    _run(cache, "smla_cache_free", _on_device(cache, workspace, 256), check_status, cache._ref, p_table, p_rows, B, n,
+         table.shape[1])
 
 
 def cache_compact(cache: PagedCache, table: torch.Tensor, workspace: Optional[Workspace] = None,
@@ -233,21 +258,17 @@ def cache_compact(cache: PagedCache, table: torch.Tensor, workspace: Optional[Wo
     are left as they are, and stay readable until a page is written; to go on
     with the compacted pool, use new_table and copy new_refcount into
     cache.refcount."""
-    _need(table, "table", torch.int32, 2)
+    p_table = _check(cache, table, "table", torch.int32, 2)
     if out is None:
         new_table, new_refcount = torch.empty_like(table), torch.empty_like(cache.refcount)
     else:
         new_table, new_refcount = out
-        _need(new_table, "new_table", torch.int32, 2)
-        _need(new_refcount, "new_refcount", torch.int32, 1)
-        if new_table.shape != table.shape or new_refcount.shape != cache.refcount.shape:
-            raise ValueError("out must be (new_table [B,max_pages], new_refcount [num_pages])")
-    _same_device(cache, table=table, new_table=new_table, new_refcount=new_refcount)
-    ws = cache._workspace(workspace, 0)
-    _finish(_lib.load().smla_cache_compact(cache._ref, _ptr(table), _ptr(new_table), _ptr(new_refcount),
-                                           table.shape[0], table.shape[1], _ptr(ws), ws.numel(),
-                                           _stream(cache.device)),
-            "smla_cache_compact", ws, check_status)
+    p_new = _check(cache, new_table, "new_table", torch.int32, 2)
+    p_count = _check(cache, new_refcount, "new_refcount", torch.int32, 1)
+    if new_table.shape != table.shape or new_refcount.shape != cache.refcount.shape:
+        raise ValueError("out must be (new_table [B,max_pages], new_refcount [num_pages])")
+    _run(cache, "smla_cache_compact", cache._workspace(workspace, 0), check_status, cache._ref, p_table, p_new,
+         p_count, table.shape[0], table.shape[1])
     return new_table, new_refcount
 
 
@@ -255,13 +276,9 @@ def cache_copy_pages(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
                      workspace: Optional[Workspace] = None, check_status: bool = True) -> None:
     """Copy whole pages and their scales, src[i] to dst[i]. Every dst must differ from the others
     and from every src, else nothing is copied (smla_cache_copy_pages)."""
-    _need(src, "src", torch.int32, 1)
-    _need(dst, "dst", torch.int32, 1)
+    p_src = _check(cache, src, "src", torch.int32, 1)
+    p_dst = _check(cache, dst, "dst", torch.int32, 1)
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
-    _same_device(cache, src=src, dst=dst)
     n = src.shape[0]
-    ws = cache._workspace(workspace, n)
-    _finish(_lib.load().smla_cache_copy_pages(cache._ref, _ptr(src), _ptr(dst), n, _ptr(ws), ws.numel(),
-                                              _stream(cache.device)),
-            "smla_cache_copy_pages", ws, check_status)
+    _run(cache, "smla_cache_copy_pages", cache._workspace(workspace, n), check_status, cache._ref, p_src, p_dst, n)

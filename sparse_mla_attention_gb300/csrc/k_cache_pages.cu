@@ -13,10 +13,12 @@
 #include <cooperative_groups.h>
 
 #include "smla_internal.cuh"
+#include "sm100.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace smla {
+using namespace sm100;
 
 namespace {
 
@@ -28,31 +30,34 @@ constexpr int kCopyVecs = 4;                                   // 16-byte pieces
 constexpr int kCopyChunk = kCopyThreads * kCopyVecs * 16;      // 16 KB
 
 struct PlanShared {
-    long long warp[kPlanWarps];
-    long long part[4];          // this CTA's totals, read by the other CTAs
+    int warp[2][kPlanWarps];    // a scan's sums by warp; two sets in turn
+    int part;                   // this CTA's total and status bits, read by the other CTAs
+    unsigned bits;
 };
 
-// Exclusive sum over the CTA's threads in thread order; *total gets the sum.
-__device__ __forceinline__ long long cta_scan(long long v, PlanShared& sh, long long* total) {
+// Exclusive sum over the CTA's threads in thread order; *total gets the sum. `turn`
+// alternates from scan to scan (one barrier a scan: the sums of the last but one are read).
+__device__ __forceinline__ int cta_scan(int v, PlanShared& sh, int& turn, int* total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long x = v;
+    int x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
     }
-    __syncthreads();                                           // the last scan's sums are read
-    if (lane == 31) sh.warp[warp] = x;
+    if (lane == 31) sh.warp[turn][warp] = x;
     __syncthreads();
-    long long before = 0, all = 0;
+    static_assert(kPlanWarps == 32, "a lane for each warp's sum");
+    int y = sh.warp[turn][lane];
 #pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w) {
-        const long long t = sh.warp[w];
-        if (w < warp) before += t;
-        all += t;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, d);
+        if (lane >= d) y += z;
     }
-    *total = all;
-    return before + x - v;
+    turn ^= 1;
+    *total = __shfl_sync(0xffffffffu, y, 31);
+    const int before = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
+    return (warp ? before : 0) + x - v;
 }
 
 // This CTA's share of the pages: [lo, hi), lo a multiple of 4.
@@ -75,28 +80,29 @@ __device__ __forceinline__ int4 load4(const int32_t* rc, int i, int hi) {
 
 // Pages i of [lo, hi) with pred(i, refcount) (refcount -1 never counts).
 template <class Pred>
-__device__ long long count_pages(const int32_t* rc, int lo, int hi, PlanShared& sh, Pred pred) {
+__device__ int count_pages(const int32_t* rc, int lo, int hi, PlanShared& sh, int& turn, Pred pred) {
     int n = 0;
+#pragma unroll 4
     for (int i = lo + 4 * int(threadIdx.x); i < hi; i += 4 * kPlanThreads) {
         const int4 v = load4(rc, i, hi);
         n += int(pred(i, v.x)) + int(pred(i + 1, v.y)) + int(pred(i + 2, v.z)) + int(pred(i + 3, v.w));
     }
-    long long total;
-    cta_scan(n, sh, &total);
+    int total;
+    cta_scan(n, sh, turn, &total);
     return total;
 }
 
 // out(rank, i) for the pages i of [lo, hi) with pred(i, refcount), in order,
 // ranks from `rank` on, until `limit`.
 template <class Pred, class Out>
-__device__ void emit_pages(const int32_t* rc, int lo, int hi, long long rank, long long limit,
-                           PlanShared& sh, Pred pred, Out out) {
+__device__ void emit_pages(const int32_t* rc, int lo, int hi, int rank, int limit, PlanShared& sh, int& turn,
+                           Pred pred, Out out) {
     for (int base = lo; base < hi && rank < limit; base += 4 * kPlanThreads) {
         const int i = base + 4 * int(threadIdx.x);
         const int4 v = load4(rc, i, hi);
         const bool p0 = pred(i, v.x), p1 = pred(i + 1, v.y), p2 = pred(i + 2, v.z), p3 = pred(i + 3, v.w);
-        long long total;
-        long long r = rank + cta_scan(int(p0) + int(p1) + int(p2) + int(p3), sh, &total);
+        int total;
+        int r = rank + cta_scan(int(p0) + int(p1) + int(p2) + int(p3), sh, turn, &total);
         if (p0) { if (r < limit) out(r, i); ++r; }
         if (p1) { if (r < limit) out(r, i + 1); ++r; }
         if (p2) { if (r < limit) out(r, i + 2); ++r; }
@@ -105,50 +111,71 @@ __device__ void emit_pages(const int32_t* rc, int lo, int hi, long long rank, lo
     }
 }
 
-// Sum of part[k] over the CTAs, and over those before this one.
-__device__ __forceinline__ void join(cg::cluster_group& cl, PlanShared& sh, int k, long long& before,
-                                     long long& all) {
+// The CTAs' totals: their sum, the sum over those before this one; and all status bits.
+__device__ __forceinline__ void join(cg::cluster_group& cl, PlanShared& sh, int& before, int& all, unsigned& bits) {
+    int part[kPlanCtas];
+    unsigned b[kPlanCtas];
+#pragma unroll
+    for (unsigned r = 0; r < kPlanCtas; ++r) {
+        part[r] = cl.map_shared_rank(&sh, r)->part;
+        b[r] = cl.map_shared_rank(&sh, r)->bits;
+    }
     before = 0;
     all = 0;
+    bits = 0;
+#pragma unroll
     for (unsigned r = 0; r < kPlanCtas; ++r) {
-        const long long t = cl.map_shared_rank(&sh, r)->part[k];
-        if (r < cl.block_rank()) before += t;
-        all += t;
+        if (r < cl.block_rank()) before += part[r];
+        all += part[r];
+        bits |= b[r];
     }
 }
 
-// Exclusive sums of need[0..n) into off (written by CTA 0 only); returns the sum.
-__device__ long long scan_needs(const int32_t* need, int n, int32_t* off, PlanShared& sh) {
-    long long sum = 0;
+// Exclusive sums of need(i), i < n, saturated at `most`; each(i, need, sum before). Returns the sum.
+template <class Need, class Each>
+__device__ int scan_needs(int n, int most, PlanShared& sh, int& turn, Need need, Each each) {
+    int64_t sum = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
         const int i = base + int(threadIdx.x);
-        long long total;
-        const long long at = sum + cta_scan(i < n ? __ldcg(need + i) : 0, sh, &total);
-        // offsets past 2^31 belong to a call that has too few pages: never used
-        if (off && i < n) off[i] = int32_t(at < INT32_MAX ? at : INT32_MAX);
+        // (a row's need is below 2^20 here or the call is short of pages anyway: see callers)
+        const int v = i < n ? need(i) : 0;
+        int total;
+        const int64_t at = sum + cta_scan(v, sh, turn, &total);
+        if (i < n) each(i, v, int(at < most ? at : most));
         sum += total;
+        if (sum > most) sum = most;
     }
-    return sum;
+    return int(sum);
 }
 
 __device__ __forceinline__ bool is_free(int, int rc) { return rc == 0; }
 
 // A length as pages, clamped to the table.
-__device__ __forceinline__ int clamp_len(int len, int64_t limit, unsigned* status) {
+__device__ __forceinline__ int clamp_len(int len, int64_t limit, unsigned& bits) {
     if (len >= 0 && len <= limit) return len;
-    flag_status(status, SMLA_ERR_INDEX);
+    bits |= 1u << SMLA_ERR_INDEX;
     return len < 0 ? 0 : int(limit);
 }
 
-// Copies 16 KB pieces of the pages in pairs (src[k], dst[k]), k < m, over the grid.
-__device__ void copy_pairs(const CacheView& c, const int32_t* src, const int32_t* dst, int m,
-                           unsigned* status) {
+// Copies 16 KB pieces of the pages in pairs (src(k), dst(k)), k < m, over the grid.
+template <class Src, class Dst>
+__device__ void copy_pairs(const CacheView& c, Src src, Dst dst, int m, unsigned* status) {
     const int64_t page_bytes = int64_t(kD) << c.page_shift;
     const int chunks = int((page_bytes + kCopyChunk - 1) / kCopyChunk);
     const int nscale = 1 << (c.page_shift - c.block_shift);
-    for (int64_t w = blockIdx.x; w < int64_t(m) * chunks; w += gridDim.x) {
-        const int k = int(w / chunks), ch = int(w % chunks);
-        const int a = __ldg(src + k), b = __ldg(dst + k);
+    // (the next piece's page numbers are read ahead)
+    const int64_t all = int64_t(m) * chunks;
+    int a1 = -1, b1 = -1;
+    if (blockIdx.x < all) {
+        a1 = src(int(blockIdx.x / chunks));
+        b1 = dst(int(blockIdx.x / chunks));
+    }
+    for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
+        const int ch = int(w % chunks), a = a1, b = b1;
+        if (w + gridDim.x < all) {
+            a1 = src(int((w + gridDim.x) / chunks));
+            b1 = dst(int((w + gridDim.x) / chunks));
+        }
         if (a < 0 || a >= c.num_pages || b < 0 || b >= c.num_pages) {
             if (threadIdx.x == 0) flag_status(status, SMLA_ERR_INDEX);
             continue;
@@ -184,8 +211,10 @@ alloc_kernel(const CacheView c, int32_t* __restrict__ table, const int32_t* __re
     const int gw = rank * kPlanWarps + (threadIdx.x >> 5);
     const int64_t limit = int64_t(max_pages) << c.page_shift;
     const int round = (1 << c.page_shift) - 1;
+    unsigned bits = 0;
+    int turn = 0;
     for (int b = gw; b < B; b += kPlanCtas * kPlanWarps) {
-        const int len = clamp_len(__ldg(lens + b), limit, status);
+        const int len = clamp_len(__ldg(lens + b), limit, bits);
         const int np = int((int64_t(len) + round) >> c.page_shift);
         int n = 0;
         for (int j = lane; j < np; j += 32) n += table[int64_t(b) * max_pages + j] == -1;
@@ -194,24 +223,45 @@ alloc_kernel(const CacheView c, int32_t* __restrict__ table, const int32_t* __re
     }
     int lo, hi;
     page_slice(c.num_pages, rank, lo, hi);
-    const long long mine = count_pages(c.refcount, lo, hi, sh, is_free);
-    if (threadIdx.x == 0) sh.part[0] = mine;
+    const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
+    bits = __syncthreads_or(bits) ? 1u << SMLA_ERR_INDEX : 0;
+    if (threadIdx.x == 0) { sh.part = mine; sh.bits = bits; }
     cl.sync();
-    long long before, have;
-    join(cl, sh, 0, before, have);
-    const long long want = scan_needs(w.need, B, rank == 0 ? w.src : nullptr, sh);
-    const bool ok = want <= have;
+    int before, have;
+    join(cl, sh, before, have, bits);
+    // A sum of 1024 needs, each cut at 2^20, fits 32 bits; a row that needs more than
+    // 2^20 pages is counted as 2^20 in the first pass only if that many are not there
+    const int cap = have < (1 << 20) ? have + 1 : (1 << 20);
+    int64_t big = 0;
+    const int want = scan_needs(B, have + 1, sh, turn,
+                                [&](int i) {
+                                    const int v = __ldcg(w.need + i);
+                                    if (v > cap) big = 1;
+                                    return v < cap ? v : cap;
+                                },
+                                [&](int i, int, int at) { if (rank == 0) w.src[i] = at; });
+    const bool huge = __syncthreads_or(int(big)) != 0 && have >= (1 << 20);
+    // (rows of more than 2^20 pages, in a pool that has as many: summed one by one)
+    int need = want;
+    if (huge) {
+        int64_t sum = 0;
+        for (int i = 0; i < B; ++i) {
+            if (rank == 0 && threadIdx.x == 0) w.src[i] = int(sum < have ? sum : have);
+            sum += __ldcg(w.need + i);
+        }
+        need = int(sum < int64_t(have) + 1 ? sum : int64_t(have) + 1);
+    }
+    const bool ok = need <= have;
     if (ok)
-        emit_pages(c.refcount, lo, hi, before, want, sh, is_free, [&](long long r, int i) {
+        emit_pages(c.refcount, lo, hi, before, need, sh, turn, is_free, [&](int r, int i) {
             w.dst[r] = i;
             c.refcount[i] = 1;
         });
-    else if (rank == 0 && threadIdx.x == 0)
-        flag_status(status, SMLA_ERR_PAGES);
-    cl.sync();                                  // offsets and pages are written; part[] is read
+    if (rank == 0 && threadIdx.x == 0) *status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
+    cl.sync();                                  // offsets and pages are written; parts are read
     if (!ok) return;
     for (int b = gw; b < B; b += kPlanCtas * kPlanWarps) {
-        const int len = min(max(__ldg(lens + b), 0), int(limit));
+        const int len = int(min(int64_t(max(__ldg(lens + b), 0)), limit));
         const int np = int((int64_t(len) + round) >> c.page_shift);
         int at = __ldcg(w.src + b);
         for (int j0 = 0; j0 < np; j0 += 32) {
@@ -224,63 +274,67 @@ alloc_kernel(const CacheView c, int32_t* __restrict__ table, const int32_t* __re
     }
 }
 
-// Plan of a fork: w.need[i] = 1 where child i needs a copy of its parent's
-// last page, w.src / w.dst the pages to copy, w.map[i] the number of child i's
-// copy, w.count[0] their number (-1: too few free pages), w.count[1] = 0.
+// Plan of a fork: w.src / w.dst the pages to copy, w.need[i] the place of child i's
+// copy in them (-1: none), w.count[0] their number (-1: too few free pages), w.count[1] = 0.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 fork_plan_kernel(const CacheView c, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
                  const int32_t* __restrict__ parents, int B, int n, int max_pages, const PageScratch w,
                  unsigned* status) {
     __shared__ PlanShared sh;
     cg::cluster_group cl = cg::this_cluster();
+    grid_dep_launch();                          // the copying kernel's blocks wait for this one's end
     const int rank = int(cl.block_rank());
     const int64_t limit = int64_t(max_pages) << c.page_shift;
-    const int gt = rank * kPlanThreads + threadIdx.x;
-    // the page that child i copies, or -1
-    auto tail_of = [&](int i, unsigned* st) {
+    unsigned bits = 0;
+    int turn = 0;
+    // w.map[i]: the page that child i copies, or -1
+    for (int i = rank * kPlanThreads + threadIdx.x; i < n; i += kPlanCtas * kPlanThreads) {
+        int e = -1;
         const int p = __ldg(parents + i);
-        if (p < 0 || p >= B) { if (st) flag_status(st, SMLA_ERR_INDEX); return -1; }
-        int len = __ldg(lens + p);
-        if (len < 0 || len > limit) {
-            if (st) flag_status(st, SMLA_ERR_INDEX);
-            len = len < 0 ? 0 : int(limit);
+        if (p < 0 || p >= B) {
+            bits |= 1u << SMLA_ERR_INDEX;
+        } else {
+            const int len = clamp_len(__ldg(lens + p), limit, bits);
+            if (len & ((1 << c.page_shift) - 1)) {
+                e = __ldg(table + int64_t(p) * max_pages + (len >> c.page_shift));
+                if (e < 0 || e >= c.num_pages) {
+                    bits |= 1u << SMLA_ERR_INDEX;
+                    e = -1;
+                } else if (__ldcg(c.refcount + e) <= 0) {
+                    bits |= 1u << SMLA_ERR_REFCOUNT;
+                    e = -1;
+                }
+            }
         }
-        if ((len & ((1 << c.page_shift) - 1)) == 0) return -1;
-        const int e = __ldg(table + int64_t(p) * max_pages + (len >> c.page_shift));
-        if (e < 0 || e >= c.num_pages) { if (st) flag_status(st, SMLA_ERR_INDEX); return -1; }
-        if (__ldcg(c.refcount + e) <= 0) { if (st) flag_status(st, SMLA_ERR_REFCOUNT); return -1; }
-        return e;
-    };
-    for (int i = gt; i < n; i += kPlanCtas * kPlanThreads) w.need[i] = tail_of(i, status) >= 0 ? 1 : 0;
+        w.tail[i] = e;
+    }
     int lo, hi;
     page_slice(c.num_pages, rank, lo, hi);
-    const long long mine = count_pages(c.refcount, lo, hi, sh, is_free);
-    if (threadIdx.x == 0) sh.part[0] = mine;
+    const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
+    const bool index = __syncthreads_or(bits & (1u << SMLA_ERR_INDEX)) != 0;
+    const bool count = __syncthreads_or(bits & (1u << SMLA_ERR_REFCOUNT)) != 0;
+    if (threadIdx.x == 0) {
+        sh.part = mine;
+        sh.bits = (index ? 1u << SMLA_ERR_INDEX : 0u) | (count ? 1u << SMLA_ERR_REFCOUNT : 0u);
+    }
     cl.sync();
-    long long before, have;
-    join(cl, sh, 0, before, have);
-    const long long want = scan_needs(w.need, n, nullptr, sh);
+    int before, have;
+    join(cl, sh, before, have, bits);
+    const int want = scan_needs(n, INT32_MAX, sh, turn,
+                                [&](int i) { return __ldcg(w.tail + i) >= 0 ? 1 : 0; },
+                                [&](int i, int need, int at) {
+                                    if (rank != 0) return;
+                                    w.need[i] = need ? at : -1;
+                                    if (need) w.src[at] = __ldcg(w.tail + i);
+                                });
     const bool ok = want <= have;
-    if (ok) emit_pages(c.refcount, lo, hi, before, want, sh, is_free,
-                       [&](long long r, int i) { w.dst[r] = i; });
-    if (ok && rank == 0) {
-        long long sum = 0;
-        for (int base = 0; base < n; base += kPlanThreads) {
-            const int i = base + int(threadIdx.x);
-            const int need = i < n ? __ldcg(w.need + i) : 0;
-            long long total;
-            const long long at = sum + cta_scan(need, sh, &total);
-            if (need) w.src[at] = tail_of(i, nullptr);
-            if (i < n) w.need[i] = need ? int(at) : -1;      // its place in the lists
-            sum += total;
-        }
-    }
+    if (ok) emit_pages(c.refcount, lo, hi, before, want, sh, turn, is_free, [&](int r, int i) { w.dst[r] = i; });
     if (rank == 0 && threadIdx.x == 0) {
-        w.count[0] = ok ? int(want) : -1;
+        w.count[0] = ok ? want : -1;
         w.count[1] = 0;
-        if (!ok) flag_status(status, SMLA_ERR_PAGES);
+        *status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
     }
-    cl.sync();                                  // no CTA leaves while another reads its part[]
+    cl.sync();                                  // no CTA leaves while another reads its part
 }
 
 // The children's table rows, the shared pages' counts and the copies.
@@ -288,7 +342,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 fork_kernel(const CacheView c, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
             const int32_t* __restrict__ parents, int32_t* __restrict__ child, int B, int n, int max_pages,
             const PageScratch w, unsigned* status) {
-    const int m = w.count[0];
+    grid_dep_wait();
+    const int m = __ldcg(w.count);
     const int64_t limit = int64_t(max_pages) << c.page_shift;
     const int64_t threads = int64_t(gridDim.x) * kCopyThreads;
     for (int64_t x = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x; x < int64_t(n) * max_pages; x += threads) {
@@ -310,13 +365,14 @@ fork_kernel(const CacheView c, const int32_t* __restrict__ table, const int32_t*
                     atomicAdd(c.refcount + e, 1);
                 }
             } else if (j == full) {
-                const int k = __ldg(w.need + i);
-                if (k >= 0) e = __ldg(w.dst + k);
+                const int k = __ldcg(w.need + i);
+                if (k >= 0) e = __ldcg(w.dst + k);
             }
         }
         child[x] = e;
     }
-    if (m > 0) copy_pairs(c, w.src, w.dst, m, status);
+    if (m > 0)
+        copy_pairs(c, [&](int k) { return __ldcg(w.src + k); }, [&](int k) { return __ldcg(w.dst + k); }, m, status);
     // the new pages are counted by the last CTA, when no other looks at counts any more
     __shared__ int last;
     __syncthreads();
@@ -326,7 +382,7 @@ fork_kernel(const CacheView c, const int32_t* __restrict__ table, const int32_t*
     }
     __syncthreads();
     if (last)
-        for (int k = threadIdx.x; k < m; k += kCopyThreads) c.refcount[__ldg(w.dst + k)] = 1;
+        for (int k = threadIdx.x; k < m; k += kCopyThreads) c.refcount[__ldcg(w.dst + k)] = 1;
 }
 
 __global__ void __launch_bounds__(256)
@@ -349,45 +405,62 @@ free_kernel(const CacheView c, int32_t* __restrict__ table, const int32_t* __res
     }
 }
 
-// Plan of a compaction: count[0] moves src[k] -> dst[k], count[1] live pages,
-// map[src[k]] = dst[k].
+// Plan of a compaction, with `live` pages in use: the holes (free pages below live) in order in
+// w.dst, the pages to move (live ones from `live` on) in reverse order in w.src, the
+// place of each in that list in w.map; count[0] their number, count[1] = live. The
+// reverse order needs no sum that only the CTA with page `live` in its share could give.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
-compact_plan_kernel(const CacheView c, const PageScratch w) {
+compact_plan_kernel(const CacheView c, const PageScratch w, unsigned* status) {
     __shared__ PlanShared sh;
     cg::cluster_group cl = cg::this_cluster();
+    grid_dep_launch();                          // the moving kernel's blocks wait for this one's end
     const int rank = int(cl.block_rank());
-    int lo, hi;
+    int lo, hi, turn = 0;
     page_slice(c.num_pages, rank, lo, hi);
-    const long long mine = count_pages(c.refcount, lo, hi, sh, [](int, int rc) { return rc > 0; });
-    if (threadIdx.x == 0) sh.part[0] = mine;
+    const int mine = count_pages(c.refcount, lo, hi, sh, turn, [](int, int rc) { return rc > 0; });
+    if (threadIdx.x == 0) { sh.part = mine; sh.bits = 0; }
     cl.sync();
-    long long before, live;
-    join(cl, sh, 0, before, live);
-    auto hole = [&](int i, int rc) { return rc == 0 && i < live; };
-    auto high = [&](int i, int rc) { return rc > 0 && i >= live; };
-    const long long holes = count_pages(c.refcount, lo, hi, sh, hole);
-    const long long highs = count_pages(c.refcount, lo, hi, sh, high);
-    if (threadIdx.x == 0) { sh.part[1] = holes; sh.part[2] = highs; }
-    cl.sync();
-    long long hole0, high0, m, m2;
-    join(cl, sh, 1, hole0, m);
-    join(cl, sh, 2, high0, m2);
-    if (m2 < m) m = m2;       // equal, unless a count is negative
-    emit_pages(c.refcount, lo, hi, hole0, m, sh, hole, [&](long long r, int i) { w.dst[r] = i; });
-    emit_pages(c.refcount, lo, hi, high0, m, sh, high, [&](long long r, int i) { w.src[r] = i; });
-    if (rank == 0 && threadIdx.x == 0) { w.count[0] = int(m); w.count[1] = int(live); }
-    cl.sync();
-    for (int k = rank * kPlanThreads + threadIdx.x; k < m; k += kPlanCtas * kPlanThreads)
-        w.map[__ldcg(w.src + k)] = __ldcg(w.dst + k);
+    int before, live;
+    unsigned bits;
+    join(cl, sh, before, live, bits);
+    // before this share: all pages are below `live` or this share has no hole
+    const int holes_before = (lo < live ? lo : live) - before;
+    if (lo < live)
+        emit_pages(c.refcount, lo, hi, holes_before, live, sh, turn,
+                   [&](int i, int rc) { return rc <= 0 && i < live && i < hi; },
+                   [&](int r, int i) { w.dst[r] = i; });
+    if (hi > live) {
+        // ranks from the front within the share, counted down from the pages behind it
+        const int behind = live - before - mine;
+        const int below = lo < live ? count_pages(c.refcount, lo, live, sh, turn, [](int, int rc) { return rc > 0; }) : 0;
+        const int here = mine - below;
+        emit_pages(c.refcount, lo, hi, 0, here, sh, turn, [&](int i, int rc) { return rc > 0 && i >= live; },
+                   [&](int r, int i) {
+                       const int k = behind + here - 1 - r;
+                       w.src[k] = i;
+                       w.map[i] = k;
+                   });
+        if (lo <= live && threadIdx.x == 0) w.count[0] = behind + here;      // all that move
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        w.count[1] = live;
+        *status = 0;
+        if (live == c.num_pages) w.count[0] = 0;
+    }
+    cl.sync();                                  // no CTA leaves while another reads its part
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
 compact_kernel(const CacheView c, const int32_t* __restrict__ table, int32_t* __restrict__ new_table,
                int32_t* __restrict__ new_refcount, int B, int max_pages, const PageScratch w,
                unsigned* status) {
-    const int m = w.count[0], live = w.count[1];
+    grid_dep_wait();
+    const int m = __ldcg(w.count), live = __ldcg(w.count + 1);
     const int64_t first = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x;
     const int64_t threads = int64_t(gridDim.x) * kCopyThreads;
+    // the k-th page that moves goes to the k-th hole; the list is in reverse order
+    auto src = [&](int k) { return __ldcg(w.src + (m - 1 - k)); };
+    auto dst = [&](int k) { return __ldcg(w.dst + k); };
     for (int64_t x = first; x < int64_t(B) * max_pages; x += threads) {
         int e = __ldg(table + x);
         if (e != -1) {
@@ -398,7 +471,7 @@ compact_kernel(const CacheView c, const int32_t* __restrict__ table, int32_t* __
                 flag_status(status, SMLA_ERR_REFCOUNT);
                 e = -1;
             } else if (e >= live) {
-                e = __ldg(w.map + e);
+                e = dst(m - 1 - __ldcg(w.map + e));
             }
         }
         new_table[x] = e;
@@ -406,11 +479,10 @@ compact_kernel(const CacheView c, const int32_t* __restrict__ table, int32_t* __
     for (int64_t i = first; i < c.num_pages; i += threads) {
         const int rc = __ldg(c.refcount + i);
         if (i >= live) new_refcount[i] = 0;
-        else if (rc != 0) new_refcount[i] = rc;             // a hole's count comes with its page, below
+        else if (rc > 0) new_refcount[i] = rc;              // a hole's count comes with its page, below
     }
-    for (int64_t k = first; k < m; k += threads)
-        new_refcount[__ldg(w.dst + k)] = __ldg(c.refcount + __ldg(w.src + k));
-    copy_pairs(c, w.src, w.dst, m, status);
+    for (int64_t k = first; k < m; k += threads) new_refcount[dst(int(k))] = __ldg(c.refcount + src(int(k)));
+    copy_pairs(c, src, dst, m, status);
 }
 
 // count[0] = n if all dst differ from each other and from every src, else 0.
@@ -420,6 +492,7 @@ copy_check_kernel(const CacheView c, const int32_t* __restrict__ src, const int3
                   const PageScratch w, unsigned* status) {
     __shared__ PlanShared sh;
     cg::cluster_group cl = cg::this_cluster();
+    grid_dep_launch();
     const int first = int(cl.block_rank()) * kPlanThreads + threadIdx.x;
     bool twice = false;
     for (int k = first; k < n; k += kPlanCtas * kPlanThreads) {
@@ -432,13 +505,14 @@ copy_check_kernel(const CacheView c, const int32_t* __restrict__ src, const int3
         if (a >= 0 && a < c.num_pages && b >= 0 && b < c.num_pages) twice |= __ldcg(w.map + a) != 0;
     }
     twice = __syncthreads_or(twice) != 0;
-    if (threadIdx.x == 0) sh.part[0] = twice;
+    if (threadIdx.x == 0) { sh.part = twice; sh.bits = 0; }
     cl.sync();
-    long long before, all;
-    join(cl, sh, 0, before, all);
+    int before, all;
+    unsigned bits;
+    join(cl, sh, before, all, bits);
     if (cl.block_rank() == 0 && threadIdx.x == 0) {
         w.count[0] = all ? 0 : n;
-        if (all) flag_status(status, SMLA_ERR_OVERLAP);
+        *status = all ? 1u << SMLA_ERR_OVERLAP : 0u;
     }
     cl.sync();
 }
@@ -446,7 +520,8 @@ copy_check_kernel(const CacheView c, const int32_t* __restrict__ src, const int3
 __global__ void __launch_bounds__(kCopyThreads)
 copy_kernel(const CacheView c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
             const PageScratch w, unsigned* status) {
-    copy_pairs(c, src, dst, w.count[0], status);
+    grid_dep_wait();
+    copy_pairs(c, [&](int k) { return __ldg(src + k); }, [&](int k) { return __ldg(dst + k); }, __ldcg(w.count), status);
 }
 
 namespace {
@@ -467,6 +542,23 @@ int64_t page_chunks(const CacheView& c) {
 
 int64_t blocks_for(int64_t n, int threads) { return (n + threads - 1) / threads; }
 
+// Launches a kernel whose blocks may start before the one ahead of it on the stream is
+// complete (they wait for that themselves).
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int grid, cudaStream_t s, Args... args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_alloc(const CacheView& c, int32_t* table, const int32_t* lens, int B,
@@ -481,10 +573,10 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
                               int max_pages, const PageScratch& w, unsigned* status, cudaStream_t s) {
     fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(c, table, lens, parents, B, n, max_pages, w, status);
     const int64_t most = n * page_chunks(c) + blocks_for(int64_t(n) * max_pages, kCopyThreads);
-    fork_kernel<<<copy_grid(most), kCopyThreads, 0, s>>>(c, table, lens, parents, child_table, B, n, max_pages,
-                                                         w, status);
-    note_launch(2);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    note_launch();
+    return launch_early(fork_kernel, copy_grid(most), s, c, table, lens, parents, child_table, B, n, max_pages, w, status);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t* rows, int B, int n,
@@ -498,22 +590,22 @@ cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t*
 cudaError_t launch_cache_compact(const CacheView& c, const int32_t* table, int32_t* new_table,
                                  int32_t* new_refcount, int B, int max_pages, const PageScratch& w,
                                  unsigned* status, cudaStream_t s) {
-    compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(c, w);
+    compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(c, w, status);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    note_launch();
     const int64_t most = c.num_pages / 2 * page_chunks(c) + 1;
-    compact_kernel<<<copy_grid(most), kCopyThreads, 0, s>>>(c, table, new_table, new_refcount, B, max_pages, w,
-                                                            status);
-    note_launch(2);
-    return cudaGetLastError();
+    return launch_early(compact_kernel, copy_grid(most), s, c, table, new_table, new_refcount, B, max_pages, w, status);
 }
 
 cudaError_t launch_cache_copy(const CacheView& c, const int32_t* src, const int32_t* dst, int n,
                               const PageScratch& w, unsigned* status, cudaStream_t s) {
-    const cudaError_t e = cudaMemsetAsync(w.map, 0, size_t(c.num_pages) * 4, s);
+    cudaError_t e = cudaMemsetAsync(w.map, 0, size_t(c.num_pages) * 4, s);
     if (e != cudaSuccess) return e;
     copy_check_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(c, src, dst, n, w, status);
-    copy_kernel<<<copy_grid(n * page_chunks(c)), kCopyThreads, 0, s>>>(c, src, dst, w, status);
-    note_launch(2);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    note_launch();
+    return launch_early(copy_kernel, copy_grid(n * page_chunks(c)), s, c, src, dst, w, status);
 }
 
 }  // namespace smla

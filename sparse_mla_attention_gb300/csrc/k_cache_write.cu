@@ -49,11 +49,15 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
     __shared__ uint32_t warp_max[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t slot = blockIdx.x;
-    // the last b with cu[b] / kBlock + 2b <= slot
+    // the last b with cu[b] / kBlock + 2b <= slot, 32 probes at a time: a halving search is a
+    // chain of loads, and a call for one token a sequence is little else
     int b = 0, above = B;
     while (above - b > 1) {
-        const int mid = b + (above - b) / 2;
-        if (int64_t(__ldg(cu + mid) / kBlock) + 2 * int64_t(mid) <= slot) b = mid; else above = mid;
+        const int step = (above - b + 31) / 32, mid = b + lane * step;
+        const bool yes = mid < above &&
+                         (lane == 0 || int64_t(__ldg(cu + mid) / kBlock) + 2 * int64_t(mid) <= slot);
+        b += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
+        above = min(above, b + step);
     }
     const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1), st = __ldg(start + b);
     const int64_t j = slot - (int64_t(c0 / kBlock) + 2 * int64_t(b));
@@ -68,16 +72,9 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
     if (hi <= lo) return;
     const int64_t pslot = p0 >> c.page_shift;
     const int page = pslot < max_pages ? __ldg(table + int64_t(b) * max_pages + pslot) : -1;
-    if (page < 0 || page >= c.num_pages) {
-        if (threadIdx.x == 0) flag_status(status, SMLA_ERR_INDEX);
-        return;
-    }
-    const int64_t row0 = (int64_t(page) << c.page_shift) + (p0 & ((1 << c.page_shift) - 1));
-    float* scale_at = c.scales + (row0 >> c.block_shift);
-    const float old = lo > 0 ? *scale_at : 0.f;
     const uint4* src = rows + (int64_t(c0) + (p0 - st)) * (kD / 8);  // row 0 of the block
 
-    uint4 v[4][2];
+    uint4 v[4][2];                               // (on their way while the page is looked up)
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -87,6 +84,13 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
             v[i][k] = r >= lo && r < hi ? __ldcs(src + int64_t(r) * (kD / 8) + 32 * k + lane)
                                         : make_uint4(0, 0, 0, 0);
     }
+    if (page < 0 || page >= c.num_pages) {
+        if (threadIdx.x == 0) flag_status(status, SMLA_ERR_INDEX);
+        return;
+    }
+    const int64_t row0 = (int64_t(page) << c.page_shift) + (p0 & ((1 << c.page_shift) - 1));
+    float* scale_at = c.scales + (row0 >> c.block_shift);
+    const float old = lo > 0 ? *scale_at : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -47,7 +47,7 @@ size_t scale_bytes(const smla_cache& c) {
 size_t count_bytes(const smla_cache& c) { return c.refcount ? size_t(c.num_pages) * 4 : 0; }
 
 struct ScratchPlan {
-    size_t need, src, dst, map, bytes;
+    size_t need, tail, src, dst, map, bytes;
 };
 
 ScratchPlan plan_pages(const smla_cache& c, int64_t n) {
@@ -56,6 +56,7 @@ ScratchPlan plan_pages(const smla_cache& c, int64_t n) {
     auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes > 0 ? bytes : 1, 256); return o; };
     const size_t list = size_t(n > c.num_pages ? n : c.num_pages) * 4;
     p.need = take(size_t(n) * 4);
+    p.tail = take(size_t(n) * 4);
     p.src = take(list);
     p.dst = take(list);
     p.map = take(size_t(c.num_pages) * 4);
@@ -65,7 +66,7 @@ ScratchPlan plan_pages(const smla_cache& c, int64_t n) {
 
 PageScratch carve(char* ws, const ScratchPlan& p) {
     return PageScratch{reinterpret_cast<int32_t*>(ws + kStatusBytes), reinterpret_cast<int32_t*>(ws + p.need),
-                       reinterpret_cast<int32_t*>(ws + p.src), reinterpret_cast<int32_t*>(ws + p.dst),
+                       reinterpret_cast<int32_t*>(ws + p.tail), reinterpret_cast<int32_t*>(ws + p.src), reinterpret_cast<int32_t*>(ws + p.dst),
                        reinterpret_cast<int32_t*>(ws + p.map)};
 }
 
@@ -189,8 +190,8 @@ int smla_cache_alloc(const smla_cache* cache, int32_t* table, const int32_t* len
                          {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 3, ins, 3))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 6, workspace, s))) return rc;
-    if (B == 0) return SMLA_OK;
+    if (B == 0) return begin(ptrs, 6, workspace, s);
+    if ((rc = check_device(ptrs, 6))) return rc;         // (the kernel writes the status word)
     return cuda_rc(launch_cache_alloc(view(c), table, lens, B, max_pages,
                                       carve(static_cast<char*>(workspace), plan),
                                       static_cast<unsigned*>(workspace), s));
@@ -216,8 +217,8 @@ int smla_cache_fork(const smla_cache* cache, const int32_t* table, const int32_t
                          {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 5, ins, 3))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 8, workspace, s))) return rc;
-    if (n == 0) return SMLA_OK;
+    if (n == 0) return begin(ptrs, 8, workspace, s);
+    if ((rc = check_device(ptrs, 8))) return rc;
     return cuda_rc(launch_cache_fork(view(c), table, lens, parents, child_table, B, n, max_pages,
                                      carve(static_cast<char*>(workspace), plan),
                                      static_cast<unsigned*>(workspace), s));
@@ -264,7 +265,7 @@ int smla_cache_compact(const smla_cache* cache, const int32_t* table, int32_t* n
                          {c.pages, page_bytes(c)}, {c.scales, scale_bytes(c)}, {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 5, ins, 2))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 7, workspace, s))) return rc;
+    if ((rc = check_device(ptrs, 7))) return rc;
     return cuda_rc(launch_cache_compact(view(c), table, new_table, new_refcount, B, max_pages,
                                         carve(static_cast<char*>(workspace), plan),
                                         static_cast<unsigned*>(workspace), s));
@@ -285,8 +286,8 @@ int smla_cache_copy_pages(const smla_cache* cache, const int32_t* src, const int
     const Span outs[] = {{c.pages, page_bytes(c)}, {c.scales, scale_bytes(c)}, {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 3, ins, 2))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 5, workspace, s))) return rc;
-    if (n == 0) return SMLA_OK;
+    if (n == 0) return begin(ptrs, 5, workspace, s);
+    if ((rc = check_device(ptrs, 5))) return rc;
     return cuda_rc(launch_cache_copy(view(c), src, dst, n, carve(static_cast<char*>(workspace), plan),
                                      static_cast<unsigned*>(workspace), s));
 }

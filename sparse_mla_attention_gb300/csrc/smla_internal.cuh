@@ -198,10 +198,11 @@ cudaError_t launch_cache_write(const CacheView& c, const int32_t* table, const i
 // Scratch of the page operations, carved from the workspace behind the status word.
 struct PageScratch {
     int32_t* count;      // [1] pairs to copy
-    int32_t* need;       // [n] pages that row i needs, then their exclusive sum
+    int32_t* need;       // [n] pages that row i needs / place of its copy in the lists
+    int32_t* tail;       // [n] page that child i copies
     int32_t* src;        // [max(n, num_pages)] pages to copy from
     int32_t* dst;        // [max(n, num_pages)] pages to copy to / free pages in order
-    int32_t* map;        // [num_pages] new number of a moved page / marks
+    int32_t* map;        // [num_pages] place of a moved page in its list / marks
 };
 cudaError_t launch_cache_alloc(const CacheView& c, int32_t* table, const int32_t* lens, int B,
                                int max_pages, const PageScratch& w, unsigned* status, cudaStream_t s);

@@ -296,7 +296,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
     if (warp == kPgMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
     grid_dep_wait();                             // what ran before is complete: nothing global was touched yet
-    grid_dep_launch();
     pg_locate(p, sh, unsigned(cta), unsigned(ctas));
     tc_fence_before();
     __syncthreads();
@@ -969,13 +968,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 }
 
 // Joins the parts of a token that several CTAs shared, in their order. Block (c, y): the
-// token that ends in CTA c, heads 4y .. 4y + 3 of its group; a thread has two columns of
-// all four. (16 heads a block: 23.2 against 19.6 us a pass for one token of 13 parts and 64
-// heads, 79.4 against 78.9 for 128 tokens of two or three.) Block (0, 0) also joins the
-// CTAs' status bits.
-__global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
+// token that ends in CTA c, heads 4y .. 4y + 3 of its group; a thread has 512 / kThreads
+// columns of all four. Block (0, 0) also joins the CTAs' status bits.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams p) {
+    constexpr int kWarps = kThreads / 32, kCols = kD / kThreads;
+    constexpr int kRounds = (kPgMaxCtas + kThreads / 4 - 1) / (kThreads / 4);
     __shared__ float4 wgt[kPgMaxCtas];
-    __shared__ float red[2][8];
+    __shared__ float red[2][kWarps];
     __shared__ float4 inv_of;
     grid_dep_wait();
     grid_dep_launch();
@@ -994,15 +994,14 @@ __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
     auto part_of = [&](int i) {
         return (int64_t(end.y + i) * p.groups + group) * 2 + (i == 0 ? end.z : 0);
     };
-    // weights: two warps a head
-    constexpr int kRounds = (kPgMaxCtas + 63) / 64;
-    const int k = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    // weights: a quarter of the threads a head
+    const int k = threadIdx.x / (kThreads / 4), lane = threadIdx.x % (kThreads / 4);
     const float sink = p.sink ? __ldg(p.sink + head0 + k) * kPgLog2e : -INFINITY;
     float2 ml[kRounds];
     float top = sink;
 #pragma unroll
     for (int j = 0; j < kRounds; ++j) {
-        const int i = lane + 64 * j;
+        const int i = lane + kThreads / 4 * j;
         ml[j] = i < n ? __ldcg(p.part_ml + part_of(i) * p.group_heads + h0 + k) : make_float2(-INFINITY, 0.f);
         if (ml[j].y != 0.f) top = fmaxf(top, ml[j].x);
     }
@@ -1010,12 +1009,13 @@ __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = top;
     __syncthreads();
-    top = fmaxf(red[0][2 * k], red[0][2 * k + 1]);
+#pragma unroll
+    for (int j = 0; j < kWarps / 4; ++j) top = fmaxf(top, red[0][kWarps / 4 * k + j]);
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < kRounds; ++j) {
-        const int i = lane + 64 * j;
+        const int i = lane + kThreads / 4 * j;
         const float w = ml[j].y == 0.f ? 0.f : ex2_approx(ml[j].x - base);
         if (i < n) reinterpret_cast<float*>(wgt + i)[k] = w;
         sum += w * ml[j].y;
@@ -1025,36 +1025,42 @@ __global__ void __launch_bounds__(256) combine_paged_kernel(const PgParams p) {
     if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = sum;
     __syncthreads();
     if (lane == 0) {
-        sum = red[1][2 * k] + red[1][2 * k + 1] + (p.sink ? ex2_approx(sink - base) : 0.f);
+        sum = p.sink ? ex2_approx(sink - base) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kWarps / 4; ++j) sum += red[1][kWarps / 4 * k + j];
         reinterpret_cast<float*>(&inv_of)[k] = sum == 0.f ? 0.f : 1.f / sum;
         p.lse[int64_t(end.x) * p.H + head0 + k] = sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
     }
     __syncthreads();
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float4 acc[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int64_t size = int64_t(p.group_heads / 4) * kD;        // float4s of a part
     const float4* src = reinterpret_cast<const float4*>(p.part_o) + (h0 / 4) * kD + threadIdx.x;
     auto add = [&](const float4* at, int i) {
-        const float4 v[2] = {__ldcg(at), __ldcg(at + 256)}, w = wgt[i];
+        const float4 w = wgt[i];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            acc[j].x = fmaf(w.x, v[j].x, acc[j].x);
-            acc[j].y = fmaf(w.y, v[j].y, acc[j].y);
-            acc[j].z = fmaf(w.z, v[j].z, acc[j].z);
-            acc[j].w = fmaf(w.w, v[j].w, acc[j].w);
+        for (int j = 0; j < kCols; ++j) {
+            const float4 v = __ldcg(at + kThreads * j);
+            acc[j].x = fmaf(w.x, v.x, acc[j].x);
+            acc[j].y = fmaf(w.y, v.y, acc[j].y);
+            acc[j].z = fmaf(w.z, v.z, acc[j].z);
+            acc[j].w = fmaf(w.w, v.w, acc[j].w);
         }
     };
     add(src + part_of(0) * size, 0);
     const float4* rest = src + part_of(1) * size;
-#pragma unroll 4
+#pragma unroll (8 / kCols)
     for (int i = 1; i < n; ++i) add(rest + (i - 1) * 2 * p.groups * size, i);
     const float4 f = inv_of;
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (int64_t(end.x) * p.H + head0) * kD + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        dst[256 * j] = __float2bfloat16_rn(acc[j].x * f.x);
-        dst[256 * j + kD] = __float2bfloat16_rn(acc[j].y * f.y);
-        dst[256 * j + 2 * kD] = __float2bfloat16_rn(acc[j].z * f.z);
-        dst[256 * j + 3 * kD] = __float2bfloat16_rn(acc[j].w * f.w);
+    for (int j = 0; j < kCols; ++j) {
+        __nv_bfloat16* to = dst + kThreads * j;
+        to[0] = __float2bfloat16_rn(acc[j].x * f.x);
+        to[kD] = __float2bfloat16_rn(acc[j].y * f.y);
+        to[2 * kD] = __float2bfloat16_rn(acc[j].z * f.z);
+        to[3 * kD] = __float2bfloat16_rn(acc[j].w * f.w);
     }
 }
 
@@ -1125,10 +1131,14 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, fwd_paged_kernel, mq, mb, p);
     if (e != cudaSuccess) return e;
+    // Few tokens have many parts each: a thread a column (three tokens of 25 parts, 128 heads: 65.5 us a
+    // pass, with 256 threads 70.8). Many have two or three: fewer threads, so that most blocks are
+    // on the GPU at once (128 tokens, 64 heads: 75.6 us with 128 threads, 77.4 with 256, 82.6 with 512).
+    const bool few = a.T < 32;
     cfg.gridDim = dim3(ctas * plan.groups, plan.group_heads / 4);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(few ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, combine_paged_kernel, p);
+    e = few ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<512>, p) : cudaLaunchKernelEx(&cfg, combine_paged_kernel<128>, p);
     if (e != cudaSuccess) return e;
     note_launch(2);
     return cudaGetLastError();

@@ -24,6 +24,7 @@ from .api import D_HEAD, Workspace, _need, device_status
 # microseconds: checks and marshalling are kept to a few attribute reads a tensor.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _check(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> int:
@@ -68,8 +69,9 @@ class PagedCache:
                             refcount=refcount.data_ptr(), num_pages=n, page_size=ps,
                             scale_block=self.scale_block, D=d)
         self._ref = ctypes.byref(self._c)
+        self._lib = _lib.load()
         size = ctypes.c_size_t(0)
-        _lib.check(_lib.load().smla_cache_workspace_size(self._ref, 0, ctypes.byref(size)), "PagedCache")
+        _lib.check(self._lib.smla_cache_workspace_size(self._ref, 0, ctypes.byref(size)), "PagedCache")
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int = 64, scale_block: int = 64, device=None) -> "PagedCache":
@@ -114,9 +116,9 @@ def _paged_size(dims: SmlaPagedDims) -> int:
 
 def _run(cache: PagedCache, where: str, ws: torch.Tensor, check_status: bool, *args) -> None:
     """Calls library function `where` with args, the workspace and the cache's device's stream."""
-    fn = getattr(_lib.load(), where)
+    fn = getattr(cache._lib, where)
     tail = (ws.data_ptr(), ws.numel(), _raw_stream(cache._index))
-    if torch.cuda.current_device() == cache._index:
+    if _current_device() == cache._index:
         code = fn(*args, *tail)
     else:
         with torch.cuda.device(cache._index):

@@ -145,6 +145,15 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int x, int
                  : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16, both addresses too) into smem, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // 2-D tiled store of one box from smem to global at (x, y). Tracked by the
 // issuing thread's bulk groups.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y, const void* src) {

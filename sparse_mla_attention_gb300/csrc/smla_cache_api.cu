@@ -159,8 +159,8 @@ int smla_cache_write(const smla_cache* cache, const int32_t* table, const int32_
     const Span outs[] = {{c.pages, page_bytes(c)}, {c.scales, scale_bytes(c)}, {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 3, ins, 4))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 7, workspace, s))) return rc;
-    if (!any) return SMLA_OK;
+    if (!any) return begin(ptrs, 7, workspace, s);
+    if ((rc = check_device(ptrs, 7))) return rc;         // (the kernel writes the status word)
     return cuda_rc(launch_cache_write(view(c), table, start, cu, rows, B, max_pages, n_rows,
                                       static_cast<unsigned*>(workspace), s));
 }
@@ -241,8 +241,8 @@ int smla_cache_free(const smla_cache* cache, int32_t* table, const int32_t* rows
                          {workspace, workspace_bytes}};
     if ((rc = check_overlap(outs, 3, ins, 3))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rc = begin(ptrs, 6, workspace, s))) return rc;
-    if (n == 0) return SMLA_OK;
+    if (n == 0) return begin(ptrs, 6, workspace, s);
+    if ((rc = check_device(ptrs, 6))) return rc;         // (the launch sees to the status word)
     return cuda_rc(launch_cache_free(view(c), table, rows, B, n, max_pages,
                                      static_cast<unsigned*>(workspace), s));
 }

@@ -28,8 +28,11 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kFreeEach = 4;                                   // entries of a thread of a small free
 constexpr int kFreeFew = kPlanCtas * kPlanThreads * kFreeEach;
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;                                   // 16-byte pieces a thread has in flight
-constexpr int kCopyChunk = kCopyThreads * kCopyVecs * 16;      // 16 KB
+constexpr int kEntryThreads = kCopyThreads - 32;               // all but the copying warp
+constexpr int kCopySlots = 6, kCopyLag = 3;
+constexpr int kCopyBytes = 32768;                              // of a slot
+constexpr int kCopySmem = kCopySlots * kCopyBytes;
+constexpr uint64_t kCopyWaitNs = 2000000000u;
 
 struct PlanShared {
     int warp[2][kPlanWarps];    // a scan's sums by warp; two sets in turn
@@ -159,46 +162,82 @@ __device__ __forceinline__ int clamp_len(int len, int64_t limit, unsigned& bits)
     return len < 0 ? 0 : int(limit);
 }
 
-// Copies 16 KB pieces of the pages in pairs (src(k), dst(k)), k < m, over the grid.
+struct CopyShared {
+    uint64_t full[kCopySlots];
+    int to[kCopySlots][kCopyBytes / (16 * kD)];
+};
+
+// Copies the pages in pairs (src(k), dst(k)), k < m, over the grid: warp 0 moves the rows, 32 KB of a
+// page or several small pages at a time, by bulk copies through a ring of six slots in shared
+// memory (three loads and three stores in flight: no register holds a byte, and one CTA an SM
+// keeps HBM busy), the other warps the scales.
 template <class Src, class Dst>
-__device__ void copy_pairs(const CacheView& c, Src src, Dst dst, int m, unsigned* status) {
-    const int64_t page_bytes = int64_t(kD) << c.page_shift;
-    const int chunks = int((page_bytes + kCopyChunk - 1) / kCopyChunk);
+__device__ void copy_pairs(const CacheView& c, uint8_t* ring, CopyShared& sh, Src src, Dst dst, int m,
+                           unsigned* status) {
     const int nscale = 1 << (c.page_shift - c.block_shift);
-    // (the next piece's page numbers are read ahead)
-    const int64_t all = int64_t(m) * chunks;
-    int a1 = -1, b1 = -1;
-    if (blockIdx.x < all) {
-        a1 = src(int(blockIdx.x / chunks));
-        b1 = dst(int(blockIdx.x / chunks));
+    if (threadIdx.x >= 32) {
+        const int64_t threads = int64_t(gridDim.x) * kEntryThreads;
+        for (int64_t x = int64_t(blockIdx.x) * kEntryThreads + threadIdx.x - 32; x < int64_t(m) * nscale; x += threads) {
+            const int k = int(x / nscale), i = int(x - int64_t(k) * nscale), a = src(k), b = dst(k);
+            if (a >= 0 && a < c.num_pages && b >= 0 && b < c.num_pages)
+                c.scales[int64_t(b) * nscale + i] = c.scales[int64_t(a) * nscale + i];
+        }
+        return;
     }
-    for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
-        const int ch = int(w % chunks), a = a1, b = b1;
-        if (w + gridDim.x < all) {
-            a1 = src(int((w + gridDim.x) / chunks));
-            b1 = dst(int((w + gridDim.x) / chunks));
-        }
-        if (a < 0 || a >= c.num_pages || b < 0 || b >= c.num_pages) {
-            if (threadIdx.x == 0) flag_status(status, SMLA_ERR_INDEX);
-            continue;
-        }
-        const uint4* from = reinterpret_cast<const uint4*>(c.pages + a * page_bytes) + ch * (kCopyChunk / 16);
-        uint4* to = reinterpret_cast<uint4*>(c.pages + b * page_bytes) + ch * (kCopyChunk / 16);
-        const int n = int((page_bytes - int64_t(ch) * kCopyChunk) / 16);
-        uint4 v[kCopyVecs];
-#pragma unroll
-        for (int i = 0; i < kCopyVecs; ++i) {
-            const int x = i * kCopyThreads + threadIdx.x;
-            if (x < n) v[i] = __ldcs(from + x);
-        }
-#pragma unroll
-        for (int i = 0; i < kCopyVecs; ++i) {
-            const int x = i * kCopyThreads + threadIdx.x;
-            if (x < n) __stcs(to + x, v[i]);
-        }
-        if (ch == 0 && threadIdx.x < nscale)
-            c.scales[int64_t(b) * nscale + threadIdx.x] = c.scales[int64_t(a) * nscale + threadIdx.x];
+    const int lane = threadIdx.x;
+    const int64_t page_bytes = int64_t(kD) << c.page_shift;
+    const int piece = int(page_bytes < kCopyBytes ? page_bytes : kCopyBytes);
+    const int per = kCopyBytes / piece;                        // pages of a slot: a lane each
+    const int parts = int(page_bytes / piece);                 // slots of a page, a power of two
+    const int shift = __ffs(parts) - 1;
+    const int64_t units = per > 1 ? (int64_t(m) + per - 1) / per : int64_t(m) * parts;
+    const int mine = units > blockIdx.x ? int((units - blockIdx.x - 1) / gridDim.x) + 1 : 0;
+    if (lane == 0) {
+        for (int i = 0; i < kCopySlots; ++i) mbar_init(&sh.full[i], 1);
+        fence_mbar_init();
     }
+    __syncwarp();
+    int a1, b1;                                  // the lane's pair in the next unit, read ahead
+    auto look = [&](int i) {
+        const int64_t u = blockIdx.x + int64_t(i) * gridDim.x, k = per > 1 ? u * per + lane : u >> shift;
+        a1 = b1 = -1;
+        if (i >= mine || lane >= per || k >= m) return;
+        a1 = src(int(k));
+        b1 = dst(int(k));
+        if (a1 < 0 || a1 >= c.num_pages || b1 < 0 || b1 >= c.num_pages) {
+            flag_status(status, SMLA_ERR_INDEX);
+            a1 = b1 = -1;
+        }
+    };
+    auto at = [&](int page, int i) {
+        return c.pages + page * page_bytes + ((blockIdx.x + int64_t(i) * gridDim.x) & (parts - 1)) * kCopyBytes;
+    };
+    look(0);
+#pragma unroll 1
+    for (int i = 0; i < mine + kCopyLag; ++i) {
+        if (i < mine) {
+            const int slot = i % kCopySlots, a = a1;
+            // the slot's store (each lane's own, six units before) has read it
+            if (i >= kCopySlots) bulk_wait_read<kCopySlots - kCopyLag - 1>();
+            const int lanes = __popc(__ballot_sync(0xffffffffu, a >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], uint32_t(lanes) * piece);
+            __syncwarp();
+            if (a >= 0) bulk_load(ring + slot * kCopyBytes + lane * piece, at(a, i), piece, &sh.full[slot]);
+            if (lane < per) sh.to[slot][lane] = b1;
+            look(i + 1);
+        }
+        if (i >= kCopyLag) {
+            const int j = i - kCopyLag, slot = j % kCopySlots;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[slot], uint32_t(j / kCopySlots) & 1u, kCopyWaitNs))) {
+                flag_status(status, SMLA_ERR_TIMEOUT);
+                break;
+            }
+            const int b = lane < per ? sh.to[slot][lane] : -1;
+            if (b >= 0) bulk_store(at(b, j), ring + slot * kCopyBytes + lane * piece, piece);
+            bulk_commit();
+        }
+    }
+    bulk_wait_all();
 }
 
 }  // namespace
@@ -344,11 +383,14 @@ __global__ void __launch_bounds__(kCopyThreads)
 fork_kernel(const CacheView c, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
             const int32_t* __restrict__ parents, int32_t* __restrict__ child, int B, int n, int max_pages,
             const PageScratch w, unsigned* status) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ CopyShared sh;
     grid_dep_wait();
     const int m = __ldcg(w.count);
     const int64_t limit = int64_t(max_pages) << c.page_shift;
-    const int64_t threads = int64_t(gridDim.x) * kCopyThreads;
-    for (int64_t x = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x; x < int64_t(n) * max_pages; x += threads) {
+    const int64_t threads = int64_t(gridDim.x) * kEntryThreads;
+    const int64_t first = int64_t(blockIdx.x) * kEntryThreads + threadIdx.x - 32;
+    for (int64_t x = threadIdx.x < 32 ? int64_t(n) * max_pages : first; x < int64_t(n) * max_pages; x += threads) {
         const int i = int(x / max_pages), j = int(x - int64_t(i) * max_pages);
         const int p = __ldg(parents + i);
         int e = -1;
@@ -374,7 +416,8 @@ fork_kernel(const CacheView c, const int32_t* __restrict__ table, const int32_t*
         child[x] = e;
     }
     if (m > 0)
-        copy_pairs(c, [&](int k) { return __ldcg(w.src + k); }, [&](int k) { return __ldcg(w.dst + k); }, m, status);
+        copy_pairs(c, ring, sh, [&](int k) { return __ldcg(w.src + k); }, [&](int k) { return __ldcg(w.dst + k); }, m,
+                   status);
     // the new pages are counted by the last CTA, when no other looks at counts any more
     __shared__ int last;
     __syncthreads();
@@ -503,13 +546,16 @@ __global__ void __launch_bounds__(kCopyThreads)
 compact_kernel(const CacheView c, const int32_t* __restrict__ table, int32_t* __restrict__ new_table,
                int32_t* __restrict__ new_refcount, int B, int max_pages, const PageScratch w,
                unsigned* status) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ CopyShared sh;
     grid_dep_wait();
     const int m = __ldcg(w.count), live = __ldcg(w.count + 1);
-    const int64_t first = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x;
-    const int64_t threads = int64_t(gridDim.x) * kCopyThreads;
     // the k-th page that moves goes to the k-th hole; the list is in reverse order
     auto src = [&](int k) { return __ldcg(w.src + (m - 1 - k)); };
     auto dst = [&](int k) { return __ldcg(w.dst + k); };
+    const int64_t threads = int64_t(gridDim.x) * kEntryThreads;
+    const int64_t first = threadIdx.x < 32 ? INT64_MAX - threads      // (the copying warp has no entries)
+                                           : int64_t(blockIdx.x) * kEntryThreads + threadIdx.x - 32;
     for (int64_t x = first; x < int64_t(B) * max_pages; x += threads) {
         int e = __ldg(table + x);
         if (e != -1) {
@@ -531,7 +577,7 @@ compact_kernel(const CacheView c, const int32_t* __restrict__ table, int32_t* __
         else if (rc > 0) new_refcount[i] = rc;              // a hole's count comes with its page, below
     }
     for (int64_t k = first; k < m; k += threads) new_refcount[dst(int(k))] = __ldg(c.refcount + src(int(k)));
-    copy_pairs(c, src, dst, m, status);
+    copy_pairs(c, ring, sh, src, dst, m, status);
 }
 
 // count[0] = n if all dst differ from each other and from every src, else 0.
@@ -569,24 +615,29 @@ copy_check_kernel(const CacheView c, const int32_t* __restrict__ src, const int3
 __global__ void __launch_bounds__(kCopyThreads)
 copy_kernel(const CacheView c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
             const PageScratch w, unsigned* status) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ CopyShared sh;
     grid_dep_wait();
-    copy_pairs(c, [&](int k) { return __ldg(src + k); }, [&](int k) { return __ldg(dst + k); }, __ldcg(w.count), status);
+    copy_pairs(c, ring, sh, [&](int k) { return __ldg(src + k); }, [&](int k) { return __ldg(dst + k); },
+               __ldcg(w.count), status);
 }
 
 namespace {
 
-// CTAs of the copying kernels: what the GPU holds at once (8 of 256 threads
-// per SM), or fewer where the call cannot have more work.
-int copy_grid(int64_t most) {
+int sm_count() {
     int dev = 0, sms = 1;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t g = 8 * int64_t(sms);
-    return int(most < 1 ? 1 : most < g ? most : g);
+    return sms;
 }
 
-int64_t page_chunks(const CacheView& c) {
-    return ((int64_t(kD) << c.page_shift) + kCopyChunk - 1) / kCopyChunk;
+// CTAs of a copying kernel: one an SM (its ring takes the shared memory), or fewer where the call
+// cannot have more work.
+int copy_grid(const CacheView& c, int64_t pages, int64_t entries) {
+    const int64_t bytes = pages * (int64_t(kD) << c.page_shift);
+    const int64_t a = (bytes + kCopyBytes - 1) / kCopyBytes, b = (entries + kEntryThreads - 1) / kEntryThreads;
+    const int64_t most = a > b ? a : b, g = sm_count();
+    return int(most < 1 ? 1 : most < g ? most : g);
 }
 
 int64_t blocks_for(int64_t n, int threads) { return (n + threads - 1) / threads; }
@@ -594,13 +645,21 @@ int64_t blocks_for(int64_t n, int threads) { return (n + threads - 1) / threads;
 // Launches a kernel whose blocks may start before the one ahead of it on the stream is
 // complete (they wait for that themselves).
 template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), int grid, cudaStream_t s, Args... args) {
+cudaError_t launch_early(void (*kernel)(Params...), bool (&attr_done)[64], int grid, cudaStream_t s, Args... args) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopySmem);
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+    }
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kCopyThreads);
+    cfg.dynamicSmemBytes = kCopySmem;
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
@@ -621,11 +680,11 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
                               const int32_t* parents, int32_t* child_table, int B, int n,
                               int max_pages, const PageScratch& w, unsigned* status, cudaStream_t s) {
     fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(c, table, lens, parents, B, n, max_pages, w, status);
-    const int64_t most = n * page_chunks(c) + blocks_for(int64_t(n) * max_pages, kCopyThreads);
+    static bool attr_done[64] = {false};
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     note_launch();
-    return launch_early(fork_kernel, copy_grid(most), s, c, table, lens, parents, child_table, B, n, max_pages, w, status);
+    return launch_early(fork_kernel, attr_done, copy_grid(c, n, int64_t(n) * max_pages), s, c, table, lens, parents, child_table, B, n, max_pages, w, status);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t* rows, int B, int n,
@@ -640,7 +699,8 @@ cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t*
     }
     const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(unsigned), s);
     if (e != cudaSuccess) return e;
-    const int grid = copy_grid(blocks_for(total, 256));
+    const int64_t most = 8 * int64_t(sm_count()), blocks = blocks_for(total, 256);
+    const int grid = int(blocks < most ? blocks : most);
     free_kernel<<<grid, 256, 0, s>>>(c, table, rows, B, n, max_pages, status);
     note_launch();
     return cudaGetLastError();
@@ -653,8 +713,10 @@ cudaError_t launch_cache_compact(const CacheView& c, const int32_t* table, int32
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     note_launch();
-    const int64_t most = c.num_pages / 2 * page_chunks(c) + 1;
-    return launch_early(compact_kernel, copy_grid(most), s, c, table, new_table, new_refcount, B, max_pages, w, status);
+    static bool attr_done[64] = {false};
+    const int64_t table_entries = int64_t(B) * max_pages;
+    const int grid = copy_grid(c, c.num_pages / 2, table_entries > c.num_pages ? table_entries : c.num_pages);
+    return launch_early(compact_kernel, attr_done, grid, s, c, table, new_table, new_refcount, B, max_pages, w, status);
 }
 
 cudaError_t launch_cache_copy(const CacheView& c, const int32_t* src, const int32_t* dst, int n,
@@ -664,7 +726,8 @@ cudaError_t launch_cache_copy(const CacheView& c, const int32_t* src, const int3
     copy_check_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(c, src, dst, n, w, status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     note_launch();
-    return launch_early(copy_kernel, copy_grid(n * page_chunks(c)), s, c, src, dst, w, status);
+    static bool attr_done[64] = {false};
+    return launch_early(copy_kernel, attr_done, copy_grid(c, n, n), s, c, src, dst, w, status);
 }
 
 }  // namespace smla

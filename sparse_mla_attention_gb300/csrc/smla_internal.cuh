@@ -197,7 +197,7 @@ cudaError_t launch_cache_write(const CacheView& c, const int32_t* table, const i
 
 // Scratch of the page operations, carved from the workspace behind the status word.
 struct PageScratch {
-    int32_t* count;      // [1] pairs to copy
+    int32_t* count;      // [2] pairs to copy; live pages, or the blocks that are done
     int32_t* need;       // [n] pages that row i needs / place of its copy in the lists
     int32_t* tail;       // [n] page that child i copies
     int32_t* src;        // [max(n, num_pages)] pages to copy from

@@ -171,7 +171,7 @@ def sparse_mla_fwd_paged(q: torch.Tensor, cache: PagedCache, table: torch.Tensor
             raise ValueError("sink must have shape [H]")
     if out is None:
         o = torch.empty_like(q)
-        lse = q.new_empty((T, H), dtype=torch.float32)
+        lse = torch.empty((T, H), dtype=torch.float32, device=cache.device)
         p_o, p_lse = o.data_ptr(), lse.data_ptr()
     else:
         o, lse = out

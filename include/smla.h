@@ -279,7 +279,7 @@ typedef struct smla_paged_dims {
     int32_t H;          /* query heads: a multiple of 16, 16..128 */
     int32_t D;          /* must be 512 */
     int32_t topk;       /* ranks per token; 0: every visible position (topk == NULL) */
-    int32_t B;          /* rows of table (sequences) */
+    int32_t B;          /* rows of table (sequences); 0 only with T = 0 */
     int32_t max_pages;  /* columns of table; max_pages * page_size < 2^31, and
                            T * ceil(max_pages * page_size / 64) < 2^31 */
     float scale;        /* score scale: 0 = 1/sqrt(D) */
@@ -368,7 +368,7 @@ int smla_cache_fork(const smla_cache* cache, const int32_t* table, const int32_t
 
 /*
  * Gives back the pages of sequences: for each of the n rows listed in `rows`
- * (all B rows if rows is NULL) every page entry becomes -1 and the page's
+ * (all B rows if rows is NULL and n is B; n = 0: none) every page entry becomes -1 and the page's
  * refcount falls by one. A row listed twice is given back once. A row or page
  * out of range sets SMLA_ERR_INDEX; a refcount that is 0 already stays 0 and
  * sets SMLA_ERR_REFCOUNT. workspace: at least 256 bytes.

@@ -108,7 +108,7 @@ int smla_fwd_paged(const uint16_t* q, const smla_cache* cache, const int32_t* ta
     const smla_cache& c = *cache;
     const smla_paged_dims& d = *dims;
     if (d.D != kD) return SMLA_ERR_D512;
-    if (d.T < 0 || d.topk < 0 || d.H < 16 || d.H > 128 || d.H % 16 != 0 || d.B < 1) return SMLA_ERR_SHAPE;
+    if (d.T < 0 || d.topk < 0 || d.H < 16 || d.H > 128 || d.H % 16 != 0 || (d.T > 0 && d.B < 1)) return SMLA_ERR_SHAPE;
     if ((rc = check_table(c, d.B, d.max_pages))) return rc;
     if (int64_t(d.T) * d.topk > int64_t(INT32_MAX) || (!seq && d.T > d.B)) return SMLA_ERR_SHAPE;
     // tiles of 64 ranks are counted in 32 bits
@@ -231,7 +231,7 @@ int smla_cache_free(const smla_cache* cache, int32_t* table, const int32_t* rows
     if (rc) return rc;
     const smla_cache& c = *cache;
     if ((rc = check_table(c, B, max_pages))) return rc;
-    if (n < 0 || n > kMaxSeqs || (!rows && n != B)) return SMLA_ERR_SHAPE;
+    if (n < 0 || n > kMaxSeqs || (!rows && n != B && n != 0)) return SMLA_ERR_SHAPE;
     if (!c.refcount || !workspace || (n > 0 && B > 0 && !table)) return SMLA_ERR_NULL;
     const void* ptrs[] = {c.pages, c.scales, c.refcount, table, rows, workspace};
     if ((rc = check_align(ptrs, 6))) return rc;

@@ -235,6 +235,27 @@ def test_calls_at_once_on_two_streams():
     pool.check(cache)
 
 
+def test_empty_batches():
+    # a step in which no sequence is left: every call does nothing and reports nothing
+    smla = _smla()
+    pool = Pool(8, 16, 16, seed=20)
+    cache = pool.device()
+    ws = smla.Workspace(DEV)
+    none, table = _i32([]), torch.empty((0, 3), dtype=torch.int32, device=DEV)
+    o, lse = smla.sparse_mla_fwd_paged(torch.empty((0, 32, 512), dtype=torch.bfloat16, device=DEV), cache, table, none,
+                                       workspace=ws)
+    assert o.shape == (0, 32, 512) and lse.shape == (0, 32)
+    smla.cache_alloc(cache, table, none, workspace=ws)
+    smla.cache_write(cache, table, none, _i32([0]), torch.empty((0, 512), dtype=torch.bfloat16, device=DEV),
+                     workspace=ws)
+    assert smla.cache_fork(cache, table, none, none, workspace=ws).shape == (0, 3)
+    smla.cache_free(cache, table, workspace=ws)
+    smla.cache_free(cache, _i32([[0, -1, -1]]), none, workspace=ws)
+    new, count = smla.cache_compact(cache, table, workspace=ws)
+    assert new.shape == (0, 3) and (count == 0).all()
+    pool.check(cache)
+
+
 # ------------------------------------------------------------------------------------------------ refusals
 def test_tensors_that_a_call_cannot_take():
     smla = _smla()

@@ -65,7 +65,8 @@ enum smla_status {
     SMLA_ERR_WORKSPACE = 8,     /* workspace NULL or smaller than smla_workspace_size() */
     SMLA_ERR_ARCH = 9,          /* current device is not compute capability 10.3 (sm_103) */
     SMLA_ERR_CUDA = 10,         /* a CUDA runtime call failed */
-    SMLA_ERR_INDEX = 11,        /* device: a topk entry outside [-1, num_kv) was seen */
+    SMLA_ERR_INDEX = 11,        /* device: a topk entry outside [-1, num_kv) was seen; paged
+                                   cache: a position, length, row or page out of range */
     SMLA_ERR_TIMEOUT = 12,      /* device: a bounded wait inside a kernel ran out */
     SMLA_ERR_SINK = 13,         /* d_sink given without sink, or sink without d_sink */
     SMLA_ERR_ARG = 14,          /* any other invalid argument (e.g. a non-finite scale) */

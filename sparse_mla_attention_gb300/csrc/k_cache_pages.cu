@@ -233,6 +233,8 @@ __device__ void copy_pairs(const CacheView& c, uint8_t* ring, CopyShared& sh, Sr
             const int j = i - kCopyLag, slot = j % kCopySlots;
             if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[slot], uint32_t(j / kCopySlots) & 1u, kCopyWaitNs))) {
                 flag_status(status, SMLA_ERR_TIMEOUT);
+                for (int k = j + 1; k <= i && k < mine; ++k)       // loads already issued land before the CTA exits
+                    mbar_wait(&sh.full[k % kCopySlots], uint32_t(k / kCopySlots) & 1u, kCopyWaitNs / 8);
                 break;
             }
             const int b = lane < per ? sh.to[slot][lane] : -1;
@@ -687,7 +689,8 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     note_launch();
-    return launch_early(fork_kernel, attr_done, copy_grid(c, n, int64_t(n) * max_pages), s, c, table, lens, parents, child_table, B, n, max_pages, w, status);
+    return launch_early(fork_kernel, attr_done, copy_grid(c, n, int64_t(n) * max_pages), s, c, table, lens, parents,
+                        child_table, B, n, max_pages, w, status);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t* rows, int B, int n,

@@ -1160,7 +1160,8 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     cfg.gridDim = dim3(ctas * plan.groups, plan.group_heads / 4);
     cfg.blockDim = dim3(few ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
-    e = few ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<512>, p) : cudaLaunchKernelEx(&cfg, combine_paged_kernel<128>, p);
+    e = few ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<512>, p)
+            : cudaLaunchKernelEx(&cfg, combine_paged_kernel<128>, p);
     if (e != cudaSuccess) return e;
     note_launch(2);
     return cudaGetLastError();

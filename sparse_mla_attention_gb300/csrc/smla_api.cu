@@ -473,7 +473,7 @@ const char* smla_status_string(int code) {
         case SMLA_ERR_WORKSPACE: return "workspace missing or smaller than smla_workspace_size()";
         case SMLA_ERR_ARCH: return "the current device is not compute capability 10.3 (sm_103)";
         case SMLA_ERR_CUDA: return "a CUDA runtime call failed";
-        case SMLA_ERR_INDEX: return "a topk index outside [-1, num_kv) was seen (treated as masked)";
+        case SMLA_ERR_INDEX: return "a topk index outside [-1, num_kv), or a position, length, row or page number out of range, was seen (treated as masked or left out)";
         case SMLA_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
         case SMLA_ERR_SINK: return "d_sink must be given exactly when sink is given";
         case SMLA_ERR_ARG: return "invalid argument (scale must be finite and >= 0)";

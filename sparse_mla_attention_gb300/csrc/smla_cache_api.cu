@@ -65,9 +65,8 @@ ScratchPlan plan_pages(const smla_cache& c, int64_t n) {
 }
 
 PageScratch carve(char* ws, const ScratchPlan& p) {
-    return PageScratch{reinterpret_cast<int32_t*>(ws + kStatusBytes), reinterpret_cast<int32_t*>(ws + p.need),
-                       reinterpret_cast<int32_t*>(ws + p.tail), reinterpret_cast<int32_t*>(ws + p.src), reinterpret_cast<int32_t*>(ws + p.dst),
-                       reinterpret_cast<int32_t*>(ws + p.map)};
+    auto at = [ws](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+    return PageScratch{at(kStatusBytes), at(p.need), at(p.tail), at(p.src), at(p.dst), at(p.map)};
 }
 
 int check_align(const void* const* ptrs, int n) {

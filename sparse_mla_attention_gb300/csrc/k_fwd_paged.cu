@@ -44,7 +44,8 @@
 // 16 of 38 for S: they read the tile at shared memory's rate), reading 32 KB at the SM's share of
 // HBM ~1500; a team has two tiles' time for a chain of loads, swaps, exponentials and
 // conversions. No unit is full (profiled: DRAM and issue slots 48% of the time, tensor pipe
-// 43%); the start, the ends of items and the join are the rest. 16 heads are bound by the loads.
+// 43%; half of the O products would save 5%); the start, the ends of items and the join are
+// the rest. 16 heads are bound by the loads.
 // Measured (one GB300, device time of a call with its join, in a graph):
 //   128 sequences of up to 5120 positions, 64 heads: 75.6 us, 3.6 TB/s of cache, 0.86 PFLOP/s
 //   96 of up to 6001, 16 heads: 55 us, 4.1 TB/s;  3 of 81920, 128 heads: 65.5 us, 0.89 PFLOP/s

@@ -295,8 +295,9 @@ typedef struct smla_paged_dims {
  * every visible position:
  *   s_r = scale * <q[t,h,:], x_r>,  x_r the cache row as code * block scale
  *   lse[t,h] = log(exp(sink[h]) + sum_r exp(s_r)),  o[t,h,:] = sum_r exp(s_r - lse) x_r
- * A token with no valid rank (lens[t] = 0: a padded slot of the batch) gets
- * o = 0 and lse = sink[h] (or -inf without a sink). Cache rows that no valid
+ * A token with no valid rank gets o = 0 and lse = sink[h] (or -inf without a
+ * sink); with lens[t] = 0 (a padded slot of the batch) its seq and picks are
+ * not looked at. Cache rows that no valid
  * rank names are not used, whatever bytes they hold.
  *   q [T,H,512] bf16, lens [T], seq [T] or NULL, topk [T,topk] or NULL int32,
  *   sink [H] fp32 (finite or -inf) or NULL -> o [T,H,512] bf16 (RNE), lse [T,H] fp32.

@@ -142,8 +142,8 @@ def sparse_mla_fwd_paged(q: torch.Tensor, cache: PagedCache, table: torch.Tensor
     q [T,H,512] bf16; table [B, max_pages] int32; token t belongs to table row
     seq[t] (row t without ``seq``) and sees positions [0, lens[t]): all of
     them, or the picks topk[t, :] (positions, -1 masked). A token with lens 0
-    (a padded slot) gets zeros. ``out`` = (o, lse) writes into the caller's
-    tensors.
+    (a padded slot: its seq and picks are not looked at) gets zeros. ``out`` =
+    (o, lse) writes into the caller's tensors.
     """
     p_q = _check(cache, q, "q", torch.bfloat16, 3)
     p_table = _check(cache, table, "table", torch.int32, 2)

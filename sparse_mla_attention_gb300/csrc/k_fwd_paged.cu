@@ -383,7 +383,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             lena = __ldg(p.lens + wa.t);
             if (lena < 0 || lena > limit) { bad = true; lena = lena < 0 ? 0 : int(limit); }
             ba = p.seq ? __ldg(p.seq + wa.t) : wa.t;
-            if (ba < 0 || ba >= p.B) { bad = true; lena = 0; }
+            if (lena > 0 && (ba < 0 || ba >= p.B)) { bad = true; lena = 0; }
         };
         // Lane's position in the next tile, as it stands in topk; for all positions that of the
         // first rank of run (lane & 3) of 16
@@ -408,7 +408,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             return x;
         };
         auto page_of = [&](const Ahead& x) {     // -1: masked
-            if (p.topk) bad |= x.pos < -1 || x.pos >= x.len;
+            if (p.topk) bad |= x.len > 0 && (x.pos < -1 || x.pos >= x.len);
             if (x.pos < 0 || x.pos >= x.len) return -1;
             return __ldg(p.table + int64_t(x.b) * p.max_pages + (x.pos >> p.page_shift));
         };

@@ -235,6 +235,34 @@ def test_calls_at_once_on_two_streams():
     pool.check(cache)
 
 
+@pytest.mark.parametrize("picks", [False, True])
+def test_padded_slots_hold_anything(picks):
+    # a captured step's batch is filled up with slots of length 0, whatever their other entries say
+    smla = _smla()
+    rng = np.random.default_rng(21)
+    pool = Pool(40, 16, 16, seed=22)
+    table = pool.place([100, 230])
+    pool.fill(table, [100, 230])
+    cache = pool.device()
+    lens = np.array([100, 0, 230, 0, 0, 0])
+    seq = np.array([0, -1, 1, 2, 1 << 30, -(1 << 31)], dtype=np.int64)
+    topk = rng.integers(-(1 << 31), 1 << 31, size=(6, 70), dtype=np.int64)
+    topk[0], topk[2] = rng.integers(0, 100, size=70), rng.integers(0, 230, size=70)
+    q = bf16(rng.standard_normal((6, 32, 512)))
+    sink = rng.standard_normal(32).astype(np.float32)
+    o, lse = smla.sparse_mla_fwd_paged(bf16_dev(q), cache, _i32(table), _i32(lens), topk=_i32(topk) if picks else None,
+                                       seq=_i32(seq), sink=torch.from_numpy(sink).to(DEV))
+    live = [0, 2]
+    ref, rl, ob, lb = R.attend(q[live], pool.codes, pool.scales, table, lens[live], 16, 16,
+                               topk[live] if picks else None, None, sink.astype(np.float64))
+    assert (np.abs(to_f64(o)[live] - ref) <= ob).all()
+    assert (np.abs(lse.double().cpu().numpy()[live] - rl) <= lb).all()
+    for t in (1, 3, 4, 5):
+        assert (o[t] == 0).all()
+        # log2(e) and back, and a sum of one: four roundings of 2^-24
+        assert (np.abs(lse.double().cpu().numpy()[t] - sink) <= 2.0 ** -22 * np.abs(sink)).all()
+
+
 def test_empty_batches():
     # a step in which no sequence is left: every call does nothing and reports nothing
     smla = _smla()

@@ -116,10 +116,11 @@ struct PgParams {
     uint16_t* o; float* lse;
     int T, H, K, B, max_pages, num_pages, page_shift, block_shift;
     int groups, group_heads;                     // head groups, heads of a full one
+    int ctas;                                    // CTAs of a group
     float scale;
     unsigned* status;                            // the call's status word
     unsigned* cta_status;                        // [CTAs]
-    int4* meta;                                  // [CTAs] end of a split token: {t, first CTA, its part, 0}
+    int4* meta;                                  // [CTAs] end of a split token: {t, first CTA, its part, 0} (t -1: none)
     float2* part_ml;                             // [CTAs][2][group_heads] maximum (log2) and sum
     float* part_o;                               // [CTAs][2][group_heads / 4][512][4] (head h: block h / 4, h % 4)
 };
@@ -993,27 +994,45 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 // Bound: the latency of the first look-ups, then L2 (a part is 2 KB a head, written by the
 // kernel before); 152 CTAs have at most two parts each. ~3 us after the kernel above at 128
 // tokens of 64 heads, 10 us with cold caches.
-template <int kThreads>
+// kFew: block (x, y) belongs to a token instead, x = t * groups + group, and looks for the CTA that
+// ends it (the parts of few tokens are many, but most CTAs end none).
+template <int kThreads, bool kFew>
 __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams p) {
     constexpr int kWarps = kThreads / 32, kCols = kD / kThreads;
     constexpr int kRounds = (kPgMaxCtas + kThreads / 4 - 1) / (kThreads / 4);
     __shared__ float4 wgt[kPgMaxCtas];
     __shared__ float red[2][kWarps];
     __shared__ float4 inv_of;
+    const int group = int(blockIdx.x) % p.groups;
     grid_dep_wait();
     grid_dep_launch();
-    const int4 end = __ldcg(p.meta + blockIdx.x);
+    int4 end;
+    if (kFew) {
+        static_assert(!kFew || kThreads >= kPgMaxCtas, "a thread a CTA");
+        __shared__ int4 found;
+        if (threadIdx.x == 0) found = make_int4(-1, 0, 0, 0);
+        __syncthreads();
+        if (int(threadIdx.x) < p.ctas) {
+            int4 m = __ldcg(p.meta + threadIdx.x * p.groups + group);
+            m.w = threadIdx.x;
+            if (m.x == int(blockIdx.x) / p.groups) found = m;
+        }
+        __syncthreads();
+        end = found;
+    } else {
+        end = __ldcg(p.meta + blockIdx.x);
+        end.w = int(blockIdx.x) / p.groups;
+    }
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
         unsigned bits = 0;
-        for (int c = threadIdx.x; c < int(gridDim.x); c += 32) bits |= __ldcg(p.cta_status + c);
+        for (int c = threadIdx.x; c < p.ctas * p.groups; c += 32) bits |= __ldcg(p.cta_status + c);
         bits = __reduce_or_sync(0xffffffffu, bits);
         if (threadIdx.x == 0) *p.status = bits;
     }
     if (end.x < 0) return;
-    const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
     const int h0 = 4 * int(blockIdx.y), head0 = group * p.group_heads + h0;
     if (head0 >= p.H) return;                            // (heads come in sixteens)
-    const int n = cta - end.y + 1;                       // parts, at most the CTAs of a group
+    const int n = end.w - end.y + 1;                     // parts, at most the CTAs of a group
     auto part_of = [&](int i) {
         return (int64_t(end.y + i) * p.groups + group) * 2 + (i == 0 ? end.z : 0);
     };
@@ -1140,6 +1159,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     p.part_o = reinterpret_cast<float*>(a.scratch + plan.o);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int ctas = (sms < kPgMaxCtas ? sms : kPgMaxCtas) / plan.groups;
+    p.ctas = ctas;
     // Programmatic launches: a kernel's blocks may start when the one before no longer needs the SMs,
     // and wait for its end (grid_dep_wait) before they read or write anything.
     cudaLaunchAttribute early{};
@@ -1158,11 +1178,11 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     // pass, with 256 threads 70.8). Many have two or three: fewer threads, so that most blocks are
     // on the GPU at once (128 tokens, 64 heads: 75.6 us with 128 threads, 77.4 with 256, 82.6 with 512).
     const bool few = a.T < 32;
-    cfg.gridDim = dim3(ctas * plan.groups, plan.group_heads / 4);
+    cfg.gridDim = dim3((few ? a.T : ctas) * plan.groups, plan.group_heads / 4);
     cfg.blockDim = dim3(few ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
-    e = few ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<512>, p)
-            : cudaLaunchKernelEx(&cfg, combine_paged_kernel<128>, p);
+    e = few ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<512, true>, p)
+            : cudaLaunchKernelEx(&cfg, combine_paged_kernel<128, false>, p);
     if (e != cudaSuccess) return e;
     note_launch(2);
     return cudaGetLastError();

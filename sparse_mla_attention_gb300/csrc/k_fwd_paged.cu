@@ -987,18 +987,21 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
 }
 
-// Joins the parts of a token that several CTAs shared, in their order (so the result does not
+// Joins the parts of a token that several CTAs shared, in a fixed order (so the result does not
 // depend on the run): o = sum_i 2^(m_i - m) O_i / (sum_i 2^(m_i - m) l_i + 2^(sink - m)), in fp32.
-// Block (c, y): the token that ends in CTA c, heads 4y .. 4y + 3 of its group; a thread has
-// 512 / kThreads columns of all four. Block (0, 0) also joins the CTAs' status bits.
+// kSplit 0: block (c, y) joins the token that ends in CTA c, heads 4y .. 4y + 3 of its group; a
+// thread has 512 / kThreads columns of all four. Else block (x, y, z) belongs to a token and group,
+// x = t * groups + group, looks for the CTA that ends it, and has 512 / kSplit columns; kStep
+// threads share a column, each with every kStep-th part, and their sums are added in order.
+// One block also joins the CTAs' status bits.
 // Bound: the latency of the first look-ups, then L2 (a part is 2 KB a head, written by the
 // kernel before); 152 CTAs have at most two parts each. ~3 us after the kernel above at 128
 // tokens of 64 heads, 10 us with cold caches.
-// kFew: block (x, y) belongs to a token instead, x = t * groups + group, and looks for the CTA that
-// ends it (the parts of few tokens are many, but most CTAs end none).
-template <int kThreads, bool kFew>
+template <int kThreads, int kSplit>
 __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams p) {
-    constexpr int kWarps = kThreads / 32, kCols = kD / kThreads;
+    constexpr bool kFew = kSplit > 0;
+    constexpr int kWidth = kFew ? kD / kSplit : kD, kStep = kFew ? kThreads / kWidth : 1;     // columns, threads a column
+    constexpr int kWarps = kThreads / 32, kCols = kFew ? 1 : kD / kThreads;
     constexpr int kRounds = (kPgMaxCtas + kThreads / 4 - 1) / (kThreads / 4);
     __shared__ float4 wgt[kPgMaxCtas];
     __shared__ float red[2][kWarps];
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams 
     grid_dep_launch();
     int4 end;
     if (kFew) {
-        static_assert(!kFew || kThreads >= kPgMaxCtas, "a thread a CTA");
+        static_assert(!kFew || (kThreads >= kPgMaxCtas && kThreads % kWidth == 0), "a thread a CTA, whole columns");
         __shared__ int4 found;
         if (threadIdx.x == 0) found = make_int4(-1, 0, 0, 0);
         __syncthreads();
@@ -1023,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams 
         end = __ldcg(p.meta + blockIdx.x);
         end.w = int(blockIdx.x) / p.groups;
     }
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 32) {
         unsigned bits = 0;
         for (int c = threadIdx.x; c < p.ctas * p.groups; c += 32) bits |= __ldcg(p.cta_status + c);
         bits = __reduce_or_sync(0xffffffffu, bits);
@@ -1066,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams 
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (lane == 0) {
+    if (lane == 0) {                             // (blocks of the same heads write the same lse)
         sum = p.sink ? ex2_approx(sink - base) : 0.f;
 #pragma unroll
         for (int j = 0; j < kWarps / 4; ++j) sum += red[1][kWarps / 4 * k + j];
@@ -1074,11 +1077,13 @@ __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams 
         p.lse[int64_t(end.x) * p.H + head0 + k] = sum == 0.f ? -INFINITY : base * kPgLn2 + logf(sum);
     }
     __syncthreads();
+    const int col = kFew ? kWidth * int(blockIdx.z) + int(threadIdx.x) % kWidth : int(threadIdx.x);
+    const int start = kFew ? int(threadIdx.x) / kWidth : 0;      // the thread's first part
     float4 acc[kCols];
 #pragma unroll
     for (int j = 0; j < kCols; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int64_t size = int64_t(p.group_heads / 4) * kD;        // float4s of a part
-    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (h0 / 4) * kD + threadIdx.x;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (h0 / 4) * kD + col;
     auto add = [&](const float4* at, int i) {
         const float4 w = wgt[i];
 #pragma unroll
@@ -1090,12 +1095,26 @@ __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams 
             acc[j].w = fmaf(w.w, v.w, acc[j].w);
         }
     };
-    add(src + part_of(0) * size, 0);
+    if (start == 0) add(src + part_of(0) * size, 0);
     const float4* rest = src + part_of(1) * size;
 #pragma unroll (8 / kCols)
-    for (int i = 1; i < n; ++i) add(rest + (i - 1) * 2 * p.groups * size, i);
+    for (int i = start == 0 ? kStep : start; i < n; i += kStep) add(rest + (i - 1) * 2 * p.groups * size, i);
+    if (kStep > 1) {
+        __shared__ float4 part_sum[kStep > 1 ? kStep - 1 : 1][kWidth];
+        if (start > 0) part_sum[start - 1][threadIdx.x % kWidth] = acc[0];
+        __syncthreads();
+        if (start > 0) return;
+#pragma unroll
+        for (int k = 0; k < kStep - 1; ++k) {
+            const float4 v = part_sum[k][threadIdx.x];
+            acc[0].x += v.x;
+            acc[0].y += v.y;
+            acc[0].z += v.z;
+            acc[0].w += v.w;
+        }
+    }
     const float4 f = inv_of;
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (int64_t(end.x) * p.H + head0) * kD + threadIdx.x;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (int64_t(end.x) * p.H + head0) * kD + col;
 #pragma unroll
     for (int j = 0; j < kCols; ++j) {
         __nv_bfloat16* to = dst + kThreads * j;
@@ -1177,12 +1196,25 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     // Few tokens have many parts each: a thread a column (three tokens of 25 parts, 128 heads: 65.5 us a
     // pass, with 256 threads 70.8). Many have two or three: fewer threads, so that most blocks are
     // on the GPU at once (128 tokens, 64 heads: 75.6 us with 128 threads, 77.4 with 256, 82.6 with 512).
-    const bool few = a.T < 32;
-    cfg.gridDim = dim3((few ? a.T : ctas) * plan.groups, plan.group_heads / 4);
-    cfg.blockDim = dim3(few ? 512 : 128);
+    // The join: few tokens have blocks of their own, with their columns split as far as the blocks stay
+    // within 256 (more wait for one another, fewer leave the parts of a long token to few SMs); more
+    // tokens have two or three parts each, and a block for each CTA and four heads, of 128 threads,
+    // so that most are on the GPU at once. Device time of a call, us (T x positions, heads;
+    // columns split in 8 / 4 / 2 / 1 / a block a CTA):
+    //   1 x 81920, 64: 24.8 / 28.0 / 31.7 / 39.2 / 82.7     8 x 10000, 64: - / 30.3 / 27.4 / 28.3 / 35.5
+    //   16 x 5000, 64: - / 34.3 / 30.7 / 27.8 / 31.4        31 x 2500, 128: - / 60.8 / 48.0 / 39.6 / 36.5
+    const int64_t work = int64_t(a.T) * a.H;                 // four times the blocks of a split of 1
+    const int split = work <= 128 ? 8 : work <= 256 ? 4 : work <= 512 ? 2 : work <= 1024 ? 1 : 0;
+    cfg.gridDim = dim3((split ? a.T : ctas) * plan.groups, plan.group_heads / 4, split ? split : 1);
+    cfg.blockDim = dim3(split ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
-    e = few ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<512, true>, p)
-            : cudaLaunchKernelEx(&cfg, combine_paged_kernel<128, false>, p);
+    switch (split) {
+        case 8: e = cudaLaunchKernelEx(&cfg, combine_paged_kernel<512, 8>, p); break;
+        case 4: e = cudaLaunchKernelEx(&cfg, combine_paged_kernel<512, 4>, p); break;
+        case 2: e = cudaLaunchKernelEx(&cfg, combine_paged_kernel<512, 2>, p); break;
+        case 1: e = cudaLaunchKernelEx(&cfg, combine_paged_kernel<512, 1>, p); break;
+        default: e = cudaLaunchKernelEx(&cfg, combine_paged_kernel<128, 0>, p);
+    }
     if (e != cudaSuccess) return e;
     note_launch(2);
     return cudaGetLastError();

@@ -48,9 +48,9 @@
 // the rest. 16 heads are bound by the loads.
 // Measured (one GB300, device time of a call with its join, in a graph):
 //   128 sequences of up to 5120 positions, 64 heads: 75.6 us, 3.6 TB/s of cache, 0.86 PFLOP/s
-//   96 of up to 6001, 16 heads: 55 us, 4.1 TB/s;  3 of 81920, 128 heads: 65.5 us, 0.89 PFLOP/s
-//   256 tokens x 512 picks, 128 heads: 73 us;  one token of 777 positions: 18.4 us, of which 16
-//   are the two launches, the look-ups' latency, q and the output.
+//   96 of up to 6001, 16 heads: 55 us, 4.1 TB/s;  3 of 81920, 128 heads: 62 us, 0.94 PFLOP/s
+//   256 tokens x 512 picks, 128 heads: 73 us;  one token of 777 positions: 14.5 us: the two
+//   launches, the look-ups' latency, q, one tile, the output and the join.
 //
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the
 // CTA's loops, waits (bounded) for its own copies and MMAs and frees TMEM.

@@ -100,6 +100,8 @@ struct PgShared {
     __align__(16) float fac[2][2][kPgHeads];     // rescaling factors (team, parity of its count)
     // per item & 1 (an item's q is split only when the output of the item two before is done)
     float qfac[2][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
+    // item & 3 (an output warp may split the q of the item after next while another still reads the done item's)
+    float qodd[4][kPgHeads];                     // NaN where a head's q holds an infinity or a NaN, else 0
     float st_ref[kPgHeads];                      // running reference of a head
     float ref[2][2][kPgHeads], l[2][2][kPgHeads];         // and team: reference and sum of a head
     __align__(16) float fin[4][kPgHeads];        // per output warp: 1 / denominator
@@ -806,12 +808,21 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     top = max(top >> 16, top & 0xffffu);
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     int e2 = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+                    // An infinity or a NaN makes the head's output NaN, where the token has a valid rank. The
+                    // scores would carry it to masked ranks too, so the row goes on as zeros and the sum is made
+                    // NaN at the end, if there is one.
+                    const bool odd = top >= 0x7f80u;
+                    if (odd)
+#pragma unroll 1
+                        for (int c = 0; c < 32; ++c)
+                            *reinterpret_cast<uint4*>(qhalf + (c >> 3) * kPgBlockBytes + ((c & 7) << 4)) =
+                                make_uint4(0, 0, 0, 0);
                     e2 = top == 0 || e2 > 119 ? 0 : e2 < -100 ? -100 : e2;
                     const float inv = __int_as_float((127 - e2) << 23);
-                    // infinities and NaN in q make every score of the head NaN
-                    if (part == 0)
-                        sh.qfac[item & 1][head] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
-                                                                 : __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
+                    if (part == 0) {
+                        sh.qfac[item & 1][head] = __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
+                        sh.qodd[item & 3][head] = odd ? __int_as_float(0x7fffffff) : 0.f;
+                    }
                     // in place: eight values become eight bytes hi and eight bytes lo
 #pragma unroll 1
                     for (int c = 0; c < 32; c += 2) {
@@ -891,8 +902,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 // references only rise within an item: the larger is the accumulator's
                 const float mu = fmaxf(ma, mb);
                 const float m2 = mu == -INFINITY ? 0.f : mu - kPgBias;
-                const float l = (la == 0.f || ma == mu ? la : la * ex2_approx(ma - mu)) +
-                                (lb == 0.f || mb == mu ? lb : lb * ex2_approx(mb - mu));
+                const float sum_l = (la == 0.f || ma == mu ? la : la * ex2_approx(ma - mu)) +
+                                    (lb == 0.f || mb == mu ? lb : lb * ex2_approx(mb - mu));
+                const float l = sum_l == 0.f ? 0.f : sum_l + sh.qodd[done & 3][h];
                 if (whole) {
                     const float sink = sinks[j];
                     // a NaN sum stays one; a sum of zero leaves the sink alone

@@ -1,0 +1,57 @@
+"""GPU tests of the paged 8-bit cache's attention at the edges of its inputs: queries that are not
+finite or near the end of bf16's range, and tokens that see nothing.
+
+Models, bounds and the pool are those of test_gpu_cache.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as R
+from gpu_helpers import to_f64
+from test_gpu_cache import DEV, Pool, _i32, _smla, bf16, bf16_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("K", [0, 40, 900])
+@pytest.mark.parametrize("H", [16, 80])
+def test_tokens_that_see_nothing_are_zero_whatever_q_holds(H, K):
+    # padded slots and tokens without a valid pick (K 900: split over several CTAs), whose q is
+    # infinite or NaN: o = 0 and lse = sink; a token that sees one row is NaN in the heads concerned
+    smla = _smla()
+    rng = np.random.default_rng(K + H)
+    pool = Pool(40, 16, 16, seed=80)
+    table = pool.place([100, 230])
+    pool.fill(table, [100, 230])
+    cache = pool.device()
+    seq = np.array([0, 0, 1, 1, 0, 1])
+    lens = np.array([0, 0, 0, 0, 100, 1])
+    q = rng.standard_normal((6, H, 512))
+    q[0], q[1], q[2, :, 7], q[3, ::2, 500] = np.nan, np.inf, -np.inf, np.nan
+    q[4, 3, 11], q[5, 5, 400], q[5, 6, 1] = np.inf, -np.inf, np.nan
+    topk = None
+    if K:
+        lens[2:4] = 230                                  # these see rows, but pick none
+        topk = rng.integers(0, 100, size=(6, K))
+        topk[:4] = -1
+        topk[5] = -1
+        topk[5, K // 2] = 0
+    sink = rng.standard_normal(H).astype(np.float32)
+    qd = torch.from_numpy(q).to(torch.bfloat16).to(DEV)
+    for with_sink in (True, False):
+        o, lse = smla.sparse_mla_fwd_paged(qd, cache, _i32(table), _i32(lens), seq=_i32(seq),
+                                           topk=None if topk is None else _i32(topk),
+                                           sink=torch.from_numpy(sink).to(DEV) if with_sink else None)
+        o, lse = to_f64(o), lse.double().cpu().numpy()
+        assert (o[:4] == 0).all()
+        if with_sink:
+            # log2(e) and back, and a sum of one: four roundings of 2^-24
+            assert (np.abs(lse[:4] - sink) <= 2.0 ** -22 * np.abs(sink)).all()
+        else:
+            assert np.isneginf(lse[:4]).all()
+        nan = np.zeros((2, H), dtype=bool)
+        nan[0, 3] = nan[1, 5] = nan[1, 6] = True
+        assert np.isnan(o[4:][nan]).all() and np.isnan(lse[4:][nan]).all()
+        assert np.isfinite(o[4:][~nan]).all() and np.isfinite(lse[4:][~nan]).all()

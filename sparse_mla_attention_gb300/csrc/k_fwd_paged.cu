@@ -817,7 +817,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         for (int c = 0; c < 32; ++c)
                             *reinterpret_cast<uint4*>(qhalf + (c >> 3) * kPgBlockBytes + ((c & 7) << 4)) =
                                 make_uint4(0, 0, 0, 0);
-                    e2 = top == 0 || e2 > 119 ? 0 : e2 < -100 ? -100 : e2;
+                    e2 = odd || top == 0 ? 0 : e2 < -100 ? -100 : e2;        // (120 at most)
                     const float inv = __int_as_float((127 - e2) << 23);
                     if (part == 0) {
                         sh.qfac[item & 1][head] = __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;

@@ -10,7 +10,7 @@ import torch
 
 import cache_reference as R
 from gpu_helpers import to_f64
-from test_gpu_cache import DEV, Pool, _i32, _smla, bf16, bf16_dev
+from test_gpu_cache import DEV, Pool, _attend_and_check, _i32, _smla, bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,21 @@ def test_tokens_that_see_nothing_are_zero_whatever_q_holds(H, K):
         nan[0, 3] = nan[1, 5] = nan[1, 6] = True
         assert np.isnan(o[4:][nan]).all() and np.isnan(lse[4:][nan]).all()
         assert np.isfinite(o[4:][~nan]).all() and np.isfinite(lse[4:][~nan]).all()
+
+
+@pytest.mark.parametrize("K", [0, 70])
+def test_q_up_to_the_largest_bf16(K):
+    # rows of q whose largest value is 1.75 * 2^127 and above, up to bf16's largest; rows of the cache and the score
+    # scale are small, so that scores are ordinary
+    rng = np.random.default_rng(81)
+    lens = [150, 70, 9]
+    pool = Pool(30, 16, 16, seed=82)
+    table = pool.place(lens)
+    pool.fill(table, lens, amp=2.0 ** -60)
+    q = np.clip(rng.standard_normal((3, 32, 512)), -3, 3) * 2.0 ** 125
+    for h in range(32):
+        big = (1.75 + 2.0 ** -7 * (h % 32)) * 2.0 ** 127             # 1.75, ..., 1.9921875, the largest
+        q[:, h, rng.integers(0, 512)] = min(big, 1.9921875 * 2.0 ** 127) * (-1) ** h
+    topk = rng.integers(0, np.array(lens)[:, None], size=(3, K)) if K else None
+    # |q . x| is about 2^(126 - 60) * 22, times 2^-70: scores of order one
+    _attend_and_check(pool, table, lens, 32, seed=83, q=q, topk=topk, scale=2.0 ** -70)

@@ -1,0 +1,68 @@
+"""GPU tests of how near the paged attention comes to 64 bits, relative to its own output
+(cache_accuracy), where the elementwise bounds of cache_reference are wide."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_accuracy as A
+import cache_reference as R
+from gpu_helpers import to_f64
+from test_gpu_cache import DEV, Pool, _i32, _smla, bf16, bf16_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def _attend(pool, table, lens, q, **kw):
+    o, lse = _smla().sparse_mla_fwd_paged(bf16_dev(q), pool.device(), _i32(table), _i32(lens),
+                                          **{k: _i32(v) for k, v in kw.items()})
+    return to_f64(o), lse.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("lens", [[333, 700, 4097], [20011]])
+def test_flat_weights(H, lens):
+    pool = Pool(sum(-(-n // 64) for n in lens) + 1, 64, 64, seed=90, junk=False)
+    table = pool.place(lens)
+    pool.fill(table, lens)
+    q = bf16(np.random.default_rng(H).standard_normal((len(lens), H, 512)))
+    o, lse = _attend(pool, table, lens, q)
+    at = (q, pool.codes, pool.scales, table, lens, 64, 64)
+    ref, rl, _, _ = R.attend(*at)
+    A.check(o, ref, A.tolerances(*at), lse, rl)
+
+
+@pytest.mark.parametrize("H,K", [(32, 400), (128, 512)])
+def test_flat_weights_of_picks(H, K):
+    rng = np.random.default_rng(K)
+    pool = Pool(60, 64, 32, seed=91, junk=False)
+    lens = [3000, 600]
+    table = pool.place(lens)
+    pool.fill(table, lens)
+    seq = np.arange(40) % 2
+    ln = np.array(lens)[seq]
+    topk = np.stack([rng.permutation(n)[:K] for n in ln])
+    q = bf16(rng.standard_normal((40, H, 512)))
+    o, lse = _attend(pool, table, ln, q, topk=topk, seq=seq)
+    at = (q, pool.codes, pool.scales, table, ln, 64, 32, topk, seq)
+    ref, rl, _, _ = R.attend(*at)
+    A.check(o, ref, A.tolerances(*at), lse, rl)
+
+
+def test_every_tile_of_a_split_sequence_counts():
+    # a head for each tile of 64, drawn to one row of it by some 14 nats: a tile that is lost or
+    # taken twice is the whole output of its head
+    n, H = 20011, 128
+    rng = np.random.default_rng(92)
+    pool = Pool(314, 64, 64, seed=93, junk=False)
+    table = pool.place([n])
+    pool.fill(table, [n])
+    at = np.minimum(np.arange(3 * H) % 313 * 64 + rng.integers(0, 64, size=3 * H), n - 1)
+    x, _, _ = R.rows_of(pool.codes, pool.scales, table[0], at, 64, 64)
+    q = bf16(x.reshape(3, H, 512) * (14 * math.sqrt(512) / 512))
+    o, lse = _attend(pool, table, [n] * 3, q, seq=[0, 0, 0])
+    at = (q, pool.codes, pool.scales, table, [n] * 3, 64, 64, None, [0, 0, 0])
+    ref, rl, _, _ = R.attend(*at)
+    A.check(o, ref, A.tolerances(*at), lse, rl)

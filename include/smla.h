@@ -266,7 +266,8 @@ int smla_dsink_static(const uint16_t* dO, const uint16_t* o, const float* lse,
  */
 typedef struct smla_cache {
     uint8_t* pages;       /* [num_pages, page_size, 512] e4m3 bit patterns */
-    float* scales;        /* [num_pages, page_size / scale_block] fp32, finite and >= 0 */
+    float* scales;        /* [num_pages, page_size / scale_block] fp32, finite and >= 0 (in the
+                             output of smla_fwd_paged a scale counts as 2^-100 at least) */
     int32_t* refcount;    /* [num_pages]; may be NULL for smla_fwd_paged, smla_cache_write and
                              smla_cache_copy_pages */
     int32_t num_pages;    /* >= 1; num_pages * page_size < 2^31 */

@@ -14,7 +14,7 @@
 //    e5m2(w - e4m3(w)), whose range reaches further down: off by at most 2^-7 w
 //    (bf16: 2^-8), and 2^-18 of the largest weight for weights near zero. Both parts
 //    accumulate into one fp32 accumulator; the denominator sums unrounded weights.
-// Block scales: s_r is multiplied by its row's scale in fp32, and w carries it.
+// Block scales: s_r is multiplied by its row's scale in fp32, and w carries it (2^-100 at least).
 //
 // S = Q K^T: M = 128 (up to 64 heads; lanes 16i .. 16i+15 of each lane quarter's first half
 // hold hi, its second half lo), N = 64 ranks, K = 512, A = Q from TMEM.
@@ -95,8 +95,10 @@ struct PgShared {
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
     int sum[kPgThreads / 32];
     __align__(16) uint32_t need[2][2][4];        // team, parity of its count, lane quarter: rescale O first
-    __align__(16) float smax[kPgSlots][kPgLoadWarps];     // largest block scale of 16 ranks
-    __align__(16) float2 scale[kPgSlots][kPgTile];        // of each rank: block scale and 0, or 0 and -inf (masked)
+    // of each rank: block scale and its log2, or 0 and -inf (masked); 1 / scale. A scale counts as 2^-100 at least in
+    // the logarithm and the reciprocal.
+    __align__(16) float2 scale[kPgSlots][kPgTile];
+    __align__(16) float inv[kPgSlots][kPgTile];
     __align__(16) float fac[2][2][kPgHeads];     // rescaling factors (team, parity of its count)
     // per item & 1 (an item's q is split only when the output of the item two before is done)
     float qfac[2][kPgHeads];                     // score factor of a head's q: 2^e * scale * log2(e)
@@ -108,8 +110,9 @@ struct PgShared {
 };
 
 constexpr int kPgStageBytes = 2048;              // an output warp's staging: two halves
-constexpr int kPgSmem =
-    int(sizeof(PgShared)) + 1024 + kPgSlots * kPgSlotBytes + 2 * kPgPBytes + 4 * kPgStageBytes;
+// The ring comes first: swizzled tiles want a base that is a multiple of 1024, as the array's is declared to be.
+constexpr int kPgSharedAt = kPgSlots * kPgSlotBytes + 2 * kPgPBytes + 4 * kPgStageBytes;
+constexpr int kPgSmem = kPgSharedAt + int(sizeof(PgShared));
 static_assert(kPgSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 
 struct PgParams {
@@ -191,6 +194,12 @@ __device__ __forceinline__ __half2 e4m3x2_half(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t e5m2x2(__half2 v) {
     return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E5M2);
+}
+// 1 / x by the PTX rcp.approx.f32 instruction (relative error at most 2^-23, subnormal results kept).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 // The CTA's share of the tiles. Picks: every token has as many tiles. All
 // positions: sums the tiles of the tokens (thread i those of a run of tokens), then
@@ -279,10 +288,8 @@ struct PgWalk {
 __global__ void __launch_bounds__(kPgThreads, 1)
 fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_box,
                  const PgParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    PgShared& sh = *reinterpret_cast<PgShared*>(smem_raw);
-    uint8_t* ring = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw + sizeof(PgShared)) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t ring[];
+    PgShared& sh = *reinterpret_cast<PgShared*>(ring + kPgSharedAt);
     uint8_t* pbuf = ring + kPgSlots * kPgSlotBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = int(blockIdx.x) % p.groups, cta = int(blockIdx.x) / p.groups;
@@ -471,11 +478,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     cp_async_commit();
                 }
-                if (lane < 16)
-                    sh.scale[slot][16 * lw + lane] = make_float2(fmaxf(sc16, 0.f), sc16 >= 0.f ? 0.f : -INFINITY);
-                // (scales are not negative: their bits order like unsigned integers)
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sc16, 0.f)));
-                if (lane == 0) sh.smax[slot][lw] = __uint_as_float(top);
+                if (lane < 16) {
+                    const float least = fmaxf(sc16, 0x1p-100f);
+                    sh.scale[slot][16 * lw + lane] = make_float2(fmaxf(sc16, 0.f), sc16 >= 0.f ? __log2f(least) : -INFINITY);
+                    sh.inv[slot][16 * lw + lane] = rcp_approx(least);
+                }
                 __syncwarp();
                 if (boxes) {
                     if (lane == 0) mbar_arrive(&sh.full[slot]);
@@ -613,12 +620,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     } else if (warp < kPgOutWarp) {
         // -------------------------------------------------------------- softmax
         // Two teams of four warps take the tiles in turn (a tile's team is its slot's
-        // parity). A head's reference r is kept so that weights 2^(s - r + bias) * block scale stay
-        // below e4m3's largest value: it starts as the first tile's largest score plus
-        // log2 of its largest scale and follows when a tile passes it by more than the
-        // slack. It passes from team to team along dec[quarter]; O is rescaled for a tile by
-        // its team, before its O product but after its weights are written, so that no
-        // warp waits for the others' verdicts on the way.
+        // parity). A head's reference r is kept so that weights 2^(s + log2(block scale) - r + bias)
+        // stay below e4m3's largest value: it starts as the first tile's largest sum of score and
+        // log2 of scale and follows when a tile passes it by more than the slack. (The sum is a
+        // rank's own: the largest score plus log2 of the largest scale may be two ranks', and
+        // then costs every weight range.) It passes from team to team along dec[quarter]; O is
+        // rescaled for a tile by its team, before its O product but after its weights are
+        // written, so that no warp waits for the others' verdicts on the way.
         const int team = warp >> 2, quarter = warp & 3;
         const int part = lane >> 4, head = 16 * quarter + (lane & 15);
         const bool active = 16 * quarter < heads;
@@ -675,7 +683,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 tc_fence_after();
                 if (i < 2) f = sh.qfac[item & 1][head] * lo_factor;
                 const float4* scp = reinterpret_cast<const float4*>(&sh.scale[slot][32 * part]);
-                float s[32];
+                const float4* invp = reinterpret_cast<const float4*>(&sh.inv[slot][32 * part]);
+                float s[32];                     // score plus log2 of the block scale: log2 of the weight
                 float mx = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -686,7 +695,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float4 c2 = scp[8 * q + e / 2];       // two ranks: scale and mask
+                        const float4 c2 = scp[8 * q + e / 2];       // two ranks: scale and its log2
                         const float g0 = __uint_as_float(part ? v0[e] : v1[e]) * f;
                         const float g1 = __uint_as_float(part ? v0[e + 1] : v1[e + 1]) * f;
                         const float x0 = fmaf(__uint_as_float(part ? v1[e] : v0[e]), f,
@@ -701,9 +710,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.s_empty[team]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float4 sm = *reinterpret_cast<const float4*>(sh.smax[slot]);
-                const float top = mx + __log2f(fmaxf(fmaxf(fmaxf(sm.x, sm.y), fmaxf(sm.z, sm.w)), 0x1p-100f));
+                const float top = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 // the reference after the tile before this one
                 if (tile > 0) ok = pg_wait_warp(&sh.dec[quarter], uint32_t(tile - 1) & 1u, ab, &sh.status);
                 if (!ok) break;
@@ -725,20 +732,22 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (!ok) break;
                 if (active) {
                     const float off = kPgBias - (ref == -INFINITY ? 0.f : ref);
+                    float l1 = 0.f;                  // (two sums: a chain each)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {            // 16 ranks: 16 bytes hi and 16 bytes lo
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e4 = 0; e4 < 4; ++e4) {
                             uint32_t hl[2], ll[2];
+                            const float4 i4 = invp[4 * q + e4];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const int e = 16 * q + 4 * e4 + 2 * k;
-                                const float4 c2 = scp[e / 2];
-                                const float p0 = ex2_approx(s[e] + off), p1 = ex2_approx(s[e + 1] + off);
-                                l += p0 + p1;
+                                const float w0 = ex2_approx(s[e] + off), w1 = ex2_approx(s[e + 1] + off);
+                                l = fmaf(w0, k ? i4.z : i4.x, l);
+                                l1 = fmaf(w1, k ? i4.w : i4.y, l1);
                                 // half precision holds a weight to 2^-12, and its e4m3 part exactly
-                                const __half2 x = __floats2half2_rn(p0 * c2.x, p1 * c2.z);
+                                const __half2 x = __floats2half2_rn(w0, w1);
                                 hl[k] = e4m3x2(x);
                                 ll[k] = e5m2x2(__hsub2(x, e4m3x2_half(hl[k])));
                             }
@@ -751,6 +760,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (head & 7)) << 4)) =
                             make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
+                    l += l1;
                     const float both = l + __shfl_xor_sync(0xffffffffu, l, 16);
                     if (part == 0) {
                         sh.ref[item & 1][team][head] = ref;

@@ -66,3 +66,34 @@ def test_every_tile_of_a_split_sequence_counts():
     at = (q, pool.codes, pool.scales, table, [n] * 3, 64, 64, None, [0, 0, 0])
     ref, rl, _, _ = R.attend(*at)
     A.check(o, ref, A.tolerances(*at), lse, rl)
+
+
+# One token repeated: as many tokens as CTAs, so that a CTA has one token's tiles in a run.
+def _repeated(pool, table, n, q, topk=None):
+    T = 160
+    kw = {} if topk is None else dict(topk=np.repeat(topk[None], T, 0))
+    o, lse = _attend(pool, np.asarray(table), [n] * T, np.repeat(q, T, 0), seq=np.zeros(T), **kw)
+    at = (q, pool.codes, pool.scales, table, [n], pool.page, pool.block, None if topk is None else topk[None])
+    ref, rl, _, _ = R.attend(*at)
+    return o, lse, ref, rl, A.tolerances(*at)
+
+
+def _loud(rng, n, louder):
+    """Rows of N(0,1), the first one `louder` times as loud and turned away from all heads; q."""
+    q = bf16(rng.standard_normal((1, 16, 512)))
+    rows = rng.standard_normal((n, 512))
+    rows[0] = -q[0].sum(axis=0) / 4 * louder
+    pool = Pool(-(-n // 64), 64, 16, seed=94, junk=False)
+    table = pool.place([n])
+    R.write(pool.codes, pool.scales, table, [0], [0, n], bf16(rows), 64, 16)
+    return pool, table, q
+
+
+def test_a_loud_row_that_nobody_heeds():
+    # its block's scale is 2^14 that of the others, its weight nothing: the others' weights must
+    # not lose its scale's range (a part of a token has its own largest weight: one tolerance holds for all)
+    rng = np.random.default_rng(95)
+    pool, table, q = _loud(rng, 4096, 2.0 ** 14)
+    picks = np.concatenate([[0], 16 + rng.permutation(4080)[:511]])       # none of its block's other rows
+    o, lse, ref, rl, tol = _repeated(pool, table, 4096, q, picks)
+    A.check(o, ref, tol, lse, rl)

@@ -303,9 +303,9 @@ typedef struct smla_paged_dims {
  *   q [T,H,512] bf16, lens [T], seq [T] or NULL, topk [T,topk] or NULL int32,
  *   sink [H] fp32 (finite or -inf) or NULL -> o [T,H,512] bf16 (RNE), lse [T,H] fp32.
  * Scores and sums are fp32; q meets the codes exactly (as two e4m3 parts), a
- * weight as an e4m3 and an e5m2 part (off by at most 2^-7 of it, or 2^-17 of the
- * token's largest weight times the largest block scale). The result is the
- * same in every run.
+ * weight, with its block scale, as an e4m3 and an e5m2 part (off by at most 2^-7
+ * of it, or 2^-20 of the token's largest such weight; the denominator is not
+ * rounded so). The result is the same in every run.
  * On the device: lens[t] outside [0, max_pages * page_size] is clamped, and a
  * seq, a topk entry >= lens[t] or < -1, or a page number that is out of range
  * masks what it names; each sets SMLA_ERR_INDEX in the status word.

@@ -97,3 +97,36 @@ def test_a_loud_row_that_nobody_heeds():
     picks = np.concatenate([[0], 16 + rng.permutation(4080)[:511]])       # none of its block's other rows
     o, lse, ref, rl, tol = _repeated(pool, table, 4096, q, picks)
     A.check(o, ref, tol, lse, rl)
+
+
+def test_a_loud_block_in_ordinary_company():
+    # all of the block's rows have the loud row's scale, and scores like any other: they take 2^12 of the weights'
+    # range. What is off by 2^-20 of the largest weight is then 2^-8 of theirs at most.
+    pool, table, q = _loud(np.random.default_rng(96), 512, 2.0 ** 12)
+    o, lse, ref, rl, tol = _repeated(pool, table, 512, q)
+    A.check(o, ref, tol, lse, rl)
+
+
+@pytest.mark.parametrize("n", [8192, 32768])
+@pytest.mark.parametrize("spread", [0.1, 0.3, 1.0])
+def test_one_row_against_thousands(n, spread):
+    # the first row has half of the weight (as a first token often has), thousands of nearly equal ones
+    # with a common direction the other half: their weights are 2^-13 and 2^-15 of the largest. They are held
+    # to 2^-20 of it, that is 2^-7 and 2^-5 of themselves; spread over more than such a step (a
+    # tenth of a nat is 2^-2.8 of them) they have no common sign for more than a quarter of it:
+    # 2^-7 of half the output at most, beside the output's own rounding, 1.7e-3.
+    rng = np.random.default_rng(n)
+    d = rng.standard_normal(512)
+    d /= np.linalg.norm(d)
+
+    def apart(v):
+        return v - (v @ d)[..., None] * d
+    rows = apart(rng.standard_normal((n, 512)) * 0.5) + 0.5 * apart(rng.standard_normal(512))
+    rows += spread * rng.standard_normal((n, 1)) * d                     # scores of N(0, spread)
+    rows[0] = apart(rng.standard_normal(512) * 0.5) + (math.log(n) + spread ** 2 / 2) * d
+    q = bf16((math.sqrt(512) * d + 0.02 * spread * rng.standard_normal((1, 16, 512))))
+    pool = Pool(n // 64, 64, 64, seed=97, junk=False)
+    table = pool.place([n])
+    R.write(pool.codes, pool.scales, table, [0], [0, n], bf16(rows), 64, 64)
+    o, lse, ref, rl, _ = _repeated(pool, table, n, q)
+    A.check(o, ref, math.hypot(1.7e-3, 2.0 ** -8) * np.linalg.norm(ref, axis=-1), lse, rl)

@@ -56,17 +56,42 @@ def workspace_size(op: int, dims: SmlaDims) -> int:
     return int(n.value)
 
 
+# (looked at in every call that takes a workspace: without torch.cuda's own checks)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_capturing = (getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
+                     or torch.cuda.is_current_stream_capturing)
+
+
+def _capturing(buf: torch.Tensor) -> bool:
+    """Whether the current stream of buf's device is being captured into a CUDA graph."""
+    index = buf.get_device()
+    if index < 0 or _current_device() == index:
+        return index >= 0 and _stream_capturing()
+    with torch.cuda.device(index):
+        return _stream_capturing()
+
+
 class Workspace:
-    """A reusable device workspace (grown on demand, never shrunk)."""
+    """A reusable device workspace (grown on demand, never shrunk).
+
+    A captured CUDA graph holds the address of the buffer that its calls were given: keep the workspace as long as
+    the graph. A buffer that a capture has used stays alive with the workspace when a larger one takes its place."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf: Optional[torch.Tensor] = None
+        self._captured = False       # a capture has used buf
+        self._kept = []              # buffers before it that captures have used
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._kept.append(self.buf)
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._captured = False
+        if not self._captured:
+            self._captured = _capturing(self.buf)
         return self.buf
 
 

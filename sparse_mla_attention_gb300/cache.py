@@ -18,13 +18,12 @@ import torch
 
 from . import _lib
 from ._lib import SmlaCache, SmlaPagedDims
-from .api import D_HEAD, Workspace, _need, device_status
+from .api import D_HEAD, Workspace, _current_device, _need, device_status
 
 # A decode step makes these calls once a layer, and their kernels take some ten
 # microseconds: checks and marshalling are kept to a few attribute reads a tensor.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _check(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> int:

@@ -96,6 +96,7 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
     extern __shared__ __align__(128) uint8_t stage[];        // kBlock rows
     __shared__ uint32_t warp_max[2][kWarps];
     __shared__ uint64_t full;
+    __shared__ int late;                                     // a wait ran out
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool bad = false;
     if (blockIdx.x == 0) {
@@ -143,6 +144,7 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
         bulk_load(stage + x.lo * (kD * 2), rows + (x.row0 + x.lo) * (kD * 2), bytes, &full);
     };
     if (threadIdx.x == 0) {
+        late = 0;
         mbar_init(&full, 1);
         fence_mbar_init();
     }
@@ -158,7 +160,7 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
         const Piece then = next();
         if (!mbar_wait(&full, n & 1u, kWriteWaitNs)) {
             flag_status(status, SMLA_ERR_TIMEOUT);           // (long after CTA 0 wrote the word)
-            return;
+            late = 1;
         }
         uint4 v[4][2];
         uint32_t top = 0;
@@ -185,6 +187,10 @@ cache_write_kernel(const CacheView c, const int32_t* __restrict__ table,
         top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
         if (lane == 0) warp_max[n & 1][warp] = top;
         __syncthreads();
+        if (late) {                              // the copy in flight lands before the CTA's memory is another's
+            if (threadIdx.x == 0) mbar_wait(&full, n & 1u, kWriteWaitNs / 8);
+            return;
+        }
         load(then);                              // all have their rows: the next block's may come
         cur = then;
         if (page < 0) continue;

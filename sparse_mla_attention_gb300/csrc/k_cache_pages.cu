@@ -233,7 +233,7 @@ __device__ void copy_pairs(const CacheView& c, uint8_t* ring, CopyShared& sh, Sr
             const int j = i - kCopyLag, slot = j % kCopySlots;
             if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[slot], uint32_t(j / kCopySlots) & 1u, kCopyWaitNs))) {
                 flag_status(status, SMLA_ERR_TIMEOUT);
-                for (int k = j + 1; k <= i && k < mine; ++k)       // loads already issued land before the CTA exits
+                for (int k = j; k <= i && k < mine; ++k)       // loads already issued land before the CTA exits
                     mbar_wait(&sh.full[k % kCopySlots], uint32_t(k / kCopySlots) & 1u, kCopyWaitNs / 8);
                 break;
             }

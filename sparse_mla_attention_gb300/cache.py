@@ -43,7 +43,9 @@ class PagedCache:
     refcount [num_pages] int32: table entries that hold the page (0: free)
 
     page_size is 16, 32, 64, 128 or 256, scale_block 16, 32 or 64. The tensors
-    are the caller's: the handle keeps them and the C struct that names them.
+    are the caller's: the handle keeps them and the C struct that names them. New
+    contents are copied into them (after cache_compact, say); other tensors need another
+    handle.
     """
 
     def __init__(self, pages: torch.Tensor, scales: torch.Tensor, refcount: torch.Tensor):
@@ -58,7 +60,7 @@ class PagedCache:
         for name, t in (("scales", scales), ("refcount", refcount)):
             if t.device != pages.device:
                 raise ValueError(f"{name} must be on {pages.device}, got {t.device}")
-        self.pages, self.scales, self.refcount = pages, scales, refcount
+        self._pages, self._scales, self._refcount = pages, scales, refcount
         self.num_pages, self.page_size = n, ps
         self.scale_block = ps // scales.shape[1]
         self.device = pages.device
@@ -71,6 +73,11 @@ class PagedCache:
         self._lib = _lib.load()
         size = ctypes.c_size_t(0)
         _lib.check(self._lib.smla_cache_workspace_size(self._ref, 0, ctypes.byref(size)), "PagedCache")
+
+    # (read-only: the calls go by the C struct, so another tensor put in place would not be seen)
+    pages = property(lambda self: self._pages)
+    scales = property(lambda self: self._scales)
+    refcount = property(lambda self: self._refcount)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int = 64, scale_block: int = 64, device=None) -> "PagedCache":

@@ -54,6 +54,8 @@
 //
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the
 // CTA's loops, waits (bounded) for its own copies and MMAs and frees TMEM.
+#include <cfloat>
+
 #include <cuda_fp8.h>
 
 #include "smla_internal.cuh"
@@ -841,7 +843,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     e2 = odd || top == 0 ? 0 : e2 < -100 ? -100 : e2;        // (120 at most)
                     const float inv = __int_as_float((127 - e2) << 23);
                     if (part == 0) {
-                        sh.qfac[item & 1][head] = __int_as_float((127 + e2) << 23) * p.scale * kPgLog2e;
+                        // (finite, so that a masked rank's zero stays one)
+                        sh.qfac[item & 1][head] = fminf(__int_as_float((127 + e2) << 23) * p.scale * kPgLog2e, FLT_MAX);
                         sh.qodd[item & 3][head] = odd ? __int_as_float(0x7fffffff) : 0.f;
                     }
                     // in place: eight values become eight bytes hi and eight bytes lo

@@ -73,3 +73,17 @@ def test_q_up_to_the_largest_bf16(K):
     topk = rng.integers(0, np.array(lens)[:, None], size=(3, K)) if K else None
     # |q . x| is about 2^(126 - 60) * 22, times 2^-70: scores of order one
     _attend_and_check(pool, table, lens, 32, seed=83, q=q, topk=topk, scale=2.0 ** -70)
+
+
+@pytest.mark.parametrize("K", [0, 5])
+def test_scores_past_float_leave_masked_tokens_alone(K):
+    # q and the score scale are finite, their product is not: a token that sees nothing is zero all the same
+    smla = _smla()
+    pool = Pool(4, 16, 16, seed=84)
+    table = pool.place([20])
+    pool.fill(table, [20])
+    q = torch.full((2, 16, 512), 3e38, dtype=torch.bfloat16, device=DEV)
+    topk = torch.full((2, K), -1, dtype=torch.int32, device=DEV) if K else None
+    o, lse = smla.sparse_mla_fwd_paged(q, pool.device(), _i32(table), _i32([20, 0] if K else [0, 0]), topk=topk,
+                                       seq=_i32([0, 0]), scale=1e10)
+    assert (o == 0).all() and torch.isneginf(lse).all()

@@ -333,7 +333,7 @@ fork_plan_kernel(const CacheView c, const int32_t* __restrict__ table, const int
     const int64_t limit = int64_t(max_pages) << c.page_shift;
     unsigned bits = 0;
     int turn = 0;
-    // w.map[i]: the page that child i copies, or -1
+    // w.tail[i]: the page that child i copies, or -1
     for (int i = rank * kPlanThreads + threadIdx.x; i < n; i += kPlanCtas * kPlanThreads) {
         int e = -1;
         const int p = __ldg(parents + i);

@@ -13,8 +13,10 @@
 // one to shared memory while the one at hand, in registers since its maximum was
 // taken, is converted and stored. 78,000 rows of 24 prompts (64-row blocks): 25.4 us, 4.7
 // TB/s of reads and writes (one block a CTA, loaded to registers, and the status word
-// cleared by a launch of its own: 29 us). One row for each of 128 sequences: 5.2 us (8.3),
-// the latency of a launch and of five loads in a row.
+// cleared by a launch of its own: 29 us). One row for each of 128 sequences: 5.3 us (8.3),
+// the latency of a launch and of five loads in a row. CTA 0's look at every slot is hidden only
+// while the slots are few: 619,000 rows take 172 us in blocks of 64, 169 in blocks of 32 and 330 in
+// blocks of 16, where it is the bound.
 #include <cuda_fp8.h>
 
 #include "smla_internal.cuh"

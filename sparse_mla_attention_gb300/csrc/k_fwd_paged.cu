@@ -40,16 +40,18 @@
 // for S; O is taken transposed because its 64 heads are then N, and V needs no copy.
 // 64 ranks a tile: S takes two buffers of 64 TMEM columns beside Q and O, which fill the
 // other 384. Two teams, because a tile's softmax is a chain of waits.
-// Bound: of a tile's ~1750 cycles on an SM at 64 heads the products take ~1600 (16 of 62 for O,
-// 16 of 38 for S: they read the tile at shared memory's rate), reading 32 KB at the SM's share of
-// HBM ~1500; a team has two tiles' time for a chain of loads, swaps, exponentials and
-// conversions. No unit is full (profiled: DRAM and issue slots 48% of the time, tensor pipe
-// 43%; half of the O products would save 5%); the start, the ends of items and the join are
-// the rest. 16 heads are bound by the loads.
-// Measured (one GB300, device time of a call with its join, in a graph):
-//   128 sequences of up to 5120 positions, 64 heads: 75.6 us, 3.6 TB/s of cache, 0.86 PFLOP/s
-//   96 of up to 6001, 16 heads: 55 us, 4.1 TB/s;  3 of 81920, 128 heads: 62 us, 0.94 PFLOP/s
-//   256 tokens x 512 picks, 128 heads: 73 us;  one token of 777 positions: 14.5 us: the two
+// Bound: 152 CTAs with one item of 8 to 64 tiles each take 17.9 us + 0.95 a tile at 64 heads (1970
+// cycles a tile: its products take ~1600, 16 of 62 for O and 16 of 38 for S, reading it at shared
+// memory's rate; reading 32 KB at the SM's share of HBM takes ~1500; a team has two tiles' time for
+// a chain of loads, swaps, exponentials and conversions), 12.8 us + 0.82 at 16 heads, which are
+// bound by the loads. No unit is full (profiled at 64 heads: DRAM 47% of its rate, issue slots
+// 44% and tensor pipe 41% of the time). The fixed part is the start, the look-ups, the first q's
+// split, the output and the second launch; second items and split tokens come on top.
+// Measured (one GB300, device time of a call with its join, in a graph, scores of N(0,1); in brackets
+// four times as far apart, where O is rescaled every few tiles):
+//   128 sequences of up to 5120 positions, 64 heads: 78 us (91), 3.3 TB/s of cache, 0.83 PFLOP/s
+//   96 of up to 6001, 16 heads: 55 us (59), 4.0 TB/s;  3 of 81920, 128 heads: 64.5 us (77), 0.90 PFLOP/s
+//   256 tokens x 512 picks, 128 heads: 74 us (82);  one token of 777 positions: 14.5 us: the two
 //   launches, the look-ups' latency, q, one tile, the output and the join.
 //
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the
@@ -1229,9 +1231,6 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, fwd_paged_kernel, mq, mb, p);
     if (e != cudaSuccess) return e;
-    // Few tokens have many parts each: a thread a column (three tokens of 25 parts, 128 heads: 65.5 us a
-    // pass, with 256 threads 70.8). Many have two or three: fewer threads, so that most blocks are
-    // on the GPU at once (128 tokens, 64 heads: 75.6 us with 128 threads, 77.4 with 256, 82.6 with 512).
     // The join: few tokens have blocks of their own, with their columns split as far as the blocks stay
     // within 256 (more wait for one another, fewer leave the parts of a long token to few SMs); more
     // tokens have two or three parts each, and a block for each CTA and four heads, of 128 threads,

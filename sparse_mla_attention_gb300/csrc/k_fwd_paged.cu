@@ -101,6 +101,7 @@ struct PgShared {
     uint32_t tbase;
     unsigned status;                             // this CTA's status bits
     volatile int abort_flag;
+    volatile int far;                            // the CTA has met a scale outside [2^-45, 2^45]
     int t0, k0, count;                           // the CTA's first token, tile in it, tiles in all
     int sum[kPgThreads / 32];
     __align__(16) uint32_t need[2][2][4];        // team, parity of its count, lane quarter: rescale O first
@@ -209,6 +210,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// x 2^d for d down to -250 (in two steps: the factor alone may be less than a float holds).
+__device__ __forceinline__ float mul_ex2(float x, float d) {
+    const float h = ex2_approx(0.5f * d);
+    return x * h * h;
 }
 // The CTA's share of the tiles. Picks: every token has as many tiles. All
 // positions: sums the tiles of the tokens (thread i those of a run of tokens), then
@@ -329,6 +335,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
         sh.abort_flag = 0;
+        sh.far = 0;
         sh.status = 0;
         fence_mbar_init();
     }
@@ -492,6 +499,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     sh.scale[slot][16 * lw + lane] = make_float2(fmaxf(sc16, 0.f), sc16 >= 0.f ? __log2f(least) : -INFINITY);
                     sh.inv[slot][16 * lw + lane] = rcp_approx(least);
                 }
+                if (sc16 > 0x1p45f || (sc16 >= 0.f && sc16 < 0x1p-45f)) sh.far = 1;
                 __syncwarp();
                 if (boxes) {
                     if (lane == 0) mbar_arrive(&sh.full[slot]);
@@ -740,14 +748,27 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (lane == 0) sh.need[team][use][quarter] = need;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.dec[quarter]);
-                l = own_ref != ref && own_ref != -INFINITY ? l * ex2_approx(own_ref - ref) : l;
+                l = own_ref != ref && own_ref != -INFINITY ? mul_ex2(l, own_ref - ref) : l;
                 own_ref = ref;
                 // the team's weights before these are used up
                 ok = pg_wait_warp(&sh.p_empty[team], use ^ 1u, ab, &sh.status);
                 if (!ok) break;
                 if (active) {
                     const float off = kPgBias - (ref == -INFINITY ? 0.f : ref);
-                    float l1 = 0.f;                  // (two sums: a chain each)
+                    // The denominator takes w / scale. Beside a scale 2^90 times as large a weight may be less than a
+                    // float holds, its rank's term of the denominator not: then the term is taken for itself.
+                    const bool wide = sh.far != 0;
+                    if (__builtin_expect(wide, 0)) {
+                        float copy[32];                      // (in local memory: short code that hardly ever runs)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) copy[e] = s[e];
+#pragma unroll 1
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = copy[e];
+                            l += x == -INFINITY ? 0.f : ex2_approx(x - sh.scale[slot][32 * part + e].y + off);
+                        }
+                    }
+                    float l0 = 0.f, l1 = 0.f;        // (two sums: a chain each)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {            // 16 ranks: 16 bytes hi and 16 bytes lo
                         uint32_t hi[4], lo[4];
@@ -759,7 +780,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             for (int k = 0; k < 2; ++k) {
                                 const int e = 16 * q + 4 * e4 + 2 * k;
                                 const float w0 = ex2_approx(s[e] + off), w1 = ex2_approx(s[e + 1] + off);
-                                l = fmaf(w0, k ? i4.z : i4.x, l);
+                                l0 = fmaf(w0, k ? i4.z : i4.x, l0);
                                 l1 = fmaf(w1, k ? i4.w : i4.y, l1);
                                 // half precision holds a weight to 2^-12, and its e4m3 part exactly
                                 const __half2 x = __floats2half2_rn(w0, w1);
@@ -775,7 +796,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         *reinterpret_cast<uint4*>(prow + (((4 + ch) ^ (head & 7)) << 4)) =
                             make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    l += l1;
+                    if (!wide) l += l0 + l1;
                     const float both = l + __shfl_xor_sync(0xffffffffu, l, 16);
                     if (part == 0) {
                         sh.ref[item & 1][team][head] = ref;
@@ -928,15 +949,15 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 // references only rise within an item: the larger is the accumulator's
                 const float mu = fmaxf(ma, mb);
                 const float m2 = mu == -INFINITY ? 0.f : mu - kPgBias;
-                const float sum_l = (la == 0.f || ma == mu ? la : la * ex2_approx(ma - mu)) +
-                                    (lb == 0.f || mb == mu ? lb : lb * ex2_approx(mb - mu));
+                const float sum_l = (la == 0.f || ma == mu ? la : mul_ex2(la, ma - mu)) +
+                                    (lb == 0.f || mb == mu ? lb : mul_ex2(lb, mb - mu));
                 const float l = sum_l == 0.f ? 0.f : sum_l + sh.qodd[done & 3][h];
                 if (whole) {
                     const float sink = sinks[j];
                     // a NaN sum stays one; a sum of zero leaves the sink alone
                     const float top = l == 0.f ? sink : fmaxf(m2, sink);
                     const float base = top == -INFINITY ? 0.f : top;
-                    const float sum = l * ex2_approx(m2 - base) + (p.sink ? ex2_approx(sink - base) : 0.f);
+                    const float sum = mul_ex2(l, m2 - base) + (p.sink ? ex2_approx(sink - base) : 0.f);
                     fin[h] = sum == 0.f ? 0.f : ex2_approx(m2 - base) / sum;
                     if (quarter == 0)
                         p.lse[int64_t(t) * p.H + head0 + h] =
@@ -1101,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads) combine_paged_kernel(const PgParams 
         const int i = lane + kThreads / 4 * j;
         const float w = ml[j].y == 0.f ? 0.f : ex2_approx(ml[j].x - base);
         if (i < n) reinterpret_cast<float*>(wgt + i)[k] = w;
-        sum += w * ml[j].y;
+        if (ml[j].y != 0.f) sum += mul_ex2(ml[j].y, ml[j].x - base);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

@@ -4,6 +4,8 @@ finite or near the end of bf16's range, and tokens that see nothing.
 Models, bounds and the pool are those of test_gpu_cache.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -87,3 +89,53 @@ def test_scores_past_float_leave_masked_tokens_alone(K):
     o, lse = smla.sparse_mla_fwd_paged(q, pool.device(), _i32(table), _i32([20, 0] if K else [0, 0]), topk=topk,
                                        seq=_i32([0, 0]), scale=1e10)
     assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("T", [1, 160])                      # split over eight CTAs; several tokens a CTA
+@pytest.mark.parametrize("at", [0, 250, 511])
+def test_a_row_near_the_end_of_the_range_leaves_the_sums_alone(T, at):
+    # one row 2^130 times the others, turned away from all heads: the other fifteen rows of its block are zeros at its
+    # scale, and count in the denominator like the 496 ordinary rows, whose outputs they drown
+    rng = np.random.default_rng(85)
+    n = 512
+    q = bf16(rng.standard_normal((160, 16, 512)))
+    q[1:] = q[0]
+    rows = rng.standard_normal((n, 512)) * 2.0 ** -20
+    rows[at] = -q[0].sum(axis=0) / 4 * 2.0 ** 110
+    pool = Pool(n // 64, 64, 16, seed=86, junk=False)
+    table = pool.place([n])
+    R.write(pool.codes, pool.scales, table, [0], [0, n], bf16(rows), 64, 16)
+    o, lse = _smla().sparse_mla_fwd_paged(torch.from_numpy(q[:T]).to(torch.bfloat16).to(DEV), pool.device(), _i32(table),
+                                          _i32([n] * T), seq=_i32(np.zeros(T)))
+    _, rl, _, _ = R.attend(q[:1], pool.codes, pool.scales, table, [n], 64, 16)
+    # 511 scores of next to nothing: lse is log(511) to a few roundings of its sum and of a logarithm of 2^116 (each 2^-24
+    # of 81 nats)
+    assert np.abs(rl - np.log(511)).max() < 1e-4
+    assert np.abs(lse.double().cpu().numpy() - rl).max() <= 511 * 2.0 ** -23 + 4 * 81 * 2.0 ** -23
+    assert torch.isfinite(o).all()
+
+
+def test_rows_of_zeros_count_beside_loud_ones():
+    # rows of zeros have the least scale, 2^-100: 16,000 of them beside one row of scale 2^13 that every head
+    # gives 2^22 times the weight of a zero row
+    rng = np.random.default_rng(87)
+    n = 16016
+    d = rng.standard_normal(512)
+    d /= np.linalg.norm(d)
+    q = bf16(math.sqrt(512) * 2.0 ** -20 * (d + 1e-3 * rng.standard_normal((160, 16, 512))))
+    q[1:] = q[0]
+    rows = np.zeros((n, 512))
+    rows[n - 3] = 22 * math.log(2.0) * 2.0 ** 20 * d
+    for first in (False, True):
+        pool = Pool(-(-n // 64), 64, 16, seed=88, junk=False)
+        table = pool.place([n])
+        R.write(pool.codes, pool.scales, table, [0], [0, n], bf16(rows[::-1] if first else rows), 64, 16)
+        assert pool.scales.max() >= 2.0 ** 8 and pool.scales.min() == 2.0 ** -100
+        o, lse = _smla().sparse_mla_fwd_paged(torch.from_numpy(q).to(torch.bfloat16).to(DEV), pool.device(),
+                                              _i32(table), _i32([n] * 160), seq=_i32(np.zeros(160)))
+        ref, rl, _, _ = R.attend(q[:1], pool.codes, pool.scales, table, [n], 64, 16)
+        # without the rows of zeros lse would be log(1 + 16,000 / 2^22) = 4e-3 less; their sum's roundings are
+        # 16,000 * 2^-24 of that, lse's of 15 nats, and the score's 512 * 2^-23 of 15
+        assert np.abs(lse.double().cpu().numpy() - rl).max() <= 16000 * 2.0 ** -24 * 4e-3 + 15 * 520 * 2.0 ** -23
+        worst = np.linalg.norm(to_f64(o) - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+        assert worst.max() <= 2.0 ** -8 + 1e-3

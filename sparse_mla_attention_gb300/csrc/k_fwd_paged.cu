@@ -51,7 +51,7 @@
 // four times as far apart, where O is rescaled every few tiles):
 //   128 sequences of up to 5120 positions, 64 heads: 78 us (91), 3.3 TB/s of cache, 0.83 PFLOP/s
 //   96 of up to 6001, 16 heads: 55 us (59), 4.0 TB/s;  3 of 81920, 128 heads: 64.5 us (77), 0.90 PFLOP/s
-//   256 tokens x 512 picks, 128 heads: 74 us (82);  one token of 777 positions: 14.5 us: the two
+//   256 tokens x 512 picks, 128 heads: 76 us (83);  one token of 777 positions: 14.5 us: the two
 //   launches, the look-ups' latency, q, one tile, the output and the join.
 //
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the

@@ -408,6 +408,104 @@ int smla_cache_copy_pages(const smla_cache* cache, const int32_t* src, const int
 int smla_cache_workspace_size(const smla_cache* cache, int32_t n, size_t* bytes);
 
 /*
+ * The attention weight that each cached position gets, the statistic that
+ * smla_cache_evict goes by. The tokens t in [cu[b], cu[b+1]) belong to the
+ * sequence in table row b (token b to row b if cu is NULL; then T <= B) and
+ * see its positions [0, lens[t]), as in smla_fwd_paged, whose lse it takes:
+ *   weights[b,p] = decay * earlier[b,p] + sum_t sum_h exp(scale * <q[t,h,:], x_p> - lse[t,h])
+ * over the tokens that see p. Positions that no token of the call sees keep
+ * what weights has. earlier may be weights itself (adding up in place) and is not read with decay = 0.
+ *   q [T,H,512] bf16, cu [B+1] (cu[0] = 0, not decreasing, cu[B] <= T) or NULL, lens [T] int32,
+ *   lse [T,H] fp32, earlier and weights [B, max_pages * page_size] fp32.
+ * A head with lse = -inf (it saw nothing) adds nothing, one whose q holds an infinity or a NaN makes
+ * the sums that it goes into NaN; a token with lens[t] = 0 is not looked at.
+ * Scores and sums are fp32; q meets the codes exactly (smla_fwd_paged); dims->topk must be 0. The
+ * result is the same in every run.
+ * On the device: lens[t] outside [0, max_pages * page_size] is clamped, a sequence whose entries of cu
+ * are out of order or range has no tokens, and a position without a page of the pool gets nothing added; each sets
+ * SMLA_ERR_INDEX. workspace: smla_weights_workspace_size() bytes.
+ */
+int smla_cache_weights(const uint16_t* q, const smla_cache* cache, const int32_t* table, const int32_t* cu,
+                       const int32_t* lens, const float* lse, const float* earlier, float decay, float* weights,
+                       const smla_paged_dims* dims, void* workspace, size_t workspace_bytes, void* stream);
+
+int smla_weights_workspace_size(const smla_paged_dims* dims, size_t* bytes);
+
+/*
+ * Eviction: of every sequence min(lens[b], keep) positions stay, in fresh
+ * pages: the first `first`, the last `recent` and, of those between, the ones of largest
+ * weight (equal weights: the lower position; NaN counts least), in the order of their positions.
+ *   kept[b,i]        = the position that row i of the new sequence had, -1 behind the last
+ *   new_weights[b,i] = weights[b,kept[b,i]], 0 behind the last
+ *   new_lens[b]      = min(lens[b], keep)
+ * Codes go over as they are where the rows of a new scale block had one scale; else the block gets
+ * the largest of their scales and the others' codes are rounded to it (RNE; by a power
+ * of two for scales of smla_cache_write: exact but for e4m3 subnormals). Rows behind the last keep their bytes.
+ * The old sequences stay as they are: smla_cache_free(table) gives their pages back. Free pages
+ * are taken as by smla_cache_alloc, for the new lengths. All or nothing: with too few,
+ * SMLA_ERR_PAGES is set, new_table is filled with -1, new_lens with 0, and nothing else of the pool changes.
+ *   table, new_table [B, max_pages], lens, new_lens [B] int32, weights, new_weights
+ *   [B, max_pages * page_size] fp32, kept [B, keep] int32; 1 <= keep <= max_pages * page_size,
+ *   first + recent <= keep.
+ * On the device: lengths are clamped, and a kept position without a page of the pool becomes a row of zeros; each
+ * sets SMLA_ERR_INDEX. workspace: smla_cache_evict_workspace_size() bytes.
+ */
+int smla_cache_evict(const smla_cache* cache, const int32_t* table, const int32_t* lens, const float* weights,
+                     int32_t* new_table, int32_t* new_lens, float* new_weights, int32_t* kept, int32_t B,
+                     int32_t max_pages, int32_t keep, int32_t first, int32_t recent, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+int smla_cache_evict_workspace_size(const smla_cache* cache, int32_t B, int32_t keep, size_t* bytes);
+
+/*
+ * Reorders sequences, as after a step of beam search: row i of new_table
+ * [n, max_pages] continues the sequence in row parents[i] of table (-1: an empty row). The first
+ * child of a row takes it over as it is; every other child shares the full pages (their refcounts rise)
+ * and gets a copy of a partly filled last one; a row without a child is given back (its pages' refcounts
+ * fall). A copy goes to the partly filled last page of a row that is given back and holds it alone, in
+ * the order of rows, and when these are used up to free pages, by page number: as many
+ * sequences as before need no page more. All or nothing: with too few pages the counts stay, new_table is filled
+ * with -1, new_lens with 0 and SMLA_ERR_PAGES is set. Else the old table is void: its pages are new_table's.
+ *   new_lens[i] = lens[parents[i]]; with weights, new_weights[i,:] = weights[parents[i],:] up to
+ *   that length and 0 behind it.
+ *   table [B, max_pages], lens [B], parents [n], new_table, new_lens [n] int32; weights
+ *   [B, max_pages * page_size], new_weights [n, max_pages * page_size] fp32, or both NULL.
+ * A parent outside [-1, B) (an empty row), a length beyond the table (clamped) or a page out of range sets
+ * SMLA_ERR_INDEX, a page to share or to give back whose refcount is 0 SMLA_ERR_REFCOUNT; such pages are left out.
+ * workspace: smla_cache_reorder_workspace_size() bytes.
+ */
+int smla_cache_reorder(const smla_cache* cache, const int32_t* table, const int32_t* lens, const int32_t* parents,
+                       const float* weights, int32_t* new_table, int32_t* new_lens, float* new_weights, int32_t B,
+                       int32_t n, int32_t max_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+int smla_cache_reorder_workspace_size(int32_t B, int32_t n, size_t* bytes);
+
+/*
+ * The choice of the next beams. Row b * K + k of logits belongs to beam k of group b; its candidate v scores
+ *   scores[b,k] + logits[b*K+k,v] - log(sum_v exp(logits[b*K+k,v]))
+ * and a finished beam (done[b,k] != 0) has the one candidate v = eos, which scores scores[b,k]. The n best
+ * of a group, best first, equal scores by k, then v:
+ *   parents[b,i] = b * K + k (a row for smla_cache_reorder or smla_cache_fork), tokens[b,i] = v,
+ *   new_scores[b,i] = the score (fp32; the order is decided in 64 bits).
+ * A score that is not finite is never taken: banned tokens have logits of -inf, dead beams scores of -inf, and
+ * a row that holds a NaN or +inf has no candidates. Where fewer than n are left the rest is -1, -1, -inf.
+ *   logits [B*K, V] of `type`, row_stride elements from row to row; scores [B,K] fp32, done [B,K] bytes or NULL
+ *   (eos in [0, V) with done); outputs [B,n]. K, n <= SMLA_MAX_BEAMS, V <= SMLA_MAX_VOCAB. Rows may start at any
+ *   element; tensors need their elements' alignment only.
+ * workspace: smla_beam_workspace_size() bytes.
+ */
+#define SMLA_MAX_BEAMS 64
+#define SMLA_MAX_VOCAB 4194304
+
+enum smla_type { SMLA_F32 = 0, SMLA_BF16 = 1, SMLA_F16 = 2 };
+
+int smla_beam_select(const void* logits, int32_t type, int64_t row_stride, const float* scores, const uint8_t* done,
+                     int32_t eos, int32_t* parents, int32_t* tokens, float* new_scores, int32_t B, int32_t K,
+                     int32_t V, int32_t n, void* workspace, size_t workspace_bytes, void* stream);
+
+int smla_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t n, size_t* bytes);
+
+/*
  * Self-test of the kernels' bounded waits (the pages have no counterpart; it
  * exists so that the failure path can be exercised without faulting a GPU).
  * Launches one CTA that waits on an mbarrier nothing arrives on, through the

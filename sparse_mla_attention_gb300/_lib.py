@@ -36,6 +36,7 @@ SMLA_ERR_PAGES = 16
 SMLA_ERR_REFCOUNT = 17
 SMLA_ERR_CACHE = 18
 
+SMLA_F32, SMLA_BF16, SMLA_F16 = 0, 1, 2
 SMLA_OP_FWD, SMLA_OP_BWD, SMLA_OP_CSR, SMLA_OP_BWD_HOST = 0, 1, 2, 3
 
 EXPORTED = ("smla_workspace_size", "smla_fwd", "smla_bwd", "smla_bwd_host", "smla_csr_build",
@@ -44,7 +45,9 @@ EXPORTED = ("smla_workspace_size", "smla_fwd", "smla_bwd", "smla_bwd_host", "sml
             "smla_selftest_wait_timeout", "smla_bwd_partial", "smla_reduce_partials",
             "smla_fwd_paged", "smla_paged_workspace_size", "smla_cache_write", "smla_cache_alloc",
             "smla_cache_fork", "smla_cache_free", "smla_cache_compact", "smla_cache_copy_pages",
-            "smla_cache_workspace_size")
+            "smla_cache_workspace_size", "smla_cache_weights", "smla_weights_workspace_size",
+            "smla_cache_evict", "smla_cache_evict_workspace_size", "smla_cache_reorder",
+            "smla_cache_reorder_workspace_size", "smla_beam_select", "smla_beam_workspace_size")
 
 
 class SmlaDims(ctypes.Structure):
@@ -126,6 +129,16 @@ def load(path: str = LIB_PATH):
         lib.smla_cache_compact.argtypes = [cache_p] + [vp] * 3 + [i32] * 2 + [vp, sz, vp]
         lib.smla_cache_copy_pages.argtypes = [cache_p] + [vp] * 2 + [i32] + [vp, sz, vp]
         lib.smla_cache_workspace_size.argtypes = [cache_p, i32, ctypes.POINTER(sz)]
+        size_p = ctypes.POINTER(sz)
+        lib.smla_cache_weights.argtypes = [vp, cache_p] + [vp] * 5 + [ctypes.c_float, vp, pdims_p, vp, sz, vp]
+        lib.smla_weights_workspace_size.argtypes = [pdims_p, size_p]
+        lib.smla_cache_evict.argtypes = [cache_p] + [vp] * 7 + [i32] * 5 + [vp, sz, vp]
+        lib.smla_cache_evict_workspace_size.argtypes = [cache_p, i32, i32, size_p]
+        lib.smla_cache_reorder.argtypes = [cache_p] + [vp] * 7 + [i32] * 3 + [vp, sz, vp]
+        lib.smla_cache_reorder_workspace_size.argtypes = [i32, i32, size_p]
+        lib.smla_beam_select.argtypes = ([vp, i32, ctypes.c_int64, vp, vp, i32] + [vp] * 3 + [i32] * 4
+                                         + [vp, sz, vp])
+        lib.smla_beam_workspace_size.argtypes = [i32] * 4 + [size_p]
         for name in EXPORTED:
             if name != "smla_status_string":
                 getattr(lib, name).restype = ctypes.c_int

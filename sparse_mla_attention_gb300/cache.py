@@ -106,7 +106,19 @@ def _on_device(cache: PagedCache, workspace: Optional[Workspace], size: int) -> 
     return ws
 
 
+def _size_of(sizes: dict, key, where: str, *args) -> int:
+    """What the library's size query `where` says, asked once for each key."""
+    size = sizes.get(key)
+    if size is None:
+        out = ctypes.c_size_t(0)
+        _lib.check(getattr(_lib.load(), where)(*args, ctypes.byref(out)), where)
+        size = sizes[key] = out.value
+    return size
+
+
 _paged_sizes = {}
+_weights_sizes = {}
+_reorder_sizes = {}
 
 
 def _paged_size(dims: SmlaPagedDims) -> int:
@@ -290,3 +302,125 @@ def cache_copy_pages(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
         raise ValueError("src and dst must have the same length")
     n = src.shape[0]
     _run(cache, "smla_cache_copy_pages", cache._workspace(workspace, n), check_status, cache._ref, p_src, p_dst, n)
+
+
+def cache_weights(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, lse: torch.Tensor,
+                  weights: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
+                  earlier: Optional[torch.Tensor] = None, decay: float = 1.0, scale: Optional[float] = None,
+                  workspace: Optional[Workspace] = None, check_status: bool = True) -> torch.Tensor:
+    """The attention weight that each cached position gets from query tokens, added up over them and their heads:
+    weights = decay * earlier + sum of exp(scale <q, x> - lse) (smla_cache_weights). Returns ``weights``.
+
+    q [T,H,512] bf16, lens [T] and lse [T,H] are those of sparse_mla_fwd_paged; the tokens
+    cu_tokens[b]:cu_tokens[b+1] belong to table row b (token b without it). weights and earlier are
+    [B, max_pages * page_size] float32; without ``earlier`` the sums are added to ``weights`` itself. With decay 0
+    nothing earlier counts. Positions that no token sees keep what ``weights`` has.
+    """
+    p_q = _check(cache, q, "q", torch.bfloat16, 3)
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_lens = _check(cache, lens, "lens", torch.int32, 1)
+    p_lse = _check(cache, lse, "lse", torch.float32, 2)
+    p_weights = _check(cache, weights, "weights", torch.float32, 2)
+    T, H, D = q.shape
+    B, max_pages = table.shape
+    width = max_pages * cache.page_size
+    if lens.shape[0] != T or tuple(lse.shape) != (T, H):
+        raise ValueError("lens must have shape [T] and lse [T, H]")
+    if tuple(weights.shape) != (B, width):
+        raise ValueError("weights must have shape [B, max_pages * page_size]")
+    p_cu, p_earlier = None, p_weights
+    if cu_tokens is not None:
+        p_cu = _check(cache, cu_tokens, "cu_tokens", torch.int32, 1)
+        if cu_tokens.shape[0] != B + 1:
+            raise ValueError("cu_tokens must have shape [B+1]")
+    elif T > B:
+        raise ValueError("without cu_tokens, table must have a row for each token")
+    if earlier is not None:
+        p_earlier = _check(cache, earlier, "earlier", torch.float32, 2)
+        if earlier.shape != weights.shape:
+            raise ValueError("earlier must have the shape of weights")
+    dims = SmlaPagedDims(T, H, D, 0, B, max_pages, 0.0 if scale is None else float(scale))
+    ws = _on_device(cache, workspace, _size_of(_weights_sizes, (T, H), "smla_weights_workspace_size", dims))
+    _run(cache, "smla_cache_weights", ws, check_status, p_q, cache._ref, p_table, p_cu, p_lens, p_lse, p_earlier,
+         float(decay), p_weights, ctypes.byref(dims))
+    return weights
+
+
+def cache_evict(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, keep: int,
+                first: int = 0, recent: int = 0, workspace: Optional[Workspace] = None, check_status: bool = True,
+                out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Keep min(lens[b], keep) positions of every sequence, in fresh pages: the first ``first``, the last ``recent``
+    and, of the others, those of largest weight (smla_cache_evict). Returns (new_table, new_lens, new_weights, kept);
+    kept [B, keep] says which position each row had.
+
+    weights [B, max_pages * page_size] float32 (cache_weights). The old sequences stay as they are: cache_free gives
+    their pages back. All or nothing where free pages are short. ``out`` takes the four results.
+    """
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_lens = _check(cache, lens, "lens", torch.int32, 1)
+    p_weights = _check(cache, weights, "weights", torch.float32, 2)
+    B, max_pages = table.shape
+    if lens.shape[0] != B:
+        raise ValueError("lens must have shape [B]")
+    if tuple(weights.shape) != (B, max_pages * cache.page_size):
+        raise ValueError("weights must have shape [B, max_pages * page_size]")
+    keep, first, recent = int(keep), int(first), int(recent)
+    if not 1 <= keep <= max_pages * cache.page_size or first < 0 or recent < 0 or first + recent > keep:
+        raise ValueError("1 <= keep <= max_pages * page_size and first + recent <= keep are needed")
+    if out is None:
+        out = (torch.empty_like(table), torch.empty_like(lens), torch.empty_like(weights),
+               torch.empty((B, keep), dtype=torch.int32, device=cache.device))
+    new_table, new_lens, new_weights, kept = out
+    p_out = (_check(cache, new_table, "new_table", torch.int32, 2), _check(cache, new_lens, "new_lens", torch.int32, 1),
+             _check(cache, new_weights, "new_weights", torch.float32, 2), _check(cache, kept, "kept", torch.int32, 2))
+    if (new_table.shape != table.shape or new_lens.shape != lens.shape or new_weights.shape != weights.shape
+            or tuple(kept.shape) != (B, keep)):
+        raise ValueError("out must be (new_table like table, new_lens like lens, new_weights like weights, "
+                         "kept [B, keep])")
+    size = _size_of(cache._sizes, ("evict", B, keep), "smla_cache_evict_workspace_size", cache._ref, B, keep)
+    _run(cache, "smla_cache_evict", _on_device(cache, workspace, size), check_status, cache._ref, p_table, p_lens,
+         p_weights, *p_out, B, max_pages, keep, first, recent)
+    return new_table, new_lens, new_weights, kept
+
+
+def cache_reorder(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
+                  weights: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None,
+                  check_status: bool = True,
+                  out: Optional[Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Row i of the new table continues row parents[i] of ``table`` (-1: an empty row): (new_table [n, max_pages],
+    new_lens [n], new_weights or None) (smla_cache_reorder).
+
+    A row's first child takes it over, its other children share its full pages and get a copy of a partly filled
+    last one, and rows without a child are given back: the old table is void afterwards, unless the call ran
+    short of pages (all or nothing). With ``weights`` [B, max_pages * page_size] the accumulated weights go along.
+    """
+    p_table = _check(cache, table, "table", torch.int32, 2)
+    p_lens = _check(cache, lens, "lens", torch.int32, 1)
+    p_parents = _check(cache, parents, "parents", torch.int32, 1)
+    B, max_pages = table.shape
+    n, width = parents.shape[0], max_pages * cache.page_size
+    if lens.shape[0] != B:
+        raise ValueError("lens must have shape [B]")
+    p_weights = p_moved = None
+    if weights is not None:
+        p_weights = _check(cache, weights, "weights", torch.float32, 2)
+        if tuple(weights.shape) != (B, width):
+            raise ValueError("weights must have shape [B, max_pages * page_size]")
+    if out is None:
+        out = (table.new_empty((n, max_pages)), lens.new_empty(n),
+               None if weights is None else weights.new_empty((n, width)))
+    new_table, new_lens, new_weights = out
+    p_new = _check(cache, new_table, "new_table", torch.int32, 2)
+    p_len = _check(cache, new_lens, "new_lens", torch.int32, 1)
+    if tuple(new_table.shape) != (n, max_pages) or new_lens.shape[0] != n or (new_weights is None) != (weights is None):
+        raise ValueError("out must be (new_table [n,max_pages], new_lens [n], new_weights with weights, else None)")
+    if weights is not None:
+        p_moved = _check(cache, new_weights, "new_weights", torch.float32, 2)
+        if tuple(new_weights.shape) != (n, width):
+            raise ValueError("new_weights must have shape [n, max_pages * page_size]")
+    size = _size_of(_reorder_sizes, (B, n), "smla_cache_reorder_workspace_size", B, n)
+    _run(cache, "smla_cache_reorder", _on_device(cache, workspace, size), check_status, cache._ref, p_table, p_lens,
+         p_parents, p_weights, p_new, p_len, p_moved, B, n, max_pages)
+    return new_table, new_lens, new_weights

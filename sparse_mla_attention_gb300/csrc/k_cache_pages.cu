@@ -13,21 +13,14 @@
 // two cluster barriers: 5 to 9 us). Compaction of 40000 pages of 32 KB, 9900 of them live and
 // 7400 of these moved: 83 us, of which the copies take 69; 5.9 TB/s over all. Fork of 1024 children, each with
 // a page to copy, after a free of as many: 26 us; of 32: 13 us.
-#include <cooperative_groups.h>
-
-#include "smla_internal.cuh"
+#include "page_plan.cuh"
 #include "sm100.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace smla {
 using namespace sm100;
 
 namespace {
 
-constexpr int kPlanCtas = 8;
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kFreeEach = 4;                                   // entries of a thread of a small free
 constexpr int kFreeFew = kPlanCtas * kPlanThreads * kFreeEach;
 constexpr int kCopyThreads = 256;
@@ -36,134 +29,6 @@ constexpr int kCopySlots = 6, kCopyLag = 3;
 constexpr int kCopyBytes = 32768;                              // of a slot
 constexpr int kCopySmem = kCopySlots * kCopyBytes;
 constexpr uint64_t kCopyWaitNs = 2000000000u;
-
-struct PlanShared {
-    int warp[2][kPlanWarps];    // a scan's sums by warp; two sets in turn
-    int part;                   // this CTA's total and status bits, read by the other CTAs
-    unsigned bits;
-};
-
-// Exclusive sum over the CTA's threads in thread order; *total gets the sum. `turn`
-// alternates from scan to scan (one barrier a scan: the sums of the last but one are read).
-__device__ __forceinline__ int cta_scan(int v, PlanShared& sh, int& turn, int* total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) sh.warp[turn][warp] = x;
-    __syncthreads();
-    static_assert(kPlanWarps == 32, "a lane for each warp's sum");
-    int y = sh.warp[turn][lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, d);
-        if (lane >= d) y += z;
-    }
-    turn ^= 1;
-    *total = __shfl_sync(0xffffffffu, y, 31);
-    const int before = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
-    return (warp ? before : 0) + x - v;
-}
-
-// This CTA's share of the pages: [lo, hi), lo a multiple of 4.
-__device__ __forceinline__ void page_slice(int num_pages, int rank, int& lo, int& hi) {
-    const int per = ((num_pages + kPlanCtas - 1) / kPlanCtas + 3) / 4 * 4;
-    const int64_t a = int64_t(per) * rank, b = a + per;
-    lo = int(a < num_pages ? a : num_pages);
-    hi = int(b < num_pages ? b : num_pages);
-}
-
-// refcount[i .. i+3]; -1 past the end.
-__device__ __forceinline__ int4 load4(const int32_t* rc, int i, int hi) {
-    if (i + 4 <= hi) return __ldcg(reinterpret_cast<const int4*>(rc + i));
-    int4 v = make_int4(-1, -1, -1, -1);
-    if (i < hi) v.x = __ldcg(rc + i);
-    if (i + 1 < hi) v.y = __ldcg(rc + i + 1);
-    if (i + 2 < hi) v.z = __ldcg(rc + i + 2);
-    return v;
-}
-
-// Pages i of [lo, hi) with pred(i, refcount) (refcount -1 never counts).
-template <class Pred>
-__device__ int count_pages(const int32_t* rc, int lo, int hi, PlanShared& sh, int& turn, Pred pred) {
-    int n = 0;
-#pragma unroll 4
-    for (int i = lo + 4 * int(threadIdx.x); i < hi; i += 4 * kPlanThreads) {
-        const int4 v = load4(rc, i, hi);
-        n += int(pred(i, v.x)) + int(pred(i + 1, v.y)) + int(pred(i + 2, v.z)) + int(pred(i + 3, v.w));
-    }
-    int total;
-    cta_scan(n, sh, turn, &total);
-    return total;
-}
-
-// out(rank, i) for the pages i of [lo, hi) with pred(i, refcount), in order,
-// ranks from `rank` on, until `limit`.
-template <class Pred, class Out>
-__device__ void emit_pages(const int32_t* rc, int lo, int hi, int rank, int limit, PlanShared& sh, int& turn,
-                           Pred pred, Out out) {
-    for (int base = lo; base < hi && rank < limit; base += 4 * kPlanThreads) {
-        const int i = base + 4 * int(threadIdx.x);
-        const int4 v = load4(rc, i, hi);
-        const bool p0 = pred(i, v.x), p1 = pred(i + 1, v.y), p2 = pred(i + 2, v.z), p3 = pred(i + 3, v.w);
-        int total;
-        int r = rank + cta_scan(int(p0) + int(p1) + int(p2) + int(p3), sh, turn, &total);
-        if (p0) { if (r < limit) out(r, i); ++r; }
-        if (p1) { if (r < limit) out(r, i + 1); ++r; }
-        if (p2) { if (r < limit) out(r, i + 2); ++r; }
-        if (p3) { if (r < limit) out(r, i + 3); ++r; }
-        rank += total;
-    }
-}
-
-// The CTAs' totals: their sum, the sum over those before this one; and all status bits.
-__device__ __forceinline__ void join(cg::cluster_group& cl, PlanShared& sh, int& before, int& all, unsigned& bits) {
-    int part[kPlanCtas];
-    unsigned b[kPlanCtas];
-#pragma unroll
-    for (unsigned r = 0; r < kPlanCtas; ++r) {
-        part[r] = cl.map_shared_rank(&sh, r)->part;
-        b[r] = cl.map_shared_rank(&sh, r)->bits;
-    }
-    before = 0;
-    all = 0;
-    bits = 0;
-#pragma unroll
-    for (unsigned r = 0; r < kPlanCtas; ++r) {
-        if (r < cl.block_rank()) before += part[r];
-        all += part[r];
-        bits |= b[r];
-    }
-}
-
-// Exclusive sums of need(i), i < n, saturated at `most`; each(i, need, sum before). Returns the sum.
-template <class Need, class Each>
-__device__ int scan_needs(int n, int most, PlanShared& sh, int& turn, Need need, Each each) {
-    int64_t sum = 0;
-    for (int base = 0; base < n; base += kPlanThreads) {
-        const int i = base + int(threadIdx.x);
-        // (a row's need is below 2^20 here or the call is short of pages anyway: see callers)
-        const int v = i < n ? need(i) : 0;
-        int total;
-        const int64_t at = sum + cta_scan(v, sh, turn, &total);
-        if (i < n) each(i, v, int(at < most ? at : most));
-        sum += total;
-        if (sum > most) sum = most;
-    }
-    return int(sum);
-}
-
-__device__ __forceinline__ bool is_free(int, int rc) { return rc == 0; }
-
-// A length as pages, clamped to the table.
-__device__ __forceinline__ int clamp_len(int len, int64_t limit, unsigned& bits) {
-    if (len >= 0 && len <= limit) return len;
-    bits |= 1u << SMLA_ERR_INDEX;
-    return len < 0 ? 0 : int(limit);
-}
 
 struct CopyShared {
     uint64_t full[kCopySlots];
@@ -267,44 +132,7 @@ alloc_kernel(const CacheView c, int32_t* __restrict__ table, const int32_t* __re
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) w.need[b] = n;
     }
-    int lo, hi;
-    page_slice(c.num_pages, rank, lo, hi);
-    const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
-    bits = __syncthreads_or(bits) ? 1u << SMLA_ERR_INDEX : 0;
-    if (threadIdx.x == 0) { sh.part = mine; sh.bits = bits; }
-    cl.sync();
-    int before, have;
-    join(cl, sh, before, have, bits);
-    // A sum of 1024 needs, each cut at 2^20, fits 32 bits; a row that needs more than
-    // 2^20 pages is counted as 2^20 in the first pass only if that many are not there
-    const int cap = have < (1 << 20) ? have + 1 : (1 << 20);
-    int64_t big = 0;
-    const int want = scan_needs(B, have + 1, sh, turn,
-                                [&](int i) {
-                                    const int v = __ldcg(w.need + i);
-                                    if (v > cap) big = 1;
-                                    return v < cap ? v : cap;
-                                },
-                                [&](int i, int, int at) { if (rank == 0) w.src[i] = at; });
-    const bool huge = __syncthreads_or(int(big)) != 0 && have >= (1 << 20);
-    // (rows of more than 2^20 pages, in a pool that has as many: summed one by one)
-    int need = want;
-    if (huge) {
-        int64_t sum = 0;
-        for (int i = 0; i < B; ++i) {
-            if (rank == 0 && threadIdx.x == 0) w.src[i] = int(sum < have ? sum : have);
-            sum += __ldcg(w.need + i);
-        }
-        need = int(sum < int64_t(have) + 1 ? sum : int64_t(have) + 1);
-    }
-    const bool ok = need <= have;
-    if (ok)
-        emit_pages(c.refcount, lo, hi, before, need, sh, turn, is_free, [&](int r, int i) {
-            w.dst[r] = i;
-            c.refcount[i] = 1;
-        });
-    if (rank == 0 && threadIdx.x == 0) *status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
-    cl.sync();                                  // offsets and pages are written; parts are read
+    const bool ok = grant_pages(c, B, w.need, w.src, w.dst, bits, sh, turn, cl, status);
     if (!ok) return;
     for (int b = gw; b < B; b += kPlanCtas * kPlanWarps) {
         const int len = int(min(int64_t(max(__ldg(lens + b), 0)), limit));
@@ -627,6 +455,178 @@ copy_kernel(const CacheView c, const int32_t* __restrict__ src, const int32_t* _
                __ldcg(w.count), status);
 }
 
+// Plan of a reordering: kids[p] the children of row p, heir[p] the first of them (-2: a childless row whose last page
+// goes to a copy), w.src / w.dst the pages to copy, need[i] the place of child i's copy in them (-1: none),
+// count[0] their number (-1: too few pages).
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+reorder_plan_kernel(const ReorderArgs a) {
+    __shared__ PlanShared sh;
+    cg::cluster_group cl = cg::this_cluster();
+    grid_dep_launch();                          // the moving kernel's blocks wait for this one's end
+    const CacheView& c = a.cache;
+    const int rank = int(cl.block_rank()), first = rank * kPlanThreads + int(threadIdx.x);
+    constexpr int kStep = kPlanCtas * kPlanThreads;
+    const int64_t limit = int64_t(a.max_pages) << c.page_shift;
+    const int page_mask = (1 << c.page_shift) - 1;
+    unsigned bits = 0;
+    int turn = 0;
+    for (int p = first; p < a.B; p += kStep) {
+        __stcg(a.kids + p, 0);
+        __stcg(a.heir + p, INT32_MAX);
+    }
+    cl.sync();
+    for (int i = first; i < a.n; i += kStep) {
+        const int p = __ldg(a.parents + i);
+        if (p < 0 || p >= a.B) {
+            if (p != -1) bits |= 1u << SMLA_ERR_INDEX;
+            continue;
+        }
+        atomicAdd(a.kids + p, 1);
+        atomicMin(a.heir + p, i);
+    }
+    cl.sync();
+    for (int i = first; i < a.n; i += kStep) {
+        int e = -1;
+        const int p = __ldg(a.parents + i);
+        if (p >= 0 && p < a.B) {
+            const int len = clamp_len(__ldg(a.lens + p), limit, bits);
+            if ((len & page_mask) && __ldcg(a.heir + p) != i) {
+                e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
+                if (e < 0 || e >= c.num_pages) {
+                    bits |= 1u << SMLA_ERR_INDEX;
+                    e = -1;
+                } else if (__ldcg(c.refcount + e) <= 0) {
+                    bits |= 1u << SMLA_ERR_REFCOUNT;
+                    e = -1;
+                }
+            }
+        }
+        __stcg(a.tail + i, e);
+    }
+    for (int p = first; p < a.B; p += kStep) {
+        int e = -1;
+        if (__ldcg(a.kids + p) == 0) {
+            const int len = clamp_len(__ldg(a.lens + p), limit, bits);
+            if (len & page_mask) {
+                e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
+                if (e < 0 || e >= c.num_pages || __ldcg(c.refcount + e) != 1) e = -1;
+            }
+        }
+        __stcg(a.spare + p, e);
+    }
+    int lo, hi;
+    page_slice(c.num_pages, rank, lo, hi);
+    const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
+    const bool index = __syncthreads_or(bits & (1u << SMLA_ERR_INDEX)) != 0;
+    const bool count = __syncthreads_or(bits & (1u << SMLA_ERR_REFCOUNT)) != 0;
+    if (threadIdx.x == 0) {
+        sh.part = mine;
+        sh.bits = (index ? 1u << SMLA_ERR_INDEX : 0u) | (count ? 1u << SMLA_ERR_REFCOUNT : 0u);
+    }
+    cl.sync();
+    int before, have;
+    join(cl, sh, before, have, bits);
+    const int want = scan_needs(a.n, INT32_MAX, sh, turn,
+                                [&](int i) { return __ldcg(a.tail + i) >= 0 ? 1 : 0; },
+                                [&](int i, int need, int at) {
+                                    if (rank != 0) return;
+                                    a.need[i] = need ? at : -1;
+                                    if (need) a.src[at] = __ldcg(a.tail + i);
+                                });
+    const int spares = scan_needs(a.B, INT32_MAX, sh, turn,
+                                  [&](int p) { return __ldcg(a.spare + p) >= 0 ? 1 : 0; },
+                                  [&](int p, int need, int at) {
+                                      if (rank != 0 || !need || at >= want) return;
+                                      a.dst[at] = __ldcg(a.spare + p);
+                                      a.heir[p] = -2;
+                                  });
+    const int used = spares < want ? spares : want;
+    const bool ok = want - used <= have;
+    if (ok)
+        emit_pages(c.refcount, lo, hi, used + before, want, sh, turn, is_free, [&](int r, int i) { a.dst[r] = i; });
+    if (rank == 0 && threadIdx.x == 0) {
+        a.count[0] = ok ? want : -1;
+        *a.status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
+    }
+    cl.sync();                                  // no CTA leaves while another reads its part
+}
+
+// The new table, lengths and weights, the counts and the copies.
+__global__ void __launch_bounds__(kCopyThreads)
+reorder_kernel(const ReorderArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ CopyShared sh;
+    grid_dep_wait();
+    const CacheView& c = a.cache;
+    const int m = __ldcg(a.count);
+    const int64_t limit = int64_t(a.max_pages) << c.page_shift;
+    if (threadIdx.x >= 32) {
+        const int64_t threads = int64_t(gridDim.x) * kEntryThreads;
+        const int64_t first = int64_t(blockIdx.x) * kEntryThreads + threadIdx.x - 32;
+        unsigned bits = 0;
+        auto len_of = [&](int p) {
+            const int len = __ldg(a.lens + p);
+            return len < 0 ? 0 : len > limit ? int(limit) : len;
+        };
+        for (int64_t x = first; x < int64_t(a.n) * a.max_pages; x += threads) {
+            const int i = int(x / a.max_pages), j = int(x - int64_t(i) * a.max_pages);
+            const int p = __ldg(a.parents + i);
+            int e = -1;
+            if (m >= 0 && p >= 0 && p < a.B) {
+                const int full = len_of(p) >> c.page_shift;
+                if (__ldcg(a.heir + p) == i) {
+                    e = __ldg(a.table + int64_t(p) * a.max_pages + j);
+                } else if (j < full) {
+                    e = __ldg(a.table + int64_t(p) * a.max_pages + j);
+                    if (e < 0 || e >= c.num_pages) {
+                        bits |= 1u << SMLA_ERR_INDEX;
+                        e = -1;
+                    } else if (atomicAdd(c.refcount + e, 1) <= 0) {
+                        atomicSub(c.refcount + e, 1);
+                        bits |= 1u << SMLA_ERR_REFCOUNT;
+                        e = -1;
+                    }
+                } else if (j == full) {
+                    const int k = __ldcg(a.need + i);
+                    if (k >= 0) e = __ldcg(a.dst + k);
+                }
+            }
+            a.new_table[x] = e;
+            if (j == 0) a.new_lens[i] = m >= 0 && p >= 0 && p < a.B ? len_of(p) : 0;
+        }
+        if (m >= 0)
+            for (int64_t x = first; x < int64_t(a.B) * a.max_pages; x += threads) {
+                const int p = int(x / a.max_pages), j = int(x - int64_t(p) * a.max_pages);
+                if (__ldcg(a.kids + p) != 0) continue;
+                if (__ldcg(a.heir + p) == -2 && j == len_of(p) >> c.page_shift) continue;
+                give_back(c, __ldg(a.table + x), bits);
+            }
+        for (int64_t k = first; k < m; k += threads) {       // (a page of a row that ended has the count already)
+            const int e = __ldcg(a.dst + k);
+            if (e >= 0 && e < c.num_pages) c.refcount[e] = 1;
+        }
+        if (a.new_weights) {
+            const int64_t quads = limit / 4;
+            for (int64_t x = first; x < a.n * quads; x += threads) {
+                const int i = int(x / quads);
+                const int64_t at = x - i * quads;
+                const int p = __ldg(a.parents + i);
+                const int64_t left = m >= 0 && p >= 0 && p < a.B ? len_of(p) - 4 * at : 0;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (left > 0) v = __ldg(reinterpret_cast<const float4*>(a.weights) + p * quads + at);
+                if (left < 2) v.y = 0.f;
+                if (left < 3) v.z = 0.f;
+                if (left < 4) v.w = 0.f;
+                reinterpret_cast<float4*>(a.new_weights)[x] = v;
+            }
+        }
+        if (bits) atomicOr(a.status, bits);
+    }
+    if (m > 0)
+        copy_pairs(c, ring, sh, [&](int k) { return __ldcg(a.src + k); }, [&](int k) { return __ldcg(a.dst + k); }, m,
+                   a.status);
+}
+
 namespace {
 
 int sm_count() {
@@ -691,6 +691,17 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
     note_launch();
     return launch_early(fork_kernel, attr_done, copy_grid(c, n, int64_t(n) * max_pages), s, c, table, lens, parents,
                         child_table, B, n, max_pages, w, status);
+}
+
+cudaError_t launch_cache_reorder(const ReorderArgs& a, cudaStream_t s) {
+    reorder_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    note_launch();
+    static bool attr_done[64] = {false};
+    int64_t entries = int64_t(a.n > a.B ? a.n : a.B) * a.max_pages;
+    if (a.new_weights) entries = entries > 1 ? entries << (a.cache.page_shift - 2) : entries;
+    return launch_early(reorder_kernel, attr_done, copy_grid(a.cache, a.n, entries), s, a);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t* rows, int B, int n,

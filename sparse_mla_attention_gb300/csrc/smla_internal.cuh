@@ -229,4 +229,49 @@ struct PagedArgs {
 size_t paged_scratch_bytes(int T, int H);
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t s);
 
+// Arguments of the weights that cached positions get.
+struct WeightsArgs {
+    const uint16_t* q; CacheView cache; const int32_t* table; const int32_t* cu; const int32_t* lens;
+    const float* lse; const float* earlier; float* weights;
+    int T, H, B, max_pages;
+    float scale, decay;
+    unsigned* status;
+    char* scratch;       // workspace behind the status word
+};
+size_t weights_scratch_bytes(int T, int H);
+cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s);
+
+// Arguments of an eviction. need, start [B], fresh [num_pages], granted [1]: workspace.
+struct EvictArgs {
+    CacheView cache; const int32_t* table; const int32_t* lens; const float* weights;
+    int32_t* new_table; int32_t* new_lens; float* new_weights; int32_t* kept;
+    int B, max_pages, keep, first, recent;
+    int32_t* need; int32_t* start; int32_t* fresh; int32_t* granted;
+    unsigned* status;
+};
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
+
+// Arguments of a reordering. count [2], kids, heir, spare [B], tail, need, src, dst [n]: workspace.
+struct ReorderArgs {
+    CacheView cache; const int32_t* table; const int32_t* lens; const int32_t* parents; const float* weights;
+    int32_t* new_table; int32_t* new_lens; float* new_weights;
+    int B, n, max_pages;
+    int32_t* count; int32_t* kids; int32_t* heir; int32_t* spare; int32_t* tail; int32_t* need; int32_t* src;
+    int32_t* dst;
+    unsigned* status;
+};
+cudaError_t launch_cache_reorder(const ReorderArgs& a, cudaStream_t s);
+
+// Arguments of the choice of the next beams. peaks, sums, lists, chunks: the launcher's.
+struct BeamArgs {
+    const void* logits; int64_t stride; const float* scores; const uint8_t* done;
+    int32_t* parents; int32_t* tokens; float* new_scores;
+    int B, K, V, n, eos;
+    int chunks; float* peaks; double* sums; unsigned long long* lists;
+    unsigned* status;
+};
+size_t beam_scratch_bytes(int B, int K, int V, int n);
+int beam_chunks(int V);
+cudaError_t launch_beam_select(BeamArgs a, int type, char* scratch, cudaStream_t s);
+
 }  // namespace smla

@@ -1,107 +1,583 @@
-// k_cache_weights.cu -- the attention weight that each cached position gets.
+// k_cache_weights.cu -- the attention weight that each cached position gets, on the tensor cores.
 //
 // For sequence b with the tokens t in [cu[b], cu[b+1]) and position p < lens[t] of any of them:
 //   weights[b,p] = decay * earlier[b,p] + sum_t sum_h exp(scale * <q[t,h,:], x_p> - lse[t,h]) [p < lens[t]],
 //   x_p = e4m3 code * block scale.
+// It needs the final lse, so it cannot ride on the attention's own pass; the scores kept for it would take 2 H
+// bytes a position, where reading the row again takes 512.
 //
-// One CTA takes 16 positions, widened in shared memory; its warps take the tokens' heads in turn, and the
-// warps' sums are added in their order.
+// S^T = X Q^T: M = 128 positions (a tile of the cache as it lies, kind::f8f6f4), N = rows of q, K = 512. A position is
+// a lane of TMEM then, and the sum over tokens and heads a thread's own: no shuffles, no atomics, one order. A row of
+// garbage (behind the end, without a page) stays in its lane, so whole pages are loaded and nothing is masked before
+// the sum.
+// q is split as in the attention: a row's power of two 2^e, hi = e4m3(q / 2^e), lo = e4m3(16 (q / 2^e - hi)), hi and
+// lo as columns of one product. weights_q_kernel does that once a call and writes each chunk of up to 128 rows
+// (token, head) as the very bytes that shared memory wants, with the factors of its columns.
+//
+// weights_kernel: persistent, one CTA an SM. The units (tile, chunk of a sequence's q) are dealt out in tiles; a
+// CTA goes through its tiles once for each chunk, q staying, the cache streaming. Warps: 0-3 and 4-7 sums, on
+// alternate tiles, 8 loads, 9 products. Shared memory: q 128 KB (one chunk of 128 rows, or two of up to 64 rows in
+// turn; reloaded in quarters of K as the last tile gets done with them), ring of 6 blocks of 128 rows x 128 bytes.
+// TMEM: two buffers of 256 columns.
+//
+// Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the CTA's loops, waits (bounded) for its own
+// copies and MMAs and frees TMEM.
+#include <cfloat>
+
 #include <cuda_fp8.h>
 
 #include "smla_internal.cuh"
 #include "sm100.cuh"
+#include "tmap.h"
 
 namespace smla {
 using namespace sm100;
 
 namespace {
 
-constexpr int kCwTile = 16, kCwThreads = 256, kCwWarps = kCwThreads / 32;
+constexpr uint32_t kCwWaitNs = 2000000000u;
 constexpr float kCwLog2e = 1.4426950408889634f;
+constexpr int kCwTile = 128;                     // positions
+constexpr int kCwRows = 128;                     // rows of q of a chunk at most
+constexpr int kCwSlots = 6, kCwSlotBytes = kCwTile * 128;
+constexpr int kCwQSlots = 8, kCwQSlotBytes = 16384;
+constexpr int kCwLoadWarp = 8, kCwMmaWarp = 9, kCwThreads = 320;
+constexpr int kCwSplitThreads = 256;
+constexpr int kCwMaxBlocks = 1024;               // of the splitting kernel
 
-}  // namespace
+struct CwShared {
+    uint64_t full[kCwSlots], empty[kCwSlots];
+    uint64_t q_full[kCwQSlots], q_empty[kCwQSlots];
+    uint64_t f_full[2], f_empty[2];              // the factors of a chunk's columns
+    uint64_t t_full[2], t_empty[2], drain;
+    uint32_t tbase;
+    volatile int abort_flag;
+    int b0;                                      // first sequence with work of this CTA
+    int64_t at0, lo, hi;                         // its first unit; the CTA's units
+    int64_t sum[kCwThreads / 32];
+};
 
-__global__ void __launch_bounds__(kCwThreads)
-cache_weights_kernel(const WeightsArgs a) {
-    __shared__ float x[kCwTile][kD];
-    __shared__ float part[kCwWarps][kCwTile];
-    __shared__ int row_of[kCwTile];
-    const CacheView& c = a.cache;
+constexpr int kCwQAt = kCwSlots * kCwSlotBytes;
+constexpr int kCwFactorAt = kCwQAt + kCwQSlots * kCwQSlotBytes;
+constexpr int kCwSharedAt = kCwFactorAt + 2 * kCwRows * int(sizeof(float2));
+constexpr int kCwSmem = kCwSharedAt + int(sizeof(CwShared));
+static_assert(kCwSmem <= 232448, "shared memory of one CTA is at most 227 KB");
+
+struct CwParams {
+    WeightsArgs a;
+    uint8_t* image;                              // [T * H] rows of q as shared memory has them, 1 KB each
+    float2* factor;                              // [T * H] score factor, -lse in log2 units
+    int32_t* seen;                               // [B] positions that a sequence's tokens see; 0: nothing to do
+    unsigned* bits;                              // status bits of each block of the splitting kernel
+    int blocks;
+};
+
+__device__ __forceinline__ bool cw_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint32_t t0 = globaltimer_lo_ns();
+        do {
+#pragma unroll 1
+            for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+            if (!ok && globaltimer_lo_ns() - t0 > kCwWaitNs) {
+                *abort_flag = 1;
+                flag_status(status, SMLA_ERR_TIMEOUT);
+            }
+        } while (!ok && !*abort_flag);
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+__device__ __forceinline__ int cw_len(const WeightsArgs& a, int t) {
+    const int64_t limit = int64_t(a.max_pages) << a.cache.page_shift;
+    const int len = __ldg(a.lens + t);
+    return len < 0 ? 0 : len > limit ? int(limit) : len;
+}
+
+// Sequence b's tokens; false if its entries of cu are out of order or range.
+__device__ __forceinline__ bool cw_tokens(const WeightsArgs& a, int b, int& c0, int& c1) {
+    c0 = b < a.T ? b : a.T;
+    c1 = b < a.T ? b + 1 : a.T;
+    if (!a.cu) return true;
+    c0 = __ldg(a.cu + b);
+    c1 = __ldg(a.cu + b + 1);
+    return c0 >= 0 && c1 >= c0 && c1 <= a.T;
+}
+
+// Rows of a sequence's chunks (but for the last): up to 64 rows are one chunk and need half of the room.
+__device__ __forceinline__ int cw_chunk_rows(int rows) { return rows <= kCwRows / 2 ? rows : kCwRows; }
+
+__device__ __forceinline__ uint32_t cw_e4m3x2(__half2 v) {
+    return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 cw_e4m3x2_half(uint32_t v) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3));
+}
+
+// Where a CTA's work lies: items (sequence b, its tiles [k0, k1)), all chunks of each.
+struct CwWalk {
+    int b, c0, c1, seen, tiles, k0, k1;
+    int rows, chunk_rows, chunks;
+    int64_t at, lo, hi;
+    __device__ __forceinline__ CwWalk(const CwShared& sh) : b(sh.b0 - 1), tiles(0), chunks(0), at(sh.at0), lo(sh.lo), hi(sh.hi) {}
+    __device__ __forceinline__ bool next(const CwParams& p) {
+        at += int64_t(tiles) * chunks;
+        do {
+            ++b;
+            if (at >= hi || b >= p.a.B) return false;
+            seen = __ldcg(p.seen + b);
+            if (seen == 0) { tiles = 0; k0 = k1 = 0; continue; }
+            cw_tokens(p.a, b, c0, c1);
+            rows = (c1 - c0) * p.a.H;
+            chunk_rows = cw_chunk_rows(rows);
+            chunks = (rows + chunk_rows - 1) / chunk_rows;
+            tiles = (seen + kCwTile - 1) / kCwTile;
+            // tile k is whose the unit at + k * chunks is
+            k0 = at >= lo ? 0 : int(min(int64_t(tiles), (lo - at + chunks - 1) / chunks));
+            k1 = int(min(int64_t(tiles), (hi - at + chunks - 1) / chunks));
+            if (k0 >= k1) at += int64_t(tiles) * chunks;
+        } while (k0 >= k1);
+        return true;
+    }
+    __device__ __forceinline__ int chunk_size(int j) const {
+        const int left = rows - j * chunk_rows;
+        return left < chunk_rows ? left : chunk_rows;
+    }
+};
+
+__device__ __forceinline__ int64_t cw_units(const CwParams& p, int b) {
+    const int seen = __ldcg(p.seen + b);
+    if (seen == 0) return 0;
+    int c0, c1;
+    cw_tokens(p.a, b, c0, c1);
+    const int rows = (c1 - c0) * p.a.H, per = cw_chunk_rows(rows);
+    return int64_t((seen + kCwTile - 1) / kCwTile) * ((rows + per - 1) / per);
+}
+
+// The CTA's share of the units and the sequence that it begins in.
+__device__ void cw_locate(const CwParams& p, CwShared& sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t width = int64_t(a.max_pages) << c.page_shift, tiles = width / kCwTile;
-    if (a.B == 0) return;
-    for (int64_t u = blockIdx.x; u < a.B * tiles; u += gridDim.x) {
-        const int b = int(u / tiles);
-        const int64_t p0 = (u - b * tiles) * kCwTile;
-        int c0 = b, c1 = b < a.T ? b + 1 : b;
-        if (a.cu) { c0 = __ldg(a.cu + b); c1 = __ldg(a.cu + b + 1); }
-        if (c0 < 0 || c1 < c0 || c1 > a.T) {
-            if (p0 == 0 && threadIdx.x == 0) flag_status(a.status, SMLA_ERR_INDEX);
-            continue;
+    const int run = (p.a.B + kCwThreads - 1) / kCwThreads;
+    const int b0 = int(min(int64_t(threadIdx.x) * run, int64_t(p.a.B))), b1 = min(b0 + run, p.a.B);
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += cw_units(p, b);
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) sh.sum[warp] = x;
+    if (threadIdx.x == 0) sh.b0 = p.a.B;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kCwThreads / 32; ++w) {
+        if (w < warp) before += sh.sum[w];
+        total += sh.sum[w];
+    }
+    int64_t at = before + x - mine;
+    const int64_t per = total / gridDim.x, rem = total - per * gridDim.x, c = blockIdx.x;
+    const int64_t lo = per * c + min(c, rem), hi = lo + per + (c < rem ? 1 : 0);
+    if (threadIdx.x == 0) { sh.lo = lo; sh.hi = hi; }
+    if (lo < hi && at <= lo && lo < at + mine) {
+        int b = b0;
+        for (int64_t n = cw_units(p, b); lo >= at + n; n = cw_units(p, b)) {
+            at += n;
+            ++b;
         }
-        int64_t seen = 0;
-        for (int t = c0; t < c1; ++t) {
-            const int len = __ldg(a.lens + t);
-            if ((len < 0 || len > width) && p0 == 0 && threadIdx.x == 0) flag_status(a.status, SMLA_ERR_INDEX);
-            seen = max(seen, min(int64_t(len), width));
-        }
-        if (p0 >= seen) continue;
-        __syncthreads();
-        if (threadIdx.x < kCwTile) {
-            const int64_t p = p0 + threadIdx.x;
-            const int page = p < seen ? __ldg(a.table + b * int64_t(a.max_pages) + (p >> c.page_shift)) : -1;
-            const bool there = page >= 0 && page < c.num_pages;
-            if (p < seen && !there) flag_status(a.status, SMLA_ERR_INDEX);
-            row_of[threadIdx.x] = there ? (page << c.page_shift) + int(p & ((1 << c.page_shift) - 1)) : -1;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < kCwTile * kD; i += kCwThreads) {
-            const int r = i / kD, row = row_of[r];
-            __nv_fp8_e4m3 code;
-            code.__x = row < 0 ? 0 : c.pages[int64_t(row) * kD + i % kD];
-            x[r][i % kD] = row < 0 ? 0.f : float(code) * c.scales[row >> c.block_shift];
-        }
-        __syncthreads();
-        float sum = 0.f;                         // of position p0 + lane
-        for (int64_t k = int64_t(c0) * a.H + warp; k < int64_t(c1) * a.H; k += kCwWarps) {
-            const int len = __ldg(a.lens + k / a.H);
-            if (p0 >= len) continue;
-            const float lse = __ldg(a.lse + k);
-            float q[16];
-            bool odd = false;                    // an infinity or a NaN makes the head's weights NaN
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t bits = a.q[k * kD + lane + 32 * e];
-                q[e] = __uint_as_float(bits << 16);
-                odd |= (bits & 0x7f80u) == 0x7f80u;
-            }
-            odd = __any_sync(0xffffffffu, odd) != 0;
-            for (int r = 0; r < kCwTile; ++r) {
-                float s = odd ? __int_as_float(0x7fffffff) : 0.f;
-                for (int e = 0; e < 16; ++e) s = fmaf(q[e], x[r][lane + 32 * e], s);
-                for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                if (lane == r && p0 + r < len && lse != -INFINITY && row_of[r] >= 0)
-                    sum += exp2f((s * a.scale - lse) * kCwLog2e);
-            }
-        }
-        if (lane < kCwTile) part[warp][lane] = sum;
-        __syncthreads();
-        if (threadIdx.x < kCwTile && p0 + threadIdx.x < seen) {
-            const int64_t at = b * width + p0 + threadIdx.x;
-            float total = a.decay != 0.f ? a.decay * a.earlier[at] : 0.f;
-            for (int w = 0; w < kCwWarps; ++w) total += part[w][threadIdx.x];
-            a.weights[at] = total;
-        }
+        sh.b0 = b;
+        sh.at0 = at;
     }
 }
 
-size_t weights_scratch_bytes(int, int) { return 0; }
+}  // namespace
+
+// q into parts, and what the sequences see.
+__global__ void __launch_bounds__(kCwSplitThreads)
+weights_q_kernel(const CwParams p) {
+    const WeightsArgs& a = p.a;
+    const int lane = threadIdx.x & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t warps = int64_t(gridDim.x) * (kCwSplitThreads / 32);
+    const int64_t first = int64_t(blockIdx.x) * (kCwSplitThreads / 32) + (threadIdx.x >> 5);
+    const int64_t limit = int64_t(a.max_pages) << a.cache.page_shift;
+    bool bad = false;
+    for (int64_t g = first; g < int64_t(a.T) * a.H; g += warps) {
+        const int t = int(g / a.H);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + g * kD) + 2 * lane;
+        const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+        const float lse = __ldg(a.lse + g);
+        int b = t;
+        if (a.cu) {
+            // the last b with cu[b] <= t, 32 probes at a time
+            b = 0;
+            for (int above = a.B; above - b > 1;) {
+                const int step = (above - b + 31) / 32, mid = b + lane * step;
+                const bool yes = mid < above && (lane == 0 || __ldg(a.cu + mid) <= t);
+                b += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
+                above = min(above, b + step);
+            }
+        }
+        int c0, c1;
+        if (!cw_tokens(a, b, c0, c1) || t < c0 || t >= c1) continue;
+        uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+        top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+        // the least 2^e with top <= 448 * 2^e (448 = 1.75 * 2^8)
+        int e = int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+        const bool odd = top >= 0x7f80u, blind = lse == -INFINITY;
+        e = odd || top == 0 ? 0 : e < -100 ? -100 : e;           // (120 at most)
+        const float inv = __int_as_float((127 - e) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (odd || blind) w[i] = 0;
+            // half precision holds a scaled value and what e4m3 leaves of it exactly
+            const __half2 v = __floats2half2_rn(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+            const uint32_t h = cw_e4m3x2(v);
+            const uint32_t l = cw_e4m3x2(__hmul2(__hsub2(v, cw_e4m3x2_half(h)), __float2half2_rn(16.f)));
+            if (i & 1) { hi[i >> 1] |= h << 16; lo[i >> 1] |= l << 16; } else { hi[i >> 1] = h; lo[i >> 1] = l; }
+        }
+        const int rows = (c1 - c0) * a.H, per = cw_chunk_rows(rows);
+        const int64_t g0 = int64_t(c0) * a.H;
+        const int l = int((g - g0) % per), left = rows - (int(g - g0) - l), r = left < per ? left : per;
+        // K block (8 lanes each), rows hi then rows lo, 16-byte pieces swizzled
+        uint8_t* at = p.image + (g - l) * 1024 + (lane >> 3) * (r * 256);
+        *reinterpret_cast<uint4*>(at + l * 128 + (((lane & 7) ^ (l & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + (r + l) * 128 + (((lane & 7) ^ (l & 7)) << 4)) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);                // (r is a multiple of 16)
+        if (lane == 0)
+            p.factor[g] = make_float2(odd && !blind ? __int_as_float(0x7fffffff)
+                                                    : fminf(__int_as_float((127 + e) << 23) * a.scale * kCwLog2e, FLT_MAX),
+                                      blind ? -INFINITY : -lse * kCwLog2e);
+    }
+    for (int64_t b = first; b < a.B; b += warps) {
+        int c0, c1, most = 0;
+        const bool ok = cw_tokens(a, int(b), c0, c1);
+        bad |= !ok;
+        for (int t = c0 + lane; ok && t < c1; t += 32) {
+            const int len = __ldg(a.lens + t);
+            bad |= len < 0 || len > limit;
+            most = max(most, cw_len(a, t));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) p.seen[b] = most;
+    }
+    bad = __syncthreads_or(bad) != 0;
+    if (threadIdx.x == 0) {
+        p.bits[blockIdx.x] = bad ? 1u << SMLA_ERR_INDEX : 0u;
+        if (blockIdx.x == 0) *a.status = 0;      // the other kernel adds to it
+    }
+}
+
+__global__ void __launch_bounds__(kCwThreads, 1)
+weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
+    extern __shared__ __align__(1024) uint8_t ring[];
+    CwShared& sh = *reinterpret_cast<CwShared*>(ring + kCwSharedAt);
+    uint8_t* qbuf = ring + kCwQAt;
+    float2* factors = reinterpret_cast<float2*>(ring + kCwFactorAt);
+    const WeightsArgs& a = p.a;
+    const CacheView& c = a.cache;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* ab = &sh.abort_flag;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kCwSlots; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
+        for (int i = 0; i < kCwQSlots; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.f_full[i], 1);
+            mbar_init(&sh.f_empty[i], 8);
+            mbar_init(&sh.t_full[i], 1);
+            mbar_init(&sh.t_empty[i], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kCwMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
+    grid_dep_wait();
+    cw_locate(p, sh);
+    if (blockIdx.x == 0 && threadIdx.x < 32) {
+        unsigned bits = 0;
+        for (int i = lane; i < p.blocks; i += 32) bits |= __ldcg(p.bits + i);
+        if (bits) atomicOr(a.status, bits);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sh.tbase;
+    const int page_mask = (1 << c.page_shift) - 1;
+    const int box_rows = page_mask + 1 < kCwTile ? page_mask + 1 : kCwTile;
+    CwWalk w(sh);
+
+    if (warp == kCwLoadWarp) {
+        // --------------------------------------------------------------- loads
+        uint32_t use = 0, q_uses = 0, f_uses = 0;       // q_uses: a parity bit a slot
+        int next_half = 0;
+        bool ok = true;
+        const int boxes = kCwTile / box_rows;
+        while (ok && w.next(p)) {
+            // lane's page of a tile: of the rows [lane * box_rows, ...)
+            auto row_of = [&](int k) {
+                const int64_t pos = int64_t(k) * kCwTile + lane * box_rows;
+                if (lane >= boxes || pos >= w.seen) return -1;
+                const int page = __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift));
+                return page >= 0 && page < c.num_pages ? (page << c.page_shift) + int(pos & page_mask) : -1;
+            };
+            int row = row_of(w.k0);
+            for (int j = 0; j < w.chunks && ok; ++j) {
+                const int r = w.chunk_size(j), f = f_uses & 1;
+                const int64_t g = (int64_t(w.c0) * a.H) + int64_t(j) * w.chunk_rows;
+                const bool big = r > kCwRows / 2;
+                ok = cw_wait(&sh.f_empty[f], ((f_uses >> 1) & 1u) ^ 1u, ab, a.status);
+                if (!ok) break;
+                ++f_uses;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.f_full[f], uint32_t(r) * 8);
+                    bulk_load(factors + f * kCwRows, p.factor + g, uint32_t(r) * 8, &sh.f_full[f]);
+                }
+                for (int k = w.k0; k < w.k1 && ok; ++k) {
+                    const int next_row = row_of(k + 1 < w.k1 ? k + 1 : w.k0);
+                    const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
+#pragma unroll 1
+                    for (int kb = 0; kb < 4; ++kb) {
+                        if (k == w.k0) {
+                            // the chunk's part of q: slots 2 kb and the next, or slot kb of a half
+                            const int s = big ? 2 * kb : 4 * next_half + kb;
+                            ok = cw_wait(&sh.q_empty[s], ((q_uses >> s) & 1u) ^ 1u, ab, a.status);
+                            if (ok && big) ok = cw_wait(&sh.q_empty[s + 1], ((q_uses >> (s + 1)) & 1u) ^ 1u, ab, a.status);
+                            if (!ok) break;
+                            q_uses ^= (big ? 3u : 1u) << s;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&sh.q_full[s], uint32_t(r) * 256);
+                                bulk_load(qbuf + s * kCwQSlotBytes, p.image + g * 1024 + kb * (r * 256),
+                                          uint32_t(r) * 256, &sh.q_full[s]);
+                                if (big) mbar_arrive(&sh.q_full[s + 1]);
+                            }
+                        }
+                        const int slot = int(use % kCwSlots);
+                        ok = cw_wait(&sh.empty[slot], ((use / kCwSlots) & 1u) ^ 1u, ab, a.status);
+                        if (!ok) break;
+                        ++use;
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], uint32_t(live * box_rows) * 128);
+                        __syncwarp();
+                        if (row >= 0)
+                            tma_load_2d(ring + slot * kCwSlotBytes + lane * box_rows * 128, &map_box, kb * 128, row,
+                                        &sh.full[slot]);
+                        __syncwarp();
+                    }
+                    row = next_row;
+                }
+                if (!big) next_half ^= 1;
+            }
+        }
+        __syncwarp();
+        if (sh.abort_flag) {                     // the loads already issued land before the CTA exits
+            for (uint32_t n = use > kCwSlots ? use - kCwSlots : 0; n < use; ++n)
+                mbar_wait(&sh.full[n % kCwSlots], (n / kCwSlots) & 1u, kCwWaitNs / 8);
+            for (int i = 0; i < kCwQSlots; ++i) mbar_wait(&sh.q_full[i], ((q_uses >> i) & 1u) ^ 1u, kCwWaitNs / 8);
+            for (uint32_t n = f_uses > 2 ? f_uses - 2 : 0; n < f_uses; ++n)
+                mbar_wait(&sh.f_full[n & 1], (n >> 1) & 1u, kCwWaitNs / 8);
+        }
+        __syncwarp();
+    } else if (warp == kCwMmaWarp) {
+        // ------------------------------------------------------------ products
+        const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(qbuf), 16, 1024);
+        const bool leader = elect_one();
+        uint32_t use = 0, q_uses = 0, t_uses[2] = {0, 0};
+        int half = 0;
+        bool ok = true;
+        while (ok && w.next(p)) {
+            for (int j = 0; j < w.chunks && ok; ++j) {
+                const int r = w.chunk_size(j);
+                const bool big = r > kCwRows / 2;
+                const uint32_t idesc = idesc_f8(128, 2 * r, false, false);
+                const uint32_t q_next = q_uses ^ (big ? 0xffu : 0xfu << (4 * half));
+                for (int k = w.k0; k < w.k1 && ok; ++k) {
+                    const int buf = (k - w.k0) & 1;
+                    const uint32_t uses = buf ? t_uses[1] : t_uses[0];
+                    ok = cw_wait(&sh.t_empty[buf], (uses & 1u) ^ 1u, ab, a.status);
+                    if (buf) ++t_uses[1]; else ++t_uses[0];
+#pragma unroll 1
+                    for (int kb = 0; kb < 4 && ok; ++kb) {
+                        const int s = big ? 2 * kb : 4 * half + kb;
+                        if (k == w.k0) {
+                            ok = cw_wait(&sh.q_full[s], (q_uses >> s) & 1u, ab, a.status);
+                            if (ok && big) ok = cw_wait(&sh.q_full[s + 1], (q_uses >> (s + 1)) & 1u, ab, a.status);
+                            if (!ok) break;
+                        }
+                        const int slot = int(use % kCwSlots);
+                        ok = cw_wait(&sh.full[slot], (use / kCwSlots) & 1u, ab, a.status);
+                        if (!ok) break;
+                        ++use;
+                        tc_fence_after();
+                        const uint64_t xa = ring_desc + uint32_t(slot) * (kCwSlotBytes >> 4);
+                        const uint64_t qa = q_desc + uint32_t(s) * (kCwQSlotBytes >> 4);
+                        if (leader) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_f8_ss(tbase + 256 * buf, xa + 2 * i, qa + 2 * i, idesc, (kb | i) != 0);
+                            mma_commit(&sh.empty[slot]);
+                            if (k == w.k1 - 1) {
+                                mma_commit(&sh.q_empty[s]);
+                                if (big) mma_commit(&sh.q_empty[s + 1]);
+                            }
+                            if (kb == 3) mma_commit(&sh.t_full[buf]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                q_uses = q_next;
+                if (!big) half ^= 1;
+            }
+        }
+        if (leader) {
+            mma_commit(&sh.drain);
+            mbar_wait(&sh.drain, 0, kCwWaitNs);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- sums
+        const int team = warp >> 2, quarter = warp & 3;
+        const uint32_t trow = tbase + 256 * team + (uint32_t(quarter * 32) << 16);
+        const int64_t width = int64_t(a.max_pages) << c.page_shift;
+        uint32_t f_uses = 0, t_uses = 0;
+        bool ok = true, bad = false;
+        while (ok && w.next(p)) {
+            const int64_t line = w.b * width;
+            // this thread's position of tile k: its block scale (-1: none), and what to add to
+            auto scale_of = [&](int k) {
+                const int64_t pos = int64_t(k) * kCwTile + 32 * quarter + lane;
+                if (k >= w.k1 || pos >= w.seen) return -1.f;
+                const int page = __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift));
+                if (page < 0 || page >= c.num_pages) { bad = true; return -1.f; }
+                return __ldg(c.scales + (((page << c.page_shift) + int(pos & page_mask)) >> c.block_shift));
+            };
+            float next_scale = scale_of(w.k0 + team);
+            for (int j = 0; j < w.chunks && ok; ++j) {
+                const int r = w.chunk_size(j), f = f_uses & 1;
+                // positions that every token of the chunk sees
+                const int t0 = w.c0 + j * w.chunk_rows / a.H, t1 = w.c0 + (j * w.chunk_rows + r - 1) / a.H;
+                int least = INT32_MAX;
+                for (int t = t0 + lane; t <= t1; t += 32) least = min(least, cw_len(a, t));
+                least = __reduce_min_sync(0xffffffffu, least);
+                ok = cw_wait(&sh.f_full[f], (f_uses >> 1) & 1u, ab, a.status);
+                if (!ok) break;
+                ++f_uses;
+                const float2* fac = factors + f * kCwRows;
+                for (int k = w.k0 + team; k < w.k1; k += 2) {
+                    const int64_t pos = int64_t(k) * kCwTile + 32 * quarter + lane;
+                    const float scale = next_scale;
+                    next_scale = scale_of(k + 2 < w.k1 ? k + 2 : w.k0 + team);
+                    float sum = 0.f;
+                    if (pos < w.seen) {
+                        if (j > 0) sum = a.weights[line + pos];
+                        else if (a.decay != 0.f) sum = a.decay * a.earlier[line + pos];
+                    }
+                    ok = cw_wait(&sh.t_full[team], t_uses & 1u, ab, a.status);
+                    if (!ok) break;
+                    ++t_uses;
+                    tc_fence_after();
+                    const bool all = (k + 1) * int64_t(kCwTile) <= least;
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int n = 0; n < r; n += 16) {
+                        uint32_t hi[16], lo[16];
+                        tmem_ld16(trow + n, hi);
+                        tmem_ld16(trow + r + n, lo);
+                        tmem_wait_ld();
+                        // (tokens have multiples of 16 rows)
+                        const bool sees = all || pos < cw_len(a, w.c0 + (j * w.chunk_rows + n) / a.H);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 x = fac[n + e];
+                            const float s = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e]));
+                            const float v = ex2_approx(fmaf(s * scale, x.x, x.y));
+                            part[e & 3] += sees ? v : 0.f;
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.t_empty[team]);
+                    if (scale >= 0.f) sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    if (pos < w.seen) a.weights[line + pos] = sum;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.f_empty[f]);
+            }
+        }
+        if (bad) flag_status(a.status, SMLA_ERR_INDEX);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kCwMmaWarp) tmem_dealloc(tbase, 512);
+}
+
+namespace {
+
+struct CwPlan { size_t image, factor, seen, bits, bytes; };
+
+CwPlan plan_weights(int64_t T, int64_t H, int64_t B) {
+    CwPlan x{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes > 0 ? bytes : 1, 256); return o; };
+    x.image = take(size_t(T) * H * 1024);
+    x.factor = take(size_t(T) * H * sizeof(float2));
+    x.seen = take(size_t(B) * 4);
+    x.bits = take(size_t(kCwMaxBlocks) * 4);
+    x.bytes = off;
+    return x;
+}
+
+}  // namespace
+
+size_t weights_scratch_bytes(int T, int H, int B) { return plan_weights(T, H, B).bytes; }
 
 cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s) {
-    const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(unsigned), s);
+    static bool attr_done[64] = {false};
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCwSmem);
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+    }
+    const CwPlan plan = plan_weights(a.T, a.H, a.B);
+    const CacheView& c = a.cache;
+    CUtensorMap mb;
+    const uint32_t box = (1 << c.page_shift) < kCwTile ? uint32_t(1) << c.page_shift : uint32_t(kCwTile);
+    if (!make_tmap_u8_rows(&mb, c.pages, uint64_t(c.num_pages) << c.page_shift, box)) return cudaErrorInvalidValue;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    CwParams p{};
+    p.a = a;
+    p.image = reinterpret_cast<uint8_t*>(a.scratch + plan.image);
+    p.factor = reinterpret_cast<float2*>(a.scratch + plan.factor);
+    p.seen = reinterpret_cast<int32_t*>(a.scratch + plan.seen);
+    p.bits = reinterpret_cast<unsigned*>(a.scratch + plan.bits);
+    const int64_t rows = int64_t(a.T) * a.H, most = rows > a.B ? rows : a.B;
+    const int64_t blocks = (most + kCwSplitThreads / 32 - 1) / (kCwSplitThreads / 32);
+    p.blocks = int(blocks < kCwMaxBlocks ? blocks : kCwMaxBlocks);
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.blocks);
+    cfg.blockDim = dim3(kCwSplitThreads);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, weights_q_kernel, p);
     if (e != cudaSuccess) return e;
-    cache_weights_kernel<<<152 * 6, kCwThreads, 0, s>>>(a);
-    note_launch();
-    return cudaGetLastError();
+    cfg.gridDim = dim3(sms);
+    cfg.blockDim = dim3(kCwThreads);
+    cfg.dynamicSmemBytes = kCwSmem;
+    note_launch(2);
+    return cudaLaunchKernelEx(&cfg, weights_kernel, mb, p);
 }
 
 }  // namespace smla

@@ -6,10 +6,10 @@
 // A row's candidates rank as its logits do, so one pass over the logits gives both parts of the answer:
 // beam_rows_kernel cuts a row into chunks, keeps a chunk's values in registers, and writes its maximum, its sum of
 // exponentials and its n best logits; beam_merge_kernel joins a row's sums and merges the lists of a group.
-// Which candidate comes first is decided in 64 bits: sums of 33 exponentials in 32 bits, the rest in 64.
+// Which candidate comes first is decided in 64 bits: a thread's sum of up to 65 exponentials in 32 bits, the rest in 64.
 //
 // A chunk's n best: a bound that n to 2n threads' largest values reach (bisection over their bits, a count and a
-// barrier a step), so that at most 66 n values pass it, then their exact ranks among those.
+// barrier a step), so that at most 2 n threads' values pass it, then their exact ranks among those.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,8 +22,10 @@ using namespace sm100;
 namespace {
 
 constexpr int kBsThreads = 256;
-constexpr int kBsPer = 32;                       // values of a thread, beside one at the row's ends
-constexpr int kBsMergeThreads = 256;
+constexpr int kBsVecs = 8;                       // 16-byte vectors of a thread, beside one value at the row's ends
+constexpr int kBsMergeThreads = 512;
+constexpr int kBsEach = 4;                       // candidates of a thread of the merge
+constexpr int kBsBatch = kBsMergeThreads * kBsEach;
 constexpr float kBsLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -34,12 +36,40 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
+// Two floats at a time.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 floats_of(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// What a type's 16-byte vectors hold; kNone: words of -inf.
 template <int kType>
 struct Logit;
 template <>
 struct Logit<SMLA_F32> {
     static constexpr int kSize = 4;
+    static constexpr uint32_t kNone = 0xff800000u;
     static __device__ __forceinline__ float one(const uint8_t* p) { return __ldg(reinterpret_cast<const float*>(p)); }
+    static __device__ __forceinline__ float top(const uint4& x) {
+        return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
+                     fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+    }
     static __device__ __forceinline__ void spread(const uint4& x, float* v) {
         v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
         v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
@@ -48,8 +78,14 @@ struct Logit<SMLA_F32> {
 template <>
 struct Logit<SMLA_BF16> {
     static constexpr int kSize = 2;
+    static constexpr uint32_t kNone = 0xff80ff80u;
     static __device__ __forceinline__ float one(const uint8_t* p) {
         return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
+    }
+    static __device__ __forceinline__ float top(const uint4& x) {
+        auto as = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(as(x.x), as(x.y)), __hmax2(as(x.z), as(x.w)));
+        return fmaxf(__low2float(m), __high2float(m));
     }
     static __device__ __forceinline__ void spread(const uint4& x, float* v) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -60,8 +96,14 @@ struct Logit<SMLA_BF16> {
 template <>
 struct Logit<SMLA_F16> {
     static constexpr int kSize = 2;
+    static constexpr uint32_t kNone = 0xfc00fc00u;
     static __device__ __forceinline__ float one(const uint8_t* p) {
         return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(p))));
+    }
+    static __device__ __forceinline__ float top(const uint4& x) {
+        auto as = [](uint32_t w) { return *reinterpret_cast<const __half2*>(&w); };
+        const float2 m = __half22float2(__hmax2(__hmax2(as(x.x), as(x.y)), __hmax2(as(x.z), as(x.w))));
+        return fmaxf(m.x, m.y);
     }
     static __device__ __forceinline__ void spread(const uint4& x, float* v) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -73,6 +115,10 @@ struct Logit<SMLA_F16> {
     }
 };
 
+constexpr int chunk_of(int type) { return kBsThreads * kBsVecs * (type == SMLA_F32 ? 4 : 8); }
+// values that pass a chunk's bound at most: those of 2 n threads
+constexpr size_t passing(int type, int n) { return size_t(2) * n * (kBsVecs * (type == SMLA_F32 ? 4 : 8) + 1); }
+
 __device__ __forceinline__ bool out_of_play(const BeamArgs& a, int row) {
     const float s = __ldg(a.scores + row);
     return !(fabsf(s) < INFINITY) || (a.done && __ldg(a.done + row));
@@ -83,14 +129,14 @@ __device__ __forceinline__ bool out_of_play(const BeamArgs& a, int row) {
 template <int kType>
 __global__ void __launch_bounds__(kBsThreads)
 beam_rows_kernel(const BeamArgs a) {
-    constexpr int kSize = Logit<kType>::kSize, kEach = 16 / kSize, kVecs = kBsPer / kEach;
-    extern __shared__ __align__(16) unsigned long long best[];    // values that pass the bound: at most 66 n
+    constexpr int kSize = Logit<kType>::kSize, kEach = 16 / kSize;
+    extern __shared__ __align__(16) unsigned long long best[];    // values that pass the bound
     __shared__ uint32_t warp_top[kBsThreads / 32], warp_low[kBsThreads / 32];
     __shared__ double warp_sum[kBsThreads / 32];
     __shared__ int count;
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = int(blockIdx.x) / a.chunks, chunk = int(blockIdx.x) % a.chunks;
+    const int row = int(blockIdx.x), chunk = int(blockIdx.y);
     if (out_of_play(a, row)) return;             // (nobody looks at its lists)
     const uint8_t* base = static_cast<const uint8_t*>(a.logits) + int64_t(row) * a.stride * kSize;
     // the row from its first 16-byte boundary on as vectors; threads of the first and the last chunk take what is
@@ -98,27 +144,25 @@ beam_rows_kernel(const BeamArgs a) {
     int lead = int((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / kSize;
     if (lead > a.V) lead = a.V;
     const int vecs = (a.V - lead) / kEach, tail = a.V - lead - vecs * kEach;
-    float v[kBsPer], x = -INFINITY;
+    const int first = chunk * kBsThreads * kBsVecs + int(threadIdx.x);
+    const uint4* src = reinterpret_cast<const uint4*>(base + lead * kSize) + first;
+    constexpr uint32_t kNone = Logit<kType>::kNone;
+    uint4 raw[kBsVecs];
+#pragma unroll
+    for (int k = 0; k < kBsVecs; ++k)
+        raw[k] = first + k * kBsThreads < vecs ? __ldg(src + k * kBsThreads) : make_uint4(kNone, kNone, kNone, kNone);
+    float x = -INFINITY;
     int xi = -1;
-    const int first = chunk * kBsThreads * kVecs + int(threadIdx.x);
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-        const int i = first + k * kBsThreads;
-        if (i < vecs) {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(base + lead * kSize) + i);
-            Logit<kType>::spread(raw, v + k * kEach);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) v[k * kEach + e] = -INFINITY;
-        }
-    }
     if (chunk == 0 && threadIdx.x < lead) xi = threadIdx.x;
     if (chunk == a.chunks - 1 && threadIdx.x >= kBsThreads - tail) xi = a.V - (kBsThreads - int(threadIdx.x));
     if (xi >= 0) x = Logit<kType>::one(base + int64_t(xi) * kSize);
 
-    float top = x;                               // (fmaxf passes over NaN)
+    float tops[kBsVecs], top = x;                // (maxima pass over NaN)
 #pragma unroll
-    for (int e = 0; e < kBsPer; ++e) top = fmaxf(top, v[e]);
+    for (int k = 0; k < kBsVecs; ++k) {
+        tops[k] = Logit<kType>::top(raw[k]);
+        top = fmaxf(top, tops[k]);
+    }
     if (top != top) top = -INFINITY;
     const uint32_t mine = order_of(top + 0.f);   // (both zeros alike)
     const uint32_t wt = __reduce_max_sync(0xffffffffu, mine), wl = __reduce_min_sync(0xffffffffu, mine);
@@ -130,13 +174,6 @@ beam_rows_kernel(const BeamArgs a) {
     for (int w = 0; w < kBsThreads / 32; ++w) { most = max(most, warp_top[w]); least = min(least, warp_low[w]); }
     const uint32_t none = order_of(-INFINITY);
     const float peak = value_of(most), ref = most == none ? 0.f : peak;
-    float sum = ex2_approx((x - ref) * kBsLog2e);
-#pragma unroll
-    for (int e = 0; e < kBsPer; ++e) sum += ex2_approx((v[e] - ref) * kBsLog2e);
-    double all = sum;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    if (lane == 0) warp_sum[warp] = all;
 
     // The bound: threads whose largest value reaches it number n to 2n. Where many threads' are equal to it, their
     // first places decide (`until`).
@@ -157,8 +194,13 @@ beam_rows_kernel(const BeamArgs a) {
             if (mine == bound) {
                 if (x == at) place = xi;
 #pragma unroll
-                for (int e = 0; e < kBsPer; ++e)
-                    if (v[e] == at) place = min(place, lead + (first + e / kEach * kBsThreads) * kEach + e % kEach);
+                for (int k = 0; k < kBsVecs; ++k) {
+                    float v[kEach];
+                    Logit<kType>::spread(raw[k], v);
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (v[e] == at) place = min(place, lead + (first + k * kBsThreads) * kEach + e);
+                }
             }
             int lo = -1, hi = a.V - 1;           // too few up to lo, enough up to hi
             until = hi;
@@ -170,6 +212,7 @@ beam_rows_kernel(const BeamArgs a) {
         }
     }
     if (mine >= bound) {
+        const float least_value = value_of(bound);
         auto pass = [&](float y, int i) {
             const uint32_t o = order_of(y + 0.f);
             if (y != y || !(o > bound || (o == bound && i <= until))) return;
@@ -177,109 +220,171 @@ beam_rows_kernel(const BeamArgs a) {
         };
         if (xi >= 0) pass(x, xi);
 #pragma unroll
-        for (int e = 0; e < kBsPer; ++e) pass(v[e], lead + (first + e / kEach * kBsThreads) * kEach + e % kEach);
+        for (int k = 0; k < kBsVecs; ++k)
+            if (tops[k] >= least_value) {
+                float v[kEach];
+                Logit<kType>::spread(raw[k], v);
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) pass(v[e], lead + (first + k * kBsThreads) * kEach + e);
+            }
     }
+    // the sum of exponentials: a thread's in fp32, two at a time, the threads' in 64 bits
+    const uint64_t shift = pair_of(-ref, -ref), log2e = pair_of(kBsLog2e, kBsLog2e);
+    uint64_t sums[2] = {pair_of(ex2_approx((x - ref) * kBsLog2e), 0.f), 0};
+#pragma unroll
+    for (int k = 0; k < kBsVecs; ++k) {
+        float v[kEach];
+        Logit<kType>::spread(raw[k], v);
+#pragma unroll
+        for (int e = 0; e < kEach; e += 2) {
+            const float2 t = floats_of(mul2(add2(pair_of(v[e], v[e + 1]), shift), log2e));
+            sums[(e >> 1) & 1] = add2(sums[(e >> 1) & 1], pair_of(ex2_approx(t.x), ex2_approx(t.y)));
+        }
+    }
+    const float2 part = floats_of(add2(sums[0], sums[1]));
+    double all = double(part.x) + double(part.y);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    if (lane == 0) warp_sum[warp] = all;
     __syncthreads();
     const int c = count;
-    const int64_t list = int64_t(blockIdx.x) * n;
+    const int64_t part_at = int64_t(row) * a.chunks + chunk;
     for (int i = threadIdx.x; i < c; i += kBsThreads) {
         const unsigned long long key = best[i];
         int rank = 0;
         for (int j = 0; j < c; ++j) rank += best[j] > key;
-        if (rank < n) a.lists[list + rank] = key;
+        if (rank < n) a.lists[part_at * n + rank] = key;
     }
-    for (int i = c + threadIdx.x; i < n; i += kBsThreads) a.lists[list + i] = 0;
-    if (threadIdx.x == 0) {
+    for (int i = c + threadIdx.x; i < n; i += kBsThreads) a.lists[part_at * n + i] = 0;
+    if (threadIdx.x == kBsThreads - 1) {
         double total = 0.0;
 #pragma unroll
         for (int w = 0; w < kBsThreads / 32; ++w) total += warp_sum[w];
-        a.peaks[blockIdx.x] = peak;
-        a.sums[blockIdx.x] = total;
+        a.peaks[part_at] = peak;
+        a.sums[part_at] = total;
     }
 }
 
+// A group's n best out of its rows' chunks' lists (each best first), 2048 candidates less the n best so far at a time:
+// the n-th of a list has n - 1 better ones, so nothing below the best n-th matters; the rest rank by counting.
 __global__ void __launch_bounds__(kBsMergeThreads)
 beam_merge_kernel(const BeamArgs a) {
-    __shared__ double lse[SMLA_MAX_BEAMS];
-    __shared__ double warp_score[2][kBsMergeThreads / 32];
-    __shared__ int warp_flat[2][kBsMergeThreads / 32];
-    extern __shared__ uint8_t taken[];           // of each list
+    __shared__ double lse[SMLA_MAX_BEAMS], before[SMLA_MAX_BEAMS];
+    __shared__ int state[SMLA_MAX_BEAMS];        // 0: runs, 1: ended, 2: dead
+    __shared__ unsigned long long warp_bar[kBsMergeThreads / 32];
+    __shared__ unsigned long long keys[kBsBatch];
+    __shared__ int flats[kBsBatch];
+    __shared__ unsigned long long top_keys[SMLA_MAX_BEAMS];
+    __shared__ int top_flats[SMLA_MAX_BEAMS], count;
     grid_dep_wait();
     const int b = int(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (b == 0 && threadIdx.x == 0) *a.status = 0;
-    for (int k = warp; k < a.K; k += kBsMergeThreads / 32) {
-        const int row = b * a.K + k;
-        if (out_of_play(a, row)) continue;
-        float peak = -INFINITY;
-        for (int i = lane; i < a.chunks; i += 32) peak = fmaxf(peak, __ldcg(a.peaks + int64_t(row) * a.chunks + i));
+    const int n = a.n, total = a.K * a.chunks * n;
+    const int64_t row0 = int64_t(b) * a.K;
+    // candidate j of the group: entry j % n of list j / n, read ahead of the sums
+    const int batch = kBsBatch - n;
+    unsigned long long raw[kBsEach];
+    auto read = [&](int base) {
 #pragma unroll
-        for (int d = 16; d; d >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, d));
-        double sum = 0.0;
-        for (int i = lane; i < a.chunks; i += 32)
-            sum += __ldcg(a.sums + int64_t(row) * a.chunks + i) *
-                   exp(double(__ldcg(a.peaks + int64_t(row) * a.chunks + i)) - double(peak));
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) lse[k] = double(peak) + log(sum);
-    }
-    const int lists = a.K * a.chunks;
-    for (int i = threadIdx.x; i < lists; i += kBsMergeThreads) taken[i] = 0;
-    __syncthreads();
-    // the best head of this thread's lists
-    double score = -INFINITY;
-    int flat = INT32_MAX, from = -1;
-    auto look = [&]() {
-        score = -INFINITY;
-        flat = INT32_MAX;
-        from = -1;
-        for (int i = threadIdx.x; i < lists; i += kBsMergeThreads) {
-            const int k = i / a.chunks, row = b * a.K + k, at = taken[i];
-            const float before = __ldg(a.scores + row);
-            double s = -INFINITY;
-            int f = 0;
-            if (!out_of_play(a, row)) {
-                const unsigned long long key =
-                    at < a.n ? __ldcg(a.lists + (int64_t(row) * a.chunks + (i - k * a.chunks)) * a.n + at) : 0;
-                if (key == 0) continue;
-                s = double(before) + (double(value_of(uint32_t(key >> 32))) - lse[k]);
-                f = k * a.V + int(0xffffffffu - uint32_t(key));
-            } else if (a.done && __ldg(a.done + row) && i == k * a.chunks && at == 0) {
-                s = before;
-                f = k * a.V + a.eos;
-            }
-            if (!(fabs(s) < INFINITY)) continue;
-            if (s > score || (s == score && f < flat)) { score = s; flat = f; from = i; }
+        for (int e = 0; e < kBsEach; ++e) {
+            const int i = e * kBsMergeThreads + int(threadIdx.x), j = base + i;
+            raw[e] = i < batch && j < total ? __ldcg(a.lists + row0 * a.chunks * n + j) : 0;
         }
     };
-    look();
-    for (int r = 0; r < a.n; ++r) {
-        double s = score;
-        int f = flat;
+    read(0);
+    for (int k = warp; k < a.K; k += kBsMergeThreads / 32) {
+        const int64_t row = row0 + k;
+        const float s = __ldg(a.scores + row);
+        const bool dead = !(fabsf(s) < INFINITY), ended = a.done && __ldg(a.done + row);
+        double l = 0.0;
+        if (!dead && !ended) {
+            float peak = -INFINITY;
+            for (int i = lane; i < a.chunks; i += 32) peak = fmaxf(peak, __ldcg(a.peaks + row * a.chunks + i));
 #pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const double os = __shfl_xor_sync(0xffffffffu, s, d);
-            const int of = __shfl_xor_sync(0xffffffffu, f, d);
-            if (os > s || (os == s && of < f)) { s = os; f = of; }
+            for (int d = 16; d; d >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, d));
+            double sum = 0.0;
+            for (int i = lane; i < a.chunks; i += 32)
+                sum += __ldcg(a.sums + row * a.chunks + i) *
+                       exp(double(__ldcg(a.peaks + row * a.chunks + i)) - double(peak));
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l = double(peak) + log(sum);
         }
-        if (lane == 0) { warp_score[r & 1][warp] = s; warp_flat[r & 1][warp] = f; }
+        if (lane == 0) {
+            lse[k] = l;
+            before[k] = s;
+            state[k] = dead ? 2 : ended ? 1 : 0;
+        }
+    }
+    int have = 0;                                // of the best so far
+    for (int base = 0; base < total; base += batch) {
+        if (threadIdx.x == 0) count = 0;
         __syncthreads();
+        unsigned long long key[kBsEach], bar = 0;
+        int flat[kBsEach];
 #pragma unroll
-        for (int w = 0; w < kBsMergeThreads / 32; ++w) {
-            const double os = warp_score[r & 1][w];
-            const int of = warp_flat[r & 1][w];
-            if (os > s || (os == s && of < f)) { s = os; f = of; }
+        for (int e = 0; e < kBsEach; ++e) {
+            const int i = e * kBsMergeThreads + int(threadIdx.x), j = base + i;
+            key[e] = 0;                          // (of a finite score it is not 0)
+            flat[e] = 0;
+            if (i >= batch || j >= total) continue;
+            const int list = j / n, at = j - list * n, k = list / a.chunks, st = state[k];
+            double s;
+            if (st == 0) {
+                if (raw[e] == 0) continue;
+                s = before[k] + (double(value_of(uint32_t(raw[e] >> 32))) - lse[k]);
+                flat[e] = k * a.V + int(0xffffffffu - uint32_t(raw[e]));
+            } else {
+                if (st == 2 || at > 0 || list != k * a.chunks) continue;
+                s = before[k];
+                flat[e] = k * a.V + a.eos;
+            }
+            if (!(fabs(s) < INFINITY)) continue;
+            const long long bits = __double_as_longlong(s + 0.0);
+            key[e] = bits < 0 ? ~bits : bits | (1ll << 63);
+            if (at == n - 1 && st == 0) bar = max(bar, key[e]);
         }
-        if (threadIdx.x == 0) {
-            const int64_t at = int64_t(b) * a.n + r;
-            const bool any = f != INT32_MAX;
-            a.parents[at] = any ? b * a.K + f / a.V : -1;
-            a.tokens[at] = any ? f % a.V : -1;
-            a.new_scores[at] = any ? float(s) : -INFINITY;
+        if (base + batch < total) read(base + batch);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) bar = max(bar, __shfl_xor_sync(0xffffffffu, bar, d));
+        if (lane == 0) warp_bar[warp] = bar;
+        __syncthreads();
+        if (have == n) bar = max(bar, top_keys[n - 1]);
+#pragma unroll
+        for (int w = 0; w < kBsMergeThreads / 32; ++w) bar = max(bar, warp_bar[w]);
+#pragma unroll
+        for (int e = 0; e < kBsEach; ++e)
+            if (key[e] != 0 && key[e] >= bar) {
+                const int at = atomicAdd(&count, 1);
+                keys[at] = key[e];
+                flats[at] = flat[e];
+            }
+        if (threadIdx.x < have) {
+            const int at = atomicAdd(&count, 1);
+            keys[at] = top_keys[threadIdx.x];
+            flats[at] = top_flats[threadIdx.x];
         }
-        if (from >= 0 && f == flat) {            // (no two candidates have one place)
-            ++taken[from];
-            look();
+        __syncthreads();
+        const int c = count;
+        for (int i = threadIdx.x; i < c; i += kBsMergeThreads) {
+            const unsigned long long mine = keys[i];
+            const int place = flats[i];
+            int rank = 0;
+            for (int j = 0; j < c; ++j) rank += keys[j] > mine || (keys[j] == mine && flats[j] < place);
+            if (rank < n) { top_keys[rank] = mine; top_flats[rank] = place; }
         }
+        have = c < n ? c : n;
+        __syncthreads();
+    }
+    if (threadIdx.x < n) {
+        const int64_t at = int64_t(b) * n + threadIdx.x;
+        const bool any = threadIdx.x < have;
+        const int f = any ? top_flats[threadIdx.x] : 0;
+        const unsigned long long key = any ? top_keys[threadIdx.x] : 0;
+        const double s = __longlong_as_double(key >> 63 ? key ^ (1ull << 63) : ~key);
+        a.parents[at] = any ? int(row0) + f / a.V : -1;
+        a.tokens[at] = any ? f % a.V : -1;
+        a.new_scores[at] = any ? float(s) : -INFINITY;
     }
 }
 
@@ -287,10 +392,9 @@ namespace {
 
 struct BeamPlan { size_t peaks, sums, lists, bytes; int chunks; };
 
-BeamPlan plan_beam(int64_t rows, int V, int n) {
+BeamPlan plan_beam(int64_t rows, int V, int n, int type) {
     BeamPlan p{};
-    // 16-byte vectors hold 4 values at least
-    p.chunks = (V + kBsThreads * kBsPer - 1) / (kBsThreads * kBsPer);
+    p.chunks = (V + chunk_of(type) - 1) / chunk_of(type);
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes, 256); return o; };
     p.peaks = take(size_t(rows) * p.chunks * 4);
@@ -302,18 +406,27 @@ BeamPlan plan_beam(int64_t rows, int V, int n) {
 
 template <int kType>
 cudaError_t launch_rows(const BeamArgs& a, cudaStream_t s) {
-    const size_t smem = size_t(a.n) * 2 * (kBsPer + 1) * 8;
-    beam_rows_kernel<kType><<<unsigned(a.B) * a.K * a.chunks, kBsThreads, smem, s>>>(a);
+    static bool attr_done[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(beam_rows_kernel<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   int(passing(kType, SMLA_MAX_BEAMS) * 8));
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+    }
+    beam_rows_kernel<kType><<<dim3(unsigned(a.B) * a.K, a.chunks), kBsThreads, passing(kType, a.n) * 8, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t beam_scratch_bytes(int B, int K, int V, int n) { return plan_beam(int64_t(B) * K, V, n).bytes; }
-int beam_chunks(int V) { return plan_beam(1, V, 1).chunks; }
+// (of the type with the smaller chunks)
+size_t beam_scratch_bytes(int B, int K, int V, int n) { return plan_beam(int64_t(B) * K, V, n, SMLA_F32).bytes; }
+int beam_chunks(int V) { return plan_beam(1, V, 1, SMLA_F32).chunks; }
 
 cudaError_t launch_beam_select(BeamArgs a, int type, char* scratch, cudaStream_t s) {
-    const BeamPlan p = plan_beam(int64_t(a.B) * a.K, a.V, a.n);
+    const BeamPlan p = plan_beam(int64_t(a.B) * a.K, a.V, a.n, type);
     a.chunks = p.chunks;
     a.peaks = reinterpret_cast<float*>(scratch + p.peaks);
     a.sums = reinterpret_cast<double*>(scratch + p.sums);
@@ -328,7 +441,6 @@ cudaError_t launch_beam_select(BeamArgs a, int type, char* scratch, cudaStream_t
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(a.B));
     cfg.blockDim = dim3(kBsMergeThreads);
-    cfg.dynamicSmemBytes = size_t(a.K) * a.chunks;
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;

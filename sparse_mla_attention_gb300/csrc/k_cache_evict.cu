@@ -3,10 +3,10 @@
 // Of a sequence with more than `keep` positions the first `first`, the last `recent` and, of those between,
 // the R = keep - first - recent of largest weight stay (ties: the lower position; NaN counts least), in
 // the order of their positions, in fresh pages. The R-th largest weight is found by a radix descent over the
-// weights' bits (four histograms of 256 counts), so the choice is exact and the same in every run.
+// weights' bits (three histograms of 2048 counts), so the choice is exact and the same in every run.
 //
 // evict_plan_kernel: cluster 0 grants the free pages, the other CTAs choose, one sequence each.
-// evict_copy_kernel: moves the rows, a scale block at a time. A block's scale is the largest of its rows'
+// evict_copy_kernel: moves the rows. A block's scale is the largest of its rows'
 // scales; the codes of rows of a smaller one are rounded to it.
 #include <cuda_fp8.h>
 
@@ -42,90 +42,170 @@ __device__ __forceinline__ int row_len(const EvictArgs& a, int b) {
     return len < 0 ? 0 : len > limit ? int(limit) : len;
 }
 
-// The positions that sequence b keeps and their weights.
-__device__ void choose(const EvictArgs& a, int b, PlanShared& sh, int* hist) {
+constexpr int kDigits = 2048;                    // bins of a pass: bits 31-21, 20-10 and 9-0 of a weight
+
+struct ChooseShared {
+    int hist[kDigits];
+    int digit, over;                             // the bin of the rest-th largest, and what lies above it
+    int above, ties;                             // of this CTA's part, read by the others
+};
+
+// Where row i of the new sequence comes from: its row of the pool (-1: no page) and block scale.
+__device__ __forceinline__ void note_row(const EvictArgs& a, int b, int64_t i, int64_t p) {
+    const CacheView& c = a.cache;
+    const int page = __ldg(a.table + int64_t(b) * a.max_pages + (p >> c.page_shift));
+    const int row = page >= 0 && page < c.num_pages
+                        ? (page << c.page_shift) + int(p & ((1 << c.page_shift) - 1)) : -1;
+    a.from[int64_t(b) * a.keep + i] = make_int2(row, row >= 0 ? __float_as_int(__ldg(c.scales + (row >> c.block_shift))) : 0);
+}
+
+// The positions that sequence b keeps, their weights and rows. `parts` CTAs share the sequence (all of a cluster, or
+// one): part `part` goes through the positions [s0, s1).
+template <int kParts>
+__device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, ChooseShared& ch) {
+    cg::cluster_group cl = cg::this_cluster();
     int turn = 0;
     const int64_t width = int64_t(a.max_pages) << a.cache.page_shift;
     const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
     const float* w = a.weights + b * width;
     int32_t* kept = a.kept + int64_t(b) * a.keep;
     float* out = a.new_weights + b * width;
-    for (int64_t i = n + int64_t(threadIdx.x); i < width; i += kPlanThreads) out[i] = 0.f;
-    for (int i = n + threadIdx.x; i < a.keep; i += kPlanThreads) kept[i] = -1;
+    constexpr int kStep = kParts * kPlanThreads;
+    const int first = part * kPlanThreads + int(threadIdx.x);
+    for (int64_t i = n + int64_t(first); i < width; i += kStep) out[i] = 0.f;
+    for (int64_t i = n + int64_t(first); i < a.keep; i += kStep) kept[i] = -1;
     if (len <= a.keep) {
-        for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-            kept[i] = i;
+        for (int64_t i = first; i < n; i += kStep) {
+            kept[i] = int(i);
             out[i] = __ldg(w + i);
+            note_row(a, b, i, i);
         }
         return;
     }
-    const int lo = a.first, hi = len - a.recent;
-    int rest = a.keep - a.first - a.recent;      // of [lo, hi), which has more
+    const int64_t per = (int64_t(len) + kParts - 1) / kParts;
+    const int64_t s0 = min(per * part, int64_t(len)), s1 = min(s0 + per, int64_t(len));
+    const int64_t mid0 = a.first, mid1 = len - a.recent;                 // between the first and the recent
+    const int64_t lo = max(s0, mid0), hi = min(s1, mid1);
+    int rest = a.keep - a.first - a.recent;      // of [mid0, mid1), which has more
     uint32_t prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    int above = 0, ties = 0;                     // of this part
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kDigits;
+        const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
+        ch.hist[threadIdx.x] = 0;
+        ch.hist[threadIdx.x + 1024] = 0;
+        if (threadIdx.x == 0) { ch.digit = bins - 1; ch.over = 0; }      // (where rest is 0: nothing stays by weight)
         __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int64_t i = lo + int(threadIdx.x); i < hi; i += kPlanThreads) {
-            const uint32_t key = order_of(__ldg(w + i));
-            if ((key & mask) == prefix) atomicAdd(hist + ((key >> shift) & 255u), 1);
+        for (int64_t i = lo + int(threadIdx.x); i < hi; i += 4 * kPlanThreads) {
+            uint32_t key[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                key[e] = i + e * kPlanThreads < hi ? order_of(__ldg(w + i + e * kPlanThreads)) : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e * kPlanThreads < hi && (key[e] & mask) == prefix)
+                    atomicAdd(ch.hist + ((key[e] >> shift) & uint32_t(bins - 1)), 1);
         }
-        __syncthreads();
-        // the digit of the rest-th largest: thread d counts those of larger digits
-        int above = 0, mine = 0;
-        if (threadIdx.x < 256) {
-            mine = hist[threadIdx.x];
-            for (int d = threadIdx.x + 1; d < 256; ++d) above += hist[d];
-            if (above < rest && rest <= above + mine) {
-                hist[256] = int(threadIdx.x);
-                hist[257] = above;
-            }
-            if (rest == 0 && threadIdx.x == 255) { hist[256] = 255; hist[257] = 0; }
-        }
-        __syncthreads();
-        prefix |= uint32_t(hist[256]) << shift;
-        rest -= hist[257];
-        __syncthreads();
-    }
-    // keys above prefix stay, and the first `rest` equal ones
-    int at = 0, ties = 0;
-    for (int64_t base = 0; base < len; base += kPlanThreads) {
-        const int64_t i = base + int(threadIdx.x);
-        const float v = i < len ? __ldg(w + i) : 0.f;
-        bool stays = false, tie = false;
-        if (i < len) {
-            if (i < lo || i >= hi) {
-                stays = true;
-            } else {
-                const uint32_t key = order_of(v);
-                stays = key > prefix && a.keep > a.first + a.recent;
-                tie = key == prefix;
+        if (kParts > 1) cl.sync(); else __syncthreads();
+        // bins in falling order, two a thread: the sums before them
+        const int d0 = bins - 1 - 2 * int(threadIdx.x), d1 = d0 - 1;
+        int h0 = 0, h1 = 0;
+        if (d0 >= 0) {
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) {
+                const int* h = kParts > 1 ? cl.map_shared_rank(ch.hist, r) : ch.hist;
+                h0 += h[d0];
+                h1 += h[d1];
             }
         }
         int total;
-        const int before = cta_scan(int(stays) | int(tie) << 16, sh, turn, &total);
-        const int tied = ties + (before >> 16);
-        if (tie) stays = tied < rest;
-        if (stays) {
-            const int to = at + (before & 0xffff) + (tied < rest ? tied : rest);
-            kept[to] = int(i);
-            out[to] = v;
+        const int before = cta_scan(h0 + h1, sh, turn, &total);
+        if (rest > 0 && before < rest && rest <= before + h0 + h1) {
+            const bool second = rest > before + h0;
+            ch.digit = second ? d1 : d0;
+            ch.over = second ? before + h0 : before;
+        }
+        __syncthreads();
+        const int digit = ch.digit;
+        prefix |= uint32_t(digit) << shift;
+        rest -= ch.over;
+        if (kParts > 1) {                        // this part's own
+            int mine = 0;
+            for (int d = digit + 1 + int(threadIdx.x); d < bins; d += kPlanThreads) mine += ch.hist[d];
+            cta_scan(mine, sh, turn, &total);
+            above += total;
+            ties = ch.hist[digit];
+            cl.sync();                           // the counts are read
+        } else {
+            __syncthreads();
+        }
+    }
+    const bool by_weight = a.keep > a.first + a.recent;
+    if (!by_weight) above = ties = 0;
+    // keys above prefix stay, and the first `rest` equal ones
+    int64_t at = min(s0, mid0) + max(int64_t(0), s0 - mid1);
+    int64_t tied_before = 0;
+    if (kParts > 1) {
+        if (threadIdx.x == 0) { ch.above = above; ch.ties = ties; }
+        cl.sync();
+        for (int r = 0; r < part; ++r) {
+            at += cl.map_shared_rank(&ch, r)->above;
+            tied_before += cl.map_shared_rank(&ch, r)->ties;
+        }
+    }
+    int t = int(tied_before);
+    for (int64_t base = s0; base < s1; base += 4 * kPlanThreads) {
+        const int64_t i = base + 4 * int64_t(threadIdx.x);
+        float v[4];
+        bool stays[4], tie[4];
+        int count = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = i + e < s1 ? __ldg(w + i + e) : 0.f;
+            stays[e] = tie[e] = false;
+            if (i + e < s1) {
+                if (i + e < mid0 || i + e >= mid1) {
+                    stays[e] = true;
+                } else if (by_weight) {
+                    const uint32_t key = order_of(v[e]);
+                    stays[e] = key > prefix;
+                    tie[e] = key == prefix;
+                }
+            }
+            count += int(stays[e]) | int(tie[e]) << 16;
+        }
+        int total;
+        const int before = cta_scan(count, sh, turn, &total);
+        int64_t to = at + (before & 0xffff);
+        int tied = t + (before >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (stays[e] || (tie[e] && tied < rest)) {
+                const int64_t row = to + min(tied, rest);
+                kept[row] = int(i + e);
+                out[row] = v[e];
+                note_row(a, b, row, i + e);
+            }
+            to += stays[e];
+            tied += tie[e];
         }
         at += total & 0xffff;
-        ties += total >> 16;
+        t += total >> 16;
     }
+    if (kParts > 1) cl.sync();                   // no CTA leaves while another reads its counts
 }
 
 }  // namespace
 
+template <int kParts>
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 evict_plan_kernel(const EvictArgs a) {
     __shared__ PlanShared sh;
-    __shared__ int hist[258];
+    __shared__ ChooseShared ch;
     grid_dep_launch();
     if (blockIdx.x >= kPlanCtas) {
-        const int b = int(blockIdx.x) - kPlanCtas;
-        if (b < a.B) choose(a, b, sh, hist);
+        const int u = int(blockIdx.x) - kPlanCtas, b = u / kParts;
+        if (b < a.B) choose<kParts>(a, b, u % kParts, sh, ch);
         return;
     }
     cg::cluster_group cl = cg::this_cluster();
@@ -141,16 +221,15 @@ evict_plan_kernel(const EvictArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) a.granted[0] = ok;
 }
 
+// A warp moves up to 16 rows at a time, all of them in flight; it looks at the scales of the whole block.
 __global__ void __launch_bounds__(kEvictCopyThreads)
 evict_copy_kernel(const EvictArgs a) {
-    __shared__ int src[64];
-    __shared__ float scale[64];
     grid_dep_wait();
     const CacheView& c = a.cache;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t threads = int64_t(gridDim.x) * kEvictCopyThreads;
+    const int lane = threadIdx.x & 31;
+    const int64_t threads = int64_t(gridDim.x) * kEvictCopyThreads, first = int64_t(blockIdx.x) * kEvictCopyThreads + threadIdx.x;
     const bool ok = __ldcg(a.granted) != 0;
-    for (int64_t x = int64_t(blockIdx.x) * kEvictCopyThreads + threadIdx.x; x < int64_t(a.B) * a.max_pages; x += threads) {
+    for (int64_t x = first; x < int64_t(a.B) * a.max_pages; x += threads) {
         const int b = int(x / a.max_pages), j = int(x - int64_t(b) * a.max_pages);
         a.new_table[x] = ok && j < __ldcg(a.need + b) ? __ldcg(a.fresh + __ldcg(a.start + b) + j) : -1;
         if (j == 0) {
@@ -160,57 +239,64 @@ evict_copy_kernel(const EvictArgs a) {
     }
     if (!ok) return;
     const int block = 1 << c.block_shift, page_mask = (1 << c.page_shift) - 1;
-    const int per = (a.keep + block - 1) >> c.block_shift;
-    for (int64_t u = blockIdx.x; u < int64_t(a.B) * per; u += gridDim.x) {
-        const int b = int(u / per), r0 = int(u - int64_t(b) * per) << c.block_shift;
+    const int64_t per = (int64_t(a.keep) + 15) >> 4;
+    bool bad = false;
+    for (int64_t u = first >> 5; u < a.B * per; u += threads >> 5) {
+        const int b = int(u / per);
+        const int64_t r0 = (u - b * per) << 4;
         const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
-        const int rows = n - r0 < block ? n - r0 : block;
+        const int rows = int(min(n - r0, int64_t(16)));
         if (rows <= 0) continue;
-        __syncthreads();
-        if (threadIdx.x < rows) {
-            const int p = __ldcg(a.kept + int64_t(b) * a.keep + r0 + threadIdx.x);
-            const int page = __ldg(a.table + int64_t(b) * a.max_pages + (p >> c.page_shift));
-            const bool there = page >= 0 && page < c.num_pages;
-            const int row = there ? (page << c.page_shift) + (p & page_mask) : -1;
-            if (!there) flag_status(a.status, SMLA_ERR_INDEX);
-            src[threadIdx.x] = row;
-            scale[threadIdx.x] = there ? c.scales[row >> c.block_shift] : 0.f;
-        }
-        __syncthreads();
+        const int64_t block0 = r0 & ~int64_t(block - 1);
+        const int page = __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift));
+        // the rows of the block, up to two a lane, and this warp's
+        const int2* list = a.from + int64_t(b) * a.keep;
         float size = 0.f;
-        for (int r = lane; r < rows; r += 32) size = fmaxf(size, scale[r]);
+        for (int r = lane; r < block && block0 + r < n; r += 32) size = fmaxf(size, __int_as_float(__ldcg(list + block0 + r).y));
+        const int2 own = lane < rows ? __ldcg(list + r0 + lane) : make_int2(-1, 0);
+        bad |= lane < rows && own.x < 0;
 #pragma unroll
         for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-        const int64_t to = (int64_t(__ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift))) << c.page_shift) +
-                           (r0 & page_mask);
-        for (int r = warp; r < rows; r += kEvictCopyThreads / 32) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (src[r] >= 0) v = *(reinterpret_cast<const uint4*>(c.pages + int64_t(src[r]) * kD) + lane);
-            if (scale[r] != size) {
-                const float ratio = scale[r] / size;
-                v = make_uint4(recode4(v.x, ratio), recode4(v.y, ratio), recode4(v.z, ratio), recode4(v.w, ratio));
-            }
-            *(reinterpret_cast<uint4*>(c.pages + (to + r) * kD) + lane) = v;
+        const int64_t to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
+        uint4 v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = __shfl_sync(0xffffffffu, own.x, r);
+            v[r] = row >= 0 ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane) : make_uint4(0, 0, 0, 0);
         }
-        if (threadIdx.x == 0) c.scales[to >> c.block_shift] = size;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            if (r >= rows) break;
+            const float scale = __int_as_float(__shfl_sync(0xffffffffu, own.y, r));
+            uint4 x = v[r];
+            if (scale != size) {
+                const float ratio = scale / size;
+                x = make_uint4(recode4(x.x, ratio), recode4(x.y, ratio), recode4(x.z, ratio), recode4(x.w, ratio));
+            }
+            *(reinterpret_cast<uint4*>(c.pages + (to + r) * kD) + lane) = x;
+        }
+        if (r0 == block0 && lane == 0) c.scales[to >> c.block_shift] = size;
     }
+    if (bad) flag_status(a.status, SMLA_ERR_INDEX);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
-    const int rows = (a.B + kPlanCtas - 1) / kPlanCtas * kPlanCtas;
-    evict_plan_kernel<<<kPlanCtas + rows, kPlanThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
     int dev = 0, sms = 1;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t units = int64_t(a.B) * ((a.keep + (1 << a.cache.block_shift) - 1) >> a.cache.block_shift);
-    const int64_t most = int64_t(sms) * 8;
+    // long sequences have a cluster each
+    const int parts = (int64_t(a.max_pages) << a.cache.page_shift) > 16384 ? kPlanCtas : 1;
+    const int64_t grid = kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas;
+    if (parts > 1) evict_plan_kernel<kPlanCtas><<<unsigned(grid), kPlanThreads, 0, s>>>(a);
+    else evict_plan_kernel<1><<<unsigned(grid), kPlanThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int64_t units = int64_t(a.B) * ((int64_t(a.keep) + 15) / 16), blocks = (units + 7) / 8, most = int64_t(sms) * 4;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(units < most ? units : most));
+    cfg.gridDim = dim3(unsigned(blocks < most ? blocks : most));
     cfg.blockDim = dim3(kEvictCopyThreads);
     cfg.stream = s;
     cfg.attrs = &early;

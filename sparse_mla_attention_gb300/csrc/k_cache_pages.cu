@@ -29,6 +29,7 @@ constexpr int kCopySlots = 6, kCopyLag = 3;
 constexpr int kCopyBytes = 32768;                              // of a slot
 constexpr int kCopySmem = kCopySlots * kCopyBytes;
 constexpr uint64_t kCopyWaitNs = 2000000000u;
+constexpr int kReorderRows = 4096;                             // rows of a plan in shared memory
 
 struct CopyShared {
     uint64_t full[kCopySlots];
@@ -455,77 +456,126 @@ copy_kernel(const CacheView c, const int32_t* __restrict__ src, const int32_t* _
                __ldcg(w.count), status);
 }
 
-// Plan of a reordering: kids[p] the children of row p, heir[p] the first of them (-2: a childless row whose last page
-// goes to a copy), w.src / w.dst the pages to copy, need[i] the place of child i's copy in them (-1: none),
+// Plan of a reordering: heir[p] the first child of row p (INT32_MAX: none; -2: none, and its last page
+// goes to a copy), a.src / a.dst the pages to copy, need[i] the place of child i's copy in them (-1: none),
 // count[0] their number (-1: too few pages).
+//
+// What child i copies (-1: nothing), given its parent and whether it is the first.
+__device__ __forceinline__ int tail_to_copy(const ReorderArgs& a, int p, bool first, unsigned& bits) {
+    const CacheView& c = a.cache;
+    const int len = clamp_len(__ldg(a.lens + p), int64_t(a.max_pages) << c.page_shift, bits);
+    if (first || (len & ((1 << c.page_shift) - 1)) == 0) return -1;
+    const int e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
+    if (e < 0 || e >= c.num_pages) { bits |= 1u << SMLA_ERR_INDEX; return -1; }
+    if (__ldcg(c.refcount + e) <= 0) { bits |= 1u << SMLA_ERR_REFCOUNT; return -1; }
+    return e;
+}
+// The last page of a row that ends, if it is partly filled and the row's alone (else -1).
+__device__ __forceinline__ int tail_to_hand_on(const ReorderArgs& a, int p, unsigned& bits) {
+    const CacheView& c = a.cache;
+    const int len = clamp_len(__ldg(a.lens + p), int64_t(a.max_pages) << c.page_shift, bits);
+    if ((len & ((1 << c.page_shift) - 1)) == 0) return -1;
+    const int e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
+    return e >= 0 && e < c.num_pages && __ldcg(c.refcount + e) == 1 ? e : -1;
+}
+// All bits of the CTA's threads.
+__device__ __forceinline__ unsigned cta_bits(unsigned bits) {
+    const bool index = __syncthreads_or(bits & (1u << SMLA_ERR_INDEX)) != 0;
+    const bool count = __syncthreads_or(bits & (1u << SMLA_ERR_REFCOUNT)) != 0;
+    return (index ? 1u << SMLA_ERR_INDEX : 0u) | (count ? 1u << SMLA_ERR_REFCOUNT : 0u);
+}
+// Free pages for the copies from number `used` on; true if there are enough.
+__device__ __forceinline__ bool pages_for_copies(const ReorderArgs& a, int used, int want, PlanShared& sh, int& turn,
+                                                 cg::cluster_group& cl, unsigned& bits) {
+    const CacheView& c = a.cache;
+    int lo, hi;
+    page_slice(c.num_pages, int(cl.block_rank()), lo, hi);
+    const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
+    if (threadIdx.x == 0) { sh.part = mine; sh.bits = bits; }
+    cl.sync();
+    int before, have;
+    join(cl, sh, before, have, bits);
+    const bool ok = want - used <= have;
+    if (ok)
+        emit_pages(c.refcount, lo, hi, used + before, want, sh, turn, is_free, [&](int r, int i) { a.dst[r] = i; });
+    cl.sync();                                   // no CTA leaves while another reads its part
+    return ok;
+}
+
+// Up to kReorderRows rows: every CTA finds children and last pages for itself, in shared memory, and only where the
+// rows that end have too few last pages do they share out the search for free ones.
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+reorder_plan_few_kernel(const ReorderArgs a) {
+    __shared__ PlanShared sh;
+    __shared__ int heir[kReorderRows], spare[kReorderRows];
+    cg::cluster_group cl = cg::this_cluster();
+    grid_dep_launch();                          // the moving kernel's blocks wait for this one's end
+    const bool lead = cl.block_rank() == 0;
+    unsigned bits = 0;
+    int turn = 0;
+    for (int p = threadIdx.x; p < a.B; p += kPlanThreads) heir[p] = INT32_MAX;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        const int p = __ldg(a.parents + i);
+        if (p >= 0 && p < a.B) atomicMin(heir + p, i);
+        else if (p != -1) bits |= 1u << SMLA_ERR_INDEX;
+    }
+    __syncthreads();
+    int want = 0, spares = 0;
+    for (int base = 0; base < a.n || base < a.B; base += kPlanThreads) {
+        const int i = base + int(threadIdx.x);
+        const int p = i < a.n ? __ldg(a.parents + i) : -1;
+        int from = -1, to = -1;
+        if (p >= 0 && p < a.B) from = tail_to_copy(a, p, heir[p] == i, bits);
+        if (i < a.B && heir[i] == INT32_MAX) to = tail_to_hand_on(a, i, bits);
+        int total;
+        const int before = cta_scan(int(from >= 0) | int(to >= 0) << 16, sh, turn, &total);
+        const int at = want + (before & 0xffff), place = spares + (before >> 16);
+        if (i < a.B) spare[i] = to >= 0 ? place : -1;
+        if (lead) {
+            if (i < a.n) a.need[i] = from >= 0 ? at : -1;
+            if (from >= 0) a.src[at] = from;
+            if (to >= 0 && place < a.n) a.dst[place] = to;
+        }
+        want += total & 0xffff;
+        spares += total >> 16;
+    }
+    bits = cta_bits(bits);
+    const bool ok = want <= spares || pages_for_copies(a, spares, want, sh, turn, cl, bits);
+    if (!lead) return;
+    for (int p = threadIdx.x; p < a.B; p += kPlanThreads) a.heir[p] = spare[p] >= 0 && spare[p] < want ? -2 : heir[p];
+    if (threadIdx.x == 0) {
+        a.count[0] = ok ? want : -1;
+        *a.status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
+    }
+}
+
+// More rows: the cluster shares them out, through the workspace.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 reorder_plan_kernel(const ReorderArgs a) {
     __shared__ PlanShared sh;
     cg::cluster_group cl = cg::this_cluster();
-    grid_dep_launch();                          // the moving kernel's blocks wait for this one's end
-    const CacheView& c = a.cache;
+    grid_dep_launch();
     const int rank = int(cl.block_rank()), first = rank * kPlanThreads + int(threadIdx.x);
     constexpr int kStep = kPlanCtas * kPlanThreads;
-    const int64_t limit = int64_t(a.max_pages) << c.page_shift;
-    const int page_mask = (1 << c.page_shift) - 1;
     unsigned bits = 0;
     int turn = 0;
-    for (int p = first; p < a.B; p += kStep) {
-        __stcg(a.kids + p, 0);
-        __stcg(a.heir + p, INT32_MAX);
+    for (int p = first; p < a.B; p += kStep) __stcg(a.heir + p, INT32_MAX);
+    cl.sync();
+    for (int i = first; i < a.n; i += kStep) {
+        const int p = __ldg(a.parents + i);
+        if (p >= 0 && p < a.B) atomicMin(a.heir + p, i);
+        else if (p != -1) bits |= 1u << SMLA_ERR_INDEX;
     }
     cl.sync();
     for (int i = first; i < a.n; i += kStep) {
         const int p = __ldg(a.parents + i);
-        if (p < 0 || p >= a.B) {
-            if (p != -1) bits |= 1u << SMLA_ERR_INDEX;
-            continue;
-        }
-        atomicAdd(a.kids + p, 1);
-        atomicMin(a.heir + p, i);
+        __stcg(a.tail + i, p >= 0 && p < a.B ? tail_to_copy(a, p, __ldcg(a.heir + p) == i, bits) : -1);
     }
+    for (int p = first; p < a.B; p += kStep)
+        __stcg(a.spare + p, __ldcg(a.heir + p) == INT32_MAX ? tail_to_hand_on(a, p, bits) : -1);
+    bits = cta_bits(bits);
     cl.sync();
-    for (int i = first; i < a.n; i += kStep) {
-        int e = -1;
-        const int p = __ldg(a.parents + i);
-        if (p >= 0 && p < a.B) {
-            const int len = clamp_len(__ldg(a.lens + p), limit, bits);
-            if ((len & page_mask) && __ldcg(a.heir + p) != i) {
-                e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
-                if (e < 0 || e >= c.num_pages) {
-                    bits |= 1u << SMLA_ERR_INDEX;
-                    e = -1;
-                } else if (__ldcg(c.refcount + e) <= 0) {
-                    bits |= 1u << SMLA_ERR_REFCOUNT;
-                    e = -1;
-                }
-            }
-        }
-        __stcg(a.tail + i, e);
-    }
-    for (int p = first; p < a.B; p += kStep) {
-        int e = -1;
-        if (__ldcg(a.kids + p) == 0) {
-            const int len = clamp_len(__ldg(a.lens + p), limit, bits);
-            if (len & page_mask) {
-                e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
-                if (e < 0 || e >= c.num_pages || __ldcg(c.refcount + e) != 1) e = -1;
-            }
-        }
-        __stcg(a.spare + p, e);
-    }
-    int lo, hi;
-    page_slice(c.num_pages, rank, lo, hi);
-    const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
-    const bool index = __syncthreads_or(bits & (1u << SMLA_ERR_INDEX)) != 0;
-    const bool count = __syncthreads_or(bits & (1u << SMLA_ERR_REFCOUNT)) != 0;
-    if (threadIdx.x == 0) {
-        sh.part = mine;
-        sh.bits = (index ? 1u << SMLA_ERR_INDEX : 0u) | (count ? 1u << SMLA_ERR_REFCOUNT : 0u);
-    }
-    cl.sync();
-    int before, have;
-    join(cl, sh, before, have, bits);
     const int want = scan_needs(a.n, INT32_MAX, sh, turn,
                                 [&](int i) { return __ldcg(a.tail + i) >= 0 ? 1 : 0; },
                                 [&](int i, int need, int at) {
@@ -540,44 +590,44 @@ reorder_plan_kernel(const ReorderArgs a) {
                                       a.dst[at] = __ldcg(a.spare + p);
                                       a.heir[p] = -2;
                                   });
-    const int used = spares < want ? spares : want;
-    const bool ok = want - used <= have;
-    if (ok)
-        emit_pages(c.refcount, lo, hi, used + before, want, sh, turn, is_free, [&](int r, int i) { a.dst[r] = i; });
+    // (the CTAs join their bits there)
+    const bool ok = pages_for_copies(a, spares < want ? spares : want, want, sh, turn, cl, bits);
     if (rank == 0 && threadIdx.x == 0) {
         a.count[0] = ok ? want : -1;
         *a.status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
     }
-    cl.sync();                                  // no CTA leaves while another reads its part
 }
 
-// The new table, lengths and weights, the counts and the copies.
+// The new table, lengths and weights, the counts and the copies. Warp 0 copies pages; of the others two see to tables
+// and counts and the rest move weights, a row's 4 KB at a time.
 __global__ void __launch_bounds__(kCopyThreads)
 reorder_kernel(const ReorderArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ CopyShared sh;
     grid_dep_wait();
     const CacheView& c = a.cache;
-    const int m = __ldcg(a.count);
+    const int m = __ldcg(a.count), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t limit = int64_t(a.max_pages) << c.page_shift;
-    if (threadIdx.x >= 32) {
-        const int64_t threads = int64_t(gridDim.x) * kEntryThreads;
-        const int64_t first = int64_t(blockIdx.x) * kEntryThreads + threadIdx.x - 32;
+    auto len_of = [&](int p) {
+        const int len = __ldg(a.lens + p);
+        return len < 0 ? 0 : len > limit ? int(limit) : len;
+    };
+    const int table_warps = a.new_weights ? 2 : kCopyThreads / 32 - 1;
+    if (warp > 0 && warp <= table_warps) {
         unsigned bits = 0;
-        auto len_of = [&](int p) {
-            const int len = __ldg(a.lens + p);
-            return len < 0 ? 0 : len > limit ? int(limit) : len;
-        };
-        for (int64_t x = first; x < int64_t(a.n) * a.max_pages; x += threads) {
+        const int64_t step = int64_t(gridDim.x) * table_warps * 32;
+        const int64_t first = (int64_t(blockIdx.x) * table_warps + warp - 1) * 32 + lane;
+        for (int64_t x = first; x < int64_t(a.n) * a.max_pages; x += step) {
             const int i = int(x / a.max_pages), j = int(x - int64_t(i) * a.max_pages);
             const int p = __ldg(a.parents + i);
             int e = -1;
             if (m >= 0 && p >= 0 && p < a.B) {
-                const int full = len_of(p) >> c.page_shift;
-                if (__ldcg(a.heir + p) == i) {
-                    e = __ldg(a.table + int64_t(p) * a.max_pages + j);
+                const int full = len_of(p) >> c.page_shift, heir = __ldcg(a.heir + p);
+                const int old = __ldg(a.table + int64_t(p) * a.max_pages + j);
+                if (heir == i) {
+                    e = old;
                 } else if (j < full) {
-                    e = __ldg(a.table + int64_t(p) * a.max_pages + j);
+                    e = old;
                     if (e < 0 || e >= c.num_pages) {
                         bits |= 1u << SMLA_ERR_INDEX;
                         e = -1;
@@ -595,32 +645,42 @@ reorder_kernel(const ReorderArgs a) {
             if (j == 0) a.new_lens[i] = m >= 0 && p >= 0 && p < a.B ? len_of(p) : 0;
         }
         if (m >= 0)
-            for (int64_t x = first; x < int64_t(a.B) * a.max_pages; x += threads) {
+            for (int64_t x = first; x < int64_t(a.B) * a.max_pages; x += step) {
                 const int p = int(x / a.max_pages), j = int(x - int64_t(p) * a.max_pages);
-                if (__ldcg(a.kids + p) != 0) continue;
-                if (__ldcg(a.heir + p) == -2 && j == len_of(p) >> c.page_shift) continue;
-                give_back(c, __ldg(a.table + x), bits);
+                const int heir = __ldcg(a.heir + p), e = __ldg(a.table + x);
+                if (heir >= 0 && heir != INT32_MAX) continue;
+                if (heir == -2 && j == len_of(p) >> c.page_shift) continue;
+                give_back(c, e, bits);
             }
-        for (int64_t k = first; k < m; k += threads) {       // (a page of a row that ended has the count already)
+        for (int64_t k = first; k < m; k += step) {          // (a page of a row that ended has the count already)
             const int e = __ldcg(a.dst + k);
             if (e >= 0 && e < c.num_pages) c.refcount[e] = 1;
         }
-        if (a.new_weights) {
-            const int64_t quads = limit / 4;
-            for (int64_t x = first; x < a.n * quads; x += threads) {
-                const int i = int(x / quads);
-                const int64_t at = x - i * quads;
-                const int p = __ldg(a.parents + i);
-                const int64_t left = m >= 0 && p >= 0 && p < a.B ? len_of(p) - 4 * at : 0;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (left > 0) v = __ldg(reinterpret_cast<const float4*>(a.weights) + p * quads + at);
-                if (left < 2) v.y = 0.f;
-                if (left < 3) v.z = 0.f;
-                if (left < 4) v.w = 0.f;
-                reinterpret_cast<float4*>(a.new_weights)[x] = v;
-            }
-        }
         if (bits) atomicOr(a.status, bits);
+    } else if (warp > table_warps) {
+        constexpr int kQuads = 256;              // of a piece: 8 a lane, on their way together
+        const int64_t quads = limit / 4, pieces = (quads + kQuads - 1) / kQuads;
+        const int warps = kCopyThreads / 32 - 1 - table_warps;
+        for (int64_t u = int64_t(blockIdx.x) * warps + warp - 1 - table_warps; u < a.n * pieces; u += int64_t(gridDim.x) * warps) {
+            const int i = int(u / pieces);
+            const int64_t at = (u - i * pieces) * kQuads + lane;
+            const int p = __ldg(a.parents + i);
+            const int len = m >= 0 && p >= 0 && p < a.B ? len_of(p) : 0;
+            const float4* src = reinterpret_cast<const float4*>(a.weights) + p * quads;
+            float4* dst = reinterpret_cast<float4*>(a.new_weights) + i * quads;
+            float4 v[kQuads / 32];
+#pragma unroll
+            for (int k = 0; k < kQuads / 32; ++k) {
+                const int64_t q = at + 32 * k, left = len - 4 * q;
+                v[k] = left > 0 ? __ldg(src + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (left < 2) v[k].y = 0.f;
+                if (left < 3) v[k].z = 0.f;
+                if (left < 4) v[k].w = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kQuads / 32; ++k)
+                if (at + 32 * k < quads) dst[at + 32 * k] = v[k];
+        }
     }
     if (m > 0)
         copy_pairs(c, ring, sh, [&](int k) { return __ldcg(a.src + k); }, [&](int k) { return __ldcg(a.dst + k); }, m,
@@ -694,7 +754,9 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
 }
 
 cudaError_t launch_cache_reorder(const ReorderArgs& a, cudaStream_t s) {
-    reorder_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(a);
+    // (a scan counts children in 16 bits)
+    if (a.B <= kReorderRows && a.n <= 4 * kReorderRows) reorder_plan_few_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(a);
+    else reorder_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     note_launch();

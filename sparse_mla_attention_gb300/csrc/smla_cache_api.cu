@@ -69,7 +69,7 @@ PageScratch carve(char* ws, const ScratchPlan& p) {
     return PageScratch{at(kStatusBytes), at(p.need), at(p.tail), at(p.src), at(p.dst), at(p.map)};
 }
 
-struct EvictPlan { size_t need, start, fresh, bytes; };
+struct EvictPlan { size_t need, start, fresh, from, bytes; };
 
 EvictPlan plan_evict(const smla_cache& c, int64_t B, int64_t keep) {
     EvictPlan p{};
@@ -78,17 +78,18 @@ EvictPlan plan_evict(const smla_cache& c, int64_t B, int64_t keep) {
     p.need = take(size_t(B) * 4);
     p.start = take(size_t(B) * 4);
     p.fresh = take(size_t(c.num_pages) * 4);
+    p.from = take(size_t(B) * keep * sizeof(int2));
     p.bytes = off;
     return p;
 }
 
-struct ReorderPlan { size_t kids, heir, spare, tail, need, src, dst, bytes; };
+struct ReorderPlan { size_t heir, spare, tail, need, src, dst, bytes; };
 
 ReorderPlan plan_reorder(int64_t B, int64_t n) {
     ReorderPlan p{};
     size_t off = kStatusBytes + 256;        // the pair count follows the status word
     auto take = [&](int64_t items) { size_t o = off; off += align_up(size_t(items > 0 ? items : 1) * 4, 256); return o; };
-    p.kids = take(B); p.heir = take(B); p.spare = take(B);
+    p.heir = take(B); p.spare = take(B);
     p.tail = take(n); p.need = take(n); p.src = take(n); p.dst = take(n);
     p.bytes = off;
     return p;
@@ -418,6 +419,7 @@ int smla_cache_evict(const smla_cache* cache, const int32_t* table, const int32_
     a.new_table = new_table; a.new_lens = new_lens; a.new_weights = new_weights; a.kept = kept;
     a.B = B; a.max_pages = max_pages; a.keep = keep; a.first = first; a.recent = recent;
     a.granted = at(kStatusBytes); a.need = at(plan.need); a.start = at(plan.start); a.fresh = at(plan.fresh);
+    a.from = reinterpret_cast<int2*>(ws + plan.from);
     a.status = static_cast<unsigned*>(workspace);
     return cuda_rc(launch_cache_evict(a, s));
 }
@@ -462,7 +464,7 @@ int smla_cache_reorder(const smla_cache* cache, const int32_t* table, const int3
     a.weights = weights;
     a.new_table = new_table; a.new_lens = new_lens; a.new_weights = new_weights;
     a.B = B; a.n = n; a.max_pages = max_pages;
-    a.count = at(kStatusBytes); a.kids = at(plan.kids); a.heir = at(plan.heir); a.spare = at(plan.spare);
+    a.count = at(kStatusBytes); a.heir = at(plan.heir); a.spare = at(plan.spare);
     a.tail = at(plan.tail); a.need = at(plan.need); a.src = at(plan.src); a.dst = at(plan.dst);
     a.status = static_cast<unsigned*>(workspace);
     return cuda_rc(launch_cache_reorder(a, s));

@@ -241,22 +241,22 @@ struct WeightsArgs {
 size_t weights_scratch_bytes(int T, int H, int B);
 cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s);
 
-// Arguments of an eviction. need, start [B], fresh [num_pages], granted [1]: workspace.
+// Arguments of an eviction. need, start [B], fresh [num_pages], granted [1], from [B, keep] (row, scale): workspace.
 struct EvictArgs {
     CacheView cache; const int32_t* table; const int32_t* lens; const float* weights;
     int32_t* new_table; int32_t* new_lens; float* new_weights; int32_t* kept;
     int B, max_pages, keep, first, recent;
-    int32_t* need; int32_t* start; int32_t* fresh; int32_t* granted;
+    int32_t* need; int32_t* start; int32_t* fresh; int32_t* granted; int2* from;
     unsigned* status;
 };
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 
-// Arguments of a reordering. count [2], kids, heir, spare [B], tail, need, src, dst [n]: workspace.
+// Arguments of a reordering. count [1], heir, spare [B], tail, need, src, dst [n]: workspace.
 struct ReorderArgs {
     CacheView cache; const int32_t* table; const int32_t* lens; const int32_t* parents; const float* weights;
     int32_t* new_table; int32_t* new_lens; float* new_weights;
     int B, n, max_pages;
-    int32_t* count; int32_t* kids; int32_t* heir; int32_t* spare; int32_t* tail; int32_t* need; int32_t* src;
+    int32_t* count; int32_t* heir; int32_t* spare; int32_t* tail; int32_t* need; int32_t* src;
     int32_t* dst;
     unsigned* status;
 };

@@ -755,3 +755,21 @@ def test_memory_behind_the_decode_outputs_stays():
     smla.beam_select(x, torch.zeros((2, 3), device=DEV), n=5, out=tuple(p[:10].view(2, 5) for p in picks))
     for t, k in zip(big + picks, (2 * table.shape[1], 2, 2 * W, 100, 10, 10, 10)):
         assert (t[k:] == 7).all()
+
+
+def test_reorder_of_more_rows_than_one_block_plans():
+    rng = np.random.default_rng(80)
+    for B, n in ((5000, 5000), (3, 20000)):
+        lens = rng.integers(0, 40, size=B)
+        pool = Pool(int((-(-lens // 16)).sum()) + n + 10, 16, 16, seed=81, junk=False)
+        table = pool.place(lens)
+        _reorder_and_check(pool, table, lens, rng.integers(-1, B, size=n))
+
+
+def test_select_of_more_candidates_than_one_batch():
+    rng = np.random.default_rng(82)
+    x = torch.randn(64, 60000, device=DEV)
+    _select_and_check(x, rng.standard_normal((1, 64)), 64)
+    x = torch.sort(torch.randn(6, 200000, device=DEV), dim=1)[0]
+    _select_and_check(x, rng.standard_normal((2, 3)), 64)
+    _select_and_check(x.flip(1).half(), rng.standard_normal((2, 3)), 17)

@@ -132,7 +132,7 @@ beam_rows_kernel(const BeamArgs a) {
     constexpr int kSize = Logit<kType>::kSize, kEach = 16 / kSize;
     extern __shared__ __align__(16) unsigned long long best[];    // values that pass the bound
     __shared__ uint32_t warp_top[kBsThreads / 32], warp_low[kBsThreads / 32];
-    __shared__ double warp_sum[kBsThreads / 32];
+    __shared__ float2 warp_sum[kBsThreads / 32];
     __shared__ int count;
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -228,7 +228,8 @@ beam_rows_kernel(const BeamArgs a) {
                 for (int e = 0; e < kEach; ++e) pass(v[e], lead + (first + k * kBsThreads) * kEach + e);
             }
     }
-    // the sum of exponentials: a thread's in fp32, two at a time, the threads' in 64 bits
+    // the sum of exponentials: a thread's in fp32, two at a time; the threads' with what each addition rounds off
+    // beside it (64-bit additions of a warp occupy their unit for 16 cycles each)
     const uint64_t shift = pair_of(-ref, -ref), log2e = pair_of(kBsLog2e, kBsLog2e);
     uint64_t sums[2] = {pair_of(ex2_approx((x - ref) * kBsLog2e), 0.f), 0};
 #pragma unroll
@@ -242,10 +243,17 @@ beam_rows_kernel(const BeamArgs a) {
         }
     }
     const float2 part = floats_of(add2(sums[0], sums[1]));
-    double all = double(part.x) + double(part.y);
+    float all = part.x, rest = 0.f;
+    auto add = [&](float y, float more) {
+        const float sum = all + y, z = sum - all;
+        rest += ((all - (sum - z)) + (y - z)) + more;
+        all = sum;
+    };
+    add(part.y, 0.f);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    if (lane == 0) warp_sum[warp] = all;
+    for (int d = 16; d; d >>= 1)
+        add(__shfl_xor_sync(0xffffffffu, all, d), __shfl_xor_sync(0xffffffffu, rest, d));
+    if (lane == 0) warp_sum[warp] = make_float2(all, rest);
     __syncthreads();
     const int c = count;
     const int64_t part_at = int64_t(row) * a.chunks + chunk;
@@ -259,10 +267,15 @@ beam_rows_kernel(const BeamArgs a) {
     if (threadIdx.x == kBsThreads - 1) {
         double total = 0.0;
 #pragma unroll
-        for (int w = 0; w < kBsThreads / 32; ++w) total += warp_sum[w];
+        for (int w = 0; w < kBsThreads / 32; ++w) total += double(warp_sum[w].x) + double(warp_sum[w].y);
         a.peaks[part_at] = peak;
         a.sums[part_at] = total;
     }
+}
+
+// A score a little below the one that a key stands for.
+__device__ __forceinline__ float float_below(unsigned long long key) {
+    return __double2float_rd(__longlong_as_double(key >> 63 ? key ^ (1ull << 63) : ~key));
 }
 
 // A group's n best out of its rows' chunks' lists (each best first), 2048 candidates less the n best so far at a time:
@@ -271,7 +284,9 @@ __global__ void __launch_bounds__(kBsMergeThreads)
 beam_merge_kernel(const BeamArgs a) {
     __shared__ double lse[SMLA_MAX_BEAMS], before[SMLA_MAX_BEAMS];
     __shared__ int state[SMLA_MAX_BEAMS];        // 0: runs, 1: ended, 2: dead
-    __shared__ unsigned long long warp_bar[kBsMergeThreads / 32];
+    __shared__ float peaks[kBsMergeThreads], row_peak[SMLA_MAX_BEAMS + 1];
+    __shared__ double sums[kBsMergeThreads];
+    __shared__ float warp_bar[kBsMergeThreads / 32];
     __shared__ unsigned long long keys[kBsBatch];
     __shared__ int flats[kBsBatch];
     __shared__ unsigned long long top_keys[SMLA_MAX_BEAMS];
@@ -292,73 +307,95 @@ beam_merge_kernel(const BeamArgs a) {
         }
     };
     read(0);
-    for (int k = warp; k < a.K; k += kBsMergeThreads / 32) {
-        const int64_t row = row0 + k;
-        const float s = __ldg(a.scores + row);
-        const bool dead = !(fabsf(s) < INFINITY), ended = a.done && __ldg(a.done + row);
-        double l = 0.0;
-        if (!dead && !ended) {
+    // The rows' log-sums. 64-bit instructions are slow and cost a warp as much for one lane as for 32: exponentials
+    // of many chunks a warp, logarithms of many rows.
+    for (int k = threadIdx.x; k < a.K; k += kBsMergeThreads) {
+        const float s = __ldg(a.scores + row0 + k);
+        before[k] = s;
+        state[k] = !(fabsf(s) < INFINITY) ? 2 : a.done && __ldg(a.done + row0 + k) ? 1 : 0;
+    }
+    const int lists = a.K * a.chunks;
+    for (int l0 = 0; l0 < lists; l0 += kBsMergeThreads) {
+        // whole rows at a time; a row of more chunks than threads goes on from part to part
+        const int l = l0 + int(threadIdx.x);
+        if (l < lists) {
+            peaks[threadIdx.x] = __ldcg(a.peaks + row0 * a.chunks + l);
+            sums[threadIdx.x] = __ldcg(a.sums + row0 * a.chunks + l);
+        }
+        __syncthreads();
+        const int k0 = l0 / a.chunks, k1 = (min(l0 + kBsMergeThreads, lists) - 1) / a.chunks;
+        // a row's peak over the part: a thread a row
+        if (k0 + int(threadIdx.x) <= k1) {
+            const int k = k0 + int(threadIdx.x), i0 = max(k * a.chunks, l0), i1 = min(min((k + 1) * a.chunks, lists), l0 + kBsMergeThreads);
             float peak = -INFINITY;
-            for (int i = lane; i < a.chunks; i += 32) peak = fmaxf(peak, __ldcg(a.peaks + row * a.chunks + i));
-#pragma unroll
-            for (int d = 16; d; d >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, d));
+            for (int i = i0; i < i1; ++i) peak = fmaxf(peak, peaks[i - l0]);
+            row_peak[k - k0] = peak;
+        }
+        __syncthreads();
+        if (l < lists) {
+            const float peak = peaks[threadIdx.x], most = row_peak[l / a.chunks - k0];
+            if (peak != most) sums[threadIdx.x] *= exp(double(peak) - double(most));
+        }
+        __syncthreads();
+        if (k0 + int(threadIdx.x) <= k1) {
+            const int k = k0 + int(threadIdx.x), i0 = max(k * a.chunks, l0), i1 = min(min((k + 1) * a.chunks, lists), l0 + kBsMergeThreads);
             double sum = 0.0;
-            for (int i = lane; i < a.chunks; i += 32)
-                sum += __ldcg(a.sums + row * a.chunks + i) *
-                       exp(double(__ldcg(a.peaks + row * a.chunks + i)) - double(peak));
-#pragma unroll
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            l = double(peak) + log(sum);
+            for (int i = i0; i < i1; ++i) sum += sums[i - l0];
+            sum = double(row_peak[k - k0]) + log(sum);
+            if (i0 > k * a.chunks) {             // joined to the parts before
+                const double x = fmax(lse[k], sum), y = fmin(lse[k], sum);
+                sum = lse[k] != lse[k] || sum != sum ? lse[k] + sum : y == -INFINITY ? x : x + log1p(exp(y - x));
+            }
+            lse[k] = sum;
         }
-        if (lane == 0) {
-            lse[k] = l;
-            before[k] = s;
-            state[k] = dead ? 2 : ended ? 1 : 0;
-        }
+        __syncthreads();
     }
     int have = 0;                                // of the best so far
     for (int base = 0; base < total; base += batch) {
         if (threadIdx.x == 0) count = 0;
         __syncthreads();
-        unsigned long long key[kBsEach], bar = 0;
-        int flat[kBsEach];
+        // In 32 bits first, with room for their rounding: what is below the bar for sure is never looked at in 64.
+        float low[kBsEach], high[kBsEach], bar = have == n ? float_below(top_keys[n - 1]) : -INFINITY;
 #pragma unroll
         for (int e = 0; e < kBsEach; ++e) {
             const int i = e * kBsMergeThreads + int(threadIdx.x), j = base + i;
-            key[e] = 0;                          // (of a finite score it is not 0)
-            flat[e] = 0;
+            high[e] = __int_as_float(0x7fffffff);                        // NaN: no candidate
             if (i >= batch || j >= total) continue;
             const int list = j / n, at = j - list * n, k = list / a.chunks, st = state[k];
-            double s;
-            if (st == 0) {
-                if (raw[e] == 0) continue;
-                s = before[k] + (double(value_of(uint32_t(raw[e] >> 32))) - lse[k]);
-                flat[e] = k * a.V + int(0xffffffffu - uint32_t(raw[e]));
-            } else {
-                if (st == 2 || at > 0 || list != k * a.chunks) continue;
-                s = before[k];
-                flat[e] = k * a.V + a.eos;
-            }
-            if (!(fabs(s) < INFINITY)) continue;
-            const long long bits = __double_as_longlong(s + 0.0);
-            key[e] = bits < 0 ? ~bits : bits | (1ll << 63);
-            if (at == n - 1 && st == 0) bar = max(bar, key[e]);
+            if (st == 0 ? raw[e] == 0 : st == 2 || at > 0 || list != k * a.chunks) continue;
+            const float s = float(before[k]), x = st ? 0.f : value_of(uint32_t(raw[e] >> 32)), l = st ? 0.f : float(lse[k]);
+            const float sum = s + (x - l), room = 0x1p-21f * (fabsf(s) + fabsf(x) + fabsf(l)) + 0x1p-100f;
+            // (where 32 bits overflow, nothing is for sure)
+            high[e] = fabsf(sum) < INFINITY && room < INFINITY ? sum + room : INFINITY;
+            low[e] = fabsf(sum) < INFINITY && room < INFINITY ? sum - room : -INFINITY;
+            if (at == n - 1 && st == 0) bar = fmaxf(bar, low[e]);
         }
-        if (base + batch < total) read(base + batch);
 #pragma unroll
-        for (int d = 16; d; d >>= 1) bar = max(bar, __shfl_xor_sync(0xffffffffu, bar, d));
+        for (int d = 16; d; d >>= 1) bar = fmaxf(bar, __shfl_xor_sync(0xffffffffu, bar, d));
         if (lane == 0) warp_bar[warp] = bar;
         __syncthreads();
-        if (have == n) bar = max(bar, top_keys[n - 1]);
 #pragma unroll
-        for (int w = 0; w < kBsMergeThreads / 32; ++w) bar = max(bar, warp_bar[w]);
+        for (int w = 0; w < kBsMergeThreads / 32; ++w) bar = fmaxf(bar, warp_bar[w]);
 #pragma unroll
         for (int e = 0; e < kBsEach; ++e)
-            if (key[e] != 0 && key[e] >= bar) {
+            if (high[e] >= bar) {
                 const int at = atomicAdd(&count, 1);
-                keys[at] = key[e];
-                flats[at] = flat[e];
+                keys[at] = raw[e];
+                flats[at] = base + e * kBsMergeThreads + int(threadIdx.x);
             }
+        if (base + batch < total) read(base + batch);
+        __syncthreads();
+        // those in 64 bits; one that is not finite is 0, below all
+        for (int i = threadIdx.x; i < count; i += kBsMergeThreads) {
+            const unsigned long long was = keys[i];
+            const int list = flats[i] / n, k = list / a.chunks;
+            const bool ended = state[k] != 0;
+            const double s = ended ? before[k] : before[k] + (double(value_of(uint32_t(was >> 32))) - lse[k]);
+            const long long bits = __double_as_longlong(s + 0.0);
+            keys[i] = !(fabs(s) < INFINITY) ? 0 : bits < 0 ? ~bits : bits | (1ll << 63);
+            flats[i] = k * a.V + (ended ? a.eos : int(0xffffffffu - uint32_t(was)));
+        }
+        __syncthreads();
         if (threadIdx.x < have) {
             const int at = atomicAdd(&count, 1);
             keys[at] = top_keys[threadIdx.x];
@@ -373,8 +410,9 @@ beam_merge_kernel(const BeamArgs a) {
             for (int j = 0; j < c; ++j) rank += keys[j] > mine || (keys[j] == mine && flats[j] < place);
             if (rank < n) { top_keys[rank] = mine; top_flats[rank] = place; }
         }
-        have = c < n ? c : n;
         __syncthreads();
+        have = c < n ? c : n;
+        while (have > 0 && top_keys[have - 1] == 0) --have;
     }
     if (threadIdx.x < n) {
         const int64_t at = int64_t(b) * n + threadIdx.x;

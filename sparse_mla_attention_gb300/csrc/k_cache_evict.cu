@@ -43,109 +43,117 @@ __device__ __forceinline__ int row_len(const EvictArgs& a, int b) {
 }
 
 constexpr int kDigits = 2048;                    // bins of a pass: bits 31-21, 20-10 and 9-0 of a weight
+constexpr int kRun = 16;                         // positions of a thread: in one page and one scale block
+constexpr int kTile = kPlanThreads * kRun;
 
 struct ChooseShared {
-    int hist[kDigits];
+    int hist[kDigits];                           // of this CTA
+    int all[3][kDigits];                         // of the cluster, in its first CTA
     int digit, over;                             // the bin of the rest-th largest, and what lies above it
     int above, ties;                             // of this CTA's part, read by the others
 };
 
-// Where row i of the new sequence comes from: its row of the pool (-1: no page) and block scale.
-__device__ __forceinline__ void note_row(const EvictArgs& a, int b, int64_t i, int64_t p) {
-    const CacheView& c = a.cache;
-    const int page = __ldg(a.table + int64_t(b) * a.max_pages + (p >> c.page_shift));
-    const int row = page >= 0 && page < c.num_pages
-                        ? (page << c.page_shift) + int(p & ((1 << c.page_shift) - 1)) : -1;
-    a.from[int64_t(b) * a.keep + i] = make_int2(row, row >= 0 ? __float_as_int(__ldg(c.scales + (row >> c.block_shift))) : 0);
-}
-
-// The positions that sequence b keeps, their weights and rows. `parts` CTAs share the sequence (all of a cluster, or
-// one): part `part` goes through the positions [s0, s1).
+// The positions that sequence b keeps, their weights and rows. kParts CTAs share the sequence (all of a cluster, or
+// one), a run of positions each. A thread's keys stay in registers where the CTA's part is one tile (16384).
 template <int kParts>
 __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, ChooseShared& ch) {
     cg::cluster_group cl = cg::this_cluster();
+    const CacheView& c = a.cache;
     int turn = 0;
-    const int64_t width = int64_t(a.max_pages) << a.cache.page_shift;
+    const int64_t width = int64_t(a.max_pages) << c.page_shift;
     const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
     const float* w = a.weights + b * width;
     int32_t* kept = a.kept + int64_t(b) * a.keep;
     float* out = a.new_weights + b * width;
-    constexpr int kStep = kParts * kPlanThreads;
     const int first = part * kPlanThreads + int(threadIdx.x);
-    for (int64_t i = n + int64_t(first); i < width; i += kStep) out[i] = 0.f;
-    for (int64_t i = n + int64_t(first); i < a.keep; i += kStep) kept[i] = -1;
-    if (len <= a.keep) {
-        for (int64_t i = first; i < n; i += kStep) {
-            kept[i] = int(i);
-            out[i] = __ldg(w + i);
-            note_row(a, b, i, i);
-        }
-        return;
-    }
-    const int64_t per = (int64_t(len) + kParts - 1) / kParts;
+    for (int64_t i = n + int64_t(first); i < width; i += kParts * kPlanThreads) out[i] = 0.f;
+    for (int64_t i = n + int64_t(first); i < a.keep; i += kParts * kPlanThreads) kept[i] = -1;
+    const int64_t per = (int64_t(len) + kParts * kRun - 1) / (kParts * kRun) * kRun;
     const int64_t s0 = min(per * part, int64_t(len)), s1 = min(s0 + per, int64_t(len));
-    const int64_t mid0 = a.first, mid1 = len - a.recent;                 // between the first and the recent
-    const int64_t lo = max(s0, mid0), hi = min(s1, mid1);
-    int rest = a.keep - a.first - a.recent;      // of [mid0, mid1), which has more
+    const bool one_tile = s1 - s0 <= kTile;
+    // all positions stay where there are no more than keep; else those between the first and the recent compete
+    const int64_t mid0 = len <= a.keep ? len : a.first, mid1 = len <= a.keep ? len : len - a.recent;
+    int rest = len <= a.keep ? 0 : a.keep - a.first - a.recent;          // of [mid0, mid1), which has more
+    const bool by_weight = rest > 0;
+    uint32_t key[kRun];
+    int64_t i0 = 0;                              // the thread's first position of the tile at hand
+    auto load = [&](int64_t base) {
+        i0 = base + kRun * int64_t(threadIdx.x);
+#pragma unroll
+        for (int e = 0; e < kRun; e += 4) {      // (width is a multiple of 16: no quad passes a row's end)
+            const float4 v = i0 + e < s1 ? __ldg(reinterpret_cast<const float4*>(w + i0 + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            key[e] = order_of(v.x); key[e + 1] = order_of(v.y); key[e + 2] = order_of(v.z); key[e + 3] = order_of(v.w);
+        }
+    };
+    auto competes = [&](int e) { return i0 + e >= mid0 && i0 + e < mid1 && i0 + e < s1; };
+    if (one_tile) load(s0);
     uint32_t prefix = 0;
-    int above = 0, ties = 0;                     // of this part
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kDigits;
-        const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
-        ch.hist[threadIdx.x] = 0;
-        ch.hist[threadIdx.x + 1024] = 0;
-        if (threadIdx.x == 0) { ch.digit = bins - 1; ch.over = 0; }      // (where rest is 0: nothing stays by weight)
-        __syncthreads();
-        for (int64_t i = lo + int(threadIdx.x); i < hi; i += 4 * kPlanThreads) {
-            uint32_t key[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                key[e] = i + e * kPlanThreads < hi ? order_of(__ldg(w + i + e * kPlanThreads)) : 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i + e * kPlanThreads < hi && (key[e] & mask) == prefix)
-                    atomicAdd(ch.hist + ((key[e] >> shift) & uint32_t(bins - 1)), 1);
+    if (by_weight) {                             // (the same in every CTA of the sequence)
+        if (kParts > 1) {
+            if (part == 0)
+                for (int i = threadIdx.x; i < 3 * kDigits; i += kPlanThreads) (&ch.all[0][0])[i] = 0;
+            cl.sync();
         }
-        if (kParts > 1) cl.sync(); else __syncthreads();
-        // bins in falling order, two a thread: the sums before them
-        const int d0 = bins - 1 - 2 * int(threadIdx.x), d1 = d0 - 1;
-        int h0 = 0, h1 = 0;
-        if (d0 >= 0) {
-#pragma unroll
-            for (int r = 0; r < kParts; ++r) {
-                const int* h = kParts > 1 ? cl.map_shared_rank(ch.hist, r) : ch.hist;
-                h0 += h[d0];
-                h1 += h[d1];
-            }
-        }
-        int total;
-        const int before = cta_scan(h0 + h1, sh, turn, &total);
-        if (rest > 0 && before < rest && rest <= before + h0 + h1) {
-            const bool second = rest > before + h0;
-            ch.digit = second ? d1 : d0;
-            ch.over = second ? before + h0 : before;
-        }
-        __syncthreads();
-        const int digit = ch.digit;
-        prefix |= uint32_t(digit) << shift;
-        rest -= ch.over;
-        if (kParts > 1) {                        // this part's own
-            int mine = 0;
-            for (int d = digit + 1 + int(threadIdx.x); d < bins; d += kPlanThreads) mine += ch.hist[d];
-            cta_scan(mine, sh, turn, &total);
-            above += total;
-            ties = ch.hist[digit];
-            cl.sync();                           // the counts are read
-        } else {
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kDigits;
+            const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
+            ch.hist[threadIdx.x] = 0;
+            ch.hist[threadIdx.x + 1024] = 0;
             __syncthreads();
+            for (int64_t base = s0; base < s1; base += kTile) {
+                if (!one_tile) load(base);
+#pragma unroll
+                for (int e = 0; e < kRun; ++e)
+                    if (competes(e) && (key[e] & mask) == prefix)
+                        atomicAdd(ch.hist + ((key[e] >> shift) & uint32_t(bins - 1)), 1);
+            }
+            __syncthreads();
+            const int* hist = ch.hist;
+            if (kParts > 1) {                    // few bins hold anything: they are added to the first CTA's
+                int* all = cl.map_shared_rank(ch.all[pass], 0);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int d = int(threadIdx.x) + 1024 * k, h = ch.hist[d];
+                    if (h) atomicAdd(all + d, h);
+                }
+                cl.sync();
+                hist = all;
+            }
+            // bins in falling order, two a thread: the sums before them
+            const int d0 = bins - 1 - 2 * int(threadIdx.x), d1 = d0 - 1;
+            const int h0 = d0 >= 0 ? hist[d0] : 0, h1 = d0 >= 0 ? hist[d1] : 0;
+            int total;
+            const int before = cta_scan(h0 + h1, sh, turn, &total);
+            if (before < rest && rest <= before + h0 + h1) {
+                const bool second = rest > before + h0;
+                ch.digit = second ? d1 : d0;
+                ch.over = second ? before + h0 : before;
+            }
+            __syncthreads();
+            prefix |= uint32_t(ch.digit) << shift;
+            rest -= ch.over;
         }
     }
-    const bool by_weight = a.keep > a.first + a.recent;
-    if (!by_weight) above = ties = 0;
-    // keys above prefix stay, and the first `rest` equal ones
-    int64_t at = min(s0, mid0) + max(int64_t(0), s0 - mid1);
-    int64_t tied_before = 0;
+    // keys above prefix stay (1), and the first `rest` equal ones (1 << 16)
+    auto verdict = [&](int e) {
+        if (i0 + e >= s1) return 0;
+        if (!competes(e)) return 1;
+        return !by_weight ? 0 : key[e] > prefix ? 1 : key[e] == prefix ? 1 << 16 : 0;
+    };
+    int64_t at = 0, tied_before = 0;
     if (kParts > 1) {
+        int above = 0, ties = 0;
+        for (int64_t base = s0; base < s1; base += kTile) {
+            if (!one_tile) load(base);
+            int count = 0, total;
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) count += verdict(e);
+            cta_scan(count & 0xffff, sh, turn, &total);
+            above += total;
+            cta_scan(count >> 16, sh, turn, &total);
+            ties += total;
+        }
         if (threadIdx.x == 0) { ch.above = above; ch.ties = ties; }
         cl.sync();
         for (int r = 0; r < part; ++r) {
@@ -154,43 +162,36 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
         }
     }
     int t = int(tied_before);
-    for (int64_t base = s0; base < s1; base += 4 * kPlanThreads) {
-        const int64_t i = base + 4 * int64_t(threadIdx.x);
-        float v[4];
-        bool stays[4], tie[4];
-        int count = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = i + e < s1 ? __ldg(w + i + e) : 0.f;
-            stays[e] = tie[e] = false;
-            if (i + e < s1) {
-                if (i + e < mid0 || i + e >= mid1) {
-                    stays[e] = true;
-                } else if (by_weight) {
-                    const uint32_t key = order_of(v[e]);
-                    stays[e] = key > prefix;
-                    tie[e] = key == prefix;
-                }
+    for (int64_t base = s0; base < s1; base += kTile) {
+        if (!one_tile) load(base);
+        int2 from = make_int2(-1, 0);            // the run's first row of the pool and its scale
+        if (i0 < s1) {
+            const int page = __ldg(a.table + int64_t(b) * a.max_pages + (i0 >> c.page_shift));
+            if (page >= 0 && page < c.num_pages) {
+                from.x = (page << c.page_shift) + int(i0 & ((1 << c.page_shift) - 1));
+                from.y = __float_as_int(__ldg(c.scales + (from.x >> c.block_shift)));
             }
-            count += int(stays[e]) | int(tie[e]) << 16;
         }
-        int total;
-        const int before = cta_scan(count, sh, turn, &total);
-        int64_t to = at + (before & 0xffff);
-        int tied = t + (before >> 16);
+        int count = 0, stay, tie;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (stays[e] || (tie[e] && tied < rest)) {
+        for (int e = 0; e < kRun; ++e) count += verdict(e);
+        const int stays = cta_scan(count & 0xffff, sh, turn, &stay), tied0 = cta_scan(count >> 16, sh, turn, &tie);
+        int64_t to = at + stays;
+        int tied = t + tied0;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+            const int v = verdict(e);
+            if (v == 1 || (v != 0 && tied < rest)) {
                 const int64_t row = to + min(tied, rest);
-                kept[row] = int(i + e);
-                out[row] = v[e];
-                note_row(a, b, row, i + e);
+                kept[row] = int(i0 + e);
+                out[row] = __ldg(w + i0 + e);
+                a.from[int64_t(b) * a.keep + row] = make_int2(from.x < 0 ? -1 : from.x + e, from.y);
             }
-            to += stays[e];
-            tied += tie[e];
+            to += v & 1;
+            tied += v >> 16;
         }
-        at += total & 0xffff;
-        t += total >> 16;
+        at += stay;
+        t += tie;
     }
     if (kParts > 1) cl.sync();                   // no CTA leaves while another reads its counts
 }
@@ -284,7 +285,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
     int dev = 0, sms = 1;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // long sequences have a cluster each
+    // Long sequences have a cluster each.
     const int parts = (int64_t(a.max_pages) << a.cache.page_shift) > 16384 ? kPlanCtas : 1;
     const int64_t grid = kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas;
     if (parts > 1) evict_plan_kernel<kPlanCtas><<<unsigned(grid), kPlanThreads, 0, s>>>(a);

@@ -29,6 +29,7 @@ constexpr int kCopySlots = 6, kCopyLag = 3;
 constexpr int kCopyBytes = 32768;                              // of a slot
 constexpr int kCopySmem = kCopySlots * kCopyBytes;
 constexpr uint64_t kCopyWaitNs = 2000000000u;
+constexpr int kReorderThreads = 1024;
 constexpr int kReorderRows = 4096;                             // rows of a plan in shared memory
 
 struct CopyShared {
@@ -45,8 +46,8 @@ __device__ void copy_pairs(const CacheView& c, uint8_t* ring, CopyShared& sh, Sr
                            unsigned* status) {
     const int nscale = 1 << (c.page_shift - c.block_shift);
     if (threadIdx.x >= 32) {
-        const int64_t threads = int64_t(gridDim.x) * kEntryThreads;
-        for (int64_t x = int64_t(blockIdx.x) * kEntryThreads + threadIdx.x - 32; x < int64_t(m) * nscale; x += threads) {
+        const int64_t each = blockDim.x - 32, threads = int64_t(gridDim.x) * each;
+        for (int64_t x = int64_t(blockIdx.x) * each + threadIdx.x - 32; x < int64_t(m) * nscale; x += threads) {
             const int k = int(x / nscale), i = int(x - int64_t(k) * nscale), a = src(k), b = dst(k);
             if (a >= 0 && a < c.num_pages && b >= 0 && b < c.num_pages)
                 c.scales[int64_t(b) * nscale + i] = c.scales[int64_t(a) * nscale + i];
@@ -598,9 +599,9 @@ reorder_plan_kernel(const ReorderArgs a) {
     }
 }
 
-// The new table, lengths and weights, the counts and the copies. Warp 0 copies pages; of the others two see to tables
-// and counts and the rest move weights, a row's 4 KB at a time.
-__global__ void __launch_bounds__(kCopyThreads)
+// The new table, lengths and weights, the counts and the copies. Warp 0 copies pages; of the others seven see to tables
+// and counts and the rest move weights (all see to tables if there are none), a row's 4 KB at a time.
+__global__ void __launch_bounds__(kReorderThreads)
 reorder_kernel(const ReorderArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ CopyShared sh;
@@ -612,7 +613,7 @@ reorder_kernel(const ReorderArgs a) {
         const int len = __ldg(a.lens + p);
         return len < 0 ? 0 : len > limit ? int(limit) : len;
     };
-    const int table_warps = a.new_weights ? 2 : kCopyThreads / 32 - 1;
+    const int table_warps = a.new_weights ? 7 : kReorderThreads / 32 - 1;
     if (warp > 0 && warp <= table_warps) {
         unsigned bits = 0;
         const int64_t step = int64_t(gridDim.x) * table_warps * 32;
@@ -660,7 +661,7 @@ reorder_kernel(const ReorderArgs a) {
     } else if (warp > table_warps) {
         constexpr int kQuads = 256;              // of a piece: 8 a lane, on their way together
         const int64_t quads = limit / 4, pieces = (quads + kQuads - 1) / kQuads;
-        const int warps = kCopyThreads / 32 - 1 - table_warps;
+        const int warps = kReorderThreads / 32 - 1 - table_warps;
         for (int64_t u = int64_t(blockIdx.x) * warps + warp - 1 - table_warps; u < a.n * pieces; u += int64_t(gridDim.x) * warps) {
             const int i = int(u / pieces);
             const int64_t at = (u - i * pieces) * kQuads + lane;
@@ -710,7 +711,8 @@ int64_t blocks_for(int64_t n, int threads) { return (n + threads - 1) / threads;
 // Launches a kernel whose blocks may start before the one ahead of it on the stream is
 // complete (they wait for that themselves).
 template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), bool (&attr_done)[64], int grid, cudaStream_t s, Args... args) {
+cudaError_t launch_early(void (*kernel)(Params...), bool (&attr_done)[64], int grid, int threads, cudaStream_t s,
+                         Args... args) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_done[dev]) {
@@ -723,7 +725,7 @@ cudaError_t launch_early(void (*kernel)(Params...), bool (&attr_done)[64], int g
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kCopyThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = kCopySmem;
     cfg.stream = s;
     cfg.attrs = &early;
@@ -749,7 +751,7 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     note_launch();
-    return launch_early(fork_kernel, attr_done, copy_grid(c, n, int64_t(n) * max_pages), s, c, table, lens, parents,
+    return launch_early(fork_kernel, attr_done, copy_grid(c, n, int64_t(n) * max_pages), kCopyThreads, s, c, table, lens, parents,
                         child_table, B, n, max_pages, w, status);
 }
 
@@ -763,7 +765,7 @@ cudaError_t launch_cache_reorder(const ReorderArgs& a, cudaStream_t s) {
     static bool attr_done[64] = {false};
     int64_t entries = int64_t(a.n > a.B ? a.n : a.B) * a.max_pages;
     if (a.new_weights) entries = entries > 1 ? entries << (a.cache.page_shift - 2) : entries;
-    return launch_early(reorder_kernel, attr_done, copy_grid(a.cache, a.n, entries), s, a);
+    return launch_early(reorder_kernel, attr_done, copy_grid(a.cache, a.n, entries), kReorderThreads, s, a);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, int32_t* table, const int32_t* rows, int B, int n,
@@ -795,7 +797,7 @@ cudaError_t launch_cache_compact(const CacheView& c, const int32_t* table, int32
     static bool attr_done[64] = {false};
     const int64_t table_entries = int64_t(B) * max_pages;
     const int grid = copy_grid(c, c.num_pages / 2, table_entries > c.num_pages ? table_entries : c.num_pages);
-    return launch_early(compact_kernel, attr_done, grid, s, c, table, new_table, new_refcount, B, max_pages, w, status);
+    return launch_early(compact_kernel, attr_done, grid, kCopyThreads, s, c, table, new_table, new_refcount, B, max_pages, w, status);
 }
 
 cudaError_t launch_cache_copy(const CacheView& c, const int32_t* src, const int32_t* dst, int n,
@@ -806,7 +808,7 @@ cudaError_t launch_cache_copy(const CacheView& c, const int32_t* src, const int3
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     note_launch();
     static bool attr_done[64] = {false};
-    return launch_early(copy_kernel, attr_done, copy_grid(c, n, n), s, c, src, dst, w, status);
+    return launch_early(copy_kernel, attr_done, copy_grid(c, n, n), kCopyThreads, s, c, src, dst, w, status);
 }
 
 }  // namespace smla

@@ -175,6 +175,23 @@ beam_rows_kernel(const BeamArgs a) {
     const uint32_t none = order_of(-INFINITY);
     const float peak = value_of(most), ref = most == none ? 0.f : peak;
 
+    // The values of the thread's vectors that hold one of at least `from`, one after the other: few threads do this, so
+    // the vectors are loaded again, in code that is short (the kernel waited for instructions most when it was not).
+    auto look = [&](auto each, float from) {
+        uint32_t which = 0;
+#pragma unroll
+        for (int k = 0; k < kBsVecs; ++k) which |= uint32_t(tops[k] >= from) << k;
+#pragma unroll 1
+        for (; which; which &= which - 1) {
+            const int k = __ffs(which) - 1;
+            const uint4 again = __ldg(src + k * kBsThreads);
+            float v[kEach];
+            Logit<kType>::spread(again, v);
+            const int place = lead + (first + k * kBsThreads) * kEach;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) each(v[e], place + e);
+        }
+    };
     // The bound: threads whose largest value reaches it number n to 2n. Where many threads' are equal to it, their
     // first places decide (`until`).
     const int n = a.n;
@@ -193,14 +210,7 @@ beam_rows_kernel(const BeamArgs a) {
             int place = INT32_MAX;               // of the thread's first value that is equal
             if (mine == bound) {
                 if (x == at) place = xi;
-#pragma unroll
-                for (int k = 0; k < kBsVecs; ++k) {
-                    float v[kEach];
-                    Logit<kType>::spread(raw[k], v);
-#pragma unroll
-                    for (int e = 0; e < kEach; ++e)
-                        if (v[e] == at) place = min(place, lead + (first + k * kBsThreads) * kEach + e);
-                }
+                look([&](float y, int i) { if (y == at) place = min(place, i); }, at);
             }
             int lo = -1, hi = a.V - 1;           // too few up to lo, enough up to hi
             until = hi;
@@ -212,21 +222,13 @@ beam_rows_kernel(const BeamArgs a) {
         }
     }
     if (mine >= bound) {
-        const float least_value = value_of(bound);
         auto pass = [&](float y, int i) {
             const uint32_t o = order_of(y + 0.f);
             if (y != y || !(o > bound || (o == bound && i <= until))) return;
             best[atomicAdd(&count, 1)] = (static_cast<unsigned long long>(o) << 32) | (0xffffffffu - uint32_t(i));
         };
         if (xi >= 0) pass(x, xi);
-#pragma unroll
-        for (int k = 0; k < kBsVecs; ++k)
-            if (tops[k] >= least_value) {
-                float v[kEach];
-                Logit<kType>::spread(raw[k], v);
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) pass(v[e], lead + (first + k * kBsThreads) * kEach + e);
-            }
+        look(pass, value_of(bound));
     }
     // the sum of exponentials: a thread's in fp32, two at a time; the threads' with what each addition rounds off
     // beside it (64-bit additions of a warp occupy their unit for 16 cycles each)

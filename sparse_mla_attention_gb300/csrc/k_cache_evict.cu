@@ -3,7 +3,8 @@
 // Of a sequence with more than `keep` positions the first `first`, the last `recent` and, of those between,
 // the R = keep - first - recent of largest weight stay (ties: the lower position; NaN counts least), in
 // the order of their positions, in fresh pages. The R-th largest weight is found by a radix descent over the
-// weights' bits (three histograms of 2048 counts), so the choice is exact and the same in every run.
+// weights' bits (a histogram of 2048 bins, and a bisection among the weights of one bin as soon as they are few), so the
+// choice is exact and the same in every run.
 //
 // evict_plan_kernel: cluster 0 grants the free pages, the other CTAs choose, one sequence each.
 // evict_copy_kernel: moves the rows. A block's scale is the largest of its rows'
@@ -43,31 +44,34 @@ __device__ __forceinline__ int row_len(const EvictArgs& a, int b) {
 }
 
 constexpr int kDigits = 2048;                    // bins of a pass: bits 31-21, 20-10 and 9-0 of a weight
-constexpr int kRun = 16;                         // positions of a thread: in one page and one scale block
+constexpr int kRun = 16;                         // positions of a thread
 constexpr int kTile = kPlanThreads * kRun;
+constexpr int kFew = 4 * kPlanThreads;           // weights that are left to a bisection
 
 struct ChooseShared {
     int hist[kDigits];                           // of this CTA
     int all[3][kDigits];                         // of the cluster, in its first CTA
-    int digit, over;                             // the bin of the rest-th largest, and what lies above it
+    union {
+        uint32_t few[kFew];                      // weights of the bin that the last one to stay is in
+        uint16_t stays[kTile];                   // positions of a tile that stay, in order
+    };
+    int digit, over, inside;                     // the bin of the rest-th largest, what lies above it and in it
+    int n_few, rest;
+    uint32_t prefix;
     int above, ties;                             // of this CTA's part, read by the others
 };
 
-// The positions that sequence b keeps, their weights and rows. kParts CTAs share the sequence (all of a cluster, or
-// one), a run of positions each. A thread's keys stay in registers where the CTA's part is one tile (16384).
+// The positions that sequence b keeps. kParts CTAs share the sequence (all of a cluster, or one), a run of positions
+// each. A thread's keys stay in registers where the CTA's part is one tile (16384).
 template <int kParts>
 __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, ChooseShared& ch) {
     cg::cluster_group cl = cg::this_cluster();
-    const CacheView& c = a.cache;
+    auto sync_all = [&]() { if (kParts > 1) cl.sync(); else __syncthreads(); };
     int turn = 0;
-    const int64_t width = int64_t(a.max_pages) << c.page_shift;
-    const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
+    const int64_t width = int64_t(a.max_pages) << a.cache.page_shift;
+    const int len = row_len(a, b);
     const float* w = a.weights + b * width;
     int32_t* kept = a.kept + int64_t(b) * a.keep;
-    float* out = a.new_weights + b * width;
-    const int first = part * kPlanThreads + int(threadIdx.x);
-    for (int64_t i = n + int64_t(first); i < width; i += kParts * kPlanThreads) out[i] = 0.f;
-    for (int64_t i = n + int64_t(first); i < a.keep; i += kParts * kPlanThreads) kept[i] = -1;
     const int64_t per = (int64_t(len) + kParts * kRun - 1) / (kParts * kRun) * kRun;
     const int64_t s0 = min(per * part, int64_t(len)), s1 = min(s0 + per, int64_t(len));
     const bool one_tile = s1 - s0 <= kTile;
@@ -75,25 +79,30 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
     const int64_t mid0 = len <= a.keep ? len : a.first, mid1 = len <= a.keep ? len : len - a.recent;
     int rest = len <= a.keep ? 0 : a.keep - a.first - a.recent;          // of [mid0, mid1), which has more
     const bool by_weight = rest > 0;
-    uint32_t key[kRun];
-    int64_t i0 = 0;                              // the thread's first position of the tile at hand
+    uint32_t key[kRun], runs, there;             // bits of the thread's positions that compete, and that exist
     auto load = [&](int64_t base) {
-        i0 = base + kRun * int64_t(threadIdx.x);
+        const int64_t i0 = base + kRun * int64_t(threadIdx.x);
+        auto below = [&](int64_t end) {          // bits of the positions before `end`
+            return end <= i0 ? 0u : end >= i0 + kRun ? (1u << kRun) - 1 : (1u << int(end - i0)) - 1;
+        };
+        there = below(s1);
+        runs = there & below(mid1) & ~below(mid0);
 #pragma unroll
         for (int e = 0; e < kRun; e += 4) {      // (width is a multiple of 16: no quad passes a row's end)
-            const float4 v = i0 + e < s1 ? __ldg(reinterpret_cast<const float4*>(w + i0 + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = (there >> e) & 1 ? __ldg(reinterpret_cast<const float4*>(w + i0 + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
             key[e] = order_of(v.x); key[e + 1] = order_of(v.y); key[e + 2] = order_of(v.z); key[e + 3] = order_of(v.w);
         }
     };
-    auto competes = [&](int e) { return i0 + e >= mid0 && i0 + e < mid1 && i0 + e < s1; };
     if (one_tile) load(s0);
     uint32_t prefix = 0;
     if (by_weight) {                             // (the same in every CTA of the sequence)
+        if (part == 0 && threadIdx.x == 0) ch.n_few = 0;
         if (kParts > 1) {
             if (part == 0)
                 for (int i = threadIdx.x; i < 3 * kDigits; i += kPlanThreads) (&ch.all[0][0])[i] = 0;
             cl.sync();
         }
+        ChooseShared* lead = kParts > 1 ? cl.map_shared_rank(&ch, 0) : &ch;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kDigits;
@@ -103,22 +112,22 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
             __syncthreads();
             for (int64_t base = s0; base < s1; base += kTile) {
                 if (!one_tile) load(base);
+                if (runs == 0) continue;
 #pragma unroll
                 for (int e = 0; e < kRun; ++e)
-                    if (competes(e) && (key[e] & mask) == prefix)
+                    if (((runs >> e) & 1) && (key[e] & mask) == prefix)
                         atomicAdd(ch.hist + ((key[e] >> shift) & uint32_t(bins - 1)), 1);
             }
             __syncthreads();
             const int* hist = ch.hist;
             if (kParts > 1) {                    // few bins hold anything: they are added to the first CTA's
-                int* all = cl.map_shared_rank(ch.all[pass], 0);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int d = int(threadIdx.x) + 1024 * k, h = ch.hist[d];
-                    if (h) atomicAdd(all + d, h);
+                    if (h) atomicAdd(lead->all[pass] + d, h);
                 }
                 cl.sync();
-                hist = all;
+                hist = lead->all[pass];
             }
             // bins in falling order, two a thread: the sums before them
             const int d0 = bins - 1 - 2 * int(threadIdx.x), d1 = d0 - 1;
@@ -129,69 +138,116 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
                 const bool second = rest > before + h0;
                 ch.digit = second ? d1 : d0;
                 ch.over = second ? before + h0 : before;
+                ch.inside = second ? h1 : h0;
             }
             __syncthreads();
             prefix |= uint32_t(ch.digit) << shift;
             rest -= ch.over;
+            if (pass == 2 || ch.inside > kFew) continue;
+            // the bin's weights in one place, and their rest-th largest by bisection
+            const uint32_t bin = ~0u << shift;
+            for (int64_t base = s0; base < s1; base += kTile) {
+                if (!one_tile) load(base);
+                if (runs == 0) continue;
+#pragma unroll
+                for (int e = 0; e < kRun; ++e)
+                    if (((runs >> e) & 1) && (key[e] & bin) == prefix) lead->few[atomicAdd(&lead->n_few, 1)] = key[e];
+            }
+            sync_all();
+            if (part == 0) {
+                const int n = ch.n_few;
+                uint32_t mine[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = int(threadIdx.x) + kPlanThreads * k;
+                    mine[k] = i < n ? ch.few[i] : 0u;                    // (below every bound)
+                }
+                // at least `rest` reach lo, fewer hi
+                uint32_t lo = prefix, hi = prefix | ~bin;
+                const bool last = [&] {          // (the bin's last value, so that hi + 1 need not exist)
+                    int r = __syncthreads_count(n > 0 && mine[0] == hi);
+                    for (int k = 1; k < 4 && kPlanThreads * k < n; ++k)
+                        r += __syncthreads_count(k == 1 ? mine[1] == hi : k == 2 ? mine[2] == hi : mine[3] == hi);
+                    if (r < rest) return false;
+                    return true;
+                }();
+                int over = 0;
+                bool exact = false;
+                if (last) lo = hi;
+                while (!last && hi - lo > 1) {
+                    const uint32_t mid = lo + (hi - lo) / 2;
+                    int r = __syncthreads_count(mine[0] >= mid);
+                    if (n > kPlanThreads) {
+                        r += __syncthreads_count(mine[1] >= mid);
+                        if (n > 2 * kPlanThreads) r += __syncthreads_count(mine[2] >= mid) + __syncthreads_count(mine[3] >= mid);
+                    }
+                    if (r == rest) { lo = mid; exact = true; break; }    // these and no others
+                    if (r > rest) lo = mid; else hi = mid;
+                }
+                if (!last && !exact) {           // those above lo
+                    over = __syncthreads_count(mine[0] > lo);
+                    if (n > kPlanThreads)
+                        over += __syncthreads_count(mine[1] > lo) + __syncthreads_count(mine[2] > lo) +
+                                __syncthreads_count(mine[3] > lo);
+                }
+                if (threadIdx.x == 0) {
+                    ch.prefix = exact ? lo - 1 : lo;
+                    ch.rest = exact ? 0 : rest - over;
+                }
+            }
+            sync_all();
+            prefix = lead->prefix;
+            rest = lead->rest;
+            break;
         }
     }
-    // keys above prefix stay (1), and the first `rest` equal ones (1 << 16)
-    auto verdict = [&](int e) {
-        if (i0 + e >= s1) return 0;
-        if (!competes(e)) return 1;
-        return !by_weight ? 0 : key[e] > prefix ? 1 : key[e] == prefix ? 1 << 16 : 0;
+    // keys above prefix stay, and the first `rest` equal ones
+    auto verdicts = [&](uint32_t& stay, uint32_t& tie) {
+        stay = there & ~runs;
+        tie = 0;
+        if (!by_weight || runs == 0) return;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+            stay |= uint32_t(key[e] > prefix) << e & runs;
+            tie |= uint32_t(key[e] == prefix) << e & runs;
+        }
     };
-    int64_t at = 0, tied_before = 0;
+    int64_t at = 0, tied = 0;
+    uint32_t stay, tie;
     if (kParts > 1) {
         int above = 0, ties = 0;
         for (int64_t base = s0; base < s1; base += kTile) {
             if (!one_tile) load(base);
-            int count = 0, total;
-#pragma unroll
-            for (int e = 0; e < kRun; ++e) count += verdict(e);
-            cta_scan(count & 0xffff, sh, turn, &total);
+            int total;
+            verdicts(stay, tie);
+            cta_scan(__popc(stay), sh, turn, &total);
             above += total;
-            cta_scan(count >> 16, sh, turn, &total);
+            cta_scan(__popc(tie), sh, turn, &total);
             ties += total;
         }
         if (threadIdx.x == 0) { ch.above = above; ch.ties = ties; }
         cl.sync();
         for (int r = 0; r < part; ++r) {
             at += cl.map_shared_rank(&ch, r)->above;
-            tied_before += cl.map_shared_rank(&ch, r)->ties;
+            tied += cl.map_shared_rank(&ch, r)->ties;
         }
     }
-    int t = int(tied_before);
+    at += min(tied, int64_t(rest));
     for (int64_t base = s0; base < s1; base += kTile) {
         if (!one_tile) load(base);
-        int2 from = make_int2(-1, 0);            // the run's first row of the pool and its scale
-        if (i0 < s1) {
-            const int page = __ldg(a.table + int64_t(b) * a.max_pages + (i0 >> c.page_shift));
-            if (page >= 0 && page < c.num_pages) {
-                from.x = (page << c.page_shift) + int(i0 & ((1 << c.page_shift) - 1));
-                from.y = __float_as_int(__ldg(c.scales + (from.x >> c.block_shift)));
-            }
-        }
-        int count = 0, stay, tie;
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) count += verdict(e);
-        const int stays = cta_scan(count & 0xffff, sh, turn, &stay), tied0 = cta_scan(count >> 16, sh, turn, &tie);
-        int64_t to = at + stays;
-        int tied = t + tied0;
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-            const int v = verdict(e);
-            if (v == 1 || (v != 0 && tied < rest)) {
-                const int64_t row = to + min(tied, rest);
-                kept[row] = int(i0 + e);
-                out[row] = __ldg(w + i0 + e);
-                a.from[int64_t(b) * a.keep + row] = make_int2(from.x < 0 ? -1 : from.x + e, from.y);
-            }
-            to += v & 1;
-            tied += v >> 16;
-        }
-        at += stay;
-        t += tie;
+        verdicts(stay, tie);
+        // of the ties those that are among the first `rest`
+        int total;
+        const int64_t first = tied + cta_scan(__popc(tie), sh, turn, &total);
+        tied += total;
+        for (int64_t drop = first + __popc(tie) - max(int64_t(rest), first); drop > 0; --drop) tie ^= 1u << (31 - __clz(tie));
+        stay |= tie;
+        int to = cta_scan(__popc(stay), sh, turn, &total);
+        for (; stay; stay &= stay - 1) ch.stays[to++] = uint16_t(kRun * threadIdx.x + __ffs(stay) - 1);
+        __syncthreads();
+        for (int i = threadIdx.x; i < total; i += kPlanThreads) kept[at + i] = int(base) + ch.stays[i];
+        at += total;
+        __syncthreads();
     }
     if (kParts > 1) cl.sync();                   // no CTA leaves while another reads its counts
 }
@@ -202,11 +258,11 @@ template <int kParts>
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 evict_plan_kernel(const EvictArgs a) {
     __shared__ PlanShared sh;
-    __shared__ ChooseShared ch;
+    extern __shared__ __align__(16) uint8_t room[];
     grid_dep_launch();
     if (blockIdx.x >= kPlanCtas) {
         const int u = int(blockIdx.x) - kPlanCtas, b = u / kParts;
-        if (b < a.B) choose<kParts>(a, b, u % kParts, sh, ch);
+        if (b < a.B) choose<kParts>(a, b, u % kParts, sh, *reinterpret_cast<ChooseShared*>(room));
         return;
     }
     cg::cluster_group cl = cg::this_cluster();
@@ -223,22 +279,14 @@ evict_plan_kernel(const EvictArgs a) {
 }
 
 // A warp moves up to 16 rows at a time, all of them in flight; it looks at the scales of the whole block.
-__global__ void __launch_bounds__(kEvictCopyThreads)
+__global__ void __launch_bounds__(kEvictCopyThreads, 2)
 evict_copy_kernel(const EvictArgs a) {
     grid_dep_wait();
     const CacheView& c = a.cache;
     const int lane = threadIdx.x & 31;
     const int64_t threads = int64_t(gridDim.x) * kEvictCopyThreads, first = int64_t(blockIdx.x) * kEvictCopyThreads + threadIdx.x;
+    const int64_t width = int64_t(a.max_pages) << c.page_shift;
     const bool ok = __ldcg(a.granted) != 0;
-    for (int64_t x = first; x < int64_t(a.B) * a.max_pages; x += threads) {
-        const int b = int(x / a.max_pages), j = int(x - int64_t(b) * a.max_pages);
-        a.new_table[x] = ok && j < __ldcg(a.need + b) ? __ldcg(a.fresh + __ldcg(a.start + b) + j) : -1;
-        if (j == 0) {
-            const int len = row_len(a, b);
-            a.new_lens[b] = !ok ? 0 : len < a.keep ? len : a.keep;
-        }
-    }
-    if (!ok) return;
     const int block = 1 << c.block_shift, page_mask = (1 << c.page_shift) - 1;
     const int64_t per = (int64_t(a.keep) + 15) >> 4;
     bool bad = false;
@@ -247,31 +295,55 @@ evict_copy_kernel(const EvictArgs a) {
         const int64_t r0 = (u - b * per) << 4;
         const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
         const int rows = int(min(n - r0, int64_t(16)));
+        int32_t* kept = a.kept + int64_t(b) * a.keep;
+        if (lane < 16 && lane >= rows && r0 + lane < a.keep) kept[r0 + lane] = -1;
         if (rows <= 0) continue;
+        // the rows of the block, up to two a lane: where they lie (-1: no page) and their scales
         const int64_t block0 = r0 & ~int64_t(block - 1);
-        const int page = __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift));
-        // the rows of the block, up to two a lane, and this warp's
-        const int2* list = a.from + int64_t(b) * a.keep;
-        float size = 0.f;
-        for (int r = lane; r < block && block0 + r < n; r += 32) size = fmaxf(size, __int_as_float(__ldcg(list + block0 + r).y));
-        const int2 own = lane < rows ? __ldcg(list + r0 + lane) : make_int2(-1, 0);
-        bad |= lane < rows && own.x < 0;
+        const int32_t* table = a.table + int64_t(b) * a.max_pages;
+        int p[2], from[2] = {-1, -1};
+        float scale[2] = {0.f, 0.f};
 #pragma unroll
-        for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-        const int64_t to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
+        for (int k = 0; k < 2; ++k) {
+            const int r = lane + 32 * k;
+            p[k] = r < block && block0 + r < n ? __ldcg(kept + block0 + r) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (p[k] >= 0) {
+                const int page = __ldg(table + (p[k] >> c.page_shift));
+                if (page >= 0 && page < c.num_pages) from[k] = (page << c.page_shift) + (p[k] & page_mask);
+                else bad = true;
+            }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (from[k] >= 0) scale[k] = __ldg(c.scales + (from[k] >> c.block_shift));
+        // this warp's 16 of them
+        const int half = int(r0 - block0) >> 5, lane0 = int(r0 - block0) & 31;
+        const int mine = half ? from[1] : from[0];
+        const float own = half ? scale[1] : scale[0];
+        if (lane >= lane0 && lane < lane0 + rows)
+            a.new_weights[b * width + r0 + lane - lane0] = __ldg(a.weights + b * width + (half ? p[1] : p[0]));
+        if (!ok) continue;
         uint4 v[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int row = __shfl_sync(0xffffffffu, own.x, r);
-            v[r] = row >= 0 ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane) : make_uint4(0, 0, 0, 0);
+            const int row = __shfl_sync(0xffffffffu, mine, lane0 + r);
+            v[r] = row >= 0 && r < rows ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane)
+                                        : make_uint4(0, 0, 0, 0);
         }
+        float size = fmaxf(scale[0], scale[1]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
+        const int page = __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift));
+        const int64_t to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
+            const float was = __shfl_sync(0xffffffffu, own, lane0 + r);
             if (r >= rows) break;
-            const float scale = __int_as_float(__shfl_sync(0xffffffffu, own.y, r));
             uint4 x = v[r];
-            if (scale != size) {
-                const float ratio = scale / size;
+            if (was != size) {
+                const float ratio = was / size;
                 x = make_uint4(recode4(x.x, ratio), recode4(x.y, ratio), recode4(x.z, ratio), recode4(x.w, ratio));
             }
             *(reinterpret_cast<uint4*>(c.pages + (to + r) * kD) + lane) = x;
@@ -279,20 +351,47 @@ evict_copy_kernel(const EvictArgs a) {
         if (r0 == block0 && lane == 0) c.scales[to >> c.block_shift] = size;
     }
     if (bad) flag_status(a.status, SMLA_ERR_INDEX);
+    // tables, lengths, and zeros behind the weights
+    for (int64_t x = first; x < int64_t(a.B) * a.max_pages; x += threads) {
+        const int b = int(x / a.max_pages), j = int(x - int64_t(b) * a.max_pages);
+        const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
+        a.new_table[x] = ok && j < __ldcg(a.need + b) ? __ldcg(a.fresh + __ldcg(a.start + b) + j) : -1;
+        if (j == 0) a.new_lens[b] = ok ? n : 0;
+    }
+    const int64_t quads = width / 4;
+    for (int64_t x = first; x < a.B * quads; x += threads) {
+        const int b = int(x / quads);
+        const int64_t i = 4 * (x - b * quads);
+        const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
+        float* out = a.new_weights + b * width + i;
+        if (i >= n) *reinterpret_cast<float4*>(out) = make_float4(0.f, 0.f, 0.f, 0.f);
+        else if (i + 4 > n)
+            for (int e = int(n - i); e < 4; ++e) out[e] = 0.f;
+    }
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
+    static bool attr_done[64] = {false};
     int dev = 0, sms = 1;
     cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(evict_plan_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(sizeof(ChooseShared)));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(evict_plan_kernel<kPlanCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     int(sizeof(ChooseShared)));
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+    }
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // Long sequences have a cluster each.
     const int parts = (int64_t(a.max_pages) << a.cache.page_shift) > 16384 ? kPlanCtas : 1;
-    const int64_t grid = kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas;
-    if (parts > 1) evict_plan_kernel<kPlanCtas><<<unsigned(grid), kPlanThreads, 0, s>>>(a);
-    else evict_plan_kernel<1><<<unsigned(grid), kPlanThreads, 0, s>>>(a);
+    const unsigned grid = unsigned(kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas);
+    if (parts > 1) evict_plan_kernel<kPlanCtas><<<grid, kPlanThreads, sizeof(ChooseShared), s>>>(a);
+    else evict_plan_kernel<1><<<grid, kPlanThreads, sizeof(ChooseShared), s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t units = int64_t(a.B) * ((int64_t(a.keep) + 15) / 16), blocks = (units + 7) / 8, most = int64_t(sms) * 4;
+    const int64_t units = int64_t(a.B) * ((int64_t(a.keep) + 15) / 16), blocks = (units + 7) / 8, most = int64_t(sms) * 2;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;

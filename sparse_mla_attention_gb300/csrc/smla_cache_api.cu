@@ -69,7 +69,7 @@ PageScratch carve(char* ws, const ScratchPlan& p) {
     return PageScratch{at(kStatusBytes), at(p.need), at(p.tail), at(p.src), at(p.dst), at(p.map)};
 }
 
-struct EvictPlan { size_t need, start, fresh, from, bytes; };
+struct EvictPlan { size_t need, start, fresh, bytes; };
 
 EvictPlan plan_evict(const smla_cache& c, int64_t B, int64_t keep) {
     EvictPlan p{};
@@ -78,7 +78,6 @@ EvictPlan plan_evict(const smla_cache& c, int64_t B, int64_t keep) {
     p.need = take(size_t(B) * 4);
     p.start = take(size_t(B) * 4);
     p.fresh = take(size_t(c.num_pages) * 4);
-    p.from = take(size_t(B) * keep * sizeof(int2));
     p.bytes = off;
     return p;
 }
@@ -419,7 +418,6 @@ int smla_cache_evict(const smla_cache* cache, const int32_t* table, const int32_
     a.new_table = new_table; a.new_lens = new_lens; a.new_weights = new_weights; a.kept = kept;
     a.B = B; a.max_pages = max_pages; a.keep = keep; a.first = first; a.recent = recent;
     a.granted = at(kStatusBytes); a.need = at(plan.need); a.start = at(plan.start); a.fresh = at(plan.fresh);
-    a.from = reinterpret_cast<int2*>(ws + plan.from);
     a.status = static_cast<unsigned*>(workspace);
     return cuda_rc(launch_cache_evict(a, s));
 }

@@ -241,12 +241,12 @@ struct WeightsArgs {
 size_t weights_scratch_bytes(int T, int H, int B);
 cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s);
 
-// Arguments of an eviction. need, start [B], fresh [num_pages], granted [1], from [B, keep] (row, scale): workspace.
+// Arguments of an eviction. need, start [B], fresh [num_pages], granted [1]: workspace.
 struct EvictArgs {
     CacheView cache; const int32_t* table; const int32_t* lens; const float* weights;
     int32_t* new_table; int32_t* new_lens; float* new_weights; int32_t* kept;
     int B, max_pages, keep, first, recent;
-    int32_t* need; int32_t* start; int32_t* fresh; int32_t* granted; int2* from;
+    int32_t* need; int32_t* start; int32_t* fresh; int32_t* granted;
     unsigned* status;
 };
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);

@@ -340,7 +340,7 @@ def cache_weights(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens:
         if earlier.shape != weights.shape:
             raise ValueError("earlier must have the shape of weights")
     dims = SmlaPagedDims(T, H, D, 0, B, max_pages, 0.0 if scale is None else float(scale))
-    ws = _on_device(cache, workspace, _size_of(_weights_sizes, (T, H, B), "smla_weights_workspace_size", dims))
+    ws = _on_device(cache, workspace, _size_of(_weights_sizes, (T, H), "smla_weights_workspace_size", dims))
     _run(cache, "smla_cache_weights", ws, check_status, p_q, cache._ref, p_table, p_cu, p_lens, p_lse, p_earlier,
          float(decay), p_weights, ctypes.byref(dims))
     return weights

@@ -290,15 +290,19 @@ evict_copy_kernel(const EvictArgs a) {
     const int block = 1 << c.block_shift, page_mask = (1 << c.page_shift) - 1;
     const int64_t per = (int64_t(a.keep) + 15) >> 4;
     bool bad = false;
-    for (int64_t u = first >> 5; u < a.B * per; u += threads >> 5) {
+    // A unit: up to 16 rows of a sequence, from r0 on. Where they lie and their scales, the block's, the place they go to.
+    struct Unit { int rows, lane0, from; float scale, size; int64_t to; };
+    auto look = [&](int64_t u) {
+        Unit x{0, 0, -1, 0.f, 0.f, -1};
+        if (u >= a.B * per) return x;
         const int b = int(u / per);
         const int64_t r0 = (u - b * per) << 4;
         const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
-        const int rows = int(min(n - r0, int64_t(16)));
+        x.rows = int(max(min(n - r0, int64_t(16)), int64_t(0)));
         int32_t* kept = a.kept + int64_t(b) * a.keep;
-        if (lane < 16 && lane >= rows && r0 + lane < a.keep) kept[r0 + lane] = -1;
-        if (rows <= 0) continue;
-        // the rows of the block, up to two a lane: where they lie (-1: no page) and their scales
+        if (lane < 16 && lane >= x.rows && r0 + lane < a.keep) kept[r0 + lane] = -1;
+        if (x.rows == 0) return x;
+        // the rows of the block, up to two a lane
         const int64_t block0 = r0 & ~int64_t(block - 1);
         const int32_t* table = a.table + int64_t(b) * a.max_pages;
         int p[2], from[2] = {-1, -1};
@@ -308,47 +312,55 @@ evict_copy_kernel(const EvictArgs a) {
             const int r = lane + 32 * k;
             p[k] = r < block && block0 + r < n ? __ldcg(kept + block0 + r) : -1;
         }
+        const int page = ok ? __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift)) : 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (p[k] >= 0) {
-                const int page = __ldg(table + (p[k] >> c.page_shift));
-                if (page >= 0 && page < c.num_pages) from[k] = (page << c.page_shift) + (p[k] & page_mask);
+                const int old = __ldg(table + (p[k] >> c.page_shift));
+                if (old >= 0 && old < c.num_pages) from[k] = (old << c.page_shift) + (p[k] & page_mask);
                 else bad = true;
             }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (from[k] >= 0) scale[k] = __ldg(c.scales + (from[k] >> c.block_shift));
         // this warp's 16 of them
-        const int half = int(r0 - block0) >> 5, lane0 = int(r0 - block0) & 31;
-        const int mine = half ? from[1] : from[0];
-        const float own = half ? scale[1] : scale[0];
-        if (lane >= lane0 && lane < lane0 + rows)
-            a.new_weights[b * width + r0 + lane - lane0] = __ldg(a.weights + b * width + (half ? p[1] : p[0]));
-        if (!ok) continue;
+        const int half = int(r0 - block0) >> 5;
+        x.lane0 = int(r0 - block0) & 31;
+        x.from = half ? from[1] : from[0];
+        x.scale = half ? scale[1] : scale[0];
+        if (lane >= x.lane0 && lane < x.lane0 + x.rows)
+            a.new_weights[b * width + r0 + lane - x.lane0] = __ldg(a.weights + b * width + (half ? p[1] : p[0]));
+        x.size = fmaxf(scale[0], scale[1]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) x.size = fmaxf(x.size, __shfl_xor_sync(0xffffffffu, x.size, d));
+        x.to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
+        if (ok && r0 == block0 && lane == 0) c.scales[x.to >> c.block_shift] = x.size;
+        return x;
+    };
+    const int64_t step = threads >> 5;
+    Unit at = look(first >> 5);
+    for (int64_t u = first >> 5; u < a.B * per; u += step) {
         uint4 v[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int row = __shfl_sync(0xffffffffu, mine, lane0 + r);
-            v[r] = row >= 0 && r < rows ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane)
-                                        : make_uint4(0, 0, 0, 0);
+            const int row = __shfl_sync(0xffffffffu, at.from, at.lane0 + r);
+            v[r] = ok && row >= 0 && r < at.rows ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane)
+                                                 : make_uint4(0, 0, 0, 0);
         }
-        float size = fmaxf(scale[0], scale[1]);
+        const Unit then = look(u + step);        // while these are on their way
+        if (ok)
 #pragma unroll
-        for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-        const int page = __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift));
-        const int64_t to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const float was = __shfl_sync(0xffffffffu, own, lane0 + r);
-            if (r >= rows) break;
-            uint4 x = v[r];
-            if (was != size) {
-                const float ratio = was / size;
-                x = make_uint4(recode4(x.x, ratio), recode4(x.y, ratio), recode4(x.z, ratio), recode4(x.w, ratio));
+            for (int r = 0; r < 16; ++r) {
+                const float was = __shfl_sync(0xffffffffu, at.scale, at.lane0 + r);
+                if (r >= at.rows) break;
+                uint4 x = v[r];
+                if (was != at.size) {
+                    const float ratio = was / at.size;
+                    x = make_uint4(recode4(x.x, ratio), recode4(x.y, ratio), recode4(x.z, ratio), recode4(x.w, ratio));
+                }
+                *(reinterpret_cast<uint4*>(c.pages + (at.to + r) * kD) + lane) = x;
             }
-            *(reinterpret_cast<uint4*>(c.pages + (to + r) * kD) + lane) = x;
-        }
-        if (r0 == block0 && lane == 0) c.scales[to >> c.block_shift] = size;
+        at = then;
     }
     if (bad) flag_status(a.status, SMLA_ERR_INDEX);
     // tables, lengths, and zeros behind the weights

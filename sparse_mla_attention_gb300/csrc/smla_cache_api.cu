@@ -330,7 +330,7 @@ int smla_cache_copy_pages(const smla_cache* cache, const int32_t* src, const int
 int smla_weights_workspace_size(const smla_paged_dims* d, size_t* bytes) {
     if (!d || !bytes) return SMLA_ERR_NULL;
     if (d->T < 0 || d->B < 0 || d->B > kMaxSeqs || d->H < 16 || d->H > 128 || d->H % 16 != 0) return SMLA_ERR_SHAPE;
-    *bytes = kStatusBytes + weights_scratch_bytes(d->T, d->H, d->B);
+    *bytes = kStatusBytes + weights_scratch_bytes(d->T, d->H);
     return SMLA_OK;
 }
 
@@ -353,7 +353,7 @@ int smla_cache_weights(const uint16_t* q, const smla_cache* cache, const int32_t
     if (decay == 0.f) earlier = nullptr;
     const void* ptrs[] = {c.pages, c.scales, q, table, cu, lens, lse, earlier, weights, workspace};
     if ((rc = check_align(ptrs, 10))) return rc;
-    if (workspace_bytes < kStatusBytes + weights_scratch_bytes(d.T, d.H, d.B)) return SMLA_ERR_WORKSPACE;
+    if (workspace_bytes < kStatusBytes + weights_scratch_bytes(d.T, d.H)) return SMLA_ERR_WORKSPACE;
     const size_t sums = size_t(d.B) * d.max_pages * c.page_size * 4;
     const bool in_place = earlier == weights;
     const Span ins[] = {{c.pages, page_bytes(c)}, {c.scales, scale_bytes(c)}, {q, size_t(d.T) * d.H * kD * 2},

@@ -238,7 +238,7 @@ struct WeightsArgs {
     unsigned* status;
     char* scratch;       // workspace behind the status word
 };
-size_t weights_scratch_bytes(int T, int H, int B);
+size_t weights_scratch_bytes(int T, int H);
 cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s);
 
 // Arguments of an eviction. need, start [B], fresh [num_pages], granted [1]: workspace.

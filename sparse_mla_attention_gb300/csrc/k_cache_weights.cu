@@ -42,7 +42,16 @@ constexpr int kCwRows = 128;                     // rows of q of a chunk at most
 constexpr int kCwSlots = 6, kCwSlotBytes = kCwTile * 128;
 constexpr int kCwQSlots = 8, kCwQSlotBytes = 16384;
 constexpr int kCwLoadWarp = 8, kCwMmaWarp = 9, kCwQWarp = 10, kCwThreads = 352;
+constexpr int kCwMmaWarp2 = 11, kCwLThreads = 384;
+// With the cache resident: rows of a chunk, chunks in flight, tiles of a pass.
+constexpr int kCwLRows = 32, kCwLSlots = 4, kCwLQSlots = 4, kCwLTiles = 3;
+constexpr int kCwLQBytes = kCwLRows * 1024;
+constexpr uint32_t kCwLColS = 128 * kCwLTiles;   // TMEM: a tile 128 columns each, then two buffers
+constexpr uint32_t kCwLCols = (512 - kCwLColS) / 2;
+static_assert(2 * kCwLRows <= int(kCwLCols), "a product has a column for each row of q and part");
+constexpr int kCwMaxCtas = 160;
 constexpr int kCwSplitThreads = 256;
+constexpr int kCwManyRows = 512;                 // rows of q a sequence, on average, from which on the cache is resident
 constexpr int kCwMaxBlocks = 1024;               // of the splitting kernel
 
 // Two floats at a time.
@@ -77,16 +86,22 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
     return r;
 }
 
+// Where a CTA's work begins and ends.
+struct CwPlace {
+    int b0;                                      // first sequence with work of this CTA
+    int64_t at0, lo, hi;                         // its first unit; the CTA's units
+    int64_t per, rem;                            // of a CTA; the first rem have one more
+    int64_t sum[kCwLThreads / 32];
+};
+
 struct CwShared {
     uint64_t full[kCwSlots], empty[kCwSlots];
     uint64_t q_full[kCwQSlots], q_empty[kCwQSlots];
     uint64_t f_full[2], f_empty[2];              // the factors of a chunk's columns
     uint64_t t_full[2], t_empty[2], drain;
+    CwPlace at;
     uint32_t tbase;
     volatile int abort_flag;
-    int b0;                                      // first sequence with work of this CTA
-    int64_t at0, lo, hi;                         // its first unit; the CTA's units
-    int64_t sum[kCwThreads / 32];
 };
 
 constexpr int kCwQAt = kCwSlots * kCwSlotBytes;
@@ -101,7 +116,28 @@ struct CwParams {
     float* factor;                               // [2][T * H] score factor, -lse in log2 units
     unsigned* bits;                              // status bits of each block of the splitting kernel
     int blocks;
+    int resident;                                // which of the two kernels follows the splitting one
+    // of the resident kernel's CTAs: sums of a pass whose chunks they have from one after the first on (0) or up to one
+    // before the last (1); and, for the CTA with the last one, the pass: {sequence (-1: none), pass, CTA with the first}
+    float* parts;                                // [CTAs][2][3][128]
+    int4* meta;                                  // [CTAs]
 };
+
+struct CwLShared {
+    uint64_t full[kCwLSlots], empty[kCwLSlots];
+    uint64_t q_full[kCwLQSlots], q_empty[kCwLQSlots];
+    uint64_t x_full;                             // the tiles of a pass are in TMEM
+    uint64_t t_full[2], t_empty[2], drain[2];
+    CwPlace at;
+    uint32_t tbase;
+    volatile int abort_flag;
+    float sums[kCwLTiles][kCwTile];              // of the second team
+};
+constexpr int kCwLQAt = kCwLSlots * kCwSlotBytes;
+constexpr int kCwLFactorAt = kCwLQAt + kCwLQSlots * kCwLQBytes;
+constexpr int kCwLSharedAt = kCwLFactorAt + kCwLQSlots * 2 * kCwLRows * 4;
+constexpr int kCwLSmem = kCwLSharedAt + int(sizeof(CwLShared));
+static_assert(kCwLSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 
 __device__ __forceinline__ bool cw_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
     bool ok = mbar_try_wait(bar, parity);
@@ -135,8 +171,11 @@ __device__ __forceinline__ bool cw_tokens(const WeightsArgs& a, int b, int& c0, 
     return c0 >= 0 && c1 >= c0 && c1 <= a.T;
 }
 
-// Rows of a sequence's chunks (but for the last): up to 64 rows are one chunk and need half of the room.
-__device__ __forceinline__ int cw_chunk_rows(int rows) { return rows <= kCwRows / 2 ? rows : kCwRows; }
+// Rows of a sequence's chunks (but for the last). Where the cache streams, up to 64 rows are one chunk and need half of
+// the room.
+__device__ __forceinline__ int cw_chunk_rows(int rows, int resident) {
+    return resident ? kCwLRows : rows <= kCwRows / 2 ? rows : kCwRows;
+}
 
 __device__ __forceinline__ uint32_t cw_e4m3x2(__half2 v) {
     return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
@@ -155,18 +194,43 @@ __device__ __forceinline__ int cw_seen(const WeightsArgs& a, int c0, int c1) {
 
 struct CwSize {
     int tiles, chunk_rows, chunks;
-    __device__ __forceinline__ CwSize(int seen, int rows)
-        : tiles((seen + kCwTile - 1) / kCwTile), chunk_rows(cw_chunk_rows(rows)),
+    __device__ __forceinline__ CwSize(int seen, int rows, int resident)
+        : tiles((seen + kCwTile - 1) / kCwTile), chunk_rows(cw_chunk_rows(rows, resident)),
           chunks(rows > 0 ? (rows + chunk_rows - 1) / chunk_rows : 0) {}
-    __device__ __forceinline__ int64_t units() const { return int64_t(tiles) * chunks; }
+    // what is dealt out: (tile, chunk), or (three tiles, chunk) where the cache is resident
+    __device__ __forceinline__ int64_t units(int resident) const {
+        return int64_t(resident ? (tiles + kCwLTiles - 1) / kCwLTiles : tiles) * chunks;
+    }
 };
 
+// The weights of 16 columns of a position, two at a time.
+__device__ __forceinline__ float cw_sum16(const uint32_t (&hi)[16], const uint32_t (&lo)[16], uint64_t scale2,
+                                          const float* fx, const float* fy) {
+    const uint64_t sixteenth = pair_of(0.0625f, 0.0625f);
+    uint64_t part[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(fx + e), y = *reinterpret_cast<const ulonglong2*>(fy + e);
+#pragma unroll
+        for (int d = 0; d < 4; d += 2) {
+            const uint64_t s = fma2(pair_of(lo[e + d], lo[e + d + 1]), sixteenth, pair_of(hi[e + d], hi[e + d + 1]));
+            const float2 w = floats_of(fma2(mul2(s, scale2), d ? x.y : x.x, d ? y.y : y.x));
+            part[d >> 1] = add2(part[d >> 1], pair_of(ex2_approx(w.x), ex2_approx(w.y)));
+        }
+    }
+    const float2 both = floats_of(add2(part[0], part[1]));
+    return both.x + both.y;
+}
+
 // Where a CTA's work lies: items (sequence b, its tiles [k0, k1)), all chunks of each. A warp walks together.
+// (The shuffles tell the compiler that a warp's lanes agree: descriptors stay in uniform registers.)
+__device__ __forceinline__ int cw_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 struct CwWalk {
     int b, c0, c1, seen, k0, k1;
     int rows, chunk_rows, chunks;
     int64_t at, units, lo, hi;
-    __device__ __forceinline__ CwWalk(const CwShared& sh) : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi) {}
+    __device__ __forceinline__ CwWalk(const CwPlace& sh) : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi) {}
     __device__ __forceinline__ bool next(const CwParams& p) {
         do {
             at += units;
@@ -175,15 +239,17 @@ struct CwWalk {
             ++b;
             if (at >= hi || b >= p.a.B) return false;
             if (!cw_tokens(p.a, b, c0, c1) || c0 == c1) continue;
+            c0 = cw_same(c0);
+            c1 = cw_same(c1);
             seen = cw_seen(p.a, c0, c1);
             rows = (c1 - c0) * p.a.H;
-            const CwSize n(seen, rows);
+            const CwSize n(seen, rows, p.resident);
             chunk_rows = n.chunk_rows;
             chunks = n.chunks;
-            units = n.units();
+            units = n.units(p.resident);
             // tile k is whose the unit at + k * chunks is
-            k0 = at >= lo ? 0 : int(min(int64_t(n.tiles), (lo - at + chunks - 1) / chunks));
-            k1 = int(min(int64_t(n.tiles), (hi - at + chunks - 1) / chunks));
+            k0 = cw_same(at >= lo ? 0 : int(min(int64_t(n.tiles), (lo - at + chunks - 1) / chunks)));
+            k1 = cw_same(int(min(int64_t(n.tiles), (hi - at + chunks - 1) / chunks)));
         } while (k0 >= k1);
         return true;
     }
@@ -193,17 +259,60 @@ struct CwWalk {
     }
 };
 
+// The resident kernel's work: items (sequence b, its units [u0, u1): three tiles from 3 (u / chunks) on, chunk u % chunks).
+struct CwUnits {
+    int b, c0, c1, seen, rows, tiles, chunks;
+    int64_t at, units, lo, hi, u0, u1;
+    __device__ __forceinline__ CwUnits(const CwPlace& sh) : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi) {}
+    __device__ __forceinline__ bool next(const CwParams& p) {
+        do {
+            at += units;
+            units = u0 = u1 = 0;
+            ++b;
+            if (at >= hi || b >= p.a.B) return false;
+            if (!cw_tokens(p.a, b, c0, c1) || c0 == c1) continue;
+            c0 = cw_same(c0);
+            c1 = cw_same(c1);
+            seen = cw_seen(p.a, c0, c1);
+            rows = (c1 - c0) * p.a.H;
+            const CwSize n(seen, rows, 1);
+            tiles = n.tiles;
+            chunks = n.chunks;
+            units = n.units(1);
+            u0 = max(lo - at, int64_t(0));
+            u1 = min(hi - at, units);
+        } while (u0 >= u1);
+        return true;
+    }
+    // the item's passes [first(), last()], a pass's tiles, and its chunks [from(k), to(k))
+    __device__ __forceinline__ int first() const { return cw_same(int(u0 / chunks)); }
+    __device__ __forceinline__ int last() const { return cw_same(int((u1 - 1) / chunks)); }
+    __device__ __forceinline__ int width(int k) const { return cw_same(min(tiles - k * kCwLTiles, kCwLTiles)); }
+    __device__ __forceinline__ int from(int k) const { return cw_same(int(max(u0 - int64_t(k) * chunks, int64_t(0)))); }
+    __device__ __forceinline__ int to(int k) const { return cw_same(int(min(u1 - int64_t(k) * chunks, int64_t(chunks)))); }
+    __device__ __forceinline__ int chunk_size(int j) const {
+        const int left = rows - j * kCwLRows;
+        return left < kCwLRows ? left : kCwLRows;
+    }
+};
+
 // Units of sequence b; the whole warp asks.
 __device__ __forceinline__ int64_t cw_units(const CwParams& p, int b) {
     int c0, c1;
     if (!cw_tokens(p.a, b, c0, c1) || c0 == c1) return 0;
-    return CwSize(cw_seen(p.a, c0, c1), (c1 - c0) * p.a.H).units();
+    return CwSize(cw_seen(p.a, c0, c1), (c1 - c0) * p.a.H, p.resident).units(p.resident);
+}
+
+// The CTA that has a unit.
+__device__ __forceinline__ int cw_owner(const CwPlace& sh, int64_t unit) {
+    const int64_t longer = sh.rem * (sh.per + 1);
+    return int(unit < longer ? unit / (sh.per + 1) : sh.rem + (unit - longer) / sh.per);
 }
 
 // The CTA's share of the units and the sequence that it begins in.
-__device__ void cw_locate(const CwParams& p, CwShared& sh) {
+__device__ void cw_locate(const CwParams& p, CwPlace& sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int run = (p.a.B + kCwThreads - 1) / kCwThreads;
+    const int run = (p.a.B + int(blockDim.x) - 1) / int(blockDim.x);
     const int b0 = int(min(int64_t(threadIdx.x) * run, int64_t(p.a.B))), b1 = min(b0 + run, p.a.B);
     int64_t mine = 0;
     for (int i = 0; i < run; ++i) {
@@ -217,7 +326,7 @@ __device__ void cw_locate(const CwParams& p, CwShared& sh) {
             const int most = cw_seen(p.a, __shfl_sync(0xffffffffu, c0, l), __shfl_sync(0xffffffffu, c1, l));
             if (lane == l) seen = most;
         }
-        if (live) mine += CwSize(seen, (c1 - c0) * p.a.H).units();
+        if (live) mine += CwSize(seen, (c1 - c0) * p.a.H, p.resident).units(p.resident);
     }
     int64_t x = mine;
 #pragma unroll
@@ -229,14 +338,14 @@ __device__ void cw_locate(const CwParams& p, CwShared& sh) {
     if (threadIdx.x == 0) sh.b0 = p.a.B;
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int w = 0; w < kCwThreads / 32; ++w) {
+    for (int w = 0; w < int(blockDim.x) / 32; ++w) {
         if (w < warp) before += sh.sum[w];
         total += sh.sum[w];
     }
     int64_t at = before + x - mine;
     const int64_t per = total / gridDim.x, rem = total - per * gridDim.x, c = blockIdx.x;
     const int64_t lo = per * c + min(c, rem), hi = lo + per + (c < rem ? 1 : 0);
-    if (threadIdx.x == 0) { sh.lo = lo; sh.hi = hi; }
+    if (threadIdx.x == 0) { sh.lo = lo; sh.hi = hi; sh.per = per; sh.rem = rem; }
     const unsigned finder = __ballot_sync(0xffffffffu, lo < hi && at <= lo && lo < at + mine);
     if (finder) {
         int b = __shfl_sync(0xffffffffu, b0, __ffs(finder) - 1);
@@ -301,7 +410,7 @@ weights_q_kernel(const CwParams p) {
             const uint32_t l = cw_e4m3x2(__hmul2(__hsub2(v, cw_e4m3x2_half(h)), __float2half2_rn(16.f)));
             if (i & 1) { hi[i >> 1] |= h << 16; lo[i >> 1] |= l << 16; } else { hi[i >> 1] = h; lo[i >> 1] = l; }
         }
-        const int rows = (c1 - c0) * a.H, per = cw_chunk_rows(rows);
+        const int rows = (c1 - c0) * a.H, per = cw_chunk_rows(rows, p.resident);
         const int64_t g0 = int64_t(c0) * a.H;
         const int l = int((g - g0) % per), left = rows - (int(g - g0) - l), r = left < per ? left : per;
         // K block (8 lanes each), rows hi then rows lo, 16-byte pieces swizzled
@@ -355,14 +464,14 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
         fence_mbar_init();
     }
     if (warp == kCwMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
-    cw_locate(p, sh);
+    cw_locate(p, sh.at);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = sh.tbase;
+    const uint32_t tbase = uint32_t(cw_same(int(sh.tbase)));
     const int page_mask = (1 << c.page_shift) - 1;
     const int box_rows = page_mask + 1 < kCwTile ? page_mask + 1 : kCwTile;
-    CwWalk w(sh);
+    CwWalk w(sh.at);
 
     if (warp == kCwLoadWarp) {
         // ------------------------------------------------------- loads of the cache
@@ -572,30 +681,17 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
                     tc_fence_after();
                     const uint32_t trow = tbase + 256 * buf + (uint32_t(quarter * 32) << 16);
                     const bool all = (k + 1) * int64_t(kCwTile) <= least;
-                    const uint64_t scale2 = pair_of(scale, scale), sixteenth = pair_of(0.0625f, 0.0625f);
+                    const uint64_t scale2 = pair_of(scale, scale);
                     float sum = 0.f;
                     uint32_t hi[2][16], lo[2][16];
                     auto read = [&](int n, int b) {
                         tmem_ld16(trow + n, hi[b]);
                         tmem_ld16(trow + r + n, lo[b]);
                     };
-                    auto add = [&](int n, int b) {           // two columns at a time
-                        uint64_t part[2] = {0, 0};
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const ulonglong2 fx = *reinterpret_cast<const ulonglong2*>(fac + n + e);
-                            const ulonglong2 fy = *reinterpret_cast<const ulonglong2*>(fac + kCwRows + n + e);
-#pragma unroll
-                            for (int d = 0; d < 4; d += 2) {
-                                const uint64_t s = fma2(pair_of(lo[b][e + d], lo[b][e + d + 1]), sixteenth,
-                                                        pair_of(hi[b][e + d], hi[b][e + d + 1]));
-                                const float2 x = floats_of(fma2(mul2(s, scale2), d ? fx.y : fx.x, d ? fy.y : fy.x));
-                                part[d >> 1] = add2(part[d >> 1], pair_of(ex2_approx(x.x), ex2_approx(x.y)));
-                            }
-                        }
-                        const float2 both = floats_of(add2(part[0], part[1]));
+                    auto add = [&](int n, int b) {
+                        const float part = cw_sum16(hi[b], lo[b], scale2, fac + n, fac + kCwRows + n);
                         // (tokens have multiples of 16 rows)
-                        if (all || pos < cw_len(a, w.c0 + (j * w.chunk_rows + n) / a.H)) sum += both.x + both.y;
+                        if (all || pos < cw_len(a, w.c0 + (j * w.chunk_rows + n) / a.H)) sum += part;
                     };
                     read(0, 0);
 #pragma unroll 1
@@ -625,9 +721,327 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
     if (warp == kCwMmaWarp) tmem_dealloc(tbase, 512);
 }
 
+// The same with the cache resident, for sequences of many rows of q: passes of three tiles, which go from shared
+// memory to TMEM (as A operands, 128 columns each) and stay there while the sequence's q streams past in chunks of
+// 32 rows, one bulk copy each, four in flight. The units (three tiles, chunk) are dealt out one by one; a pass whose
+// chunks several CTAs have is joined by weights_join_kernel. Warps as above, and 11 for products too; the teams take the
+// products in turn (tiles within chunks), keep their sums of a pass in registers and join them at its end.
+__global__ void __launch_bounds__(kCwLThreads, 1)
+weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
+    extern __shared__ __align__(1024) uint8_t ring[];
+    CwLShared& sh = *reinterpret_cast<CwLShared*>(ring + kCwLSharedAt);
+    uint8_t* qbuf = ring + kCwLQAt;
+    float* factors = reinterpret_cast<float*>(ring + kCwLFactorAt);
+    const WeightsArgs& a = p.a;
+    const CacheView& c = a.cache;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* ab = &sh.abort_flag;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kCwLSlots; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 4); }
+        // a chunk's slot is free when its products are done and both teams are done with its factors
+        for (int i = 0; i < kCwLQSlots; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_empty[i], 10); }
+        mbar_init(&sh.x_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.t_full[i], 1);
+            mbar_init(&sh.t_empty[i], 4);
+            mbar_init(&sh.drain[i], 1);
+        }
+        sh.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kCwMmaWarp) { tmem_alloc(&sh.tbase, 512); tmem_relinquish(); }
+    cw_locate(p, sh.at);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = uint32_t(cw_same(int(sh.tbase)));
+    const int page_mask = (1 << c.page_shift) - 1;
+    const int box_rows = page_mask + 1 < kCwTile ? page_mask + 1 : kCwTile;
+    CwUnits w(sh.at);
+
+    if (warp == kCwLoadWarp) {
+        // ------------------------------------------------------- loads of the cache
+        uint32_t use = 0;
+        bool ok = true;
+        const int boxes = kCwTile / box_rows;
+        while (ok && w.next(p)) {
+            const int end = min((w.last() + 1) * kCwLTiles, w.tiles);
+            for (int k = w.first() * kCwLTiles; k < end && ok; ++k) {
+                const int64_t pos = int64_t(k) * kCwTile + lane * box_rows;
+                int row = -1;
+                if (lane < boxes && pos < w.seen) {
+                    const int page = __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift));
+                    if (page >= 0 && page < c.num_pages) row = (page << c.page_shift) + int(pos & page_mask);
+                }
+                const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
+#pragma unroll 1
+                for (int kb = 0; kb < 4; ++kb) {
+                    const int slot = int(use % kCwLSlots);
+                    ok = cw_wait(&sh.empty[slot], ((use / kCwLSlots) & 1u) ^ 1u, ab, a.status);
+                    if (!ok) break;
+                    ++use;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], uint32_t(live * box_rows) * 128);
+                    __syncwarp();
+                    if (row >= 0)
+                        tma_load_2d(ring + slot * kCwSlotBytes + lane * box_rows * 128, &map_box, kb * 128, row,
+                                    &sh.full[slot]);
+                    __syncwarp();
+                }
+            }
+        }
+        __syncwarp();
+        if (sh.abort_flag)                       // the loads already issued land before the CTA exits
+            for (uint32_t n = use > kCwLSlots ? use - kCwLSlots : 0; n < use; ++n)
+                mbar_wait(&sh.full[n % kCwLSlots], (n / kCwLSlots) & 1u, kCwWaitNs / 8);
+        __syncwarp();
+    } else if (warp == kCwQWarp) {
+        // ------------------------------------------------------- loads of q and its factors
+        uint32_t use = 0;
+        bool ok = true;
+        grid_dep_wait();                         // the splitting kernel is complete
+        if (blockIdx.x == 0) {
+            unsigned bits = 0;
+            for (int i = lane; i < p.blocks; i += 32) bits |= __ldcg(p.bits + i);
+            if (bits) atomicOr(a.status, bits);
+            __syncwarp();
+        }
+        while (ok && w.next(p)) {
+            const int last = w.last();
+            for (int k = w.first(); k <= last && ok; ++k) {
+                const int j1 = w.to(k);
+                for (int j = w.from(k); j < j1 && ok; ++j) {
+                    const int r = w.chunk_size(j), slot = int(use % kCwLQSlots);
+                    const int64_t g = (int64_t(w.c0) * a.H) + int64_t(j) * kCwLRows;
+                    ok = cw_wait(&sh.q_empty[slot], ((use / kCwLQSlots) & 1u) ^ 1u, ab, a.status);
+                    if (!ok) break;
+                    ++use;
+                    if (lane == 0) {
+                        float* f = factors + slot * 2 * kCwLRows;
+                        mbar_arrive_expect_tx(&sh.q_full[slot], uint32_t(r) * 1032);
+                        bulk_load(f, p.factor + g, uint32_t(r) * 4, &sh.q_full[slot]);
+                        bulk_load(f + kCwLRows, p.factor + int64_t(a.T) * a.H + g, uint32_t(r) * 4, &sh.q_full[slot]);
+                        bulk_load(qbuf + slot * kCwLQBytes, p.image + g * 1024, uint32_t(r) * 1024, &sh.q_full[slot]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        __syncwarp();
+        if (sh.abort_flag)                       // the loads already issued land before the CTA exits
+            for (uint32_t n = use > kCwLQSlots ? use - kCwLQSlots : 0; n < use; ++n)
+                mbar_wait(&sh.q_full[n % kCwLQSlots], (n / kCwLQSlots) & 1u, kCwWaitNs / 8);
+        __syncwarp();
+    } else if (warp == kCwMmaWarp || warp == kCwMmaWarp2) {
+        // ------------------------------------------------------------ products
+        // Two warps take them in turn, a buffer each: one's waits and its way to the next product (some 250 cycles,
+        // with the tensor core idle when there was one warp) pass while the other's are issued.
+        const uint64_t q_desc = sdesc_sw128(smem_u32(qbuf), 16, 1024);
+        const int buf = warp == kCwMmaWarp ? 0 : 1;
+        const bool leader = elect_one();
+        uint32_t use = 0, tile = 0, pass = 0;
+        bool ok = true;
+        while (ok && w.next(p)) {
+            const int last = w.last();
+            for (int k = w.first(); k <= last && ok; ++k, ++pass) {
+                const int n = w.width(k), j1 = w.to(k);
+                ok = cw_wait(&sh.x_full, pass & 1u, ab, a.status);
+                for (int j = w.from(k); j < j1 && ok; ++j) {
+                    const int r = w.chunk_size(j), slot = int(use % kCwLQSlots);
+                    const uint32_t idesc = idesc_f8(128, 2 * r, false, false);
+                    ok = cw_wait(&sh.q_full[slot], (use / kCwLQSlots) & 1u, ab, a.status);
+                    ++use;
+#pragma unroll 1
+                    for (int i = (int(tile) & 1) == buf ? 0 : 1; i < n && ok; i += 2) {
+                        const uint32_t at = tile + i;
+                        ok = cw_wait(&sh.t_empty[buf], ((at >> 1) & 1u) ^ 1u, ab, a.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            uint64_t qa = q_desc + uint32_t(slot) * (kCwLQBytes >> 4);
+                            uint32_t xa = tbase + 128 * i;
+#pragma unroll 1
+                            for (int kb = 0; kb < 4; ++kb) {
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    mma_f8_ts(tbase + kCwLColS + kCwLCols * buf, xa + 8 * d, qa + 2 * d, idesc, (kb | d) != 0);
+                                qa += uint32_t(r * 256) >> 4;
+                                xa += 32;
+                            }
+                            mma_commit(&sh.t_full[buf]);
+                            if (i + 2 >= n) mma_commit(&sh.q_empty[slot]);       // this warp's last of the chunk
+                        }
+                        __syncwarp();
+                    }
+                    // (a chunk of one product is the other warp's alone)
+                    if (leader && n == 1 && int(tile & 1) != buf) mbar_arrive(&sh.q_empty[slot]);
+                    tile += n;
+                    __syncwarp();
+                }
+            }
+        }
+        if (leader) {
+            mma_commit(&sh.drain[buf]);
+            mbar_wait(&sh.drain[buf], 0, kCwWaitNs);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------- the tiles into TMEM, and sums
+        const int team = warp >> 2, quarter = warp & 3;
+        const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
+        const int row_in = 32 * quarter + lane;  // this thread's position in a tile
+        const int64_t width = int64_t(a.max_pages) << c.page_shift;
+        const int blocks_of = a.H >> 4;          // blocks of 16 rows of a token
+        uint32_t x_use = 0, use = 0, tile = 0;
+        int4 joins = make_int4(-1, 0, 0, 0);
+        bool ok = true, bad = false;
+        while (ok && w.next(p)) {
+            const int64_t line = w.b * width;
+            const int last = w.last();
+            int least = INT32_MAX;               // positions that all of the sequence's tokens see
+            for (int t = w.c0 + lane; t < w.c1; t += 32) least = min(least, cw_len(a, t));
+            least = __reduce_min_sync(0xffffffffu, least);
+            for (int k = w.first(); k <= last && ok; ++k) {
+                const int tiles = w.width(k), j0 = w.from(k), j1 = w.to(k);
+                const int64_t pos0 = int64_t(k) * (kCwLTiles * kCwTile) + row_in;
+                float scale[kCwLTiles], sum[kCwLTiles];
+#pragma unroll
+                for (int i = 0; i < kCwLTiles; ++i) {
+                    const int64_t pos = pos0 + i * kCwTile;
+                    scale[i] = -1.f;             // (no row)
+                    sum[i] = 0.f;
+                    if (i >= tiles || pos >= w.seen) continue;
+                    const int page = __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift));
+                    if (page < 0 || page >= c.num_pages) bad = true;
+                    else scale[i] = __ldg(c.scales + (((page << c.page_shift) + int(pos & page_mask)) >> c.block_shift));
+                }
+                // the blocks of 128 columns in turn, a team every other one
+                for (int i = 0; i < 4 * tiles && ok; ++i, ++x_use) {
+                    if (int(x_use & 1) != team) continue;
+                    const int slot = int(x_use % kCwLSlots);
+                    ok = cw_wait(&sh.full[slot], (x_use / kCwLSlots) & 1u, ab, a.status);
+                    if (!ok) break;
+                    const uint8_t* from = ring + slot * kCwSlotBytes + row_in * 128;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(from + (((4 * h + d) ^ (lane & 7)) << 4));
+                            v[4 * d] = y.x; v[4 * d + 1] = y.y; v[4 * d + 2] = y.z; v[4 * d + 3] = y.w;
+                        }
+                        tmem_st16(trow + 128 * (i >> 2) + 32 * (i & 3) + 16 * h, v);
+                    }
+                    fence_proxy_async_smem();    // the slot's next load comes after these reads
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.x_full);
+                const bool clear = (int64_t(k) * kCwLTiles + tiles) * kCwTile <= least;
+                for (int j = j0; j < j1 && ok; ++j) {
+                    const int r = w.chunk_size(j), slot = int(use % kCwLQSlots);
+                    ++use;
+                    const float* fac = factors + slot * 2 * kCwLRows;
+                    ok = cw_wait(&sh.q_full[slot], ((use - 1) / kCwLQSlots) & 1u, ab, a.status);
+#pragma unroll
+                    for (int i = 0; i < kCwLTiles; ++i) {
+                        if (!ok || i >= tiles) continue;
+                        const int buf = tile & 1;
+                        const uint32_t turn = (tile++ >> 1) & 1u;
+                        if (buf != team) continue;
+                        ok = cw_wait(&sh.t_full[buf], turn, ab, a.status);
+                        if (!ok) continue;
+                        tc_fence_after();
+                        const uint32_t at = trow + kCwLColS + kCwLCols * buf;
+                        constexpr int kBlocks = kCwLRows / 16;
+                        uint32_t hi[kBlocks][16], lo[kBlocks][16];
+#pragma unroll
+                        for (int n = 0; n < kBlocks; ++n)
+                            if (16 * n < r) {
+                                tmem_ld16(at + 16 * n, hi[n]);
+                                tmem_ld16(at + r + 16 * n, lo[n]);
+                            }
+                        tmem_wait_ld();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.t_empty[buf]);
+                        const uint64_t scale2 = pair_of(scale[i], scale[i]);
+#pragma unroll
+                        for (int n = 0; n < kBlocks; ++n) {
+                            if (16 * n >= r) break;
+                            const float part = cw_sum16(hi[n], lo[n], scale2, fac + 16 * n, fac + kCwLRows + 16 * n);
+                            if (clear || pos0 + i * kCwTile < cw_len(a, w.c0 + (j * kBlocks + n) / blocks_of)) sum[i] += part;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.q_empty[slot]);
+                }
+                // The teams' sums together; behind the second barrier all of the pass's products are done and the
+                // tiles may go.
+                if (team == 1)
+#pragma unroll
+                    for (int i = 0; i < kCwLTiles; ++i) sh.sums[i][row_in] = sum[i];
+                // (if a wait ran out in one of these warps, all of them stop here)
+                uint32_t stop;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\t"
+                    "setp.ne.u32 p, %1, 0;\n\t"
+                    "barrier.cta.red.or.pred.aligned q, 1, 256, p;\n\t"
+                    "selp.u32 %0, 1, 0, q;\n\t}"
+                    : "=r"(stop)
+                    : "r"(uint32_t(!ok))
+                    : "memory");
+                ok = stop == 0;
+                if (team == 0)
+#pragma unroll
+                    for (int i = 0; i < kCwLTiles; ++i) {
+                        if (i >= tiles || !ok) continue;
+                        const int64_t pos = pos0 + i * kCwTile;
+                        const float both = scale[i] >= 0.f ? sum[i] + sh.sums[i][row_in] : 0.f;
+                        if (j0 > 0 || j1 < w.chunks) {
+                            p.parts[((2 * blockIdx.x + (j0 > 0 ? 0 : 1)) * kCwLTiles + i) * kCwTile + row_in] = both;
+                        } else if (pos < w.seen) {
+                            a.weights[line + pos] = a.decay != 0.f ? fmaf(a.decay, a.earlier[line + pos], both) : both;
+                        }
+                    }
+                if (j0 > 0 && j1 == w.chunks) joins = make_int4(w.b, k, cw_owner(sh.at, w.at + int64_t(k) * w.chunks), 0);
+                asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+                tc_fence_after();
+            }
+        }
+        if (threadIdx.x == 0) p.meta[blockIdx.x] = joins;
+        if (bad) flag_status(a.status, SMLA_ERR_INDEX);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kCwMmaWarp) tmem_dealloc(tbase, 512);
+}
+
+// The passes that several CTAs of the resident kernel have a part in, their parts in order: a block for each CTA and tile.
+__global__ void __launch_bounds__(kCwTile)
+weights_join_kernel(const CwParams p) {
+    grid_dep_wait();
+    const WeightsArgs& a = p.a;
+    const int4 pass = __ldcg(p.meta + blockIdx.x);
+    if (pass.x < 0) return;
+    const int row = blockIdx.y * kCwTile + threadIdx.x;
+    float sum = __ldcg(p.parts + (2 * pass.z + 1) * (kCwLTiles * kCwTile) + row);
+#pragma unroll 8
+    for (int i = pass.z + 1; i <= int(blockIdx.x); ++i) sum += __ldcg(p.parts + 2 * i * (kCwLTiles * kCwTile) + row);
+    int c0, c1;
+    cw_tokens(a, pass.x, c0, c1);
+    const int seen = cw_seen(a, c0, c1);
+    const int64_t pos = int64_t(pass.y) * (kCwLTiles * kCwTile) + row;
+    const int64_t at = pass.x * (int64_t(a.max_pages) << a.cache.page_shift) + pos;
+    if (pos < seen) a.weights[at] = a.decay != 0.f ? fmaf(a.decay, a.earlier[at], sum) : sum;
+}
+
 namespace {
 
-struct CwPlan { size_t image, factor, bits, bytes; };
+struct CwPlan { size_t image, factor, bits, parts, meta, bytes; };
 
 CwPlan plan_weights(int64_t T, int64_t H) {
     CwPlan x{};
@@ -636,6 +1050,8 @@ CwPlan plan_weights(int64_t T, int64_t H) {
     x.image = take(size_t(T) * H * 1024);
     x.factor = take(size_t(T) * H * sizeof(float2));
     x.bits = take(size_t(kCwMaxBlocks) * 4);
+    x.parts = take(size_t(kCwMaxCtas) * 2 * kCwLTiles * kCwTile * 4);
+    x.meta = take(size_t(kCwMaxCtas) * sizeof(int4));
     x.bytes = off;
     return x;
 }
@@ -649,7 +1065,9 @@ cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCwSmem);
+        cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCwSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(weights_resident_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCwLSmem);
         if (e != cudaSuccess) return e;
         attr_done[dev] = true;
     }
@@ -664,6 +1082,9 @@ cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s) {
     p.image = reinterpret_cast<uint8_t*>(a.scratch + plan.image);
     p.factor = reinterpret_cast<float*>(a.scratch + plan.factor);
     p.bits = reinterpret_cast<unsigned*>(a.scratch + plan.bits);
+    p.parts = reinterpret_cast<float*>(a.scratch + plan.parts);
+    p.meta = reinterpret_cast<int4*>(a.scratch + plan.meta);
+    p.resident = int64_t(a.T) * a.H > kCwManyRows * int64_t(a.B);
     const int64_t rows = int64_t(a.T) * a.H, most = rows > a.B ? rows : a.B;
     const int64_t blocks = (most + kCwSplitThreads / 32 - 1) / (kCwSplitThreads / 32);
     p.blocks = int(blocks < kCwMaxBlocks ? blocks : kCwMaxBlocks);
@@ -678,11 +1099,18 @@ cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, weights_q_kernel, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(sms);
-    cfg.blockDim = dim3(kCwThreads);
-    cfg.dynamicSmemBytes = kCwSmem;
+    cfg.gridDim = dim3(sms < kCwMaxCtas ? sms : kCwMaxCtas);
+    cfg.blockDim = dim3(p.resident ? kCwLThreads : kCwThreads);
+    cfg.dynamicSmemBytes = p.resident ? kCwLSmem : kCwSmem;
     note_launch(2);
-    return cudaLaunchKernelEx(&cfg, weights_kernel, mb, p);
+    if (!p.resident) return cudaLaunchKernelEx(&cfg, weights_kernel, mb, p);
+    e = cudaLaunchKernelEx(&cfg, weights_resident_kernel, mb, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim.y = kCwLTiles;
+    cfg.blockDim = dim3(kCwTile);
+    cfg.dynamicSmemBytes = 0;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, weights_join_kernel, p);
 }
 
 }  // namespace smla

@@ -99,6 +99,46 @@ def test_weights_of_several_tokens(H, counts, page, block):
     _watch(pool, table, counts, lens, H)
 
 
+@pytest.mark.parametrize("H,counts", [(16, [41, 0, 77, 33, 30]), (48, [31, 1, 0, 29, 40]), (64, [0, 60, 0, 0, 0]),
+                                      (112, [12, 2, 30, 9, 1]), (128, [9, 1, 40, 0, 5])])
+@pytest.mark.parametrize("page,block", [(16, 16), (64, 32), (256, 64)])
+def test_weights_of_many_tokens(H, counts, page, block):
+    pool = Pool(300, page, block, seed=H)
+    full = [300, 67, 1500, 129, 256]
+    table = pool.place(full)
+    pool.fill(table, full)
+    lens = [max(0, n - c + 1 + i) for n, c in zip(full, counts) for i in range(c)]
+    lens[3] = 0                                       # a padded slot
+    _watch(pool, table, counts, lens, H, decay=0.9)
+    _watch(pool, table, counts, lens, H, decay=0.0)
+
+
+def test_weights_of_many_tokens_with_a_missing_page():
+    from sparse_mla_attention_gb300 import SmlaError, _lib
+    smla = _smla()
+    rng = np.random.default_rng(90)
+    pool = Pool(100, 16, 16, seed=91)
+    table = pool.place([900, 40])
+    pool.fill(table, [900, 40])
+    lens, cu = [900 - 39 + i for i in range(40)] + [40], [0, 40, 41]
+    q = bf16(rng.standard_normal((41, 64, 512)))
+    lse = _lse(q, pool, table, cu, lens)
+    bad = table.astype(np.int64).copy()
+    bad[0, [0, 30]] = 100, -1
+    W = table.shape[1] * 16
+    earlier = rng.exponential(size=(2, W)).astype(np.float32)
+    out = _f32(np.full((2, W), 7.0))
+    with pytest.raises(SmlaError) as e:
+        smla.cache_weights(bf16_dev(q), pool.device(), _i32(bad), _i32(lens), _f32(lse), out, cu_tokens=_i32(cu),
+                           earlier=_f32(earlier), decay=0.5)
+    assert e.value.code == _lib.SMLA_ERR_INDEX
+    ref, bound = M.weights(q, pool.codes, pool.scales, table, cu, lens, lse, earlier, 0.5,
+                           np.full((2, W), 7.0, dtype=np.float32), 16, 16)
+    for p in (0, 480):                                # (halving is exact)
+        ref[0, p:p + 16], bound[0, p:p + 16] = 0.5 * earlier[0, p:p + 16], 0.0
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+
+
 def test_weights_of_a_long_sequence_and_many_short_ones():
     lens = [20000] + list(range(1, 120))
     pool = Pool(1200, 64, 64, seed=4)
@@ -773,3 +813,14 @@ def test_select_of_more_candidates_than_one_batch():
     x = torch.sort(torch.randn(6, 200000, device=DEV), dim=1)[0]
     _select_and_check(x, rng.standard_normal((2, 3)), 64)
     _select_and_check(x.flip(1).half(), rng.standard_normal((2, 3)), 17)
+
+
+@pytest.mark.parametrize("H,tokens,n", [(128, 300, 300), (16, 700, 130), (48, 211, 5), (64, 150, 2000)])
+def test_weights_of_whole_prompts(H, tokens, n):
+    # few tiles and many tokens: every processor has a part of a tile
+    pool = Pool(100, 32, 32, seed=H)
+    table = pool.place([n, 20])
+    pool.fill(table, [n, 20])
+    lens = [min(n, i + 1) for i in range(tokens)] + [20]
+    lse = np.full((tokens + 1, H), 4.0, dtype=np.float32)
+    _watch(pool, table, [tokens, 1], lens, H, decay=0.5, lse=lse)

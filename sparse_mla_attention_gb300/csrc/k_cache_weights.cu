@@ -113,7 +113,7 @@ static_assert(kCwSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 struct CwParams {
     WeightsArgs a;
     uint8_t* image;                              // [T * H] rows of q as shared memory has them, 1 KB each
-    float* factor;                               // [2][T * H] score factor, -lse in log2 units
+    float* factor;                               // [3][T * H] of a row: score factor, -lse in log2 units, lens (int bits)
     unsigned* bits;                              // status bits of each block of the splitting kernel
     int blocks;
     int resident;                                // which of the two kernels follows the splitting one
@@ -135,7 +135,7 @@ struct CwLShared {
 };
 constexpr int kCwLQAt = kCwLSlots * kCwSlotBytes;
 constexpr int kCwLFactorAt = kCwLQAt + kCwLQSlots * kCwLQBytes;
-constexpr int kCwLSharedAt = kCwLFactorAt + kCwLQSlots * 2 * kCwLRows * 4;
+constexpr int kCwLSharedAt = kCwLFactorAt + kCwLQSlots * 3 * kCwLRows * 4;
 constexpr int kCwLSmem = kCwLSharedAt + int(sizeof(CwLShared));
 static_assert(kCwLSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 
@@ -350,10 +350,11 @@ __device__ void cw_locate(const CwParams& p, CwPlace& sh) {
     if (finder) {
         int b = __shfl_sync(0xffffffffu, b0, __ffs(finder) - 1);
         at = __shfl_sync(0xffffffffu, at, __ffs(finder) - 1);
-        for (int64_t n = cw_units(p, b); lo >= at + n; n = cw_units(p, b)) {
-            at += n;
-            ++b;
-        }
+        if (run > 1)
+            for (int64_t n = cw_units(p, b); lo >= at + n; n = cw_units(p, b)) {
+                at += n;
+                ++b;
+            }
         if (lane == 0) { sh.b0 = b; sh.at0 = at; }
     }
 }
@@ -422,6 +423,7 @@ weights_q_kernel(const CwParams p) {
             p.factor[g] = odd && !blind ? __int_as_float(0x7fffffff)
                                         : fminf(__int_as_float((127 + e) << 23) * a.scale * kCwLog2e, FLT_MAX);
             p.factor[int64_t(a.T) * a.H + g] = blind ? -INFINITY : -lse * kCwLog2e;
+            p.factor[2 * int64_t(a.T) * a.H + g] = __int_as_float(cw_len(a, t));
         }
     }
     for (int64_t b = first; b < a.B; b += warps) {
@@ -657,6 +659,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
                 if (!ok) break;
                 ++f_uses;
                 const float* fac = factors + 2 * f * kCwRows;
+                const float* seen = p.factor + (2 * int64_t(a.T) + w.c0) * a.H + int64_t(j) * w.chunk_rows;
                 // what the sum is added to: the chunks before, or the caller's
                 const float* base = j > 0 ? a.weights : a.earlier;
                 const float keep = j > 0 ? 1.f : a.decay;
@@ -691,7 +694,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
                     auto add = [&](int n, int b) {
                         const float part = cw_sum16(hi[b], lo[b], scale2, fac + n, fac + kCwRows + n);
                         // (tokens have multiples of 16 rows)
-                        if (all || pos < cw_len(a, w.c0 + (j * w.chunk_rows + n) / a.H)) sum += part;
+                        if (all || pos < __float_as_int(__ldcg(seen + n))) sum += part;
                     };
                     read(0, 0);
 #pragma unroll 1
@@ -816,10 +819,10 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
                     if (!ok) break;
                     ++use;
                     if (lane == 0) {
-                        float* f = factors + slot * 2 * kCwLRows;
-                        mbar_arrive_expect_tx(&sh.q_full[slot], uint32_t(r) * 1032);
-                        bulk_load(f, p.factor + g, uint32_t(r) * 4, &sh.q_full[slot]);
-                        bulk_load(f + kCwLRows, p.factor + int64_t(a.T) * a.H + g, uint32_t(r) * 4, &sh.q_full[slot]);
+                        mbar_arrive_expect_tx(&sh.q_full[slot], uint32_t(r) * 1036);
+                        for (int i = 0; i < 3; ++i)
+                            bulk_load(factors + (3 * slot + i) * kCwLRows, p.factor + i * int64_t(a.T) * a.H + g,
+                                      uint32_t(r) * 4, &sh.q_full[slot]);
                         bulk_load(qbuf + slot * kCwLQBytes, p.image + g * 1024, uint32_t(r) * 1024, &sh.q_full[slot]);
                     }
                     __syncwarp();
@@ -890,16 +893,12 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
         const int row_in = 32 * quarter + lane;  // this thread's position in a tile
         const int64_t width = int64_t(a.max_pages) << c.page_shift;
-        const int blocks_of = a.H >> 4;          // blocks of 16 rows of a token
         uint32_t x_use = 0, use = 0, tile = 0;
         int4 joins = make_int4(-1, 0, 0, 0);
         bool ok = true, bad = false;
         while (ok && w.next(p)) {
             const int64_t line = w.b * width;
             const int last = w.last();
-            int least = INT32_MAX;               // positions that all of the sequence's tokens see
-            for (int t = w.c0 + lane; t < w.c1; t += 32) least = min(least, cw_len(a, t));
-            least = __reduce_min_sync(0xffffffffu, least);
             for (int k = w.first(); k <= last && ok; ++k) {
                 const int tiles = w.width(k), j0 = w.from(k), j1 = w.to(k);
                 const int64_t pos0 = int64_t(k) * (kCwLTiles * kCwTile) + row_in;
@@ -939,11 +938,10 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.x_full);
-                const bool clear = (int64_t(k) * kCwLTiles + tiles) * kCwTile <= least;
                 for (int j = j0; j < j1 && ok; ++j) {
                     const int r = w.chunk_size(j), slot = int(use % kCwLQSlots);
                     ++use;
-                    const float* fac = factors + slot * 2 * kCwLRows;
+                    const float* fac = factors + slot * 3 * kCwLRows;
                     ok = cw_wait(&sh.q_full[slot], ((use - 1) / kCwLQSlots) & 1u, ab, a.status);
 #pragma unroll
                     for (int i = 0; i < kCwLTiles; ++i) {
@@ -972,7 +970,8 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
                         for (int n = 0; n < kBlocks; ++n) {
                             if (16 * n >= r) break;
                             const float part = cw_sum16(hi[n], lo[n], scale2, fac + 16 * n, fac + kCwLRows + 16 * n);
-                            if (clear || pos0 + i * kCwTile < cw_len(a, w.c0 + (j * kBlocks + n) / blocks_of)) sum[i] += part;
+                            // (tokens have multiples of 16 rows)
+                            if (pos0 + i * kCwTile < __float_as_int(fac[2 * kCwLRows + 16 * n])) sum[i] += part;
                         }
                     }
                     __syncwarp();
@@ -1048,7 +1047,7 @@ CwPlan plan_weights(int64_t T, int64_t H) {
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes > 0 ? bytes : 1, 256); return o; };
     x.image = take(size_t(T) * H * 1024);
-    x.factor = take(size_t(T) * H * sizeof(float2));
+    x.factor = take(size_t(T) * H * 3 * sizeof(float));
     x.bits = take(size_t(kCwMaxBlocks) * 4);
     x.parts = take(size_t(kCwMaxCtas) * 2 * kCwLTiles * kCwTile * 4);
     x.meta = take(size_t(kCwMaxCtas) * sizeof(int4));

@@ -30,6 +30,14 @@ __device__ __forceinline__ uint32_t recode2(uint32_t v, float ratio) {
 __device__ __forceinline__ uint32_t recode4(uint32_t v, float ratio) {
     return recode2(v, ratio) | recode2(v >> 16, ratio) << 16;
 }
+// The same where ratio is a power of two, in half precision: a code times 2^-14 or more is exact there, and what is
+// less than 2^-10 (all codes times 2^-19) becomes 0 whatever its last bits.
+__device__ __forceinline__ uint32_t shift4(uint32_t v, __half2 ratio) {
+    const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v & 0xffffu), __NV_E4M3));
+    const __half2 hi = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v >> 16), __NV_E4M3));
+    return uint32_t(__nv_cvt_halfraw2_to_fp8x2(__half2_raw(__hmul2(lo, ratio)), __NV_SATFINITE, __NV_E4M3)) |
+           uint32_t(__nv_cvt_halfraw2_to_fp8x2(__half2_raw(__hmul2(hi, ratio)), __NV_SATFINITE, __NV_E4M3)) << 16;
+}
 
 // A weight's bits in an order of unsigned numbers; both zeros alike, NaN below all.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -56,7 +64,9 @@ struct ChooseShared {
         uint16_t stays[kTile];                   // positions of a tile that stay, in order
     };
     int digit, over, inside;                     // the bin of the rest-th largest, what lies above it and in it
-    int n_few, rest;
+    int n_few, n_all, rest;
+    uint32_t all_few[kFew];                      // the cluster's, in its first CTA
+    int warp[2][kPlanWarps];
     uint32_t prefix;
     int above, ties;                             // of this CTA's part, read by the others
 };
@@ -96,7 +106,7 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
     if (one_tile) load(s0);
     uint32_t prefix = 0;
     if (by_weight) {                             // (the same in every CTA of the sequence)
-        if (part == 0 && threadIdx.x == 0) ch.n_few = 0;
+        if (threadIdx.x == 0) ch.n_few = ch.n_all = 0;
         if (kParts > 1) {
             if (part == 0)
                 for (int i = threadIdx.x; i < 3 * kDigits; i += kPlanThreads) (&ch.all[0][0])[i] = 0;
@@ -151,47 +161,49 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
                 if (runs == 0) continue;
 #pragma unroll
                 for (int e = 0; e < kRun; ++e)
-                    if (((runs >> e) & 1) && (key[e] & bin) == prefix) lead->few[atomicAdd(&lead->n_few, 1)] = key[e];
+                    if (((runs >> e) & 1) && (key[e] & bin) == prefix) ch.few[atomicAdd(&ch.n_few, 1)] = key[e];
+            }
+            if (kParts > 1) {                    // from each CTA to the first in one piece
+                __syncthreads();
+                if (threadIdx.x == 0) ch.digit = atomicAdd(&lead->n_all, ch.n_few);
+                __syncthreads();
+                for (int i = threadIdx.x; i < ch.n_few; i += kPlanThreads) lead->all_few[ch.digit + i] = ch.few[i];
             }
             sync_all();
             if (part == 0) {
-                const int n = ch.n_few;
+                const int n = kParts > 1 ? ch.n_all : ch.n_few;
+                const uint32_t* few = kParts > 1 ? ch.all_few : ch.few;
                 uint32_t mine[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = int(threadIdx.x) + kPlanThreads * k;
-                    mine[k] = i < n ? ch.few[i] : 0u;                    // (below every bound)
+                    mine[k] = i < n ? few[i] : 0u;                       // (below every bound)
                 }
-                // at least `rest` reach lo, fewer hi
-                uint32_t lo = prefix, hi = prefix | ~bin;
-                const bool last = [&] {          // (the bin's last value, so that hi + 1 need not exist)
-                    int r = __syncthreads_count(n > 0 && mine[0] == hi);
-                    for (int k = 1; k < 4 && kPlanThreads * k < n; ++k)
-                        r += __syncthreads_count(k == 1 ? mine[1] == hi : k == 2 ? mine[2] == hi : mine[3] == hi);
-                    if (r < rest) return false;
-                    return true;
-                }();
+                int set = 0;                     // of the warps' counts: two in turn, a barrier a count
+                auto reach = [&](uint32_t bound) {
+                    int c = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) c += int(mine[k] >= bound);
+                    c = __reduce_add_sync(0xffffffffu, c);
+                    if ((threadIdx.x & 31) == 0) ch.warp[set][threadIdx.x >> 5] = c;
+                    __syncthreads();
+                    c = __reduce_add_sync(0xffffffffu, ch.warp[set][threadIdx.x & 31]);
+                    set ^= 1;
+                    return c;
+                };
+                // at least `rest` reach lo, fewer hi (2^32 if the bin is the last: what passes all)
+                uint64_t lo = prefix, hi = (uint64_t(prefix) | ~bin) + 1;
                 int over = 0;
                 bool exact = false;
-                if (last) lo = hi;
-                while (!last && hi - lo > 1) {
-                    const uint32_t mid = lo + (hi - lo) / 2;
-                    int r = __syncthreads_count(mine[0] >= mid);
-                    if (n > kPlanThreads) {
-                        r += __syncthreads_count(mine[1] >= mid);
-                        if (n > 2 * kPlanThreads) r += __syncthreads_count(mine[2] >= mid) + __syncthreads_count(mine[3] >= mid);
-                    }
+                while (hi - lo > 1) {
+                    const uint64_t mid = lo + (hi - lo) / 2;
+                    const int r = reach(uint32_t(mid));
                     if (r == rest) { lo = mid; exact = true; break; }    // these and no others
                     if (r > rest) lo = mid; else hi = mid;
                 }
-                if (!last && !exact) {           // those above lo
-                    over = __syncthreads_count(mine[0] > lo);
-                    if (n > kPlanThreads)
-                        over += __syncthreads_count(mine[1] > lo) + __syncthreads_count(mine[2] > lo) +
-                                __syncthreads_count(mine[3] > lo);
-                }
+                if (!exact && hi <= (uint64_t(prefix) | ~bin)) over = reach(uint32_t(hi));       // those above lo
                 if (threadIdx.x == 0) {
-                    ch.prefix = exact ? lo - 1 : lo;
+                    ch.prefix = uint32_t(exact ? lo - 1 : lo);
                     ch.rest = exact ? 0 : rest - over;
                 }
             }
@@ -290,19 +302,15 @@ evict_copy_kernel(const EvictArgs a) {
     const int block = 1 << c.block_shift, page_mask = (1 << c.page_shift) - 1;
     const int64_t per = (int64_t(a.keep) + 15) >> 4;
     bool bad = false;
-    // A unit: up to 16 rows of a sequence, from r0 on. Where they lie and their scales, the block's, the place they go to.
-    struct Unit { int rows, lane0, from; float scale, size; int64_t to; };
-    auto look = [&](int64_t u) {
-        Unit x{0, 0, -1, 0.f, 0.f, -1};
-        if (u >= a.B * per) return x;
+    for (int64_t u = first >> 5; u < a.B * per; u += threads >> 5) {
         const int b = int(u / per);
         const int64_t r0 = (u - b * per) << 4;
         const int len = row_len(a, b), n = len < a.keep ? len : a.keep;
-        x.rows = int(max(min(n - r0, int64_t(16)), int64_t(0)));
+        const int rows = int(min(n - r0, int64_t(16)));
         int32_t* kept = a.kept + int64_t(b) * a.keep;
-        if (lane < 16 && lane >= x.rows && r0 + lane < a.keep) kept[r0 + lane] = -1;
-        if (x.rows == 0) return x;
-        // the rows of the block, up to two a lane
+        if (lane < 16 && lane >= rows && r0 + lane < a.keep) kept[r0 + lane] = -1;
+        if (rows <= 0) continue;
+        // the rows of the block, up to two a lane: where they lie (-1: no page) and their scales
         const int64_t block0 = r0 & ~int64_t(block - 1);
         const int32_t* table = a.table + int64_t(b) * a.max_pages;
         int p[2], from[2] = {-1, -1};
@@ -312,55 +320,52 @@ evict_copy_kernel(const EvictArgs a) {
             const int r = lane + 32 * k;
             p[k] = r < block && block0 + r < n ? __ldcg(kept + block0 + r) : -1;
         }
-        const int page = ok ? __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift)) : 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (p[k] >= 0) {
-                const int old = __ldg(table + (p[k] >> c.page_shift));
-                if (old >= 0 && old < c.num_pages) from[k] = (old << c.page_shift) + (p[k] & page_mask);
+                const int page = __ldg(table + (p[k] >> c.page_shift));
+                if (page >= 0 && page < c.num_pages) from[k] = (page << c.page_shift) + (p[k] & page_mask);
                 else bad = true;
             }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (from[k] >= 0) scale[k] = __ldg(c.scales + (from[k] >> c.block_shift));
         // this warp's 16 of them
-        const int half = int(r0 - block0) >> 5;
-        x.lane0 = int(r0 - block0) & 31;
-        x.from = half ? from[1] : from[0];
-        x.scale = half ? scale[1] : scale[0];
-        if (lane >= x.lane0 && lane < x.lane0 + x.rows)
-            a.new_weights[b * width + r0 + lane - x.lane0] = __ldg(a.weights + b * width + (half ? p[1] : p[0]));
-        x.size = fmaxf(scale[0], scale[1]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) x.size = fmaxf(x.size, __shfl_xor_sync(0xffffffffu, x.size, d));
-        x.to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
-        if (ok && r0 == block0 && lane == 0) c.scales[x.to >> c.block_shift] = x.size;
-        return x;
-    };
-    const int64_t step = threads >> 5;
-    Unit at = look(first >> 5);
-    for (int64_t u = first >> 5; u < a.B * per; u += step) {
+        const int half = int(r0 - block0) >> 5, lane0 = int(r0 - block0) & 31;
+        const int mine = half ? from[1] : from[0];
+        const float own = half ? scale[1] : scale[0];
+        if (lane >= lane0 && lane < lane0 + rows)
+            a.new_weights[b * width + r0 + lane - lane0] = __ldg(a.weights + b * width + (half ? p[1] : p[0]));
+        if (!ok) continue;
         uint4 v[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int row = __shfl_sync(0xffffffffu, at.from, at.lane0 + r);
-            v[r] = ok && row >= 0 && r < at.rows ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane)
-                                                 : make_uint4(0, 0, 0, 0);
+            const int row = __shfl_sync(0xffffffffu, mine, lane0 + r);
+            v[r] = row >= 0 && r < rows ? __ldcg(reinterpret_cast<const uint4*>(c.pages + int64_t(row) * kD) + lane)
+                                        : make_uint4(0, 0, 0, 0);
         }
-        const Unit then = look(u + step);        // while these are on their way
-        if (ok)
+        float size = fmaxf(scale[0], scale[1]);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float was = __shfl_sync(0xffffffffu, at.scale, at.lane0 + r);
-                if (r >= at.rows) break;
-                uint4 x = v[r];
-                if (was != at.size) {
-                    const float ratio = was / at.size;
+        for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
+        const int page = __ldcg(a.fresh + __ldcg(a.start + b) + (r0 >> c.page_shift));
+        const int64_t to = (int64_t(page) << c.page_shift) + (r0 & page_mask);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float was = __shfl_sync(0xffffffffu, own, lane0 + r);
+            if (r >= rows) break;
+            uint4 x = v[r];
+            if (was != size) {
+                const float ratio = was / size;
+                if ((__float_as_uint(ratio) & 0x807fffffu) == 0) {
+                    const __half2 h = __float2half2_rn(ratio);
+                    x = make_uint4(shift4(x.x, h), shift4(x.y, h), shift4(x.z, h), shift4(x.w, h));
+                } else {
                     x = make_uint4(recode4(x.x, ratio), recode4(x.y, ratio), recode4(x.z, ratio), recode4(x.w, ratio));
                 }
-                *(reinterpret_cast<uint4*>(c.pages + (at.to + r) * kD) + lane) = x;
             }
-        at = then;
+            *(reinterpret_cast<uint4*>(c.pages + (to + r) * kD) + lane) = x;
+        }
+        if (r0 == block0 && lane == 0) c.scales[to >> c.block_shift] = size;
     }
     if (bad) flag_status(a.status, SMLA_ERR_INDEX);
     // tables, lengths, and zeros behind the weights

@@ -32,13 +32,13 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     _need(scores, "scores", torch.float32, 2)
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _TYPES:
         raise TypeError("logits must be a float32, bfloat16 or float16 tensor")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be [B*K, V] with a row's values side by side")
     B, K = scores.shape
     rows, V = logits.shape
-    index = scores.get_device()
+    index, device = scores.get_device(), scores.device
     if logits.get_device() != index:
-        raise ValueError(f"logits must be on {scores.device}, got {logits.device}")
+        raise ValueError(f"logits must be on {device}, got {logits.device}")
     if rows != B * K or K < 1 or V < 1:
         raise ValueError("logits must have a row for each beam")
     n = K if n is None else int(n)
@@ -51,21 +51,21 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
             raise ValueError("done needs eos in [0, V)")
         p_done = done.data_ptr()
     size = _size_of(_sizes, (B, K, V, n), "smla_beam_workspace_size", B, K, V, n)
-    if out is None:
-        out = (torch.empty((B, n), dtype=torch.int32, device=scores.device),
-               torch.empty((B, n), dtype=torch.int32, device=scores.device),
-               torch.empty((B, n), dtype=torch.float32, device=scores.device))
-    parents, tokens, best = out
-    for name, t, dtype in (("parents", parents, torch.int32), ("tokens", tokens, torch.int32),
-                           ("scores", best, torch.float32)):
-        _need(t, f"out {name}", dtype, 2)
-        if tuple(t.shape) != (B, n) or t.get_device() != index:
-            raise ValueError("out must be (parents, tokens, scores), each [B, n], on the device of scores")
-    ws = (workspace or Workspace(scores.device)).get(size)
+    ws = (workspace or Workspace(device)).get(size)
     if ws.get_device() != index:
-        raise ValueError(f"workspace must be on {scores.device}, got {ws.device}")
-    args = (logits.data_ptr(), _TYPES[logits.dtype], logits.stride(0) if rows > 1 else V, scores.data_ptr(), p_done,
-            int(eos), parents.data_ptr(), tokens.data_ptr(), best.data_ptr(), B, K, V, n, ws.data_ptr(), ws.numel(),
+        raise ValueError(f"workspace must be on {device}, got {ws.device}")
+    if out is None:
+        out = (torch.empty((B, n), dtype=torch.int32, device=device),
+               torch.empty((B, n), dtype=torch.int32, device=device),
+               torch.empty((B, n), dtype=torch.float32, device=device))
+    else:
+        for t, dtype in zip(out, (torch.int32, torch.int32, torch.float32)):
+            _need(t, "out", dtype, 2)
+            if t.shape != (B, n) or t.get_device() != index:
+                raise ValueError("out must be (parents, tokens, scores), each [B, n], on the device of scores")
+    parents, tokens, best = out
+    args = (logits.data_ptr(), _TYPES[logits.dtype], logits.stride(0) if rows > 1 else V, scores.data_ptr(), p_done, eos,
+            parents.data_ptr(), tokens.data_ptr(), best.data_ptr(), B, K, V, n, ws.data_ptr(), ws.numel(),
             _raw_stream(index))
     fn = _lib.load().smla_beam_select
     if _current_device() == index:
@@ -73,5 +73,6 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     else:
         with torch.cuda.device(index):
             code = fn(*args)
-    _lib.check(code, "smla_beam_select")
+    if code != _lib.SMLA_OK:
+        raise _lib.SmlaError(code, "smla_beam_select")
     return parents, tokens, best

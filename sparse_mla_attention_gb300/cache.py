@@ -106,6 +106,22 @@ def _on_device(cache: PagedCache, workspace: Optional[Workspace], size: int) -> 
     return ws
 
 
+def _check2(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, n: int, m: int) -> int:
+    """_check of a tensor of n x m."""
+    p = _check(cache, t, name, dtype, 2)
+    if t.shape != (n, m):
+        raise ValueError(f"{name} must have shape [{n}, {m}], got {tuple(t.shape)}")
+    return p
+
+
+def _check1(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> int:
+    """_check of a vector of n."""
+    p = _check(cache, t, name, dtype, 1)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
+    return p
+
+
 def _size_of(sizes: dict, key, where: str, *args) -> int:
     """What the library's size query `where` says, asked once for each key."""
     size = sizes.get(key)
@@ -318,31 +334,23 @@ def cache_weights(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens:
     """
     p_q = _check(cache, q, "q", torch.bfloat16, 3)
     p_table = _check(cache, table, "table", torch.int32, 2)
-    p_lens = _check(cache, lens, "lens", torch.int32, 1)
-    p_lse = _check(cache, lse, "lse", torch.float32, 2)
-    p_weights = _check(cache, weights, "weights", torch.float32, 2)
     T, H, D = q.shape
     B, max_pages = table.shape
     width = max_pages * cache.page_size
-    if lens.shape[0] != T or tuple(lse.shape) != (T, H):
-        raise ValueError("lens must have shape [T] and lse [T, H]")
-    if tuple(weights.shape) != (B, width):
-        raise ValueError("weights must have shape [B, max_pages * page_size]")
+    p_lens = _check1(cache, lens, "lens", torch.int32, T)
+    p_lse = _check2(cache, lse, "lse", torch.float32, T, H)
+    p_weights = _check2(cache, weights, "weights", torch.float32, B, width)
     p_cu, p_earlier = None, p_weights
     if cu_tokens is not None:
-        p_cu = _check(cache, cu_tokens, "cu_tokens", torch.int32, 1)
-        if cu_tokens.shape[0] != B + 1:
-            raise ValueError("cu_tokens must have shape [B+1]")
+        p_cu = _check1(cache, cu_tokens, "cu_tokens", torch.int32, B + 1)
     elif T > B:
         raise ValueError("without cu_tokens, table must have a row for each token")
     if earlier is not None:
-        p_earlier = _check(cache, earlier, "earlier", torch.float32, 2)
-        if earlier.shape != weights.shape:
-            raise ValueError("earlier must have the shape of weights")
+        p_earlier = _check2(cache, earlier, "earlier", torch.float32, B, width)
     dims = SmlaPagedDims(T, H, D, 0, B, max_pages, 0.0 if scale is None else float(scale))
     ws = _on_device(cache, workspace, _size_of(_weights_sizes, (T, H), "smla_weights_workspace_size", dims))
     _run(cache, "smla_cache_weights", ws, check_status, p_q, cache._ref, p_table, p_cu, p_lens, p_lse, p_earlier,
-         float(decay), p_weights, ctypes.byref(dims))
+         decay, p_weights, ctypes.byref(dims))
     return weights
 
 
@@ -358,30 +366,25 @@ def cache_evict(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, weig
     their pages back. All or nothing where free pages are short. ``out`` takes the four results.
     """
     p_table = _check(cache, table, "table", torch.int32, 2)
-    p_lens = _check(cache, lens, "lens", torch.int32, 1)
-    p_weights = _check(cache, weights, "weights", torch.float32, 2)
     B, max_pages = table.shape
-    if lens.shape[0] != B:
-        raise ValueError("lens must have shape [B]")
-    if tuple(weights.shape) != (B, max_pages * cache.page_size):
-        raise ValueError("weights must have shape [B, max_pages * page_size]")
+    width = max_pages * cache.page_size
+    p_lens = _check1(cache, lens, "lens", torch.int32, B)
+    p_weights = _check2(cache, weights, "weights", torch.float32, B, width)
     keep, first, recent = int(keep), int(first), int(recent)
-    if not 1 <= keep <= max_pages * cache.page_size or first < 0 or recent < 0 or first + recent > keep:
+    if not 1 <= keep <= width or first < 0 or recent < 0 or first + recent > keep:
         raise ValueError("1 <= keep <= max_pages * page_size and first + recent <= keep are needed")
     if out is None:
         out = (torch.empty_like(table), torch.empty_like(lens), torch.empty_like(weights),
                torch.empty((B, keep), dtype=torch.int32, device=cache.device))
     new_table, new_lens, new_weights, kept = out
-    p_out = (_check(cache, new_table, "new_table", torch.int32, 2), _check(cache, new_lens, "new_lens", torch.int32, 1),
-             _check(cache, new_weights, "new_weights", torch.float32, 2), _check(cache, kept, "kept", torch.int32, 2))
-    if (new_table.shape != table.shape or new_lens.shape != lens.shape or new_weights.shape != weights.shape
-            or tuple(kept.shape) != (B, keep)):
-        raise ValueError("out must be (new_table like table, new_lens like lens, new_weights like weights, "
-                         "kept [B, keep])")
+    p_new = _check2(cache, new_table, "new_table", torch.int32, B, max_pages)
+    p_len = _check1(cache, new_lens, "new_lens", torch.int32, B)
+    p_moved = _check2(cache, new_weights, "new_weights", torch.float32, B, width)
+    p_kept = _check2(cache, kept, "kept", torch.int32, B, keep)
     size = _size_of(cache._sizes, ("evict", B, keep), "smla_cache_evict_workspace_size", cache._ref, B, keep)
     _run(cache, "smla_cache_evict", _on_device(cache, workspace, size), check_status, cache._ref, p_table, p_lens,
-         p_weights, *p_out, B, max_pages, keep, first, recent)
-    return new_table, new_lens, new_weights, kept
+         p_weights, p_new, p_len, p_moved, p_kept, B, max_pages, keep, first, recent)
+    return out
 
 
 def cache_reorder(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
@@ -397,30 +400,23 @@ def cache_reorder(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, pa
     short of pages (all or nothing). With ``weights`` [B, max_pages * page_size] the accumulated weights go along.
     """
     p_table = _check(cache, table, "table", torch.int32, 2)
-    p_lens = _check(cache, lens, "lens", torch.int32, 1)
     p_parents = _check(cache, parents, "parents", torch.int32, 1)
     B, max_pages = table.shape
-    n, width = parents.shape[0], max_pages * cache.page_size
-    if lens.shape[0] != B:
-        raise ValueError("lens must have shape [B]")
-    p_weights = p_moved = None
-    if weights is not None:
-        p_weights = _check(cache, weights, "weights", torch.float32, 2)
-        if tuple(weights.shape) != (B, width):
-            raise ValueError("weights must have shape [B, max_pages * page_size]")
+    n = parents.shape[0]
+    p_lens = _check1(cache, lens, "lens", torch.int32, B)
     if out is None:
         out = (table.new_empty((n, max_pages)), lens.new_empty(n),
-               None if weights is None else weights.new_empty((n, width)))
+               None if weights is None else weights.new_empty((n, max_pages * cache.page_size)))
     new_table, new_lens, new_weights = out
-    p_new = _check(cache, new_table, "new_table", torch.int32, 2)
-    p_len = _check(cache, new_lens, "new_lens", torch.int32, 1)
-    if tuple(new_table.shape) != (n, max_pages) or new_lens.shape[0] != n or (new_weights is None) != (weights is None):
-        raise ValueError("out must be (new_table [n,max_pages], new_lens [n], new_weights with weights, else None)")
+    p_new = _check2(cache, new_table, "new_table", torch.int32, n, max_pages)
+    p_len = _check1(cache, new_lens, "new_lens", torch.int32, n)
+    p_weights = p_moved = None
     if weights is not None:
-        p_moved = _check(cache, new_weights, "new_weights", torch.float32, 2)
-        if tuple(new_weights.shape) != (n, width):
-            raise ValueError("new_weights must have shape [n, max_pages * page_size]")
+        p_weights = _check2(cache, weights, "weights", torch.float32, B, max_pages * cache.page_size)
+        p_moved = _check2(cache, new_weights, "new_weights", torch.float32, n, max_pages * cache.page_size)
+    elif new_weights is not None:
+        raise ValueError("out must have None for the weights where none are given")
     size = _size_of(_reorder_sizes, (B, n), "smla_cache_reorder_workspace_size", B, n)
     _run(cache, "smla_cache_reorder", _on_device(cache, workspace, size), check_status, cache._ref, p_table, p_lens,
          p_parents, p_weights, p_new, p_len, p_moved, B, n, max_pages)
-    return new_table, new_lens, new_weights
+    return out

@@ -123,22 +123,6 @@ struct CwParams {
     int4* meta;                                  // [CTAs]
 };
 
-struct CwLShared {
-    uint64_t full[kCwLSlots], empty[kCwLSlots];
-    uint64_t q_full[kCwLQSlots], q_empty[kCwLQSlots];
-    uint64_t x_full;                             // the tiles of a pass are in TMEM
-    uint64_t t_full[2], t_empty[2], drain[2];
-    CwPlace at;
-    uint32_t tbase;
-    volatile int abort_flag;
-    float sums[kCwLTiles][kCwTile];              // of the second team
-};
-constexpr int kCwLQAt = kCwLSlots * kCwSlotBytes;
-constexpr int kCwLFactorAt = kCwLQAt + kCwLQSlots * kCwLQBytes;
-constexpr int kCwLSharedAt = kCwLFactorAt + kCwLQSlots * 3 * kCwLRows * 4;
-constexpr int kCwLSmem = kCwLSharedAt + int(sizeof(CwLShared));
-static_assert(kCwLSmem <= 232448, "shared memory of one CTA is at most 227 KB");
-
 __device__ __forceinline__ bool cw_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
@@ -263,6 +247,7 @@ struct CwWalk {
 struct CwUnits {
     int b, c0, c1, seen, rows, tiles, chunks;
     int64_t at, units, lo, hi, u0, u1;
+    CwUnits() = default;
     __device__ __forceinline__ CwUnits(const CwPlace& sh) : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi) {}
     __device__ __forceinline__ bool next(const CwParams& p) {
         do {
@@ -295,6 +280,24 @@ struct CwUnits {
         return left < kCwLRows ? left : kCwLRows;
     }
 };
+
+struct CwLShared {
+    uint64_t full[kCwLSlots], empty[kCwLSlots];
+    uint64_t q_full[kCwLQSlots], q_empty[kCwLQSlots];
+    uint64_t x_full;                             // the tiles of a pass are in TMEM
+    uint64_t t_full[2], t_empty[2], drain[2];
+    CwPlace at;
+    uint32_t tbase;
+    volatile int abort_flag;
+    float sums[kCwLTiles][kCwTile];              // of the second team
+    CwUnits item;                                // of the sums' warps
+    int more;
+};
+constexpr int kCwLQAt = kCwLSlots * kCwSlotBytes;
+constexpr int kCwLFactorAt = kCwLQAt + kCwLQSlots * kCwLQBytes;
+constexpr int kCwLSharedAt = kCwLFactorAt + kCwLQSlots * 3 * kCwLRows * 4;
+constexpr int kCwLSmem = kCwLSharedAt + int(sizeof(CwLShared));
+static_assert(kCwLSmem <= 232448, "shared memory of one CTA is at most 227 KB");
 
 // Units of sequence b; the whole warp asks.
 __device__ __forceinline__ int64_t cw_units(const CwParams& p, int b) {
@@ -896,7 +899,16 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
         uint32_t x_use = 0, use = 0, tile = 0;
         int4 joins = make_int4(-1, 0, 0, 0);
         bool ok = true, bad = false;
-        while (ok && w.next(p)) {
+        for (;;) {
+            // One warp looks for the next item and the others take its word: they meet at barriers in each pass, and
+            // would not leave them if they saw different numbers.
+            if (warp == 0) {
+                const bool more = ok && w.next(p);
+                if (lane == 0) { sh.item = w; sh.more = more; }
+            }
+            asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+            if (!sh.more) break;
+            w = sh.item;
             const int64_t line = w.b * width;
             const int last = w.last();
             for (int k = w.first(); k <= last && ok; ++k) {

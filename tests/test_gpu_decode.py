@@ -824,3 +824,21 @@ def test_weights_of_whole_prompts(H, tokens, n):
     lens = [min(n, i + 1) for i in range(tokens)] + [20]
     lse = np.full((tokens + 1, H), 4.0, dtype=np.float32)
     _watch(pool, table, [tokens, 1], lens, H, decay=0.5, lse=lse)
+
+
+def test_weights_of_fewer_tokens_than_rows():
+    # a batch whose last rows have no token in this step: their weights stay
+    pool = Pool(60, 16, 16, seed=92)
+    full = [100, 33, 50, 7]
+    table = pool.place(full)
+    pool.fill(table, full)
+    smla = _smla()
+    rng = np.random.default_rng(93)
+    q = bf16(rng.standard_normal((2, 32, 512)))
+    lse = _lse(q, pool, table, [0, 1, 2, 2, 2], full[:2])
+    out = _f32(np.full((4, table.shape[1] * 16), 3.0))
+    smla.cache_weights(bf16_dev(q), pool.device(), _i32(table), _i32(full[:2]), _f32(lse), out)
+    ref, bound = M.weights(q, pool.codes, pool.scales, table, [0, 1, 2, 2, 2], full[:2], lse, np.full(out.shape, 3.0), 1.0,
+                           np.full(out.shape, 3.0, dtype=np.float32), 16, 16)
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - ref) <= bound).all() and (got[2:] == 3.0).all()

@@ -108,18 +108,20 @@ def _on_device(cache: PagedCache, workspace: Optional[Workspace], size: int) -> 
 
 def _check2(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, n: int, m: int) -> int:
     """_check of a tensor of n x m."""
-    p = _check(cache, t, name, dtype, 2)
-    if t.shape != (n, m):
-        raise ValueError(f"{name} must have shape [{n}, {m}], got {tuple(t.shape)}")
-    return p
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n, m) and t.get_device() == cache._index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _check(cache, t, name, dtype, 2)
+    raise ValueError(f"{name} must have shape [{n}, {m}], got {tuple(t.shape)}")
 
 
 def _check1(cache: "PagedCache", t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> int:
     """_check of a vector of n."""
-    p = _check(cache, t, name, dtype, 1)
-    if t.shape != (n,):
-        raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
-    return p
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n,) and t.get_device() == cache._index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _check(cache, t, name, dtype, 1)
+    raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
 
 
 def _size_of(sizes: dict, key, where: str, *args) -> int:

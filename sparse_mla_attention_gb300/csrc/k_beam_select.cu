@@ -22,7 +22,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kBsThreads = 256;
-constexpr int kBsVecs = 8;                       // 16-byte vectors of a thread, beside one value at the row's ends
+constexpr int kBsVecs = 16, kBsGroup = 2;        // 16-byte vectors of a thread, beside one value at the row's ends; on their way together
 constexpr int kBsMergeThreads = 512;
 constexpr int kBsEach = 4;                       // candidates of a thread of the merge
 constexpr int kBsBatch = kBsMergeThreads * kBsEach;
@@ -127,7 +127,7 @@ __device__ __forceinline__ bool out_of_play(const BeamArgs& a, int row) {
 }  // namespace
 
 template <int kType>
-__global__ void __launch_bounds__(kBsThreads)
+__global__ void __launch_bounds__(kBsThreads, 6)
 beam_rows_kernel(const BeamArgs a) {
     constexpr int kSize = Logit<kType>::kSize, kEach = 16 / kSize;
     extern __shared__ __align__(16) unsigned long long best[];    // values that pass the bound
@@ -147,21 +147,52 @@ beam_rows_kernel(const BeamArgs a) {
     const int first = chunk * kBsThreads * kBsVecs + int(threadIdx.x);
     const uint4* src = reinterpret_cast<const uint4*>(base + lead * kSize) + first;
     constexpr uint32_t kNone = Logit<kType>::kNone;
-    uint4 raw[kBsVecs];
-#pragma unroll
-    for (int k = 0; k < kBsVecs; ++k)
-        raw[k] = first + k * kBsThreads < vecs ? __ldg(src + k * kBsThreads) : make_uint4(kNone, kNone, kNone, kNone);
     float x = -INFINITY;
     int xi = -1;
     if (chunk == 0 && threadIdx.x < lead) xi = threadIdx.x;
     if (chunk == a.chunks - 1 && threadIdx.x >= kBsThreads - tail) xi = a.V - (kBsThreads - int(threadIdx.x));
     if (xi >= 0) x = Logit<kType>::one(base + int64_t(xi) * kSize);
 
-    float tops[kBsVecs], top = x;                // (maxima pass over NaN)
+    // A thread's largest value and its sum of exponentials relative to it, which follow each other from group to group
+    // (two values at a time); the largest of each vector.
+    const uint64_t log2e = pair_of(kBsLog2e, kBsLog2e);
+    float tops[kBsVecs], top = x, sum = xi >= 0 ? (x == -INFINITY ? 0.f : x - x + 1.f) : 0.f;       // (NaN for NaN and inf)
+    uint4 raw[2][kBsGroup];
+    auto load = [&](int g, uint4 (&to)[kBsGroup]) {
 #pragma unroll
-    for (int k = 0; k < kBsVecs; ++k) {
-        tops[k] = Logit<kType>::top(raw[k]);
-        top = fmaxf(top, tops[k]);
+        for (int k = 0; k < kBsGroup; ++k) {
+            const int v = (g * kBsGroup + k) * kBsThreads;
+            to[k] = first + v < vecs ? __ldg(src + v) : make_uint4(kNone, kNone, kNone, kNone);
+        }
+    };
+    load(0, raw[0]);
+#pragma unroll
+    for (int g = 0; g < kBsVecs / kBsGroup; ++g) {
+        uint4 (&now)[kBsGroup] = raw[g & 1];
+        if (g + 1 < kBsVecs / kBsGroup) load(g + 1, raw[(g + 1) & 1]);
+        float high = top;                        // (maxima pass over NaN)
+#pragma unroll
+        for (int k = 0; k < kBsGroup; ++k) {
+            tops[g * kBsGroup + k] = Logit<kType>::top(now[k]);
+            high = fmaxf(high, tops[g * kBsGroup + k]);
+        }
+        if (high > top) sum *= ex2_approx((top - high) * kBsLog2e);      // (top -inf: sum is 0)
+        top = high;
+        const float ref = top == -INFINITY ? 0.f : top;
+        const uint64_t shift = pair_of(-ref, -ref);
+        uint64_t part[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < kBsGroup; ++k) {
+            float v[kEach];
+            Logit<kType>::spread(now[k], v);
+#pragma unroll
+            for (int e = 0; e < kEach; e += 2) {
+                const float2 t = floats_of(mul2(add2(pair_of(v[e], v[e + 1]), shift), log2e));
+                part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pair_of(ex2_approx(t.x), ex2_approx(t.y)));
+            }
+        }
+        const float2 both = floats_of(add2(part[0], part[1]));
+        sum += both.x + both.y;
     }
     if (top != top) top = -INFINITY;
     const uint32_t mine = order_of(top + 0.f);   // (both zeros alike)
@@ -230,28 +261,15 @@ beam_rows_kernel(const BeamArgs a) {
         if (xi >= 0) pass(x, xi);
         look(pass, value_of(bound));
     }
-    // the sum of exponentials: a thread's in fp32, two at a time; the threads' with what each addition rounds off
-    // beside it (64-bit additions of a warp occupy their unit for 16 cycles each)
-    const uint64_t shift = pair_of(-ref, -ref), log2e = pair_of(kBsLog2e, kBsLog2e);
-    uint64_t sums[2] = {pair_of(ex2_approx((x - ref) * kBsLog2e), 0.f), 0};
-#pragma unroll
-    for (int k = 0; k < kBsVecs; ++k) {
-        float v[kEach];
-        Logit<kType>::spread(raw[k], v);
-#pragma unroll
-        for (int e = 0; e < kEach; e += 2) {
-            const float2 t = floats_of(mul2(add2(pair_of(v[e], v[e + 1]), shift), log2e));
-            sums[(e >> 1) & 1] = add2(sums[(e >> 1) & 1], pair_of(ex2_approx(t.x), ex2_approx(t.y)));
-        }
-    }
-    const float2 part = floats_of(add2(sums[0], sums[1]));
-    float all = part.x, rest = 0.f;
+    // the threads' sums, relative to the chunk's largest, with what each addition rounds off beside them (64-bit
+    // additions of a warp occupy their unit for 16 cycles each)
+    if (top != peak) sum *= ex2_approx((top - ref) * kBsLog2e);
+    float all = sum, rest = 0.f;
     auto add = [&](float y, float more) {
-        const float sum = all + y, z = sum - all;
-        rest += ((all - (sum - z)) + (y - z)) + more;
-        all = sum;
+        const float both = all + y, z = both - all;
+        rest += ((all - (both - z)) + (y - z)) + more;
+        all = both;
     };
-    add(part.y, 0.f);
 #pragma unroll
     for (int d = 16; d; d >>= 1)
         add(__shfl_xor_sync(0xffffffffu, all, d), __shfl_xor_sync(0xffffffffu, rest, d));

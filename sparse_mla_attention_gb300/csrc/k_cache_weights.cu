@@ -51,7 +51,11 @@ constexpr uint32_t kCwLCols = (512 - kCwLColS) / 2;
 static_assert(2 * kCwLRows <= int(kCwLCols), "a product has a column for each row of q and part");
 constexpr int kCwMaxCtas = 160;
 constexpr int kCwSplitThreads = 256;
-constexpr int kCwManyRows = 512;                 // rows of q a sequence, on average, from which on the cache is resident
+// Rows of q a sequence, on average, above which the cache is resident. Device time in us, streaming / resident (sequences
+// x positions, heads, rows): 64 x 3000, 128, 192: 42.5 / 63.3, 386: 77.0 / 87.0, 768: 137 / 125; 16 x 4000, 64, 288: 30.9 /
+// 30.3, 392: 37.2 / 34.6, 760: 59.8 / 49.6; 2 x 30000, 128, 448: 35.5 / 31.4, 1216: 79.0 / 50.6; 1 x 2000, 128, 4096: 125 /
+// 24.6 (streaming, a tile's chunks are one CTA's).
+constexpr int kCwManyRows = 400;
 constexpr int kCwMaxBlocks = 1024;               // of the splitting kernel
 
 // Two floats at a time.

@@ -483,7 +483,7 @@ int smla_beam_select(const void* logits, int32_t type, int64_t row_stride, const
     if (rc) return rc;
     if (type != SMLA_F32 && type != SMLA_BF16 && type != SMLA_F16) return SMLA_ERR_ARG;
     const int64_t size = type == SMLA_F32 ? 4 : 2, rows = int64_t(B) * K;
-    if (row_stride < 0 || row_stride > (int64_t(1) << 40)) return SMLA_ERR_SHAPE;
+    if (row_stride < 0 || (rows > 1 && row_stride > (int64_t(1) << 60) / rows)) return SMLA_ERR_SHAPE;
     if (done && (eos < 0 || eos >= V)) return SMLA_ERR_ARG;
     if (!workspace) return SMLA_ERR_NULL;
     if (B > 0 && (!logits || !scores || !parents || !tokens || !new_scores)) return SMLA_ERR_NULL;

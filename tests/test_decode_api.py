@@ -154,7 +154,7 @@ def test_reorder_rejections(lib):
     (dict(K=0), _lib.SMLA_ERR_SHAPE), (dict(K=65), _lib.SMLA_ERR_SHAPE), (dict(n=0), _lib.SMLA_ERR_SHAPE),
     (dict(n=65), _lib.SMLA_ERR_SHAPE), (dict(V=0), _lib.SMLA_ERR_SHAPE), (dict(V=(1 << 22) + 1), _lib.SMLA_ERR_SHAPE),
     (dict(B=-1), _lib.SMLA_ERR_SHAPE), (dict(B=1 << 24, K=64, V=1 << 22), _lib.SMLA_ERR_SHAPE),
-    (dict(stride=-1), _lib.SMLA_ERR_SHAPE), (dict(type=3), _lib.SMLA_ERR_ARG), (dict(type=-1), _lib.SMLA_ERR_ARG),
+    (dict(stride=-1), _lib.SMLA_ERR_SHAPE), (dict(stride=(1 << 63) - 1), _lib.SMLA_ERR_SHAPE), (dict(type=3), _lib.SMLA_ERR_ARG), (dict(type=-1), _lib.SMLA_ERR_ARG),
     (dict(eos=-1), _lib.SMLA_ERR_ARG), (dict(eos=1000), _lib.SMLA_ERR_ARG), (dict(ws_bytes=255), _lib.SMLA_ERR_WORKSPACE)])
 def test_select_rejects_bad_sizes(lib, change, code):
     assert _select(lib, _addrs(), **change) == code

@@ -842,3 +842,76 @@ def test_weights_of_fewer_tokens_than_rows():
                            np.full(out.shape, 3.0, dtype=np.float32), 16, 16)
     got = out.double().cpu().numpy()
     assert (np.abs(got - ref) <= bound).all() and (got[2:] == 3.0).all()
+
+
+def test_decode_calls_refuse_what_they_cannot_take():
+    smla = _smla()
+    from sparse_mla_attention_gb300 import SmlaError, _lib
+    pool = Pool(20, 16, 16, seed=94)
+    table = pool.place([40, 20], extra=0)
+    cache = pool.device()
+    tt, lt = _i32(table), _i32([40, 20])
+    W = table.shape[1] * 16
+    w, q, lse = torch.zeros((2, W), device=DEV), bf16_dev(np.zeros((2, 16, 512))), torch.zeros((2, 16), device=DEV)
+    weights = lambda **k: smla.cache_weights(**{**dict(q=q, cache=cache, table=tt, lens=lt, lse=lse, weights=w), **k})
+    evict = lambda **k: smla.cache_evict(**{**dict(cache=cache, table=tt, lens=lt, weights=w, keep=8), **k})
+    reorder = lambda **k: smla.cache_reorder(**{**dict(cache=cache, table=tt, lens=lt, parents=_i32([0, 1])), **k})
+    for call, kind, bad in ((weights, ValueError, dict(lens=_i32([1]))), (weights, ValueError, dict(lse=lse[:, :8])),
+                            (weights, ValueError, dict(weights=torch.zeros((2, W + 16), device=DEV))),
+                            (weights, TypeError, dict(weights=w.double())), (weights, ValueError, dict(earlier=w[:1])),
+                            (weights, ValueError, dict(cu_tokens=_i32([0, 2]))), (weights, ValueError, dict(table=tt[:1])),
+                            (weights, ValueError, dict(q=q.transpose(0, 1))), (weights, TypeError, dict(lens=lt.long())),
+                            (evict, ValueError, dict(keep=0)), (evict, ValueError, dict(keep=W + 1)),
+                            (evict, ValueError, dict(first=5, recent=4)), (evict, ValueError, dict(first=-1)),
+                            (evict, ValueError, dict(weights=w.t())), (evict, ValueError, dict(lens=lt.cpu())),
+                            (evict, ValueError, dict(out=(tt.clone(), lt.clone(), w.clone(), _i32(np.zeros((2, 9)))))),
+                            (reorder, TypeError, dict(parents=torch.zeros(2, device=DEV))),
+                            (reorder, ValueError, dict(weights=w[:1])),
+                            (reorder, ValueError, dict(out=(tt.clone(), lt.clone(), w.clone())))):
+        with pytest.raises(kind):
+            call(**bad)
+    for call, bad, code in ((weights, dict(decay=float("nan")), _lib.SMLA_ERR_ARG),
+                            (weights, dict(scale=-1.0), _lib.SMLA_ERR_ARG),
+                            (evict, dict(out=(tt, lt.clone(), w.clone(), _i32(np.zeros((2, 8))))), _lib.SMLA_ERR_OVERLAP),
+                            (reorder, dict(out=(tt, lt.clone(), None)), _lib.SMLA_ERR_OVERLAP)):
+        with pytest.raises(SmlaError) as e:
+            call(**bad)
+        assert e.value.code == code
+    x, s = torch.zeros((6, 50), device=DEV), torch.zeros((2, 3), device=DEV)
+    for kind, args, kw in ((TypeError, (x.double(), s), {}), (ValueError, (x[:5], s), {}), (ValueError, (x.t(), s), {}),
+                           (ValueError, (x, s), dict(done=torch.zeros((2, 3), dtype=torch.bool, device=DEV))),
+                           (TypeError, (x, s), dict(done=torch.zeros((2, 3), device=DEV), eos=1)),
+                           (SmlaError, (x, s), dict(out=(tt, tt, tt.float()))),         # (of the right shape, but one tensor twice)
+                           (ValueError, (x, s), dict(n=2, out=(tt, tt, tt.float()))), (SmlaError, (x, s), dict(n=65)),
+                           (SmlaError, (x, s), dict(n=0)), (ValueError, (x.cpu(), s), {})):
+        with pytest.raises(kind):
+            smla.beam_select(*args, **kw)
+    pool.check(cache)
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_what_is_kept_is_attended_to_as_before(page):
+    # attention over the kept rows is attention over the picks of the same positions
+    smla = _smla()
+    rng = np.random.default_rng(95)
+    lens = [700, 300, 90]
+    pool = Pool(300, page, 16, seed=96)
+    table = pool.place(lens)
+    pool.fill(table, lens)
+    cache = pool.device()
+    tt, lt = _i32(table), _i32(lens)
+    q = bf16_dev(rng.standard_normal((3, 48, 512)))
+    o, lse = smla.sparse_mla_fwd_paged(q, cache, tt, lt)
+    w = smla.cache_weights(q, cache, tt, lt, lse, torch.zeros((3, table.shape[1] * page), device=DEV))
+    # a head's weights sum to 1 (lse and each weight off by a few 2^-20)
+    np.testing.assert_allclose(w.double().sum(1).cpu().numpy(), 48.0, rtol=1e-4)
+    new, new_lens, _, kept = smla.cache_evict(cache, tt, lt, w, 128, first=4, recent=16)
+    a, la = smla.sparse_mla_fwd_paged(q, cache, new, new_lens)
+    b, lb = smla.sparse_mla_fwd_paged(q, cache, tt, lt, topk=kept)
+    pool.refcount[:] = _np(cache.refcount)
+    ref, rl, ob, lbound = R.attend(to_f64(q), pool.codes, pool.scales, table, lens, page, 16, topk=_np(kept))
+    for got, gl in ((a, la), (b, lb)):                 # (scales may have grown: codes rounded to 2^-4 of the values at most)
+        assert (np.abs(gl.double().cpu().numpy() - rl) <= lbound + 2.0 ** -4).all()
+    assert (np.abs(to_f64(b) - ref) <= ob).all()
+    err = np.linalg.norm(to_f64(a) - ref) / np.linalg.norm(ref)
+    assert err <= 2.0 ** -4

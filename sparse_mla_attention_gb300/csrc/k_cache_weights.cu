@@ -56,7 +56,7 @@ constexpr int kCwSplitThreads = 256;
 // 30.3, 392: 37.2 / 34.6, 760: 59.8 / 49.6; 2 x 30000, 128, 448: 35.5 / 31.4, 1216: 79.0 / 50.6; 1 x 2000, 128, 4096: 125 /
 // 24.6 (streaming, a tile's chunks are one CTA's).
 constexpr int kCwManyRows = 400;
-constexpr int kCwMaxBlocks = 1024;               // of the splitting kernel
+constexpr int kCwMaxBlocks = 608;                // of the splitting kernel: four an SM leave room for the other's, which start meanwhile
 
 // Two floats at a time.
 __device__ __forceinline__ uint64_t pair_of(float x, float y) {
@@ -92,7 +92,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
 
 // Where a CTA's work begins and ends.
 struct CwPlace {
-    int b0;                                      // first sequence with work of this CTA
+    int b0;                                      // first sequence with work of this CTA,
+    int c0, c1, seen;                            // its tokens and what they see
     int64_t at0, lo, hi;                         // its first unit; the CTA's units
     int64_t per, rem;                            // of a CTA; the first rem have one more
     int64_t sum[kCwLThreads / 32];
@@ -172,12 +173,30 @@ __device__ __forceinline__ __half2 cw_e4m3x2_half(uint32_t v) {
     return __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v), __NV_E4M3));
 }
 
+// (The shuffles tell the compiler that a warp's lanes agree: descriptors stay in uniform registers.)
+__device__ __forceinline__ int cw_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Positions that some token of a sequence sees (0: nothing to do). The whole warp asks for one sequence.
 __device__ __forceinline__ int cw_seen(const WeightsArgs& a, int c0, int c1) {
     int most = 0;
 #pragma unroll 4
     for (int t = c0 + int(threadIdx.x & 31); t < c1; t += 32) most = max(most, cw_len(a, t));
     return __reduce_max_sync(0xffffffffu, most);
+}
+
+// Sequence b's tokens and what they see, for a whole warp; the first one's are at hand. False: it has none.
+__device__ __forceinline__ bool cw_look(const WeightsArgs& a, const CwPlace& place, int b, int& c0, int& c1, int& seen) {
+    if (b == place.b0) {
+        c0 = cw_same(place.c0);
+        c1 = cw_same(place.c1);
+        seen = cw_same(place.seen);
+        return true;
+    }
+    if (!cw_tokens(a, b, c0, c1) || c0 == c1) return false;
+    c0 = cw_same(c0);
+    c1 = cw_same(c1);
+    seen = cw_seen(a, c0, c1);
+    return true;
 }
 
 struct CwSize {
@@ -211,14 +230,13 @@ __device__ __forceinline__ float cw_sum16(const uint32_t (&hi)[16], const uint32
 }
 
 // Where a CTA's work lies: items (sequence b, its tiles [k0, k1)), all chunks of each. A warp walks together.
-// (The shuffles tell the compiler that a warp's lanes agree: descriptors stay in uniform registers.)
-__device__ __forceinline__ int cw_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
 struct CwWalk {
     int b, c0, c1, seen, k0, k1;
     int rows, chunk_rows, chunks;
     int64_t at, units, lo, hi;
-    __device__ __forceinline__ CwWalk(const CwPlace& sh) : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi) {}
+    const CwPlace* place;
+    __device__ __forceinline__ CwWalk(const CwPlace& sh)
+        : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi), place(&sh) {}
     __device__ __forceinline__ bool next(const CwParams& p) {
         do {
             at += units;
@@ -226,10 +244,7 @@ struct CwWalk {
             k0 = k1 = 0;
             ++b;
             if (at >= hi || b >= p.a.B) return false;
-            if (!cw_tokens(p.a, b, c0, c1) || c0 == c1) continue;
-            c0 = cw_same(c0);
-            c1 = cw_same(c1);
-            seen = cw_seen(p.a, c0, c1);
+            if (!cw_look(p.a, *place, b, c0, c1, seen)) continue;
             rows = (c1 - c0) * p.a.H;
             const CwSize n(seen, rows, p.resident);
             chunk_rows = n.chunk_rows;
@@ -251,18 +266,17 @@ struct CwWalk {
 struct CwUnits {
     int b, c0, c1, seen, rows, tiles, chunks;
     int64_t at, units, lo, hi, u0, u1;
+    const CwPlace* place;
     CwUnits() = default;
-    __device__ __forceinline__ CwUnits(const CwPlace& sh) : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi) {}
+    __device__ __forceinline__ CwUnits(const CwPlace& sh)
+        : b(sh.b0 - 1), at(sh.at0), units(0), lo(sh.lo), hi(sh.hi), place(&sh) {}
     __device__ __forceinline__ bool next(const CwParams& p) {
         do {
             at += units;
             units = u0 = u1 = 0;
             ++b;
             if (at >= hi || b >= p.a.B) return false;
-            if (!cw_tokens(p.a, b, c0, c1) || c0 == c1) continue;
-            c0 = cw_same(c0);
-            c1 = cw_same(c1);
-            seen = cw_seen(p.a, c0, c1);
+            if (!cw_look(p.a, *place, b, c0, c1, seen)) continue;
             rows = (c1 - c0) * p.a.H;
             const CwSize n(seen, rows, 1);
             tiles = n.tiles;
@@ -322,12 +336,12 @@ __device__ void cw_locate(const CwParams& p, CwPlace& sh) {
     const int run = (p.a.B + int(blockDim.x) - 1) / int(blockDim.x);
     const int b0 = int(min(int64_t(threadIdx.x) * run, int64_t(p.a.B))), b1 = min(b0 + run, p.a.B);
     int64_t mine = 0;
+    int c0 = 0, c1 = 0, seen = 0;                // of the last sequence looked at
     for (int i = 0; i < run; ++i) {
         // a lane its own sequence if that has one token, the warp together one after the other that have more
         const int b = b0 + i;
-        int c0 = 0, c1 = 0;
         const bool live = b < b1 && cw_tokens(p.a, b, c0, c1) && c1 > c0;
-        int seen = live && c1 == c0 + 1 ? cw_len(p.a, c0) : 0;
+        seen = live && c1 == c0 + 1 ? cw_len(p.a, c0) : 0;
         for (unsigned more = __ballot_sync(0xffffffffu, live && c1 > c0 + 1); more; more &= more - 1) {
             const int l = __ffs(more) - 1;
             const int most = cw_seen(p.a, __shfl_sync(0xffffffffu, c0, l), __shfl_sync(0xffffffffu, c1, l));
@@ -357,12 +371,15 @@ __device__ void cw_locate(const CwParams& p, CwPlace& sh) {
     if (finder) {
         int b = __shfl_sync(0xffffffffu, b0, __ffs(finder) - 1);
         at = __shfl_sync(0xffffffffu, at, __ffs(finder) - 1);
-        if (run > 1)
+        if (run > 1) {
             for (int64_t n = cw_units(p, b); lo >= at + n; n = cw_units(p, b)) {
                 at += n;
                 ++b;
             }
-        if (lane == 0) { sh.b0 = b; sh.at0 = at; }
+            cw_tokens(p.a, b, c0, c1);
+            seen = cw_seen(p.a, c0, c1);
+        }
+        if (lane == __ffs(finder) - 1) { sh.b0 = b; sh.at0 = at; sh.c0 = c0; sh.c1 = c1; sh.seen = seen; }
     }
 }
 

@@ -8,6 +8,11 @@
 // exponentials and its n best logits; beam_merge_kernel joins a row's sums and merges the lists of a group.
 // Which candidate comes first is decided in 64 bits: a thread's sum of up to 65 exponentials in 32 bits, the rest in 64.
 //
+// Bound: 256 rows of 128000 in bf16 (65.5 MB): 25 us, of which the rows take 13.4 (4.9 TB/s) and the merge 7 with its
+// start behind them; 4 rows of 32000 in fp32: 11 us. Chunks of 64 KB in groups of two loads a thread, six CTAs an
+// SM: 25.7 us; of four, four CTAs: 27.2; 512 threads: 28.7; chunks of 32 KB held in registers whole: 32, and of 16 KB 40. The merge: log-sums
+// 3 us (64-bit exponentials and logarithms: latency), bound and ranks 3.
+//
 // A chunk's n best: a bound that n to 2n threads' largest values reach (bisection over their bits, a count and a
 // barrier a step), so that at most 2 n threads' values pass it, then their exact ranks among those.
 #include <cuda_bf16.h>

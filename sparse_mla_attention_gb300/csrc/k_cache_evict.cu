@@ -6,6 +6,13 @@
 // weights' bits (a histogram of 2048 bins, and a bisection among the weights of one bin as soon as they are few), so the
 // choice is exact and the same in every run.
 //
+// Bound: the copies by HBM, the choice by latency. 64 sequences of up to 8192 positions to 2048 each, pages and
+// blocks of 64: 46 us with a free of the last call's pages, of which the copies take 24 (134 MB read and written: 5.6
+// TB/s), the choice 9 and the free 4; 3 of up to 81920 to 16384: 38 us, 14 and 18 and 4; one of 1500 to 1024: 17 us. The choice of
+// a sequence in one CTA: weights into registers 1 us, histogram 1, its scan 0.5, collecting the bin 1.4,
+// bisection 0.8, the list 1.9. Three histograms instead of the bisection: 50 us, 49 with a cluster; rows looked up by
+// the choice instead of the copies: 50.
+//
 // evict_plan_kernel: cluster 0 grants the free pages, the other CTAs choose, one sequence each.
 // evict_copy_kernel: moves the rows. A block's scale is the largest of its rows'
 // scales; the codes of rows of a smaller one are rounded to it.
@@ -401,7 +408,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
         attr_done[dev] = true;
     }
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // Long sequences have a cluster each.
+    // A sequence has one CTA, whose registers hold 16384 weights; tables of longer ones give it a cluster (3 of 81920:
+    // 38 us; with one CTA, which goes over its weights tile by tile, 126).
     const int parts = (int64_t(a.max_pages) << a.cache.page_shift) > 16384 ? kPlanCtas : 1;
     const unsigned grid = unsigned(kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas);
     if (parts > 1) evict_plan_kernel<kPlanCtas><<<grid, kPlanThreads, sizeof(ChooseShared), s>>>(a);

@@ -16,9 +16,18 @@
 //
 // weights_kernel: persistent, one CTA an SM. The units (tile, chunk of a sequence's q) are dealt out in tiles; a
 // CTA goes through its tiles once for each chunk, q staying, the cache streaming. Warps: 0-3 and 4-7 sums, on
-// alternate tiles, 8 and 10 loads of the cache and of q, 9 products. Shared memory: q 128 KB (one chunk of 128 rows, or two of up to 64 rows in
-// turn; reloaded in quarters of K as the last tile gets done with them), ring of 6 blocks of 128 rows x 128 bytes.
-// TMEM: two buffers of 256 columns.
+// alternate tiles, 8 and 10 loads of the cache and of q, 9 products. Shared memory: q 128 KB (one chunk of 128 rows, or
+// two of up to 64 rows in turn; reloaded in quarters of K as the last tile gets done with them), ring of 6 blocks of 128
+// rows x 128 bytes. TMEM: two buffers of 256 columns.
+// Many rows of q (kCwManyRows): streaming the cache once a chunk is bound by L2 (207 us where the other takes 132), so
+// weights_resident_kernel keeps three tiles in TMEM and streams q; see there.
+//
+// Bound: HBM for few rows: 128 sequences of up to 5120 positions, 64 heads 53 us, 96 of up to 6001, 16 heads 44 us,
+// 5.0 and 5.1 TB/s over all; from the first tile to the last (40 of the 53 us) 6.6 TB/s. The rest is the splitting
+// kernel's start (2 us), the deal (2), look-ups and first loads (3 to 4) and the last tile's way out. More or fewer ring
+// slots: 4 / 5 / 6 / 9 56.7 / 54.4 / 53.7 / - and 45.9 / 44.4 / 44.0 / 43.9 us; the same pages asked of L2 three tiles ahead: 58.8
+// and 48.8. One token of 777 positions: 8 us. Many rows: the tensor core (78% busy): 4 prompts of up to 20000
+// positions, 32 tokens, 128 heads 132 us, 1.62 PFLOP/s, of which the 8-bit products are twice as many.
 //
 // Every mbarrier wait is bounded; a timeout sets SMLA_ERR_TIMEOUT, stops the CTA's loops, waits (bounded) for its own
 // copies and MMAs and frees TMEM.
@@ -753,6 +762,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
 // 32 rows, one bulk copy each, four in flight. The units (three tiles, chunk) are dealt out one by one; a pass whose
 // chunks several CTAs have is joined by weights_join_kernel. Warps as above, and 11 for products too; the teams take the
 // products in turn (tiles within chunks), keep their sums of a pass in registers and join them at its end.
+// Why so: with the cache as the streamed operand each product of 128 x 128 x 512 takes 64 KB from L2, 9 TB/s at the
+// tensor core's rate over all SMs; with three tiles resident it takes 43. Three tiles and 64 columns twice fill TMEM. A
+// as a TMEM operand leaves shared memory's rate to q (as a shared one with 64 columns it would need 1.5 times that rate).
+// Products of 16 x (128 x 64 x 32) take 512 to 535 cycles, back to back within a chunk; one issuing warp left 250 to 400
+// between them (224 us). Passes by tile, not by three: the CTAs with a fourth tile took 1.5 times as long (169 us).
 __global__ void __launch_bounds__(kCwLThreads, 1)
 weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
     extern __shared__ __align__(1024) uint8_t ring[];

@@ -408,8 +408,9 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
         attr_done[dev] = true;
     }
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // A sequence has one CTA, whose registers hold 16384 weights; tables of longer ones give it a cluster (3 of 81920:
-    // 38 us; with one CTA, which goes over its weights tile by tile, 126).
+    // A sequence has one CTA, whose registers hold 16384 weights; wider tables give it a cluster. Both sides, device time:
+    // 3 of 81920 68 us with one CTA each (it goes over its weights tile by tile), 38 with a cluster; 64 of 8192 47 and 113
+    // (512 CTAs take turns), one of 1500 17 and 23.
     const int parts = (int64_t(a.max_pages) << a.cache.page_shift) > 16384 ? kPlanCtas : 1;
     const unsigned grid = unsigned(kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas);
     if (parts > 1) evict_plan_kernel<kPlanCtas><<<grid, kPlanThreads, sizeof(ChooseShared), s>>>(a);

@@ -67,15 +67,16 @@ struct ChooseShared {
     int hist[kDigits];                           // of this CTA
     int all[3][kDigits];                         // of the cluster, in its first CTA
     union {
-        uint32_t few[kFew];                      // weights of the bin that the last one to stay is in
+        uint32_t few[kFew];                      // weights of the bin that the last one to stay is in; the first CTA's
         uint16_t stays[kTile];                   // positions of a tile that stay, in order
     };
     int digit, over, inside;                     // the bin of the rest-th largest, what lies above it and in it
-    int n_few, n_all, rest;
-    uint32_t all_few[kFew];                      // the cluster's, in its first CTA
-    int warp[2][kPlanWarps];
+    int n_few;                                   // of this CTA
+    __align__(16) int fine[3][128];              // bins of the few
+    int3 found;
     uint32_t prefix;
-    int above, ties;                             // of this CTA's part, read by the others
+    int rest;
+    int2 counts[kPlanCtas];                      // of each CTA's part: those above prefix, and equal
 };
 
 // The positions that sequence b keeps. kParts CTAs share the sequence (all of a cluster, or one), a run of positions
@@ -110,15 +111,14 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
             key[e] = order_of(v.x); key[e + 1] = order_of(v.y); key[e + 2] = order_of(v.z); key[e + 3] = order_of(v.w);
         }
     };
+    if (threadIdx.x == 0) ch.n_few = 0;
+    if (threadIdx.x < 3 * 128) (&ch.fine[0][0])[threadIdx.x] = 0;
+    if (kParts > 1 && part == 0)
+        for (int i = threadIdx.x; i < 3 * kDigits; i += kPlanThreads) (&ch.all[0][0])[i] = 0;
     if (one_tile) load(s0);
     uint32_t prefix = 0;
     if (by_weight) {                             // (the same in every CTA of the sequence)
-        if (threadIdx.x == 0) ch.n_few = ch.n_all = 0;
-        if (kParts > 1) {
-            if (part == 0)
-                for (int i = threadIdx.x; i < 3 * kDigits; i += kPlanThreads) (&ch.all[0][0])[i] = 0;
-            cl.sync();
-        }
+        if (kParts > 1) cl.sync();
         ChooseShared* lead = kParts > 1 ? cl.map_shared_rank(&ch, 0) : &ch;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
@@ -144,131 +144,149 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
                     if (h) atomicAdd(lead->all[pass] + d, h);
                 }
                 cl.sync();
-                hist = lead->all[pass];
+                hist = ch.all[pass];
             }
-            // bins in falling order, two a thread: the sums before them
-            const int d0 = bins - 1 - 2 * int(threadIdx.x), d1 = d0 - 1;
-            const int h0 = d0 >= 0 ? hist[d0] : 0, h1 = d0 >= 0 ? hist[d1] : 0;
-            int total;
-            const int before = cta_scan(h0 + h1, sh, turn, &total);
-            if (before < rest && rest <= before + h0 + h1) {
-                const bool second = rest > before + h0;
-                ch.digit = second ? d1 : d0;
-                ch.over = second ? before + h0 : before;
-                ch.inside = second ? h1 : h0;
+            if (part == 0) {                     // bins in falling order, two a thread: the sums before them
+                const int d0 = bins - 1 - 2 * int(threadIdx.x), d1 = d0 - 1;
+                const int h0 = d0 >= 0 ? hist[d0] : 0, h1 = d0 >= 0 ? hist[d1] : 0;
+                int total;
+                const int before = cta_scan(h0 + h1, sh, turn, &total);
+                if (before < rest && rest <= before + h0 + h1) {
+                    const bool second = rest > before + h0;
+                    const int3 found = second ? make_int3(d1, before + h0, h1) : make_int3(d0, before, h0);
+#pragma unroll
+                    for (int r = 0; r < kParts; ++r) {
+                        ChooseShared* to = kParts > 1 ? cl.map_shared_rank(&ch, r) : &ch;
+                        to->digit = found.x;
+                        to->over = found.y;
+                        to->inside = found.z;
+                    }
+                }
             }
-            __syncthreads();
+            sync_all();
             prefix |= uint32_t(ch.digit) << shift;
             rest -= ch.over;
             if (pass == 2 || ch.inside > kFew) continue;
-            // the bin's weights in one place, and their rest-th largest by bisection
+            // the bin's weights in the first CTA, behind those of the CTAs before, and their rest-th largest there
             const uint32_t bin = ~0u << shift;
+            const int lane = int(threadIdx.x & 31), n = ch.inside;
+            int to0 = 0;
+            if (kParts > 1) to0 = __reduce_add_sync(0xffffffffu, lane < part ? cl.map_shared_rank(&ch, lane)->hist[ch.digit] : 0);
             for (int64_t base = s0; base < s1; base += kTile) {
                 if (!one_tile) load(base);
-                if (runs == 0) continue;
+                uint32_t in = 0;
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) in |= uint32_t((key[e] & bin) == prefix) << e;
+                in &= runs;
+                if (in == 0) continue;
+                int to = to0 + atomicAdd(&ch.n_few, __popc(in));
 #pragma unroll
                 for (int e = 0; e < kRun; ++e)
-                    if (((runs >> e) & 1) && (key[e] & bin) == prefix) ch.few[atomicAdd(&ch.n_few, 1)] = key[e];
-            }
-            if (kParts > 1) {                    // from each CTA to the first in one piece
-                __syncthreads();
-                if (threadIdx.x == 0) ch.digit = atomicAdd(&lead->n_all, ch.n_few);
-                __syncthreads();
-                for (int i = threadIdx.x; i < ch.n_few; i += kPlanThreads) lead->all_few[ch.digit + i] = ch.few[i];
+                    if ((in >> e) & 1) lead->few[to++] = key[e];
             }
             sync_all();
             if (part == 0) {
-                const int n = kParts > 1 ? ch.n_all : ch.n_few;
-                const uint32_t* few = kParts > 1 ? ch.all_few : ch.few;
-                uint32_t mine[4];
+                int mine[4];                     // what lies above prefix; -1: none
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = int(threadIdx.x) + kPlanThreads * k;
-                    mine[k] = i < n ? few[i] : 0u;                       // (below every bound)
+                    mine[k] = i < n ? int(ch.few[i] - prefix) : -1;
                 }
-                int set = 0;                     // of the warps' counts: two in turn, a barrier a count
-                auto reach = [&](uint32_t bound) {
-                    int c = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) c += int(mine[k] >= bound);
-                    c = __reduce_add_sync(0xffffffffu, c);
-                    if ((threadIdx.x & 31) == 0) ch.warp[set][threadIdx.x >> 5] = c;
-                    __syncthreads();
-                    c = __reduce_add_sync(0xffffffffu, ch.warp[set][threadIdx.x & 31]);
-                    set ^= 1;
-                    return c;
-                };
-                // at least `rest` reach lo, fewer hi (2^32 if the bin is the last: what passes all)
-                uint64_t lo = prefix, hi = (uint64_t(prefix) | ~bin) + 1;
-                int over = 0;
+                // seven bits of the rest-th largest at a time: a histogram of [lo, lo + 2^(s + 7)), `over` lie above
+                int lo = 0, over = 0, s = shift == 21 ? 14 : 7;
                 bool exact = false;
-                while (hi - lo > 1) {
-                    const uint64_t mid = lo + (hi - lo) / 2;
-                    const int r = reach(uint32_t(mid));
-                    if (r == rest) { lo = mid; exact = true; break; }    // these and no others
-                    if (r > rest) lo = mid; else hi = mid;
+#pragma unroll 1
+                for (int* fine = ch.fine[0]; s >= 0 && !exact; fine += 128, s -= 7) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int d = (mine[k] - lo) >> s;
+                        if (mine[k] >= lo && d < 128) atomicAdd(fine + d, 1);
+                    }
+                    __syncthreads();
+                    if (threadIdx.x < 32) {      // four bins a lane, the largest first
+                        const int4 h = reinterpret_cast<const int4*>(fine)[31 - lane];
+                        const int sum = h.x + h.y + h.z + h.w;
+                        int before = sum;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const int x = __shfl_up_sync(0xffffffffu, before, d);
+                            if (lane >= d) before += x;
+                        }
+                        before += over - sum;
+                        if (before < rest && rest <= before + sum) {
+                            int d = 127 - 4 * lane;
+                            int in = h.w;
+                            if (before + in < rest) { before += in; in = h.z; --d; }
+                            if (before + in < rest) { before += in; in = h.y; --d; }
+                            if (before + in < rest) { before += in; in = h.x; --d; }
+                            // where all of the bin stay: those above the key before its first (there is one)
+                            ch.found = make_int3(lo + (d << s), before, before + in == rest && (prefix | uint32_t(lo + (d << s))));
+                        }
+                    }
+                    __syncthreads();
+                    lo = ch.found.x;
+                    over = ch.found.y;
+                    exact = ch.found.z;
                 }
-                if (!exact && hi <= (uint64_t(prefix) | ~bin)) over = reach(uint32_t(hi));       // those above lo
-                if (threadIdx.x == 0) {
-                    ch.prefix = uint32_t(exact ? lo - 1 : lo);
-                    ch.rest = exact ? 0 : rest - over;
+                if (threadIdx.x < kParts) {
+                    ChooseShared* to = kParts > 1 ? cl.map_shared_rank(&ch, threadIdx.x) : &ch;
+                    to->prefix = prefix + uint32_t(lo) - (exact ? 1u : 0u);
+                    to->rest = exact ? 0 : rest - over;
                 }
             }
             sync_all();
-            prefix = lead->prefix;
-            rest = lead->rest;
+            prefix = ch.prefix;
+            rest = ch.rest;
             break;
         }
     }
     // keys above prefix stay, and the first `rest` equal ones
-    auto verdicts = [&](uint32_t& stay, uint32_t& tie) {
+    uint32_t stay, tie;
+    int total, before = 0;                       // those above prefix in the high half, equal ones in the low
+    auto count = [&]() {
         stay = there & ~runs;
         tie = 0;
-        if (!by_weight || runs == 0) return;
+        if (by_weight && runs) {
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-            stay |= uint32_t(key[e] > prefix) << e & runs;
-            tie |= uint32_t(key[e] == prefix) << e & runs;
+            for (int e = 0; e < kRun; ++e) {
+                stay |= uint32_t(key[e] > prefix) << e & runs;
+                tie |= uint32_t(key[e] == prefix) << e & runs;
+            }
         }
+        before = cta_scan(__popc(stay) << 16 | __popc(tie), sh, turn, &total);
     };
-    int64_t at = 0, tied = 0;
-    uint32_t stay, tie;
+    int64_t at = 0, tied = 0;                    // before the tile
     if (kParts > 1) {
-        int above = 0, ties = 0;
+        int2 mine = make_int2(0, 0);
         for (int64_t base = s0; base < s1; base += kTile) {
             if (!one_tile) load(base);
-            int total;
-            verdicts(stay, tie);
-            cta_scan(__popc(stay), sh, turn, &total);
-            above += total;
-            cta_scan(__popc(tie), sh, turn, &total);
-            ties += total;
+            count();
+            mine.x += total >> 16;
+            mine.y += total & 0xffff;
         }
-        if (threadIdx.x == 0) { ch.above = above; ch.ties = ties; }
-        cl.sync();
+        if (threadIdx.x < kParts) cl.map_shared_rank(&ch, threadIdx.x)->counts[part] = mine;
+        cl.sync();                               // (the last look at another CTA's memory is behind every CTA here)
         for (int r = 0; r < part; ++r) {
-            at += cl.map_shared_rank(&ch, r)->above;
-            tied += cl.map_shared_rank(&ch, r)->ties;
+            at += ch.counts[r].x;
+            tied += ch.counts[r].y;
         }
     }
     at += min(tied, int64_t(rest));
     for (int64_t base = s0; base < s1; base += kTile) {
         if (!one_tile) load(base);
-        verdicts(stay, tie);
-        // of the ties those that are among the first `rest`
-        int total;
-        const int64_t first = tied + cta_scan(__popc(tie), sh, turn, &total);
-        tied += total;
-        for (int64_t drop = first + __popc(tie) - max(int64_t(rest), first); drop > 0; --drop) tie ^= 1u << (31 - __clz(tie));
+        if (kParts == 1 || !one_tile) count();
+        const int64_t ties = tied + (before & 0xffff), done = min(tied, int64_t(rest));
+        int to = (before >> 16) + int(min(ties, int64_t(rest)) - done);
+        for (int64_t drop = ties + __popc(tie) - max(int64_t(rest), ties); drop > 0; --drop) tie ^= 1u << (31 - __clz(tie));
         stay |= tie;
-        int to = cta_scan(__popc(stay), sh, turn, &total);
         for (; stay; stay &= stay - 1) ch.stays[to++] = uint16_t(kRun * threadIdx.x + __ffs(stay) - 1);
+        tied += total & 0xffff;
+        const int n = (total >> 16) + int(min(tied, int64_t(rest)) - done);
         __syncthreads();
-        for (int i = threadIdx.x; i < total; i += kPlanThreads) kept[at + i] = int(base) + ch.stays[i];
-        at += total;
+        for (int i = threadIdx.x; i < n; i += kPlanThreads) kept[at + i] = int(base) + ch.stays[i];
+        at += n;
         __syncthreads();
     }
-    if (kParts > 1) cl.sync();                   // no CTA leaves while another reads its counts
 }
 
 }  // namespace

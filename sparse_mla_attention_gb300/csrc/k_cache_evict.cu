@@ -3,15 +3,17 @@
 // Of a sequence with more than `keep` positions the first `first`, the last `recent` and, of those between,
 // the R = keep - first - recent of largest weight stay (ties: the lower position; NaN counts least), in
 // the order of their positions, in fresh pages. The R-th largest weight is found by a radix descent over the
-// weights' bits (a histogram of 2048 bins, and a bisection among the weights of one bin as soon as they are few), so the
-// choice is exact and the same in every run.
+// weights' bits (a histogram of 2048 bins, and steps of seven bits among the weights of one bin as soon as they are
+// few), so the choice is exact and the same in every run.
 //
 // Bound: the copies by HBM, the choice by latency. 64 sequences of up to 8192 positions to 2048 each, pages and
-// blocks of 64: 46 us with a free of the last call's pages, of which the copies take 24 (134 MB read and written: 5.6
-// TB/s), the choice 9 and the free 4; 3 of up to 81920 to 16384: 38 us, 14 and 18 and 4; one of 1500 to 1024: 17 us. The choice of
-// a sequence in one CTA: weights into registers 1 us, histogram 1, its scan 0.5, collecting the bin 1.4,
-// bisection 0.8, the list 1.9. Three histograms instead of the bisection: 50 us, 49 with a cluster; rows looked up by
-// the choice instead of the copies: 50.
+// blocks of 64: 44 us with a free of the last call's pages, of which the copies take 24 (134 MB read and written: 5.6
+// TB/s), the choice 7 and the free 4; 3 of up to 81920 to 16384: 32 us, 14 and 11 and 3; one of 1500 to 1024: 16 us. The
+// choice of a sequence in one CTA: weights into registers 1.1 us, histogram 0.9, its scan 0.4, collecting the bin 1,
+// seven bits a step 0.7, the list 1.8; in eight, of 81920: 1.2 and 0.4 for the first barrier, 1.3, 0.5 joined, 0.8, 1.1,
+// 0.9 joined, 1.2, 0.4, the counts 1.4, the list 1.2. Bisection of the few, a count and a barrier a step: 46 and 38 us (with
+// lists gathered twice); bins read by every CTA from the first: 36 for the long ones. Three full histograms: 50 and 49
+// us; rows looked up by the choice instead of the copies: 50.
 //
 // evict_plan_kernel: cluster 0 grants the free pages, the other CTAs choose, one sequence each.
 // evict_copy_kernel: moves the rows. A block's scale is the largest of its rows'
@@ -427,8 +429,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
     }
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // A sequence has one CTA, whose registers hold 16384 weights; wider tables give it a cluster. Both sides, device time:
-    // 3 of 81920 68 us with one CTA each (it goes over its weights tile by tile), 38 with a cluster; 64 of 8192 47 and 113
-    // (512 CTAs take turns), one of 1500 17 and 23.
+    // 3 of 81920 61 us with one CTA each (it goes over its weights tile by tile), 32 with a cluster; 64 of 8192 44 and 83
+    // (512 CTAs take turns), one of 1500 16 and 18.
     const int parts = (int64_t(a.max_pages) << a.cache.page_shift) > 16384 ? kPlanCtas : 1;
     const unsigned grid = unsigned(kPlanCtas + (int64_t(a.B) * parts + kPlanCtas - 1) / kPlanCtas * kPlanCtas);
     if (parts > 1) evict_plan_kernel<kPlanCtas><<<grid, kPlanThreads, sizeof(ChooseShared), s>>>(a);

@@ -309,6 +309,32 @@ def test_evict_by_odd_weights():
     pool.check(cache)
 
 
+def _crowded(rng, shape, kind):
+    """Weights that differ in their last bits only: all in one of the 2048 widest bins (kind 21), all alike but for 10
+    bits (kind 10), or half and half, so that the last one to stay can be in either."""
+    bits = np.float32(1.0).view(np.int32) + rng.integers(0, 1 << min(kind, 21), size=shape)
+    if kind == 22:
+        low = rng.random(shape) < 0.5
+        bits[low] = np.float32(0.75).view(np.int32) + rng.integers(0, 1 << 10, size=int(low.sum()))
+    return bits.astype(np.int32).view(np.float32)
+
+
+@pytest.mark.parametrize("kind", [10, 21, 22])
+@pytest.mark.parametrize("lens,keep", [([16384, 9000, 5000, 4097], 1), ([16000, 8300, 5000, 4100], 2500),
+                                       ([16384, 16383, 12001], 8191), ([60000, 30001], 11111), ([140003, 131072], 70001),
+                                       ([140003], 9)])
+def test_evict_by_crowded_weights(lens, keep, kind):
+    rng = np.random.default_rng(keep + kind)
+    pool = Pool(7000, 64, 64, seed=38, junk=False)
+    table = pool.place(lens)
+    _evict_and_check(pool, table, lens, _crowded(rng, (len(lens), table.shape[1] * 64), kind), keep, 0, 0)
+    w = -_crowded(rng, (len(lens), table.shape[1] * 64), kind)
+    w[:, 5::7] = np.nan
+    pool = Pool(7000, 64, 64, seed=39, junk=False)
+    table = pool.place(lens)
+    _evict_and_check(pool, table, lens, w, keep, min(keep, 3), 0)
+
+
 def test_evict_many_sequences():
     rng = np.random.default_rng(18)
     lens = rng.integers(0, 200, size=700)

@@ -423,7 +423,8 @@ int smla_cache_workspace_size(const smla_cache* cache, int32_t n, size_t* bytes)
  * result is the same in every run.
  * On the device: lens[t] outside [0, max_pages * page_size] is clamped, a sequence whose entries of cu
  * are out of order or range has no tokens (others that share tokens with it are unspecified), and a
- * position without a page of the pool gets nothing added; each sets SMLA_ERR_INDEX. workspace: smla_weights_workspace_size() bytes.
+ * position without a page of the pool gets nothing added; each sets SMLA_ERR_INDEX. workspace:
+ * smla_weights_workspace_size() bytes.
  */
 int smla_cache_weights(const uint16_t* q, const smla_cache* cache, const int32_t* table, const int32_t* cu,
                        const int32_t* lens, const float* lse, const float* earlier, float decay, float* weights,

@@ -119,8 +119,10 @@ __device__ void choose(const EvictArgs& a, int b, int part, PlanShared& sh, Choo
         for (int i = threadIdx.x; i < 3 * kDigits; i += kPlanThreads) (&ch.all[0][0])[i] = 0;
     if (one_tile) load(s0);
     uint32_t prefix = 0;
+    // Another CTA's shared memory exists once that CTA runs: every sequence waits for all of its CTAs, those whose
+    // choice needs no weights too (they write their counts to the others below).
+    if (kParts > 1) cl.sync();
     if (by_weight) {                             // (the same in every CTA of the sequence)
-        if (kParts > 1) cl.sync();
         ChooseShared* lead = kParts > 1 ? cl.map_shared_rank(&ch, 0) : &ch;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {

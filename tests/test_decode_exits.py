@@ -1,0 +1,29 @@
+"""What the decode calls' kernels must do where it cannot be run: a look at another CTA's shared memory before that CTA
+has started would fault, and a copy that never comes is not to be had. The sources are looked at."""
+
+import os
+import re
+
+from sparse_mla_attention_gb300 import build
+
+
+def _source(name):
+    with open(os.path.join(build.CSRC, name)) as f:
+        return f.read()
+
+
+def _depth(text):
+    """How many braces are open at the end of text."""
+    return text.count("{") - text.count("}")
+
+
+def test_evictions_clusters_meet_before_they_write_to_each_other():
+    text = _source("k_cache_evict.cu")
+    body = text[text.index("__device__ void choose("):]
+    body = body[body.index("{"):body.index("\n}\n")]
+    # the lambda that joins a CTA or a cluster is no barrier yet
+    remote = re.search(r"map_shared_rank\(", body).start()
+    meet = [m.start() for m in re.finditer(r"\n    if \(kParts > 1\) cl\.sync\(\);", body)]
+    assert meet and meet[0] < remote, "a CTA looks at another's shared memory that may not have started"
+    # in every sequence: not within a branch or a loop
+    assert _depth(body[:meet[0]]) == 1

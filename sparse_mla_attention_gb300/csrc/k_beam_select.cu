@@ -27,10 +27,11 @@ using namespace sm100;
 namespace {
 
 constexpr int kBsThreads = 256;
-constexpr int kBsVecs = 16, kBsGroup = 2;        // 16-byte vectors of a thread, beside one value at the row's ends; on their way together
+constexpr int kBsVecs = 16, kBsGroup = 2;        // 16-byte vectors of a thread; on their way together
 constexpr int kBsMergeThreads = 512;
 constexpr int kBsEach = 4;                       // candidates of a thread of the merge
 constexpr int kBsBatch = kBsMergeThreads * kBsEach;
+static_assert(SMLA_MAX_VOCAB / (kBsThreads * kBsVecs * 4) <= kBsMergeThreads, "a row's chunks are joined in one part");
 constexpr float kBsLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -70,7 +71,9 @@ template <>
 struct Logit<SMLA_F32> {
     static constexpr int kSize = 4;
     static constexpr uint32_t kNone = 0xff800000u;
-    static __device__ __forceinline__ float one(const uint8_t* p) { return __ldg(reinterpret_cast<const float*>(p)); }
+    static __device__ __forceinline__ void copy(uint4* to, int e, const uint8_t* row, int i, int V) {
+        reinterpret_cast<uint32_t*>(to)[e] = i < V ? __ldg(reinterpret_cast<const uint32_t*>(row) + i) : kNone;
+    }
     static __device__ __forceinline__ float top(const uint4& x) {
         return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
                      fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
@@ -84,8 +87,8 @@ template <>
 struct Logit<SMLA_BF16> {
     static constexpr int kSize = 2;
     static constexpr uint32_t kNone = 0xff80ff80u;
-    static __device__ __forceinline__ float one(const uint8_t* p) {
-        return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
+    static __device__ __forceinline__ void copy(uint4* to, int e, const uint8_t* row, int i, int V) {
+        reinterpret_cast<uint16_t*>(to)[e] = i < V ? __ldg(reinterpret_cast<const uint16_t*>(row) + i) : 0xff80u;
     }
     static __device__ __forceinline__ float top(const uint4& x) {
         auto as = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
@@ -102,8 +105,8 @@ template <>
 struct Logit<SMLA_F16> {
     static constexpr int kSize = 2;
     static constexpr uint32_t kNone = 0xfc00fc00u;
-    static __device__ __forceinline__ float one(const uint8_t* p) {
-        return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(p))));
+    static __device__ __forceinline__ void copy(uint4* to, int e, const uint8_t* row, int i, int V) {
+        reinterpret_cast<uint16_t*>(to)[e] = i < V ? __ldg(reinterpret_cast<const uint16_t*>(row) + i) : 0xfc00u;
     }
     static __device__ __forceinline__ float top(const uint4& x) {
         auto as = [](uint32_t w) { return *reinterpret_cast<const __half2*>(&w); };
@@ -122,7 +125,22 @@ struct Logit<SMLA_F16> {
 
 constexpr int chunk_of(int type) { return kBsThreads * kBsVecs * (type == SMLA_F32 ? 4 : 8); }
 // values that pass a chunk's bound at most: those of 2 n threads
-constexpr size_t passing(int type, int n) { return size_t(2) * n * (kBsVecs * (type == SMLA_F32 ? 4 : 8) + 1); }
+constexpr size_t passing(int type, int n) { return size_t(2) * n * kBsVecs * (type == SMLA_F32 ? 4 : 8); }
+
+// The 16 bytes from byte `off` of two vectors on; off is a multiple of kSize.
+template <int kSize>
+__device__ __forceinline__ uint4 cut(const uint4& lo, const uint4& hi, int off) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+    if (kSize < 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 __device__ __forceinline__ bool out_of_play(const BeamArgs& a, int row) {
     const float s = __ldg(a.scores + row);
@@ -131,53 +149,72 @@ __device__ __forceinline__ bool out_of_play(const BeamArgs& a, int row) {
 
 }  // namespace
 
-template <int kType>
-__global__ void __launch_bounds__(kBsThreads, 6)
+// kShift: rows may start between 16-byte boundaries.
+template <int kType, bool kShift>
+__global__ void __launch_bounds__(kBsThreads, kShift ? 4 : 6)
 beam_rows_kernel(const BeamArgs a) {
     constexpr int kSize = Logit<kType>::kSize, kEach = 16 / kSize;
     extern __shared__ __align__(16) unsigned long long best[];    // values that pass the bound
     __shared__ uint32_t warp_top[kBsThreads / 32], warp_low[kBsThreads / 32];
     __shared__ float2 warp_sum[kBsThreads / 32];
+    __shared__ uint4 ends[3];
     __shared__ int count;
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = int(blockIdx.x), chunk = int(blockIdx.y);
     if (out_of_play(a, row)) return;             // (nobody looks at its lists)
+    // Vector v of a row is its values from kEach * v on, wherever they lie: what is added to what goes by the values'
+    // indices alone, and equal rows have equal sums. A vector between two boundaries is cut from two aligned ones.
+    // [from, to) are the vectors that can be, without a look outside of the row; its others, at most one at its start and
+    // two at its end, come value by value into `ends`.
     const uint8_t* base = static_cast<const uint8_t*>(a.logits) + int64_t(row) * a.stride * kSize;
-    // the row from its first 16-byte boundary on as vectors; threads of the first and the last chunk take what is
-    // before and behind them, a value each
-    int lead = int((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / kSize;
-    if (lead > a.V) lead = a.V;
-    const int vecs = (a.V - lead) / kEach, tail = a.V - lead - vecs * kEach;
-    const int first = chunk * kBsThreads * kBsVecs + int(threadIdx.x);
-    const uint4* src = reinterpret_cast<const uint4*>(base + lead * kSize) + first;
+    const int off = kShift ? int(reinterpret_cast<uintptr_t>(base) & 15) : 0;
+    const int vecs = (a.V + kEach - 1) / kEach, from = off ? 1 : 0;
+    const int to = max(from, kShift ? (a.V * kSize + off) / 16 - 1 : a.V / kEach);
+    const int chunk0 = chunk * kBsThreads * kBsVecs, first = chunk0 + int(threadIdx.x);
+    const uint4* src = reinterpret_cast<const uint4*>(base - off) + first;
     constexpr uint32_t kNone = Logit<kType>::kNone;
-    float x = -INFINITY;
-    int xi = -1;
-    if (chunk == 0 && threadIdx.x < lead) xi = threadIdx.x;
-    if (chunk == a.chunks - 1 && threadIdx.x >= kBsThreads - tail) xi = a.V - (kBsThreads - int(threadIdx.x));
-    if (xi >= 0) x = Logit<kType>::one(base + int64_t(xi) * kSize);
+    const uint4 none4 = make_uint4(kNone, kNone, kNone, kNone);
+    uint4 raw[2][kBsGroup][kShift ? 2 : 1];
+    auto load = [&](int g) {
+#pragma unroll
+        for (int k = 0; k < kBsGroup; ++k) {
+            const int at = (g * kBsGroup + k) * kBsThreads;
+            const bool whole = first + at >= from && first + at < to;
+#pragma unroll
+            for (int h = 0; h < (kShift ? 2 : 1); ++h) raw[g & 1][k][h] = whole ? __ldg(src + at + h) : none4;
+        }
+    };
+    load(0);
+    uint32_t odd = 0;                            // which of the thread's vectors are in `ends`
+    if (first < from) odd = 1;
+#pragma unroll
+    for (int i = 0; i < (kShift ? 2 : 1); ++i) {
+        const int d = to + i - first;
+        if (to + i < vecs && d >= 0 && d % kBsThreads == 0 && d < kBsThreads * kBsVecs) odd |= 1u << (d / kBsThreads);
+    }
+    auto slot = [&](int v) { return !kShift ? 1 : v < from ? 0 : 1 + v - to; };
+    if (threadIdx.x < 3 * kEach) {
+        const int i = threadIdx.x / kEach, e = threadIdx.x % kEach, v = i ? to + i - 1 : 0;
+        if ((i || from) && v >= chunk0 && v < min(vecs, chunk0 + kBsThreads * kBsVecs))
+            Logit<kType>::copy(ends + i, e, base, v * kEach + e, a.V);
+    }
+    __syncthreads();
 
     // A thread's largest value and its sum of exponentials relative to it, which follow each other from group to group
     // (two values at a time); the largest of each vector.
     const uint64_t log2e = pair_of(kBsLog2e, kBsLog2e);
-    float tops[kBsVecs], top = x, sum = xi >= 0 ? (x == -INFINITY ? 0.f : x - x + 1.f) : 0.f;       // (NaN for NaN and inf)
-    uint4 raw[2][kBsGroup];
-    auto load = [&](int g, uint4 (&to)[kBsGroup]) {
-#pragma unroll
-        for (int k = 0; k < kBsGroup; ++k) {
-            const int v = (g * kBsGroup + k) * kBsThreads;
-            to[k] = first + v < vecs ? __ldg(src + v) : make_uint4(kNone, kNone, kNone, kNone);
-        }
-    };
-    load(0, raw[0]);
+    float tops[kBsVecs], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int g = 0; g < kBsVecs / kBsGroup; ++g) {
-        uint4 (&now)[kBsGroup] = raw[g & 1];
-        if (g + 1 < kBsVecs / kBsGroup) load(g + 1, raw[(g + 1) & 1]);
+        uint4 now[kBsGroup];
+        if (g + 1 < kBsVecs / kBsGroup) load(g + 1);
         float high = top;                        // (maxima pass over NaN)
 #pragma unroll
         for (int k = 0; k < kBsGroup; ++k) {
+            const int i = g * kBsGroup + k;
+            now[k] = kShift ? cut<kSize>(raw[g & 1][k][0], raw[g & 1][k][kShift], off) : raw[g & 1][k][0];
+            if ((odd >> i) & 1) now[k] = ends[slot(first + i * kBsThreads)];
             tops[g * kBsGroup + k] = Logit<kType>::top(now[k]);
             high = fmaxf(high, tops[g * kBsGroup + k]);
         }
@@ -199,7 +236,6 @@ beam_rows_kernel(const BeamArgs a) {
         const float2 both = floats_of(add2(part[0], part[1]));
         sum += both.x + both.y;
     }
-    if (top != top) top = -INFINITY;
     const uint32_t mine = order_of(top + 0.f);   // (both zeros alike)
     const uint32_t wt = __reduce_max_sync(0xffffffffu, mine), wl = __reduce_min_sync(0xffffffffu, mine);
     if (lane == 0) { warp_top[warp] = wt; warp_low[warp] = wl; }
@@ -220,12 +256,14 @@ beam_rows_kernel(const BeamArgs a) {
 #pragma unroll 1
         for (; which; which &= which - 1) {
             const int k = __ffs(which) - 1;
-            const uint4 again = __ldg(src + k * kBsThreads);
+            const int at = k * kBsThreads;
+            uint4 again;
+            if ((odd >> k) & 1) again = ends[slot(first + at)];
+            else again = kShift ? cut<kSize>(__ldg(src + at), __ldg(src + at + 1), off) : __ldg(src + at);
             float v[kEach];
             Logit<kType>::spread(again, v);
-            const int place = lead + (first + k * kBsThreads) * kEach;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) each(v[e], place + e);
+            for (int e = 0; e < kEach; ++e) each(v[e], (first + at) * kEach + e);
         }
     };
     // The bound: threads whose largest value reaches it number n to 2n. Where many threads' are equal to it, their
@@ -244,10 +282,7 @@ beam_rows_kernel(const BeamArgs a) {
             const int over = __syncthreads_count(mine > bound);
             const float at = value_of(bound);
             int place = INT32_MAX;               // of the thread's first value that is equal
-            if (mine == bound) {
-                if (x == at) place = xi;
-                look([&](float y, int i) { if (y == at) place = min(place, i); }, at);
-            }
+            if (mine == bound) look([&](float y, int i) { if (y == at) place = min(place, i); }, at);
             int lo = -1, hi = a.V - 1;           // too few up to lo, enough up to hi
             until = hi;
             while (hi - lo > 1 && reached > 2 * n) {
@@ -263,7 +298,6 @@ beam_rows_kernel(const BeamArgs a) {
             if (y != y || !(o > bound || (o == bound && i <= until))) return;
             best[atomicAdd(&count, 1)] = (static_cast<unsigned long long>(o) << 32) | (0xffffffffu - uint32_t(i));
         };
-        if (xi >= 0) pass(x, xi);
         look(pass, value_of(bound));
     }
     // the threads' sums, relative to the chunk's largest, with what each addition rounds off beside them (64-bit
@@ -309,7 +343,7 @@ __global__ void __launch_bounds__(kBsMergeThreads)
 beam_merge_kernel(const BeamArgs a) {
     __shared__ double lse[SMLA_MAX_BEAMS], before[SMLA_MAX_BEAMS];
     __shared__ int state[SMLA_MAX_BEAMS];        // 0: runs, 1: ended, 2: dead
-    __shared__ float peaks[kBsMergeThreads], row_peak[SMLA_MAX_BEAMS + 1];
+    __shared__ float peaks[kBsMergeThreads], row_peak[SMLA_MAX_BEAMS];
     __shared__ double sums[kBsMergeThreads];
     __shared__ float warp_bar[kBsMergeThreads / 32];
     __shared__ unsigned long long keys[kBsBatch];
@@ -340,38 +374,31 @@ beam_merge_kernel(const BeamArgs a) {
         state[k] = !(fabsf(s) < INFINITY) ? 2 : a.done && __ldg(a.done + row0 + k) ? 1 : 0;
     }
     const int lists = a.K * a.chunks;
-    for (int l0 = 0; l0 < lists; l0 += kBsMergeThreads) {
-        // whole rows at a time; a row of more chunks than threads goes on from part to part
-        const int l = l0 + int(threadIdx.x);
-        if (l < lists) {
+    const int part = kBsMergeThreads / a.chunks * a.chunks;              // whole rows: all sums are made alike
+    for (int l0 = 0; l0 < lists; l0 += part) {
+        const int l = l0 + int(threadIdx.x), l1 = min(l0 + part, lists);
+        if (l < l1) {
             peaks[threadIdx.x] = __ldcg(a.peaks + row0 * a.chunks + l);
             sums[threadIdx.x] = __ldcg(a.sums + row0 * a.chunks + l);
         }
         __syncthreads();
-        const int k0 = l0 / a.chunks, k1 = (min(l0 + kBsMergeThreads, lists) - 1) / a.chunks;
-        // a row's peak over the part: a thread a row
-        if (k0 + int(threadIdx.x) <= k1) {
-            const int k = k0 + int(threadIdx.x), i0 = max(k * a.chunks, l0), i1 = min(min((k + 1) * a.chunks, lists), l0 + kBsMergeThreads);
+        const int k0 = l0 / a.chunks, i0 = int(threadIdx.x) * a.chunks;  // a row's peak and sum: a thread a row
+        const bool mine = k0 + int(threadIdx.x) < l1 / a.chunks;
+        if (mine) {
             float peak = -INFINITY;
-            for (int i = i0; i < i1; ++i) peak = fmaxf(peak, peaks[i - l0]);
-            row_peak[k - k0] = peak;
+            for (int i = i0; i < i0 + a.chunks; ++i) peak = fmaxf(peak, peaks[i]);
+            row_peak[threadIdx.x] = peak;
         }
         __syncthreads();
-        if (l < lists) {
-            const float peak = peaks[threadIdx.x], most = row_peak[l / a.chunks - k0];
+        if (l < l1) {
+            const float peak = peaks[threadIdx.x], most = row_peak[threadIdx.x / a.chunks];
             if (peak != most) sums[threadIdx.x] *= exp(double(peak) - double(most));
         }
         __syncthreads();
-        if (k0 + int(threadIdx.x) <= k1) {
-            const int k = k0 + int(threadIdx.x), i0 = max(k * a.chunks, l0), i1 = min(min((k + 1) * a.chunks, lists), l0 + kBsMergeThreads);
+        if (mine) {
             double sum = 0.0;
-            for (int i = i0; i < i1; ++i) sum += sums[i - l0];
-            sum = double(row_peak[k - k0]) + log(sum);
-            if (i0 > k * a.chunks) {             // joined to the parts before
-                const double x = fmax(lse[k], sum), y = fmin(lse[k], sum);
-                sum = lse[k] != lse[k] || sum != sum ? lse[k] + sum : y == -INFINITY ? x : x + log1p(exp(y - x));
-            }
-            lse[k] = sum;
+            for (int i = i0; i < i0 + a.chunks; ++i) sum += sums[i];
+            lse[k0 + threadIdx.x] = double(row_peak[threadIdx.x]) + log(sum);
         }
         __syncthreads();
     }
@@ -467,19 +494,27 @@ BeamPlan plan_beam(int64_t rows, int V, int n, int type) {
     return p;
 }
 
-template <int kType>
+template <int kType, bool kShift>
 cudaError_t launch_rows(const BeamArgs& a, cudaStream_t s) {
     static bool attr_done[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(beam_rows_kernel<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(beam_rows_kernel<kType, kShift>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    int(passing(kType, SMLA_MAX_BEAMS) * 8));
         if (e != cudaSuccess) return e;
         attr_done[dev] = true;
     }
-    beam_rows_kernel<kType><<<dim3(unsigned(a.B) * a.K, a.chunks), kBsThreads, passing(kType, a.n) * 8, s>>>(a);
+    beam_rows_kernel<kType, kShift><<<dim3(unsigned(a.B) * a.K, a.chunks), kBsThreads, passing(kType, a.n) * 8, s>>>(a);
     return cudaGetLastError();
+}
+
+template <int kType>
+cudaError_t launch_rows(const BeamArgs& a, cudaStream_t s) {
+    const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                         (int64_t(a.B) * a.K == 1 || a.stride * Logit<kType>::kSize % 16 == 0);
+    return aligned ? launch_rows<kType, false>(a, s) : launch_rows<kType, true>(a, s);
 }
 
 }  // namespace

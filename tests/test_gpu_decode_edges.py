@@ -23,3 +23,43 @@ def test_evict_of_sequences_without_a_choice_in_wide_tables(lens, keep, first, r
     table = pool.place(lens)
     assert table.shape[1] * 64 > 16384
     _evict_and_check(pool, table, lens, _heavy(rng, len(lens), table.shape[1] * 64), keep, first, recent)
+
+
+# ------------------------------------------------------------------------------------------------ beams
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def _picked(x, scores, n):
+    got = _smla().beam_select(x, _f32(scores), n=n)
+    return _np(got[0]), _np(got[1]), got[2].double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,pad", [(1, 0), (3, 0), (7, 0), (9, 0), (17, 0), (31, 2), (9001, 0), (9000, 1), (9000, 3), (16385, 0),
+                                   (32001, 0), (32767, 0), (32769, 0), (50001, 0), (50257, 5), (65537, 0), (151665, 0)])
+def test_equal_beams_in_rows_of_any_alignment(dtype, V, pad):
+    # equal rows have equal log-sums wherever they start: of equal candidates the lower beam's comes first
+    g = torch.Generator(device=DEV).manual_seed(V)
+    one = torch.randn(3, 1, V, generator=g, device=DEV) * 3
+    x = torch.full((24, V + pad), 50.0, device=DEV)
+    x[:, :V] = one.expand(3, 8, V).reshape(24, V)
+    x = x.to(dtype)[:, :V]
+    scores = np.repeat(-np.arange(3.0)[:, None], 8, 1)
+    for n in (8, 20):
+        p, t, s = _picked(x, scores, n)
+        ref = M.select(x.double().cpu().numpy(), scores, n)
+        np.testing.assert_array_equal(p, ref[0])
+        np.testing.assert_array_equal(t, ref[1])
+        for b in range(3):                             # a token's scores are the same number
+            for v in set(t[b].tolist()):
+                assert len(set(s[b][t[b] == v].tolist())) == 1
+
+
+@pytest.mark.parametrize("K,V", [(64, 151936), (60, 200001), (3, 4194304)])
+def test_equal_beams_of_more_chunks_than_a_part(K, V):
+    g = torch.Generator(device=DEV).manual_seed(K)
+    x = (torch.randn(1, V, generator=g, device=DEV) * 3).expand(K, V).contiguous()
+    p, t, _ = _picked(x, np.zeros((1, K)), 64)
+    best = torch.sort(x[0], descending=True, stable=True)[1][:64].tolist()
+    want = [(k, v) for v in best for k in range(K)][:64]
+    assert list(zip(p[0].tolist(), t[0].tolist())) == want

@@ -337,6 +337,13 @@ __device__ __forceinline__ float float_below(unsigned long long key) {
     return __double2float_rd(__longlong_as_double(key >> 63 ? key ^ (1ull << 63) : ~key));
 }
 
+// Where a candidate of beam k stands among those of equal scores: by beam, then by its logit (a score of a large size
+// rounds off what tells a beam's logits apart), then by token.
+__device__ __forceinline__ unsigned long long place_of(int k, uint32_t order, int v) {
+    static_assert(SMLA_MAX_VOCAB == 1 << 22 && SMLA_MAX_BEAMS <= 1 << 10, "22 bits of token, 32 of logit, 10 of beam");
+    return static_cast<unsigned long long>(k) << 54 | static_cast<unsigned long long>(~order) << 22 | uint32_t(v);
+}
+
 // A group's n best out of its rows' chunks' lists (each best first), 2048 candidates less the n best so far at a time:
 // the n-th of a list has n - 1 better ones, so nothing below the best n-th matters; the rest rank by counting.
 __global__ void __launch_bounds__(kBsMergeThreads)
@@ -347,9 +354,10 @@ beam_merge_kernel(const BeamArgs a) {
     __shared__ double sums[kBsMergeThreads];
     __shared__ float warp_bar[kBsMergeThreads / 32];
     __shared__ unsigned long long keys[kBsBatch];
-    __shared__ int flats[kBsBatch];
+    __shared__ unsigned long long places[kBsBatch];
     __shared__ unsigned long long top_keys[SMLA_MAX_BEAMS];
-    __shared__ int top_flats[SMLA_MAX_BEAMS], count;
+    __shared__ unsigned long long top_places[SMLA_MAX_BEAMS];
+    __shared__ int count;
     grid_dep_wait();
     const int b = int(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (b == 0 && threadIdx.x == 0) *a.status = 0;
@@ -433,34 +441,34 @@ beam_merge_kernel(const BeamArgs a) {
             if (high[e] >= bar) {
                 const int at = atomicAdd(&count, 1);
                 keys[at] = raw[e];
-                flats[at] = base + e * kBsMergeThreads + int(threadIdx.x);
+                places[at] = base + e * kBsMergeThreads + int(threadIdx.x);
             }
         if (base + batch < total) read(base + batch);
         __syncthreads();
         // those in 64 bits; one that is not finite is 0, below all
         for (int i = threadIdx.x; i < count; i += kBsMergeThreads) {
             const unsigned long long was = keys[i];
-            const int list = flats[i] / n, k = list / a.chunks;
+            const int list = int(places[i]) / n, k = list / a.chunks;
             const bool ended = state[k] != 0;
             const double s = ended ? before[k] : before[k] + (double(value_of(uint32_t(was >> 32))) - lse[k]);
             const long long bits = __double_as_longlong(s + 0.0);
             keys[i] = !(fabs(s) < INFINITY) ? 0 : bits < 0 ? ~bits : bits | (1ll << 63);
-            flats[i] = k * a.V + (ended ? a.eos : int(0xffffffffu - uint32_t(was)));
+            places[i] = place_of(k, ended ? 0u : uint32_t(was >> 32), ended ? a.eos : int(0xffffffffu - uint32_t(was)));
         }
         __syncthreads();
         if (threadIdx.x < have) {
             const int at = atomicAdd(&count, 1);
             keys[at] = top_keys[threadIdx.x];
-            flats[at] = top_flats[threadIdx.x];
+            places[at] = top_places[threadIdx.x];
         }
         __syncthreads();
         const int c = count;
         for (int i = threadIdx.x; i < c; i += kBsMergeThreads) {
             const unsigned long long mine = keys[i];
-            const int place = flats[i];
+            const unsigned long long place = places[i];
             int rank = 0;
-            for (int j = 0; j < c; ++j) rank += keys[j] > mine || (keys[j] == mine && flats[j] < place);
-            if (rank < n) { top_keys[rank] = mine; top_flats[rank] = place; }
+            for (int j = 0; j < c; ++j) rank += keys[j] > mine || (keys[j] == mine && places[j] < place);
+            if (rank < n) { top_keys[rank] = mine; top_places[rank] = place; }
         }
         __syncthreads();
         have = c < n ? c : n;
@@ -469,11 +477,11 @@ beam_merge_kernel(const BeamArgs a) {
     if (threadIdx.x < n) {
         const int64_t at = int64_t(b) * n + threadIdx.x;
         const bool any = threadIdx.x < have;
-        const int f = any ? top_flats[threadIdx.x] : 0;
+        const unsigned long long place = any ? top_places[threadIdx.x] : 0;
         const unsigned long long key = any ? top_keys[threadIdx.x] : 0;
         const double s = __longlong_as_double(key >> 63 ? key ^ (1ull << 63) : ~key);
-        a.parents[at] = any ? int(row0) + f / a.V : -1;
-        a.tokens[at] = any ? f % a.V : -1;
+        a.parents[at] = any ? int(row0) + int(place >> 54) : -1;
+        a.tokens[at] = any ? int(place & (SMLA_MAX_VOCAB - 1)) : -1;
         a.new_scores[at] = any ? float(s) : -INFINITY;
     }
 }

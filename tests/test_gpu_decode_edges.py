@@ -63,3 +63,32 @@ def test_equal_beams_of_more_chunks_than_a_part(K, V):
     best = torch.sort(x[0], descending=True, stable=True)[1][:64].tolist()
     want = [(k, v) for v in best for k in range(K)][:64]
     assert list(zip(p[0].tolist(), t[0].tolist())) == want
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("before", [-1e9, -1e20, 1e20, float(np.finfo(np.float32).min)])
+def test_beams_of_huge_scores_go_by_their_logits(dtype, before):
+    # in 64 bits such a beam's scores are equal or nearly so: what its logits say still holds
+    g = torch.Generator(device=DEV).manual_seed(7)
+    x = (torch.randn(4, 40001, generator=g, device=DEV)).to(dtype)
+    x[3] = x[2]
+    scores = np.array([[before] * 2, [before * 2 if abs(before) < 1e30 else before, before]])
+    n = 12
+    p, t, _ = _picked(x, scores, n)
+    v = x.double().cpu().numpy()
+    for b in range(2):
+        s = scores[b].astype(np.float32).astype(np.float64)
+        lse = [np.log(np.exp(v[2 * b + k]).sum()) for k in range(2)]
+        cand = []
+        for k in range(2):
+            order = np.lexsort((np.arange(v.shape[1]), -v[2 * b + k]))[:n]
+            cand += [(-(s[k] + (v[2 * b + k, i] - lse[k])), k, -v[2 * b + k, i], i) for i in order]
+        if before == -1e9:                             # (scores apart by less than the log-sums' own error are not held apart)
+            got = [(a, c) for a, c in zip(p[b], t[b])]
+            for k in range(2):
+                mine = [c for a, c in got if a == 2 * b + k]
+                order = np.lexsort((np.arange(v.shape[1]), -v[2 * b + k]))
+                assert mine == order[:len(mine)].tolist()
+        else:
+            want = [(2 * b + k, i) for _, k, _, i in sorted(cand)[:n]]
+            assert list(zip(p[b].tolist(), t[b].tolist())) == want

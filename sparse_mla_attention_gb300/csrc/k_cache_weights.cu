@@ -663,17 +663,18 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
         bool ok = true, bad = false;
         while (ok && w.next(p)) {
             const int64_t line = w.b * width;
-            // This thread's position of a tile: its page, two of the team's tiles ahead, its block scale (-1: none), one
-            // ahead, so that no load is waited for.
+            // This thread's position of a tile: its page, two of the team's tiles ahead, its block scale and whether it
+            // has a row, one ahead, so that no load is waited for.
+            auto seen_in = [&](int k) { return k < w.k1 && int64_t(k) * kCwTile + 32 * quarter + lane < w.seen; };
             auto page_of = [&](int k) {
                 const int64_t pos = int64_t(k) * kCwTile + 32 * quarter + lane;
-                return k < w.k1 && pos < w.seen ? __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift)) : INT32_MAX;
+                return seen_in(k) ? __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift)) : -1;
             };
+            bool next_there = false;
             auto scale_of = [&](int k, int page) {
-                if (page < 0 || page >= c.num_pages) {
-                    bad |= page != INT32_MAX;
-                    return -1.f;
-                }
+                next_there = page >= 0 && page < c.num_pages;            // (a page was looked up for positions that are seen)
+                bad |= !next_there && seen_in(k);
+                if (!next_there) return 0.f;
                 const int64_t pos = int64_t(k) * kCwTile + 32 * quarter + lane;
                 return __ldg(c.scales + (((page << c.page_shift) + int(pos & page_mask)) >> c.block_shift));
             };
@@ -701,6 +702,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
                     const bool own = ((k - w.k0) & 1) == team;
                     const int64_t pos = int64_t(k) * kCwTile + 32 * quarter + lane;
                     const float scale = next_scale;
+                    const bool there = next_there;
                     float before = 0.f;
                     if (own) {
                         if (pos < w.seen && keep != 0.f) before = base[line + pos];
@@ -743,7 +745,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.t_empty[buf]);
-                    if (pos < w.seen) a.weights[line + pos] = fmaf(before, keep, scale >= 0.f ? sum : 0.f);
+                    if (pos < w.seen) a.weights[line + pos] = fmaf(before, keep, there ? sum : 0.f);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.f_empty[f]);
@@ -950,15 +952,20 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
                 const int tiles = w.width(k), j0 = w.from(k), j1 = w.to(k);
                 const int64_t pos0 = int64_t(k) * (kCwLTiles * kCwTile) + row_in;
                 float scale[kCwLTiles], sum[kCwLTiles];
+                uint32_t there = 0;              // a bit a tile: the position has a row
 #pragma unroll
                 for (int i = 0; i < kCwLTiles; ++i) {
                     const int64_t pos = pos0 + i * kCwTile;
-                    scale[i] = -1.f;             // (no row)
+                    scale[i] = 0.f;
                     sum[i] = 0.f;
                     if (i >= tiles || pos >= w.seen) continue;
                     const int page = __ldg(a.table + int64_t(w.b) * a.max_pages + (pos >> c.page_shift));
-                    if (page < 0 || page >= c.num_pages) bad = true;
-                    else scale[i] = __ldg(c.scales + (((page << c.page_shift) + int(pos & page_mask)) >> c.block_shift));
+                    if (page < 0 || page >= c.num_pages) {
+                        bad = true;
+                        continue;
+                    }
+                    there |= 1u << i;
+                    scale[i] = __ldg(c.scales + (((page << c.page_shift) + int(pos & page_mask)) >> c.block_shift));
                 }
                 // the blocks of 128 columns in turn, a team every other one
                 for (int i = 0; i < 4 * tiles && ok; ++i, ++x_use) {
@@ -1045,7 +1052,7 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
                     for (int i = 0; i < kCwLTiles; ++i) {
                         if (i >= tiles || !ok) continue;
                         const int64_t pos = pos0 + i * kCwTile;
-                        const float both = scale[i] >= 0.f ? sum[i] + sh.sums[i][row_in] : 0.f;
+                        const float both = (there >> i) & 1 ? sum[i] + sh.sums[i][row_in] : 0.f;
                         if (j0 > 0 || j1 < w.chunks) {
                             p.parts[((2 * blockIdx.x + (j0 > 0 ? 0 : 1)) * kCwLTiles + i) * kCwTile + row_in] = both;
                         } else if (pos < w.seen) {

@@ -92,3 +92,48 @@ def test_beams_of_huge_scores_go_by_their_logits(dtype, before):
         else:
             want = [(2 * b + k, i) for _, k, _, i in sorted(cand)[:n]]
             assert list(zip(p[b].tolist(), t[b].tolist())) == want
+
+
+# ------------------------------------------------------------------------------------------------ weights
+@pytest.mark.parametrize("counts", [[1, 1, 1], [40, 1, 40]])           # few rows of q a sequence, and many
+def test_weights_report_every_page_out_of_range_and_take_any_scale(counts):
+    from sparse_mla_attention_gb300 import SmlaError, _lib
+    smla = _smla()
+    rng = np.random.default_rng(10)
+    pool = Pool(60, 16, 16, seed=11)
+    full = [300, 45, 130]
+    table = pool.place(full)
+    pool.fill(table, full)
+    cu = np.concatenate([[0], np.cumsum(counts)])
+    lens = [n - c + 1 + i for n, c in zip(full, counts) for i in range(c)]
+    T, W = len(lens), table.shape[1] * 16
+    q = bf16(rng.standard_normal((T, 32, 512)))
+    lse = _lse(q, pool, table, cu, lens)
+    zero = np.zeros((3, W), dtype=np.float32)
+    ref, bound = M.weights(q, pool.codes, pool.scales, table, cu, lens, lse, zero, 0.0, zero, 16, 16)
+    args = lambda t: (bf16_dev(q), pool.device(), _i32(t), _i32(lens), _f32(lse))
+    for page in (-1, 60, 1 << 30, -(1 << 31), (1 << 31) - 1):
+        for b, j in ((0, 0), (0, 17), (2, 8)):
+            bad = table.astype(np.int64).copy()
+            bad[b, j] = page
+            out = torch.zeros((3, W), device=DEV)
+            with pytest.raises(SmlaError) as e:
+                smla.cache_weights(*args(bad), out, cu_tokens=_i32(cu))
+            assert e.value.code == _lib.SMLA_ERR_INDEX
+            live = np.ones((3, W), dtype=bool)
+            live[b, 16 * j:16 * j + 16] = False
+            got = out.double().cpu().numpy()
+            assert (np.abs(got - ref)[live] <= bound[live]).all() and (got[~live] == 0).all()
+    # a block whose scale is not a number says so in its positions; one below zero counts as it is
+    for scale in (np.nan, -0.25):
+        was, pool.scales[table[0, 3], 0] = pool.scales[table[0, 3], 0], scale
+        out = smla.cache_weights(*args(table), torch.zeros((3, W), device=DEV), cu_tokens=_i32(cu)).double().cpu().numpy()
+        odd = np.zeros((3, W), dtype=bool)
+        odd[0, 48:64] = True
+        assert (np.abs(out - ref)[~odd] <= bound[~odd]).all()
+        if np.isnan(scale):
+            assert np.isnan(out[odd]).all()
+        else:
+            r, o = M.weights(q, pool.codes, pool.scales, table, cu, lens, lse, zero, 0.0, zero, 16, 16)
+            assert (np.abs(out - r)[odd] <= o[odd]).all()
+        pool.scales[table[0, 3], 0] = was

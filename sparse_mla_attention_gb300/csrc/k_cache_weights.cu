@@ -507,10 +507,10 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
     const int page_mask = (1 << c.page_shift) - 1;
     const int box_rows = page_mask + 1 < kCwTile ? page_mask + 1 : kCwTile;
     CwWalk w(sh.at);
+    uint32_t use = 0, q_uses = 0, f_uses = 0;    // of the ring, of q's slots (a parity bit each), of the factors
 
     if (warp == kCwLoadWarp) {
         // ------------------------------------------------------- loads of the cache
-        uint32_t use = 0;
         bool ok = true;
         const int boxes = kCwTile / box_rows;
         while (ok && w.next(p)) {
@@ -543,13 +543,8 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
                 }
         }
         __syncwarp();
-        if (sh.abort_flag)                       // the loads already issued land before the CTA exits
-            for (uint32_t n = use > kCwSlots ? use - kCwSlots : 0; n < use; ++n)
-                mbar_wait(&sh.full[n % kCwSlots], (n / kCwSlots) & 1u, kCwWaitNs / 8);
-        __syncwarp();
     } else if (warp == kCwQWarp) {
         // ------------------------------------------------------- loads of q and its factors
-        uint32_t q_uses = 0, f_uses = 0;         // q_uses: a parity bit a slot
         int half = 0;
         bool ok = true;
         grid_dep_wait();                         // the splitting kernel is complete
@@ -593,18 +588,12 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
             }
         }
         __syncwarp();
-        if (sh.abort_flag) {                     // the loads already issued land before the CTA exits
-            for (int i = 0; i < kCwQSlots; ++i) mbar_wait(&sh.q_full[i], ((q_uses >> i) & 1u) ^ 1u, kCwWaitNs / 8);
-            for (uint32_t n = f_uses > 2 ? f_uses - 2 : 0; n < f_uses; ++n)
-                mbar_wait(&sh.f_full[n & 1], (n >> 1) & 1u, kCwWaitNs / 8);
-        }
-        __syncwarp();
     } else if (warp == kCwMmaWarp) {
         // ------------------------------------------------------------ products
         const uint64_t ring_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
         const uint64_t q_desc = sdesc_sw128(smem_u32(qbuf), 16, 1024);
         const bool leader = elect_one();
-        uint32_t use = 0, q_uses = 0, tile = 0;
+        uint32_t tile = 0;
         int half = 0;
         bool ok = true;
         while (ok && w.next(p)) {
@@ -659,7 +648,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
         // ---------------------------------------------------------------- sums
         const int team = warp >> 2, quarter = warp & 3;
         const int64_t width = int64_t(a.max_pages) << c.page_shift;
-        uint32_t f_uses = 0, tile = 0;
+        uint32_t tile = 0;
         bool ok = true, bad = false;
         while (ok && w.next(p)) {
             const int64_t line = w.b * width;
@@ -757,6 +746,15 @@ weights_kernel(const __grid_constant__ CUtensorMap map_box, const CwParams p) {
     __syncthreads();
     tc_fence_after();
     if (warp == kCwMmaWarp) tmem_dealloc(tbase, 512);
+    // Whichever warp gave up a wait, all are out of their loops here: the loads already issued land before the CTA exits.
+    if (sh.abort_flag && warp == kCwLoadWarp) {
+        for (uint32_t n = use > kCwSlots ? use - kCwSlots : 0; n < use; ++n)
+            mbar_wait(&sh.full[n % kCwSlots], (n / kCwSlots) & 1u, kCwWaitNs / 8);
+    } else if (sh.abort_flag && warp == kCwQWarp) {
+        for (int i = 0; i < kCwQSlots; ++i) mbar_wait(&sh.q_full[i], ((q_uses >> i) & 1u) ^ 1u, kCwWaitNs / 8);
+        for (uint32_t n = f_uses > 2 ? f_uses - 2 : 0; n < f_uses; ++n)
+            mbar_wait(&sh.f_full[n & 1], (n >> 1) & 1u, kCwWaitNs / 8);
+    }
 }
 
 // The same with the cache resident, for sequences of many rows of q: passes of three tiles, which go from shared
@@ -801,10 +799,10 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
     const int page_mask = (1 << c.page_shift) - 1;
     const int box_rows = page_mask + 1 < kCwTile ? page_mask + 1 : kCwTile;
     CwUnits w(sh.at);
+    uint32_t use = 0;                            // of the ring, or of q's slots
 
     if (warp == kCwLoadWarp) {
         // ------------------------------------------------------- loads of the cache
-        uint32_t use = 0;
         bool ok = true;
         const int boxes = kCwTile / box_rows;
         while (ok && w.next(p)) {
@@ -833,13 +831,8 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
             }
         }
         __syncwarp();
-        if (sh.abort_flag)                       // the loads already issued land before the CTA exits
-            for (uint32_t n = use > kCwLSlots ? use - kCwLSlots : 0; n < use; ++n)
-                mbar_wait(&sh.full[n % kCwLSlots], (n / kCwLSlots) & 1u, kCwWaitNs / 8);
-        __syncwarp();
     } else if (warp == kCwQWarp) {
         // ------------------------------------------------------- loads of q and its factors
-        uint32_t use = 0;
         bool ok = true;
         grid_dep_wait();                         // the splitting kernel is complete
         if (blockIdx.x == 0) {
@@ -870,10 +863,6 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
             }
         }
         __syncwarp();
-        if (sh.abort_flag)                       // the loads already issued land before the CTA exits
-            for (uint32_t n = use > kCwLQSlots ? use - kCwLQSlots : 0; n < use; ++n)
-                mbar_wait(&sh.q_full[n % kCwLQSlots], (n / kCwLQSlots) & 1u, kCwWaitNs / 8);
-        __syncwarp();
     } else if (warp == kCwMmaWarp || warp == kCwMmaWarp2) {
         // ------------------------------------------------------------ products
         // Two warps take them in turn, a buffer each: one's waits and its way to the next product (some 250 cycles,
@@ -881,7 +870,7 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
         const uint64_t q_desc = sdesc_sw128(smem_u32(qbuf), 16, 1024);
         const int buf = warp == kCwMmaWarp ? 0 : 1;
         const bool leader = elect_one();
-        uint32_t use = 0, tile = 0, pass = 0;
+        uint32_t tile = 0, pass = 0;
         bool ok = true;
         while (ok && w.next(p)) {
             const int last = w.last();
@@ -933,7 +922,7 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
         const uint32_t trow = tbase + (uint32_t(quarter * 32) << 16);
         const int row_in = 32 * quarter + lane;  // this thread's position in a tile
         const int64_t width = int64_t(a.max_pages) << c.page_shift;
-        uint32_t x_use = 0, use = 0, tile = 0;
+        uint32_t x_use = 0, tile = 0;
         int4 joins = make_int4(-1, 0, 0, 0);
         bool ok = true, bad = false;
         for (;;) {
@@ -1071,6 +1060,13 @@ weights_resident_kernel(const __grid_constant__ CUtensorMap map_box, const CwPar
     __syncthreads();
     tc_fence_after();
     if (warp == kCwMmaWarp) tmem_dealloc(tbase, 512);
+    // Whichever warp gave up a wait, all are out of their loops here: the loads already issued land before the CTA exits.
+    if (sh.abort_flag && warp == kCwLoadWarp)
+        for (uint32_t n = use > kCwLSlots ? use - kCwLSlots : 0; n < use; ++n)
+            mbar_wait(&sh.full[n % kCwLSlots], (n / kCwLSlots) & 1u, kCwWaitNs / 8);
+    else if (sh.abort_flag && warp == kCwQWarp)
+        for (uint32_t n = use > kCwLQSlots ? use - kCwLQSlots : 0; n < use; ++n)
+            mbar_wait(&sh.q_full[n % kCwLQSlots], (n / kCwLQSlots) & 1u, kCwWaitNs / 8);
 }
 
 // The passes that several CTAs of the resident kernel have a part in, their parts in order: a block for each CTA and tile.

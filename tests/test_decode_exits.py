@@ -27,3 +27,16 @@ def test_evictions_clusters_meet_before_they_write_to_each_other():
     assert meet and meet[0] < remote, "a CTA looks at another's shared memory that may not have started"
     # in every sequence: not within a branch or a loop
     assert _depth(body[:meet[0]]) == 1
+
+
+def test_a_weights_cta_that_gave_up_leaves_after_its_loads():
+    # any warp may give up, also when the loading ones are done: they wait once all warps are out of their loops
+    text = _source("k_cache_weights.cu")
+    for kernel, bars in (("weights_kernel", ("full", "q_full", "f_full")), ("weights_resident_kernel", ("full", "q_full"))):
+        body = text[re.search(r"\n%s\(" % kernel, text).start():]
+        body = body[:body.index("\n}\n")]
+        out = body.rindex("__syncthreads();")
+        for bar in bars:
+            waits = [m.start() for m in re.finditer(r"mbar_wait\(&sh\.%s\[" % bar, body)]
+            assert waits and min(waits) > out, f"{kernel}: a copy of {bar} may be in flight when the CTA leaves"
+        assert "sh.abort_flag" in body[out:]

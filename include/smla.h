@@ -443,8 +443,10 @@ int smla_weights_workspace_size(const smla_paged_dims* dims, size_t* bytes);
  * the largest of their scales and the others' codes are rounded to it (RNE; by a power
  * of two for scales of smla_cache_write: exact but for e4m3 subnormals). Rows behind the last keep their bytes.
  * The old sequences stay as they are: smla_cache_free(table) gives their pages back. Free pages
- * are taken as by smla_cache_alloc, for the new lengths. All or nothing: with too few,
- * SMLA_ERR_PAGES is set, new_table is filled with -1, new_lens with 0, and nothing else of the pool changes.
+ * are taken as by smla_cache_alloc, for the new lengths. All or nothing: with too few
+ * SMLA_ERR_PAGES is set, with a page below a sequence's length that nobody owns (refcount 0: the call might take it)
+ * SMLA_ERR_REFCOUNT; new_table is filled with -1, new_lens with 0 then, and nothing of the pool changes (kept and
+ * new_weights have what would have stayed).
  *   table, new_table [B, max_pages], lens, new_lens [B] int32, weights, new_weights
  *   [B, max_pages * page_size] fp32, kept [B, keep] int32; 1 <= keep <= max_pages * page_size,
  *   first + recent <= keep.

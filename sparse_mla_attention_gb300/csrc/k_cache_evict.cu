@@ -315,6 +315,17 @@ evict_plan_kernel(const EvictArgs a) {
         const int len = clamp_len(__ldg(a.lens + b), limit, bits);
         a.need[b] = int((int64_t(len < a.keep ? len : a.keep) + (1 << c.page_shift) - 1) >> c.page_shift);
     }
+    // A sequence's page that nobody owns may be among those that this call takes, which would be written as it is read:
+    // nothing is granted then. (Counts change once all CTAs have looked.)
+    constexpr int kStep = kPlanCtas * kPlanThreads;
+#pragma unroll 4
+    for (int64_t x = int64_t(blockIdx.x) * kPlanThreads + threadIdx.x; x < int64_t(a.B) * a.max_pages; x += kStep) {
+        const int b = int(x / a.max_pages), j = int(x - int64_t(b) * a.max_pages);
+        const int page = __ldg(a.table + x);
+        if (int64_t(j) << c.page_shift < row_len(a, b) && page >= 0 && page < c.num_pages &&
+            __ldcg(c.refcount + page) <= 0)
+            bits |= 1u << SMLA_ERR_REFCOUNT;
+    }
     const bool ok = grant_pages(c, a.B, a.need, a.start, a.fresh, bits, sh, turn, cl, a.status);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.granted[0] = ok;
 }

@@ -481,12 +481,6 @@ __device__ __forceinline__ int tail_to_hand_on(const ReorderArgs& a, int p, unsi
     const int e = __ldg(a.table + int64_t(p) * a.max_pages + (len >> c.page_shift));
     return e >= 0 && e < c.num_pages && __ldcg(c.refcount + e) == 1 ? e : -1;
 }
-// All bits of the CTA's threads.
-__device__ __forceinline__ unsigned cta_bits(unsigned bits) {
-    const bool index = __syncthreads_or(bits & (1u << SMLA_ERR_INDEX)) != 0;
-    const bool count = __syncthreads_or(bits & (1u << SMLA_ERR_REFCOUNT)) != 0;
-    return (index ? 1u << SMLA_ERR_INDEX : 0u) | (count ? 1u << SMLA_ERR_REFCOUNT : 0u);
-}
 // Free pages for the copies from number `used` on; true if there are enough.
 __device__ __forceinline__ bool pages_for_copies(const ReorderArgs& a, int used, int want, PlanShared& sh, int& turn,
                                                  cg::cluster_group& cl, unsigned& bits) {

@@ -144,17 +144,24 @@ __device__ __forceinline__ int clamp_len(int len, int64_t limit, unsigned& bits)
     return len < 0 ? 0 : int(limit);
 }
 
+// All bits of the CTA's threads.
+__device__ __forceinline__ unsigned cta_bits(unsigned bits) {
+    const bool index = __syncthreads_or(bits & (1u << SMLA_ERR_INDEX)) != 0;
+    const bool count = __syncthreads_or(bits & (1u << SMLA_ERR_REFCOUNT)) != 0;
+    return (index ? 1u << SMLA_ERR_INDEX : 0u) | (count ? 1u << SMLA_ERR_REFCOUNT : 0u);
+}
+
 // Free pages for the rows i < B, need_of[i] each (written by the cluster before this call), rows in order,
 // pages in the order of their numbers: row i gets pages[first[i]] and on, whose refcounts become 1. All or
-// nothing. Writes the status word with `bits` (SMLA_ERR_INDEX only, of any thread) and SMLA_ERR_PAGES where there are
-// too few; returns whether there were enough.
+// nothing. Writes the status word with `bits` (of any thread; one with SMLA_ERR_REFCOUNT grants nothing) and
+// SMLA_ERR_PAGES where there are too few; returns whether the pages were granted.
 __device__ bool grant_pages(const CacheView& c, int B, const int32_t* need_of, int32_t* first, int32_t* pages,
                             unsigned bits, PlanShared& sh, int& turn, cg::cluster_group& cl, unsigned* status) {
     const int rank = int(cl.block_rank());
     int lo, hi;
     page_slice(c.num_pages, rank, lo, hi);
     const int mine = count_pages(c.refcount, lo, hi, sh, turn, is_free);
-    bits = __syncthreads_or(bits) ? 1u << SMLA_ERR_INDEX : 0;
+    bits = cta_bits(bits);
     if (threadIdx.x == 0) { sh.part = mine; sh.bits = bits; }
     cl.sync();
     int before, have;
@@ -181,13 +188,13 @@ __device__ bool grant_pages(const CacheView& c, int B, const int32_t* need_of, i
         }
         need = int(sum < int64_t(have) + 1 ? sum : int64_t(have) + 1);
     }
-    const bool ok = need <= have;
+    const bool enough = need <= have, ok = enough && !(bits & (1u << SMLA_ERR_REFCOUNT));
     if (ok)
         emit_pages(c.refcount, lo, hi, before, need, sh, turn, is_free, [&](int r, int i) {
             pages[r] = i;
             c.refcount[i] = 1;
         });
-    if (rank == 0 && threadIdx.x == 0) *status = bits | (ok ? 0u : 1u << SMLA_ERR_PAGES);
+    if (rank == 0 && threadIdx.x == 0) *status = bits | (enough ? 0u : 1u << SMLA_ERR_PAGES);
     cl.sync();                                  // offsets and pages are written; parts are read
     return ok;
 }

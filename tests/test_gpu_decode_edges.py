@@ -137,3 +137,31 @@ def test_weights_report_every_page_out_of_range_and_take_any_scale(counts):
             r, o = M.weights(q, pool.codes, pool.scales, table, cu, lens, lse, zero, 0.0, zero, 16, 16)
             assert (np.abs(out - r)[odd] <= o[odd]).all()
         pool.scales[table[0, 3], 0] = was
+
+
+# ------------------------------------------------------------------------------------------------ pages that nobody owns
+@pytest.mark.parametrize("page,lens,keep", [(16, [100, 80, 33], 60), (64, [20000, 300], 9000)])
+def test_evict_refuses_sequences_with_pages_that_nobody_owns(page, lens, keep):
+    # such a page is free, and the lowest free ones are what the kept rows would be written to
+    from sparse_mla_attention_gb300 import SmlaError, _lib
+    smla = _smla()
+    rng = np.random.default_rng(3)
+    for b, j in ((0, 0), (1, 2), (0, 3)):
+        pool = Pool(800, page, 16, seed=110)
+        table = pool.place(lens, extra=2)
+        pool.fill(table, lens)
+        pool.refcount[table[b, j]] = 0
+        w = _heavy(rng, len(lens), table.shape[1] * page)
+        cache = pool.device()
+        out = (_i32(table), _i32(lens), _f32(w), _i32(np.zeros((len(lens), keep))))
+        with pytest.raises(SmlaError) as e:
+            smla.cache_evict(cache, _i32(table), _i32(lens), _f32(w), keep, out=out)
+        assert e.value.code == _lib.SMLA_ERR_REFCOUNT
+        assert (out[0] == -1).all() and (out[1] == 0).all()
+        pool.check(cache)
+    # entries behind a sequence's length are not looked at
+    pool = Pool(800, page, 16, seed=111)
+    table = pool.place(lens, extra=2)
+    pool.fill(table, lens)
+    table[:, -1] = np.flatnonzero(pool.refcount == 0)[:len(lens)]
+    _evict_and_check(pool, table, lens, _heavy(rng, len(lens), table.shape[1] * page), keep, 1, 2)

@@ -251,7 +251,7 @@ struct EvictArgs {
 };
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 
-// Arguments of a reordering. count [1], heir, spare [B], tail, need, src, dst [n]: workspace.
+// Arguments of a reordering. count [3] (copies, CTAs that are done, copies to pages of rows that ended), heir, spare [B], tail, need, src, dst [n]: workspace.
 struct ReorderArgs {
     CacheView cache; const int32_t* table; const int32_t* lens; const int32_t* parents; const float* weights;
     int32_t* new_table; int32_t* new_lens; float* new_weights;

@@ -165,3 +165,35 @@ def test_evict_refuses_sequences_with_pages_that_nobody_owns(page, lens, keep):
     pool.fill(table, lens)
     table[:, -1] = np.flatnonzero(pool.refcount == 0)[:len(lens)]
     _evict_and_check(pool, table, lens, _heavy(rng, len(lens), table.shape[1] * page), keep, 1, 2)
+
+
+@pytest.mark.parametrize("last", [0, 5])                               # the parent ends with its page, or each child copies one
+@pytest.mark.parametrize("n", [40, 5000])
+def test_reorder_leaves_out_pages_that_nobody_owns(n, last):
+    from sparse_mla_attention_gb300 import SmlaError, _lib
+    smla = _smla()
+    page, full = 16, 6
+    lens = [full * page + last, 3 * page, 2 * page]
+    pool = Pool(30 + n, page, 16, seed=120, junk=False)
+    table = pool.place(lens)
+    loose, ended = table[0, 2], table[1, 1]            # one that n - 1 children would share, one of a row that ends
+    pool.refcount[[loose, ended]] = 0
+    cache = pool.device()
+    ws = smla.Workspace(DEV)
+    out = (_i32(np.zeros((n + 1, table.shape[1]))), _i32(np.zeros(n + 1)), None)
+    with pytest.raises(SmlaError) as e:
+        smla.cache_reorder(cache, _i32(table), _i32(lens), _i32([0] * n + [2]), out=out, workspace=ws)
+    assert e.value.code == _lib.SMLA_ERR_REFCOUNT
+    got, count = _np(out[0]), _np(cache.refcount)
+    np.testing.assert_array_equal(got[0], table[0])
+    assert (got[1:n, 2] == -1).all()
+    own = [j for j in range(full) if j != 2]
+    assert (got[1:n][:, own] == table[0][own]).all() and (count[table[0][own]] == n).all()
+    free = np.flatnonzero(pool.refcount == 0)[:n - 1 if last else 0]
+    if last:
+        np.testing.assert_array_equal(got[1:n, full], free)
+    want = pool.refcount.copy()
+    want[table[0][own]] = n
+    want[[table[1, 0], table[1, 2]]] = 0
+    want[free] = 1
+    np.testing.assert_array_equal(count, want)

@@ -386,13 +386,11 @@ sdi_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
                     advance(slot, phase, C::kSlots);
                 }
             }
-            if (sh.abort_flag) {
-                // bounded wait for this thread's own copies still in flight
-                int s = slot; uint32_t ph = phase;
-                for (int k = 0; k < C::kSlots && k < issued; ++k) {
-                    if (--s < 0) { s = C::kSlots - 1; ph ^= 1u; }
-                    mbar_wait(&sh.full[s], ph, kWaitNs / 8);
-                }
+            // bounded wait for this thread's own copies still in flight, whichever warp gives up a wait after this
+            int s = slot; uint32_t ph = phase;
+            for (int k = 0; k < C::kSlots && k < issued; ++k) {
+                if (--s < 0) { s = C::kSlots - 1; ph ^= 1u; }
+                mbar_wait(&sh.full[s], ph, kWaitNs / 8);
             }
         }
         __syncwarp();
@@ -991,12 +989,10 @@ dq_kernel(const __grid_constant__ CUtensorMap map_ds, const __grid_constant__ CU
                 }
                 SMLA_TRACE_EV(1, it, 1);
             }
-            if (sh.abort_flag) {
-                int s = slot; uint32_t ph = phase;
-                for (int k = 0; k < kDqSlots && k < issued; ++k) {
-                    if (--s < 0) { s = kDqSlots - 1; ph ^= 1u; }
-                    mbar_wait(&sh.full[s], ph, kWaitNs / 8);
-                }
+            int s = slot; uint32_t ph = phase;   // as above
+            for (int k = 0; k < kDqSlots && k < issued; ++k) {
+                if (--s < 0) { s = kDqSlots - 1; ph ^= 1u; }
+                mbar_wait(&sh.full[s], ph, kWaitNs / 8);
             }
         }
         __syncwarp();

@@ -525,12 +525,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
         land_all();
         if (bad) flag_status(&sh.status, SMLA_ERR_INDEX);
-        if (sh.abort_flag) {     // the loads already issued land before the CTA exits
-            for (int slot = 0; slot < kPgSlots; ++slot)
-                mbar_wait(&sh.full[slot], pg_parity(loads, slot) ^ 1u, kPgWaitNs / 8);
-            for (int q = q_last > 2 ? q_last - 2 : 0; q <= q_last; ++q)
-                mbar_wait(&sh.q_load[q & 3], uint32_t(q >> 2) & 1u, kPgWaitNs / 8);
-        }
+        // the loads already issued land before the CTA exits, whichever warp gives up a wait after this
+        for (int slot = 0; slot < kPgSlots; ++slot)
+            mbar_wait(&sh.full[slot], pg_parity(loads, slot) ^ 1u, kPgWaitNs / 8);
+        for (int q = q_last > 2 ? q_last - 2 : 0; q <= q_last; ++q)
+            mbar_wait(&sh.q_load[q & 3], uint32_t(q >> 2) & 1u, kPgWaitNs / 8);
         __syncwarp();
     } else if (warp >= kPgMmaWarp) {
         // ------------------------------------------------------------ MMA issue

@@ -215,9 +215,9 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     tma_load_2d(qbuf + b * kFtQBytes, &map_q, c * 64, t * H, &sh.q_full[b]);
                 }
             }
-            if (sh.abort_flag)   // the loads already issued land before the CTA exits
-                for (int k = 1; k <= kFtQBufs && qi - k >= 0; ++k)
-                    mbar_wait(&sh.q_full[(qi - k) % kFtQBufs], uint32_t((qi - k) / kFtQBufs) & 1u, kFtWaitNs / 8);
+            // the loads already issued land before the CTA exits, whichever warp gives up a wait after this
+            for (int k = 1; k <= kFtQBufs && qi - k >= 0; ++k)
+                mbar_wait(&sh.q_full[(qi - k) % kFtQBufs], uint32_t((qi - k) / kFtQBufs) & 1u, kFtWaitNs / 8);
         }
         __syncwarp();
     } else if (warp >= kFtCopyWarp0) {

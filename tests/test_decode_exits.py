@@ -4,6 +4,8 @@ has started would fault, and a copy that never comes is not to be had. The sourc
 import os
 import re
 
+import pytest
+
 from sparse_mla_attention_gb300 import build
 
 
@@ -40,3 +42,15 @@ def test_a_weights_cta_that_gave_up_leaves_after_its_loads():
             waits = [m.start() for m in re.finditer(r"mbar_wait\(&sh\.%s\[" % bar, body)]
             assert waits and min(waits) > out, f"{kernel}: a copy of {bar} may be in flight when the CTA leaves"
         assert "sh.abort_flag" in body[out:]
+
+
+@pytest.mark.parametrize("name", ["k_fwd_paged.cu", "k_fwd_tc.cu", "k_attn_tc.cu"])
+def test_a_loading_warp_waits_for_its_loads_whoever_gives_up(name):
+    # not only where a wait has run out already: another warp's may, once this one has left its loop
+    text = _source(name)
+    waits = [m.start() for m in re.finditer(r"mbar_wait\(&sh\.(full|q_full)\[", text)]
+    assert waits
+    for at in waits:
+        before = text[max(0, at - 600):at]
+        guard = before.rfind("if (sh.abort_flag)")
+        assert guard < 0 or _depth(before[guard:]) < 0, f"{name}: {text[at - 200:at + 60]!r}"

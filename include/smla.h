@@ -487,10 +487,13 @@ int smla_cache_reorder_workspace_size(int32_t B, int32_t n, size_t* bytes);
  * The choice of the next beams. Row b * K + k of logits belongs to beam k of group b; its candidate v scores
  *   scores[b,k] + logits[b*K+k,v] - log(sum_v exp(logits[b*K+k,v]))
  * and a finished beam (done[b,k] != 0) has the one candidate v = eos, which scores scores[b,k]. The n best
- * of a group, best first, equal scores by k, then v:
+ * of a group, best first, equal scores by k, then the logit, then v:
  *   parents[b,i] = b * K + k (a row for smla_cache_reorder or smla_cache_fork), tokens[b,i] = v,
- *   new_scores[b,i] = the score (fp32; the order is decided in 64 bits).
- * A score that is not finite is never taken: banned tokens have logits of -inf, dead beams scores of -inf, and
+ *   new_scores[b,i] = the score (fp32).
+ * Scores are compared in 64 bits, with a row's log-sum as it is made of fp32 exponentials and sums: off by less than
+ * 2^-17 (2^-23 as a rule), and the same for rows of equal logits. A beam's own candidates, and those of
+ * beams with equal logits, are in their exact order; others that are closer than the log-sums' errors may change places.
+ * A score that is not finite (in 64 bits) is never taken: banned tokens have logits of -inf, dead beams scores of -inf, and
  * a row that holds a NaN or +inf has no candidates. Where fewer than n are left the rest is -1, -1, -inf.
  *   logits [B*K, V] of `type`, row_stride elements from row to row; scores [B,K] fp32, done [B,K] bytes or NULL
  *   (eos in [0, V) with done); outputs [B,n]. K, n <= SMLA_MAX_BEAMS, V <= SMLA_MAX_VOCAB. Rows may start at any

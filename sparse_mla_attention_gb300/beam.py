@@ -26,7 +26,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     logits [B*K, V] float32, bfloat16 or float16 (rows may be any stride apart, a row's values lie side by side);
     scores [B, K] float32. Candidate v of beam k scores scores[b,k] + log_softmax(logits[b*K+k])[v]; a beam that is
     ``done`` [B, K] bool has the one candidate ``eos``, with its score as it is. Equal scores: the lower beam, then the
-    lower token. Scores that are not finite are never taken; where fewer than n candidates are left the rest is
+    larger logit, then the lower token (candidates of beams with different logits that are closer than 1e-5, as a rule 1e-7, may change
+    places: smla_beam_select). Scores that are not finite are never taken; where fewer than n candidates are left the rest is
     (-1, -1, -inf). parents are row numbers b * K + k, tokens and parents int32. n is K if not given. Only enqueues work.
     """
     _need(scores, "scores", torch.float32, 2)

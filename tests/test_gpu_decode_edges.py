@@ -197,3 +197,34 @@ def test_reorder_leaves_out_pages_that_nobody_owns(n, last):
     want[[table[1, 0], table[1, 2]]] = 0
     want[free] = 1
     np.testing.assert_array_equal(count, want)
+
+
+# ------------------------------------------------------------------------------------------------ what small parts of the inputs do
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["normal", "flat", "rising", "falling", "peaked"])
+def test_selections_scores_are_as_exact_as_their_sums(dtype, kind):
+    # A value d below its row's maximum passes up to 13 additions, 8 scalings by an approximate power (2^-22, and 2^-24 for the
+    # product), one power of its own, and arguments off by 2.7 d 2^-24 in all (a subtraction, the factor log2(e), the
+    # product): relative to the sum 2^-24 (13 + 8 * 5 + 4 + 2.7 sum_i w_i d_i), w_i its softmax. The score's own rounding
+    # is 2^-24 of it.
+    V = 50001
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(6, V, generator=g, device=DEV) * 3
+    if kind == "flat":
+        x = x * 1e-3
+    elif kind in ("rising", "falling"):
+        x = torch.sort(x, dim=1, descending=kind == "falling")[0]
+    elif kind == "peaked":
+        x[:, ::5000] += 20.0
+    x = x.to(dtype)
+    scores = -np.arange(6.0).reshape(2, 3) / 8
+    p, t, s = _picked(x, scores, 9)
+    v = x.double().cpu().numpy()
+    ref = M.select(v, scores, 9)
+    np.testing.assert_array_equal(p, ref[0])
+    np.testing.assert_array_equal(t, ref[1])
+    top = v.max(axis=1, keepdims=True)
+    w = np.exp(v - top)
+    d = (w * (top - v)).sum(axis=1) / w.sum(axis=1)
+    bound = 2.0 ** -24 * (np.abs(ref[2]) + 57 + 2.7 * d[p])
+    assert (np.abs(s - ref[2]) <= bound).all()

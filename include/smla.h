@@ -302,8 +302,8 @@ typedef struct smla_paged_dims {
  * rank names are not used, whatever bytes they hold.
  *   q [T,H,512] bf16, lens [T], seq [T] or NULL, topk [T,topk] or NULL int32,
  *   sink [H] fp32 (finite or -inf) or NULL -> o [T,H,512] bf16 (RNE), lse [T,H] fp32.
- * Scores and sums are fp32; q meets the codes exactly (as two e4m3 parts), a
- * weight, with its block scale, as an e4m3 and an e5m2 part (off by at most 2^-7
+ * Scores and sums are fp32; q meets the codes as two e4m3 parts (values of 2^-13 of their row's
+ * largest and more exactly, smaller ones to within 2^-21 of it), a weight, with its block scale, as an e4m3 and an e5m2 part (off by at most 2^-7
  * of it, or 2^-20 of the token's largest such weight; the denominator is not
  * rounded so). The result is the same in every run.
  * On the device: lens[t] outside [0, max_pages * page_size] is clamped, and a
@@ -411,15 +411,16 @@ int smla_cache_workspace_size(const smla_cache* cache, int32_t n, size_t* bytes)
  * The attention weight that each cached position gets, the statistic that
  * smla_cache_evict goes by. The tokens t in [cu[b], cu[b+1]) belong to the
  * sequence in table row b (token b to row b if cu is NULL; then T <= B) and
- * see its positions [0, lens[t]), as in smla_fwd_paged, whose lse it takes:
+ * see its positions [0, lens[t]), as in smla_fwd_paged without topk, whose lse it takes (that of a call with
+ * topk leaves out positions that are counted here: the terms are no weights then):
  *   weights[b,p] = decay * earlier[b,p] + sum_t sum_h exp(scale * <q[t,h,:], x_p> - lse[t,h])
  * over the tokens that see p. Positions that no token of the call sees keep
  * what weights has. earlier may be weights itself (adding up in place) and is not read with decay = 0.
  *   q [T,H,512] bf16, cu [B+1] (cu[0] = 0, not decreasing, cu[B] <= T) or NULL, lens [T] int32,
  *   lse [T,H] fp32, earlier and weights [B, max_pages * page_size] fp32.
- * A head with lse = -inf (it saw nothing) adds nothing, one whose q holds an infinity or a NaN makes
- * the sums that it goes into NaN; a token with lens[t] = 0 is not looked at.
- * Scores and sums are fp32; q meets the codes exactly (smla_fwd_paged); dims->topk must be 0. The
+ * A head with lse = -inf (it saw nothing) adds nothing to positions whose row is free of NaN, one whose q holds an
+ * infinity or a NaN makes the sums that it goes into NaN; a token with lens[t] = 0 is not looked at.
+ * Scores and sums are fp32; q meets the codes as in smla_fwd_paged; dims->topk must be 0. The
  * result is the same in every run.
  * On the device: lens[t] outside [0, max_pages * page_size] is clamped, a sequence whose entries of cu
  * are out of order or range has no tokens (others that share tokens with it are unspecified), and a
@@ -440,7 +441,7 @@ int smla_weights_workspace_size(const smla_paged_dims* dims, size_t* bytes);
  *   new_weights[b,i] = weights[b,kept[b,i]], 0 behind the last
  *   new_lens[b]      = min(lens[b], keep)
  * Codes go over as they are where the rows of a new scale block had one scale; else the block gets
- * the largest of their scales and the others' codes are rounded to it (RNE; by a power
+ * the largest of their scales and the others' codes, times the fp32 ratio of the scales, are rounded (RNE; by a power
  * of two for scales of smla_cache_write: exact but for e4m3 subnormals). Rows behind the last keep their bytes.
  * The old sequences stay as they are: smla_cache_free(table) gives their pages back. Free pages
  * are taken as by smla_cache_alloc, for the new lengths. All or nothing: with too few
@@ -468,7 +469,7 @@ int smla_cache_evict_workspace_size(const smla_cache* cache, int32_t B, int32_t 
  * fall). A copy goes to the partly filled last page of a row that is given back and holds it alone, in
  * the order of rows, and when these are used up to free pages, by page number: as many
  * sequences as before need no page more. All or nothing: with too few pages the counts stay, new_table is filled
- * with -1, new_lens with 0 and SMLA_ERR_PAGES is set. Else the old table is void: its pages are new_table's.
+ * with -1, new_lens and new_weights with 0 and SMLA_ERR_PAGES is set. Else the old table is void: its pages are new_table's.
  *   new_lens[i] = lens[parents[i]]; with weights, new_weights[i,:] = weights[parents[i],:] up to
  *   that length and 0 behind it.
  *   table [B, max_pages], lens [B], parents [n], new_table, new_lens [n] int32; weights

@@ -329,8 +329,9 @@ def cache_weights(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens:
     """The attention weight that each cached position gets from query tokens, added up over them and their heads:
     weights = decay * earlier + sum of exp(scale <q, x> - lse) (smla_cache_weights). Returns ``weights``.
 
-    q [T,H,512] bf16, lens [T] and lse [T,H] are those of sparse_mla_fwd_paged; the tokens
-    cu_tokens[b]:cu_tokens[b+1] belong to table row b (token b without it). weights and earlier are
+    q [T,H,512] bf16, lens [T] and lse [T,H] are those of sparse_mla_fwd_paged over all positions (the lse of a call
+    with ``topk`` does not fit: the terms would be no weights); the tokens cu_tokens[b]:cu_tokens[b+1] belong to table
+    row b (token b without it), so tokens come in the order of their sequences. weights and earlier are
     [B, max_pages * page_size] float32; without ``earlier`` the sums are added to ``weights`` itself. With decay 0
     nothing earlier counts. Positions that no token sees keep what ``weights`` has.
     """
@@ -365,7 +366,8 @@ def cache_evict(cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, weig
     kept [B, keep] says which position each row had.
 
     weights [B, max_pages * page_size] float32 (cache_weights). The old sequences stay as they are: cache_free gives
-    their pages back. All or nothing where free pages are short. ``out`` takes the four results.
+    their pages back. All or nothing where free pages are short or a sequence has a page that nobody owns (refcount 0).
+    ``out`` takes the four results.
     """
     p_table = _check(cache, table, "table", torch.int32, 2)
     B, max_pages = table.shape

@@ -64,6 +64,10 @@ constexpr int kCwSplitThreads = 256;
 // x positions, heads, rows): 64 x 3000, 128, 192: 42.5 / 63.3, 386: 77.0 / 87.0, 768: 137 / 125; 16 x 4000, 64, 288: 30.9 /
 // 30.3, 392: 37.2 / 34.6, 760: 59.8 / 49.6; 2 x 30000, 128, 448: 35.5 / 31.4, 1216: 79.0 / 50.6; 1 x 2000, 128, 4096: 125 /
 // 24.6 (streaming, a tile's chunks are one CTA's).
+// The rule sees the average alone, as cu is on the device. In a batch of single tokens and one sequence of many, that
+// sequence's tiles, all chunks of each, stay on a few CTAs where the cache streams: 255 x 1 token and one of 512, 2000
+// positions, 128 heads, 383 rows: 2166 / 337; 127 x 1 and one of 64, 3000, 128, 191: 300 / 133; 31 x 1 and one of 32, 20000,
+// 128, 252: 184 / 236. Two calls, one for the single tokens and one for the many, are the way around it.
 constexpr int kCwManyRows = 400;
 constexpr int kCwMaxBlocks = 608;                // of the splitting kernel: four an SM leave room for the other's, which start meanwhile
 

@@ -8,7 +8,7 @@ import torch
 
 import decode_reference as M
 from test_gpu_cache import DEV, Pool, _i32, _smla, bf16, bf16_dev
-from test_gpu_decode import _evict_and_check, _f32, _heavy, _lse, _np
+from test_gpu_decode import _evict_and_check, _f32, _heavy, _lse, _np, _watch
 
 pytestmark = pytest.mark.gpu
 
@@ -228,3 +228,49 @@ def test_selections_scores_are_as_exact_as_their_sums(dtype, kind):
     d = (w * (top - v)).sum(axis=1) / w.sum(axis=1)
     bound = 2.0 ** -24 * (np.abs(ref[2]) + 57 + 2.7 * d[p])
     assert (np.abs(s - ref[2]) <= bound).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 40])                            # both forms
+def test_weights_see_every_bit_of_q(tokens):
+    # One value a cached row, 448 in column p % 512: a score is one product of q, exact in fp32 (8 x 4 bits) where q's two parts
+    # hold it, which is for 2^-13 of the row's largest (here 1) and more; below that they are off by up to 2^-21 of it.
+    # The argument: factors scale, log2(e) and their product, lse in log2 units, the sum; the power 2^-22; up to 16 * tokens
+    # additions a position (16 columns at a time as a tree, so fewer).
+    smla = _smla()
+    rng = np.random.default_rng(130)
+    H, L, page = 16, 1024, 64
+    pool = Pool(40, page, 64, seed=131, junk=False)
+    table = pool.place([L])
+    pool.codes[:] = 0
+    pool.scales[:] = 1.0
+    for p in range(L):
+        pool.codes[table[0, p // page], p % page, p % 512] = 0x7E
+    q = np.exp2(rng.uniform(-18, 0, size=(tokens, H, 512))) * rng.choice([-1.0, 1.0], size=(tokens, H, 512))
+    q[:, :, 0] = 1.0
+    q = np.clip(bf16(q), -1.0, 1.0)
+    lse = rng.uniform(1, 5, size=(tokens, H)).astype(np.float32)
+    W = table.shape[1] * page
+    out = smla.cache_weights(bf16_dev(q), pool.device(), _i32(table), _i32([L] * tokens), _f32(lse),
+                             torch.zeros((1, W), device=DEV), cu_tokens=_i32([0, tokens]))
+    got = out.double().cpu().numpy()[0, :L]
+    a = q[:, :, np.arange(L) % 512] * 448.0 / np.sqrt(512.0)
+    l = lse[:, :, None].astype(np.float64)
+    w = np.exp(a - l)
+    d = 2.0 ** -24 * (5 * np.abs(a) + 3 * l + 2 * np.abs(a - l) + 16 * tokens + 4) + 2.0 ** -22
+    d = d + np.where(np.abs(q) < 2.0 ** -13, 2.0 ** -21, 0.0)[:, :, np.arange(L) % 512] * 448.0 / np.sqrt(512.0)
+    assert (np.abs(got - w.sum(axis=(0, 1))) <= (w * np.expm1(d)).sum(axis=(0, 1))).all()
+
+
+@pytest.mark.parametrize("most", [3, 40])                              # few rows of q a sequence, and many
+def test_weights_of_more_sequences_than_a_block_has_threads(most):
+    rng = np.random.default_rng(140)
+    B = 1100
+    full = rng.integers(0, 150, size=B)
+    full[5], full[1099] = 2000, 700
+    counts = [int(min(n, c)) for n, c in zip(full, rng.integers(0, most + 1, size=B) * (rng.random(B) < 0.5))]
+    counts[5], counts[7] = 2 * most, 0
+    pool = Pool(12000, 16, 16, seed=141, junk=False)
+    table = pool.place(full)
+    pool.fill(table, full)
+    lens = [n - c + 1 + i for n, c in zip(full, counts) for i in range(c)]
+    _watch(pool, table, counts, lens, 16 if most == 3 else 48, decay=0.5, lse=np.full((len(lens), 16 if most == 3 else 48), 3.0, np.float32))

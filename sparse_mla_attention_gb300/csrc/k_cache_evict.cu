@@ -6,10 +6,11 @@
 // weights' bits (a histogram of 2048 bins, and steps of seven bits among the weights of one bin as soon as they are
 // few), so the choice is exact and the same in every run.
 //
-// Bound: the copies by HBM, the choice by latency. 64 sequences of up to 8192 positions to 2048 each, pages and
-// blocks of 64: 44 us with a free of the last call's pages, of which the copies take 24 (134 MB read and written: 5.6
-// TB/s), the choice 7 and the free 4; 3 of up to 81920 to 16384: 32 us, 14 and 11 and 3; one of 1500 to 1024: 16 us. The
-// choice of a sequence in one CTA: weights into registers 1.1 us, histogram 0.9, its scan 0.4, collecting the bin 1,
+// Bound: latency, in the choice and in the copies (a warp follows positions, pages, scales and rows of a unit before it
+// takes the next). 64 sequences of up to 8192 positions to 2048 each, pages and blocks of 64: 44 us with a free of the
+// last call's pages, of which the copies take 31 (134 MB read and written: 4.3 TB/s), the choice 8 and the free 4; 3 of up
+// to 81920 to 16384: 32 us, 15 and 12 and 4; one of 1500 to 1024: 16 us. The choice of a sequence in one CTA: weights
+// into registers 1.1 us, histogram 0.9, its scan 0.4, collecting the bin 1,
 // seven bits a step 0.7, the list 1.8; in eight, of 81920: 1.2 and 0.4 for the first barrier, 1.3, 0.5 joined, 0.8, 1.1,
 // 0.9 joined, 1.2, 0.4, the counts 1.4, the list 1.2. Bisection of the few, a count and a barrier a step: 46 and 38 us (with
 // lists gathered twice); bins read by every CTA from the first: 36 for the long ones. Three full histograms: 50 and 49
@@ -63,7 +64,7 @@ __device__ __forceinline__ int row_len(const EvictArgs& a, int b) {
 constexpr int kDigits = 2048;                    // bins of a pass: bits 31-21, 20-10 and 9-0 of a weight
 constexpr int kRun = 16;                         // positions of a thread
 constexpr int kTile = kPlanThreads * kRun;
-constexpr int kFew = 4 * kPlanThreads;           // weights that are left to a bisection
+constexpr int kFew = 4 * kPlanThreads;           // weights of one bin that its first CTA goes through seven bits at a time
 
 struct ChooseShared {
     int hist[kDigits];                           // of this CTA

@@ -420,7 +420,8 @@ int smla_cache_workspace_size(const smla_cache* cache, int32_t n, size_t* bytes)
  *   lse [T,H] fp32, earlier and weights [B, max_pages * page_size] fp32.
  * A head with lse = -inf (it saw nothing) adds nothing to positions whose row is free of NaN, one whose q holds an
  * infinity or a NaN makes the sums that it goes into NaN; a token with lens[t] = 0 is not looked at.
- * Scores and sums are fp32; q meets the codes as in smla_fwd_paged; dims->topk must be 0. The
+ * Scores and sums are fp32; q meets the codes as in smla_fwd_paged; dims->topk must be 0 and T * H at most 2^25 (more
+ * tokens: one call after the other, adding up in place). The
  * result is the same in every run.
  * On the device: lens[t] outside [0, max_pages * page_size] is clamped, a sequence whose entries of cu
  * are out of order or range has no tokens (others that share tokens with it are unspecified), and a

@@ -333,7 +333,7 @@ def cache_weights(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens:
     with ``topk`` does not fit: the terms would be no weights); the tokens cu_tokens[b]:cu_tokens[b+1] belong to table
     row b (token b without it), so tokens come in the order of their sequences. weights and earlier are
     [B, max_pages * page_size] float32; without ``earlier`` the sums are added to ``weights`` itself. With decay 0
-    nothing earlier counts. Positions that no token sees keep what ``weights`` has.
+    nothing earlier counts. Positions that no token sees keep what ``weights`` has. T * H is at most 2^25.
     """
     p_q = _check(cache, q, "q", torch.bfloat16, 3)
     p_table = _check(cache, table, "table", torch.int32, 2)

@@ -29,6 +29,10 @@ int check_cache(const smla_cache* c) {
 // Sequences and children per call: grids and slot numbers stay within 32 bits.
 constexpr int kMaxSeqs = 1 << 24;
 
+// Rows of q of a call of accumulated weights: a pass over a sequence's takes 0.8 us for each 32 of them (1.2 at the lowest
+// clocks under load), and the warp that loads the next pass's tiles waits that long, with a limit of 2 s.
+constexpr int64_t kMaxWeightsRows = int64_t(1) << 25;
+
 int check_table(const smla_cache& c, int B, int max_pages) {
     if (B < 0 || B > kMaxSeqs || max_pages < 1 || int64_t(max_pages) * c.page_size > int64_t(INT32_MAX))
         return SMLA_ERR_SHAPE;
@@ -329,7 +333,9 @@ int smla_cache_copy_pages(const smla_cache* cache, const int32_t* src, const int
 
 int smla_weights_workspace_size(const smla_paged_dims* d, size_t* bytes) {
     if (!d || !bytes) return SMLA_ERR_NULL;
-    if (d->T < 0 || d->B < 0 || d->B > kMaxSeqs || d->H < 16 || d->H > 128 || d->H % 16 != 0) return SMLA_ERR_SHAPE;
+    if (d->T < 0 || d->B < 0 || d->B > kMaxSeqs || d->H < 16 || d->H > 128 || d->H % 16 != 0 ||
+        int64_t(d->T) * d->H > kMaxWeightsRows)
+        return SMLA_ERR_SHAPE;
     *bytes = kStatusBytes + weights_scratch_bytes(d->T, d->H);
     return SMLA_OK;
 }
@@ -345,7 +351,7 @@ int smla_cache_weights(const uint16_t* q, const smla_cache* cache, const int32_t
     if (d.D != kD) return SMLA_ERR_D512;
     if (d.T < 0 || d.H < 16 || d.H > 128 || d.H % 16 != 0) return SMLA_ERR_SHAPE;
     if ((rc = check_table(c, d.B, d.max_pages))) return rc;
-    if (int64_t(d.T) * d.H > int64_t(INT32_MAX) || (!cu && d.T > d.B)) return SMLA_ERR_SHAPE;
+    if (int64_t(d.T) * d.H > kMaxWeightsRows || (!cu && d.T > d.B)) return SMLA_ERR_SHAPE;
     if (d.topk != 0 || !std::isfinite(d.scale) || d.scale < 0.f || !std::isfinite(decay)) return SMLA_ERR_ARG;
     if (!workspace) return SMLA_ERR_NULL;
     const bool any = d.B > 0 && d.T > 0;

@@ -13,8 +13,8 @@
 // two cluster barriers: 5 to 9 us). Compaction of 40000 pages of 32 KB, 9900 of them live and
 // 7400 of these moved: 83 us, of which the copies take 69; 5.9 TB/s over all. Fork of 1024 children, each with
 // a page to copy, after a free of as many: 26 us; of 32: 13 us. Reordering of 1024 beams (their weights too) in that
-// pool: 16 us with a copy of the counts before it (plan 4.5, moves 7.5), where fork and free copy every beam's last
-// page; of 32: 9.
+// pool: 17 us with a copy of the counts before it (plan 4.5, moves 8.5), where fork and free copy every beam's last
+// page; of 32: 10.
 #include "page_plan.cuh"
 #include "sm100.cuh"
 
@@ -773,8 +773,8 @@ cudaError_t launch_cache_fork(const CacheView& c, const int32_t* table, const in
 }
 
 cudaError_t launch_cache_reorder(const ReorderArgs& a, cudaStream_t s) {
-    // Both sides, device time of a call and a copy before it: 1024 rows 16.3 us planned in shared memory, 21.1 through
-    // the workspace; 32 rows 8.8 and 13.2.
+    // Both sides, device time of a call and a copy before it: 1024 rows 16.8 us planned in shared memory, 21.8 through
+    // the workspace; 32 rows 9.9 and 14.0.
     if (a.B <= kReorderRows && a.n <= 4 * kReorderRows) reorder_plan_few_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(a);
     else reorder_plan_kernel<<<kPlanCtas, kPlanThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
